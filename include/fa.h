@@ -450,6 +450,150 @@ FA_API int fa_fwd_splitkv_strided(const void* q, const int64_t* q_strides, const
                                   int n_split, int causal, float scale, fa_stream_t stream);
 
 /*
+ * Scored attention: attention whose scores get a tanh cap, a bias that falls with
+ * distance, and a mask of packed documents with prefixes, with shared key/value
+ * heads.  (The pages name none of these; they are the ordinary forms of causal
+ * language-model attention around the exact softmax of fa_fwd.)
+ *
+ *   a_ij = scale * q_i . k_j
+ *   c_ij = softcap * tanh(a_ij / softcap)      (softcap > 0; softcap = 0: c = a)
+ *   s_ij = c_ij - slopes[h] * |i - j|          (slopes NULL: no bias)
+ *   LSE_i = ln sum_{j visible} exp(s_ij),   O_i = sum_{j visible} exp(s_ij - LSE_i) v_j
+ *   A row that sees no key: O_i = 0, LSE_i = -inf.
+ *
+ * Query head h reads key/value head h / (H / Hkv); H must be a multiple of Hkv.
+ *
+ * The mask.  Without a plan: causal = 1 (j <= i) or 0 (every key).  With a plan
+ * (fa_mask_plan) the mask is the plan's, and `causal` must be 0 in the calls that
+ * take it.  Each row of the batch holds n_docs documents packed one after another:
+ * document t is positions [s, e) = [cu_docs[t], cu_docs[t + 1]) and has a prefix of
+ * p = prefix[t] positions (prefix NULL: 0).  Position i of the document sees
+ *   causal:      s <= j < max(i + 1, min(s + p, e))     not causal:  s <= j < e
+ * Documents may be empty.  Positions in no document (before cu_docs[0], from
+ * cu_docs[n_docs] on) are padding: they see nothing and nothing sees them; their O
+ * is 0, their LSE -inf, and their dQ, dK, dV are 0.  What q, k, v and dout hold in
+ * padding does not matter as long as it is finite (a weight of exactly 0 times an
+ * infinity or NaN would not be 0).
+ */
+
+/* Bytes of a mask plan for B rows of N positions (16 B N; 0 for invalid sizes). */
+FA_API size_t fa_mask_plan_size(int B, int N);
+
+/*
+ * fa_mask_plan -- the mask as intervals, made once for a batch and used by the
+ * forward and the backward of every layer: for each query the keys it sees, for
+ * each key the queries that see it.
+ *   cu_docs : const int32 [B, n_docs + 1] on the device, nondecreasing in each row,
+ *             within [0, N]; or NULL for one document of N positions (n_docs = 1)
+ *   prefix  : const int32 [B, n_docs] on the device, or NULL (only read if causal;
+ *             negative counts as 0, longer than the document as its length)
+ *   plan    : device memory of fa_mask_plan_size(B, N) bytes, 16-byte aligned
+ * The offsets are not checked on the host.  Offsets that decrease or leave [0, N]
+ * give an unspecified mask, but no access outside the tensors.
+ * Errors: FA_ERR_INVALID_ARG (sizes, n_docs < 1, n_docs != 1 without cu_docs,
+ * causal not 0/1), FA_ERR_WORKSPACE (plan missing or short), FA_ERR_MISALIGNED.
+ */
+FA_API int fa_mask_plan(const int32_t* cu_docs, const int32_t* prefix, int n_docs, void* plan, size_t plan_bytes,
+                        int B, int N, int causal, fa_stream_t stream);
+
+/*
+ * fa_fwd_scored -- bf16 forward of scored attention.
+ *   q, o : bf16 [B, H, N, d]     k, v : bf16 [B, Hkv, N, d]     lse : float [B, H, N]
+ * with the stride rules of fa_fwd_strided (NULL = dense).
+ *   plan    : from fa_mask_plan for the same B, N (plan_bytes its size), or NULL
+ *   softcap : 0 or a finite number > 0
+ *   slopes  : const float [H] on the device (finite), or NULL
+ * Numerics as fa_fwd: scores, their cap and bias, the running maximum and sum and
+ * the accumulators in fp32, P rounded to bf16 for P V.  The same bits on every run.
+ * Errors as fa_fwd_strided; FA_ERR_INVALID_ARG also for H not a multiple of Hkv, a
+ * bad softcap, or causal = 1 with a plan; FA_ERR_WORKSPACE for a short plan.
+ */
+FA_API int fa_fwd_scored(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                         const void* v, const int64_t* v_strides, void* o, const int64_t* o_strides, float* lse,
+                         int B, int H, int Hkv, int N, int d, const void* plan, size_t plan_bytes, int causal,
+                         float scale, float softcap, const float* slopes, fa_stream_t stream);
+
+/* Bytes of workspace fa_bwd_scored needs (0 for invalid or unsupported sizes). */
+FA_API size_t fa_bwd_scored_workspace_size(int B, int H, int Hkv, int N, int d);
+
+/*
+ * fa_bwd_scored -- gradient of fa_fwd_scored with respect to q, k and v:
+ *   P = exp(s - LSE) (0 where masked),  dP = dO V^T,  D_i = dO_i . O_i,
+ *   dS = P (dP - D) (1 - tanh^2(a / softcap)),
+ *   dQ = scale dS K,  dK = scale sum_h dS^T Q,  dV = sum_h P^T dO
+ * with the sums over the query heads that share the key/value head, in fp32.
+ *   q, o, dout, dq : bf16 [B, H, N, d]   k, v, dk, dv : bf16 [B, Hkv, N, d]
+ *   o, lse         : the forward's outputs for the same arguments
+ * plan, causal, scale, softcap, slopes as given to the forward (the slopes get no
+ * gradient).  workspace, `deterministic` and errors as fa_bwd_strided, with
+ * fa_bwd_scored_workspace_size(...) bytes.
+ */
+FA_API int fa_bwd_scored(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                         const void* v, const int64_t* v_strides, const void* o, const int64_t* o_strides,
+                         const void* dout, const int64_t* dout_strides, const float* lse, void* dq,
+                         const int64_t* dq_strides, void* dk, const int64_t* dk_strides, void* dv,
+                         const int64_t* dv_strides, void* workspace, size_t ws_bytes, int B, int H, int Hkv, int N,
+                         int d, const void* plan, size_t plan_bytes, int causal, float scale, float softcap,
+                         const float* slopes, int deterministic, fa_stream_t stream);
+
+/*
+ * Paged key/value cache: the serving form of scored attention.  The cache is n_pages
+ * pages of page_size tokens; the tokens of sequence b lie in the pages
+ * page_table[b][0], page_table[b][1], ... in order.
+ *   k_cache, v_cache : indexed [n_pages, Hkv, page_size, d], d contiguous; element
+ *       (p, h, r, c) at ptr + p*strides[2] + h*strides[1] + r*strides[0] + c (NULL =
+ *       dense), strides positive multiples of 8 elements, strides[0] >= d
+ *   page_table : const int32, row b at page_table + b*table_stride, max_pages entries
+ *   seq_lens   : const int32 [B], tokens of each sequence, the new ones included
+ * all on the device.  dtype: 1 = bf16, 2 = fp16, for every 16-bit tensor of a call.
+ * page_size is a multiple of 16 up to 1024; d is 64 or 128.
+ * seq_lens is clamped to [0, max_pages * page_size].  A page index outside
+ * [0, n_pages) is the caller's error: its tokens read as zeros and are not written;
+ * no access leaves the cache.  Nothing past a sequence's last token is read into a
+ * result or written, whatever it holds.
+ */
+
+/*
+ * fa_paged_append -- write new tokens' keys and values into the cache.
+ *   k, v   : [T, Hkv, d], element (t, h, c) at ptr + t*strides[1] + h*strides[0] + c
+ *            (NULL = dense; multiples of 8 elements, positive)
+ *   cu_new : const int32 [B + 1] on the device: rows cu_new[b] .. cu_new[b + 1] - 1
+ *            are the last tokens of sequence b (positions seq_lens[b] - n_b ...);
+ *            nondecreasing within [0, T].  A token whose position would be negative
+ *            or past the table is not written, nor are rows from cu_new[B] on.
+ * Two sequences that share a page must not both write to it in one call.
+ */
+FA_API int fa_paged_append(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                           void* k_cache, const int64_t* k_cache_strides, void* v_cache,
+                           const int64_t* v_cache_strides, const int32_t* page_table, int64_t table_stride,
+                           const int32_t* seq_lens, const int32_t* cu_new, int B, int T, int Hkv, int d, int page_size,
+                           int n_pages, int max_pages, int dtype, fa_stream_t stream);
+
+/* Bytes of workspace fa_paged_decode needs on the current device (0 for invalid or
+ * unsupported sizes).  It does not grow with the cache's length. */
+FA_API size_t fa_paged_decode_workspace_size(int B, int H, int Hkv, int d);
+
+/*
+ * fa_paged_decode -- scored attention of one token a sequence, the last one
+ * (position seq_lens[b] - 1), against the sequence's whole cache:
+ *   s_j = c(scale q . k_j) - slopes[h] * (seq_lens[b] - 1 - j),  0 <= j < seq_lens[b]
+ *   q, o : [B, H, d], element (b, h, c) at ptr + b*strides[1] + h*strides[0] + c
+ *          (NULL = dense; multiples of 8 elements, positive)
+ *   lse  : float [B, H]
+ * An empty sequence: o = 0, lse = -inf.  The tokens of all sequences are dealt out
+ * evenly over the SMs on the device (the lengths are never read by the host) and the
+ * parts of a sequence joined by their LSE; the same bits on every run.
+ * The workspace (256-byte aligned) is scratch; calls that overlap need their own.
+ * softcap and slopes as fa_fwd_scored.  Errors as fa_fwd_splitkv.
+ */
+FA_API int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache,
+                           const int64_t* k_cache_strides, const void* v_cache, const int64_t* v_cache_strides,
+                           const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens, void* o,
+                           const int64_t* o_strides, float* lse, void* workspace, size_t ws_bytes, int B, int H,
+                           int Hkv, int d, int page_size, int n_pages, int max_pages, int dtype, float scale,
+                           float softcap, const float* slopes, fa_stream_t stream);
+
+/*
  * W4A16: 4-bit weights times 16-bit activations, dequantised on the fly
  * ("FlashAttention-Skalierung, Multi-GPU-Training und Gewichtsquantisierung",
  * section 3, "Wie spezielle CUDA-Kernels während der Ausführung dequantisieren

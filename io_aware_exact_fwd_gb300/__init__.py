@@ -19,6 +19,8 @@ __all__ = [
     "FAError", "load_library", "library_path", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_noalloc",
     "fa_bwd_noalloc_max_workspace", "fa_bwd_prep", "fa_bwd_main", "fa_bwd_dq", "fa_fp8_workspace_size",
     "fa_fp8_workspace_offsets", "fa_fp8_prepare", "fa_fp8_prepare_seeded", "fa_fp8_rotation_signs", "fa_fwd_fp8",
+    "fa_mask_plan_size", "fa_mask_plan", "fa_fwd_scored", "fa_bwd_scored_workspace_size", "fa_bwd_scored",
+    "fa_paged_append", "fa_paged_decode_workspace_size", "fa_paged_decode",
     "fa_sync_check",
     "fa_strerror",
     "fa_version", "fa_last_error_site", "fa_debug_set_wait_limit_ns", "fa_debug_set_fault",
@@ -119,6 +121,23 @@ def load_library():
     lib.fa_fwd_splitkv_strided.restype = i
     lib.fa_fwd_splitkv_strided.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, i, i, i, i, i, i,
                                            i, f, vp]
+    sz, i64 = ctypes.c_size_t, ctypes.c_int64
+    lib.fa_mask_plan_size.restype = sz
+    lib.fa_mask_plan_size.argtypes = [i, i]
+    lib.fa_mask_plan.restype = i
+    lib.fa_mask_plan.argtypes = [vp, vp, i, vp, sz, i, i, i, vp]
+    lib.fa_fwd_scored.restype = i
+    lib.fa_fwd_scored.argtypes = [vp] * 9 + [i] * 5 + [vp, sz, i, f, f, vp, vp]
+    lib.fa_bwd_scored_workspace_size.restype = sz
+    lib.fa_bwd_scored_workspace_size.argtypes = [i] * 5
+    lib.fa_bwd_scored.restype = i
+    lib.fa_bwd_scored.argtypes = [vp] * 17 + [vp, sz] + [i] * 5 + [vp, sz, i, f, f, vp, i, vp]
+    lib.fa_paged_append.restype = i
+    lib.fa_paged_append.argtypes = [vp] * 9 + [i64, vp, vp] + [i] * 8 + [vp]
+    lib.fa_paged_decode_workspace_size.restype = sz
+    lib.fa_paged_decode_workspace_size.argtypes = [i] * 4
+    lib.fa_paged_decode.restype = i
+    lib.fa_paged_decode.argtypes = [vp] * 7 + [i64] + [vp] * 5 + [sz] + [i] * 8 + [f, f, vp, vp]
     lib.fa_w4a16_workspace_size.restype = ctypes.c_size_t
     lib.fa_w4a16_workspace_size.argtypes = [i, i, i, i]
     lib.fa_w4a16_default_splits.restype = i
@@ -597,6 +616,260 @@ def fa_fwd_splitkv(q, k, v, o=None, lse=None, workspace=None, n_split: int = 0, 
                                             _strides(o), _ptr(lse), _ptr(workspace), _ws_bytes(workspace), B, H, Nq,
                                             Nk, d, n, int(bool(causal)), sc, _stream_handle(stream))
     _check(st, "fa_fwd_splitkv")
+    return o, lse
+
+
+def _check_layout(name, t, shape, dtype, device):
+    """Any layout whose last dimension is contiguous, on `device`.  Returns the strides argument: None
+    when the tensor is dense, else its strides from the second-to-last dimension outwards (dimensions
+    of one element, whose stride means nothing, count as dense)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    out, dense = [], shape[-1]
+    for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
+        out.append(x if n != 1 else dense)
+        dense *= n
+    return (ctypes.c_int64 * len(out))(*out)
+
+
+def _check_flat(name, t, shape, dtype, device):
+    """A dense tensor on `device`, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _scratch(workspace, need, device):
+    """The caller's workspace (a dense CUDA tensor on `device`), or a new one."""
+    import torch
+
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return workspace
+
+
+def fa_mask_plan_size(B: int, N: int) -> int:
+    """Bytes of a mask plan for B rows of N positions (0 if unsupported)."""
+    return int(load_library().fa_mask_plan_size(B, N))
+
+
+def fa_mask_plan(B: int, N: int, cu_docs=None, prefix=None, causal: bool = True, plan=None, device=None, stream=None):
+    """The mask of B rows of N positions as intervals (uint8 CUDA tensor), for fa_fwd_scored and fa_bwd_scored.
+
+    cu_docs: int32 [B, n_docs + 1], offsets of the documents packed in each row (None:
+    one document of N positions); prefix: int32 [B, n_docs], positions at each
+    document's start that the whole document sees (None: none; only read if causal).
+    Positions in no document are padding.  One plan serves every layer of a batch.
+    """
+    import torch
+
+    lib = load_library()
+    ref = cu_docs if cu_docs is not None else prefix if prefix is not None else plan
+    dev = ref.device if ref is not None else torch.device("cuda" if device is None else device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    n_docs = 1 if cu_docs is None else cu_docs.shape[1] - 1
+    _check_flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, dev)
+    _check_flat("prefix", prefix, (B, n_docs), torch.int32, dev)
+    plan = _scratch(plan, fa_mask_plan_size(B, N), dev)
+    with torch.cuda.device(dev):
+        st = lib.fa_mask_plan(_ptr(cu_docs), _ptr(prefix), n_docs, _ptr(plan), _ws_bytes(plan), B, N,
+                              int(bool(causal)), _stream_handle(stream))
+    _check(st, "fa_mask_plan")
+    return plan
+
+
+def _plan_args(plan, device):
+    if plan is None:
+        return None, 0
+    if plan.device != device or not plan.is_contiguous():
+        raise ValueError(f"plan must be a contiguous CUDA tensor on {device}")
+    return plan.data_ptr(), _ws_bytes(plan)
+
+
+def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
+                  slopes=None, plan=None, stream=None):
+    """bf16 attention with capped, biased and masked scores: returns (o, lse).
+
+    q: bf16 [B, H, N, d]; k, v: bf16 [B, Hkv, N, d] with H a multiple of Hkv (query head
+    h reads head h // (H // Hkv)); any layout with contiguous d.  softcap > 0 caps a
+    score a to softcap * tanh(a / softcap); slopes (fp32 [H]) subtracts slopes[h] *
+    |i - j|; the mask is `causal`, or a plan of fa_mask_plan (then leave causal
+    False).  A row that sees no key gets o = 0 and lse = -inf.
+    """
+    import torch
+
+    lib = load_library()
+    B, H, N, d = q.shape
+    Hkv, dev, bf = k.shape[1], q.device, torch.bfloat16
+    sq = _check_layout("q", q, (B, H, N, d), bf, dev)
+    sk = _check_layout("k", k, (B, Hkv, N, d), bf, dev)
+    sv = _check_layout("v", v, (B, Hkv, N, d), bf, dev)
+    if o is None:
+        o = torch.empty((B, H, N, d), dtype=bf, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+    so = _check_layout("o", o, (B, H, N, d), bf, dev)
+    _check_flat("lse", lse, (B, H, N), torch.float32, dev)
+    _check_flat("slopes", slopes, (H,), torch.float32, dev)
+    pp, pb = _plan_args(plan, dev)
+    with torch.cuda.device(dev):
+        st = lib.fa_fwd_scored(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(o), so, _ptr(lse), B, H, Hkv, N, d, pp, pb,
+                               int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
+                               _ptr(slopes), _stream_handle(stream))
+    _check(st, "fa_fwd_scored")
+    return o, lse
+
+
+def fa_bwd_scored_workspace_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
+    """Bytes of device workspace fa_bwd_scored needs (0 if unsupported)."""
+    return int(load_library().fa_bwd_scored_workspace_size(B, H, Hkv, N, d))
+
+
+def fa_bwd_scored(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None, causal: bool = False,
+                  scale: float | None = None, softcap: float = 0.0, slopes=None, plan=None, stream=None,
+                  deterministic: bool = False):
+    """Gradients of fa_fwd_scored for the same arguments: returns (dq, dk, dv), bf16.
+
+    o, lse: the forward's outputs; do: bf16 [B, H, N, d].  dk and dv ([B, Hkv, N, d]) sum
+    over the query heads that share a head.  ``deterministic=True`` gives dq the same
+    bits on every run (dk and dv always have them).
+    """
+    import torch
+
+    lib = load_library()
+    B, H, N, d = q.shape
+    Hkv, dev, bf = k.shape[1], q.device, torch.bfloat16
+    qs, ks = (B, H, N, d), (B, Hkv, N, d)
+    dq = torch.empty(qs, dtype=bf, device=dev) if dq is None else dq
+    dk = torch.empty(ks, dtype=bf, device=dev) if dk is None else dk
+    dv = torch.empty(ks, dtype=bf, device=dev) if dv is None else dv
+    args = []
+    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs), ("do", do, qs)):
+        args += [_ptr(t), _check_layout(name, t, shape, bf, dev)]
+    args.append(_ptr(lse))
+    for name, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
+        args += [_ptr(t), _check_layout(name, t, shape, bf, dev)]
+    _check_flat("lse", lse, (B, H, N), torch.float32, dev)
+    _check_flat("slopes", slopes, (H,), torch.float32, dev)
+    pp, pb = _plan_args(plan, dev)
+    if workspace is None:
+        workspace = torch.empty(max(int(lib.fa_bwd_scored_workspace_size(B, H, Hkv, N, d)), 1), dtype=torch.uint8,
+                                device=dev)
+    workspace = _scratch(workspace, 0, dev)
+    with torch.cuda.device(dev):
+        st = lib.fa_bwd_scored(*args, _ptr(workspace), _ws_bytes(workspace), B, H, Hkv, N, d, pp, pb,
+                               int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
+                               _ptr(slopes), int(bool(deterministic)), _stream_handle(stream))
+    _check(st, "fa_bwd_scored")
+    return dq, dk, dv
+
+
+def _paged_dtype(t):
+    import torch
+
+    code = {torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"the cache must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _check_cache(k_cache, v_cache, page_table, seq_lens, dev):
+    import torch
+
+    shape = tuple(k_cache.shape)
+    if len(shape) != 4:
+        raise ValueError("k_cache must be indexed [n_pages, Hkv, page_size, d]")
+    sk = _check_layout("k_cache", k_cache, shape, k_cache.dtype, dev)
+    sv = _check_layout("v_cache", v_cache, shape, k_cache.dtype, dev)
+    B, max_pages = page_table.shape
+    if page_table.dtype != torch.int32 or page_table.device != dev or (max_pages > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be an int32 CUDA tensor [B, max_pages] with contiguous rows on {dev}")
+    _check_flat("seq_lens", seq_lens, (B,), torch.int32, dev)
+    return sk, sv, shape, B, max_pages, page_table.stride(0) if B > 1 else max(max_pages, page_table.stride(0))
+
+
+def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream=None):
+    """Write new tokens' keys and values into the pages of the cache (in place).
+
+    k, v: [T, Hkv, d], bf16 or fp16 as the cache; k_cache, v_cache: indexed
+    [n_pages, Hkv, page_size, d], any layout with contiguous d; page_table: int32
+    [B, max_pages]; seq_lens: int32 [B], lengths with the new tokens; cu_new: int32
+    [B + 1]: rows cu_new[b] .. cu_new[b + 1] - 1 are the last tokens of sequence b.
+    """
+    import torch
+
+    lib = load_library()
+    dev = k_cache.device
+    code = _paged_dtype(k_cache)
+    skc, svc, (n_pages, Hkv, page, d), B, max_pages, ts = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
+    T = k.shape[0]
+    sk = _check_layout("k", k, (T, Hkv, d), k_cache.dtype, dev)
+    sv = _check_layout("v", v, (T, Hkv, d), k_cache.dtype, dev)
+    _check_flat("cu_new", cu_new, (B + 1,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        st = lib.fa_paged_append(_ptr(k), sk, _ptr(v), sv, _ptr(k_cache), skc, _ptr(v_cache), svc, _ptr(page_table),
+                                 ts, _ptr(seq_lens), _ptr(cu_new), B, T, Hkv, d, page, n_pages, max_pages, code,
+                                 _stream_handle(stream))
+    _check(st, "fa_paged_append")
+
+
+def fa_paged_decode_workspace_size(B: int, H: int, Hkv: int, d: int) -> int:
+    """Bytes of device workspace fa_paged_decode needs on the current device (0 if unsupported)."""
+    return int(load_library().fa_paged_decode_workspace_size(B, H, Hkv, d))
+
+
+def fa_paged_decode(q, k_cache, v_cache, page_table, seq_lens, o=None, lse=None, workspace=None,
+                    scale: float | None = None, softcap: float = 0.0, slopes=None, stream=None):
+    """Attention of each sequence's last token over its paged cache: returns (o [B, H, d], lse fp32 [B, H]).
+
+    q: [B, H, d], bf16 or fp16 as the cache (laid out as for fa_paged_append); the
+    token's own key and value are in the cache and counted in seq_lens.  softcap and
+    slopes as fa_fwd_scored.  An empty sequence gets o = 0 and lse = -inf.
+    """
+    import torch
+
+    lib = load_library()
+    B, H, d = q.shape
+    dev, dt = q.device, q.dtype
+    code = _paged_dtype(k_cache)
+    skc, svc, (n_pages, Hkv, page, dc), Bt, max_pages, ts = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
+    if Bt != B or dc != d:
+        raise ValueError(f"q is for {B} sequences of head dim {d}, the page table for {Bt} and the cache for {dc}")
+    sq = _check_layout("q", q, (B, H, d), k_cache.dtype, dev)
+    if o is None:
+        o = torch.empty((B, H, d), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+    so = _check_layout("o", o, (B, H, d), dt, dev)
+    _check_flat("lse", lse, (B, H), torch.float32, dev)
+    _check_flat("slopes", slopes, (H,), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty(max(int(lib.fa_paged_decode_workspace_size(B, H, Hkv, d)), 1), dtype=torch.uint8,
+                                    device=dev)
+        workspace = _scratch(workspace, 0, dev)
+        st = lib.fa_paged_decode(_ptr(q), sq, _ptr(k_cache), skc, _ptr(v_cache), svc, _ptr(page_table), ts,
+                                 _ptr(seq_lens), _ptr(o), so, _ptr(lse), _ptr(workspace), _ws_bytes(workspace), B, H,
+                                 Hkv, d, page, n_pages, max_pages, code, d ** -0.5 if scale is None else float(scale),
+                                 float(softcap), _ptr(slopes), _stream_handle(stream))
+    _check(st, "fa_paged_decode")
     return o, lse
 
 

@@ -105,22 +105,33 @@ int validate_shape(int B, int H, int N, int d, int causal, float scale) {
 // Row, head and batch strides of a strided tensor (NULL: dense [B, H, N, d]).  Each
 // must be positive and a multiple of 8 elements (16 bytes), as the tensor maps need.
 int strides_or_dense(fa::Strides* out, const int64_t* s, int H, int N, int d) {
-  if (!s) {
-    *out = fa::dense_strides(H, N, d);
-    return FA_OK;
-  }
-  for (int i = 0; i < 3; ++i) {
-    if (s[i] <= 0 || s[i] > (int64_t(1) << 38)) return FA_ERR_INVALID_ARG;
-    if (s[i] % 8 != 0) return FA_ERR_MISALIGNED;
-    out->s[i] = s[i];
-  }
-  if (s[0] < d) return FA_ERR_INVALID_ARG;  // rows of one head may not overlap
-  return FA_OK;
+  return fa::strides_or(out, s, 3, fa::dense_strides(H, N, d), d);
 }
 
 }  // namespace
 
 namespace fa {
+
+int call_context(CallContext* c) {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds, &c->err_word);
+  c->dbg = knobs();
+  return st;
+}
+
+int strides_or(Strides* out, const int64_t* s, int n_strides, const Strides& dense, int d) {
+  if (!s) {
+    *out = dense;
+    return FA_OK;
+  }
+  for (int i = 0; i < n_strides; ++i) {
+    if (s[i] <= 0 || s[i] > (int64_t(1) << 38)) return FA_ERR_INVALID_ARG;
+    if (s[i] % 8 != 0) return FA_ERR_MISALIGNED;
+    out->s[i] = s[i];
+  }
+  if (s[0] < d) return FA_ERR_INVALID_ARG;  // rows may not overlap
+  return FA_OK;
+}
 
 cudaError_t make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes, int cols,
                          int rows, int depth, int box_cols, int box_rows) {

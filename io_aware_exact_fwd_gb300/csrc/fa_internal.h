@@ -31,6 +31,18 @@ inline Strides dense_strides(int H, int N, int d) {
   return Strides{{static_cast<int64_t>(d), static_cast<int64_t>(N) * d, static_cast<int64_t>(H) * N * d}};
 }
 
+// What a call needs of the current device, for entry points outside fa_api.cu: the
+// error word's address and the debug knobs.  Returns an fa_status (FA_ERR_UNSUPPORTED
+// on a device that is not sm_103).
+struct CallContext {
+  unsigned int* err_word;
+  DebugKnobs dbg;
+};
+int call_context(CallContext* c);
+// The first n_strides of `s` (innermost first, in elements), or `dense` for NULL.  Each
+// must be positive and a multiple of 8 elements, the innermost at least d.
+int strides_or(Strides* out, const int64_t* s, int n_strides, const Strides& dense, int d);
+
 struct FwdArgs {
   const void* q;
   const void* k;
@@ -212,6 +224,71 @@ int w4a16_chunks_per_split(int K, int n_split);
 // output row, no split and no workspace.
 bool w4a16_uses_gemv(int M, int K);
 cudaError_t launch_w4a16(const W4a16Args& a, cudaStream_t stream);
+
+// ------------------------------------------------ scored attention (fa_scored*.cu)
+
+// The mask as intervals (written by the plan kernel, fa_scored.cu): query i sees keys
+// [q[i].x, q[i].y), key j is seen by queries [k[j].x, k[j].y).  Both ends do not
+// decrease along a row of the batch; an empty interval has equal ends.
+struct MaskPlan {
+  const int2* q;  // [B, N], or NULL: no plan, the mask is `causal` alone
+  const int2* k;  // [B, N]
+};
+inline MaskPlan mask_plan_of(const void* plan, int B, int N) {
+  const int2* p = static_cast<const int2*>(plan);
+  return MaskPlan{p, p ? p + static_cast<size_t>(B) * N : nullptr};
+}
+cudaError_t launch_mask_plan(const int32_t* cu_docs, const int32_t* prefix, int n_docs, void* plan, int B, int N,
+                             int causal, cudaStream_t stream);
+
+// How scores are made from q . k: scale, tanh cap (0: none), slopes (NULL: none), the
+// mask, and the query heads that share a key/value head.
+struct ScoreArgs {
+  MaskPlan plan;
+  int causal;
+  float scale, softcap;
+  const float* slopes;
+  int Hkv;
+};
+cudaError_t launch_fwd_scored(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream);
+cudaError_t launch_bwd_scored(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream);
+
+// ------------------------------------------------------- paged cache (fa_paged.cu)
+
+struct PagedCache {
+  void* k;
+  void* v;
+  Strides sk, sv;            // element strides (row, head, page)
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  int B, Hkv, d, page_size, n_pages, max_pages;
+};
+struct PagedAppendArgs {
+  PagedCache c;
+  const void* k;
+  const void* v;
+  Strides sk, sv;            // (head, token)
+  const int32_t* cu_new;
+  int T;
+};
+struct PagedDecodeArgs {
+  PagedCache c;
+  const void* q;
+  void* o;
+  Strides sq, so;            // (head, batch)
+  float* lse;
+  void* workspace;
+  int H;
+  int fp16;                  // 0: bf16, 1: fp16
+  float scale, softcap;
+  const float* slopes;
+  unsigned int* err_word;
+  DebugKnobs dbg;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream);
+size_t paged_decode_workspace(int B, int H, int Hkv, int d);
 
 cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes, int cols,
                          int rows, int heads, int batch, const int64_t strides[3], int box_cols, int box_rows,

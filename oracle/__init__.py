@@ -32,6 +32,9 @@ check it against the pages by eye:
   textbook gradient on the dequantised operands (rounded to bf16), carried back
   through the rotation (dQ = (dQ' H) * s, dK likewise).  The pages give FP8 for
   the forward only; this is the plainest reading of its backward.
+* ``scored``     -- attention with capped, biased and masked scores and shared heads, its
+  gradient, and its decode over a paged cache.  The pages name none of these; the
+  definition is the dense one, pair by pair.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 ``--impl reference`` legs of ``bench.py`` may import this package.  The product
@@ -78,6 +81,7 @@ from .fp8_backward import (
     fp8_backward_from_operands,
     fp8_backward,
 )
+from .scored import visible, scored_forward, scored_backward, paged_gather, paged_decode, paged_append
 
 __all__ = [
     "attention_forward",
@@ -112,4 +116,10 @@ __all__ = [
     "fp8_operands",
     "fp8_backward_from_operands",
     "fp8_backward",
+    "visible",
+    "scored_forward",
+    "scored_backward",
+    "paged_gather",
+    "paged_decode",
+    "paged_append",
 ]

@@ -1,0 +1,272 @@
+"""Scored attention on the GPU against the float64 oracle, element by element.
+
+The bounds are the oracle's (oracle/scored.py): the roundings the path makes on purpose,
+2^-8 relative each, carried through the formulas, plus the fp32 error of the scores.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import io_aware_exact_fwd_gb300 as fa
+from oracle import scored_backward, scored_forward
+
+from gpu_util import host_f64, report
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fa.load_library()
+    fa.fa_debug_set_fault(0)
+    fa.fa_debug_set_wait_limit_ns(0)
+
+
+def _slopes(H):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], dtype=torch.float32, device="cuda")
+
+
+def _inputs(B, H, Hkv, N, d, seed, qscale=1.0, layout="bhnd"):
+    g = torch.Generator().manual_seed(seed)
+
+    def one(n, f=1.0):
+        x = (torch.randn(B, N, n, d, generator=g) * f).to(torch.bfloat16).cuda()
+        return x.transpose(1, 2) if layout == "bnhd" else x.transpose(1, 2).contiguous()
+    return one(H, qscale), one(Hkv), one(Hkv), one(H)
+
+
+def _docs(cu, prefix, causal, B, N):
+    if cu is None and prefix is None:
+        return None
+    t = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+    return fa.fa_mask_plan(B, N, t(cu), t(prefix), causal=causal, device="cuda")
+
+
+def _check(got, ref, bound, what):
+    got = host_f64(got)
+    same = np.isneginf(got) == np.isneginf(ref)
+    assert same.all(), f"{what}: -inf in {int((~same).sum())} places where the oracle has none, or the reverse"
+    fin = np.isfinite(ref)
+    assert np.isfinite(got[fin]).all(), f"{what}: not finite"
+    ratio = np.abs(got[fin] - ref[fin]) / np.maximum(bound[fin], 1e-300)
+    assert ratio.size == 0 or ratio.max() <= 1.0, f"{what}: error {ratio.max():.3f} of its bound"
+    return float(ratio.max(initial=0.0))
+
+
+# B, H, Hkv, N, d, causal, cap, bias, documents, prefix
+CASES = [
+    (1, 1, 1, 1, 64, True, 0.0, False, None, None),
+    (1, 2, 1, 1, 128, False, 30.0, True, None, None),
+    (1, 2, 2, 127, 64, True, 30.0, False, None, None),
+    (1, 2, 2, 128, 128, False, 0.0, True, None, None),
+    (1, 3, 1, 129, 128, True, 50.0, True, None, None),
+    (2, 4, 2, 257, 64, False, 20.0, False, None, None),
+    (1, 2, 2, 600, 128, True, 0.0, True, None, None),
+    (1, 2, 1, 700, 64, True, 0.0, False, [[0, 3, 3, 260, 555]], None),
+    (2, 2, 1, 300, 128, True, 20.0, True, [[0, 1, 128, 300], [5, 100, 100, 129]], [[1, 40, 90], [95, 3, 0]]),
+    (1, 2, 2, 513, 64, False, 0.0, True, [[0, 200, 213, 512]], None),
+    (1, 2, 2, 513, 128, False, 8.0, False, [[130, 200, 256, 384]], None),
+    (2, 2, 2, 200, 128, True, 30.0, False, [[0, 0], [0, 200]], None),          # one row all padding
+    (1, 8, 1, 384, 64, True, 0.0, False, None, [[300]]),                       # a prefix and no documents
+    (1, 5, 5, 130, 128, True, 5.0, False, [[0, 130]], [[1000]]),               # the prefix passes the end
+    (1, 2, 1, 1100, 128, True, 0.0, True, [[0, 500, 1100]], [[499, 30]]),
+    (3, 2, 2, 65, 64, True, 0.0, False, [[64, 65, 65], [0, 1, 2], [0, 64, 65]], None),
+]
+
+
+def _kw(case, plan):
+    B, H, Hkv, N, d, causal, cap, bias, cu, pre = case
+    return dict(causal=causal and plan is None, softcap=cap, slopes=_slopes(H) if bias else None, plan=plan)
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_forward_and_gradients(case, layout):
+    B, H, Hkv, N, d, causal, cap, bias, cu, pre = case
+    q, k, v, do = _inputs(B, H, Hkv, N, d, 11 + N, 3.0 if cap else 1.0, layout)
+    plan = _docs(cu, pre, causal, B, N)
+    kw = _kw(case, plan)
+    slopes = None if not bias else _slopes(H).cpu().numpy()
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    fa.fa_sync_check()
+    args = (d ** -0.5, causal, cap, slopes, cu, pre)
+    x = [host_f64(t) for t in (q, k, v, do)]
+    o_ref, lse_ref, ob, lb = scored_forward(*x[:3], *args)
+    r = {"o": _check(o, o_ref, ob, "O"), "lse": _check(lse, lse_ref, lb, "LSE")}
+    for det in (False, True):
+        grads = fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=det, **kw)
+        fa.fa_sync_check()
+        refs, bounds = scored_backward(*x, *args)
+        for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
+            r[name] = _check(a, ref, bd, f"{name} deterministic={det}")
+    report(f"scored {case} {layout} (shares of the bounds)", **r)
+
+
+def test_large_scores_and_slopes():
+    # Scores far past the cap on both sides, and slopes that leave only the nearest keys.
+    B, H, N, d = 1, 2, 300, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 5, 40.0)
+    slopes = torch.tensor([8.0, -0.03], device="cuda")
+    for causal in (False, True):
+        o, lse = fa.fa_fwd_scored(q, k, v, causal=causal, softcap=10.0, slopes=slopes)
+        fa.fa_sync_check()
+        x = [host_f64(t) for t in (q, k, v, do)]
+        o_ref, lse_ref, ob, lb = scored_forward(*x[:3], d ** -0.5, causal, 10.0, slopes.cpu().numpy())
+        _check(o, o_ref, ob, "O")
+        _check(lse, lse_ref, lb, "LSE")
+        grads = fa.fa_bwd_scored(q, k, v, o, do, lse, causal=causal, softcap=10.0, slopes=slopes)
+        fa.fa_sync_check()
+        refs, bounds = scored_backward(*x, d ** -0.5, causal, 10.0, slopes.cpu().numpy())
+        for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
+            _check(a, ref, bd, name)
+
+
+def test_scores_that_fall_and_rise_along_the_keys():
+    # Row maxima far apart between key blocks, both ways, without a cap: -400 to 400.
+    B, H, N, d = 1, 1, 640, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 6)
+    ramp = torch.linspace(-1, 1, N, device="cuda")[None, None, :, None]
+    for sign in (1.0, -1.0):
+        qq = torch.ones_like(q) * 8.0
+        kk = (sign * ramp * 50.0 * torch.ones_like(k) + 0.1 * k).to(torch.bfloat16)
+        plan = _docs([[0, 333, 600]], None, True, B, N)
+        o, lse = fa.fa_fwd_scored(qq, kk, v, plan=plan)
+        fa.fa_sync_check()
+        x = [host_f64(t) for t in (qq, kk, v, do)]
+        o_ref, lse_ref, ob, lb = scored_forward(*x[:3], d ** -0.5, True, 0.0, None, [[0, 333, 600]])
+        _check(o, o_ref, ob, "O")
+        _check(lse, lse_ref, lb, "LSE")
+
+
+def test_without_options_it_agrees_with_fa_fwd():
+    q, k, v, _ = _inputs(2, 3, 3, 300, 128, 8)
+    for causal in (False, True):
+        o, lse = fa.fa_fwd_scored(q, k, v, causal=causal)
+        o1, lse1 = fa.fa_fwd(q, k, v, causal=causal)
+        fa.fa_sync_check()
+        # Both are within 2^-8 (P) + 2^-8 (O) of the same value.
+        assert float((lse - lse1).abs().max()) <= 1e-5
+        assert float((o.float() - o1.float()).abs().max()) <= 2 * 2.0 ** -7 * float(v.float().abs().max())
+
+
+def test_same_bits_on_every_run():
+    q, k, v, do = _inputs(1, 4, 2, 700, 64, 9, 3.0)
+    plan = _docs([[0, 300, 690]], [[20, 50]], True, 1, 700)
+    kw = dict(softcap=20.0, slopes=_slopes(4), plan=plan)
+    runs = []
+    for _ in range(3):
+        o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+        runs.append((o, lse, *fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, **kw)))
+    fa.fa_sync_check()
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            assert torch.equal(a, b)
+
+
+def test_outputs_of_another_layout_and_neighbours_untouched():
+    # o, dq, dk, dv as views of larger buffers: what lies between their rows stays.
+    B, H, Hkv, N, d = 1, 2, 1, 150, 64
+    q, k, v, do = _inputs(B, H, Hkv, N, d, 10, layout="bnhd")
+    kw = dict(causal=True, softcap=15.0)
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    ref = (o, *fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, **kw))
+    bufs, views = [], []
+    for n in (H, H, Hkv, Hkv):
+        buf = torch.full((B, N + 3, n + 1, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+        bufs.append(buf)
+        views.append(buf[:, :N, :n, :d].transpose(1, 2))
+    o2, _ = fa.fa_fwd_scored(q, k, v, o=views[0], **kw)
+    fa.fa_bwd_scored(q, k, v, o, do, lse, dq=views[1], dk=views[2], dv=views[3], deterministic=True, **kw)
+    fa.fa_sync_check()
+    for buf, view, want in zip(bufs, views, ref):
+        assert torch.equal(view, want)
+        rest = buf.clone()
+        rest[:, :N, :view.shape[1], :d] = 7.0
+        assert torch.equal(rest, torch.full_like(rest, 7.0))
+
+
+def test_captured_step_replays_with_new_inputs_and_documents():
+    # plan, forward and backward in one graph on a side stream; replayed after the inputs and the
+    # document offsets changed in place.
+    B, H, N, d = 1, 2, 260, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 12)
+    cu = torch.tensor([[0, 100, 260]], dtype=torch.int32, device="cuda")
+    plan = fa.fa_mask_plan(B, N, cu)
+    o, lse = torch.empty_like(q), torch.empty(B, H, N, device="cuda")
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    ws = torch.empty(fa.fa_bwd_scored_workspace_size(B, H, H, N, d), dtype=torch.uint8, device="cuda")
+
+    def step():
+        fa.fa_mask_plan(B, N, cu, plan=plan)
+        fa.fa_fwd_scored(q, k, v, o=o, lse=lse, softcap=25.0, plan=plan)
+        fa.fa_bwd_scored(q, k, v, o, do, lse, dq=dq, dk=dk, dv=dv, workspace=ws, softcap=25.0, plan=plan, deterministic=True)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    cu.copy_(torch.tensor([[0, 31, 250]], dtype=torch.int32))
+    q2, k2, v2, do2 = _inputs(B, H, H, N, d, 13)
+    for a, b in ((q, q2), (k, k2), (v, v2), (do, do2)):
+        a.copy_(b)
+    g.replay()
+    got = [t.clone() for t in (o, lse, dq, dk, dv)]
+    step()
+    fa.fa_sync_check()
+    for a, b in zip(got, (o, lse, dq, dk, dv)):
+        assert torch.equal(a, b)
+    o_ref, lse_ref, ob, lb = scored_forward(*(host_f64(t) for t in (q, k, v)), d ** -0.5, True, 25.0, None, [[0, 31, 250]])
+    _check(o, o_ref, ob, "O")
+    _check(lse, lse_ref, lb, "LSE")
+
+
+def test_two_streams_at_once():
+    ins = [_inputs(1, 4, 2, 500, 128, 20 + n) for n in range(2)]
+    want = []
+    for q, k, v, do in ins:
+        o, lse = fa.fa_fwd_scored(q, k, v, causal=True, softcap=30.0)
+        want.append((o, lse, *fa.fa_bwd_scored(q, k, v, o, do, lse, causal=True, softcap=30.0, deterministic=True)))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ins], []
+    for (q, k, v, do), s in zip(ins, streams):
+        with torch.cuda.stream(s):
+            o, lse = fa.fa_fwd_scored(q, k, v, causal=True, softcap=30.0)
+            got.append((o, lse, *fa.fa_bwd_scored(q, k, v, o, do, lse, causal=True, softcap=30.0, deterministic=True)))
+    torch.cuda.synchronize()
+    fa.fa_sync_check()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_offsets_that_break_the_contract_stay_in_bounds():
+    # Decreasing and out-of-range offsets: unspecified values, but finite ones, no error, and no
+    # write outside the outputs (canaries around them).
+    B, H, N, d = 1, 2, 400, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 14)
+    for cu in ([[-50, 300, 100, 9999]], [[390, 10, 380, 20]], [[500, 600, 700, 800]], [[-9, -8, -7, -6]]):
+        plan = _docs(cu, [[7, -3, 2 ** 31 - 1]], True, B, N)
+        buf = torch.full((B, H + 2, N, d), 3.0, dtype=torch.bfloat16, device="cuda")
+        o, lse = fa.fa_fwd_scored(q, k, v, o=buf[:, 1:-1], plan=plan)
+        fa.fa_bwd_scored(q, k, v, o, do, lse, plan=plan)
+        fa.fa_sync_check()
+        assert bool((buf[:, 0] == 3).all()) and bool((buf[:, -1] == 3).all())
+
+
+def test_refusals_in_the_binding():
+    q, k, v, do = _inputs(1, 4, 2, 64, 64, 15)
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_scored(q, k, v, causal=True, plan=fa.fa_mask_plan(1, 64, device="cuda"))
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_scored(q, k, v, plan=fa.fa_mask_plan(1, 32, device="cuda"))  # a plan for fewer positions
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_scored(q[:, :3].contiguous(), k, v)
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_scored(q, k[:, :1].expand(1, 4, 64, 64), v[:, :1].expand(1, 4, 64, 64))  # a stride of 0
+    with pytest.raises(ValueError):
+        fa.fa_fwd_scored(q, k, v, slopes=torch.ones(3, device="cuda"))
+    with pytest.raises(ValueError):
+        fa.fa_fwd_scored(q, k, v, slopes=torch.ones(4))
+    with pytest.raises(ValueError):
+        fa.fa_fwd_scored(q.transpose(2, 3), k, v)
