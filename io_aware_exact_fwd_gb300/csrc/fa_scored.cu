@@ -1,10 +1,11 @@
-// Scored attention: the mask plan, and the forward and backward in their simplest form,
-// one warp per row on the CUDA cores (the formulas: include/fa.h).
+// Scored attention: the mask plan, and the backward in its simplest form, one warp per
+// row on the CUDA cores (the formulas: include/fa.h).
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "fa_score.cuh"
 
 namespace fa {
 namespace {
@@ -52,16 +53,6 @@ __global__ void __launch_bounds__(256) mask_plan_kernel(const int32_t* __restric
   ki[r] = make_int2(causal && i >= reach ? i : s, e);
 }
 
-// The interval of keys that query i sees, and of queries that see key j.
-__device__ __forceinline__ int2 keys_of(const MaskPlan& p, int causal, int b, int i, int N) {
-  if (p.q) return p.q[static_cast<size_t>(b) * N + i];
-  return make_int2(0, causal ? i + 1 : N);
-}
-__device__ __forceinline__ int2 queries_of(const MaskPlan& p, int causal, int b, int j, int N) {
-  if (p.k) return p.k[static_cast<size_t>(b) * N + j];
-  return make_int2(causal ? j : 0, N);
-}
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
@@ -100,34 +91,6 @@ __device__ __forceinline__ float score(float qk, const ScoreArgs& sc, float slop
     bend = 1.f - t * t;
   }
   return a - slope * fabsf(static_cast<float>(i - j));
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) fwd_rows_kernel(FwdArgs a, ScoreArgs sc, long long rows) {
-  constexpr int E = D / 32;
-  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  const int i = static_cast<int>(r % a.N), h = static_cast<int>(r / a.N % a.H), b = static_cast<int>(r / a.N / a.H);
-  const int hk = h / (a.H / sc.Hkv);
-  const float slope = sc.slopes ? sc.slopes[h] : 0.f;
-  const int2 see = keys_of(sc.plan, sc.causal, b, i, a.N);
-  float q[E], k[E], v[E], o[E] = {}, m = -INFINITY, l = 0.f, bend;
-  load_row(q, a.q, a.sq, b, h, i);
-  for (int j = see.x; j < see.y; ++j) {
-    load_row(k, a.k, a.sk, b, hk, j);
-    load_row(v, a.v, a.sv, b, hk, j);
-    const float s = score(dot(q, k), sc, slope, i, j, bend);
-    const float mn = fmaxf(m, s), w = expf(m - mn), p = expf(s - mn);
-    l = l * w + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * w + p * v[e];
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] *= inv;
-  store_row(o, a.o, a.so, b, h, i);
-  if ((threadIdx.x & 31) == 0) a.lse[r] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 // One warp per query row: dQ.
@@ -198,13 +161,6 @@ cudaError_t launch_mask_plan(const int32_t* cu_docs, const int32_t* prefix, int 
   int2* qi = static_cast<int2*>(plan);
   mask_plan_kernel<<<static_cast<unsigned>((rows + 255) / 256), 256, 0, stream>>>(cu_docs, prefix, n_docs, qi,
                                                                                   qi + rows, N, rows, causal);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_fwd_scored(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(a.B) * a.H * a.N;
-  auto kern = a.d == 64 ? fwd_rows_kernel<64> : fwd_rows_kernel<128>;
-  kern<<<blocks_of(rows), 128, 0, stream>>>(a, sc, rows);
   return cudaGetLastError();
 }
 

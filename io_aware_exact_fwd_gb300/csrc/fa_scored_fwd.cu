@@ -1,0 +1,668 @@
+// Scored attention forward for sm_103a: tanh cap, distance bias, interval masks
+// (documents, prefixes), shared key/value heads.  bf16 in and out, fp32 logsumexp.
+//
+// The pipeline is the plain forward's (fa_fwd.cu): persistent CTAs, each unit 256 query
+// rows of one head as two 128-row tiles; K_j, V_j stream through a TMA ring; one thread
+// issues S_t = Q_t K_j^T and O_t += P_t V_j on tcgen05 with S, P and O in TMEM; two
+// softmax warpgroups hold one query row per thread.  What differs:
+//
+//  * The keys of a tile are the blocks between its first row's first key and its last
+//    row's last key (intervals of the plan, both ends nondecreasing along the rows), so
+//    blocks of other documents are never loaded.  A unit streams the union of its two
+//    tiles' blocks, and each tile takes part in a contiguous run of that stream.
+//  * The stream runs from the last block to the first.  A causal row then meets its
+//    diagonal block first, where a distance bias is smallest, so the reference maximum
+//    of the first block holds for the rest (forward order would raise every row's
+//    maximum in every block) and no row of a document waits masked for its first key.
+//  * Scores are put in place in log2 units (cap, bias, mask) before the softmax.
+#include <math.h>
+
+#include "fa_device.cuh"
+#include "fa_internal.h"
+#include "fa_score.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kTiles = 2;                       // query tiles per unit
+constexpr int kUnitRows = kTiles * kBlockQ;
+constexpr int kThreads = 384;                   // warps 0-7 softmax (2 groups), 8 K/V TMA, 9 MMA, 10 Q TMA, 11 spare
+constexpr int kWarpLoad = 8;
+constexpr int kWarpMma = 9;
+constexpr int kWarpLoadQ = 10;
+// 168 registers x 384 threads at launch = 2 x 128 x 216 + 128 x 72.
+constexpr uint32_t kRegsSoftmax = 216;
+constexpr uint32_t kRegsControl = 72;
+constexpr uint32_t kRegsNeeded = 2 * 128 * kRegsSoftmax + 128 * kRegsControl;
+static_assert(kRegsNeeded <= 65536, "register split exceeds the SM register file");
+constexpr uint32_t kTmemCols = 512;
+// A block is exponentiated against the running reference without its own maximum; its
+// row sum then proves that no P passed 2^16 (else the block is redone).
+constexpr float kSpeculationSumBound = 65536.0f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum : uint32_t {
+  kSiteLoadEmpty = 0x121,
+  kSiteLoadQ = 0x122,
+  kSiteMmaQ = 0x221,
+  kSiteMmaK = 0x222,
+  kSiteMmaP = 0x223,
+  kSiteMmaV = 0x224,
+  kSiteSoftS = 0x321,
+  kSiteSoftO = 0x322,
+  kSiteEpi = 0x323,
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kBoxes = kRowBytes / 128;
+  static constexpr int kBoxBytes = kBlockK * 128;
+  static constexpr int kTileBytes = kBlockK * kRowBytes;
+  static constexpr int kKSteps = D / 16;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kQOff = 0;
+  static constexpr int kOOff = kTiles * kTileBytes;     // O staging, shared by both tiles in turn
+  static constexpr int kRingOff = kOOff + kTileBytes;
+  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], epi[2], stg, drain
+  static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+  static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * static_cast<uint32_t>(t); }
+  static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * static_cast<uint32_t>(t); }
+};
+
+struct Params {
+  MaskPlan plan;
+  int causal, N, H, group, BH, nunits;
+  float scale_log2;   // scale log2(e)
+  float cap_in;       // scale / softcap
+  float cap_out;      // softcap log2(e)
+  const float* slopes;
+  float* lse;
+  unsigned int* err_word;
+  unsigned long long wait_ns;
+};
+
+// A unit's key blocks: tile t attends blocks [begin[t], end[t]) (empty: begin = end = 0),
+// the stream covers [first, last) from last - 1 down.
+struct Span {
+  int begin[kTiles], end[kTiles], first, last;
+  __device__ __forceinline__ int count() const { return last - first; }
+  // Tile t's run of the stream.
+  __device__ __forceinline__ int from(int t) const { return last - end[t]; }
+  __device__ __forceinline__ int to(int t) const { return last - begin[t]; }
+  __device__ __forceinline__ bool has(int t) const { return end[t] > begin[t]; }
+};
+// Blocks [x, y) of the tile whose first row is r0.
+__device__ __forceinline__ int2 tile_blocks(const Params& p, int r0, int b) {
+  if (r0 >= p.N) return make_int2(0, 0);
+  const int lo = keys_of(p.plan, p.causal, b, r0, p.N).x;
+  const int hi = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N).y;
+  return hi > lo ? make_int2(lo / kBlockK, (hi + kBlockK - 1) / kBlockK) : make_int2(0, 0);
+}
+__device__ __forceinline__ Span span_of(const Params& p, int u, int b) {
+  Span s;
+  s.first = 0x7fffffff;
+  s.last = 0;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int2 x = tile_blocks(p, u * kUnitRows + t * kBlockQ, b);
+    s.begin[t] = x.x;
+    s.end[t] = x.y;
+    if (x.y > x.x) {
+      s.first = min(s.first, x.x);
+      s.last = max(s.last, x.y);
+    }
+  }
+  s.first = min(s.first, s.last);
+  return s;
+}
+
+// k-th unit of CTA c out of G: zigzag passes over units numbered last rows first (the
+// heaviest, when causal), heads next to one another.
+struct Unit {
+  int u, bh;
+};
+__device__ __forceinline__ bool unit_at(int k, int c, int G, const Params& p, Unit& x) {
+  const int w = k * G + ((k & 1) ? (G - 1 - c) : c);
+  if (w >= p.nunits * p.BH) return false;
+  x.u = p.nunits - 1 - w / p.BH;
+  x.bh = w % p.BH;
+  return true;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc, uint32_t site) {
+  const bool ok = mbar_wait(bar, parity, wc, site);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_wait_suspend(uint64_t* bar, uint32_t parity, const WaitCtl& wc, uint32_t site) {
+  const bool ok = mbar_wait_suspend(bar, parity, wc, site, 20000u);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// MODE 0: scores as they are; 1: with a distance bias; 2: capped (and biased if slopes).
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                      const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::kQOff;
+  uint8_t* sO = smem + C::kOOff;
+  uint8_t* sRing = smem + C::kRingOff;
+  uint64_t* bar_q = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [2] per tile: Q landed
+  uint64_t* bar_qe = bar_q + 2;              // [2] per tile: last Q K^T of a unit done (Q slot free)
+  uint64_t* bar_full = bar_qe + 2;           // [kSlots]
+  uint64_t* bar_empty = bar_full + C::kSlots;
+  uint64_t* bar_s = bar_empty + C::kSlots;   // [2] per tile: S ready
+  uint64_t* bar_p = bar_s + 2;               // [2] per tile: P written
+  uint64_t* bar_o = bar_p + 2;               // [2] per tile: last P V of a unit done
+  uint64_t* bar_epi = bar_o + 2;             // [2] per tile: O staged in shared memory
+  uint64_t* bar_stg = bar_epi + 2;           // O staging buffer read out by the previous store
+  uint64_t* bar_drain = bar_stg + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(&bar_q[t], 1);
+      mbar_init(&bar_qe[t], 1);
+      mbar_init(&bar_s[t], 1);
+      mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_o[t], 1);
+      mbar_init(&bar_epi[t], 4);
+    }
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], 1);
+    }
+    mbar_init(bar_stg, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_o);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
+
+  if (warp >= 8) {
+    regs_decrease<kRegsControl>();
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------------- K/V TMA producer
+      if (lane == 0) {
+        int issued = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          Unit x;
+          if (!unit_at(k, cta, G, p, x)) break;
+          const int b = x.bh / p.H, hk = (x.bh % p.H) / p.group;
+          const Span sp = span_of(p, x.u, b);
+          for (int j = sp.last - 1; ok && j >= sp.first; --j) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {  // K_j, then V_j
+              const int slot = issued % C::kSlots;
+              if (!(ok = mbar_wait(&bar_empty[slot], ((issued / C::kSlots) & 1) ^ 1, wc, kSiteLoadEmpty))) break;
+              mbar_arrive_expect_tx(&bar_full[slot], C::kTileBytes);
+              uint8_t* dst = sRing + slot * C::kTileBytes;
+#pragma unroll
+              for (int c = 0; c < C::kBoxes; ++c)
+                tma_load_4d(dst + c * C::kBoxBytes, kv ? &tm_v : &tm_k, &bar_full[slot], c * kBoxCols, j * kBlockK,
+                            hk, b);
+              ++issued;
+            }
+          }
+        }
+        if (!ok)  // drain: the last (up to kSlots) issued copies may still be landing
+          for (int t = max(0, issued - C::kSlots); t < issued; ++t)
+            mbar_wait_drain(&bar_full[t % C::kSlots], (t / C::kSlots) & 1, p.wait_ns);
+      }
+      __syncwarp();
+    } else if (warp == kWarpLoadQ) {
+      // --------------------------------------------------------- Q TMA producer
+      if (lane == 0) {
+        int nload[kTiles] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          Unit x;
+          if (!unit_at(k, cta, G, p, x)) break;
+          const int b = x.bh / p.H, h = x.bh % p.H;
+          const Span sp = span_of(p, x.u, b);
+#pragma unroll
+          for (int tt = 0; tt < kTiles; ++tt) {
+            const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
+            if (!ok || !sp.has(t)) continue;
+            if (nload[t] > 0 && !(ok = mbar_wait(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ))) continue;
+            mbar_arrive_expect_tx(&bar_q[t], C::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < C::kBoxes; ++c)
+              tma_load_4d(sQ + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, &bar_q[t], c * kBoxCols,
+                          x.u * kUnitRows + t * kBlockQ, h, b);
+            ++nload[t];
+          }
+        }
+        if (!ok)
+          for (int t = 0; t < kTiles; ++t)
+            if (nload[t] > 0) mbar_wait_drain(&bar_q[t], (nload[t] - 1) & 1, p.wait_ns);
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockQ, kBlockK, 0, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kBlockQ, D, 0, 1);
+        const uint64_t qdesc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t kdesc = sdesc_sw128(smem_u32(sRing), 16, 1024);
+        const uint64_t vdesc = sdesc_sw128(smem_u32(sRing), C::kBoxBytes, 1024);
+        auto qk = [&](int t, int slot) {  // S_t = Q_t K^T: both K-major, 16 columns of d per MMA
+          const uint64_t qd = sdesc_add(qdesc, t * C::kTileBytes);
+          const uint64_t kd = sdesc_add(kdesc, slot * C::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < C::kKSteps; ++kk) {
+            const uint32_t off = (kk / 4) * C::kBoxBytes + (kk % 4) * 32;
+            mma_bf16_ss(tmem + C::col_s(t), sdesc_add(qd, off), sdesc_add(kd, off), idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bar_s[t]);
+        };
+        auto pv = [&](int t, int slot, bool accumulate) {  // O_t += P_t V: P from TMEM, V MN-major
+          const uint64_t vd = sdesc_add(vdesc, slot * C::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            mma_bf16_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, sdesc_add(vd, kk * 16 * 128), idesc_pv,
+                        (accumulate || kk > 0) ? 1u : 0u);
+        };
+        int item = 0;  // ring index of the next K or V block to consume
+        uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q tiles and P blocks consumed so far
+        bool ok = true;
+        Unit x{0, 0}, nx{0, 0};
+        bool more = unit_at(0, cta, G, p, x);
+        Span sp{}, nsp{};
+        if (more) sp = span_of(p, x.u, x.bh / p.H);
+        for (int k = 0; ok && more; ++k, x = nx, sp = nsp) {
+          // The next unit's intervals are fetched while this unit runs.
+          more = unit_at(k + 1, cta, G, p, nx);
+          if (more) nsp = span_of(p, nx.u, nx.bh / p.H);
+          const int n = sp.count();
+          // Stream position s: K_s is ring item 2 s, V_s item 2 s + 1 of the unit.  S_t of position
+          // s is issued right after the P_t V of position s - 1 (position 0: before the loop).
+          for (int s = -1; ok && s < n; ++s) {
+            const int slot_v = item % C::kSlots;
+            if (s >= 0) {
+              if (!(ok = mbar_wait(&bar_full[slot_v], (item / C::kSlots) & 1, wc, kSiteMmaV))) break;
+              ++item;
+            }
+            const bool has_next = s + 1 < n;
+            const int slot_k = item % C::kSlots;
+            const uint32_t par_k = (item / C::kSlots) & 1;
+            if (has_next) ++item;
+            bool k_ready = false;
+#pragma unroll
+            for (int tt = 0; tt < kTiles; ++tt) {
+              const int t = kTiles - 1 - tt;
+              const int f = sp.from(t), l = sp.has(t) ? sp.to(t) : f;
+              if (ok && s >= f && s < l) {
+                if (!(ok = mbar_wait(&bar_p[t], (t ? np1 : np0) & 1, wc, kSiteMmaP))) continue;
+                if (t) ++np1; else ++np0;
+                tc_fence_after();
+                pv(t, slot_v, s > f);
+                if (s + 1 == l) mma_commit(&bar_o[t]);
+              }
+              if (ok && s + 1 >= f && s + 1 < l) {
+                if (!k_ready) {
+                  if (!(ok = mbar_wait(&bar_full[slot_k], par_k, wc, kSiteMmaK))) continue;
+                  k_ready = true;
+                }
+                if (s + 1 == f) {
+                  if (!(ok = mbar_wait(&bar_q[t], (t ? nq1 : nq0) & 1, wc, kSiteMmaQ))) continue;
+                  if (t) ++nq1; else ++nq0;
+                }
+                tc_fence_after();
+                qk(t, slot_k);
+                if (s + 2 == l) mma_commit(&bar_qe[t]);
+              }
+            }
+            if (!ok) break;
+            if (s >= 0) mma_commit(&bar_empty[slot_v]);
+            if (has_next) {
+              if (!k_ready && !(ok = mbar_wait(&bar_full[slot_k], par_k, wc, kSiteMmaK))) break;
+              mma_commit(&bar_empty[slot_k]);
+            }
+          }
+        }
+        mma_commit(bar_drain);  // every issued MMA must finish before TMEM is released
+        mbar_wait_drain(bar_drain, 0, p.wait_ns);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    // ------------------------------------------ softmax warpgroups (0-3, 4-7)
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t col_s = C::col_s(t), col_o = C::col_o(t);
+    uint32_t scnt = 0;   // S blocks consumed so far (bar_s phase)
+    uint32_t nout = 0;   // units of this tile with keys (bar_o phase)
+    uint32_t nepi = 0;   // epilogues of this tile (bar_epi phase)
+    uint32_t nstg = 0;   // epilogues of both tiles before this unit's (bar_stg phase)
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Unit x;
+      if (!unit_at(k, cta, G, p, x)) break;
+      const int b = x.bh / p.H, h = x.bh % p.H;
+      const int row0 = x.u * kUnitRows + t * kBlockQ;
+      const uint32_t my_stg = nstg + static_cast<uint32_t>(t);
+      nstg += x.u * kUnitRows + kBlockQ < p.N ? 2u : 1u;
+      if (row0 >= p.N) continue;
+      const int qrow = row0 + row;
+      const int2 blocks = tile_blocks(p, row0, b);
+      const int2 see = qrow < p.N ? keys_of(p.plan, p.causal, b, qrow, p.N) : make_int2(0, 0);
+      // Keys that every row of the tile sees: [all_lo, all_hi).
+      const int all_lo = keys_of(p.plan, p.causal, b, min(row0 + kBlockQ, p.N) - 1, p.N).x;
+      const int all_hi = keys_of(p.plan, p.causal, b, row0, p.N).y;
+      const float slope2 = MODE != 0 && p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
+      const int nkt = blocks.y - blocks.x;
+      float m_used = 0.f;  // reference maximum, log2 units (0 until the row has seen a key)
+      bool seen = false;
+      float l = 0.f;
+
+      for (int j = 0; j < nkt; ++j, ++scnt) {
+        if (!warp_wait_suspend(&bar_s[t], scnt & 1, wc, kSiteSoftS)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int kbase = (blocks.y - 1 - j) * kBlockK;
+        const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
+        // Sign of j - i over the block: all <= 0, all >= 0, or mixed.
+        const bool left = kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
+        uint32_t r[4][32];
+        // Chunk c's scores in log2 units, in place: cap, bias, mask.  MODE 0 keeps the raw
+        // products (their scale is folded into the exponentials).
+        auto score = [&](int c) {
+          if constexpr (MODE == 2) {
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx = max3(mx, fabsf(__uint_as_float(r[c][i])), fabsf(__uint_as_float(r[c][i + 1])));
+            if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[c][i] = __float_as_uint(p.cap_out * tanh_any(__uint_as_float(r[c][i]) * p.cap_in));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                const float2 y = __fmul2_rn(tanh_small(__fmul2_rn(s, pair(p.cap_in))), pair(p.cap_out));
+                r[c][i] = __float_as_uint(y.x);
+                r[c][i + 1] = __float_as_uint(y.y);
+              }
+            }
+          }
+          if (MODE == 1 || (MODE == 2 && p.slopes)) {
+            const float mul = MODE == 1 ? p.scale_log2 : 1.f;
+            const float off = static_cast<float>(kbase + c * 32 - qrow);  // j - i of the chunk's first key
+            if (left || right) {
+              const float sg = left ? slope2 : -slope2;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 dist = __fadd2_rn(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), pair(off));
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])),
+                                            pair(mul), __fmul2_rn(dist, pair(sg)));
+                r[c][i] = __float_as_uint(y.x);
+                r[c][i + 1] = __float_as_uint(y.y);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                r[c][i] = __float_as_uint(
+                    fmaf(__uint_as_float(r[c][i]), mul, -slope2 * fabsf(off + static_cast<float>(i))));
+            }
+          }
+          if (need_mask) {
+            const int a = see.x - kbase - c * 32, e = see.y - kbase - c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < a || i >= e) r[c][i] = __float_as_uint(-INFINITY);
+          }
+        };
+        const float c_mul = MODE == 0 ? p.scale_log2 : 1.f;
+        auto tile_max = [&]() -> float {
+          float mc[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float a[11];
+#pragma unroll
+            for (int i = 0; i < 10; ++i)
+              a[i] = max3(__uint_as_float(r[c][3 * i]), __uint_as_float(r[c][3 * i + 1]),
+                          __uint_as_float(r[c][3 * i + 2]));
+            a[10] = fmaxf(__uint_as_float(r[c][30]), __uint_as_float(r[c][31]));
+            mc[c] = fmaxf(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
+                          fmaxf(a[9], a[10]));
+          }
+          return fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * c_mul;  // c_mul > 0
+        };
+        // P = exp2(score - m) over chunk c, packed bf16 over the S columns.
+        float2 part;
+        auto exp_chunk = [&](int c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 s = make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1]));
+            const float2 y = MODE == 0 ? __ffma2_rn(s, pair(c_mul), pair(-m_used)) : __fadd2_rn(s, pair(-m_used));
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            part = __fadd2_rn(part, e);
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st16(trow + col_s + c * 16, pk);
+        };
+        // The block against its own maximum: the reference moves up to it where it is higher (or
+        // the row's first), and O_t, which holds P V of the earlier blocks, is rescaled.
+        auto with_own_max = [&]() {
+          const float mt = tile_max();
+          const bool first = !seen && mt > -INFINITY;
+          const bool up = first || mt > m_used;
+          const float alpha = up && seen ? ex2_approx(m_used - mt) : 1.f;
+          const bool scale_o = up && seen;
+          if (up && mt > -INFINITY) m_used = mt;
+          seen = seen || first;
+          l *= alpha;
+          if (j > 0 && __any_sync(0xffffffffu, scale_o)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(trow + col_o + c * 32, o);
+              tmem_ld_wait32(o);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y =
+                    __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pair(alpha));
+                o[i] = __float_as_uint(y.x);
+                o[i + 1] = __float_as_uint(y.y);
+              }
+              tmem_st32(trow + col_o + c * 32, o);
+            }
+          }
+          part = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) exp_chunk(c);
+        };
+
+        part = make_float2(0.f, 0.f);
+        // A bias that falls with distance makes the maxima grow while the blocks lie right of the
+        // rows: there, too, the maximum comes first.
+        if (j == 0 || (MODE != 0 && slope2 > 0.f && right)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) score(c);
+          with_own_max();
+        } else {
+          tmem_ld32(trow + col_s, r[0]);
+          tmem_ld32(trow + col_s + 32, r[1]);
+          tmem_ld_wait32(r[0]);
+          tmem_ld_wait32(r[1]);
+          tmem_ld32(trow + col_s + 64, r[2]);
+          tmem_ld32(trow + col_s + 96, r[3]);
+          score(0);
+          exp_chunk(0);
+          score(1);
+          exp_chunk(1);
+          tmem_ld_wait32(r[2]);
+          tmem_ld_wait32(r[3]);
+          score(2);
+          exp_chunk(2);
+          score(3);
+          exp_chunk(3);
+          const float sum = part.x + part.y;
+          // Redo when a P may have overflowed (also inf and NaN), or when the block holds the row's
+          // first visible keys (the reference is then no maximum at all).
+          const bool bad = !(sum <= kSpeculationSumBound) ||
+                           (!seen && see.x < kbase + kBlockK && see.y > kbase && see.x < see.y);
+          if (__any_sync(0xffffffffu, bad)) {
+            tmem_st_wait();  // the speculative P has landed before it is overwritten
+            with_own_max();
+          }
+        }
+        l += part.x + part.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_p[t]);
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------------ epilogue
+      if (nkt > 0) {
+        if (!(ok = warp_wait(&bar_o[t], nout & 1, wc, kSiteSoftO))) break;
+        ++nout;
+        tc_fence_after();
+      }
+      // The staging buffer is free once the previous epilogue's store has read it.
+      if (my_stg > 0 && !(ok = warp_wait(bar_stg, (my_stg - 1) & 1, wc, kSiteEpi))) break;
+      const bool any_key = l > 0.f;
+      const float inv_l = any_key ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (nkt > 0) {
+          tmem_ld32(trow + col_o + c * 32, o);
+          tmem_ld_wait32(o);
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {  // a row without keys is 0 whatever the accumulator holds
+          const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), pair(inv_l));
+          pk[i] = any_key ? pack_bf16x2(y.x, y.y) : 0u;
+        }
+        uint8_t* box = sO + (c / 2) * C::kBoxBytes + row * 128;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const int chunk = (c % 2) * 4 + q4;
+          *reinterpret_cast<uint4*>(box + ((chunk ^ (row & 7)) * 16)) =
+              make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_epi[t]);
+      if (qrow < p.N)
+        p.lse[static_cast<size_t>(x.bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+      if (row == 0) {
+        if ((ok = mbar_wait(&bar_epi[t], nepi & 1, wc, kSiteEpi))) {
+#pragma unroll
+          for (int c = 0; c < C::kBoxes; ++c)
+            tma_store_4d(&tm_o, sO + c * C::kBoxBytes, c * kBoxCols, row0, h, b);
+          tma_store_commit_and_wait_read();
+          mbar_arrive(bar_stg);
+        }
+      }
+      ++nepi;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int MODE>
+cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  using C = Cfg<D>;
+  CUtensorMap tq, tk, tv, to;
+  cudaError_t e;
+  constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((e = make_tmap_4d(&tq, a.q, kBf16, 2, D, a.N, a.H, a.B, a.sq.s, kBoxCols, kBlockQ))) return e;
+  if ((e = make_tmap_4d(&tk, a.k, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sk.s, kBoxCols, kBlockK))) return e;
+  if ((e = make_tmap_4d(&tv, a.v, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sv.s, kBoxCols, kBlockK))) return e;
+  if ((e = make_tmap_4d(&to, a.o, kBf16, 2, D, a.N, a.H, a.B, a.so.s, kBoxCols, kBlockQ))) return e;
+  Params p{};
+  p.plan = sc.plan;
+  p.causal = sc.causal;
+  p.N = a.N;
+  p.H = a.H;
+  p.group = a.H / sc.Hkv;
+  p.BH = a.B * a.H;
+  p.nunits = (a.N + kUnitRows - 1) / kUnitRows;
+  p.scale_log2 = a.scale * kLog2e;
+  if (MODE == 2) {
+    p.cap_in = a.scale / sc.softcap;
+    p.cap_out = sc.softcap * kLog2e;
+  }
+  p.slopes = sc.slopes;
+  p.lse = a.lse;
+  p.err_word = a.err_word;
+  p.wait_ns = a.dbg.wait_limit_ns;
+  auto kern = fwd_scored_kernel<D, MODE>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
+  // setmaxnreg.inc can only draw on the registers the block was launched with.
+  cudaFuncAttributes fattr;
+  if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
+  if (static_cast<uint32_t>(fattr.numRegs) * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev))) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return e;
+  const long long units = static_cast<long long>(p.nunits) * p.BH;
+  kern<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  if (sc.softcap > 0.f) return launch<D, 2>(a, sc, stream);
+  return sc.slopes ? launch<D, 1>(a, sc, stream) : launch<D, 0>(a, sc, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_fwd_scored(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  return a.d == 64 ? launch_d<64>(a, sc, stream) : launch_d<128>(a, sc, stream);
+}
+
+}  // namespace fa
