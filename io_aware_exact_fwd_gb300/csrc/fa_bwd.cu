@@ -44,162 +44,12 @@
 // That doubles only the dQ^T product (one fifth of the backward's FLOPs).
 #include <math.h>
 
+#include "fa_bwd_common.cuh"
 #include "fa_device.cuh"
 #include "fa_internal.h"
 
 namespace fa {
 namespace {
-
-constexpr int kBkB = 128;       // keys per CTA
-constexpr int kBqB = 64;        // query rows per inner step
-constexpr int kThreads = 512;   // 0-7 compute, 8-11 dQ reduction, 12 TMA, 13-15 MMA issuers (15: see kSplitSdp)
-constexpr int kWarpDq = 8;
-constexpr int kWarpCtl = 12;
-constexpr int kWarpLoad = 12;
-constexpr int kWarpMma = 13;     // issues dV, dK, dQ^T (and owns the TMEM allocation)
-constexpr int kWarpMmaS = 14;    // issues S^T
-constexpr int kWarpMmaDP = 15;   // issues dP^T when the kernel splits that issue (kSplitSdp), else idle
-constexpr int kStages = 3;
-constexpr uint32_t kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f;
-// Launch budget 128 x 512 registers: the two compute warpgroups (one 32-query
-// half of a score row each) take 160, the dQ warpgroup 120, the control
-// warpgroup (TMA, MMA) gives back to 72.
-constexpr uint32_t kLaunchRegs = 128;
-constexpr uint32_t kRegsCompute = 160;
-constexpr uint32_t kRegsDq = 120;
-constexpr uint32_t kRegsControl = 72;
-static_assert(128 * (2 * kRegsCompute + kRegsDq + kRegsControl) <= kLaunchRegs * kThreads, "register split");
-
-enum : uint32_t {
-  kSiteBLoad = 0x111,
-  kSiteBMmaKV = 0x211,
-  kSiteBMmaQ = 0x212,
-  kSiteBMmaC = 0x213,
-  kSiteBMmaDq = 0x214,
-  kSiteBMmaSd = 0x215,
-  kSiteBComp = 0x311,
-  kSiteBDq = 0x312,
-  kSiteBEpi = 0x313,
-};
-
-template <int D>
-struct BwdCfg {
-  static_assert(D == 64 || D == 128, "head dim");
-  static constexpr int kBoxes = D / 64;                 // 128-byte TMA boxes per bf16 row
-  static constexpr int kKVBox = kBkB * 64 * 2;          // 16 KB: 128 rows x 128 B
-  static constexpr int kKVTile = kBkB * D * 2;          // 32 KB (d=128), 16 KB (d=64)
-  static constexpr int kQBox = kBqB * 64 * 2;           // 8 KB: 64 rows x 128 B
-  static constexpr int kQTile = kBqB * D * 2;           // 16 KB (d=128), 8 KB (d=64)
-  static constexpr int kStageQ = 0;
-  static constexpr int kStageDO = kQTile;
-  // The extra K-step's per-query tiles (64 rows x 32 bytes, 32-byte swizzle):
-  // [a1 a2 a3 a1 a2 a3 a1 a2 a3 0...] with a1 + a2 + a3 = -LSE2 for S^T, then
-  // [d1 d2 d3 0...] with d1 + d2 + d3 = -D for dP^T (three-term bf16 splits).
-  static constexpr int kAugTile = kBqB * 32;           // 2 KB
-  static constexpr int kStageAug = 2 * kQTile;
-  static constexpr int kStageTx = 2 * kQTile + 2 * kAugTile;  // bytes landing per stage
-  static constexpr int kStageBytes = (kStageTx + 1023) / 1024 * 1024;
-  static constexpr int kDsBytes = kBkB * kBqB * 2;      // 16 KB: 128 key rows x 128 B
-  // K, then (d = 64) the zero box that pads K^T to the dQ^T MMA's 128 rows, then V,
-  // then the extra K-step's constant key-side tiles (128 rows x 32 bytes each):
-  // [c1 c1 c1 c2 c2 c2 c3 c3 c3 0...] with c1 + c2 + c3 = 1 / (scale log2 e) for S^T
-  // (so the nine products sum to (c1 + c2 + c3)(a1 + a2 + a3)), [1 1 1 0...] for dP^T.
-  static constexpr int kKOff = 0;
-  static constexpr int kZeroOff = kKVTile;
-  static constexpr int kVOff = kKVTile + (D == 64 ? kKVBox : 0);
-  static constexpr int kKAugOff = kVOff + kKVTile;
-  static constexpr int kVAugOff = kKAugOff + kBkB * 32;
-  static constexpr int kRingOff = kVAugOff + kBkB * 32;
-  static constexpr int kDsOff = kRingOff + kStages * kStageBytes;
-  static constexpr int kBarOff = kDsOff + 2 * kDsBytes;
-  // kv, full[S], empty[S], sdp, sde, comp[2], dqf[2], dqe[2], dkv, epi, drain
-  static constexpr int kNumBars = 1 + 2 * kStages + 1 + 1 + 2 + 2 + 2 + 1 + 1 + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
-  // TMEM columns: dV, dK accumulators (D columns each); one S^T, dP^T pair (fp32,
-  // read once by the compute warps, then free for the next query block); two
-  // 64-column buffers that hold P^T | dS^T (bf16, 32 columns each) and then dQ^T (fp32).
-  static constexpr uint32_t kColDV = 0, kColDK = 128, kColS = 256, kColDP = 320;
-  static __device__ __forceinline__ uint32_t col_pdq(int b) { return 384u + 64u * b; }
-  static_assert(kStageTx <= kStageBytes, "stage layout");
-  static_assert(kZeroOff % 1024 == 0 && kKAugOff % 1024 == 0 && kRingOff % 1024 == 0, "operand tile alignment");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-};
-
-__device__ __forceinline__ bool warp_wait_b(uint64_t* bar, uint32_t parity, const WaitCtl& wc, uint32_t site) {
-  const bool ok = mbar_wait(bar, parity, wc, site);
-  return __all_sync(0xffffffffu, ok);
-}
-// For the compute and dQ warps' long waits (S^T, dP^T ready; dQ^T ready): their polls
-// suspend instead of spinning beside the MMA-issuing warps.
-__device__ __forceinline__ bool warp_wait_b_suspend(uint64_t* bar, uint32_t parity, const WaitCtl& wc, uint32_t site) {
-  const bool ok = mbar_wait_suspend(bar, parity, wc, site, 20000u);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// Deterministic dQ: fixed-point accumulation.  Every contribution of a key block
-// to dQacc[i, c] is sum_j dS_ij k_jc, and the whole sum over all key blocks obeys
-//   |sum_j dS_ij k_jc| <= sum_j |dS_ij| max|k| <= 2 max_j |dP_ij| max|k|
-//                      <= 2 |dO_i| max_j |v_j| max|k|
-// (|dS_ij| = P_ij |dP_ij - D_i| with D_i a P-weighted mean of dP_i., and
-// |dP_ij| = |dO_i . v_j| <= |dO_i| |v_j|).  With a 64-row block's largest |dO_i|,
-// the head's largest |v_j| and largest |k_jc|, and a 12.5 % margin for the bf16
-// rounding of P and dS, the power of two 2^S below puts every partial sum of the
-// block's rows under 2^22 in magnitude.  Contributions are rounded to integers
-// once (x 2^S, nearest) and added as int32: integer addition does not depend on
-// order, so dQ is the same bits on every run.  2^22 keeps the float-to-int step
-// a single add of 1.5 * 2^23 (the rounding is the fp32 add's).
-__device__ __forceinline__ int det_shift(float dq_block_max, float vmax, float kmax) {
-  const float bound = 2.25f * dq_block_max * vmax * kmax;
-  if (!(bound > 0.f)) return 100;           // all-zero block (or no data): nothing to scale
-  if (!(bound < 3.0e38f)) return -100;      // non-finite inputs: the result is undefined anyway
-  int e;
-  frexpf(bound, &e);                        // bound < 2^e
-  return max(-100, min(100, 22 - e));
-}
-__device__ __forceinline__ float pow2f(int s) { return __int_as_float((s + 127) << 23); }  // -126 <= s <= 127
-
-// Three-term bf16 split of x: t1 = bf16(x), t2 = bf16(x - t1), t3 = bf16(x - t1 - t2)
-// (each difference exact in fp32), so t1 + t2 + t3 carries about 24 significant
-// bits of x.  Returned as raw bf16 bits.
-__device__ __forceinline__ void split3_bf16(float x, uint32_t (&t)[3]) {
-  float r = x;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(r);
-    t[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h));
-    r -= __bfloat162float(h);
-  }
-}
-
-// Element offset of row n of head (b, h) in a strided [B, H, N, d] tensor.
-__device__ __forceinline__ size_t row_offset(const Strides& st, long long bh, int H, int n) {
-  return static_cast<size_t>((bh / H) * st.s[2] + (bh % H) * st.s[1] + static_cast<long long>(n) * st.s[0]);
-}
-
-// Stage this thread's D-column fp32 accumulator row as bf16 into 128-byte-swizzled
-// [128 rows][64 cols] TMA boxes (D / 64 of them).
-template <int D>
-__device__ __forceinline__ void stage_row_bf16(uint32_t taddr_row, uint8_t* boxes, int row, float mul) {
-#pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    uint32_t o[32];
-    tmem_ld32(taddr_row + c * 32, o);
-    tmem_ld_wait32(o);
-    uint32_t pk[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      pk[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
-    uint8_t* box = boxes + (c / 2) * BwdCfg<D>::kKVBox + row * 128;
-#pragma unroll
-    for (int q4 = 0; q4 < 4; ++q4) {
-      const int chunk = (c % 2) * 4 + q4;
-      *reinterpret_cast<uint4*>(box + ((chunk ^ (row & 7)) * 16)) =
-          make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
-    }
-  }
-}
 
 template <int D, bool CAUSAL, bool DET>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -583,14 +433,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // one pair per 64-row query block): [a1 a2 a3 a1 a2 a3 a1 a2 a3 0...] with
 // a1 + a2 + a3 = -LSE2 and [d1 d2 d3 0...] with d1 + d2 + d3 = -D (three-term bf16
 // splits).  Rows >= N get -LSE2 = -1e30 (their P is exactly 0) and D = 0.
-// dQacc rows < N are zeroed.  D / 8 threads per row, 8 elements each.
+// dQacc rows < N are zeroed.  D / 8 threads per row, 8 elements each.  A row that saw no
+// key (LSE = -inf, scored attention only) is written like a padded one.  With raw_lse
+// the first tile of each query block holds its 64 values of LSE2 as fp32 instead (1e30
+// where a row has none), for scores that pass through a cap before LSE2 is subtracted.
 template <int D, bool DET>
 __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16* __restrict__ o,
                                                              const __nv_bfloat16* __restrict__ dout,
                                                              const float* __restrict__ lse, uint8_t* __restrict__ aug,
                                                              float* __restrict__ dq_acc,
                                                              unsigned int* __restrict__ dq_bmax, int N, int Npad,
-                                                             long long rows_pad, int H, Strides so, Strides sdo) {
+                                                             long long rows_pad, int H, Strides so, Strides sdo,
+                                                             int raw_lse) {
   constexpr int kTpr = D / 8;          // threads per row
   constexpr int kRpb = 256 / kTpr;     // rows per block: 16 (d=128) or 32 (d=64)
   const long long r = static_cast<long long>(blockIdx.x) * kRpb + (threadIdx.x / kTpr);
@@ -599,6 +453,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
   // thread has a row and all of them reach the shuffles and the barrier below.
   const long long bh = r / Npad;
   const int nrow = static_cast<int>(r - bh * Npad);
+  const float lse_row = nrow < N ? lse[static_cast<size_t>(bh) * N + nrow] : -INFINITY;
   float acc = 0.f, nrm = 0.f;
   if (nrow < N) {
     const size_t base = (static_cast<size_t>(bh) * N + nrow) * D + t * 8;  // dense: the dQ accumulator
@@ -625,15 +480,20 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
   for (int m = kTpr / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m, kTpr);
   if (t == 0) {
     uint32_t a[3], dd[3];
-    split3_bf16(nrow < N ? -lse[static_cast<size_t>(bh) * N + nrow] * kLog2e : -1e30f, a);
+    const float neg_lse2 = lse_row > -INFINITY ? -lse_row * kLog2e : -1e30f;
+    split3_bf16(neg_lse2, a);
     split3_bf16(nrow < N ? -acc : 0.f, dd);
     const int rr = nrow % kBqB;
     uint8_t* tile = aug + (static_cast<size_t>(r / kBqB)) * (2 * kBqB * 32);  // r / 64 = (bh, query block)
     const int h0 = ((rr >> 2) & 1) << 4, h1 = (1 ^ ((rr >> 2) & 1)) << 4;     // swizzled half-row positions
-    // elements 0-7: a1 a2 a3 a1 a2 a3 a1 a2; element 8: a3
-    *reinterpret_cast<uint4*>(tile + rr * 32 + h0) =
-        make_uint4(a[0] | (a[1] << 16), a[2] | (a[0] << 16), a[1] | (a[2] << 16), a[0] | (a[1] << 16));
-    *reinterpret_cast<uint4*>(tile + rr * 32 + h1) = make_uint4(a[2], 0u, 0u, 0u);
+    if (raw_lse) {
+      reinterpret_cast<float*>(tile)[rr] = -neg_lse2;
+    } else {
+      // elements 0-7: a1 a2 a3 a1 a2 a3 a1 a2; element 8: a3
+      *reinterpret_cast<uint4*>(tile + rr * 32 + h0) =
+          make_uint4(a[0] | (a[1] << 16), a[2] | (a[0] << 16), a[1] | (a[2] << 16), a[0] | (a[1] << 16));
+      *reinterpret_cast<uint4*>(tile + rr * 32 + h1) = make_uint4(a[2], 0u, 0u, 0u);
+    }
     *reinterpret_cast<uint4*>(tile + kBqB * 32 + rr * 32 + h0) = make_uint4(dd[0] | (dd[1] << 16), dd[2], 0u, 0u);
     *reinterpret_cast<uint4*>(tile + kBqB * 32 + rr * 32 + h1) = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -642,7 +502,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
     // multiples of kRpb, which divides 64): reduce to one atomic per block.
 #pragma unroll
     for (int m = kTpr / 2; m >= 1; m >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, m, kTpr);
-    float mx = sqrtf(nrm);  // 0 for padded rows
+    float mx = lse_row > -INFINITY ? sqrtf(nrm) : 0.f;  // 0 for padded rows and rows without keys
 #pragma unroll
     for (int m = kTpr; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
     __shared__ float red[8];
@@ -666,7 +526,7 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_kv_bound_kernel(const __nv_bfloat16* __restrict__ k,
                                                            const __nv_bfloat16* __restrict__ v,
                                                            unsigned int* __restrict__ kv_max, int N, int H,
-                                                           Strides sk, Strides sv) {
+                                                           Strides sk, Strides sv, const int2* __restrict__ seen_by) {
   constexpr int kTpr = D / 8;
   constexpr int kRpp = 256 / kTpr;  // rows per pass
   const int bh = blockIdx.y;
@@ -679,7 +539,12 @@ __global__ void __launch_bounds__(256) bwd_kv_bound_kernel(const __nv_bfloat16* 
   for (int pass = 0; pass < kBoundRows / kRpp; ++pass) {
     const int r = r0 + pass * kRpp;
     uint4 kv4 = make_uint4(0, 0, 0, 0), vv4 = make_uint4(0, 0, 0, 0);
-    if (r < N) {
+    bool counts = r < N;
+    if (seen_by && counts) {  // a key that no query sees (padding) may hold anything
+      const int2 q = seen_by[static_cast<size_t>(bh / H) * N + r];
+      counts = q.x < q.y;
+    }
+    if (counts) {
       kv4 = *reinterpret_cast<const uint4*>(k + row_offset(sk, bh, H, r) + t * 8);
       vv4 = *reinterpret_cast<const uint4*>(v + row_offset(sv, bh, H, r) + t * 8);
     }
@@ -725,7 +590,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
                                                              __nv_bfloat16* __restrict__ dq, float scale,
                                                              long long n8, const float* __restrict__ dq_bmax,
                                                              const float* __restrict__ kv_max, int N, int Npad, int H,
-                                                             Strides sdq) {
+                                                             int group, Strides sdq) {
   const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= n8) return;
   float4 a = reinterpret_cast<const float4*>(dq_acc)[2 * idx];
@@ -734,7 +599,9 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
   const long long bh = row / N;
   const int qrow = static_cast<int>(row - bh * N);
   if (DET) {
-    const float inv = pow2f(-det_shift(dq_bmax[bh * (Npad / kBqB) + qrow / kBqB], kv_max[2 * bh], kv_max[2 * bh + 1]));
+    const long long kvh = bh / group;  // = b Hkv + h / group: the key/value head that query head bh reads
+    const float inv =
+        pow2f(-det_shift(dq_bmax[bh * (Npad / kBqB) + qrow / kBqB], kv_max[2 * kvh], kv_max[2 * kvh + 1]));
     auto cv = [&](float x) { return static_cast<float>(__float_as_int(x)) * inv; };
     a = make_float4(cv(a.x), cv(a.y), cv(a.z), cv(a.w));
     b = make_float4(cv(b.x), cv(b.y), cv(b.z), cv(b.w));
@@ -777,16 +644,18 @@ cudaError_t launch_bwd_prep_d(const BwdArgs& a, cudaStream_t stream) {
     // The block and head maxima are built with atomicMax from zero.
     cudaError_t e = cudaMemsetAsync(ws + w.off_dqmax, 0, w.total - w.off_dqmax, stream);
     if (e) return e;
-    bwd_kv_bound_kernel<D><<<dim3(static_cast<unsigned>((a.N + kBoundRows - 1) / kBoundRows), BH), 256, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(a.k), static_cast<const __nv_bfloat16*>(a.v),
-        reinterpret_cast<unsigned int*>(ws + w.off_kvmax), a.N, a.H, a.sk, a.sv);
+    bwd_kv_bound_kernel<D><<<dim3(static_cast<unsigned>((a.N + kBoundRows - 1) / kBoundRows), BH / a.group), 256, 0,
+                             stream>>>(static_cast<const __nv_bfloat16*>(a.k), static_cast<const __nv_bfloat16*>(a.v),
+                                       reinterpret_cast<unsigned int*>(ws + w.off_kvmax), a.N, a.H / a.group, a.sk,
+                                       a.sv, a.seen_by);
     if ((e = cudaGetLastError())) return e;
   }
   constexpr int kRpb = 256 / (D / 8);
   auto kern = a.deterministic ? bwd_preprocess_kernel<D, true> : bwd_preprocess_kernel<D, false>;
   kern<<<static_cast<unsigned>(rows_pad / kRpb), 256, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(a.o), static_cast<const __nv_bfloat16*>(a.dout), a.lse,
-      ws + w.off_aug, reinterpret_cast<float*>(ws + w.off_dq), dq_bmax, a.N, w.npad, rows_pad, a.H, a.so, a.sdo);
+      ws + w.off_aug, reinterpret_cast<float*>(ws + w.off_dq), dq_bmax, a.N, w.npad, rows_pad, a.H, a.so, a.sdo,
+      a.raw_lse);
   return cudaGetLastError();
 }
 
@@ -829,7 +698,7 @@ cudaError_t launch_bwd_dq_d(const BwdArgs& a, cudaStream_t stream) {
   auto kern = a.deterministic ? bwd_dq_convert_kernel<D, true> : bwd_dq_convert_kernel<D, false>;
   kern<<<static_cast<unsigned>((n8 + 255) / 256), 256, 0, stream>>>(
       dq_acc, static_cast<__nv_bfloat16*>(a.dq), a.scale, n8, reinterpret_cast<const float*>(ws + w.off_dqmax),
-      reinterpret_cast<const float*>(ws + w.off_kvmax), a.N, w.npad, a.H, a.sdq);
+      reinterpret_cast<const float*>(ws + w.off_kvmax), a.N, w.npad, a.H, a.group, a.sdq);
   return cudaGetLastError();
 }
 

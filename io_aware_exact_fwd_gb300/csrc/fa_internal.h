@@ -117,6 +117,9 @@ struct BwdArgs {
   float scale;
   unsigned int* err_word;
   DebugKnobs dbg;
+  int group = 1;      // query heads that share a key/value head (scored attention)
+  int raw_lse = 0;    // 1: LSE * log2(e) per query as fp32 instead of operand tiles (scored attention with a cap)
+  const int2* seen_by = nullptr;  // [B, N] queries that see each key, or NULL (every key counts)
 };
 
 // Workspace of the backward: fp32 dQ accumulator [BH, N, d] (int32 in the
@@ -225,9 +228,9 @@ int w4a16_chunks_per_split(int K, int n_split);
 bool w4a16_uses_gemv(int M, int K);
 cudaError_t launch_w4a16(const W4a16Args& a, cudaStream_t stream);
 
-// ------------------------------------------------ scored attention (fa_scored*.cu)
+// ------------------------------------------------ scored attention (fa_mask_plan.cu, fa_scored_*.cu)
 
-// The mask as intervals (written by the plan kernel, fa_scored.cu): query i sees keys
+// The mask as intervals (written by fa_mask_plan.cu): query i sees keys
 // [q[i].x, q[i].y), key j is seen by queries [k[j].x, k[j].y).  Both ends do not
 // decrease along a row of the batch; an empty interval has equal ends.
 struct MaskPlan {

@@ -125,6 +125,7 @@ int fa_bwd_scored(const void* q, const int64_t* q_strides, const void* k, const 
   if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
   int st = validate_plan(plan, plan_bytes, B, N, causal);
   if (st != FA_OK) return st;
+  if (deterministic && static_cast<long long>(B) * Hkv > 65535) return FA_ERR_UNSUPPORTED;  // a grid's second axis
   if (!workspace || ws_bytes < fa::bwd_workspace_layout(B, H, N, d).total) return FA_ERR_WORKSPACE;
   fa::BwdArgs a{};
   const fa::Strides ds = fa::dense_strides(H, N, d), dkv = fa::dense_strides(Hkv, N, d);

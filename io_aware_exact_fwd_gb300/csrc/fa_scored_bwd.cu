@@ -1,0 +1,540 @@
+// Scored attention backward for sm_103a (the gradient of fa_scored_fwd.cu), bf16.
+//
+//   P_ij = exp(s_ij - LSE_i) (0 where masked), dP = dO V^T, D_i = dO_i . O_i
+//   dS   = P (dP - D) (1 - tanh^2)   dQ = scale dS K   dK = scale sum_h dS^T Q   dV = sum_h P^T dO
+//
+// The preprocess and the dQ conversion are the plain backward's (fa_bwd.cu), and so is
+// the main kernel's pipeline: one CTA per 128-key block, K_j and V_j resident, 64-row
+// blocks of Q and dO streaming through a TMA ring, S^T and dP^T in TMEM, P^T and dS^T
+// written back as bf16 operands of dV, dK and dQ^T, dQ added to an fp32 accumulator.
+// What differs:
+//
+//  * A CTA owns a key block of one key/value head and walks the query blocks of every
+//    query head of the group, so dK and dV of shared heads are summed in the same TMEM
+//    accumulators (no atomics, one rounding).
+//  * Its query blocks are those between its first key's first query and its last key's
+//    last query (the plan's intervals); each thread holds one key and its interval.
+//  * Without a cap, LSE and D still enter through the extra K-step of S^T and dP^T. With
+//    one, tanh needs the bare products: S^T goes without, and the compute warps subtract
+//    LSE2 (64 fp32 values beside each query block) after the cap.
+#include <math.h>
+
+#include "fa_bwd_common.cuh"
+#include "fa_device.cuh"
+#include "fa_internal.h"
+#include "fa_score.cuh"
+
+namespace fa {
+namespace {
+
+struct Params {
+  MaskPlan plan;
+  int causal, N, Npad, H, Hkv, group, nkb;
+  float scale, scale_log2;
+  float cap_in, cap_out;  // scale / softcap, softcap log2(e)
+  const float* slopes;
+  const uint8_t* aug;
+  float* dq_acc;
+  const float* dq_bmax;
+  const float* kv_max;
+  unsigned int* err_word;
+  unsigned long long wait_ns;
+};
+
+// The CTA's steps: query blocks [i0, i0 + nq) of each head of the group, head by head.
+struct Steps {
+  int i0, nq, n;
+};
+__device__ __forceinline__ Steps steps_of(const Params& p, int kb, int b) {
+  const int lo = queries_of(p.plan, p.causal, b, kb * kBkB, p.N).x;
+  const int hi = queries_of(p.plan, p.causal, b, min(kb * kBkB + kBkB, p.N) - 1, p.N).y;
+  const int i0 = lo / kBqB;
+  const int nq = hi > lo ? (hi + kBqB - 1) / kBqB - i0 : 0;
+  return {i0, nq, nq * p.group};
+}
+
+// MODE 0: scores as they are; 1: with a distance bias; 2: capped (and biased if slopes).
+template <int D, int MODE, bool DET>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
+                      const __grid_constant__ Params p) {
+  using C = BwdCfg<D>;
+  constexpr bool kSplitSdp = D == 128 && !DET;  // as in the plain backward
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem + C::kKOff;
+  uint8_t* sV = smem + C::kVOff;
+  uint8_t* sRing = smem + C::kRingOff;
+  uint8_t* sDs = smem + C::kDsOff;
+  uint64_t* bar_kv = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* bar_full = bar_kv + 1;
+  uint64_t* bar_empty = bar_full + kStages;
+  uint64_t* bar_sdp = bar_empty + kStages;  // S^T, dP^T ready in TMEM
+  uint64_t* bar_sde = bar_sdp + 1;          // S^T, dP^T read out of TMEM
+  uint64_t* bar_comp = bar_sde + 1;         // [2] P^T, dS^T written
+  uint64_t* bar_dqf = bar_comp + 2;         // [2] dQ^T ready in TMEM
+  uint64_t* bar_dqe = bar_dqf + 2;          // [2] dQ^T read out of TMEM
+  uint64_t* bar_dkv = bar_dqe + 2;
+  uint64_t* bar_epi = bar_dkv + 1;
+  uint64_t* bar_drain = bar_epi + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // Key blocks in order, heads next to one another: causal key blocks near the start see
+  // the most queries and go first.
+  const int kvheads = static_cast<int>(gridDim.x) / p.nkb;  // B Hkv
+  const int kb = static_cast<int>(blockIdx.x) / kvheads, bhk = static_cast<int>(blockIdx.x) % kvheads;
+  const int hk = bhk % p.Hkv, b_idx = bhk / p.Hkv;
+  const int h0 = hk * p.group;               // first query head of the group
+  const int bh0 = b_idx * p.H + h0;
+  const Steps st = steps_of(p, kb, b_idx);
+  const int n = st.n;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_kv, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], 1);
+    }
+    mbar_init(bar_sdp, kSplitSdp ? 2 : 1);
+    mbar_init(bar_sde, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar_comp[b], 8);
+      mbar_init(&bar_dqf[b], 1);
+      mbar_init(&bar_dqe[b], 4);
+    }
+    mbar_init(bar_dkv, 1);
+    mbar_init(bar_epi, 8);
+    mbar_init(bar_drain, kSplitSdp ? 3 : 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if constexpr (D == 64) {
+    // Rows 64..127 of the dQ^T MMA's A operand: zeros, read by the tensor core.
+    uint4* z = reinterpret_cast<uint4*>(smem + C::kZeroOff);
+    for (int i = threadIdx.x; i < C::kKVBox / 16; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  {
+    // The extra K-step's key-side tiles (BwdCfg), one 16-byte half-row per thread.
+    const int tile = threadIdx.x >> 8, krow = (threadIdx.x >> 1) & 127, half = threadIdx.x & 1;
+    uint4 val = make_uint4(0u, 0u, 0u, 0u);
+    if (tile == 0) {
+      uint32_t c[3];
+      split3_bf16(1.f / p.scale_log2, c);
+      val = half == 0 ? make_uint4(c[0] | (c[0] << 16), c[0] | (c[1] << 16), c[1] | (c[1] << 16), c[2] | (c[2] << 16))
+                      : make_uint4(c[2], 0u, 0u, 0u);
+    } else if (half == 0) {
+      val = make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u);  // bf16 1.0, 1.0, 1.0
+    }
+    uint8_t* base = smem + (tile == 0 ? C::kKAugOff : C::kVAugOff);
+    *reinterpret_cast<uint4*>(base + krow * 32 + ((half ^ ((krow >> 2) & 1)) << 4)) = val;
+    fence_proxy_async_smem();
+  }
+  if (warp == kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
+  const size_t head_blocks = static_cast<size_t>(p.Npad / kBqB);
+
+  if (warp >= kWarpCtl) {
+    regs_decrease<kRegsControl>();
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------------------ TMA producer
+      if (lane == 0 && n > 0) {
+        mbar_arrive_expect_tx(bar_kv, 2 * C::kKVTile);
+        for (int c = 0; c < C::kBoxes; ++c) {
+          tma_load_4d(sK + c * C::kKVBox, &tm_k, bar_kv, c * 64, kb * kBkB, hk, b_idx);
+          tma_load_4d(sV + c * C::kKVBox, &tm_v, bar_kv, c * 64, kb * kBkB, hk, b_idx);
+        }
+        int issued = 0, g = 0, i = st.i0;
+        for (int it = 0; it < n; ++it) {
+          const int slot = it % kStages;
+          if (!mbar_wait(&bar_empty[slot], ((it / kStages) & 1) ^ 1, wc, kSiteBLoad)) break;
+          uint8_t* dst = sRing + slot * C::kStageBytes;
+          mbar_arrive_expect_tx(&bar_full[slot], C::kStageTx);
+          for (int c = 0; c < C::kBoxes; ++c) {
+            tma_load_4d(dst + C::kStageQ + c * C::kQBox, &tm_q, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
+            tma_load_4d(dst + C::kStageDO + c * C::kQBox, &tm_do, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
+          }
+          bulk_load(dst + C::kStageAug, p.aug + ((bh0 + g) * head_blocks + i) * (2 * C::kAugTile), 2 * C::kAugTile,
+                    &bar_full[slot]);
+          ++issued;
+          if (++i == st.i0 + st.nq) {
+            i = st.i0;
+            ++g;
+          }
+        }
+        if (issued < n) {  // aborted: let the copies already in flight land
+          mbar_wait_drain(bar_kv, 0, p.wait_ns);
+          for (int t = max(0, issued - kStages); t < issued; ++t)
+            mbar_wait_drain(&bar_full[t % kStages], (t / kStages) & 1, p.wait_ns);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma || warp == kWarpMmaS || (kSplitSdp && warp == kWarpMmaDP)) {
+      // -------------------------------------------- MMA issuers (one thread each)
+      // Hazards between the issuing threads are covered as in the plain backward.
+      if (lane == 0) {
+        constexpr uint32_t idesc_sdp = idesc_bf16_f32(kBkB, kBqB, 0, 0);   // keys x queries, K = d
+        constexpr uint32_t idesc_dkv = idesc_bf16_f32(kBkB, D, 0, 1);      // keys x d, K = queries
+        constexpr uint32_t idesc_dq = idesc_bf16_f32(128, kBqB, 1, 1);     // d x queries, K = keys
+        const uint64_t k_kmaj = sdesc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t v_kmaj = sdesc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t k_mn = sdesc_sw128(smem_u32(sK), C::kKVBox, 1024);
+        const uint64_t ring_kmaj = sdesc_sw128(smem_u32(sRing), 16, 1024);
+        const uint64_t ring_mn = sdesc_sw128(smem_u32(sRing), C::kQBox, 1024);
+        const uint64_t ds_mn = sdesc_sw128(smem_u32(sDs), 16, 1024);
+        const uint64_t kaug = sdesc_sw32(smem_u32(smem + C::kKAugOff));
+        const uint64_t vaug = sdesc_sw32(smem_u32(smem + C::kVAugOff));
+        const uint64_t ring_aug = sdesc_sw32(smem_u32(sRing + C::kStageAug));
+        bool ok = n == 0 || mbar_wait(bar_kv, 0, wc, kSiteBMmaKV);
+        int slot = 0;
+        uint32_t stage = 0;
+        if (warp != kWarpMma) {
+          const bool issue_s = warp == kWarpMmaS;
+          const bool issue_dp = kSplitSdp ? warp == kWarpMmaDP : warp == kWarpMmaS;
+          uint32_t ring_ph = 0;
+          for (int it = 0; ok && it < n; ++it) {
+            if (!(ok = mbar_wait(&bar_full[slot], ring_ph, wc, kSiteBMmaQ))) break;
+            if (it >= 1 && !(ok = mbar_wait(bar_sde, (it - 1) & 1, wc, kSiteBMmaSd))) break;
+            tc_fence_after();
+            if (issue_s) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t offa = (kk / 4) * C::kKVBox + (kk % 4) * 32;
+                const uint32_t offb = (kk / 4) * C::kQBox + (kk % 4) * 32;
+                mma_bf16_ss(tmem + C::kColS, sdesc_add(k_kmaj, offa), sdesc_add(ring_kmaj, stage + C::kStageQ + offb),
+                            idesc_sdp, kk > 0 ? 1u : 0u);
+              }
+              if (MODE != 2) mma_bf16_ss(tmem + C::kColS, kaug, sdesc_add(ring_aug, stage), idesc_sdp, 1u);
+            }
+            if (issue_dp) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t offa = (kk / 4) * C::kKVBox + (kk % 4) * 32;
+                const uint32_t offb = (kk / 4) * C::kQBox + (kk % 4) * 32;
+                mma_bf16_ss(tmem + C::kColDP, sdesc_add(v_kmaj, offa),
+                            sdesc_add(ring_kmaj, stage + C::kStageDO + offb), idesc_sdp, kk > 0 ? 1u : 0u);
+              }
+              mma_bf16_ss(tmem + C::kColDP, vaug, sdesc_add(ring_aug, stage + C::kAugTile), idesc_sdp, 1u);  // - D
+            }
+            mma_commit(bar_sdp);
+            if (++slot == kStages) {
+              slot = 0;
+              ring_ph ^= 1u;
+              stage = 0;
+            } else {
+              stage += C::kStageBytes;
+            }
+          }
+        } else {
+          for (int it = 0; ok && it < n; ++it) {
+            const int b = it & 1;
+            if (!(ok = mbar_wait(&bar_comp[b], (it >> 1) & 1, wc, kSiteBMmaC))) break;
+            tc_fence_after();
+            // dV += P^T dO_i ; dK += dS^T Q_i
+#pragma unroll
+            for (int kk = 0; kk < kBqB / 16; ++kk)
+              mma_bf16_ts(tmem + C::kColDV, tmem + C::col_pdq(b) + kk * 8,
+                          sdesc_add(ring_mn, stage + C::kStageDO + kk * 2048), idesc_dkv, (it > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < kBqB / 16; ++kk)
+              mma_bf16_ts(tmem + C::kColDK, tmem + C::col_pdq(b) + 32 + kk * 8,
+                          sdesc_add(ring_mn, stage + C::kStageQ + kk * 2048), idesc_dkv, (it > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&bar_empty[slot]);
+            // dQ_i^T = K^T dS^T
+#pragma unroll
+            for (int kk = 0; kk < kBkB / 16; ++kk)
+              mma_bf16_ss(tmem + C::col_pdq(b), sdesc_add(k_mn, kk * 2048),
+                          sdesc_add(ds_mn, b * C::kDsBytes + kk * 2048), idesc_dq, kk > 0 ? 1u : 0u);
+            mma_commit(&bar_dqf[b]);
+            if (++slot == kStages) {
+              slot = 0;
+              stage = 0;
+            } else {
+              stage += C::kStageBytes;
+            }
+          }
+          if (ok) mma_commit(bar_dkv);
+        }
+        // Every issued MMA of every issuing thread must finish before TMEM is released.
+        mma_commit(bar_drain);
+        mbar_wait_drain(bar_drain, 0, p.wait_ns);
+      }
+      __syncwarp();
+    }
+  } else if (warp < kWarpDq) {
+    regs_increase<kRegsCompute>();
+    // --------------------------------------- P and dS (one key row per thread)
+    const int g = warp >> 2;  // queries 32g .. 32g+31 of every block
+    const int row = threadIdx.x & 127;
+    const int key = kb * kBkB + row;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int2 by = key < p.N ? queries_of(p.plan, p.causal, b_idx, key, p.N) : make_int2(0, 0);
+    // Queries that see every key of the block: [all_lo, all_hi); none if the block is ragged.
+    const bool ragged = kb * kBkB + kBkB > p.N;
+    const int all_lo = queries_of(p.plan, p.causal, b_idx, min(kb * kBkB + kBkB, p.N) - 1, p.N).x;
+    const int all_hi = ragged ? 0 : queries_of(p.plan, p.causal, b_idx, kb * kBkB, p.N).y;
+    const bool biased = MODE == 1 || (MODE == 2 && p.slopes != nullptr);
+    bool ok = true;
+    int head = 0, i = st.i0, slot = 0;
+    uint32_t ring_ph = 0;
+    float slope2 = biased && n > 0 ? __ldg(p.slopes + h0) * kLog2e : 0.f;
+    for (int it = 0; it < n; ++it) {
+      const int b = it & 1;
+      if (!(ok = warp_wait_b_suspend(bar_sdp, it & 1, wc, kSiteBComp))) break;
+      tc_fence_after();
+      uint32_t s[32], dp[32];
+      tmem_ld32(trow + C::kColS + 32 * g, s);
+      tmem_ld32(trow + C::kColDP + 32 * g, dp);
+      tmem_ld_wait32(s);
+      tmem_ld_wait32(dp);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sde);  // the MMA warp may now overwrite S^T, dP^T
+      const int qb = i * kBqB, q0 = qb + 32 * g;
+      const bool need_mask = qb < all_lo || qb + kBqB > all_hi;
+      // s becomes the exponent of P in log2 units, dp becomes dS / P.
+      if constexpr (MODE == 2) {
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) mx = max3(mx, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+        const bool large = __any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f));
+        // LSE2 of the step's queries: the slot landed before S^T was made of it (the wait makes its
+        // bytes visible here), and is refilled only after this step's dV and dK.
+        if (!(ok = warp_wait_b(&bar_full[slot], ring_ph, wc, kSiteBComp))) break;
+        const float4* lse4 =
+            reinterpret_cast<const float4*>(sRing + slot * C::kStageBytes + C::kStageAug) + 8 * g;
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 l4 = lse4[c4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = 4 * c4 + 2 * e;
+            const float2 u = __fmul2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(p.cap_in));
+            const float2 t = large ? make_float2(tanh_any(u.x), tanh_any(u.y)) : tanh_small(u);
+            const float2 x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
+            const float2 bend = __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f));
+            const float2 y = __fmul2_rn(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), bend);
+            s[c] = __float_as_uint(x.x);
+            s[c + 1] = __float_as_uint(x.y);
+            dp[c] = __float_as_uint(y.x);
+            dp[c + 1] = __float_as_uint(y.y);
+          }
+        }
+      }
+      uint32_t ppk[16], dpk[16];
+      const float mul = MODE == 2 ? 1.f : p.scale_log2;
+      const float off = static_cast<float>(q0 - key);  // i - j of the first query
+      const bool below = qb >= kb * kBkB + kBkB - 1, above = qb + kBqB - 1 <= kb * kBkB;
+      const float sg = below ? -slope2 : slope2;
+#pragma unroll
+      for (int c2 = 0; c2 < 16; ++c2) {
+        const int c = 2 * c2;
+        float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        if (MODE == 1 || (MODE == 2 && biased)) {
+          float2 dist = __fadd2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)), pair(off));
+          if (!below && !above) dist = make_float2(-fabsf(dist.x), -fabsf(dist.y));
+          x = __ffma2_rn(x, pair(mul), __fmul2_rn(dist, pair(sg)));
+        } else if (MODE == 0) {
+          x = __fmul2_rn(x, pair(mul));
+        }
+        float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        if (need_mask) {
+          if (q0 + c < by.x || q0 + c >= by.y) pp.x = 0.f;
+          if (q0 + c + 1 < by.x || q0 + c + 1 >= by.y) pp.y = 0.f;
+        }
+        const float2 ds = __fmul2_rn(pp, make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])));
+        ppk[c2] = pack_bf16x2(pp.x, pp.y);
+        dpk[c2] = pack_bf16x2(ds.x, ds.y);
+      }
+      // P^T, dS^T(it) overwrite dQ^T(it-2) (TMEM) and dS^T(it-2) (shared memory).
+      if (it >= 2 && !(ok = warp_wait_b(&bar_dqe[b], ((it - 2) >> 1) & 1, wc, kSiteBComp))) break;
+      tc_fence_after();
+      tmem_st16(trow + C::col_pdq(b) + 16 * g, ppk);
+      tmem_st16(trow + C::col_pdq(b) + 32 + 16 * g, dpk);
+      uint8_t* ds_row = sDs + b * C::kDsBytes + row * 128;
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        const int ch = g * 4 + c4;
+        *reinterpret_cast<uint4*>(ds_row + ((ch ^ (row & 7)) * 16)) =
+            make_uint4(dpk[4 * c4], dpk[4 * c4 + 1], dpk[4 * c4 + 2], dpk[4 * c4 + 3]);
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_comp[b]);
+      if (++slot == kStages) {
+        slot = 0;
+        ring_ph ^= 1u;
+      }
+      if (++i == st.i0 + st.nq) {
+        i = st.i0;
+        ++head;
+        if (biased && head < p.group) slope2 = __ldg(p.slopes + h0 + head) * kLog2e;
+      }
+    }
+    // ------------------------------- dK, dV epilogue (warpgroup 0: dV, 1: dK)
+    if (ok && n > 0) ok = warp_wait_b(bar_dkv, 0, wc, kSiteBEpi);
+    if (ok) {
+      tc_fence_after();
+      if (n > 0) {
+        if (g == 0) stage_row_bf16<D>(trow + C::kColDV, sV, row, 1.f);
+        else stage_row_bf16<D>(trow + C::kColDK, sK, row, p.scale);
+      } else {  // no query sees the block: zeros (nothing was loaded into sV, sK)
+        uint8_t* box = (g == 0 ? sV : sK) + row * 128;
+        for (int c = 0; c < C::kBoxes; ++c)
+          for (int q4 = 0; q4 < 8; ++q4)
+            *reinterpret_cast<uint4*>(box + c * C::kKVBox + q4 * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_epi);
+      if (threadIdx.x == 0 && mbar_wait(bar_epi, 0, wc, kSiteBEpi)) {
+        for (int c = 0; c < C::kBoxes; ++c) {
+          tma_store_4d(&tm_dv, sV + c * C::kKVBox, c * 64, kb * kBkB, hk, b_idx);
+          tma_store_4d(&tm_dk, sK + c * C::kKVBox, c * 64, kb * kBkB, hk, b_idx);
+        }
+        tma_store_commit_and_wait_read();
+      }
+    }
+    __syncwarp();
+  } else {
+    regs_decrease<kRegsDq>();
+    // -------------------------------- dQ reduction (one d-row of dQ^T per thread)
+    const int dcol = threadIdx.x - kWarpDq * 32;
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int head = 0, i = st.i0;
+    for (int it = 0; it < n; ++it) {
+      const int b = it & 1;
+      const int q0 = i * kBqB, bh = bh0 + head;
+      if (++i == st.i0 + st.nq) {
+        i = st.i0;
+        ++head;
+      }
+      if (!warp_wait_b_suspend(&bar_dqf[b], (it >> 1) & 1, wc, kSiteBDq)) break;
+      if (D == 64 && dcol >= D) {  // the zero-padded rows of dQ^T: nothing to read or add
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_dqe[b]);
+        continue;
+      }
+      tc_fence_after();
+      uint32_t v[2][32];
+      tmem_ld32(trow + C::col_pdq(b), v[0]);
+      tmem_ld32(trow + C::col_pdq(b) + 32, v[1]);
+      tmem_ld_wait32(v[0]);
+      tmem_ld_wait32(v[1]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_dqe[b]);
+      float* dst = p.dq_acc + (static_cast<size_t>(bh) * p.N + q0) * D + dcol;
+      const int lim = min(kBqB, p.N - q0);
+      if constexpr (DET) {
+        const float mul =
+            pow2f(det_shift(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1]));
+        constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic rounds x to an integer in the low bits
+        int* dsti = reinterpret_cast<int*>(dst);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (hh * 32 + c < lim)
+              atomicAdd(dsti + static_cast<size_t>(hh * 32 + c) * D,
+                        __float_as_int(fmaf(__uint_as_float(v[hh][c]), mul, kMagic)) - 0x4B400000);
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (hh * 32 + c < lim) atomicAdd(dst + static_cast<size_t>(hh * 32 + c) * D, __uint_as_float(v[hh][c]));
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int MODE, bool DET>
+cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  using C = BwdCfg<D>;
+  const BwdWorkspace w = bwd_workspace_layout(a.B, a.H, a.N, a.d);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  cudaError_t e;
+  CUtensorMap tq, tk, tv, tdo, tdk, tdv;
+  constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if ((e = make_tmap_4d(&tq, a.q, kBf16, 2, D, a.N, a.H, a.B, a.sq.s, 64, kBqB))) return e;
+  if ((e = make_tmap_4d(&tdo, a.dout, kBf16, 2, D, a.N, a.H, a.B, a.sdo.s, 64, kBqB))) return e;
+  if ((e = make_tmap_4d(&tk, a.k, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sk.s, 64, kBkB))) return e;
+  if ((e = make_tmap_4d(&tv, a.v, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sv.s, 64, kBkB))) return e;
+  if ((e = make_tmap_4d(&tdk, a.dk, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sdk.s, 64, kBkB))) return e;
+  if ((e = make_tmap_4d(&tdv, a.dv, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sdv.s, 64, kBkB))) return e;
+  Params p{};
+  p.plan = sc.plan;
+  p.causal = sc.causal;
+  p.N = a.N;
+  p.Npad = w.npad;
+  p.H = a.H;
+  p.Hkv = sc.Hkv;
+  p.group = a.group;
+  p.nkb = (a.N + kBkB - 1) / kBkB;
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * kLog2e;
+  if (MODE == 2) {
+    p.cap_in = a.scale / sc.softcap;
+    p.cap_out = sc.softcap * kLog2e;
+  }
+  p.slopes = sc.slopes;
+  p.aug = ws + w.off_aug;
+  p.dq_acc = reinterpret_cast<float*>(ws + w.off_dq);
+  p.dq_bmax = reinterpret_cast<const float*>(ws + w.off_dqmax);
+  p.kv_max = reinterpret_cast<const float*>(ws + w.off_kvmax);
+  p.err_word = a.err_word;
+  p.wait_ns = a.dbg.wait_limit_ns;
+  auto kern = bwd_scored_kernel<D, MODE, DET>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
+  // The register split assumes the block launches with kLaunchRegs per thread.
+  cudaFuncAttributes fattr;
+  if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
+  if (static_cast<uint32_t>(fattr.numRegs) < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  kern<<<static_cast<unsigned>(p.nkb * a.B * sc.Hkv), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
+  return cudaGetLastError();
+}
+
+template <int D, int MODE>
+cudaError_t launch_mode(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  return a.deterministic ? launch_main<D, MODE, true>(a, sc, stream) : launch_main<D, MODE, false>(a, sc, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  if (sc.softcap > 0.f) return launch_mode<D, 2>(a, sc, stream);
+  return sc.slopes ? launch_mode<D, 1>(a, sc, stream) : launch_mode<D, 0>(a, sc, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_scored(const BwdArgs& args, const ScoreArgs& sc, cudaStream_t stream) {
+  BwdArgs a = args;
+  a.group = a.H / sc.Hkv;
+  a.raw_lse = sc.softcap > 0.f;
+  a.seen_by = sc.plan.k;
+  cudaError_t e;
+  if ((e = launch_bwd_prep(a, stream))) return e;
+  if ((e = a.d == 64 ? launch_d<64>(a, sc, stream) : launch_d<128>(a, sc, stream))) return e;
+  return launch_bwd_dq(a, stream);
+}
+
+}  // namespace fa
