@@ -619,10 +619,17 @@ def fa_fwd_splitkv(q, k, v, o=None, lse=None, workspace=None, n_split: int = 0, 
     return o, lse
 
 
+_Int64x2, _Int64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
 def _check_layout(name, t, shape, dtype, device):
-    """Any layout whose last dimension is contiguous, on `device`.  Returns the strides argument: None
-    when the tensor is dense, else its strides from the second-to-last dimension outwards (dimensions
-    of one element, whose stride means nothing, count as dense)."""
+    """(address, strides) of a tensor in any layout whose last dimension is contiguous, on `device`.
+
+    strides is None when the tensor is dense, else its strides from the second-to-last
+    dimension outwards (dimensions of one element, whose stride means nothing, count as
+    dense)."""
+    if getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr(), None
     import torch
 
     if not isinstance(t, torch.Tensor):
@@ -631,37 +638,58 @@ def _check_layout(name, t, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if t.is_contiguous():
-        return None
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    out, dense = [], shape[-1]
-    for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
-        out.append(x if n != 1 else dense)
-        dense *= n
-    return (ctypes.c_int64 * len(out))(*out)
+    if 1 in shape:
+        out, dense = [], shape[-1]
+        for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
+            out.append(x if n != 1 else dense)
+            dense *= n
+    else:
+        out = st[-2::-1]
+    return t.data_ptr(), (_Int64x3 if len(out) == 3 else _Int64x2)(*out)
 
 
 def _check_flat(name, t, shape, dtype, device):
-    """A dense tensor on `device`, or None."""
+    """The address of a dense tensor on `device` (None: 0)."""
     if t is None:
-        return
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)} on {device}")
+        return 0
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
-def _scratch(workspace, need, device):
-    """The caller's workspace (a dense CUDA tensor on `device`), or a new one."""
+def _check_cuda(name, t, dtype=None):
+    """The device of a CUDA tensor (of `dtype`, if given)."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {dev}")
+    return dev
+
+
+def _bytes_of(name, t, device):
+    """(address, bytes) of a plan or workspace: a dense tensor on `device`."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
     import torch
 
-    if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
-    return workspace
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, where, device, stream, *args)
+    # The raw handle of the current stream: building a Stream object for it costs more than the call.
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise FAError(st, where)
 
 
 def fa_mask_plan_size(B: int, N: int) -> int:
@@ -681,26 +709,20 @@ def fa_mask_plan(B: int, N: int, cu_docs=None, prefix=None, causal: bool = True,
 
     lib = load_library()
     ref = cu_docs if cu_docs is not None else prefix if prefix is not None else plan
-    dev = ref.device if ref is not None else torch.device("cuda" if device is None else device)
-    if dev.type == "cuda" and dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
+    if ref is not None:
+        dev = _check_cuda("cu_docs, prefix or plan", ref)
+    else:
+        dev = torch.device("cuda" if device is None else device)
+        if dev.index is None:
+            dev = torch.device(dev.type, torch.cuda.current_device())
     n_docs = 1 if cu_docs is None else cu_docs.shape[1] - 1
-    _check_flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, dev)
-    _check_flat("prefix", prefix, (B, n_docs), torch.int32, dev)
-    plan = _scratch(plan, fa_mask_plan_size(B, N), dev)
-    with torch.cuda.device(dev):
-        st = lib.fa_mask_plan(_ptr(cu_docs), _ptr(prefix), n_docs, _ptr(plan), _ws_bytes(plan), B, N,
-                              int(bool(causal)), _stream_handle(stream))
-    _check(st, "fa_mask_plan")
-    return plan
-
-
-def _plan_args(plan, device):
+    pc = _check_flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, dev)
+    px = _check_flat("prefix", prefix, (B, n_docs), torch.int32, dev)
     if plan is None:
-        return None, 0
-    if plan.device != device or not plan.is_contiguous():
-        raise ValueError(f"plan must be a contiguous CUDA tensor on {device}")
-    return plan.data_ptr(), _ws_bytes(plan)
+        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=dev)
+    pp, pb = _bytes_of("plan", plan, dev)
+    _call(lib.fa_mask_plan, "fa_mask_plan", dev, stream, pc, px, n_docs, pp, pb, B, N, int(bool(causal)))
+    return plan
 
 
 def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float | None = None, softcap: float = 0.0,
@@ -716,24 +738,21 @@ def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float 
     import torch
 
     lib = load_library()
-    B, H, N, d = q.shape
-    Hkv, dev, bf = k.shape[1], q.device, torch.bfloat16
-    sq = _check_layout("q", q, (B, H, N, d), bf, dev)
-    sk = _check_layout("k", k, (B, Hkv, N, d), bf, dev)
-    sv = _check_layout("v", v, (B, Hkv, N, d), bf, dev)
+    bf = torch.bfloat16
+    qs, dev = q.shape, _check_cuda("q", q, bf)
+    B, H, N, d = qs
+    Hkv = k.shape[1]
+    ks = (B, Hkv, N, d)
     if o is None:
-        o = torch.empty((B, H, N, d), dtype=bf, device=dev)
+        o = torch.empty(qs, dtype=bf, device=dev)
     if lse is None:
         lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-    so = _check_layout("o", o, (B, H, N, d), bf, dev)
-    _check_flat("lse", lse, (B, H, N), torch.float32, dev)
-    _check_flat("slopes", slopes, (H,), torch.float32, dev)
-    pp, pb = _plan_args(plan, dev)
-    with torch.cuda.device(dev):
-        st = lib.fa_fwd_scored(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, _ptr(o), so, _ptr(lse), B, H, Hkv, N, d, pp, pb,
-                               int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
-                               _ptr(slopes), _stream_handle(stream))
-    _check(st, "fa_fwd_scored")
+    pp, pb = (0, 0) if plan is None else _bytes_of("plan", plan, dev)
+    _call(lib.fa_fwd_scored, "fa_fwd_scored", dev, stream, *_check_layout("q", q, qs, bf, dev),
+          *_check_layout("k", k, ks, bf, dev), *_check_layout("v", v, ks, bf, dev), *_check_layout("o", o, qs, bf, dev),
+          _check_flat("lse", lse, (B, H, N), torch.float32, dev), B, H, Hkv, N, d, pp, pb, int(bool(causal)),
+          d ** -0.5 if scale is None else float(scale), float(softcap),
+          _check_flat("slopes", slopes, (H,), torch.float32, dev))
     return o, lse
 
 
@@ -754,55 +773,51 @@ def fa_bwd_scored(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None
     import torch
 
     lib = load_library()
-    B, H, N, d = q.shape
-    Hkv, dev, bf = k.shape[1], q.device, torch.bfloat16
-    qs, ks = (B, H, N, d), (B, Hkv, N, d)
+    bf = torch.bfloat16
+    qs, dev = q.shape, _check_cuda("q", q, bf)
+    B, H, N, d = qs
+    Hkv = k.shape[1]
+    ks = (B, Hkv, N, d)
     dq = torch.empty(qs, dtype=bf, device=dev) if dq is None else dq
     dk = torch.empty(ks, dtype=bf, device=dev) if dk is None else dk
     dv = torch.empty(ks, dtype=bf, device=dev) if dv is None else dv
-    args = []
-    for name, t, shape in (("q", q, qs), ("k", k, ks), ("v", v, ks), ("o", o, qs), ("do", do, qs)):
-        args += [_ptr(t), _check_layout(name, t, shape, bf, dev)]
-    args.append(_ptr(lse))
-    for name, t, shape in (("dq", dq, qs), ("dk", dk, ks), ("dv", dv, ks)):
-        args += [_ptr(t), _check_layout(name, t, shape, bf, dev)]
-    _check_flat("lse", lse, (B, H, N), torch.float32, dev)
-    _check_flat("slopes", slopes, (H,), torch.float32, dev)
-    pp, pb = _plan_args(plan, dev)
     if workspace is None:
-        workspace = torch.empty(max(int(lib.fa_bwd_scored_workspace_size(B, H, Hkv, N, d)), 1), dtype=torch.uint8,
-                                device=dev)
-    workspace = _scratch(workspace, 0, dev)
-    with torch.cuda.device(dev):
-        st = lib.fa_bwd_scored(*args, _ptr(workspace), _ws_bytes(workspace), B, H, Hkv, N, d, pp, pb,
-                               int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
-                               _ptr(slopes), int(bool(deterministic)), _stream_handle(stream))
-    _check(st, "fa_bwd_scored")
+        workspace = torch.empty(max(fa_bwd_scored_workspace_size(B, H, Hkv, N, d), 1), dtype=torch.uint8, device=dev)
+    pp, pb = (0, 0) if plan is None else _bytes_of("plan", plan, dev)
+    _call(lib.fa_bwd_scored, "fa_bwd_scored", dev, stream, *_check_layout("q", q, qs, bf, dev),
+          *_check_layout("k", k, ks, bf, dev), *_check_layout("v", v, ks, bf, dev), *_check_layout("o", o, qs, bf, dev),
+          *_check_layout("do", do, qs, bf, dev), _check_flat("lse", lse, (B, H, N), torch.float32, dev),
+          *_check_layout("dq", dq, qs, bf, dev), *_check_layout("dk", dk, ks, bf, dev),
+          *_check_layout("dv", dv, ks, bf, dev), *_bytes_of("workspace", workspace, dev), B, H, Hkv, N, d, pp, pb,
+          int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
+          _check_flat("slopes", slopes, (H,), torch.float32, dev), int(bool(deterministic)))
     return dq, dk, dv
 
 
-def _paged_dtype(t):
+def _cache_device(k_cache):
     import torch
 
-    code = {torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"the cache must be bfloat16 or float16, got {t.dtype}")
-    return code
+    if k_cache.dtype is not torch.bfloat16 and k_cache.dtype is not torch.float16:
+        raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype}")
+    return _check_cuda("k_cache", k_cache)
 
 
 def _check_cache(k_cache, v_cache, page_table, seq_lens, dev):
+    """The arguments that describe a paged cache, its dtype code and sizes (pages, heads, page size, d; sequences)."""
     import torch
 
-    shape = tuple(k_cache.shape)
-    if len(shape) != 4:
-        raise ValueError("k_cache must be indexed [n_pages, Hkv, page_size, d]")
-    sk = _check_layout("k_cache", k_cache, shape, k_cache.dtype, dev)
-    sv = _check_layout("v_cache", v_cache, shape, k_cache.dtype, dev)
+    dt = k_cache.dtype
+    shape = k_cache.shape
+    if len(shape) != 4 or page_table.dim() != 2:
+        raise ValueError("k_cache must be indexed [n_pages, Hkv, page_size, d], page_table [B, max_pages]")
     B, max_pages = page_table.shape
+    ts = page_table.stride(0)
     if page_table.dtype != torch.int32 or page_table.device != dev or (max_pages > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be an int32 CUDA tensor [B, max_pages] with contiguous rows on {dev}")
-    _check_flat("seq_lens", seq_lens, (B,), torch.int32, dev)
-    return sk, sv, shape, B, max_pages, page_table.stride(0) if B > 1 else max(max_pages, page_table.stride(0))
+        raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on {dev}")
+    cache = (*_check_layout("k_cache", k_cache, shape, dt, dev), *_check_layout("v_cache", v_cache, shape, dt, dev),
+             page_table.data_ptr(), ts if B > 1 else max(max_pages, ts),
+             _check_flat("seq_lens", seq_lens, (B,), torch.int32, dev))
+    return cache, 1 if dt is torch.bfloat16 else 2, shape, B, max_pages
 
 
 def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream=None):
@@ -816,18 +831,12 @@ def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream
     import torch
 
     lib = load_library()
-    dev = k_cache.device
-    code = _paged_dtype(k_cache)
-    skc, svc, (n_pages, Hkv, page, d), B, max_pages, ts = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
-    T = k.shape[0]
-    sk = _check_layout("k", k, (T, Hkv, d), k_cache.dtype, dev)
-    sv = _check_layout("v", v, (T, Hkv, d), k_cache.dtype, dev)
-    _check_flat("cu_new", cu_new, (B + 1,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        st = lib.fa_paged_append(_ptr(k), sk, _ptr(v), sv, _ptr(k_cache), skc, _ptr(v_cache), svc, _ptr(page_table),
-                                 ts, _ptr(seq_lens), _ptr(cu_new), B, T, Hkv, d, page, n_pages, max_pages, code,
-                                 _stream_handle(stream))
-    _check(st, "fa_paged_append")
+    dev = _cache_device(k_cache)
+    cache, code, (n_pages, Hkv, page, d), B, max_pages = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
+    T, dt = k.shape[0], k_cache.dtype
+    _call(lib.fa_paged_append, "fa_paged_append", dev, stream, *_check_layout("k", k, (T, Hkv, d), dt, dev),
+          *_check_layout("v", v, (T, Hkv, d), dt, dev), *cache,
+          _check_flat("cu_new", cu_new, (B + 1,), torch.int32, dev), B, T, Hkv, d, page, n_pages, max_pages, code)
 
 
 def fa_paged_decode_workspace_size(B: int, H: int, Hkv: int, d: int) -> int:
@@ -846,30 +855,24 @@ def fa_paged_decode(q, k_cache, v_cache, page_table, seq_lens, o=None, lse=None,
     import torch
 
     lib = load_library()
-    B, H, d = q.shape
-    dev, dt = q.device, q.dtype
-    code = _paged_dtype(k_cache)
-    skc, svc, (n_pages, Hkv, page, dc), Bt, max_pages, ts = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
+    qs, dev, dt = q.shape, _cache_device(k_cache), k_cache.dtype
+    B, H, d = qs
+    cache, code, (n_pages, Hkv, page, dc), Bt, max_pages = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
     if Bt != B or dc != d:
         raise ValueError(f"q is for {B} sequences of head dim {d}, the page table for {Bt} and the cache for {dc}")
-    sq = _check_layout("q", q, (B, H, d), k_cache.dtype, dev)
+    pq, sq = _check_layout("q", q, qs, dt, dev)
     if o is None:
-        o = torch.empty((B, H, d), dtype=dt, device=dev)
+        o = torch.empty(qs, dtype=dt, device=dev)
     if lse is None:
         lse = torch.empty((B, H), dtype=torch.float32, device=dev)
-    so = _check_layout("o", o, (B, H, d), dt, dev)
-    _check_flat("lse", lse, (B, H), torch.float32, dev)
-    _check_flat("slopes", slopes, (H,), torch.float32, dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(max(int(lib.fa_paged_decode_workspace_size(B, H, Hkv, d)), 1), dtype=torch.uint8,
-                                    device=dev)
-        workspace = _scratch(workspace, 0, dev)
-        st = lib.fa_paged_decode(_ptr(q), sq, _ptr(k_cache), skc, _ptr(v_cache), svc, _ptr(page_table), ts,
-                                 _ptr(seq_lens), _ptr(o), so, _ptr(lse), _ptr(workspace), _ws_bytes(workspace), B, H,
-                                 Hkv, d, page, n_pages, max_pages, code, d ** -0.5 if scale is None else float(scale),
-                                 float(softcap), _ptr(slopes), _stream_handle(stream))
-    _check(st, "fa_paged_decode")
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = fa_paged_decode_workspace_size(B, H, Hkv, d)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _call(lib.fa_paged_decode, "fa_paged_decode", dev, stream, pq, sq, *cache, *_check_layout("o", o, qs, dt, dev),
+          _check_flat("lse", lse, (B, H), torch.float32, dev), *_bytes_of("workspace", workspace, dev), B, H, Hkv, d,
+          page, n_pages, max_pages, code, d ** -0.5 if scale is None else float(scale), float(softcap),
+          _check_flat("slopes", slopes, (H,), torch.float32, dev))
     return o, lse
 
 
