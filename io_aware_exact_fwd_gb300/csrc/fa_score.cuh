@@ -19,24 +19,33 @@ __device__ __forceinline__ int2 queries_of(const MaskPlan& p, int causal, int b,
   return make_int2(causal ? j : 0, N);
 }
 
-// tanh for the cap, to an absolute error of about 2^-23 (the cap's scores are
-// cap * tanh, so tanh.approx, off by up to 2^-11 relative, would move a capped score by
-// percents of 1 and its weight with it).
+// tanh for the cap.  A capped score is softcap * tanh(u); tanh.approx, off by up to
+// 2^-11 relative, would move scores by up to hundredths and their weights by percents.
 //
-// |u| <= 1: u p(u^2), p of degree 6 with the smallest relative error on [0, 1] (3.5e-8,
-// found by linear programming on 4001 points).  Pairs, on the FMA pipe: 8 packed
-// operations, none on the MUFU that the exponentials need.
-__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 tanh_small(float2 u) {
+// |u| <= 1: u p(u^2) with p of degree 5 of the smallest relative error on [0, 1] (5.6e-7,
+// found by linear programming on 4001 points; the score is a dot product of 64 or 128
+// terms, whose own fp32 error is larger).  On the FMA pipe in pairs, none of it on the
+// MUFU that the exponentials need.  The coefficients come with a factor (CapPoly), the
+// result is factor * tanh(u).
+__host__ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+struct CapPoly {
+  float2 c[6];
+};
+inline CapPoly cap_poly(float factor) {
+  const float c[6] = {0.999999463558197f,     -0.33328977227211f,    0.13280832767486572f,
+                      -0.05158914253115654f, 0.016724668443202972f, -0.0030597823206335306f};
+  CapPoly p;
+  for (int i = 0; i < 6; ++i) p.c[i] = pair(c[i] * factor);
+  return p;
+}
+// tanh(u) * factor / u.
+__device__ __forceinline__ float2 tanh_over_u(float2 u, const CapPoly& k) {
   const float2 w = __fmul2_rn(u, u);
-  float2 p = pair(0.001009133062325418f);
-  p = __ffma2_rn(p, w, pair(-0.0061064367182552814f));
-  p = __ffma2_rn(p, w, pair(0.0201801136136055f));
-  p = __ffma2_rn(p, w, pair(-0.05340071767568588f));
-  p = __ffma2_rn(p, w, pair(0.13323982059955597f));
-  p = __ffma2_rn(p, w, pair(-0.33332768082618713f));
-  p = __ffma2_rn(p, w, pair(0.9999999403953552f));
-  return __fmul2_rn(u, p);
+  float2 p = __ffma2_rn(k.c[5], w, k.c[4]);
+  p = __ffma2_rn(p, w, k.c[3]);
+  p = __ffma2_rn(p, w, k.c[2]);
+  p = __ffma2_rn(p, w, k.c[1]);
+  return __ffma2_rn(p, w, k.c[0]);
 }
 // Any u: 1 - 2 / (1 + e^2u), which keeps its absolute error at both ends (e^2u -> 0 or
 // infinity gives -1 or 1).

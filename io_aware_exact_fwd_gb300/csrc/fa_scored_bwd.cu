@@ -32,6 +32,7 @@ struct Params {
   int causal, N, Npad, H, Hkv, group, nkb;
   float scale, scale_log2;
   float cap_in, cap_out;  // scale / softcap, softcap log2(e)
+  CapPoly poly;           // factor 1
   const float* slopes;
   const uint8_t* aug;
   float* dq_acc;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             const int c = 4 * c4 + 2 * e;
             const float2 u = __fmul2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(p.cap_in));
-            const float2 t = large ? make_float2(tanh_any(u.x), tanh_any(u.y)) : tanh_small(u);
+            const float2 t = large ? make_float2(tanh_any(u.x), tanh_any(u.y)) : __fmul2_rn(u, tanh_over_u(u, p.poly));
             const float2 x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
             const float2 bend = __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f));
             const float2 y = __fmul2_rn(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), bend);
@@ -495,6 +496,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   if (MODE == 2) {
     p.cap_in = a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
+    p.poly = cap_poly(1.f);
   }
   p.slopes = sc.slopes;
   p.aug = ws + w.off_aug;

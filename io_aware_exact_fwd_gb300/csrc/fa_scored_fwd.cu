@@ -81,6 +81,7 @@ struct Params {
   float scale_log2;   // scale log2(e)
   float cap_in;       // scale / softcap
   float cap_out;      // softcap log2(e)
+  CapPoly poly;       // factor cap_out
   const float* slopes;
   float* lse;
   unsigned int* err_word;
@@ -383,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_used = 0.f;  // reference maximum, log2 units (0 until the row has seen a key)
       bool seen = false;
       float l = 0.f;
+      // No row of the warp sees a key right of itself: |i - j| = i - j wherever it counts.
+      const bool one_sided = MODE == 0 || __all_sync(0xffffffffu, see.y <= qrow + 1);
 
       for (int j = 0; j < nkt; ++j, ++scnt) {
         if (!warp_wait_suspend(&bar_s[t], scnt & 1, wc, kSiteSoftS)) {
@@ -392,157 +395,152 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int kbase = (blocks.y - 1 - j) * kBlockK;
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
-        // Sign of j - i over the block: all <= 0, all >= 0, or mixed.
-        const bool left = kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
+        const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
         uint32_t r[4][32];
-        // Chunk c's scores in log2 units, in place: cap, bias, mask.  MODE 0 keeps the raw
-        // products (their scale is folded into the exponentials).
-        auto score = [&](int c) {
-          if constexpr (MODE == 2) {
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx = max3(mx, fabsf(__uint_as_float(r[c][i])), fabsf(__uint_as_float(r[c][i + 1])));
-            if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[c][i] = __float_as_uint(p.cap_out * tanh_any(__uint_as_float(r[c][i]) * p.cap_in));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-                const float2 y = __fmul2_rn(tanh_small(__fmul2_rn(s, pair(p.cap_in))), pair(p.cap_out));
-                r[c][i] = __float_as_uint(y.x);
-                r[c][i + 1] = __float_as_uint(y.y);
-              }
-            }
-          }
-          if (MODE == 1 || (MODE == 2 && p.slopes)) {
-            const float mul = MODE == 1 ? p.scale_log2 : 1.f;
-            const float off = static_cast<float>(kbase + c * 32 - qrow);  // j - i of the chunk's first key
-            if (left || right) {
-              const float sg = left ? slope2 : -slope2;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 dist = __fadd2_rn(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), pair(off));
-                const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])),
-                                            pair(mul), __fmul2_rn(dist, pair(sg)));
-                r[c][i] = __float_as_uint(y.x);
-                r[c][i + 1] = __float_as_uint(y.y);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[c][i] = __float_as_uint(
-                    fmaf(__uint_as_float(r[c][i]), mul, -slope2 * fabsf(off + static_cast<float>(i))));
-            }
-          }
-          if (need_mask) {
-            const int a = see.x - kbase - c * 32, e = see.y - kbase - c * 32;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < a || i >= e) r[c][i] = __float_as_uint(-INFINITY);
-          }
-        };
-        const float c_mul = MODE == 0 ? p.scale_log2 : 1.f;
-        auto tile_max = [&]() -> float {
-          float mc[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float a[11];
-#pragma unroll
-            for (int i = 0; i < 10; ++i)
-              a[i] = max3(__uint_as_float(r[c][3 * i]), __uint_as_float(r[c][3 * i + 1]),
-                          __uint_as_float(r[c][3 * i + 2]));
-            a[10] = fmaxf(__uint_as_float(r[c][30]), __uint_as_float(r[c][31]));
-            mc[c] = fmaxf(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
-                          fmaxf(a[9], a[10]));
-          }
-          return fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * c_mul;  // c_mul > 0
-        };
-        // P = exp2(score - m) over chunk c, packed bf16 over the S columns.
-        float2 part;
-        auto exp_chunk = [&](int c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 s = make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1]));
-            const float2 y = MODE == 0 ? __ffma2_rn(s, pair(c_mul), pair(-m_used)) : __fadd2_rn(s, pair(-m_used));
-            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            part = __fadd2_rn(part, e);
-            pk[i] = pack_bf16x2(e.x, e.y);
-          }
-          tmem_st16(trow + col_s + c * 16, pk);
-        };
-        // The block against its own maximum: the reference moves up to it where it is higher (or
-        // the row's first), and O_t, which holds P V of the earlier blocks, is rescaled.
-        auto with_own_max = [&]() {
-          const float mt = tile_max();
-          const bool first = !seen && mt > -INFINITY;
-          const bool up = first || mt > m_used;
-          const float alpha = up && seen ? ex2_approx(m_used - mt) : 1.f;
-          const bool scale_o = up && seen;
-          if (up && mt > -INFINITY) m_used = mt;
-          seen = seen || first;
-          l *= alpha;
-          if (j > 0 && __any_sync(0xffffffffu, scale_o)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(trow + col_o + c * 32, o);
-              tmem_ld_wait32(o);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y =
-                    __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), pair(alpha));
-                o[i] = __float_as_uint(y.x);
-                o[i + 1] = __float_as_uint(y.y);
-              }
-              tmem_st32(trow + col_o + c * 32, o);
-            }
-          }
-          part = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) exp_chunk(c);
-        };
-
-        part = make_float2(0.f, 0.f);
-        // A bias that falls with distance makes the maxima grow while the blocks lie right of the
-        // rows: there, too, the maximum comes first.
-        if (j == 0 || (MODE != 0 && slope2 > 0.f && right)) {
+        auto load = [&]() {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
+        };
+        load();
+        // The general form of the scores (any tanh argument, keys on both sides of the row), eight
+        // columns at a time in place in TMEM: a small rolled loop, because it is rare and the
+        // kernel's speed depends on its code fitting the instruction caches.
+        bool pre = MODE != 0 && !left && !right && (MODE == 1 || p.slopes != nullptr);
+        if constexpr (MODE == 2) {
+          float mx = 0.f;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) score(c);
-          with_own_max();
-        } else {
-          tmem_ld32(trow + col_s, r[0]);
-          tmem_ld32(trow + col_s + 32, r[1]);
-          tmem_ld_wait32(r[0]);
-          tmem_ld_wait32(r[1]);
-          tmem_ld32(trow + col_s + 64, r[2]);
-          tmem_ld32(trow + col_s + 96, r[3]);
-          score(0);
-          exp_chunk(0);
-          score(1);
-          exp_chunk(1);
-          tmem_ld_wait32(r[2]);
-          tmem_ld_wait32(r[3]);
-          score(2);
-          exp_chunk(2);
-          score(3);
-          exp_chunk(3);
-          const float sum = part.x + part.y;
-          // Redo when a P may have overflowed (also inf and NaN), or when the block holds the row's
-          // first visible keys (the reference is then no maximum at all).
-          const bool bad = !(sum <= kSpeculationSumBound) ||
-                           (!seen && see.x < kbase + kBlockK && see.y > kbase && see.x < see.y);
-          if (__any_sync(0xffffffffu, bad)) {
-            tmem_st_wait();  // the speculative P has landed before it is overwritten
-            with_own_max();
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx = max3(mx, fabsf(__uint_as_float(r[c][i])), fabsf(__uint_as_float(r[c][i + 1])));
+          pre = pre || __any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f));
+        }
+        if (MODE != 0 && pre) {
+#pragma unroll 1
+          for (int c = 0; c < kBlockK; c += 8) {
+            uint32_t x[8];
+            tmem_ld8_wait(trow + col_s + c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float s = __uint_as_float(x[i]);
+              const float a = MODE == 2 ? p.cap_out * tanh_any(s * p.cap_in) : s * p.scale_log2;
+              x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
+            }
+            tmem_st8(trow + col_s + c, x);
           }
+          tmem_st_wait();
+          load();
+        }
+        // r becomes the score minus the reference, in log2 units: cap, bias, mask.
+        const float sg = left ? slope2 : -slope2;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (MODE != 0 && pre) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) - m_used);
+          } else {
+            // The bias of the chunk's first key less the reference; sg more for every key.
+            const float base = MODE == 0 ? -m_used : fmaf(sg, static_cast<float>(kbase + c * 32 - qrow), -m_used);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+              float2 off = pair(base);
+              if (MODE == 1 || (MODE == 2 && p.slopes))
+                off = __ffma2_rn(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), pair(sg), off);
+              float2 y;
+              if constexpr (MODE == 2) {
+                const float2 u = __fmul2_rn(s, pair(p.cap_in));
+                y = __ffma2_rn(u, tanh_over_u(u, p.poly), off);
+              } else {
+                y = __ffma2_rn(s, pair(p.scale_log2), off);
+              }
+              r[c][i] = __float_as_uint(y.x);
+              r[c][i + 1] = __float_as_uint(y.y);
+            }
+          }
+          if (need_mask) {
+            // Bit i: key i of the chunk lies in the row's interval.
+            const int a = min(max(see.x - kbase - c * 32, 0), 32), e = min(max(see.y - kbase - c * 32, 0), 32);
+            const uint32_t vis = static_cast<uint32_t>((1ull << e) - 1ull) & ~static_cast<uint32_t>((1ull << a) - 1ull);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
+          }
+        }
+        // P = exp2(r), packed bf16 over the S columns.  The row's reference is its first block's
+        // maximum.  Later blocks are first taken against the reference as it is, and taken again
+        // against their own maximum if a P may have overflowed, or if they hold the row's first
+        // visible keys.  A bias that falls with distance makes the maxima grow while the blocks lie
+        // right of the rows: there the maximum comes first, too.
+        bool own_max = j == 0 || (MODE != 0 && slope2 > 0.f && right && !one_sided);
+        float2 part;
+        while (true) {
+          if (own_max) {
+            float mc[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float a[11];
+#pragma unroll
+              for (int i = 0; i < 10; ++i)
+                a[i] = max3(__uint_as_float(r[c][3 * i]), __uint_as_float(r[c][3 * i + 1]),
+                            __uint_as_float(r[c][3 * i + 2]));
+              a[10] = fmaxf(__uint_as_float(r[c][30]), __uint_as_float(r[c][31]));
+              mc[c] = fmaxf(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
+                            fmaxf(a[9], a[10]));
+            }
+            const float mt = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            // The reference moves by mt where that is up, or the row's first.
+            const bool first = !seen && mt > -INFINITY;
+            const bool up = first || (seen && mt > 0.f);
+            const float delta = up ? mt : 0.f;
+            const float alpha = up && seen ? ex2_approx(-delta) : 1.f;
+            const bool scale_o = up && seen;
+            m_used += delta;
+            seen = seen || first;
+            l *= alpha;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])),
+                                            pair(-delta));
+                r[c][i] = __float_as_uint(y.x);
+                r[c][i + 1] = __float_as_uint(y.y);
+              }
+            // O_t holds P V of the earlier blocks (Q K^T of this block was issued after them).
+            if (j > 0 && __any_sync(0xffffffffu, scale_o)) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 8) {
+                uint32_t o[8];
+                tmem_ld8_wait(trow + col_o + c, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st8(trow + col_o + c, o);
+              }
+            }
+          }
+          part = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = make_float2(ex2_approx(__uint_as_float(r[c][2 * i])),
+                                           ex2_approx(__uint_as_float(r[c][2 * i + 1])));
+              part = __fadd2_rn(part, e);
+              pk[i] = pack_bf16x2(e.x, e.y);
+            }
+            tmem_st16(trow + col_s + c * 16, pk);
+          }
+          if (own_max) break;
+          const float sum = part.x + part.y;
+          const bool bad = !(sum <= kSpeculationSumBound) ||  // also inf and NaN
+                           (!seen && see.x < kbase + kBlockK && see.y > kbase && see.x < see.y);
+          if (!__any_sync(0xffffffffu, bad)) break;
+          tmem_st_wait();  // the speculative P has landed before it is overwritten
+          own_max = true;
         }
         l += part.x + part.y;
         tmem_st_wait();
@@ -634,6 +632,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   if (MODE == 2) {
     p.cap_in = a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
+    p.poly = cap_poly(p.cap_out);
   }
   p.slopes = sc.slopes;
   p.lse = a.lse;
