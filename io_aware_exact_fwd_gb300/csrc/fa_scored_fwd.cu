@@ -37,8 +37,14 @@ constexpr uint32_t kRegsNeeded = 2 * 128 * kRegsSoftmax + 128 * kRegsControl;
 static_assert(kRegsNeeded <= 65536, "register split exceeds the SM register file");
 constexpr uint32_t kTmemCols = 512;
 // A block is exponentiated against the running reference without its own maximum; its
-// row sum then proves that no P passed 2^16 (else the block is redone).
-constexpr float kSpeculationSumBound = 65536.0f;
+// row sum then proves that no P passed 2^60 (else the block is redone).  P is bf16 and
+// everything it enters is fp32, so a reference that is off costs no precision while
+// weights, sums and O stay far from the ends of the exponent's range.
+constexpr float kSpeculationSumBound = 1.152921504606847e18f;
+// With a cap, scores lie in [-softcap, softcap] log2(e) (plus a bias whose maximum over
+// the row's keys is known): up to this bound on softcap log2(e) that maximum alone is the
+// reference, with P in 2^-80 .. 2^80 and no maximum taken at all.
+constexpr float kBoundedCap = 80.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -145,7 +151,14 @@ __device__ __forceinline__ bool warp_wait_suspend(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, ok);
 }
 
-// MODE 0: scores as they are; 1: with a distance bias; 2: capped (and biased if slopes).
+// Bit i: key k0 + i lies in the row's interval.
+__device__ __forceinline__ uint32_t visible_bits(int2 see, int k0) {
+  const int a = min(max(see.x - k0, 0), 32), e = min(max(see.y - k0, 0), 32);
+  return static_cast<uint32_t>((1ull << e) - 1ull) & ~static_cast<uint32_t>((1ull << a) - 1ull);
+}
+
+// MODE 0: scores as they are; 1: with a distance bias; 2: capped within kBoundedCap, 3:
+// capped beyond it (both biased if slopes).
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -381,7 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_hi = keys_of(p.plan, p.causal, b, row0, p.N).y;
       const float slope2 = MODE != 0 && p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
       const int nkt = blocks.y - blocks.x;
-      float m_used = 0.f;  // reference maximum, log2 units (0 until the row has seen a key)
+      // Reference maximum, log2 units (0 until the row has seen a key).  MODE 2: the largest bias
+      // among the row's keys: 0, at the row's own position, or for a negative slope at its farthest.
+      float m_used = 0.f;
+      if (MODE == 2 && slope2 < 0.f && see.x < see.y)
+        m_used = -slope2 * static_cast<float>(max(qrow - see.x, see.y - 1 - qrow));
       bool seen = false;
       float l = 0.f;
       // No row of the warp sees a key right of itself: |i - j| = i - j wherever it counts.
@@ -396,6 +413,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kbase = (blocks.y - 1 - j) * kBlockK;
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
         const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
+        float2 part = make_float2(0.f, 0.f);
+        if constexpr (MODE == 2) {
+          // The fixed reference: P = exp2(cap + bias - m_used), 32 columns at a time, the next 32
+          // loading meanwhile.  P of columns 32c.. goes over S columns 16c.., which are consumed.
+          uint32_t x[2][32];
+          tmem_ld32(trow + col_s, x[0]);
+          tmem_ld_wait32(x[0]);
+#pragma unroll 1
+          for (int c0 = 0; c0 < 4; c0 += 2) {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              const int c = c0 + cc;
+              uint32_t (&r)[32] = x[cc];
+              if (c < 3) tmem_ld32(trow + col_s + (c + 1) * 32, x[cc ^ 1]);
+              float mx = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                mx = max3(mx, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+              if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  r[i] = __float_as_uint(fmaf(p.cap_out, tanh_any(__uint_as_float(r[i]) * p.cap_in), -m_used));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float2 u = __fmul2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(p.cap_in));
+                  const float2 y = __ffma2_rn(u, tanh_over_u(u, p.poly), pair(-m_used));
+                  r[i] = __float_as_uint(y.x);
+                  r[i + 1] = __float_as_uint(y.y);
+                }
+              }
+              if (p.slopes) {
+                const float off0 = static_cast<float>(kbase + c * 32 - qrow);
+                if (left || right) {
+                  const float sg = left ? slope2 : -slope2, base = sg * off0;
+                  float2 off = make_float2(base, base + sg);
+#pragma unroll
+                  for (int i = 0; i < 32; i += 2) {
+                    if (i > 0)
+                      off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
+                                       : __fadd2_rn(off, pair(2.f * sg));
+                    const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), off);
+                    r[i] = __float_as_uint(y.x);
+                    r[i + 1] = __float_as_uint(y.y);
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    r[i] = __float_as_uint(fmaf(-slope2, fabsf(off0 + static_cast<float>(i)), __uint_as_float(r[i])));
+                }
+              }
+              if (need_mask) {
+                const uint32_t vis = visible_bits(see, kbase + c * 32);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
+              }
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = make_float2(ex2_approx(__uint_as_float(r[2 * i])), ex2_approx(__uint_as_float(r[2 * i + 1])));
+                part = __fadd2_rn(part, e);
+                pk[i] = pack_bf16x2(e.x, e.y);
+              }
+              tmem_st16(trow + col_s + c * 16, pk);
+              if (c < 3) tmem_ld_wait32(x[cc ^ 1]);
+            }
+          }
+        }
+        if constexpr (MODE != 2) {
         uint32_t r[4][32];
         auto load = [&]() {
 #pragma unroll
@@ -408,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns at a time in place in TMEM: a small rolled loop, because it is rare and the
         // kernel's speed depends on its code fitting the instruction caches.
         bool pre = MODE != 0 && !left && !right && (MODE == 1 || p.slopes != nullptr);
-        if constexpr (MODE == 2) {
+        if constexpr (MODE == 3) {
           float mx = 0.f;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -425,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float s = __uint_as_float(x[i]);
-              const float a = MODE == 2 ? p.cap_out * tanh_any(s * p.cap_in) : s * p.scale_log2;
+              const float a = MODE == 3 ? p.cap_out * tanh_any(s * p.cap_in) : s * p.scale_log2;
               x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
             }
             tmem_st8(trow + col_s + c, x);
@@ -443,14 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // The bias of the chunk's first key less the reference; sg more for every key.
             const float base = MODE == 0 ? -m_used : fmaf(sg, static_cast<float>(kbase + c * 32 - qrow), -m_used);
+            float2 off = make_float2(base, MODE == 0 ? base : base + sg);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-              float2 off = pair(base);
-              if (MODE == 1 || (MODE == 2 && p.slopes))
-                off = __ffma2_rn(make_float2(static_cast<float>(i), static_cast<float>(i + 1)), pair(sg), off);
+              if (MODE != 0 && i > 0)  // four keys' steps are added up, then the sum starts afresh
+                off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
+                                 : __fadd2_rn(off, pair(2.f * sg));
               float2 y;
-              if constexpr (MODE == 2) {
+              if constexpr (MODE == 3) {
                 const float2 u = __fmul2_rn(s, pair(p.cap_in));
                 y = __ffma2_rn(u, tanh_over_u(u, p.poly), off);
               } else {
@@ -461,9 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (need_mask) {
-            // Bit i: key i of the chunk lies in the row's interval.
-            const int a = min(max(see.x - kbase - c * 32, 0), 32), e = min(max(see.y - kbase - c * 32, 0), 32);
-            const uint32_t vis = static_cast<uint32_t>((1ull << e) - 1ull) & ~static_cast<uint32_t>((1ull << a) - 1ull);
+            const uint32_t vis = visible_bits(see, kbase + c * 32);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
@@ -475,7 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // visible keys.  A bias that falls with distance makes the maxima grow while the blocks lie
         // right of the rows: there the maximum comes first, too.
         bool own_max = j == 0 || (MODE != 0 && slope2 > 0.f && right && !one_sided);
-        float2 part;
         while (true) {
           if (own_max) {
             float mc[4];
@@ -541,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__any_sync(0xffffffffu, bad)) break;
           tmem_st_wait();  // the speculative P has landed before it is overwritten
           own_max = true;
+        }
         }
         l += part.x + part.y;
         tmem_st_wait();
@@ -629,7 +715,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.BH = a.B * a.H;
   p.nunits = (a.N + kUnitRows - 1) / kUnitRows;
   p.scale_log2 = a.scale * kLog2e;
-  if (MODE == 2) {
+  if (MODE >= 2) {
     p.cap_in = a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
     p.poly = cap_poly(p.cap_out);
@@ -654,7 +740,8 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_d(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  if (sc.softcap > 0.f) return launch<D, 2>(a, sc, stream);
+  if (sc.softcap > 0.f)
+    return sc.softcap * kLog2e <= kBoundedCap ? launch<D, 2>(a, sc, stream) : launch<D, 3>(a, sc, stream);
   return sc.slopes ? launch<D, 1>(a, sc, stream) : launch<D, 0>(a, sc, stream);
 }
 

@@ -71,6 +71,8 @@ CASES = [
     (1, 8, 1, 384, 64, True, 0.0, False, None, [[300]]),                       # a prefix and no documents
     (1, 5, 5, 130, 128, True, 5.0, False, [[0, 130]], [[1000]]),               # the prefix passes the end
     (1, 2, 1, 1100, 128, True, 0.0, True, [[0, 500, 1100]], [[499, 30]]),
+    (1, 2, 2, 400, 64, True, 200.0, True, [[0, 130, 390]], [[20, 100]]),       # a cap far above the scores
+    (1, 2, 1, 300, 128, False, 80.0, True, None, None),
     (3, 2, 2, 65, 64, True, 0.0, False, [[64, 65, 65], [0, 1, 2], [0, 64, 65]], None),
 ]
 
@@ -103,21 +105,23 @@ def test_forward_and_gradients(case, layout):
     report(f"scored {case} {layout} (shares of the bounds)", **r)
 
 
-def test_large_scores_and_slopes():
-    # Scores far past the cap on both sides, and slopes that leave only the nearest keys.
-    B, H, N, d = 1, 2, 300, 64
+@pytest.mark.parametrize("cap", [0.0, 10.0, 55.0, 60.0, 1000.0])
+def test_large_scores_and_slopes(cap):
+    # Scores far past the cap on both sides (or without one), and slopes that leave only the nearest
+    # keys, or the farthest.
+    B, H, N, d = 1, 3, 300, 64
     q, k, v, do = _inputs(B, H, H, N, d, 5, 40.0)
-    slopes = torch.tensor([8.0, -0.03], device="cuda")
+    slopes = torch.tensor([8.0, -0.03, -2.0], device="cuda")
     for causal in (False, True):
-        o, lse = fa.fa_fwd_scored(q, k, v, causal=causal, softcap=10.0, slopes=slopes)
+        o, lse = fa.fa_fwd_scored(q, k, v, causal=causal, softcap=cap, slopes=slopes)
         fa.fa_sync_check()
         x = [host_f64(t) for t in (q, k, v, do)]
-        o_ref, lse_ref, ob, lb = scored_forward(*x[:3], d ** -0.5, causal, 10.0, slopes.cpu().numpy())
+        o_ref, lse_ref, ob, lb = scored_forward(*x[:3], d ** -0.5, causal, cap, slopes.cpu().numpy())
         _check(o, o_ref, ob, "O")
         _check(lse, lse_ref, lb, "LSE")
-        grads = fa.fa_bwd_scored(q, k, v, o, do, lse, causal=causal, softcap=10.0, slopes=slopes)
+        grads = fa.fa_bwd_scored(q, k, v, o, do, lse, causal=causal, softcap=cap, slopes=slopes)
         fa.fa_sync_check()
-        refs, bounds = scored_backward(*x, d ** -0.5, causal, 10.0, slopes.cpu().numpy())
+        refs, bounds = scored_backward(*x, d ** -0.5, causal, cap, slopes.cpu().numpy())
         for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
             _check(a, ref, bd, name)
 
