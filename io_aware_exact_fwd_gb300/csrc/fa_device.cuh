@@ -426,6 +426,33 @@ __device__ __forceinline__ void regs_decrease() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// --------------------------------------------------- cluster launch control --
+
+// Ask for a block of this grid that has not started: the 16-byte answer lands in `dst`
+// and completes 16 bytes on `bar`.  Not to be asked again after an answer that names no
+// block (launch_answer).
+__device__ __forceinline__ void try_cancel(void* dst, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(dst)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The x index of the block an answer names (this block runs it in its place), or -1.
+__device__ __forceinline__ int launch_answer(const void* src) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
+
 // ------------------------------------------------------------------- math --
 
 __device__ __forceinline__ float ex2_approx(float x) {

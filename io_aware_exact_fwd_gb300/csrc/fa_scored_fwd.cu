@@ -1,8 +1,8 @@
 // Scored attention forward for sm_103a: tanh cap, distance bias, interval masks
 // (documents, prefixes), shared key/value heads.  bf16 in and out, fp32 logsumexp.
 //
-// The pipeline is the plain forward's (fa_fwd.cu): persistent CTAs, each unit 256 query
-// rows of one head as two 128-row tiles; K_j, V_j stream through a TMA ring; one thread
+// The pipeline is the plain forward's (fa_fwd.cu): each unit 256 query rows of one head
+// as two 128-row tiles; K_j, V_j stream through a TMA ring; one thread
 // issues S_t = Q_t K_j^T and O_t += P_t V_j on tcgen05 with S, P and O in TMEM; two
 // softmax warpgroups hold one query row per thread.  What differs:
 //
@@ -14,7 +14,11 @@
 //    diagonal block first, where a distance bias is smallest, so the reference maximum
 //    of the first block holds for the rest (forward order would raise every row's
 //    maximum in every block) and no row of a document waits masked for its first key.
-//  * Scores are put in place in log2 units (cap, bias, mask) before the softmax.
+//  * A unit's work depends on the mask, which only the device knows, so units are not
+//    dealt out beforehand: the grid has one block per unit, heaviest rows first, and a
+//    running block takes over blocks that have not started (cluster launch control), its
+//    pipeline running on from unit to unit.  A scheduler warp asks for the next unit
+//    while the current one runs and publishes its key blocks in shared memory.
 #include <math.h>
 
 #include "fa_device.cuh"
@@ -26,10 +30,11 @@ namespace {
 
 constexpr int kTiles = 2;                       // query tiles per unit
 constexpr int kUnitRows = kTiles * kBlockQ;
-constexpr int kThreads = 384;                   // warps 0-7 softmax (2 groups), 8 K/V TMA, 9 MMA, 10 Q TMA, 11 spare
+constexpr int kThreads = 384;                   // warps 0-7 softmax (2 groups), 8 K/V TMA, 9 MMA, 10 Q TMA, 11 scheduler
 constexpr int kWarpLoad = 8;
 constexpr int kWarpMma = 9;
 constexpr int kWarpLoadQ = 10;
+constexpr int kWarpSched = 11;
 // 168 registers x 384 threads at launch = 2 x 128 x 216 + 128 x 72.
 constexpr uint32_t kRegsSoftmax = 216;
 constexpr uint32_t kRegsControl = 72;
@@ -58,6 +63,8 @@ enum : uint32_t {
   kSiteSoftS = 0x321,
   kSiteSoftO = 0x322,
   kSiteEpi = 0x323,
+  kSiteUnit = 0x324,
+  kSiteSched = 0x325,
 };
 
 template <int D>
@@ -72,10 +79,13 @@ struct Cfg {
   static constexpr int kOOff = kTiles * kTileBytes;     // O staging, shared by both tiles in turn
   static constexpr int kRingOff = kOOff + kTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
-  // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], epi[2], stg, drain
-  static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+  // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], epi[2], stg, drain,
+  // unit_full, unit_empty, answer
+  static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1 + 3;
+  static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kAnswerOff = kMiscOff + 16;                  // launch control's 16-byte answer
+  static constexpr int kUnitOff = kAnswerOff + 16;                  // the published unit
+  static constexpr int kSmemBytes = kUnitOff + 64 + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static __device__ __forceinline__ uint32_t col_s(int t) { return 128u * static_cast<uint32_t>(t); }
   static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + D * static_cast<uint32_t>(t); }
@@ -94,52 +104,44 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-// A unit's key blocks: tile t attends blocks [begin[t], end[t]) (empty: begin = end = 0),
-// the stream covers [first, last) from last - 1 down.
-struct Span {
-  int begin[kTiles], end[kTiles], first, last;
-  __device__ __forceinline__ int count() const { return last - first; }
-  // Tile t's run of the stream.
-  __device__ __forceinline__ int from(int t) const { return last - end[t]; }
-  __device__ __forceinline__ int to(int t) const { return last - begin[t]; }
-  __device__ __forceinline__ bool has(int t) const { return end[t] > begin[t]; }
-};
-// Blocks [x, y) of the tile whose first row is r0.
-__device__ __forceinline__ int2 tile_blocks(const Params& p, int r0, int b) {
-  if (r0 >= p.N) return make_int2(0, 0);
-  const int lo = keys_of(p.plan, p.causal, b, r0, p.N).x;
-  const int hi = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N).y;
-  return hi > lo ? make_int2(lo / kBlockK, (hi + kBlockK - 1) / kBlockK) : make_int2(0, 0);
-}
-__device__ __forceinline__ Span span_of(const Params& p, int u, int b) {
-  Span s;
-  s.first = 0x7fffffff;
-  s.last = 0;
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int2 x = tile_blocks(p, u * kUnitRows + t * kBlockQ, b);
-    s.begin[t] = x.x;
-    s.end[t] = x.y;
-    if (x.y > x.x) {
-      s.first = min(s.first, x.x);
-      s.last = max(s.last, x.y);
-    }
-  }
-  s.first = min(s.first, s.last);
-  return s;
-}
-
-// k-th unit of CTA c out of G: zigzag passes over units numbered last rows first (the
-// heaviest, when causal), heads next to one another.
+// A unit as the scheduler publishes it: query rows u * 256 .. of head bh (u < 0: no more
+// units).  Tile t attends key blocks [begin[t], end[t]) (empty: both 0), and every row of
+// it sees the keys [all_lo[t], all_hi[t]).  The stream covers blocks [first, last) from
+// last - 1 down.
 struct Unit {
   int u, bh;
+  int begin[kTiles], end[kTiles], all_lo[kTiles], all_hi[kTiles];
+  __device__ __forceinline__ bool has(int t) const { return end[t] > begin[t]; }
+  __device__ __forceinline__ int first() const {
+    return min(has(0) ? begin[0] : last(), has(1) ? begin[1] : last());
+  }
+  __device__ __forceinline__ int last() const { return max(end[0], end[1]); }
+  // Tile t's run of the stream.
+  __device__ __forceinline__ int from(int t) const { return last() - end[t]; }
+  __device__ __forceinline__ int to(int t) const { return last() - begin[t]; }
 };
-__device__ __forceinline__ bool unit_at(int k, int c, int G, const Params& p, Unit& x) {
-  const int w = k * G + ((k & 1) ? (G - 1 - c) : c);
-  if (w >= p.nunits * p.BH) return false;
+// Block w of the grid: the last rows (the heaviest, when causal) first, heads next to one another.
+__device__ __forceinline__ Unit unit_of(const Params& p, int w) {
+  Unit x;
   x.u = p.nunits - 1 - w / p.BH;
   x.bh = w % p.BH;
-  return true;
+  const int b = x.bh / p.H;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int r0 = x.u * kUnitRows + t * kBlockQ;
+    x.begin[t] = x.end[t] = x.all_lo[t] = x.all_hi[t] = 0;
+    if (r0 < p.N) {
+      const int2 head = keys_of(p.plan, p.causal, b, r0, p.N);
+      const int2 tail = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N);
+      if (tail.y > head.x) {
+        x.begin[t] = head.x / kBlockK;
+        x.end[t] = (tail.y + kBlockK - 1) / kBlockK;
+      }
+      x.all_lo[t] = tail.x;
+      x.all_hi[t] = head.y;
+    }
+  }
+  return x;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc, uint32_t site) {
@@ -180,12 +182,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_epi = bar_o + 2;             // [2] per tile: O staged in shared memory
   uint64_t* bar_stg = bar_epi + 2;           // O staging buffer read out by the previous store
   uint64_t* bar_drain = bar_stg + 1;
+  uint64_t* bar_unit = bar_drain + 1;        // a unit is published
+  uint64_t* bar_unit_read = bar_unit + 1;    // every role has read it
+  uint64_t* bar_answer = bar_unit_read + 1;  // launch control answered
+  Unit* s_unit = reinterpret_cast<Unit*>(smem + C::kUnitOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < kTiles; ++t) {
@@ -202,6 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar_stg, 1);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_unit, 1);
+    mbar_init(bar_unit_read, 3 + 8);  // the K/V, Q and MMA threads, eight softmax warps
+    mbar_init(bar_answer, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -217,20 +225,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
+  // The k-th unit of this block, for a role that is one thread.  False: no more (or aborting).
+  auto next_unit = [&](int k, Unit& x, bool& ok) -> bool {
+    if (!(ok = mbar_wait(bar_unit, k & 1, wc, kSiteUnit))) return false;
+    x = *s_unit;
+    mbar_arrive(bar_unit_read);
+    return x.u >= 0;
+  };
 
   if (warp >= 8) {
     regs_decrease<kRegsControl>();
-    if (warp == kWarpLoad) {
+    if (warp == kWarpSched) {
+      // --------------------------------------------------------------- scheduler
+      // Unit 0 is the block's own.  The next is asked for once every role has started on the
+      // current one: early enough to hide the answer, late enough to keep units for others.
+      if (lane == 0) {
+        int w = static_cast<int>(blockIdx.x);
+        for (int k = 0;; ++k) {
+          Unit x{};
+          x.u = -1;
+          if (w >= 0) x = unit_of(p, w);
+          if (k > 0 && !mbar_wait(bar_unit_read, (k - 1) & 1, wc, kSiteSched)) break;
+          *s_unit = x;
+          mbar_arrive(bar_unit);
+          if (w < 0) break;
+          if (k > 0 && !mbar_wait(bar_unit_read, k & 1, wc, kSiteSched)) break;
+          mbar_arrive_expect_tx(bar_answer, 16);
+          try_cancel(smem + C::kAnswerOff, bar_answer);
+          if (!mbar_wait_drain(bar_answer, k & 1, p.wait_ns)) {
+            record_timeout(wc, kSiteSched);
+            break;
+          }
+          w = launch_answer(smem + C::kAnswerOff);
+          fence_proxy_async_smem();  // the answer is read before the next one lands
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWarpLoad) {
       // ------------------------------------------------------- K/V TMA producer
       if (lane == 0) {
         int issued = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-          Unit x;
-          if (!unit_at(k, cta, G, p, x)) break;
+        Unit x;
+        for (int k = 0; ok && next_unit(k, x, ok); ++k) {
           const int b = x.bh / p.H, hk = (x.bh % p.H) / p.group;
-          const Span sp = span_of(p, x.u, b);
-          for (int j = sp.last - 1; ok && j >= sp.first; --j) {
+          const int first = x.first();
+          for (int j = x.last() - 1; ok && j >= first; --j) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {  // K_j, then V_j
               const int slot = issued % C::kSlots;
@@ -255,15 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         int nload[kTiles] = {0, 0};
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-          Unit x;
-          if (!unit_at(k, cta, G, p, x)) break;
+        Unit x;
+        for (int k = 0; ok && next_unit(k, x, ok); ++k) {
           const int b = x.bh / p.H, h = x.bh % p.H;
-          const Span sp = span_of(p, x.u, b);
 #pragma unroll
           for (int tt = 0; tt < kTiles; ++tt) {
             const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
-            if (!ok || !sp.has(t)) continue;
+            if (!ok || !x.has(t)) continue;
             if (nload[t] > 0 && !(ok = mbar_wait(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ))) continue;
             mbar_arrive_expect_tx(&bar_q[t], C::kTileBytes);
 #pragma unroll
@@ -306,15 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int item = 0;  // ring index of the next K or V block to consume
         uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q tiles and P blocks consumed so far
         bool ok = true;
-        Unit x{0, 0}, nx{0, 0};
-        bool more = unit_at(0, cta, G, p, x);
-        Span sp{}, nsp{};
-        if (more) sp = span_of(p, x.u, x.bh / p.H);
-        for (int k = 0; ok && more; ++k, x = nx, sp = nsp) {
-          // The next unit's intervals are fetched while this unit runs.
-          more = unit_at(k + 1, cta, G, p, nx);
-          if (more) nsp = span_of(p, nx.u, nx.bh / p.H);
-          const int n = sp.count();
+        Unit x;
+        for (int k = 0; ok && next_unit(k, x, ok); ++k) {
+          const int n = x.last() - x.first();
           // Stream position s: K_s is ring item 2 s, V_s item 2 s + 1 of the unit.  S_t of position
           // s is issued right after the P_t V of position s - 1 (position 0: before the loop).
           for (int s = -1; ok && s < n; ++s) {
@@ -331,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int tt = 0; tt < kTiles; ++tt) {
               const int t = kTiles - 1 - tt;
-              const int f = sp.from(t), l = sp.has(t) ? sp.to(t) : f;
+              const int f = x.from(t), l = x.has(t) ? x.to(t) : f;
               if (ok && s >= f && s < l) {
                 if (!(ok = mbar_wait(&bar_p[t], (t ? np1 : np0) & 1, wc, kSiteMmaP))) continue;
                 if (t) ++np1; else ++np0;
@@ -379,21 +411,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t nstg = 0;   // epilogues of both tiles before this unit's (bar_stg phase)
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      Unit x;
-      if (!unit_at(k, cta, G, p, x)) break;
-      const int b = x.bh / p.H, h = x.bh % p.H;
-      const int row0 = x.u * kUnitRows + t * kBlockQ;
+      if (!(ok = warp_wait(bar_unit, k & 1, wc, kSiteUnit))) break;
+      const int u = s_unit->u, bh = s_unit->bh;
+      const int blk0 = s_unit->begin[t], blk1 = s_unit->end[t];
+      // Keys that every row of the tile sees: [all_lo, all_hi).
+      const int all_lo = s_unit->all_lo[t], all_hi = s_unit->all_hi[t];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_unit_read);
+      if (u < 0) break;
+      const int b = bh / p.H, h = bh % p.H;
+      const int row0 = u * kUnitRows + t * kBlockQ;
       const uint32_t my_stg = nstg + static_cast<uint32_t>(t);
-      nstg += x.u * kUnitRows + kBlockQ < p.N ? 2u : 1u;
+      nstg += u * kUnitRows + kBlockQ < p.N ? 2u : 1u;
       if (row0 >= p.N) continue;
       const int qrow = row0 + row;
-      const int2 blocks = tile_blocks(p, row0, b);
       const int2 see = qrow < p.N ? keys_of(p.plan, p.causal, b, qrow, p.N) : make_int2(0, 0);
-      // Keys that every row of the tile sees: [all_lo, all_hi).
-      const int all_lo = keys_of(p.plan, p.causal, b, min(row0 + kBlockQ, p.N) - 1, p.N).x;
-      const int all_hi = keys_of(p.plan, p.causal, b, row0, p.N).y;
       const float slope2 = MODE != 0 && p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
-      const int nkt = blocks.y - blocks.x;
+      const int nkt = blk1 - blk0;
       // Reference maximum, log2 units (0 until the row has seen a key).  MODE 2: the largest bias
       // among the row's keys: 0, at the row's own position, or for a negative slope at its farthest.
       float m_used = 0.f;
@@ -410,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const int kbase = (blocks.y - 1 - j) * kBlockK;
+        const int kbase = (blk1 - 1 - j) * kBlockK;
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
         const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
         float2 part = make_float2(0.f, 0.f);
@@ -672,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_epi[t]);
       if (qrow < p.N)
-        p.lse[static_cast<size_t>(x.bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[static_cast<size_t>(bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
       if (row == 0) {
         if ((ok = mbar_wait(&bar_epi[t], nepi & 1, wc, kSiteEpi))) {
 #pragma unroll
@@ -730,11 +764,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   cudaFuncAttributes fattr;
   if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
   if (static_cast<uint32_t>(fattr.numRegs) * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev))) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return e;
-  const long long units = static_cast<long long>(p.nunits) * p.BH;
-  kern<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  kern<<<static_cast<unsigned>(p.nunits) * static_cast<unsigned>(p.BH), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
