@@ -30,16 +30,23 @@ namespace {
 
 constexpr int kTiles = 2;                       // query tiles per unit
 constexpr int kUnitRows = kTiles * kBlockQ;
-constexpr int kThreads = 384;                   // warps 0-7 softmax (2 groups), 8 K/V TMA, 9 MMA, 10 Q TMA, 11 scheduler
-constexpr int kWarpLoad = 8;
-constexpr int kWarpMma = 9;
-constexpr int kWarpLoadQ = 10;
-constexpr int kWarpSched = 11;
-// 168 registers x 384 threads at launch = 2 x 128 x 216 + 128 x 72.
-constexpr uint32_t kRegsSoftmax = 216;
-constexpr uint32_t kRegsControl = 72;
-constexpr uint32_t kRegsNeeded = 2 * 128 * kRegsSoftmax + 128 * kRegsControl;
-static_assert(kRegsNeeded <= 65536, "register split exceeds the SM register file");
+// Warp roles.  With one part, each of the 8 softmax warps holds 32 rows of a tile, 128
+// keys a thread; with two, each of 16 holds 64 keys of 32 rows, and two threads share a
+// row.  Then K/V TMA, MMA, Q TMA and the scheduler, one warp each.
+template <int PARTS>
+struct Roles {
+  static constexpr int kSoftWarps = 8 * PARTS;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr int kWarpLoad = kSoftWarps, kWarpMma = kSoftWarps + 1, kWarpLoadQ = kSoftWarps + 2,
+                       kWarpSched = kSoftWarps + 3;
+  // Registers a thread: at launch (65536 / kThreads, down to a multiple of 8), then for the softmax
+  // and the control warpgroups.
+  static constexpr uint32_t kRegsLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr uint32_t kRegsSoftmax = PARTS == 1 ? 216 : 104;
+  static constexpr uint32_t kRegsControl = PARTS == 1 ? 72 : 64;
+  static constexpr uint32_t kRegsNeeded = 32 * kSoftWarps * kRegsSoftmax + 128 * kRegsControl;
+  static_assert(kRegsNeeded <= kRegsLaunch * kThreads, "register split exceeds the launch's registers");
+};
 constexpr uint32_t kTmemCols = 512;
 // A block is exponentiated against the running reference without its own maximum; its
 // row sum then proves that no P passed 2^60 (else the block is redone).  P is bf16 and
@@ -153,6 +160,20 @@ __device__ __forceinline__ bool warp_wait_suspend(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, ok);
 }
 
+// The barrier of two warps, and the same with an "any".
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_or(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
 // Bit i: key k0 + i lies in the row's interval.
 __device__ __forceinline__ uint32_t visible_bits(int2 see, int k0) {
   const int a = min(max(see.x - k0, 0), 32), e = min(max(see.y - k0, 0), 32);
@@ -161,12 +182,17 @@ __device__ __forceinline__ uint32_t visible_bits(int2 see, int k0) {
 
 // MODE 0: scores as they are; 1: with a distance bias; 2: capped within kBoundedCap, 3:
 // capped beyond it (both biased if slopes).
+template <int MODE>
+constexpr int kPartsOf = MODE == 2 ? 2 : 1;
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                       const __grid_constant__ Params p) {
   using C = Cfg<D>;
+  constexpr int kParts = kPartsOf<MODE>;
+  using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::kQOff;
@@ -197,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_q[t], 1);
       mbar_init(&bar_qe[t], 1);
       mbar_init(&bar_s[t], 1);
-      mbar_init(&bar_p[t], 4);
+      mbar_init(&bar_p[t], 4 * kParts);
       mbar_init(&bar_o[t], 1);
-      mbar_init(&bar_epi[t], 4);
+      mbar_init(&bar_epi[t], 4 * kParts);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&bar_full[s], 1);
@@ -208,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_stg, 1);
     mbar_init(bar_drain, 1);
     mbar_init(bar_unit, 1);
-    mbar_init(bar_unit_read, 3 + 8);  // the K/V, Q and MMA threads, eight softmax warps
+    mbar_init(bar_unit_read, 3 + R::kSoftWarps);  // the K/V, Q and MMA threads, the softmax warps
     mbar_init(bar_answer, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
-  if (warp == kWarpLoad && lane == 0) {
+  if (warp == R::kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == R::kWarpLoad && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
@@ -233,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return x.u >= 0;
   };
 
-  if (warp >= 8) {
-    regs_decrease<kRegsControl>();
-    if (warp == kWarpSched) {
+  if (warp >= R::kSoftWarps) {
+    regs_decrease<R::kRegsControl>();
+    if (warp == R::kWarpSched) {
       // --------------------------------------------------------------- scheduler
       // Unit 0 is the block's own.  The next is asked for once every role has started on the
       // current one: early enough to hide the answer, late enough to keep units for others.
@@ -261,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == kWarpLoad) {
+    } else if (warp == R::kWarpLoad) {
       // ------------------------------------------------------- K/V TMA producer
       if (lane == 0) {
         int issued = 0;
@@ -290,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_drain(&bar_full[t % C::kSlots], (t / C::kSlots) & 1, p.wait_ns);
       }
       __syncwarp();
-    } else if (warp == kWarpLoadQ) {
+    } else if (warp == R::kWarpLoadQ) {
       // --------------------------------------------------------- Q TMA producer
       if (lane == 0) {
         int nload[kTiles] = {0, 0};
@@ -316,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nload[t] > 0) mbar_wait_drain(&bar_q[t], (nload[t] - 1) & 1, p.wait_ns);
       }
       __syncwarp();
-    } else if (warp == kWarpMma) {
+    } else if (warp == R::kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
       if (lane == 0) {
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kBlockQ, kBlockK, 0, 0);
@@ -338,8 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t vd = sdesc_add(vdesc, slot * C::kTileBytes);
 #pragma unroll
           for (int kk = 0; kk < kBlockK / 16; ++kk)
-            mma_bf16_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, sdesc_add(vd, kk * 16 * 128), idesc_pv,
-                        (accumulate || kk > 0) ? 1u : 0u);
+            // With two parts, P of keys 64-127 lies over S columns 64-95, each part over its own S.
+            mma_bf16_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8 + (kParts == 2 ? (kk / 4) * 32 : 0),
+                        sdesc_add(vd, kk * 16 * 128), idesc_pv, (accumulate || kk > 0) ? 1u : 0u);
         };
         int item = 0;  // ring index of the next K or V block to consume
         uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q tiles and P blocks consumed so far
@@ -399,19 +426,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    regs_increase<kRegsSoftmax>();
-    // ------------------------------------------ softmax warpgroups (0-3, 4-7)
-    const int t = warp >> 2;
+    regs_increase<R::kRegsSoftmax>();
+    // ------------------------------------------------------ softmax warpgroups
+    const int t = warp / (4 * kParts), half = kParts == 2 ? (warp >> 2) & 1 : 0;
     const int row = threadIdx.x & 127;
+    const int pair_id = 1 + t * 4 + (warp & 3);  // named barrier of the two warps that share 32 rows
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t col_s = C::col_s(t), col_o = C::col_o(t);
+    const uint32_t col_s = C::col_s(t) + 64 * half, col_o = C::col_o(t);
     uint32_t scnt = 0;   // S blocks consumed so far (bar_s phase)
     uint32_t nout = 0;   // units of this tile with keys (bar_o phase)
     uint32_t nepi = 0;   // epilogues of this tile (bar_epi phase)
     uint32_t nstg = 0;   // epilogues of both tiles before this unit's (bar_stg phase)
+    // The warps of a pair meet at their barrier in every unit, so a warp whose wait gave up (the block
+    // is aborting) carries on with whatever TMEM holds, and both leave together at the next unit.
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!(ok = warp_wait(bar_unit, k & 1, wc, kSiteUnit))) break;
+    for (int k = 0;; ++k) {
+      ok = ok && warp_wait(bar_unit, k & 1, wc, kSiteUnit);
+      if (kParts == 2 ? pair_or(pair_id, !ok) : !ok) break;
       const int u = s_unit->u, bh = s_unit->bh;
       const int blk0 = s_unit->begin[t], blk1 = s_unit->end[t];
       // Keys that every row of the tile sees: [all_lo, all_hi).
@@ -439,81 +470,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool one_sided = MODE == 0 || __all_sync(0xffffffffu, see.y <= qrow + 1);
 
       for (int j = 0; j < nkt; ++j, ++scnt) {
-        if (!warp_wait_suspend(&bar_s[t], scnt & 1, wc, kSiteSoftS)) {
-          ok = false;
-          break;
-        }
+        ok = warp_wait_suspend(&bar_s[t], scnt & 1, wc, kSiteSoftS) && ok;
         tc_fence_after();
         const int kbase = (blk1 - 1 - j) * kBlockK;
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
         const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
         float2 part = make_float2(0.f, 0.f);
         if constexpr (MODE == 2) {
-          // The fixed reference: P = exp2(cap + bias - m_used), 32 columns at a time, the next 32
-          // loading meanwhile.  P of columns 32c.. goes over S columns 16c.., which are consumed.
-          uint32_t x[2][32];
-          tmem_ld32(trow + col_s, x[0]);
-          tmem_ld_wait32(x[0]);
+          // The fixed reference: P = exp2(cap + bias - m_used), 32 columns at a time.  P of columns 32c..
+          // goes over columns 16c.. of the thread's S, which are consumed.
 #pragma unroll 1
-          for (int c0 = 0; c0 < 4; c0 += 2) {
+          for (int c = 0; c < 4 / kParts; ++c) {
+            uint32_t r[32];
+            tmem_ld32(trow + col_s + c * 32, r);
+            tmem_ld_wait32(r);
+            const int key0 = kbase + 64 * half + c * 32;
+            float mx = 0.f;
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const int c = c0 + cc;
-              uint32_t (&r)[32] = x[cc];
-              if (c < 3) tmem_ld32(trow + col_s + (c + 1) * 32, x[cc ^ 1]);
-              float mx = 0.f;
+            for (int i = 0; i < 32; i += 2)
+              mx = max3(mx, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+            if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                mx = max3(mx, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-              if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
+              for (int i = 0; i < 32; ++i)
+                r[i] = __float_as_uint(fmaf(p.cap_out, tanh_any(__uint_as_float(r[i]) * p.cap_in), -m_used));
+            } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  r[i] = __float_as_uint(fmaf(p.cap_out, tanh_any(__uint_as_float(r[i]) * p.cap_in), -m_used));
-              } else {
+              for (int i = 0; i < 32; i += 2) {
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(p.cap_in));
+                const float2 y = __ffma2_rn(x, tanh_over_u(x, p.poly), pair(-m_used));
+                r[i] = __float_as_uint(y.x);
+                r[i + 1] = __float_as_uint(y.y);
+              }
+            }
+            if (p.slopes) {
+              const float off0 = static_cast<float>(key0 - qrow);
+              if (left || right) {
+                // sg more for every key: four steps are added up, then the sum starts afresh.
+                const float sg = left ? slope2 : -slope2, base = sg * off0;
+                float2 off = make_float2(base, base + sg);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                  const float2 u = __fmul2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(p.cap_in));
-                  const float2 y = __ffma2_rn(u, tanh_over_u(u, p.poly), pair(-m_used));
+                  if (i > 0)
+                    off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
+                                     : __fadd2_rn(off, pair(2.f * sg));
+                  const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), off);
                   r[i] = __float_as_uint(y.x);
                   r[i + 1] = __float_as_uint(y.y);
                 }
-              }
-              if (p.slopes) {
-                const float off0 = static_cast<float>(kbase + c * 32 - qrow);
-                if (left || right) {
-                  const float sg = left ? slope2 : -slope2, base = sg * off0;
-                  float2 off = make_float2(base, base + sg);
-#pragma unroll
-                  for (int i = 0; i < 32; i += 2) {
-                    if (i > 0)
-                      off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
-                                       : __fadd2_rn(off, pair(2.f * sg));
-                    const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), off);
-                    r[i] = __float_as_uint(y.x);
-                    r[i + 1] = __float_as_uint(y.y);
-                  }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    r[i] = __float_as_uint(fmaf(-slope2, fabsf(off0 + static_cast<float>(i)), __uint_as_float(r[i])));
-                }
-              }
-              if (need_mask) {
-                const uint32_t vis = visible_bits(see, kbase + c * 32);
+              } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
+                  r[i] = __float_as_uint(fmaf(-slope2, fabsf(off0 + static_cast<float>(i)), __uint_as_float(r[i])));
               }
-              uint32_t pk[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 e = make_float2(ex2_approx(__uint_as_float(r[2 * i])), ex2_approx(__uint_as_float(r[2 * i + 1])));
-                part = __fadd2_rn(part, e);
-                pk[i] = pack_bf16x2(e.x, e.y);
-              }
-              tmem_st16(trow + col_s + c * 16, pk);
-              if (c < 3) tmem_ld_wait32(x[cc ^ 1]);
             }
+            if (need_mask) {
+              const uint32_t vis = visible_bits(see, key0);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = make_float2(ex2_approx(__uint_as_float(r[2 * i])), ex2_approx(__uint_as_float(r[2 * i + 1])));
+              part = __fadd2_rn(part, e);
+              pk[i] = pack_bf16x2(e.x, e.y);
+            }
+            tmem_st16(trow + col_s + c * 16, pk);
           }
         }
         if constexpr (MODE != 2) {
@@ -663,25 +686,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         }
         l += part.x + part.y;
+        if (kParts == 2 && j == nkt - 1) {
+          // The two halves of the row sum, swapped through S column 56 of each half (consumed, and not
+          // P's), before the last P lets the next unit's S overwrite it.
+          tmem_st1(trow + col_s + 56, l);
+          tmem_st_wait();
+          tc_fence_before();
+          pair_sync(pair_id);
+          tc_fence_after();
+          l += tmem_ld1_wait(trow + (col_s ^ 64) + 56);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_p[t]);
       }
-      if (!ok) break;
 
       // ------------------------------------------------------------ epilogue
       if (nkt > 0) {
-        if (!(ok = warp_wait(&bar_o[t], nout & 1, wc, kSiteSoftO))) break;
+        ok = warp_wait(&bar_o[t], nout & 1, wc, kSiteSoftO) && ok;
         ++nout;
         tc_fence_after();
       }
       // The staging buffer is free once the previous epilogue's store has read it.
-      if (my_stg > 0 && !(ok = warp_wait(bar_stg, (my_stg - 1) & 1, wc, kSiteEpi))) break;
+      if (my_stg > 0) ok = warp_wait(bar_stg, (my_stg - 1) & 1, wc, kSiteEpi) && ok;
+      if (!ok) continue;
       const bool any_key = l > 0.f;
       const float inv_l = any_key ? 1.f / l : 0.f;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = half * (D / 64); c < (kParts == 2 ? (half + 1) * (D / 64) : D / 32); ++c) {
         uint32_t o[32];
         if (nkt > 0) {
           tmem_ld32(trow + col_o + c * 32, o);
@@ -705,9 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_epi[t]);
-      if (qrow < p.N)
+      if (half == 0 && qrow < p.N)
         p.lse[static_cast<size_t>(bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
-      if (row == 0) {
+      if (half == 0 && row == 0) {
         if ((ok = mbar_wait(&bar_epi[t], nepi & 1, wc, kSiteEpi))) {
 #pragma unroll
           for (int c = 0; c < C::kBoxes; ++c)
@@ -724,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == R::kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -733,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int MODE>
 cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   using C = Cfg<D>;
+  using R = Roles<kPartsOf<MODE>>;
   CUtensorMap tq, tk, tv, to;
   cudaError_t e;
   constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -763,8 +797,8 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   // setmaxnreg.inc can only draw on the registers the block was launched with.
   cudaFuncAttributes fattr;
   if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
-  if (static_cast<uint32_t>(fattr.numRegs) * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
-  kern<<<static_cast<unsigned>(p.nunits) * static_cast<unsigned>(p.BH), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  if (static_cast<uint32_t>(fattr.numRegs) * R::kThreads < R::kRegsNeeded) return cudaErrorInvalidConfiguration;
+  kern<<<static_cast<unsigned>(p.nunits) * static_cast<unsigned>(p.BH), R::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
