@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + 8 * nt + gc + (e & 1);
               float x = s[mt][nt][e];
-              x = p.cap_out > 0.f ? p.cap_out * tanh_any(x * p.cap_in) : x * p.scale_log2;
+              x = p.cap_out > 0.f ? tanh_any(pair(x * p.cap_in), p.cap_out, pair(0.f)).x : x * p.scale_log2;
               x = fmaf(-slope2[mt][e >> 1], static_cast<float>(at.n - 1 - key), x);
               x = key < at.n ? x : -INFINITY;
               s[mt][nt][e] = x;
@@ -620,7 +620,7 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   p.piece = std::min(kTile, a.c.page_size & -a.c.page_size);
   p.scale_log2 = a.scale * kLog2e;
   if (a.softcap > 0.f) {
-    p.cap_in = a.scale / a.softcap;
+    p.cap_in = 4.f * a.scale / a.softcap;  // tanh_any takes four times the cap's argument
     p.cap_out = a.softcap * kLog2e;
   }
   p.slopes = a.slopes;

@@ -21,39 +21,46 @@ __device__ __forceinline__ int2 queries_of(const MaskPlan& p, int causal, int b,
 
 // tanh for the cap.  A capped score is softcap * tanh(u); tanh.approx, off by up to
 // 2^-11 relative, would move scores by up to hundredths and their weights by percents.
+// The kernels work with x = 4 u, whose bits say which of two forms applies: |x| < 2
+// exactly when bit 30 of the fp32 is clear (it is set in infinities and NaN too), so one
+// OR over a thread's values finds whether any |u| reaches 1/2.
 //
-// |u| <= 1: u p(u^2) with p of degree 5 of the smallest relative error on [0, 1] (5.6e-7,
-// found by linear programming on 4001 points; the score is a dot product of 64 or 128
-// terms, whose own fp32 error is larger).  On the FMA pipe in pairs, none of it on the
-// MUFU that the exponentials need.  The coefficients come with a factor (CapPoly), the
-// result is factor * tanh(u).
+// |u| < 1/2: u p(u^2) with p of degree 3 of the smallest relative error on [0, 1/4]
+// (5.4e-7, found by linear programming on 4001 points; the score is a dot product of 64 or
+// 128 terms, whose own fp32 error is larger).  On the FMA pipe in pairs, none of it on the
+// MUFU that the exponentials need.  The coefficients come with a factor and the powers
+// of two of x (CapPoly).
 __host__ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 struct CapPoly {
-  float2 c[6];
+  float2 c[4];
 };
 inline CapPoly cap_poly(float factor) {
-  const float c[6] = {0.999999463558197f,     -0.33328977227211f,    0.13280832767486572f,
-                      -0.05158914253115654f, 0.016724668443202972f, -0.0030597823206335306f};
+  const float c[4] = {0.999999463558197f, -0.33326318860054016f, 0.13190294802188873f, -0.04440207779407501f};
   CapPoly p;
-  for (int i = 0; i < 6; ++i) p.c[i] = pair(c[i] * factor);
+  float f = 0.25f * factor;
+  for (int i = 0; i < 4; ++i, f *= 0.0625f) p.c[i] = pair(c[i] * f);
   return p;
 }
-// tanh(u) * factor / u.
-__device__ __forceinline__ float2 tanh_over_u(float2 u, const CapPoly& k) {
-  const float2 w = __fmul2_rn(u, u);
-  float2 p = __ffma2_rn(k.c[5], w, k.c[4]);
-  p = __ffma2_rn(p, w, k.c[3]);
-  p = __ffma2_rn(p, w, k.c[2]);
+// factor * tanh(x / 4) / x, |x| < 2.
+__device__ __forceinline__ float2 tanh_over_x(float2 x, const CapPoly& k) {
+  const float2 w = __fmul2_rn(x, x);
+  float2 p = __ffma2_rn(k.c[3], w, k.c[2]);
   p = __ffma2_rn(p, w, k.c[1]);
   return __ffma2_rn(p, w, k.c[0]);
 }
-// Any u: 1 - 2 / (1 + e^2u), which keeps its absolute error at both ends (e^2u -> 0 or
-// infinity gives -1 or 1).
-__device__ __forceinline__ float tanh_any(float u) {
-  const float e = ex2_approx(u * 2.885390081777927f);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return fmaf(-2.f, r, 1.f);
+__device__ __forceinline__ uint32_t or_bits(uint32_t acc, float2 x) {
+  return acc | __float_as_uint(x.x) | __float_as_uint(x.y);
+}
+constexpr uint32_t kReachesTwo = 0x40000000u;
+// factor * tanh(x / 4) + add, any x: 1 - 2 / (1 + e^2u), which keeps its absolute error
+// (about 2^-22 factor) at both ends (e^2u -> 0 or infinity gives -1 or 1).
+__device__ __forceinline__ float2 tanh_any(float2 x, float factor, float2 add) {
+  const float2 a = __fmul2_rn(x, pair(0.7213475204444817f));
+  const float2 e = __fadd2_rn(make_float2(ex2_approx(a.x), ex2_approx(a.y)), pair(1.f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return __ffma2_rn(r, pair(-2.f * factor), __fadd2_rn(add, pair(factor)));
 }
 
 }  // namespace fa

@@ -31,7 +31,7 @@ struct Params {
   MaskPlan plan;
   int causal, N, Npad, H, Hkv, group, nkb;
   float scale, scale_log2;
-  float cap_in, cap_out;  // scale / softcap, softcap log2(e)
+  float cap_in, cap_out;  // 4 scale / softcap (products to x = 4 u), softcap log2(e)
   CapPoly poly;           // factor 1
   const float* slopes;
   const uint8_t* aug;
@@ -303,10 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool need_mask = qb < all_lo || qb + kBqB > all_hi;
       // s becomes the exponent of P in log2 units, dp becomes dS / P.
       if constexpr (MODE == 2) {
-        float mx = 0.f;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) mx = max3(mx, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-        const bool large = __any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f));
+        for (int c = 0; c < 32; c += 2) {
+          const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(p.cap_in));
+          bits = or_bits(bits, x);
+          s[c] = __float_as_uint(x.x);
+          s[c + 1] = __float_as_uint(x.y);
+        }
+        const bool large = __any_sync(0xffffffffu, bits & kReachesTwo);
         // LSE2 of the step's queries: the slot landed before S^T was made of it (the wait makes its
         // bytes visible here), and is refilled only after this step's dV and dK.
         if (!(ok = warp_wait_b(&bar_full[slot], ring_ph, wc, kSiteBComp))) break;
@@ -318,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int c = 4 * c4 + 2 * e;
-            const float2 u = __fmul2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(p.cap_in));
-            const float2 t = large ? make_float2(tanh_any(u.x), tanh_any(u.y)) : __fmul2_rn(u, tanh_over_u(u, p.poly));
+            const float2 u4 = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            const float2 t = large ? tanh_any(u4, 1.f, pair(0.f)) : __fmul2_rn(u4, tanh_over_x(u4, p.poly));
             const float2 x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
             const float2 bend = __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f));
             const float2 y = __fmul2_rn(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), bend);
@@ -494,7 +499,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE == 2) {
-    p.cap_in = a.scale / sc.softcap;
+    p.cap_in = 4.f * a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
     p.poly = cap_poly(1.f);
   }

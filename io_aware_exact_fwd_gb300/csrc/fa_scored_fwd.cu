@@ -102,7 +102,7 @@ struct Params {
   MaskPlan plan;
   int causal, N, H, group, BH, nunits;
   float scale_log2;   // scale log2(e)
-  float cap_in;       // scale / softcap
+  float cap_in;       // 4 scale / softcap: products to x = 4 u
   float cap_out;      // softcap log2(e)
   CapPoly poly;       // factor cap_out
   const float* slopes;
@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           Unit x{};
           x.u = -1;
           if (w >= 0) x = unit_of(p, w);
-          if (k > 0 && !mbar_wait(bar_unit_read, (k - 1) & 1, wc, kSiteSched)) break;
+          if (k > 0 && !mbar_wait_suspend(bar_unit_read, (k - 1) & 1, wc, kSiteSched, 20000u)) break;
           *s_unit = x;
           mbar_arrive(bar_unit);
           if (w < 0) break;
-          if (k > 0 && !mbar_wait(bar_unit_read, k & 1, wc, kSiteSched)) break;
+          if (k > 0 && !mbar_wait_suspend(bar_unit_read, k & 1, wc, kSiteSched, 20000u)) break;
           mbar_arrive_expect_tx(bar_answer, 16);
           try_cancel(smem + C::kAnswerOff, bar_answer);
           if (!mbar_wait_drain(bar_answer, k & 1, p.wait_ns)) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {  // K_j, then V_j
               const int slot = issued % C::kSlots;
-              if (!(ok = mbar_wait(&bar_empty[slot], ((issued / C::kSlots) & 1) ^ 1, wc, kSiteLoadEmpty))) break;
+              if (!(ok = mbar_wait_suspend(&bar_empty[slot], ((issued / C::kSlots) & 1) ^ 1, wc, kSiteLoadEmpty, 20000u))) break;
               mbar_arrive_expect_tx(&bar_full[slot], C::kTileBytes);
               uint8_t* dst = sRing + slot * C::kTileBytes;
 #pragma unroll
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           for (int tt = 0; tt < kTiles; ++tt) {
             const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
             if (!ok || !x.has(t)) continue;
-            if (nload[t] > 0 && !(ok = mbar_wait(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ))) continue;
+            if (nload[t] > 0 && !(ok = mbar_wait_suspend(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ, 20000u))) continue;
             mbar_arrive_expect_tx(&bar_q[t], C::kTileBytes);
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
@@ -485,19 +485,26 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             tmem_ld32(trow + col_s + c * 32, r);
             tmem_ld_wait32(r);
             const int key0 = kbase + 64 * half + c * 32;
-            float mx = 0.f;
+            uint32_t bits = 0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx = max3(mx, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-            if (__any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f))) {
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = __fmul2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(p.cap_in));
+              bits = or_bits(bits, x);
+              r[i] = __float_as_uint(x.x);
+              r[i + 1] = __float_as_uint(x.y);
+            }
+            if (__any_sync(0xffffffffu, bits & kReachesTwo)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(fmaf(p.cap_out, tanh_any(__uint_as_float(r[i]) * p.cap_in), -m_used));
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = tanh_any(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), p.cap_out, pair(-m_used));
+                r[i] = __float_as_uint(y.x);
+                r[i + 1] = __float_as_uint(y.y);
+              }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
-                const float2 x = __fmul2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), pair(p.cap_in));
-                const float2 y = __ffma2_rn(x, tanh_over_u(x, p.poly), pair(-m_used));
+                const float2 x = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                const float2 y = __ffma2_rn(x, tanh_over_x(x, p.poly), pair(-m_used));
                 r[i] = __float_as_uint(y.x);
                 r[i + 1] = __float_as_uint(y.y);
               }
@@ -553,13 +560,13 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         // kernel's speed depends on its code fitting the instruction caches.
         bool pre = MODE != 0 && !left && !right && (MODE == 1 || p.slopes != nullptr);
         if constexpr (MODE == 3) {
-          float mx = 0.f;
+          uint32_t bits = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
-              mx = max3(mx, fabsf(__uint_as_float(r[c][i])), fabsf(__uint_as_float(r[c][i + 1])));
-          pre = pre || __any_sync(0xffffffffu, !(mx * p.cap_in <= 1.f));
+              bits = or_bits(bits, __fmul2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), pair(p.cap_in)));
+          pre = pre || __any_sync(0xffffffffu, bits & kReachesTwo);
         }
         if (MODE != 0 && pre) {
 #pragma unroll 1
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float s = __uint_as_float(x[i]);
-              const float a = MODE == 3 ? p.cap_out * tanh_any(s * p.cap_in) : s * p.scale_log2;
+              const float a = MODE == 3 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x : s * p.scale_log2;
               x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
             }
             tmem_st8(trow + col_s + c, x);
@@ -596,8 +603,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
                                  : __fadd2_rn(off, pair(2.f * sg));
               float2 y;
               if constexpr (MODE == 3) {
-                const float2 u = __fmul2_rn(s, pair(p.cap_in));
-                y = __ffma2_rn(u, tanh_over_u(u, p.poly), off);
+                const float2 x = __fmul2_rn(s, pair(p.cap_in));
+                y = __ffma2_rn(x, tanh_over_x(x, p.poly), off);
               } else {
                 y = __ffma2_rn(s, pair(p.scale_log2), off);
               }
@@ -784,7 +791,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.nunits = (a.N + kUnitRows - 1) / kUnitRows;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE >= 2) {
-    p.cap_in = a.scale / sc.softcap;
+    p.cap_in = 4.f * a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
     p.poly = cap_poly(p.cap_out);
   }
