@@ -19,6 +19,13 @@ __device__ __forceinline__ int2 queries_of(const MaskPlan& p, int causal, int b,
   return make_int2(causal ? j : 0, N);
 }
 
+// Bits a .. e - 1 of 32 (a and e clamped to [0, 32]).
+__device__ __forceinline__ uint32_t bits_between(int a, int e) {
+  a = min(max(a, 0), 32);
+  e = min(max(e, 0), 32);
+  return static_cast<uint32_t>((1ull << e) - 1ull) & ~static_cast<uint32_t>((1ull << a) - 1ull);
+}
+
 // tanh for the cap.  A capped score is softcap * tanh(u); tanh.approx, off by up to
 // 2^-11 relative, would move scores by up to hundredths and their weights by percents.
 // The kernels work with x = 4 u, whose bits say which of two forms applies: |x| < 2

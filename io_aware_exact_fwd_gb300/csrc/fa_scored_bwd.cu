@@ -312,6 +312,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[c + 1] = __float_as_uint(x.y);
         }
         const bool large = __any_sync(0xffffffffu, bits & kReachesTwo);
+        // s becomes tanh; as two loops under one branch, or both forms would be computed for every pair.
+        if (large) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 t = tanh_any(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), 1.f, pair(0.f));
+            s[c] = __float_as_uint(t.x);
+            s[c + 1] = __float_as_uint(t.y);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            const float2 t = __fmul2_rn(x, tanh_over_x(x, p.poly));
+            s[c] = __float_as_uint(t.x);
+            s[c + 1] = __float_as_uint(t.y);
+          }
+        }
         // LSE2 of the step's queries: the slot landed before S^T was made of it (the wait makes its
         // bytes visible here), and is refilled only after this step's dV and dK.
         if (!(ok = warp_wait_b(&bar_full[slot], ring_ph, wc, kSiteBComp))) break;
@@ -323,8 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int c = 4 * c4 + 2 * e;
-            const float2 u4 = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            const float2 t = large ? tanh_any(u4, 1.f, pair(0.f)) : __fmul2_rn(u4, tanh_over_x(u4, p.poly));
+            const float2 t = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             const float2 x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
             const float2 bend = __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f));
             const float2 y = __fmul2_rn(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), bend);
@@ -335,27 +351,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // The bias, as loops of their own under branches (see the cap); without a cap s is still the
+      // product, whose scale goes with it.
+      if (biased) {
+        const float mul = MODE == 2 ? 1.f : p.scale_log2;
+        const float off0 = static_cast<float>(q0 - key);  // i - j of the first query
+        const bool below = qb >= kb * kBkB + kBkB - 1, above = qb + kBqB - 1 <= kb * kBkB;
+        if (below || above) {
+          // sg more for every query: four steps are added up, then the sum starts afresh.
+          const float sg = below ? -slope2 : slope2, base = sg * off0;
+          float2 off = make_float2(base, base + sg);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            if (c > 0)
+              off = c % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(c), base), fmaf(sg, static_cast<float>(c + 1), base))
+                               : __fadd2_rn(off, pair(2.f * sg));
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(mul), off);
+            s[c] = __float_as_uint(x.x);
+            s[c + 1] = __float_as_uint(x.y);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            s[c] = __float_as_uint(
+                fmaf(__uint_as_float(s[c]), mul, -slope2 * fabsf(off0 + static_cast<float>(c))));
+        }
+      }
+      if (need_mask) {
+        const uint32_t vis = bits_between(by.x - q0, by.y - q0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!(vis & (1u << c))) s[c] = __float_as_uint(-INFINITY);
+      }
       uint32_t ppk[16], dpk[16];
-      const float mul = MODE == 2 ? 1.f : p.scale_log2;
-      const float off = static_cast<float>(q0 - key);  // i - j of the first query
-      const bool below = qb >= kb * kBkB + kBkB - 1, above = qb + kBqB - 1 <= kb * kBkB;
-      const float sg = below ? -slope2 : slope2;
 #pragma unroll
       for (int c2 = 0; c2 < 16; ++c2) {
         const int c = 2 * c2;
         float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        if (MODE == 1 || (MODE == 2 && biased)) {
-          float2 dist = __fadd2_rn(make_float2(static_cast<float>(c), static_cast<float>(c + 1)), pair(off));
-          if (!below && !above) dist = make_float2(-fabsf(dist.x), -fabsf(dist.y));
-          x = __ffma2_rn(x, pair(mul), __fmul2_rn(dist, pair(sg)));
-        } else if (MODE == 0) {
-          x = __fmul2_rn(x, pair(mul));
-        }
-        float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        if (need_mask) {
-          if (q0 + c < by.x || q0 + c >= by.y) pp.x = 0.f;
-          if (q0 + c + 1 < by.x || q0 + c + 1 >= by.y) pp.y = 0.f;
-        }
+        if (MODE == 0) x = __fmul2_rn(x, pair(p.scale_log2));
+        const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         const float2 ds = __fmul2_rn(pp, make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])));
         ppk[c2] = pack_bf16x2(pp.x, pp.y);
         dpk[c2] = pack_bf16x2(ds.x, ds.y);

@@ -174,12 +174,6 @@ __device__ __forceinline__ bool pair_or(int id, bool x) {
   return r != 0;
 }
 
-// Bit i: key k0 + i lies in the row's interval.
-__device__ __forceinline__ uint32_t visible_bits(int2 see, int k0) {
-  const int a = min(max(see.x - k0, 0), 32), e = min(max(see.y - k0, 0), 32);
-  return static_cast<uint32_t>((1ull << e) - 1ull) & ~static_cast<uint32_t>((1ull << a) - 1ull);
-}
-
 // MODE 0: scores as they are; 1: with a distance bias; 2: capped within kBoundedCap, 3:
 // capped beyond it (both biased if slopes).
 template <int MODE>
@@ -531,7 +525,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
               }
             }
             if (need_mask) {
-              const uint32_t vis = visible_bits(see, key0);
+              const uint32_t vis = bits_between(see.x - (key0), see.y - (key0));
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
@@ -613,7 +607,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             }
           }
           if (need_mask) {
-            const uint32_t vis = visible_bits(see, kbase + c * 32);
+            const uint32_t vis = bits_between(see.x - (kbase + c * 32), see.y - (kbase + c * 32));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
