@@ -69,7 +69,6 @@ enum : uint32_t {
   kSiteMmaV = 0x224,
   kSiteSoftS = 0x321,
   kSiteSoftO = 0x322,
-  kSiteEpi = 0x323,
   kSiteUnit = 0x324,
   kSiteSched = 0x325,
 };
@@ -81,14 +80,13 @@ struct Cfg {
   static constexpr int kBoxBytes = kBlockK * 128;
   static constexpr int kTileBytes = kBlockK * kRowBytes;
   static constexpr int kKSteps = D / 16;
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kSlots = D == 128 ? 5 : 10;
   static constexpr int kQOff = 0;
-  static constexpr int kOOff = kTiles * kTileBytes;     // O staging, shared by both tiles in turn
-  static constexpr int kRingOff = kOOff + kTileBytes;
+  static constexpr int kRingOff = kTiles * kTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
-  // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], epi[2], stg, drain,
-  // unit_full, unit_empty, answer
-  static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 1 + 3;
+  // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], drain, unit,
+  // unit_read, answer
+  static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 1 + 3;
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kAnswerOff = kMiscOff + 16;                  // launch control's 16-byte answer
   static constexpr int kUnitOff = kAnswerOff + 16;                  // the published unit
@@ -106,6 +104,8 @@ struct Params {
   float cap_out;      // softcap log2(e)
   CapPoly poly;       // factor cap_out
   const float* slopes;
+  __nv_bfloat16* o;
+  Strides so;
   float* lse;
   unsigned int* err_word;
   unsigned long long wait_ns;
@@ -182,15 +182,13 @@ constexpr int kPartsOf = MODE == 2 ? 2 : 1;
 template <int D, int MODE>
 __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                      const __grid_constant__ Params p) {
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using C = Cfg<D>;
   constexpr int kParts = kPartsOf<MODE>;
   using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::kQOff;
-  uint8_t* sO = smem + C::kOOff;
   uint8_t* sRing = smem + C::kRingOff;
   uint64_t* bar_q = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [2] per tile: Q landed
   uint64_t* bar_qe = bar_q + 2;              // [2] per tile: last Q K^T of a unit done (Q slot free)
@@ -199,9 +197,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
   uint64_t* bar_s = bar_empty + C::kSlots;   // [2] per tile: S ready
   uint64_t* bar_p = bar_s + 2;               // [2] per tile: P written
   uint64_t* bar_o = bar_p + 2;               // [2] per tile: last P V of a unit done
-  uint64_t* bar_epi = bar_o + 2;             // [2] per tile: O staged in shared memory
-  uint64_t* bar_stg = bar_epi + 2;           // O staging buffer read out by the previous store
-  uint64_t* bar_drain = bar_stg + 1;
+  uint64_t* bar_drain = bar_o + 2;
   uint64_t* bar_unit = bar_drain + 1;        // a unit is published
   uint64_t* bar_unit_read = bar_unit + 1;    // every role has read it
   uint64_t* bar_answer = bar_unit_read + 1;  // launch control answered
@@ -219,13 +215,11 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       mbar_init(&bar_s[t], 1);
       mbar_init(&bar_p[t], 4 * kParts);
       mbar_init(&bar_o[t], 1);
-      mbar_init(&bar_epi[t], 4 * kParts);
     }
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], 1);
     }
-    mbar_init(bar_stg, 1);
     mbar_init(bar_drain, 1);
     mbar_init(bar_unit, 1);
     mbar_init(bar_unit_read, 3 + R::kSoftWarps);  // the K/V, Q and MMA threads, the softmax warps
@@ -238,7 +232,6 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
-    prefetch_tmap(&tm_o);
   }
   tc_fence_before();
   __syncthreads();
@@ -429,8 +422,6 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     const uint32_t col_s = C::col_s(t) + 64 * half, col_o = C::col_o(t);
     uint32_t scnt = 0;   // S blocks consumed so far (bar_s phase)
     uint32_t nout = 0;   // units of this tile with keys (bar_o phase)
-    uint32_t nepi = 0;   // epilogues of this tile (bar_epi phase)
-    uint32_t nstg = 0;   // epilogues of both tiles before this unit's (bar_stg phase)
     // The warps of a pair meet at their barrier in every unit, so a warp whose wait gave up (the block
     // is aborting) carries on with whatever TMEM holds, and both leave together at the next unit.
     bool ok = true;
@@ -446,8 +437,6 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       if (u < 0) break;
       const int b = bh / p.H, h = bh % p.H;
       const int row0 = u * kUnitRows + t * kBlockQ;
-      const uint32_t my_stg = nstg + static_cast<uint32_t>(t);
-      nstg += u * kUnitRows + kBlockQ < p.N ? 2u : 1u;
       if (row0 >= p.N) continue;
       const int qrow = row0 + row;
       const int2 see = qrow < p.N ? keys_of(p.plan, p.causal, b, qrow, p.N) : make_int2(0, 0);
@@ -709,11 +698,12 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         ++nout;
         tc_fence_after();
       }
-      // The staging buffer is free once the previous epilogue's store has read it.
-      if (my_stg > 0) ok = warp_wait(bar_stg, (my_stg - 1) & 1, wc, kSiteEpi) && ok;
       if (!ok) continue;
+      // O straight to memory, 16 bytes a store: staging it for a TMA store would need 32 KB that the
+      // two tiles share, so one tile's epilogue would wait for the other's, and it costs ring slots.
       const bool any_key = l > 0.f;
       const float inv_l = any_key ? 1.f / l : 0.f;
+      uint4* orow = reinterpret_cast<uint4*>(p.o + b * p.so.s[2] + h * p.so.s[1] + static_cast<int64_t>(qrow) * p.so.s[0]);
 #pragma unroll 1
       for (int c = half * (D / 64); c < (kParts == 2 ? (half + 1) * (D / 64) : D / 32); ++c) {
         uint32_t o[32];
@@ -727,31 +717,15 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), pair(inv_l));
           pk[i] = any_key ? pack_bf16x2(y.x, y.y) : 0u;
         }
-        uint8_t* box = sO + (c / 2) * C::kBoxBytes + row * 128;
+        if (qrow < p.N) {
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const int chunk = (c % 2) * 4 + q4;
-          *reinterpret_cast<uint4*>(box + ((chunk ^ (row & 7)) * 16)) =
-              make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
+          for (int q4 = 0; q4 < 4; ++q4)
+            orow[c * 4 + q4] = make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
         }
       }
       tc_fence_before();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_epi[t]);
       if (half == 0 && qrow < p.N)
         p.lse[static_cast<size_t>(bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
-      if (half == 0 && row == 0) {
-        if ((ok = mbar_wait(&bar_epi[t], nepi & 1, wc, kSiteEpi))) {
-#pragma unroll
-          for (int c = 0; c < C::kBoxes; ++c)
-            tma_store_4d(&tm_o, sO + c * C::kBoxBytes, c * kBoxCols, row0, h, b);
-          tma_store_commit_and_wait_read();
-          mbar_arrive(bar_stg);
-        }
-      }
-      ++nepi;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
     __syncwarp();
   }
@@ -768,13 +742,12 @@ template <int D, int MODE>
 cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   using C = Cfg<D>;
   using R = Roles<kPartsOf<MODE>>;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv;
   cudaError_t e;
   constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   if ((e = make_tmap_4d(&tq, a.q, kBf16, 2, D, a.N, a.H, a.B, a.sq.s, kBoxCols, kBlockQ))) return e;
   if ((e = make_tmap_4d(&tk, a.k, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sk.s, kBoxCols, kBlockK))) return e;
   if ((e = make_tmap_4d(&tv, a.v, kBf16, 2, D, a.N, sc.Hkv, a.B, a.sv.s, kBoxCols, kBlockK))) return e;
-  if ((e = make_tmap_4d(&to, a.o, kBf16, 2, D, a.N, a.H, a.B, a.so.s, kBoxCols, kBlockQ))) return e;
   Params p{};
   p.plan = sc.plan;
   p.causal = sc.causal;
@@ -790,6 +763,8 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
     p.poly = cap_poly(p.cap_out);
   }
   p.slopes = sc.slopes;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.so = a.so;
   p.lse = a.lse;
   p.err_word = a.err_word;
   p.wait_ns = a.dbg.wait_limit_ns;
@@ -799,7 +774,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   cudaFuncAttributes fattr;
   if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
   if (static_cast<uint32_t>(fattr.numRegs) * R::kThreads < R::kRegsNeeded) return cudaErrorInvalidConfiguration;
-  kern<<<static_cast<unsigned>(p.nunits) * static_cast<unsigned>(p.BH), R::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, p);
+  kern<<<static_cast<unsigned>(p.nunits) * static_cast<unsigned>(p.BH), R::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
