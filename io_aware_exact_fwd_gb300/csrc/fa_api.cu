@@ -164,7 +164,7 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
 
 cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes, int cols,
                          int rows, int heads, int batch, const int64_t strides[3], int box_cols, int box_rows,
-                         CUtensorMapSwizzle swizzle) {
+                         CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
   if (!g_encode) return cudaErrorInitializationError;
   // strides: {row, head, batch} in elements; the column stride is 1.
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
@@ -176,7 +176,7 @@ cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = g_encode(map, dtype, 4, const_cast<void*>(base), dims, gstr, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
