@@ -619,27 +619,27 @@ def fa_fwd_splitkv(q, k, v, o=None, lse=None, workspace=None, n_split: int = 0, 
     return o, lse
 
 
+# The calls of scored attention and of the paged cache are made once a layer and token, so their
+# checks are written to cost little: one attribute read where one will do, ints instead of device
+# objects, no ctypes object where an int or None passes.
+
 _Int64x2, _Int64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
 
 
-def _check_layout(name, t, shape, dtype, device):
-    """(address, strides) of a tensor in any layout whose last dimension is contiguous, on `device`.
+def _layout(name, t, shape, dtype, index):
+    """(address, strides) of a tensor in any layout whose last dimension is contiguous, on GPU `index`.
 
     strides is None when the tensor is dense, else its strides from the second-to-last
     dimension outwards (dimensions of one element, whose stride means nothing, count as
     dense)."""
-    if getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return t.data_ptr(), None
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
@@ -648,46 +648,49 @@ def _check_layout(name, t, shape, dtype, device):
         for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
             out.append(x if n != 1 else dense)
             dense *= n
-    else:
-        out = st[-2::-1]
-    return t.data_ptr(), (_Int64x3 if len(out) == 3 else _Int64x2)(*out)
+        st = (*reversed(out), 1)
+    if len(st) == 4:
+        return t.data_ptr(), _Int64x3(st[2], st[1], st[0])
+    return t.data_ptr(), _Int64x2(st[1], st[0])
 
 
-def _check_flat(name, t, shape, dtype, device):
-    """The address of a dense tensor on `device` (None: 0)."""
+def _flat(name, t, shape, dtype, index):
+    """The address of a dense tensor on GPU `index` (None: 0)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
-def _check_cuda(name, t, dtype=None):
-    """The device of a CUDA tensor (of `dtype`, if given)."""
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor, got {dev}")
-    return dev
+def _bytes(name, t, index):
+    """(address, bytes) of a plan or workspace: a dense tensor on GPU `index`."""
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{index}")
+    return t.data_ptr(), t.nbytes
 
 
-def _bytes_of(name, t, device):
-    """(address, bytes) of a plan or workspace: a dense tensor on `device`."""
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+def _gpu(name, t, dtypes):
+    """The GPU index of a tensor of one of `dtypes`."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return index
 
 
-def _call(fn, where, device, stream, *args):
-    """fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
-    import torch
+def _call(fn, where, index, stream, args):
+    """fn(*args, stream) with GPU `index` current, on `stream` or that GPU's current stream."""
+    from torch import _C
 
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call(fn, where, device, stream, *args)
+    if _C._cuda_getDevice() != index:
+        import torch
+
+        with torch.cuda.device(index):
+            return _call(fn, where, index, stream, args)
     # The raw handle of the current stream: building a Stream object for it costs more than the call.
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    st = fn(*args, _C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if st != 0:
         raise FAError(st, where)
 
@@ -709,19 +712,18 @@ def fa_mask_plan(B: int, N: int, cu_docs=None, prefix=None, causal: bool = True,
 
     lib = load_library()
     ref = cu_docs if cu_docs is not None else prefix if prefix is not None else plan
-    if ref is not None:
-        dev = _check_cuda("cu_docs, prefix or plan", ref)
+    if ref is None:
+        index = torch.device("cuda" if device is None else device).index
+        index = torch.cuda.current_device() if index is None else index
     else:
-        dev = torch.device("cuda" if device is None else device)
-        if dev.index is None:
-            dev = torch.device(dev.type, torch.cuda.current_device())
+        index = _gpu("cu_docs, prefix or plan", ref, (torch.int32, torch.uint8))
     n_docs = 1 if cu_docs is None else cu_docs.shape[1] - 1
-    pc = _check_flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, dev)
-    px = _check_flat("prefix", prefix, (B, n_docs), torch.int32, dev)
+    pc = _flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, index)
+    px = _flat("prefix", prefix, (B, n_docs), torch.int32, index)
     if plan is None:
-        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=dev)
-    pp, pb = _bytes_of("plan", plan, dev)
-    _call(lib.fa_mask_plan, "fa_mask_plan", dev, stream, pc, px, n_docs, pp, pb, B, N, int(bool(causal)))
+        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=f"cuda:{index}")
+    _call(lib.fa_mask_plan, "fa_mask_plan", index, stream,
+          (pc, px, n_docs, *_bytes("plan", plan, index), B, N, int(bool(causal))))
     return plan
 
 
@@ -737,22 +739,23 @@ def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float 
     """
     import torch
 
-    lib = load_library()
-    bf = torch.bfloat16
-    qs, dev = q.shape, _check_cuda("q", q, bf)
+    bf, f32 = torch.bfloat16, torch.float32
+    index, qs = _gpu("q", q, (bf,)), q.shape
     B, H, N, d = qs
     Hkv = k.shape[1]
     ks = (B, Hkv, N, d)
+    pq, sq = _layout("q", q, qs, bf, index)
+    pk, sk = _layout("k", k, ks, bf, index)
+    pv, sv = _layout("v", v, ks, bf, index)
     if o is None:
-        o = torch.empty(qs, dtype=bf, device=dev)
+        o = q.new_empty(qs)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-    pp, pb = (0, 0) if plan is None else _bytes_of("plan", plan, dev)
-    _call(lib.fa_fwd_scored, "fa_fwd_scored", dev, stream, *_check_layout("q", q, qs, bf, dev),
-          *_check_layout("k", k, ks, bf, dev), *_check_layout("v", v, ks, bf, dev), *_check_layout("o", o, qs, bf, dev),
-          _check_flat("lse", lse, (B, H, N), torch.float32, dev), B, H, Hkv, N, d, pp, pb, int(bool(causal)),
-          d ** -0.5 if scale is None else float(scale), float(softcap),
-          _check_flat("slopes", slopes, (H,), torch.float32, dev))
+        lse = q.new_empty((B, H, N), dtype=f32)
+    po, so = _layout("o", o, qs, bf, index)
+    pp, pb = (0, 0) if plan is None else _bytes("plan", plan, index)
+    _call(load_library().fa_fwd_scored, "fa_fwd_scored", index, stream,
+          (pq, sq, pk, sk, pv, sv, po, so, _flat("lse", lse, (B, H, N), f32, index), B, H, Hkv, N, d, pp, pb,
+           1 if causal else 0, d ** -0.5 if scale is None else scale, softcap, _flat("slopes", slopes, (H,), f32, index)))
     return o, lse
 
 
@@ -772,52 +775,42 @@ def fa_bwd_scored(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None
     """
     import torch
 
-    lib = load_library()
-    bf = torch.bfloat16
-    qs, dev = q.shape, _check_cuda("q", q, bf)
+    bf, f32 = torch.bfloat16, torch.float32
+    index, qs = _gpu("q", q, (bf,)), q.shape
     B, H, N, d = qs
     Hkv = k.shape[1]
     ks = (B, Hkv, N, d)
-    dq = torch.empty(qs, dtype=bf, device=dev) if dq is None else dq
-    dk = torch.empty(ks, dtype=bf, device=dev) if dk is None else dk
-    dv = torch.empty(ks, dtype=bf, device=dev) if dv is None else dv
+    dq = q.new_empty(qs) if dq is None else dq
+    dk = q.new_empty(ks) if dk is None else dk
+    dv = q.new_empty(ks) if dv is None else dv
     if workspace is None:
-        workspace = torch.empty(max(fa_bwd_scored_workspace_size(B, H, Hkv, N, d), 1), dtype=torch.uint8, device=dev)
-    pp, pb = (0, 0) if plan is None else _bytes_of("plan", plan, dev)
-    _call(lib.fa_bwd_scored, "fa_bwd_scored", dev, stream, *_check_layout("q", q, qs, bf, dev),
-          *_check_layout("k", k, ks, bf, dev), *_check_layout("v", v, ks, bf, dev), *_check_layout("o", o, qs, bf, dev),
-          *_check_layout("do", do, qs, bf, dev), _check_flat("lse", lse, (B, H, N), torch.float32, dev),
-          *_check_layout("dq", dq, qs, bf, dev), *_check_layout("dk", dk, ks, bf, dev),
-          *_check_layout("dv", dv, ks, bf, dev), *_bytes_of("workspace", workspace, dev), B, H, Hkv, N, d, pp, pb,
-          int(bool(causal)), d ** -0.5 if scale is None else float(scale), float(softcap),
-          _check_flat("slopes", slopes, (H,), torch.float32, dev), int(bool(deterministic)))
+        workspace = q.new_empty(max(fa_bwd_scored_workspace_size(B, H, Hkv, N, d), 1), dtype=torch.uint8)
+    pp, pb = (0, 0) if plan is None else _bytes("plan", plan, index)
+    _call(load_library().fa_bwd_scored, "fa_bwd_scored", index, stream,
+          (*_layout("q", q, qs, bf, index), *_layout("k", k, ks, bf, index), *_layout("v", v, ks, bf, index),
+           *_layout("o", o, qs, bf, index), *_layout("do", do, qs, bf, index), _flat("lse", lse, (B, H, N), f32, index),
+           *_layout("dq", dq, qs, bf, index), *_layout("dk", dk, ks, bf, index), *_layout("dv", dv, ks, bf, index),
+           *_bytes("workspace", workspace, index), B, H, Hkv, N, d, pp, pb, 1 if causal else 0,
+           d ** -0.5 if scale is None else scale, softcap, _flat("slopes", slopes, (H,), f32, index),
+           1 if deterministic else 0))
     return dq, dk, dv
 
 
-def _cache_device(k_cache):
-    import torch
+def _cache(k_cache, v_cache, page_table, seq_lens, index):
+    """The arguments that describe a paged cache, its shape (pages, heads, page size, d), sequences and table width."""
+    from torch import int32
 
-    if k_cache.dtype is not torch.bfloat16 and k_cache.dtype is not torch.float16:
-        raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype}")
-    return _check_cuda("k_cache", k_cache)
-
-
-def _check_cache(k_cache, v_cache, page_table, seq_lens, dev):
-    """The arguments that describe a paged cache, its dtype code and sizes (pages, heads, page size, d; sequences)."""
-    import torch
-
-    dt = k_cache.dtype
-    shape = k_cache.shape
+    shape, dt = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or page_table.dim() != 2:
         raise ValueError("k_cache must be indexed [n_pages, Hkv, page_size, d], page_table [B, max_pages]")
-    B, max_pages = page_table.shape
-    ts = page_table.stride(0)
-    if page_table.dtype != torch.int32 or page_table.device != dev or (max_pages > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on {dev}")
-    cache = (*_check_layout("k_cache", k_cache, shape, dt, dev), *_check_layout("v_cache", v_cache, shape, dt, dev),
-             page_table.data_ptr(), ts if B > 1 else max(max_pages, ts),
-             _check_flat("seq_lens", seq_lens, (B,), torch.int32, dev))
-    return cache, 1 if dt is torch.bfloat16 else 2, shape, B, max_pages
+    B, width = page_table.shape
+    ts, row = page_table.stride()
+    if page_table.dtype is not int32 or page_table.get_device() != index or (width > 1 and row != 1):
+        raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on cuda:{index}")
+    pk, sk = _layout("k_cache", k_cache, shape, dt, index)
+    pv, sv = _layout("v_cache", v_cache, shape, dt, index)
+    return ((pk, sk, pv, sv, page_table.data_ptr(), ts if B > 1 or ts > width else width,
+             _flat("seq_lens", seq_lens, (B,), int32, index)), shape, B, width)
 
 
 def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream=None):
@@ -830,13 +823,14 @@ def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream
     """
     import torch
 
-    lib = load_library()
-    dev = _cache_device(k_cache)
-    cache, code, (n_pages, Hkv, page, d), B, max_pages = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
-    T, dt = k.shape[0], k_cache.dtype
-    _call(lib.fa_paged_append, "fa_paged_append", dev, stream, *_check_layout("k", k, (T, Hkv, d), dt, dev),
-          *_check_layout("v", v, (T, Hkv, d), dt, dev), *cache,
-          _check_flat("cu_new", cu_new, (B + 1,), torch.int32, dev), B, T, Hkv, d, page, n_pages, max_pages, code)
+    dt = k_cache.dtype
+    index = _gpu("k_cache", k_cache, (torch.bfloat16, torch.float16))
+    cache, (n_pages, Hkv, page, d), B, width = _cache(k_cache, v_cache, page_table, seq_lens, index)
+    T = k.shape[0]
+    _call(load_library().fa_paged_append, "fa_paged_append", index, stream,
+          (*_layout("k", k, (T, Hkv, d), dt, index), *_layout("v", v, (T, Hkv, d), dt, index), *cache,
+           _flat("cu_new", cu_new, (B + 1,), torch.int32, index), B, T, Hkv, d, page, n_pages, width,
+           1 if dt is torch.bfloat16 else 2))
 
 
 def fa_paged_decode_workspace_size(B: int, H: int, Hkv: int, d: int) -> int:
@@ -854,25 +848,26 @@ def fa_paged_decode(q, k_cache, v_cache, page_table, seq_lens, o=None, lse=None,
     """
     import torch
 
-    lib = load_library()
-    qs, dev, dt = q.shape, _cache_device(k_cache), k_cache.dtype
+    dt, f32, qs = k_cache.dtype, torch.float32, q.shape
+    index = _gpu("k_cache", k_cache, (torch.bfloat16, torch.float16))
     B, H, d = qs
-    cache, code, (n_pages, Hkv, page, dc), Bt, max_pages = _check_cache(k_cache, v_cache, page_table, seq_lens, dev)
+    cache, (n_pages, Hkv, page, dc), Bt, width = _cache(k_cache, v_cache, page_table, seq_lens, index)
     if Bt != B or dc != d:
         raise ValueError(f"q is for {B} sequences of head dim {d}, the page table for {Bt} and the cache for {dc}")
-    pq, sq = _check_layout("q", q, qs, dt, dev)
+    pq, sq = _layout("q", q, qs, dt, index)
     if o is None:
-        o = torch.empty(qs, dtype=dt, device=dev)
+        o = q.new_empty(qs)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, H), dtype=f32)
+    po, so = _layout("o", o, qs, dt, index)
     if workspace is None:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             need = fa_paged_decode_workspace_size(B, H, Hkv, d)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _call(lib.fa_paged_decode, "fa_paged_decode", dev, stream, pq, sq, *cache, *_check_layout("o", o, qs, dt, dev),
-          _check_flat("lse", lse, (B, H), torch.float32, dev), *_bytes_of("workspace", workspace, dev), B, H, Hkv, d,
-          page, n_pages, max_pages, code, d ** -0.5 if scale is None else float(scale), float(softcap),
-          _check_flat("slopes", slopes, (H,), torch.float32, dev))
+        workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
+    _call(load_library().fa_paged_decode, "fa_paged_decode", index, stream,
+          (pq, sq, *cache, po, so, _flat("lse", lse, (B, H), f32, index), *_bytes("workspace", workspace, index), B, H,
+           Hkv, d, page, n_pages, width, 1 if dt is torch.bfloat16 else 2, d ** -0.5 if scale is None else scale, softcap,
+           _flat("slopes", slopes, (H,), f32, index)))
     return o, lse
 
 
