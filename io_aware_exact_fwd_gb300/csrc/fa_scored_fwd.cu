@@ -358,8 +358,14 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         int item = 0;  // ring index of the next K or V block to consume
         uint32_t nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // Q tiles and P blocks consumed so far
         bool ok = true;
-        Unit x;
-        for (int k = 0; ok && next_unit(k, x, ok); ++k) {
+        Unit x{}, nx{};
+        bool have_next = false;             // nx is the next unit
+        bool early0 = false, early1 = false;  // its first S of tile 0, 1 is issued
+        for (int k = 0; ok; ++k) {
+          if (have_next) x = nx;
+          else if (!next_unit(k, x, ok)) break;
+          if (x.u < 0) break;
+          have_next = false;
           const int n = x.last() - x.first();
           // Stream position s: K_s is ring item 2 s, V_s item 2 s + 1 of the unit.  S_t of position
           // s is issued right after the P_t V of position s - 1 (position 0: before the loop).
@@ -385,7 +391,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
                 pv(t, slot_v, s > f);
                 if (s + 1 == l) mma_commit(&bar_o[t]);
               }
-              if (ok && s + 1 >= f && s + 1 < l) {
+              if (ok && s + 1 >= f && s + 1 < l && !(s == -1 && (t ? early1 : early0))) {
                 if (!k_ready) {
                   if (!(ok = mbar_wait(&bar_full[slot_k], par_k, wc, kSiteMmaK))) continue;
                   k_ready = true;
@@ -397,6 +403,23 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
                 tc_fence_after();
                 qk(t, slot_k);
                 if (s + 2 == l) mma_commit(&bar_qe[t]);
+              }
+              if (s == -1) (t ? early1 : early0) = false;
+              // The unit's last position: tile t's first S of the next unit need not wait for the other
+              // tile's last P, if all it needs has arrived.  (With one part the unit change is a smaller
+              // share and the code costs more: causal 447 -> 465 us at B=2 H=16/4 N=8192 d=128.)
+              if (kParts == 2 && ok && s == n - 1) {
+                if (!have_next && mbar_try_wait(bar_unit, (k + 1) & 1)) have_next = next_unit(k + 1, nx, ok) || nx.u < 0;
+                const int slot0 = item % C::kSlots;  // K_0 of the next unit
+                if (have_next && nx.u >= 0 && nx.has(t) && nx.from(t) == 0 &&
+                    mbar_try_wait(&bar_full[slot0], (item / C::kSlots) & 1) &&
+                    mbar_try_wait(&bar_q[t], (t ? nq1 : nq0) & 1)) {
+                  if (t) ++nq1; else ++nq0;
+                  tc_fence_after();
+                  qk(t, slot0);
+                  if (nx.to(t) == 1) mma_commit(&bar_qe[t]);
+                  (t ? early1 : early0) = true;
+                }
               }
             }
             if (!ok) break;
@@ -425,23 +448,46 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     // The warps of a pair meet at their barrier in every unit, so a warp whose wait gave up (the block
     // is aborting) carries on with whatever TMEM holds, and both leave together at the next unit.
     bool ok = true;
-    for (int k = 0;; ++k) {
-      ok = ok && warp_wait(bar_unit, k & 1, wc, kSiteUnit);
-      if (kParts == 2 ? pair_or(pair_id, !ok) : !ok) break;
-      const int u = s_unit->u, bh = s_unit->bh;
-      const int blk0 = s_unit->begin[t], blk1 = s_unit->end[t];
-      // Keys that every row of the tile sees: [all_lo, all_hi).
-      const int all_lo = s_unit->all_lo[t], all_hi = s_unit->all_hi[t];
+    // The next unit; with two parts, read (and its row's interval and slope requested) before the
+    // epilogue of the current one if it is published by then.  With one part the registers that takes
+    // cost more than it saves (bias 542 -> 667 us at B=2 H=16/4 N=8192 d=128).
+    struct {
+      int u, bh, blk0, blk1, all_lo, all_hi;
+      int2 see;
+      float slope2;
+    } nu;
+    bool have_next = false;
+    auto read_unit = [&]() {
+      nu.u = s_unit->u;
+      nu.bh = s_unit->bh;
+      nu.blk0 = s_unit->begin[t];
+      nu.blk1 = s_unit->end[t];
+      nu.all_lo = s_unit->all_lo[t];
+      nu.all_hi = s_unit->all_hi[t];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_unit_read);
-      if (u < 0) break;
-      const int b = bh / p.H, h = bh % p.H;
-      const int row0 = u * kUnitRows + t * kBlockQ;
+      const int qrow = nu.u * kUnitRows + t * kBlockQ + row;
+      nu.see = make_int2(0, 0);
+      nu.slope2 = 0.f;
+      if (nu.u >= 0) {
+        if (qrow < p.N) nu.see = keys_of(p.plan, p.causal, nu.bh / p.H, qrow, p.N);
+        if (MODE != 0 && p.slopes) nu.slope2 = __ldg(p.slopes + nu.bh % p.H) * kLog2e;
+      }
+    };
+    for (int k = 0;; ++k) {
+      if (!have_next) ok = ok && warp_wait(bar_unit, k & 1, wc, kSiteUnit);
+      if (kParts == 2 ? pair_or(pair_id, !ok) : !ok) break;
+      if (!have_next) read_unit();
+      have_next = false;
+      if (nu.u < 0) break;
+      const int bh = nu.bh, b = bh / p.H, h = bh % p.H;
+      const int row0 = nu.u * kUnitRows + t * kBlockQ;
       if (row0 >= p.N) continue;
       const int qrow = row0 + row;
-      const int2 see = qrow < p.N ? keys_of(p.plan, p.causal, b, qrow, p.N) : make_int2(0, 0);
-      const float slope2 = MODE != 0 && p.slopes ? __ldg(p.slopes + h) * kLog2e : 0.f;
-      const int nkt = blk1 - blk0;
+      const int2 see = nu.see;
+      const float slope2 = nu.slope2;
+      // Keys that every row of the tile sees: [all_lo, all_hi).
+      const int all_lo = nu.all_lo, all_hi = nu.all_hi, blk1 = nu.blk1, nkt = nu.blk1 - nu.blk0;
       // Reference maximum, log2 units (0 until the row has seen a key).  MODE 2: the largest bias
       // among the row's keys: 0, at the row's own position, or for a negative slope at its farthest.
       float m_used = 0.f;
@@ -693,6 +739,10 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       }
 
       // ------------------------------------------------------------ epilogue
+      if (kParts == 2 && ok && __all_sync(0xffffffffu, mbar_try_wait(bar_unit, (k + 1) & 1))) {
+        read_unit();
+        have_next = true;
+      }
       if (nkt > 0) {
         ok = warp_wait(&bar_o[t], nout & 1, wc, kSiteSoftO) && ok;
         ++nout;
