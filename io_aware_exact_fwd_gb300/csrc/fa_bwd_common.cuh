@@ -121,19 +121,6 @@ __device__ __forceinline__ int det_shift(float dq_block_max, float vmax, float k
 }
 __device__ __forceinline__ float pow2f(int s) { return __int_as_float((s + 127) << 23); }  // -126 <= s <= 127
 
-// Three-term bf16 split of x: t1 = bf16(x), t2 = bf16(x - t1), t3 = bf16(x - t1 - t2)
-// (each difference exact in fp32), so t1 + t2 + t3 carries about 24 significant
-// bits of x.  Returned as raw bf16 bits.
-__device__ __forceinline__ void split3_bf16(float x, uint32_t (&t)[3]) {
-  float r = x;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(r);
-    t[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h));
-    r -= __bfloat162float(h);
-  }
-}
-
 // Element offset of row n of head (b, h) in a strided [B, H, N, d] tensor.
 __device__ __forceinline__ size_t row_offset(const Strides& st, long long bh, int H, int n) {
   return static_cast<size_t>((bh / H) * st.s[2] + (bh % H) * st.s[1] + static_cast<long long>(n) * st.s[0]);

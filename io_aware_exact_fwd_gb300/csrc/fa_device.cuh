@@ -489,6 +489,19 @@ __device__ __forceinline__ uint32_t e4m3x2_bits(float lo, float hi) {
   return r;
 }
 
+// Three-term bf16 split of x: t1 = bf16(x), t2 = bf16(x - t1), t3 = bf16(x - t1 - t2)
+// (each difference exact in fp32), so t1 + t2 + t3 carries about 24 significant
+// bits of x.  Returned as raw bf16 bits.
+__device__ __forceinline__ void split3_bf16(float x, uint32_t (&t)[3]) {
+  float r = x;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(r);
+    t[i] = static_cast<uint32_t>(__bfloat16_as_ushort(h));
+    r -= __bfloat162float(h);
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);

@@ -73,17 +73,22 @@ enum : uint32_t {
   kSiteSched = 0x325,
 };
 
-template <int D>
+template <int D, int MODE>
 struct Cfg {
   static constexpr int kRowBytes = D * 2;
   static constexpr int kBoxes = kRowBytes / 128;
   static constexpr int kBoxBytes = kBlockK * 128;
   static constexpr int kTileBytes = kBlockK * kRowBytes;
   static constexpr int kKSteps = D / 16;
-  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kSlots = D == 64 ? 10 : MODE == 1 ? 4 : 5;
+  // MODE 1: one more K-step of Q K^T adds the bias's growth along the block's keys: rows of 16 bf16
+  // (32-byte swizzle), [s1 s2 s3 0...] with s1 + s2 + s3 = slope / scale for every query of a tile,
+  // [j j j 0...] for key j of the block (0 .. 127, exact in bf16).
+  static constexpr int kBiasTile = MODE == 1 ? kBlockK * 32 : 0;
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kTiles * kTileBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kBiasOff = kRingOff + kSlots * kTileBytes;   // the two tiles' query side, the key side
+  static constexpr int kBarOff = kBiasOff + 3 * kBiasTile;
   // q_full[2], q_empty[2], full[kSlots], empty[kSlots], s_full[2], p_full[2], o_done[2], drain, unit,
   // unit_read, answer
   static constexpr int kNumBars = 2 + 2 + 2 * kSlots + 2 + 2 + 2 + 1 + 3;
@@ -99,7 +104,7 @@ struct Cfg {
 struct Params {
   MaskPlan plan;
   int causal, N, H, group, BH, nunits;
-  float scale_log2;   // scale log2(e)
+  float scale, scale_log2;  // scale_log2 = scale log2(e)
   float cap_in;       // 4 scale / softcap: products to x = 4 u
   float cap_out;      // softcap log2(e)
   CapPoly poly;       // factor cap_out
@@ -183,7 +188,7 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   constexpr int kParts = kPartsOf<MODE>;
   using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
@@ -226,6 +231,15 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     mbar_init(bar_answer, 1);
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if constexpr (MODE == 1) {
+    for (int x = threadIdx.x; x < 2 * kBlockK; x += R::kThreads) {  // 16-byte half rows, swizzled
+      const int j = x >> 1, part = x & 1;
+      const uint32_t v = pack_bf16x2(static_cast<float>(j), static_cast<float>(j));
+      *reinterpret_cast<uint4*>(smem + C::kBiasOff + 2 * C::kBiasTile + j * 32 + ((part ^ ((j >> 2) & 1)) << 4)) =
+          part == 0 ? make_uint4(v, v & 0xffffu, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
   }
   if (warp == R::kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
   if (warp == R::kWarpLoad && lane == 0) {
@@ -305,29 +319,45 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       __syncwarp();
     } else if (warp == R::kWarpLoadQ) {
       // --------------------------------------------------------- Q TMA producer
-      if (lane == 0) {
-        int nload[kTiles] = {0, 0};
-        bool ok = true;
-        Unit x;
-        for (int k = 0; ok && next_unit(k, x, ok); ++k) {
-          const int b = x.bh / p.H, h = x.bh % p.H;
+      int nload[kTiles] = {0, 0};
+      bool ok = true;
+      for (int k = 0; (ok = warp_wait_suspend(bar_unit, k & 1, wc, kSiteUnit)); ++k) {
+        const Unit x = *s_unit;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_unit_read);
+        if (x.u < 0) break;
+        const int b = x.bh / p.H, h = x.bh % p.H;
 #pragma unroll
-          for (int tt = 0; tt < kTiles; ++tt) {
-            const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
-            if (!ok || !x.has(t)) continue;
-            if (nload[t] > 0 && !(ok = mbar_wait_suspend(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ, 20000u))) continue;
+        for (int tt = 0; tt < kTiles; ++tt) {
+          const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
+          if (!ok || !x.has(t)) continue;
+          if (nload[t] > 0 && !(ok = warp_wait_suspend(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ))) continue;
+          if constexpr (MODE == 1) {  // the head's slope for the bias's K-step
+            uint32_t c[3];
+            split3_bf16(__ldg(p.slopes + h) / p.scale, c);
+            for (int r = lane; r < kBlockQ; r += 32) {
+              uint8_t* dst = smem + C::kBiasOff + t * C::kBiasTile + r * 32;
+              const int half = (r >> 2) & 1;
+              *reinterpret_cast<uint4*>(dst + half * 16) = make_uint4(c[0] | (c[1] << 16), c[2], 0u, 0u);
+              *reinterpret_cast<uint4*>(dst + (half ^ 1) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
             mbar_arrive_expect_tx(&bar_q[t], C::kTileBytes);
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
               tma_load_4d(sQ + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, &bar_q[t], c * kBoxCols,
                           x.u * kUnitRows + t * kBlockQ, h, b);
-            ++nload[t];
           }
+          ++nload[t];
         }
-        if (!ok)
-          for (int t = 0; t < kTiles; ++t)
-            if (nload[t] > 0) mbar_wait_drain(&bar_q[t], (nload[t] - 1) & 1, p.wait_ns);
+        if (!ok) break;
       }
+      if (!ok && lane == 0)
+        for (int t = 0; t < kTiles; ++t)
+          if (nload[t] > 0) mbar_wait_drain(&bar_q[t], (nload[t] - 1) & 1, p.wait_ns);
       __syncwarp();
     } else if (warp == R::kWarpMma) {
       // ------------------------------------------------------------ MMA issuer
@@ -337,6 +367,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         const uint64_t qdesc = sdesc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t kdesc = sdesc_sw128(smem_u32(sRing), 16, 1024);
         const uint64_t vdesc = sdesc_sw128(smem_u32(sRing), C::kBoxBytes, 1024);
+        const uint64_t bias_q = sdesc_sw32(smem_u32(smem + C::kBiasOff));
+        const uint64_t bias_k = sdesc_sw32(smem_u32(smem + C::kBiasOff + 2 * C::kBiasTile));
         auto qk = [&](int t, int slot) {  // S_t = Q_t K^T: both K-major, 16 columns of d per MMA
           const uint64_t qd = sdesc_add(qdesc, t * C::kTileBytes);
           const uint64_t kd = sdesc_add(kdesc, slot * C::kTileBytes);
@@ -345,6 +377,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             const uint32_t off = (kk / 4) * C::kBoxBytes + (kk % 4) * 32;
             mma_bf16_ss(tmem + C::col_s(t), sdesc_add(qd, off), sdesc_add(kd, off), idesc_qk, kk > 0 ? 1u : 0u);
           }
+          if (MODE == 1)  // + slope / scale times the key's place in the block
+            mma_bf16_ss(tmem + C::col_s(t), sdesc_add(bias_q, t * C::kBiasTile), bias_k, idesc_qk, 1u);
           mma_commit(&bar_s[t]);
         };
         auto pv = [&](int t, int slot, bool accumulate) {  // O_t += P_t V: P from TMEM, V MN-major
@@ -560,7 +594,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
               }
             }
             if (need_mask) {
-              const uint32_t vis = bits_between(see.x - (key0), see.y - (key0));
+              const uint32_t vis = bits_between(see.x - key0, see.y - key0);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
@@ -576,28 +610,25 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           }
         }
         if constexpr (MODE != 2) {
-        uint32_t r[4][32];
-        auto load = [&]() {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
-        };
-        load();
-        // The general form of the scores (any tanh argument, keys on both sides of the row), eight
-        // columns at a time in place in TMEM: a small rolled loop, because it is rare and the
-        // kernel's speed depends on its code fitting the instruction caches.
-        bool pre = MODE != 0 && !left && !right && (MODE == 1 || p.slopes != nullptr);
+        // The general form of the scores (any argument of the cap, a bias with keys right of the row),
+        // eight columns at a time in place in TMEM before they are loaded: a small rolled loop, because
+        // it is rare, the kernel's speed depends on its code fitting the instruction caches, and a
+        // second form of 128 scores in registers would cost the common one a move for each.
+        const bool biased = MODE == 1 || (MODE == 3 && p.slopes != nullptr);
+        bool pre = biased && !left;
         if constexpr (MODE == 3) {
           uint32_t bits = 0;
+#pragma unroll 1
+          for (int c = 0; c < kBlockK; c += 8) {
+            uint32_t x[8];
+            tmem_ld8_wait(trow + col_s + c, x);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              bits = or_bits(bits, __fmul2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), pair(p.cap_in)));
+            for (int i = 0; i < 8; i += 2)
+              bits = or_bits(bits, __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pair(p.cap_in)));
+          }
           pre = pre || __any_sync(0xffffffffu, bits & kReachesTwo);
         }
-        if (MODE != 0 && pre) {
+        if (pre) {
 #pragma unroll 1
           for (int c = 0; c < kBlockK; c += 8) {
             uint32_t x[8];
@@ -605,44 +636,53 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float s = __uint_as_float(x[i]);
-              const float a = MODE == 3 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x : s * p.scale_log2;
+              // MODE 1: the K-step's slope times the key's place is taken out again.
+              const float a = MODE == 3 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x
+                                        : fmaf(-slope2, static_cast<float>(c + i), s * p.scale_log2);
               x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
             }
             tmem_st8(trow + col_s + c, x);
           }
           tmem_st_wait();
-          load();
         }
-        // r becomes the score minus the reference, in log2 units: cap, bias, mask.
-        const float sg = left ? slope2 : -slope2;
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
+        // r becomes the score minus the reference, in log2 units: r mul + base, or r (polynomial) + bias,
+        // with the identity where the loop above has made the scores.  On the row's left the bias of
+        // the block's first key is left to add; its growth from there is in S (MODE 1).
+        const float first = slope2 * static_cast<float>(kbase - qrow);
+        const float mul = pre ? 1.f : MODE == 3 ? p.cap_in : p.scale_log2;
+        const float base = pre || MODE == 0 ? -m_used : first - m_used;
+        CapPoly poly = p.poly;
+        if (MODE == 3 && pre) {
+          poly.c[0] = pair(1.f);
+          poly.c[1] = poly.c[2] = poly.c[3] = pair(0.f);
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if (MODE != 0 && pre) {
+          float2 off = pair(base);
+          const float step = MODE == 3 && !pre ? slope2 : 0.f, off0 = fmaf(step, 32.f * c, base);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[c][i] = __float_as_uint(__uint_as_float(r[c][i]) - m_used);
-          } else {
-            // The bias of the chunk's first key less the reference; sg more for every key.
-            const float base = MODE == 0 ? -m_used : fmaf(sg, static_cast<float>(kbase + c * 32 - qrow), -m_used);
-            float2 off = make_float2(base, MODE == 0 ? base : base + sg);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-              if (MODE != 0 && i > 0)  // four keys' steps are added up, then the sum starts afresh
-                off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
-                                 : __fadd2_rn(off, pair(2.f * sg));
-              float2 y;
-              if constexpr (MODE == 3) {
-                const float2 x = __fmul2_rn(s, pair(p.cap_in));
-                y = __ffma2_rn(x, tanh_over_x(x, p.poly), off);
-              } else {
-                y = __ffma2_rn(s, pair(p.scale_log2), off);
-              }
-              r[c][i] = __float_as_uint(y.x);
-              r[c][i + 1] = __float_as_uint(y.y);
+          for (int i = 0; i < 32; i += 2) {
+            const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+            float2 y;
+            if constexpr (MODE == 3) {
+              // step more for every key: four steps are added up, then the sum starts afresh.
+              off = i % 8 == 0 ? make_float2(fmaf(step, static_cast<float>(i), off0), fmaf(step, static_cast<float>(i + 1), off0))
+                               : __fadd2_rn(off, pair(2.f * step));
+              const float2 x = __fmul2_rn(s, pair(mul));
+              y = __ffma2_rn(x, tanh_over_x(x, poly), off);
+            } else {
+              y = __ffma2_rn(s, pair(mul), off);
             }
+            r[c][i] = __float_as_uint(y.x);
+            r[c][i + 1] = __float_as_uint(y.y);
           }
           if (need_mask) {
-            const uint32_t vis = bits_between(see.x - (kbase + c * 32), see.y - (kbase + c * 32));
+            const uint32_t vis = bits_between(see.x - kbase - c * 32, see.y - kbase - c * 32);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
@@ -790,7 +830,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 
 template <int D, int MODE>
 cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   using R = Roles<kPartsOf<MODE>>;
   CUtensorMap tq, tk, tv;
   cudaError_t e;
@@ -806,6 +846,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.group = a.H / sc.Hkv;
   p.BH = a.B * a.H;
   p.nunits = (a.N + kUnitRows - 1) / kUnitRows;
+  p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE >= 2) {
     p.cap_in = 4.f * a.scale / sc.softcap;
