@@ -179,10 +179,10 @@ __device__ __forceinline__ bool pair_or(int id, bool x) {
   return r != 0;
 }
 
-// MODE 0: scores as they are; 1: with a distance bias; 2: capped within kBoundedCap, 3:
-// capped beyond it (both biased if slopes).
+// MODE 0: scores as they are; 1: with a distance bias; 2 and 3: capped within kBoundedCap,
+// without and with a bias; 4: capped beyond it (biased if slopes).
 template <int MODE>
-constexpr int kPartsOf = MODE == 2 ? 2 : 1;
+constexpr int kPartsOf = MODE == 2 || MODE == 3 ? 2 : 1;
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using C = Cfg<D, MODE>;
   constexpr int kParts = kPartsOf<MODE>;
+  constexpr bool kBounded = MODE == 2 || MODE == 3;  // the fixed reference (kBoundedCap)
   using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -522,10 +523,10 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       const float slope2 = nu.slope2;
       // Keys that every row of the tile sees: [all_lo, all_hi).
       const int all_lo = nu.all_lo, all_hi = nu.all_hi, blk1 = nu.blk1, nkt = nu.blk1 - nu.blk0;
-      // Reference maximum, log2 units (0 until the row has seen a key).  MODE 2: the largest bias
+      // Reference maximum, log2 units (0 until the row has seen a key).  kBounded: the largest bias
       // among the row's keys: 0, at the row's own position, or for a negative slope at its farthest.
       float m_used = 0.f;
-      if (MODE == 2 && slope2 < 0.f && see.x < see.y)
+      if (MODE == 3 && slope2 < 0.f && see.x < see.y)
         m_used = -slope2 * static_cast<float>(max(qrow - see.x, see.y - 1 - qrow));
       bool seen = false;
       float l = 0.f;
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
         const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
         float2 part = make_float2(0.f, 0.f);
-        if constexpr (MODE == 2) {
+        if constexpr (kBounded) {
           // The fixed reference: P = exp2(cap + bias - m_used), 32 columns at a time.  P of columns 32c..
           // goes over columns 16c.. of the thread's S, which are consumed.
 #pragma unroll 1
@@ -556,67 +557,78 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
               r[i] = __float_as_uint(x.x);
               r[i + 1] = __float_as_uint(x.y);
             }
-            if (__any_sync(0xffffffffu, bits & kReachesTwo)) {
+            const bool general = __any_sync(0xffffffffu, bits & kReachesTwo) || (MODE == 3 && !left);
+            const uint32_t vis = bits_between(see.x - key0, see.y - key0);
+            // Each way below stores its own P: scores in registers at the meeting of two ways cost the
+            // common one a move each (14 % of the kernel).
+            if (general) {
+              // Any argument of the cap, a bias with keys right of the row: a small rolled loop from S,
+              // still whole in TMEM (P of these columns trails the columns read).
+#pragma unroll 1
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t x[8], pk[4];
+                tmem_ld8_wait(trow + col_s + c * 32 + i, x);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = tanh_any(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), p.cap_out, pair(-m_used));
-                r[i] = __float_as_uint(y.x);
-                r[i + 1] = __float_as_uint(y.y);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 x = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-                const float2 y = __ffma2_rn(x, tanh_over_x(x, p.poly), pair(-m_used));
-                r[i] = __float_as_uint(y.x);
-                r[i + 1] = __float_as_uint(y.y);
-              }
-            }
-            if (p.slopes) {
-              const float off0 = static_cast<float>(key0 - qrow);
-              if (left || right) {
-                // sg more for every key: four steps are added up, then the sum starts afresh.
-                const float sg = left ? slope2 : -slope2, base = sg * off0;
-                float2 off = make_float2(base, base + sg);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  if (i > 0)
-                    off = i % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(i), base), fmaf(sg, static_cast<float>(i + 1), base))
-                                     : __fadd2_rn(off, pair(2.f * sg));
-                  const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), off);
-                  r[i] = __float_as_uint(y.x);
-                  r[i + 1] = __float_as_uint(y.y);
+                for (int e = 0; e < 8; e += 2) {
+                  float2 y = tanh_any(__fmul2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), pair(p.cap_in)),
+                                      p.cap_out, pair(-m_used));
+                  if (MODE == 3) {
+                    const float off = static_cast<float>(key0 + i + e - qrow);
+                    y.x = fmaf(-slope2, fabsf(off), y.x);
+                    y.y = fmaf(-slope2, fabsf(off + 1.f), y.y);
+                  }
+                  const uint32_t v = vis >> (i + e);
+                  const float2 w = make_float2(v & 1u ? ex2_approx(y.x) : 0.f, v & 2u ? ex2_approx(y.y) : 0.f);
+                  part = __fadd2_rn(part, w);
+                  pk[e / 2] = pack_bf16x2(w.x, w.y);
                 }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  r[i] = __float_as_uint(fmaf(-slope2, fabsf(off0 + static_cast<float>(i)), __uint_as_float(r[i])));
+                tmem_st4(trow + col_s + c * 16 + i / 2, pk);
               }
+              continue;
             }
-            if (need_mask) {
-              const uint32_t vis = bits_between(see.x - key0, see.y - key0);
+            // The bias on the row's left: slope2 more for every key; four steps are added up, then the
+            // sum starts afresh.
+            const float off0 = MODE == 3 ? fmaf(slope2, static_cast<float>(key0 - qrow), -m_used) : -m_used;
+            float2 off = make_float2(off0, MODE == 3 ? off0 + slope2 : off0);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(vis & (1u << i))) r[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 x = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+              if (MODE == 3 && i > 0)
+                off = i % 8 == 0 ? make_float2(fmaf(slope2, static_cast<float>(i), off0), fmaf(slope2, static_cast<float>(i + 1), off0))
+                                 : __fadd2_rn(off, pair(2.f * slope2));
+              const float2 y = __ffma2_rn(x, tanh_over_x(x, p.poly), off);
+              r[i] = __float_as_uint(y.x);
+              r[i + 1] = __float_as_uint(y.y);
             }
             uint32_t pk[16];
+            if (need_mask) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 e = make_float2(ex2_approx(__uint_as_float(r[2 * i])), ex2_approx(__uint_as_float(r[2 * i + 1])));
-              part = __fadd2_rn(part, e);
-              pk[i] = pack_bf16x2(e.x, e.y);
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = make_float2(vis & (1u << (2 * i)) ? ex2_approx(__uint_as_float(r[2 * i])) : 0.f,
+                                             vis & (2u << (2 * i)) ? ex2_approx(__uint_as_float(r[2 * i + 1])) : 0.f);
+                part = __fadd2_rn(part, e);
+                pk[i] = pack_bf16x2(e.x, e.y);
+              }
+              tmem_st16(trow + col_s + c * 16, pk);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = make_float2(ex2_approx(__uint_as_float(r[2 * i])), ex2_approx(__uint_as_float(r[2 * i + 1])));
+                part = __fadd2_rn(part, e);
+                pk[i] = pack_bf16x2(e.x, e.y);
+              }
+              tmem_st16(trow + col_s + c * 16, pk);
             }
-            tmem_st16(trow + col_s + c * 16, pk);
           }
         }
-        if constexpr (MODE != 2) {
+        if constexpr (!kBounded) {
         // The general form of the scores (any argument of the cap, a bias with keys right of the row),
         // eight columns at a time in place in TMEM before they are loaded: a small rolled loop, because
         // it is rare, the kernel's speed depends on its code fitting the instruction caches, and a
         // second form of 128 scores in registers would cost the common one a move for each.
-        const bool biased = MODE == 1 || (MODE == 3 && p.slopes != nullptr);
+        const bool biased = MODE == 1 || (MODE == 4 && p.slopes != nullptr);
         bool pre = biased && !left;
-        if constexpr (MODE == 3) {
+        if constexpr (MODE == 4) {
           uint32_t bits = 0;
 #pragma unroll 1
           for (int c = 0; c < kBlockK; c += 8) {
@@ -637,7 +649,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             for (int i = 0; i < 8; ++i) {
               const float s = __uint_as_float(x[i]);
               // MODE 1: the K-step's slope times the key's place is taken out again.
-              const float a = MODE == 3 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x
+              const float a = MODE == 4 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x
                                         : fmaf(-slope2, static_cast<float>(c + i), s * p.scale_log2);
               x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
             }
@@ -654,22 +666,22 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         // with the identity where the loop above has made the scores.  On the row's left the bias of
         // the block's first key is left to add; its growth from there is in S (MODE 1).
         const float first = slope2 * static_cast<float>(kbase - qrow);
-        const float mul = pre ? 1.f : MODE == 3 ? p.cap_in : p.scale_log2;
+        const float mul = pre ? 1.f : MODE == 4 ? p.cap_in : p.scale_log2;
         const float base = pre || MODE == 0 ? -m_used : first - m_used;
         CapPoly poly = p.poly;
-        if (MODE == 3 && pre) {
+        if (MODE == 4 && pre) {
           poly.c[0] = pair(1.f);
           poly.c[1] = poly.c[2] = poly.c[3] = pair(0.f);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float2 off = pair(base);
-          const float step = MODE == 3 && !pre ? slope2 : 0.f, off0 = fmaf(step, 32.f * c, base);
+          const float step = MODE == 4 && !pre ? slope2 : 0.f, off0 = fmaf(step, 32.f * c, base);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
             float2 y;
-            if constexpr (MODE == 3) {
+            if constexpr (MODE == 4) {
               // step more for every key: four steps are added up, then the sum starts afresh.
               off = i % 8 == 0 ? make_float2(fmaf(step, static_cast<float>(i), off0), fmaf(step, static_cast<float>(i + 1), off0))
                                : __fadd2_rn(off, pair(2.f * step));
@@ -872,7 +884,9 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_d(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   if (sc.softcap > 0.f)
-    return sc.softcap * kLog2e <= kBoundedCap ? launch<D, 2>(a, sc, stream) : launch<D, 3>(a, sc, stream);
+    return sc.softcap * kLog2e > kBoundedCap ? launch<D, 4>(a, sc, stream)
+           : sc.slopes                       ? launch<D, 3>(a, sc, stream)
+                                             : launch<D, 2>(a, sc, stream);
   return sc.slopes ? launch<D, 1>(a, sc, stream) : launch<D, 0>(a, sc, stream);
 }
 
