@@ -19,6 +19,8 @@
 //    LSE2 (64 fp32 values beside each query block) after the cap.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa_bwd_common.cuh"
 #include "fa_device.cuh"
 #include "fa_internal.h"
@@ -54,7 +56,7 @@ __device__ __forceinline__ Steps steps_of(const Params& p, int kb, int b) {
   return {i0, nq, nq * p.group};
 }
 
-// MODE 0: scores as they are; 1: with a distance bias; 2: capped (and biased if slopes).
+// MODE 0: scores as they are; 1: with a distance bias; 2: capped; 3: capped and biased.
 template <int D, int MODE, bool DET>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -63,6 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ Params p) {
   using C = BwdCfg<D>;
   constexpr bool kSplitSdp = D == 128 && !DET;  // as in the plain backward
+  constexpr bool kCapped = MODE >= 2, kBiased = MODE == 1 || MODE == 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kKOff;
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_bf16_ss(tmem + C::kColS, sdesc_add(k_kmaj, offa), sdesc_add(ring_kmaj, stage + C::kStageQ + offb),
                             idesc_sdp, kk > 0 ? 1u : 0u);
               }
-              if (MODE != 2) mma_bf16_ss(tmem + C::kColS, kaug, sdesc_add(ring_aug, stage), idesc_sdp, 1u);
+              if (!kCapped) mma_bf16_ss(tmem + C::kColS, kaug, sdesc_add(ring_aug, stage), idesc_sdp, 1u);
             }
             if (issue_dp) {
 #pragma unroll
@@ -282,11 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ragged = kb * kBkB + kBkB > p.N;
     const int all_lo = queries_of(p.plan, p.causal, b_idx, min(kb * kBkB + kBkB, p.N) - 1, p.N).x;
     const int all_hi = ragged ? 0 : queries_of(p.plan, p.causal, b_idx, kb * kBkB, p.N).y;
-    const bool biased = MODE == 1 || (MODE == 2 && p.slopes != nullptr);
+    // No key of the warp is seen by a query before it: |i - j| = i - j wherever it counts.
+    const bool one_sided = !kBiased || __all_sync(0xffffffffu, by.x >= key || by.x >= by.y);
     bool ok = true;
     int head = 0, i = st.i0, slot = 0;
     uint32_t ring_ph = 0;
-    float slope2 = biased && n > 0 ? __ldg(p.slopes + h0) * kLog2e : 0.f;
+    float slope2 = kBiased && n > 0 ? __ldg(p.slopes + h0) * kLog2e : 0.f;
     for (int it = 0; it < n; ++it) {
       const int b = it & 1;
       if (!(ok = warp_wait_b_suspend(bar_sdp, it & 1, wc, kSiteBComp))) break;
@@ -301,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar_sde);  // the MMA warp may now overwrite S^T, dP^T
       const int qb = i * kBqB, q0 = qb + 32 * g;
       const bool need_mask = qb < all_lo || qb + kBqB > all_hi;
-      // s becomes the exponent of P in log2 units, dp becomes dS / P.
-      if constexpr (MODE == 2) {
+      bool general = kBiased && !one_sided && qb < kb * kBkB + kBkB - 1;
+      const float4* lse4 = nullptr;
+      if constexpr (kCapped) {
         uint32_t bits = 0;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -311,101 +316,73 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[c] = __float_as_uint(x.x);
           s[c + 1] = __float_as_uint(x.y);
         }
-        const bool large = __any_sync(0xffffffffu, bits & kReachesTwo);
-        // s becomes tanh; as two loops under one branch, or both forms would be computed for every pair.
-        if (large) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 t = tanh_any(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), 1.f, pair(0.f));
-            s[c] = __float_as_uint(t.x);
-            s[c + 1] = __float_as_uint(t.y);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            const float2 t = __fmul2_rn(x, tanh_over_x(x, p.poly));
-            s[c] = __float_as_uint(t.x);
-            s[c + 1] = __float_as_uint(t.y);
-          }
-        }
+        general = general || __any_sync(0xffffffffu, bits & kReachesTwo);
         // LSE2 of the step's queries: the slot landed before S^T was made of it (the wait makes its
         // bytes visible here), and is refilled only after this step's dV and dK.
         if (!(ok = warp_wait_b(&bar_full[slot], ring_ph, wc, kSiteBComp))) break;
-        const float4* lse4 =
-            reinterpret_cast<const float4*>(sRing + slot * C::kStageBytes + C::kStageAug) + 8 * g;
-#pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 l4 = lse4[c4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = 4 * c4 + 2 * e;
-            const float2 t = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            const float2 x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
-            const float2 bend = __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f));
-            const float2 y = __fmul2_rn(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), bend);
-            s[c] = __float_as_uint(x.x);
-            s[c + 1] = __float_as_uint(x.y);
-            dp[c] = __float_as_uint(y.x);
-            dp[c + 1] = __float_as_uint(y.y);
-          }
-        }
-      }
-      // The bias, as loops of their own under branches (see the cap); without a cap s is still the
-      // product, whose scale goes with it.
-      if (biased) {
-        const float mul = MODE == 2 ? 1.f : p.scale_log2;
-        const float off0 = static_cast<float>(q0 - key);  // i - j of the first query
-        const bool below = qb >= kb * kBkB + kBkB - 1, above = qb + kBqB - 1 <= kb * kBkB;
-        if (below || above) {
-          // sg more for every query: four steps are added up, then the sum starts afresh.
-          const float sg = below ? -slope2 : slope2, base = sg * off0;
-          float2 off = make_float2(base, base + sg);
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            if (c > 0)
-              off = c % 8 == 0 ? make_float2(fmaf(sg, static_cast<float>(c), base), fmaf(sg, static_cast<float>(c + 1), base))
-                               : __fadd2_rn(off, pair(2.f * sg));
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), pair(mul), off);
-            s[c] = __float_as_uint(x.x);
-            s[c + 1] = __float_as_uint(x.y);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            s[c] = __float_as_uint(
-                fmaf(__uint_as_float(s[c]), mul, -slope2 * fabsf(off0 + static_cast<float>(c))));
-        }
-      }
-      if (need_mask) {
-        const uint32_t vis = bits_between(by.x - q0, by.y - q0);
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!(vis & (1u << c))) s[c] = __float_as_uint(-INFINITY);
-      }
-      uint32_t ppk[16], dpk[16];
-#pragma unroll
-      for (int c2 = 0; c2 < 16; ++c2) {
-        const int c = 2 * c2;
-        float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        if (MODE == 0) x = __fmul2_rn(x, pair(p.scale_log2));
-        const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        const float2 ds = __fmul2_rn(pp, make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])));
-        ppk[c2] = pack_bf16x2(pp.x, pp.y);
-        dpk[c2] = pack_bf16x2(ds.x, ds.y);
+        lse4 = reinterpret_cast<const float4*>(sRing + slot * C::kStageBytes + C::kStageAug) + 8 * g;
       }
       // P^T, dS^T(it) overwrite dQ^T(it-2) (TMEM) and dS^T(it-2) (shared memory).
       if (it >= 2 && !(ok = warp_wait_b(&bar_dqe[b], ((it - 2) >> 1) & 1, wc, kSiteBComp))) break;
       tc_fence_after();
-      tmem_st16(trow + C::col_pdq(b) + 16 * g, ppk);
-      tmem_st16(trow + C::col_pdq(b) + 32 + 16 * g, dpk);
-      uint8_t* ds_row = sDs + b * C::kDsBytes + row * 128;
+      // P and dS of the 32 queries, written out.  Three ways, each whole (scores in registers at the
+      // meeting of two ways would cost the common one a move each): every key seen by every query;
+      // masked; and masked in the general form (any argument of the cap, queries on both sides).
+      auto step = [&](auto masked_c, auto general_c) {
+        constexpr bool kMasked = decltype(masked_c)::value, kGeneral = decltype(general_c)::value;
+        const uint32_t vis = kMasked ? bits_between(by.x - q0, by.y - q0) : 0xffffffffu;
+        // The bias with i >= j: -slope2 more for every query; four steps are added up, then the sum
+        // starts afresh.
+        const float off0 = -slope2 * static_cast<float>(q0 - key);
+        float2 off = make_float2(off0, off0 - slope2);
+        uint32_t ppk[16], dpk[16];
 #pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {
-        const int ch = g * 4 + c4;
-        *reinterpret_cast<uint4*>(ds_row + ((ch ^ (row & 7)) * 16)) =
-            make_uint4(dpk[4 * c4], dpk[4 * c4 + 1], dpk[4 * c4 + 2], dpk[4 * c4 + 3]);
-      }
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 l4 = kCapped ? lse4[c4] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = 4 * c4 + 2 * e;
+            float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            float2 dpp = make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
+            if constexpr (kCapped) {
+              const float2 t = kGeneral ? tanh_any(x, 1.f, pair(0.f)) : __fmul2_rn(x, tanh_over_x(x, p.poly));
+              x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
+              dpp = __fmul2_rn(dpp, __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f)));
+            }
+            const float2 mul = pair(kCapped ? 1.f : p.scale_log2);
+            if constexpr (kBiased && kGeneral) {
+              const float d = static_cast<float>(q0 - key);
+              x = __ffma2_rn(x, mul, make_float2(-slope2 * fabsf(d + static_cast<float>(c)),
+                                                 -slope2 * fabsf(d + static_cast<float>(c + 1))));
+            } else if constexpr (kBiased) {
+              if (c > 0)
+                off = c % 8 == 0 ? make_float2(fmaf(-slope2, static_cast<float>(c), off0), fmaf(-slope2, static_cast<float>(c + 1), off0))
+                                 : __fadd2_rn(off, pair(-2.f * slope2));
+              x = __ffma2_rn(x, mul, off);
+            } else if constexpr (!kCapped) {
+              x = __fmul2_rn(x, mul);
+            }
+            float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            if (kMasked) pp = make_float2(vis & (1u << c) ? pp.x : 0.f, vis & (2u << c) ? pp.y : 0.f);
+            const float2 ds = __fmul2_rn(pp, dpp);
+            ppk[c / 2] = pack_bf16x2(pp.x, pp.y);
+            dpk[c / 2] = pack_bf16x2(ds.x, ds.y);
+          }
+        }
+        tmem_st16(trow + C::col_pdq(b) + 16 * g, ppk);
+        tmem_st16(trow + C::col_pdq(b) + 32 + 16 * g, dpk);
+        // dS row into shared memory, 128-byte swizzle: chunk ch holds queries 8ch..8ch+7.
+        uint8_t* ds_row = sDs + b * C::kDsBytes + row * 128;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          const int ch = g * 4 + c4;
+          *reinterpret_cast<uint4*>(ds_row + ((ch ^ (row & 7)) * 16)) =
+              make_uint4(dpk[4 * c4], dpk[4 * c4 + 1], dpk[4 * c4 + 2], dpk[4 * c4 + 3]);
+        }
+      };
+      if (general) step(std::true_type{}, std::true_type{});
+      else if (need_mask) step(std::true_type{}, std::false_type{});
+      else step(std::false_type{}, std::false_type{});
       tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -418,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++i == st.i0 + st.nq) {
         i = st.i0;
         ++head;
-        if (biased && head < p.group) slope2 = __ldg(p.slopes + h0 + head) * kLog2e;
+        if (kBiased && head < p.group) slope2 = __ldg(p.slopes + h0 + head) * kLog2e;
       }
     }
     // ------------------------------- dK, dV epilogue (warpgroup 0: dV, 1: dK)
@@ -532,7 +509,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   p.nkb = (a.N + kBkB - 1) / kBkB;
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
-  if (MODE == 2) {
+  if (MODE >= 2) {
     p.cap_in = 4.f * a.scale / sc.softcap;
     p.cap_out = sc.softcap * kLog2e;
     p.poly = cap_poly(1.f);
@@ -561,7 +538,7 @@ cudaError_t launch_mode(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
 
 template <int D>
 cudaError_t launch_d(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  if (sc.softcap > 0.f) return launch_mode<D, 2>(a, sc, stream);
+  if (sc.softcap > 0.f) return sc.slopes ? launch_mode<D, 3>(a, sc, stream) : launch_mode<D, 2>(a, sc, stream);
   return sc.slopes ? launch_mode<D, 1>(a, sc, stream) : launch_mode<D, 0>(a, sc, stream);
 }
 
