@@ -657,6 +657,20 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           }
           tmem_st_wait();
         }
+        if (MODE != 4 && need_mask) {  // in TMEM as well: -inf stays -inf below (its factor is positive)
+#pragma unroll 1
+          for (int c = 0; c < kBlockK; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(trow + col_s + c, x);
+            tmem_ld_wait32(x);
+            const uint32_t vis = bits_between(see.x - kbase - c, see.y - kbase - c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(vis & (1u << i))) x[i] = __float_as_uint(-INFINITY);
+            tmem_st32(trow + col_s + c, x);
+          }
+          tmem_st_wait();
+        }
         uint32_t r[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             r[c][i] = __float_as_uint(y.x);
             r[c][i + 1] = __float_as_uint(y.y);
           }
-          if (need_mask) {
+          if (MODE == 4 && need_mask) {
             const uint32_t vis = bits_between(see.x - kbase - c * 32, see.y - kbase - c * 32);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
