@@ -676,45 +676,41 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(trow + col_s + c * 32, r[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait32(r[c]);
-        // r becomes the score minus the reference, in log2 units: r mul + base, or r (polynomial) + bias,
-        // with the identity where the loop above has made the scores.  On the row's left the bias of
-        // the block's first key is left to add; its growth from there is in S (MODE 1).
+        // The score less the reference, in log2 units, is r mul + base.  On the row's left, base has the
+        // bias of the block's first key; its growth from there is in S (MODE 1).
         const float first = slope2 * static_cast<float>(kbase - qrow);
-        const float mul = pre ? 1.f : MODE == 4 ? p.cap_in : p.scale_log2;
-        const float base = pre || MODE == 0 ? -m_used : first - m_used;
-        CapPoly poly = p.poly;
-        if (MODE == 4 && pre) {
-          poly.c[0] = pair(1.f);
-          poly.c[1] = poly.c[2] = poly.c[3] = pair(0.f);
-        }
+        const float mul = MODE == 4 || pre ? 1.f : p.scale_log2;
+        float base = MODE == 0 || MODE == 4 || pre ? -m_used : first - m_used;
+        if constexpr (MODE == 4) {  // the cap and the bias, in place; the identity where `pre` has made the scores
+          CapPoly poly = p.poly;
+          if (pre) {
+            poly.c[0] = pair(1.f);
+            poly.c[1] = poly.c[2] = poly.c[3] = pair(0.f);
+          }
+          const float in = pre ? 1.f : p.cap_in, step = pre ? 0.f : slope2;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float2 off = pair(base);
-          const float step = MODE == 4 && !pre ? slope2 : 0.f, off0 = fmaf(step, 32.f * c, base);
+          for (int c = 0; c < 4; ++c) {
+            // step more for every key: four steps are added up, then the sum starts afresh.
+            const float off0 = pre ? 0.f : fmaf(step, 32.f * c, first);
+            float2 off = pair(off0);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 s = make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-            float2 y;
-            if constexpr (MODE == 4) {
-              // step more for every key: four steps are added up, then the sum starts afresh.
+            for (int i = 0; i < 32; i += 2) {
               off = i % 8 == 0 ? make_float2(fmaf(step, static_cast<float>(i), off0), fmaf(step, static_cast<float>(i + 1), off0))
                                : __fadd2_rn(off, pair(2.f * step));
-              const float2 x = __fmul2_rn(s, pair(mul));
-              y = __ffma2_rn(x, tanh_over_x(x, poly), off);
-            } else {
-              y = __ffma2_rn(s, pair(mul), off);
+              const float2 x = __fmul2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), pair(in));
+              const float2 y = __ffma2_rn(x, tanh_over_x(x, poly), off);
+              r[c][i] = __float_as_uint(y.x);
+              r[c][i + 1] = __float_as_uint(y.y);
             }
-            r[c][i] = __float_as_uint(y.x);
-            r[c][i + 1] = __float_as_uint(y.y);
-          }
-          if (MODE == 4 && need_mask) {
-            const uint32_t vis = bits_between(see.x - kbase - c * 32, see.y - kbase - c * 32);
+            if (need_mask) {
+              const uint32_t vis = bits_between(see.x - kbase - c * 32, see.y - kbase - c * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
+              for (int i = 0; i < 32; ++i)
+                if (!(vis & (1u << i))) r[c][i] = __float_as_uint(-INFINITY);
+            }
           }
         }
-        // P = exp2(r), packed bf16 over the S columns.  The row's reference is its first block's
+        // P = exp2(r mul + base), packed bf16 over the S columns.  The row's reference is its first block's
         // maximum.  Later blocks are first taken against the reference as it is, and taken again
         // against their own maximum if a P may have overflowed, or if they hold the row's first
         // visible keys.  A bias that falls with distance makes the maxima grow while the blocks lie
@@ -734,7 +730,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
               mc[c] = fmaxf(max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), max3(a[6], a[7], a[8])),
                             fmaxf(a[9], a[10]));
             }
-            const float mt = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
+            const float mt = fmaf(fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])), mul, base);  // mul > 0
             // The reference moves by mt where that is up, or the row's first.
             const bool first = !seen && mt > -INFINITY;
             const bool up = first || (seen && mt > 0.f);
@@ -744,15 +740,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             m_used += delta;
             seen = seen || first;
             l *= alpha;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = __fadd2_rn(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])),
-                                            pair(-delta));
-                r[c][i] = __float_as_uint(y.x);
-                r[c][i + 1] = __float_as_uint(y.y);
-              }
+            base -= delta;
             // O_t holds P V of the earlier blocks (Q K^T of this block was issued after them).
             if (j > 0 && __any_sync(0xffffffffu, scale_o)) {
 #pragma unroll 1
@@ -771,8 +759,9 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 e = make_float2(ex2_approx(__uint_as_float(r[c][2 * i])),
-                                           ex2_approx(__uint_as_float(r[c][2 * i + 1])));
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])),
+                                          pair(mul), pair(base));
+              const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
               part = __fadd2_rn(part, e);
               pk[i] = pack_bf16x2(e.x, e.y);
             }
