@@ -95,10 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hk = bhk % p.Hkv, b_idx = bhk / p.Hkv;
   const int h0 = hk * p.group;               // first query head of the group
   const int bh0 = b_idx * p.H + h0;
-  const Steps st = steps_of(p, kb, b_idx);
-  const int n = st.n;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kWarpLoad * 32) {
     mbar_init(bar_kv, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar_full[s], 1);
@@ -116,7 +114,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_drain, kSplitSdp ? 3 : 2);
     *abort_flag = 0;
     fence_mbar_init();
+    // K and V start at once, while the intervals are read and TMEM is allocated.
+    mbar_arrive_expect_tx(bar_kv, 2 * C::kKVTile);
+    for (int c = 0; c < C::kBoxes; ++c) {
+      tma_load_4d(sK + c * C::kKVBox, &tm_k, bar_kv, c * 64, kb * kBkB, hk, b_idx);
+      tma_load_4d(sV + c * C::kKVBox, &tm_v, bar_kv, c * 64, kb * kBkB, hk, b_idx);
+    }
   }
+  const Steps st = steps_of(p, kb, b_idx);
+  const int n = st.n;
   if constexpr (D == 64) {
     // Rows 64..127 of the dQ^T MMA's A operand: zeros, read by the tensor core.
     uint4* z = reinterpret_cast<uint4*>(smem + C::kZeroOff);
@@ -150,12 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_decrease<kRegsControl>();
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
-      if (lane == 0 && n > 0) {
-        mbar_arrive_expect_tx(bar_kv, 2 * C::kKVTile);
-        for (int c = 0; c < C::kBoxes; ++c) {
-          tma_load_4d(sK + c * C::kKVBox, &tm_k, bar_kv, c * 64, kb * kBkB, hk, b_idx);
-          tma_load_4d(sV + c * C::kKVBox, &tm_v, bar_kv, c * 64, kb * kBkB, hk, b_idx);
-        }
+      if (lane == 0) {
         int issued = 0, g = 0, i = st.i0;
         for (int it = 0; it < n; ++it) {
           const int slot = it % kStages;
@@ -399,13 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ------------------------------- dK, dV epilogue (warpgroup 0: dV, 1: dK)
-    if (ok && n > 0) ok = warp_wait_b(bar_dkv, 0, wc, kSiteBEpi);
+    // (A block that no query sees only waits for K and V to land where its zeros go.)
+    if (ok) ok = warp_wait_b(n > 0 ? bar_dkv : bar_kv, 0, wc, kSiteBEpi);
     if (ok) {
       tc_fence_after();
       if (n > 0) {
         if (g == 0) stage_row_bf16<D>(trow + C::kColDV, sV, row, 1.f);
         else stage_row_bf16<D>(trow + C::kColDK, sK, row, p.scale);
-      } else {  // no query sees the block: zeros (nothing was loaded into sV, sK)
+      } else {  // no query sees the block: zeros
         uint8_t* box = (g == 0 ? sV : sK) + row * 128;
         for (int c = 0; c < C::kBoxes; ++c)
           for (int q4 = 0; q4 < 8; ++q4)
