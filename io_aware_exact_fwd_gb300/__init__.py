@@ -7,7 +7,9 @@ tensors, passes their device pointers and the current CUDA stream, and raises
 kernels; there is no fallback.  If libfa.so is missing, importing the binding
 still works but every call raises, so a missing build is never silent.
 
-PyTorch is used only as device-memory and stream plumbing.
+PyTorch is used only as device-memory and stream plumbing.  Most calls marshal with
+ctypes; those of scored attention and of the paged cache, made once a layer and token,
+with a small compiled module (csrc/fa_torch.cpp).
 """
 
 from __future__ import annotations
@@ -16,7 +18,7 @@ import ctypes
 import os
 
 __all__ = [
-    "FAError", "load_library", "library_path", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_noalloc",
+    "FAError", "load_library", "load_binding", "library_path", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_noalloc",
     "fa_bwd_noalloc_max_workspace", "fa_bwd_prep", "fa_bwd_main", "fa_bwd_dq", "fa_fp8_workspace_size",
     "fa_fp8_workspace_offsets", "fa_fp8_prepare", "fa_fp8_prepare_seeded", "fa_fp8_rotation_signs", "fa_fwd_fp8",
     "fa_mask_plan_size", "fa_mask_plan", "fa_fwd_scored", "fa_bwd_scored_workspace_size", "fa_bwd_scored",
@@ -29,7 +31,9 @@ __all__ = [
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "lib", "libfa.so")
+_TORCH_PATH = os.path.join(_PKG, "lib", "_fa_torch.so")
 _lib = None
+_torch_binding = None
 
 STATUS = {
     0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_ERR_MISALIGNED",
@@ -619,80 +623,31 @@ def fa_fwd_splitkv(q, k, v, o=None, lse=None, workspace=None, n_split: int = 0, 
     return o, lse
 
 
-# The calls of scored attention and of the paged cache are made once a layer and token, so their
-# checks are written to cost little: one attribute read where one will do, ints instead of device
-# objects, no ctypes object where an int or None passes.
+def load_binding():
+    """The compiled binding (loaded once).  Raises if it has not been built."""
+    global _torch_binding
+    if _torch_binding is None:
+        import importlib.machinery
+        import importlib.util
 
-_Int64x2, _Int64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+        import torch  # noqa: F401  (its libraries have to be loaded first)
 
-
-def _layout(name, t, shape, dtype, index):
-    """(address, strides) of a tensor in any layout whose last dimension is contiguous, on GPU `index`.
-
-    strides is None when the tensor is dense, else its strides from the second-to-last
-    dimension outwards (dimensions of one element, whose stride means nothing, count as
-    dense)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    if t.is_contiguous():
-        return t.data_ptr(), None
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    if 1 in shape:
-        out, dense = [], shape[-1]
-        for n, x in zip(reversed(shape[:-1]), reversed(st[:-1])):
-            out.append(x if n != 1 else dense)
-            dense *= n
-        st = (*reversed(out), 1)
-    if len(st) == 4:
-        return t.data_ptr(), _Int64x3(st[2], st[1], st[0])
-    return t.data_ptr(), _Int64x2(st[1], st[0])
+        load_library()
+        if not os.path.exists(_TORCH_PATH):
+            raise RuntimeError(
+                f"{_TORCH_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_fa_torch", _TORCH_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fa_torch", loader))
+        loader.exec_module(module)
+        _torch_binding = module
+    return _torch_binding
 
 
-def _flat(name, t, shape, dtype, index):
-    """The address of a dense tensor on GPU `index` (None: 0)."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
-    return t.data_ptr()
-
-
-def _bytes(name, t, index):
-    """(address, bytes) of a plan or workspace: a dense tensor on GPU `index`."""
-    if t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on cuda:{index}")
-    return t.data_ptr(), t.nbytes
-
-
-def _gpu(name, t, dtypes):
-    """The GPU index of a tensor of one of `dtypes`."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-    return index
-
-
-def _call(fn, where, index, stream, args):
-    """fn(*args, stream) with GPU `index` current, on `stream` or that GPU's current stream."""
-    from torch import _C
-
-    if _C._cuda_getDevice() != index:
-        import torch
-
-        with torch.cuda.device(index):
-            return _call(fn, where, index, stream, args)
-    # The raw handle of the current stream: building a Stream object for it costs more than the call.
-    st = fn(*args, _C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
-    if st != 0:
-        raise FAError(st, where)
+def _done(result, where: str):
+    """The outputs of a call of the compiled binding, or its refusal raised."""
+    if type(result) is int:
+        raise FAError(result, where)
+    return result
 
 
 def fa_mask_plan_size(B: int, N: int) -> int:
@@ -710,20 +665,12 @@ def fa_mask_plan(B: int, N: int, cu_docs=None, prefix=None, causal: bool = True,
     """
     import torch
 
-    lib = load_library()
-    ref = cu_docs if cu_docs is not None else prefix if prefix is not None else plan
-    if ref is None:
-        index = torch.device("cuda" if device is None else device).index
-        index = torch.cuda.current_device() if index is None else index
-    else:
-        index = _gpu("cu_docs, prefix or plan", ref, (torch.int32, torch.uint8))
-    n_docs = 1 if cu_docs is None else cu_docs.shape[1] - 1
-    pc = _flat("cu_docs", cu_docs, (B, n_docs + 1), torch.int32, index)
-    px = _flat("prefix", prefix, (B, n_docs), torch.int32, index)
     if plan is None:
-        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=f"cuda:{index}")
-    _call(lib.fa_mask_plan, "fa_mask_plan", index, stream,
-          (pc, px, n_docs, *_bytes("plan", plan, index), B, N, int(bool(causal))))
+        ref = cu_docs if cu_docs is not None else prefix
+        dev = ref.device if ref is not None else torch.device("cuda" if device is None else device)
+        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=dev)
+    _done(load_binding().mask_plan(B, N, cu_docs, prefix, causal, plan, None if stream is None else stream.cuda_stream),
+          "fa_mask_plan")
     return plan
 
 
@@ -737,26 +684,8 @@ def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float 
     |i - j|; the mask is `causal`, or a plan of fa_mask_plan (then leave causal
     False).  A row that sees no key gets o = 0 and lse = -inf.
     """
-    import torch
-
-    bf, f32 = torch.bfloat16, torch.float32
-    index, qs = _gpu("q", q, (bf,)), q.shape
-    B, H, N, d = qs
-    Hkv = k.shape[1]
-    ks = (B, Hkv, N, d)
-    pq, sq = _layout("q", q, qs, bf, index)
-    pk, sk = _layout("k", k, ks, bf, index)
-    pv, sv = _layout("v", v, ks, bf, index)
-    if o is None:
-        o = q.new_empty(qs)
-    if lse is None:
-        lse = q.new_empty((B, H, N), dtype=f32)
-    po, so = _layout("o", o, qs, bf, index)
-    pp, pb = (0, 0) if plan is None else _bytes("plan", plan, index)
-    _call(load_library().fa_fwd_scored, "fa_fwd_scored", index, stream,
-          (pq, sq, pk, sk, pv, sv, po, so, _flat("lse", lse, (B, H, N), f32, index), B, H, Hkv, N, d, pp, pb,
-           1 if causal else 0, d ** -0.5 if scale is None else scale, softcap, _flat("slopes", slopes, (H,), f32, index)))
-    return o, lse
+    return _done(load_binding().fwd_scored(q, k, v, o, lse, causal, scale, softcap, slopes, plan,
+                                    None if stream is None else stream.cuda_stream), "fa_fwd_scored")
 
 
 def fa_bwd_scored_workspace_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
@@ -773,44 +702,8 @@ def fa_bwd_scored(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None
     over the query heads that share a head.  ``deterministic=True`` gives dq the same
     bits on every run (dk and dv always have them).
     """
-    import torch
-
-    bf, f32 = torch.bfloat16, torch.float32
-    index, qs = _gpu("q", q, (bf,)), q.shape
-    B, H, N, d = qs
-    Hkv = k.shape[1]
-    ks = (B, Hkv, N, d)
-    dq = q.new_empty(qs) if dq is None else dq
-    dk = q.new_empty(ks) if dk is None else dk
-    dv = q.new_empty(ks) if dv is None else dv
-    if workspace is None:
-        workspace = q.new_empty(max(fa_bwd_scored_workspace_size(B, H, Hkv, N, d), 1), dtype=torch.uint8)
-    pp, pb = (0, 0) if plan is None else _bytes("plan", plan, index)
-    _call(load_library().fa_bwd_scored, "fa_bwd_scored", index, stream,
-          (*_layout("q", q, qs, bf, index), *_layout("k", k, ks, bf, index), *_layout("v", v, ks, bf, index),
-           *_layout("o", o, qs, bf, index), *_layout("do", do, qs, bf, index), _flat("lse", lse, (B, H, N), f32, index),
-           *_layout("dq", dq, qs, bf, index), *_layout("dk", dk, ks, bf, index), *_layout("dv", dv, ks, bf, index),
-           *_bytes("workspace", workspace, index), B, H, Hkv, N, d, pp, pb, 1 if causal else 0,
-           d ** -0.5 if scale is None else scale, softcap, _flat("slopes", slopes, (H,), f32, index),
-           1 if deterministic else 0))
-    return dq, dk, dv
-
-
-def _cache(k_cache, v_cache, page_table, seq_lens, index):
-    """The arguments that describe a paged cache, its shape (pages, heads, page size, d), sequences and table width."""
-    from torch import int32
-
-    shape, dt = k_cache.shape, k_cache.dtype
-    if len(shape) != 4 or page_table.dim() != 2:
-        raise ValueError("k_cache must be indexed [n_pages, Hkv, page_size, d], page_table [B, max_pages]")
-    B, width = page_table.shape
-    ts, row = page_table.stride()
-    if page_table.dtype is not int32 or page_table.get_device() != index or (width > 1 and row != 1):
-        raise ValueError(f"page_table must be an int32 tensor [B, max_pages] with contiguous rows on cuda:{index}")
-    pk, sk = _layout("k_cache", k_cache, shape, dt, index)
-    pv, sv = _layout("v_cache", v_cache, shape, dt, index)
-    return ((pk, sk, pv, sv, page_table.data_ptr(), ts if B > 1 or ts > width else width,
-             _flat("seq_lens", seq_lens, (B,), int32, index)), shape, B, width)
+    return _done(load_binding().bwd_scored(q, k, v, o, do, lse, dq, dk, dv, workspace, causal, scale, softcap, slopes, plan,
+                                    None if stream is None else stream.cuda_stream, deterministic), "fa_bwd_scored")
 
 
 def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream=None):
@@ -821,16 +714,8 @@ def fa_paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, stream
     [B, max_pages]; seq_lens: int32 [B], lengths with the new tokens; cu_new: int32
     [B + 1]: rows cu_new[b] .. cu_new[b + 1] - 1 are the last tokens of sequence b.
     """
-    import torch
-
-    dt = k_cache.dtype
-    index = _gpu("k_cache", k_cache, (torch.bfloat16, torch.float16))
-    cache, (n_pages, Hkv, page, d), B, width = _cache(k_cache, v_cache, page_table, seq_lens, index)
-    T = k.shape[0]
-    _call(load_library().fa_paged_append, "fa_paged_append", index, stream,
-          (*_layout("k", k, (T, Hkv, d), dt, index), *_layout("v", v, (T, Hkv, d), dt, index), *cache,
-           _flat("cu_new", cu_new, (B + 1,), torch.int32, index), B, T, Hkv, d, page, n_pages, width,
-           1 if dt is torch.bfloat16 else 2))
+    _done(load_binding().paged_append(k, v, k_cache, v_cache, page_table, seq_lens, cu_new,
+                               None if stream is None else stream.cuda_stream), "fa_paged_append")
 
 
 def fa_paged_decode_workspace_size(B: int, H: int, Hkv: int, d: int) -> int:
@@ -846,29 +731,8 @@ def fa_paged_decode(q, k_cache, v_cache, page_table, seq_lens, o=None, lse=None,
     token's own key and value are in the cache and counted in seq_lens.  softcap and
     slopes as fa_fwd_scored.  An empty sequence gets o = 0 and lse = -inf.
     """
-    import torch
-
-    dt, f32, qs = k_cache.dtype, torch.float32, q.shape
-    index = _gpu("k_cache", k_cache, (torch.bfloat16, torch.float16))
-    B, H, d = qs
-    cache, (n_pages, Hkv, page, dc), Bt, width = _cache(k_cache, v_cache, page_table, seq_lens, index)
-    if Bt != B or dc != d:
-        raise ValueError(f"q is for {B} sequences of head dim {d}, the page table for {Bt} and the cache for {dc}")
-    pq, sq = _layout("q", q, qs, dt, index)
-    if o is None:
-        o = q.new_empty(qs)
-    if lse is None:
-        lse = q.new_empty((B, H), dtype=f32)
-    po, so = _layout("o", o, qs, dt, index)
-    if workspace is None:
-        with torch.cuda.device(index):
-            need = fa_paged_decode_workspace_size(B, H, Hkv, d)
-        workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
-    _call(load_library().fa_paged_decode, "fa_paged_decode", index, stream,
-          (pq, sq, *cache, po, so, _flat("lse", lse, (B, H), f32, index), *_bytes("workspace", workspace, index), B, H,
-           Hkv, d, page, n_pages, width, 1 if dt is torch.bfloat16 else 2, d ** -0.5 if scale is None else scale, softcap,
-           _flat("slopes", slopes, (H,), f32, index)))
-    return o, lse
+    return _done(load_binding().paged_decode(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, scale, softcap, slopes,
+                                      None if stream is None else stream.cuda_stream), "fa_paged_decode")
 
 
 def fa_w4a16_workspace_size(M: int, N: int, K: int, n_split: int) -> int:
