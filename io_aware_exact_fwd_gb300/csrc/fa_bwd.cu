@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
                                                              unsigned int* __restrict__ dq_bmax, int N, int Npad,
                                                              long long rows_pad, int H, Strides so, Strides sdo,
                                                              int raw_lse) {
+  grid_release();                      // the main kernel's blocks may set themselves up meanwhile
   constexpr int kTpr = D / 8;          // threads per row
   constexpr int kRpb = 256 / kTpr;     // rows per block: 16 (d=128) or 32 (d=64)
   const long long r = static_cast<long long>(blockIdx.x) * kRpb + (threadIdx.x / kTpr);
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
                                                              int group, Strides sdq) {
   const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (idx >= n8) return;
+  grid_wait();
   float4 a = reinterpret_cast<const float4*>(dq_acc)[2 * idx];
   float4 b = reinterpret_cast<const float4*>(dq_acc)[2 * idx + 1];
   const long long row = idx * 8 / D;  // (bh, query row) flattened
@@ -696,9 +698,14 @@ cudaError_t launch_bwd_dq_d(const BwdArgs& a, cudaStream_t stream) {
   const float* dq_acc = reinterpret_cast<const float*>(ws + w.off_dq);
   const long long n8 = static_cast<long long>(a.B) * a.H * a.N * D / 8;
   auto kern = a.deterministic ? bwd_dq_convert_kernel<D, true> : bwd_dq_convert_kernel<D, false>;
-  kern<<<static_cast<unsigned>((n8 + 255) / 256), 256, 0, stream>>>(
-      dq_acc, static_cast<__nv_bfloat16*>(a.dq), a.scale, n8, reinterpret_cast<const float*>(ws + w.off_dqmax),
-      reinterpret_cast<const float*>(ws + w.off_kvmax), a.N, w.npad, a.H, a.group, a.sdq);
+  const unsigned grid = static_cast<unsigned>((n8 + 255) / 256);
+  const float* dq_bmax = reinterpret_cast<const float*>(ws + w.off_dqmax);
+  const float* kv_max = reinterpret_cast<const float*>(ws + w.off_kvmax);
+  __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(a.dq);
+  if (a.dependent)
+    return launch_dependent(kern, grid, 256, 0, stream, dq_acc, dq, a.scale, n8, dq_bmax, kv_max, a.N, w.npad, a.H,
+                            a.group, a.sdq);
+  kern<<<grid, 256, 0, stream>>>(dq_acc, dq, a.scale, n8, dq_bmax, kv_max, a.N, w.npad, a.H, a.group, a.sdq);
   return cudaGetLastError();
 }
 

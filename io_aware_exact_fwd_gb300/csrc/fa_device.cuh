@@ -443,6 +443,14 @@ __device__ __forceinline__ void regs_decrease() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// ------------------------------------------------------- dependent launches --
+
+// The next kernel of the stream, if launched as a dependent (launch_dependent), may start
+// once every block of this one has said so or ended; it waits with grid_wait for this
+// one's writes.  Neither does anything otherwise.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // --------------------------------------------------- cluster launch control --
 
 // Ask for a block of this grid that has not started: the 16-byte answer lands in `dst`

@@ -119,6 +119,7 @@ struct BwdArgs {
   DebugKnobs dbg;
   int group = 1;      // query heads that share a key/value head (scored attention)
   int raw_lse = 0;    // 1: LSE * log2(e) per query as fp32 instead of operand tiles (scored attention with a cap)
+  int dependent = 0;  // 1: the dQ conversion is launched as a dependent of the main kernel
   const int2* seen_by = nullptr;  // [B, N] queries that see each key, or NULL (every key counts)
 };
 
@@ -292,6 +293,24 @@ struct PagedDecodeArgs {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream);
 size_t paged_decode_workspace(int B, int H, int Hkv, int d);
+
+// kern<<<grid, block, smem, stream>>>(args...) that may start before the stream's previous
+// kernel has ended; the kernel waits for it (grid_wait, fa_device.cuh).
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                             const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes, int cols,
                          int rows, int heads, int batch, const int64_t strides[3], int box_cols, int box_rows,

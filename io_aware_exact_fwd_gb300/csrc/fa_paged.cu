@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
     *reinterpret_cast<long long*>(s_start + 2) = w0 - before;
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (w0 >= total) return;
   Place<kTile> at;
   at.b = s_start[0];
@@ -571,7 +571,7 @@ template <int D, bool FP16>
 __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_part) {
   __shared__ float2 s_ml[4];
   __shared__ __align__(16) float s_o[4][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  grid_wait();  // the parts are written
   const int b = blockIdx.x / p.H, head = blockIdx.x % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = D / 32;
@@ -684,17 +684,8 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
   kern<<<static_cast<unsigned>(decode_ctas(p.group)), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
-  // The join starts while the decode drains and waits for it (griddepcontrol).
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, FP16>, p, C::kRows);
+  return launch_dependent(decode_join_kernel<D, FP16>, static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H), 128, 0,
+                          stream, p, C::kRows);
 }
 
 template <int D, bool FP16>

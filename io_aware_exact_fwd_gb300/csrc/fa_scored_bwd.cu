@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
+  grid_release();
+  grid_wait();  // the preprocess has written LSE and D and zeroed the dQ accumulator
   const size_t head_blocks = static_cast<size_t>(p.Npad / kBqB);
 
   if (warp >= kWarpCtl) {
@@ -529,8 +531,8 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   cudaFuncAttributes fattr;
   if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
   if (static_cast<uint32_t>(fattr.numRegs) < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kern<<<static_cast<unsigned>(p.nkb * a.B * sc.Hkv), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, p);
-  return cudaGetLastError();
+  return launch_dependent(kern, static_cast<unsigned>(p.nkb * a.B * sc.Hkv), kThreads, C::kSmemBytes, stream, tq, tk, tv,
+                          tdo, tdk, tdv, p);
 }
 
 template <int D, int MODE>
@@ -551,6 +553,7 @@ cudaError_t launch_bwd_scored(const BwdArgs& args, const ScoreArgs& sc, cudaStre
   a.group = a.H / sc.Hkv;
   a.raw_lse = sc.softcap > 0.f;
   a.seen_by = sc.plan.k;
+  a.dependent = 1;
   cudaError_t e;
   if ((e = launch_bwd_prep(a, stream))) return e;
   if ((e = a.d == 64 ? launch_d<64>(a, sc, stream) : launch_d<128>(a, sc, stream))) return e;
