@@ -17,18 +17,33 @@ __device__ __forceinline__ int tokens_of(const PagedCache& c, int b) {
   return min(max(c.seq_lens[b], 0), c.max_pages * c.page_size);
 }
 
-// Append: one row of d values of K and of V per d / 8 lanes, 16 bytes each.  A row's
-// sequence is found by a binary search in cu_new.
-__global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, long long chunks) {
-  const int per_row = a.c.d / 8;
-  const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (x >= chunks) return;
-  const int col = static_cast<int>(x % per_row) * 8;
-  const int h = static_cast<int>(x / per_row % a.c.Hkv), t = static_cast<int>(x / per_row / a.c.Hkv);
+// Append: one warp a new token, 16 bytes a lane, up to four pieces of K and of V a lane in
+// flight while the token's sequence, position and page are looked up, once a warp.  Bound
+// by HBM: the new rows are read once and written once.  Measured with 8 heads x 128: 35k
+// tokens in 45.6 us, 6.3 TB/s; 64 tokens in 4.1 us, a launch and three dependent loads.
+// (One 16-byte piece a thread, each with its own look-up: 49.1 us.)
+__global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a) {
+  const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const uint16_t* ks = static_cast<const uint16_t*>(a.k) + t * a.sk.s[1];
+  const uint16_t* vs = static_cast<const uint16_t*>(a.v) + t * a.sv.s[1];
+  const int shift = a.c.d == 64 ? 3 : 4, pieces = a.c.Hkv << shift;  // a head's row is 8 or 16 pieces
+  uint4 kv[4], vv[4];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = p0 + 32 * i, h = x >> shift, col = (x & ((1 << shift) - 1)) * 8;
+      if (x < pieces) {
+        kv[i] = *reinterpret_cast<const uint4*>(ks + h * a.sk.s[0] + col);
+        vv[i] = *reinterpret_cast<const uint4*>(vs + h * a.sv.s[0] + col);
+      }
+    }
+  };
+  load(lane);  // in flight while the place is looked up
   int lo = 0, hi = a.c.B + 1;  // the number of offsets <= t
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (a.cu_new[mid] <= t) lo = mid + 1;
+    if (__ldg(a.cu_new + mid) <= t) lo = mid + 1;
     else hi = mid;
   }
   if (lo == 0 || lo == a.c.B + 1) return;  // a row of no sequence
@@ -38,10 +53,19 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, lo
   const int at = static_cast<int>(pos) / a.c.page_size, off = static_cast<int>(pos) % a.c.page_size;
   const int page = a.c.page_table[b * a.c.table_stride + at];
   if (page < 0 || page >= a.c.n_pages) return;
-  const uint4 kv = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + t * a.sk.s[1] + h * a.sk.s[0] + col);
-  const uint4 vv = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + t * a.sv.s[1] + h * a.sv.s[0] + col);
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + page * a.c.sk.s[2] + h * a.c.sk.s[1] + off * a.c.sk.s[0] + col) = kv;
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + page * a.c.sv.s[2] + h * a.c.sv.s[1] + off * a.c.sv.s[0] + col) = vv;
+  uint16_t* kd = static_cast<uint16_t*>(a.c.k) + page * a.c.sk.s[2] + off * a.c.sk.s[0];
+  uint16_t* vd = static_cast<uint16_t*>(a.c.v) + page * a.c.sv.s[2] + off * a.c.sv.s[0];
+  for (int p0 = lane; p0 < pieces; p0 += 128) {
+    if (p0 != lane) load(p0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = p0 + 32 * i, h = x >> shift, col = (x & ((1 << shift) - 1)) * 8;
+      if (x < pieces) {
+        *reinterpret_cast<uint4*>(kd + h * a.c.sk.s[1] + col) = kv[i];
+        *reinterpret_cast<uint4*>(vd + h * a.c.sv.s[1] + col) = vv[i];
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------
@@ -67,7 +91,6 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a, lo
 // of their rate is used, and a tcgen05 tile of 128 rows would waste more.
 constexpr int kConsumers = 4;     // consumer warps
 constexpr int kDecThreads = 32 * (kConsumers + 1);
-constexpr int kMinShare = 2;      // tiles per CTA at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -212,8 +235,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   }
   before -= mine;
   const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
-  long long share = (total + G - 1) / G;
-  if (share < kMinShare) share = kMinShare;
+  const long long share = (total + G - 1) / G;  // down to one tile: a block's tile costs more than its join
   const long long w0 = cta * share, w1 = min(w0 + share, total);
   const long long after = before + mine;
   if (cta == 0) {  // for the join
@@ -696,8 +718,7 @@ cudaError_t launch_decode_mt(const PagedDecodeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  const long long chunks = static_cast<long long>(a.T) * a.c.Hkv * (a.c.d / 8);
-  paged_append_kernel<<<static_cast<unsigned>((chunks + 255) / 256), 256, 0, stream>>>(a, chunks);
+  paged_append_kernel<<<static_cast<unsigned>((static_cast<long long>(a.T) + 3) / 4), 128, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
