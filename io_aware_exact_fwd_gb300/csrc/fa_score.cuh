@@ -9,13 +9,15 @@
 
 namespace fa {
 
-// The interval of keys that query i sees, and of queries that see key j.
+// The interval of keys that query i sees, and of queries that see key j.  Clamped to the
+// row: a plan made for longer rows gives a wrong mask, but no position outside the tensors.
+__device__ __forceinline__ int2 in_row(int2 x, int N) { return make_int2(min(max(x.x, 0), N), min(max(x.y, 0), N)); }
 __device__ __forceinline__ int2 keys_of(const MaskPlan& p, int causal, int b, int i, int N) {
-  if (p.q) return __ldg(p.q + static_cast<size_t>(b) * N + i);
+  if (p.q) return in_row(__ldg(p.q + static_cast<size_t>(b) * N + i), N);
   return make_int2(0, causal ? i + 1 : N);
 }
 __device__ __forceinline__ int2 queries_of(const MaskPlan& p, int causal, int b, int j, int N) {
-  if (p.k) return __ldg(p.k + static_cast<size_t>(b) * N + j);
+  if (p.k) return in_row(__ldg(p.k + static_cast<size_t>(b) * N + j), N);
   return make_int2(causal ? j : 0, N);
 }
 

@@ -367,7 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             if (kMasked) pp = make_float2(vis & (1u << c) ? pp.x : 0.f, vis & (2u << c) ? pp.y : 0.f);
-            const float2 ds = __fmul2_rn(pp, dpp);
+            float2 ds = __fmul2_rn(pp, dpp);
+            // (dP of a masked pair may have overflowed.)
+            if (kMasked) ds = make_float2(vis & (1u << c) ? ds.x : 0.f, vis & (2u << c) ? ds.y : 0.f);
             ppk[c / 2] = pack_bf16x2(pp.x, pp.y);
             dpk[c / 2] = pack_bf16x2(ds.x, ds.y);
           }

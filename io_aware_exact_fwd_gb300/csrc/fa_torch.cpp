@@ -106,7 +106,11 @@ float number(PyObject* x) {
   return static_cast<float>(v);
 }
 float scale_of(PyObject* x, int64_t d) { return x == Py_None ? static_cast<float>(std::pow(d, -0.5)) : number(x); }
-int truth(PyObject* x) { return PyObject_IsTrue(x) == 1; }
+int truth(PyObject* x) {
+  const int t = PyObject_IsTrue(x);
+  if (t < 0) throw python_error();
+  return t;
+}
 
 // The caller's stream (its handle), or the GPU's current one.
 fa_stream_t stream_of(PyObject* x, int gpu) {
@@ -118,11 +122,19 @@ fa_stream_t stream_of(PyObject* x, int gpu) {
 
 // The sizes the library takes as int.
 int whole(int64_t n, const char* name) {
-  if (n > INT32_MAX) unfit(PyExc_ValueError, c10::str(name, " is too large: ", n));
+  if (n > INT32_MAX || n < INT32_MIN) unfit(PyExc_ValueError, c10::str(name, " is too large: ", n));
   return static_cast<int>(n);
 }
 
-// fn() with the GPU current and the interpreter's lock released.
+// A workspace the caller did not give.  It is let go when the call returns, so it comes from
+// the memory of the stream that uses it: what that stream gets it for next runs after the call.
+Tensor scratch(size_t n, const Tensor& like, fa_stream_t stream, int gpu) {
+  c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream),
+                                                                    static_cast<c10::DeviceIndex>(gpu)));
+  return at::empty({static_cast<int64_t>(n)}, like.options().dtype(at::kByte));
+}
+
+// fn() with the GPU current, and without the interpreter's lock (nothing in fn may throw).
 template <class F>
 int call(int gpu, F fn) {
   c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(gpu));
@@ -166,10 +178,9 @@ PyObject* mask_plan(PyObject* const* a) {
   const int32_t* cu = flat<const int32_t>(a[2], "cu_docs", at::kInt, {B, docs + 1}, gpu);
   const int32_t* prefix = flat<const int32_t>(a[3], "prefix", at::kInt, {B, docs}, gpu);
   const Bytes p = bytes(a[5], "plan", gpu);
+  const int t = whole(docs, "cu_docs"), b = whole(B, "B"), n = whole(N, "N"), causal = truth(a[4]);
   const fa_stream_t s = stream_of(a[6], gpu);
-  const int st = call(gpu, [&] {
-    return fa_mask_plan(cu, prefix, whole(docs, "cu_docs"), p.p, p.n, whole(B, "B"), whole(N, "N"), truth(a[4]), s);
-  });
+  const int st = call(gpu, [&] { return fa_mask_plan(cu, prefix, t, p.p, p.n, b, n, causal, s); });
   if (st) return PyLong_FromLong(st);
   Py_RETURN_NONE;
 }
@@ -193,11 +204,12 @@ PyObject* fwd_scored(PyObject* const* a) {
   const float* slopes = flat<const float>(a[8], "slopes", at::kFloat, {H}, gpu);
   const Bytes plan = bytes(a[9], "plan", gpu);
   const float scale = scale_of(a[6], d), cap = number(a[7]);
-  const int causal = truth(a[5]), b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N");
+  const int causal = truth(a[5]), b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N"),
+            dim = whole(d, "d");
   const fa_stream_t s = stream_of(a[10], gpu);
   const int st = call(gpu, [&] {
     return fa_fwd_scored(lq.p, lq.strides(), lk.p, lk.strides(), lv.p, lv.strides(), lo.p, lo.strides(),
-                         static_cast<float*>(lse.data_ptr()), b, h, hkv, n, static_cast<int>(d), plan.p, plan.n, causal,
+                         static_cast<float*>(lse.data_ptr()), b, h, hkv, n, dim, plan.p, plan.n, causal,
                          scale, cap, slopes, s);
   });
   return st ? PyLong_FromLong(st) : tuple_of({o, lse});
@@ -222,23 +234,23 @@ PyObject* bwd_scored(PyObject* const* a) {
                dv = given_or_new(a[8], "dv", ks, q, type);
   const Layout ldq = layout(dq, "dq", type, qs, gpu), ldk = layout(dk, "dk", type, ks, gpu),
                ldv = layout(dv, "dv", type, ks, gpu);
-  const int b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N");
+  const int b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N"), dim = whole(d, "d");
+  const fa_stream_t s = stream_of(a[15], gpu);
   Tensor own;
   Bytes ws = bytes(a[9], "workspace", gpu);
   if (a[9] == Py_None) {
-    ws.n = fa_bwd_scored_workspace_size(b, h, hkv, n, static_cast<int>(d));
-    own = at::empty({static_cast<int64_t>(ws.n)}, q.options().dtype(at::kByte));
+    ws.n = fa_bwd_scored_workspace_size(b, h, hkv, n, dim);
+    own = scratch(ws.n, q, s, gpu);
     ws.p = own.data_ptr();
   }
   const float* slopes = flat<const float>(a[13], "slopes", at::kFloat, {H}, gpu);
   const Bytes plan = bytes(a[14], "plan", gpu);
   const float scale = scale_of(a[11], d), cap = number(a[12]);
   const int causal = truth(a[10]), deterministic = truth(a[16]);
-  const fa_stream_t s = stream_of(a[15], gpu);
   const int st = call(gpu, [&] {
     return fa_bwd_scored(lq.p, lq.strides(), lk.p, lk.strides(), lv.p, lv.strides(), lo.p, lo.strides(), lg.p,
                          lg.strides(), lse, ldq.p, ldq.strides(), ldk.p, ldk.strides(), ldv.p, ldv.strides(), ws.p, ws.n,
-                         b, h, hkv, n, static_cast<int>(d), plan.p, plan.n, causal, scale, cap, slopes, deterministic, s);
+                         b, h, hkv, n, dim, plan.p, plan.n, causal, scale, cap, slopes, deterministic, s);
   });
   return st ? PyLong_FromLong(st) : tuple_of({dq, dk, dv});
 }
@@ -311,17 +323,17 @@ PyObject* paged_decode(PyObject* const* a) {
   check(lse, "lse", at::kFloat, {c.B, H}, c.gpu);
   if (!lse.is_contiguous()) unfit(PyExc_ValueError, "lse must be contiguous");
   const int b = whole(c.B, "B"), h = whole(H, "H");
+  const fa_stream_t s = stream_of(a[11], c.gpu);
   Tensor own;
   Bytes ws = bytes(a[7], "workspace", c.gpu);
   if (a[7] == Py_None) {
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.gpu));
     ws.n = fa_paged_decode_workspace_size(b, h, c.hkv, c.d);
-    own = at::empty({static_cast<int64_t>(ws.n)}, q.options().dtype(at::kByte));
+    own = scratch(ws.n, q, s, c.gpu);
     ws.p = own.data_ptr();
   }
   const float* slopes = flat<const float>(a[10], "slopes", at::kFloat, {H}, c.gpu);
   const float scale = scale_of(a[8], c.d), cap = number(a[9]);
-  const fa_stream_t s = stream_of(a[11], c.gpu);
   const int st = call(c.gpu, [&] {
     return fa_paged_decode(lq.p, lq.strides(), c.k.p, c.k.strides(), c.v.p, c.v.strides(), c.table, c.table_stride,
                            c.lens, lo.p, lo.strides(), static_cast<float*>(lse.data_ptr()), ws.p, ws.n, b, h, c.hkv, c.d,

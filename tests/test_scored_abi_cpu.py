@@ -44,7 +44,7 @@ BAD_COMMON = [
     (dict(B=-1), INV), (dict(H=-2), INV), (dict(N=-1), INV), (dict(Hkv=0), INV), (dict(Hkv=3), INV), (dict(Hkv=-1), INV),
     (dict(causal=2), INV), (dict(causal=1, plan=FAKE, pb=1 << 30), INV), (dict(d=96), UNSUP), (dict(d=256), UNSUP),
     (dict(scale=0.0), INV), (dict(scale=float("nan")), INV), (dict(cap=-1.0), INV), (dict(cap=float("inf")), INV),
-    (dict(cap=float("nan")), INV), (dict(plan=FAKE, pb=16 * 200 - 1), WS), (dict(plan=FAKE + 4, pb=1 << 20), MIS),
+    (dict(cap=float("nan")), INV), (dict(cap=1e-39), INV), (dict(cap=3e38), INV), (dict(plan=FAKE, pb=16 * 200 - 1), WS), (dict(plan=FAKE + 4, pb=1 << 20), MIS),
     (dict(q=0), INV), (dict(v=FAKE + 2), MIS), (dict(lse=FAKE + 2), MIS), (dict(slopes=FAKE + 2), MIS),
     (dict(qs=_st(63, 6400, 25600)), MIS), (dict(qs=_st(56, 6400, 25600)), INV), (dict(qs=_st(64, 0, 25600)), INV),
     (dict(qs=_st(64, -64, 25600)), INV), (dict(B=1 << 16, H=1 << 16), UNSUP), (dict(B=64, H=1 << 14, N=1 << 14), UNSUP),
@@ -77,6 +77,14 @@ def test_scored_backward_workspace(lib):
         return lib.fa_bwd_scored(*t, *t, *t, *t, *t, vp(FAKE), *t, *t, *t, vp(ws), nb, 2, 4, 2, 100, 64, vp(0), 0, 0, 0.1, 0.0,
                                  vp(0), det, vp(0))
     assert call(0, need) == WS and call(FAKE, need - 1) == WS and call(FAKE + 16, need) == MIS and call(FAKE, need, 2) == INV
+
+
+def test_deterministic_backward_of_too_many_heads(lib):
+    # (the maxima of a key/value head are a grid's second axis)
+    t = (vp(FAKE), None)
+    for det, status in ((1, UNSUP), (0, WS)):
+        assert lib.fa_bwd_scored(*t, *t, *t, *t, *t, vp(FAKE), *t, *t, *t, vp(0), 0, 1, 65536, 65536, 16, 64, vp(0), 0, 0, 0.1,
+                                 0.0, vp(0), det, vp(0)) == status
 
 
 def test_empty_problems_are_no_ops(lib):
@@ -117,6 +125,7 @@ def test_paged_decode_refusals(lib):
     need = lib.fa_paged_decode_workspace_size(2, 4, 2, 64)
     assert need > 0 and lib.fa_paged_decode_workspace_size(2, 3, 2, 64) == 0
     assert call(H=3) == INV and call(H=-4) == INV and call(scale=-1.0) == INV and call(cap=-2.0) == INV
+    assert call(cap=1e-40) == INV and call(cap=3.3e38) == INV
     assert call(ws=0) == WS and call(nb=need - 1) == WS and call(ws=FAKE + 16) == MIS
     assert call(o=0) == INV and call(o=FAKE + 2) == MIS and call(lse=FAKE + 2) == MIS and call(slopes=FAKE + 2) == MIS
 

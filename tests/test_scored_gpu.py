@@ -274,3 +274,81 @@ def test_refusals_in_the_binding():
         fa.fa_fwd_scored(q, k, v, slopes=torch.ones(4))
     with pytest.raises(ValueError):
         fa.fa_fwd_scored(q.transpose(2, 3), k, v)
+
+
+def test_a_plan_of_other_rows_stays_in_bounds():
+    # A plan with the same bytes but longer rows, and arbitrary bytes: an unspecified mask, outputs that are
+    # finite, and nothing written outside them.
+    B, H, N, d = 2, 2, 192, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 16)
+    longer = fa.fa_mask_plan(1, 2 * N, device="cuda")
+    bytes_ = torch.randint(0, 256, (16 * B * N,), dtype=torch.uint8, generator=torch.Generator().manual_seed(3)).cuda()
+    for plan in (longer, bytes_):
+        buf = torch.full((B, H + 2, N, d), 3.0, dtype=torch.bfloat16, device="cuda")
+        o, lse = fa.fa_fwd_scored(q, k, v, o=buf[:, 1:-1], plan=plan)
+        grads = [torch.full((B, H + 2, N, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        fa.fa_bwd_scored(q, k, v, o, do, lse, *(x[:, 1:-1] for x in grads), plan=plan)
+        fa.fa_sync_check()
+        for x in (buf, *grads):
+            assert bool((x[:, 0] == 3).all()) and bool((x[:, -1] == 3).all())
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_what_padding_holds_does_not_matter(cap, deterministic):
+    # The largest finite values in padding, alone and opposite in sign: their products pass the range
+    # of fp32 and give infinities and NaN, none of which may reach a result.
+    B, H, N, d = 1, 2, 300, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 17)
+    plan = _docs([[40, 150, 220]], None, True, B, N)
+    kw = dict(softcap=cap, plan=plan)
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    want = (o, lse, *fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, **kw))
+    x = [host_f64(t) for t in (q, k, v, do)]
+    args = (d ** -0.5, True, cap, None, [[40, 150, 220]], None)
+    o_ref, lse_ref, ob, lb = scored_forward(*x[:3], *args)
+    refs, bounds = scored_backward(*x, *args)
+    big = torch.finfo(torch.bfloat16).max
+    for x, f in ((q, big), (k, -big), (v, big), (do, big)):
+        for part in (slice(0, 40), slice(220, N)):
+            x[:, :, part] = f
+            x[:, :, part, ::2] = -f
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    got = (o, lse, *fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=deterministic, **kw))
+    fa.fa_sync_check()
+    for name, a, b, ref, bound in zip(("o", "lse", "dq", "dk", "dv"), got, want, (o_ref, lse_ref, *refs), (ob, lb, *bounds)):
+        _check(a, ref, bound, name)
+        # The same bits, but where dq's sum has no fixed order, and with a cap, whose form is chosen by
+        # the largest argument of 32 neighbours: padding may send a row to the other form, whose
+        # values differ by an fp32 error that the oracle's bounds count.
+        if cap == 0.0 and (name != "dq" or deterministic):
+            assert torch.equal(a, b), name
+
+
+def test_a_stream_given_by_the_caller():
+    # Everything on `stream`, the workspace made by the call; the current stream's memory churns beside it.
+    q, k, v, do = _inputs(1, 4, 2, 700, 64, 18)
+    kw = dict(causal=True, softcap=30.0)
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    want = fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, **kw)
+    size = fa.fa_bwd_scored_workspace_size(1, 4, 2, 700, 64)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        got.append(fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, stream=s, **kw))
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    fa.fa_sync_check()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
+def test_sizes_past_int_are_refused():
+    plan = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for B, N in ((2 ** 31, 1), (1, 2 ** 31)):
+        with pytest.raises(ValueError):
+            fa.fa_mask_plan(B, N, plan=plan)
+    with pytest.raises(OverflowError):
+        fa.fa_mask_plan(2 ** 70, 1, plan=plan)
