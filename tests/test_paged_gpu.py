@@ -289,3 +289,76 @@ def test_refusals_in_the_binding():
         fa.fa_paged_decode(q, kc[:, :, :8], vc[:, :, :8], table, n)  # pages of 8 tokens
     with pytest.raises(fa.FAError):
         fa.fa_paged_decode(q, kc, vc, table, n, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_sequences_that_share_pages():
+    # Three sequences with the same first pages (a common prompt), one page twice in one table.
+    kc, vc, table, n = _cache([100, 30, 64], 2, 64, 16, torch.bfloat16, 21)
+    table[1, :2] = table[0, :2]
+    table[2, :4] = table[0, :4]
+    table[2, 3] = table[0, 0]
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(22)).to(torch.bfloat16).cuda()
+    o, lse = fa.fa_paged_decode(q, kc, vc, table, n, softcap=20.0)
+    fa.fa_sync_check()
+    ref = paged_decode(host_f64(q), host_f64(kc), host_f64(vc), table.tolist(), n.tolist(), 0.125, 20.0)
+    _check(o, ref[0], ref[2], "O")
+    _check(lse, ref[1], ref[3], "LSE")
+
+
+def test_more_sequences_than_threads_of_a_block():
+    lens = [(7 * b) % 61 for b in range(700)]
+    _decode((lens, 4, 2, 64, 16, torch.bfloat16, 0.0, True), "nhd", None)
+
+
+def test_append_of_many_heads():
+    # More 16-byte pieces in a token's row than a warp holds at once, the last of them partial.
+    Hkv, d, page = 21, 128, 16
+    kc, vc, table, n = _cache([19, 3], Hkv, d, page, torch.bfloat16, 23)
+    x = torch.randn(9, 2, Hkv, d, generator=torch.Generator().manual_seed(24)).to(torch.bfloat16).cuda()
+    cu = torch.tensor([0, 6, 9], dtype=torch.int32, device="cuda")
+    want = [paged_append(host_f64(x[:, i]), host_f64(c), table.tolist(), n.tolist(), cu.tolist()) for i, c in enumerate((kc, vc))]
+    fa.fa_paged_append(x[:, 0], x[:, 1], kc, vc, table, n, cu)
+    fa.fa_sync_check()
+    assert np.array_equal(host_f64(kc), want[0]) and np.array_equal(host_f64(vc), want[1])
+
+
+def test_two_graphs_share_a_workspace():
+    # Captured for two batches of other sizes over one workspace and replayed in turn on one stream.
+    kc, vc, table, n = _cache([700, 90, 333], 2, 64, 16, torch.bfloat16, 25)
+    q = torch.randn(3, 8, 64, generator=torch.Generator().manual_seed(26)).to(torch.bfloat16).cuda()
+    ws = torch.empty(fa.fa_paged_decode_workspace_size(3, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    runs = [lambda o, l: fa.fa_paged_decode(q, kc, vc, table, n, o=o, lse=l, workspace=ws),
+            lambda o, l: fa.fa_paged_decode(q[:1], kc, vc, table[:1], n[:1], o=o, lse=l, workspace=ws)]
+    want = [fa.fa_paged_decode(q, kc, vc, table, n), fa.fa_paged_decode(q[:1], kc, vc, table[:1], n[:1])]
+    outs = [(torch.zeros_like(o), torch.zeros_like(l)) for o, l in want]
+    graphs = []
+    for run, out in zip(runs, outs):
+        run(*out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(*out)
+        graphs.append(g)
+    for turn in (0, 1, 1, 0):
+        for t in outs[turn]:
+            t.fill_(7)
+        graphs[turn].replay()
+        for a, b in zip(outs[turn], want[turn]):
+            assert torch.equal(a, b)
+    fa.fa_sync_check()
+
+
+def test_a_stream_given_by_the_caller():
+    kc, vc, table, n = _cache([3000, 1], 2, 128, 64, torch.float16, 27)
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(28)).half().cuda()
+    want = fa.fa_paged_decode(q, kc, vc, table, n)
+    size = fa.fa_paged_decode_workspace_size(2, 8, 2, 128)
+    torch.cuda.synchronize()
+    s, got = torch.cuda.Stream(), []
+    for _ in range(8):
+        got.append(fa.fa_paged_decode(q, kc, vc, table, n, stream=s))
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    fa.fa_sync_check()
+    for o, lse in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
