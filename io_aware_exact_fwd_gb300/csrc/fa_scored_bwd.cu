@@ -65,6 +65,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ Params p) {
   using C = BwdCfg<D>;
   constexpr bool kSplitSdp = D == 128 && !DET;  // as in the plain backward
+  // Full query blocks add dQ without a test of every row.  Tested adds leave the dQ warps at d = 64, two of which
+  // have all the rows, behind the rest (B=2 H=32 N=8192 causal: 2380 us, 1747 without; deterministic 3095, 1781;
+  // d = 128 deterministic, H=16/4, cap 50: 1641, 1391).  At d = 128 four warps keep up, and adds that come in
+  // bursts hold up the compute warps' stores (cap 50: 1272 us, 1337 without the test).
+  constexpr bool kWholeAdds = D == 64 || DET;
   constexpr bool kCapped = MODE >= 2, kBiased = MODE == 1 || MODE == 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -459,25 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bar_dqe[b]);
       float* dst = p.dq_acc + (static_cast<size_t>(bh) * p.N + q0) * D + dcol;
       const int lim = min(kBqB, p.N - q0);
-      if constexpr (DET) {
-        const float mul =
-            pow2f(det_shift(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1]));
-        constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic rounds x to an integer in the low bits
-        int* dsti = reinterpret_cast<int*>(dst);
+      float mul = 1.f;
+      if constexpr (DET)
+        mul = pow2f(det_shift(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1]));
+      auto add = [&](auto whole_c) {
+        constexpr bool kWhole = decltype(whole_c)::value;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (hh * 32 + c < lim)
-              atomicAdd(dsti + static_cast<size_t>(hh * 32 + c) * D,
-                        __float_as_int(fmaf(__uint_as_float(v[hh][c]), mul, kMagic)) - 0x4B400000);
-      } else {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (hh * 32 + c < lim) atomicAdd(dst + static_cast<size_t>(hh * 32 + c) * D, __uint_as_float(v[hh][c]));
-      }
+          for (int c = 0; c < 32; ++c) {
+            if (!kWhole && hh * 32 + c >= lim) continue;
+            float* at = dst + static_cast<size_t>(hh * 32 + c) * D;
+            const float x = __uint_as_float(v[hh][c]);
+            if constexpr (DET) {
+              constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic rounds x to an integer in the low bits
+              atomicAdd(reinterpret_cast<int*>(at), __float_as_int(fmaf(x, mul, kMagic)) - 0x4B400000);
+            } else {
+              atomicAdd(at, x);
+            }
+          }
+      };
+      if (kWholeAdds && lim == kBqB) add(std::true_type{});
+      else add(std::false_type{});
     }
     __syncwarp();
   }
