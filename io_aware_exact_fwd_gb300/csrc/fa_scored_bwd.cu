@@ -64,7 +64,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                       const __grid_constant__ Params p) {
   using C = BwdCfg<D>;
-  constexpr bool kSplitSdp = D == 128 && !DET;  // as in the plain backward
+  // S^T and dP^T from two threads: at d = 128 their 18 MMAs a step delay each other's issue (B=2 H=16/4 N=8192
+  // causal: 1075 us against 1135 from one; deterministic 1107 against 1205); at d = 64 there are 10 (H=32: 1764
+  // against 1727).
+  constexpr bool kSplitSdp = D == 128;
   // Full query blocks add dQ without a test of every row.  Tested adds leave the dQ warps at d = 64, two of which
   // have all the rows, behind the rest (B=2 H=32 N=8192 causal: 2380 us, 1747 without; deterministic 3095, 1781;
   // d = 128 deterministic, H=16/4, cap 50: 1641, 1391).  At d = 128 four warps keep up, and adds that come in
