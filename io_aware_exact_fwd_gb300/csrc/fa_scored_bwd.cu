@@ -17,6 +17,10 @@
 //  * Without a cap, LSE and D still enter through the extra K-step of S^T and dP^T. With
 //    one, tanh needs the bare products: S^T goes without, and the compute warps subtract
 //    LSE2 (64 fp32 values beside each query block) after the cap.
+//  * At d = 64 dQ^T is an MMA of 64 rows, whose accumulator lies in 16 lanes of each of
+//    the four dQ warps' quarters, so all four add (with K^T padded to 128 rows two do:
+//    cap 50, B=2 H=32 N=8192 causal 2287 us, 2145 so).  The padding's box stays unused.
+//
 #include <math.h>
 
 #include <type_traits>
@@ -68,11 +72,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // causal: 1075 us against 1135 from one; deterministic 1107 against 1205); at d = 64 there are 10 (H=32: 1764
   // against 1727).
   constexpr bool kSplitSdp = D == 128;
-  // Full query blocks add dQ without a test of every row.  Tested adds leave the dQ warps at d = 64, two of which
-  // have all the rows, behind the rest (B=2 H=32 N=8192 causal: 2380 us, 1747 without; deterministic 3095, 1781;
-  // d = 128 deterministic, H=16/4, cap 50: 1641, 1391).  At d = 128 four warps keep up, and adds that come in
-  // bursts hold up the compute warps' stores (cap 50: 1272 us, 1337 without the test).
-  constexpr bool kWholeAdds = D == 64 || DET;
+  // The deterministic form adds full query blocks without a test of every row (B=2 N=8192 causal, cap 50, d = 128,
+  // H=16/4: 1641 us with the test, 1391 without; d = 64, H=32: 3390 | 2269).  The fp32 adds keep it: they take less
+  // time, and in bursts hold up the compute warps' stores (d = 128: 1272 us with the test, 1337 without; d = 64: 2145 |
+  // 2325).
+  constexpr bool kWholeAdds = DET;
   constexpr bool kCapped = MODE >= 2, kBiased = MODE == 1 || MODE == 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -131,11 +135,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Steps st = steps_of(p, kb, b_idx);
   const int n = st.n;
-  if constexpr (D == 64) {
-    // Rows 64..127 of the dQ^T MMA's A operand: zeros, read by the tensor core.
-    uint4* z = reinterpret_cast<uint4*>(smem + C::kZeroOff);
-    for (int i = threadIdx.x; i < C::kKVBox / 16; i += kThreads) z[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   {
     // The extra K-step's key-side tiles (BwdCfg), one 16-byte half-row per thread.
     const int tile = threadIdx.x >> 8, krow = (threadIdx.x >> 1) & 127, half = threadIdx.x & 1;
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         constexpr uint32_t idesc_sdp = idesc_bf16_f32(kBkB, kBqB, 0, 0);   // keys x queries, K = d
         constexpr uint32_t idesc_dkv = idesc_bf16_f32(kBkB, D, 0, 1);      // keys x d, K = queries
-        constexpr uint32_t idesc_dq = idesc_bf16_f32(128, kBqB, 1, 1);     // d x queries, K = keys
+        constexpr uint32_t idesc_dq = idesc_bf16_f32(D, kBqB, 1, 1);       // d x queries, K = keys
         const uint64_t k_kmaj = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t v_kmaj = sdesc_sw128(smem_u32(sV), 16, 1024);
         const uint64_t k_mn = sdesc_sw128(smem_u32(sK), C::kKVBox, 1024);
@@ -439,8 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     regs_decrease<kRegsDq>();
-    // -------------------------------- dQ reduction (one d-row of dQ^T per thread)
-    const int dcol = threadIdx.x - kWarpDq * 32;
+    // -------------------------------- dQ reduction (one d-row of dQ^T per thread; at d = 64 half of one)
+    const int wq = warp - kWarpDq;
+    const int dcol = D == 128 ? 32 * wq + lane : 16 * wq + (lane & 15), q_lane = D == 128 ? 0 : 32 * (lane >> 4);
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     int head = 0, i = st.i0;
     for (int it = 0; it < n; ++it) {
@@ -451,29 +451,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++head;
       }
       if (!warp_wait_b_suspend(&bar_dqf[b], (it >> 1) & 1, wc, kSiteBDq)) break;
-      if (D == 64 && dcol >= D) {  // the zero-padded rows of dQ^T: nothing to read or add
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_dqe[b]);
-        continue;
-      }
       tc_fence_after();
-      uint32_t v[2][32];
-      tmem_ld32(trow + C::col_pdq(b), v[0]);
-      tmem_ld32(trow + C::col_pdq(b) + 32, v[1]);
-      tmem_ld_wait32(v[0]);
-      tmem_ld_wait32(v[1]);
+      uint32_t v[D / 64][32];
+      if constexpr (D == 64) {
+        tmem_ld16x64(trow + C::col_pdq(b), v[0]);
+        tmem_ld_wait32(v[0]);
+      } else {
+        tmem_ld32(trow + C::col_pdq(b), v[0]);
+        tmem_ld32(trow + C::col_pdq(b) + 32, v[1]);
+        tmem_ld_wait32(v[0]);
+        tmem_ld_wait32(v[1]);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_dqe[b]);
-      float* dst = p.dq_acc + (static_cast<size_t>(bh) * p.N + q0) * D + dcol;
-      const int lim = min(kBqB, p.N - q0);
+      float* dst = p.dq_acc + (static_cast<size_t>(bh) * p.N + q0 + q_lane) * D + dcol;
+      const int lim = p.N - q0 - q_lane;
       float mul = 1.f;
       if constexpr (DET)
         mul = pow2f(det_shift(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1]));
       auto add = [&](auto whole_c) {
         constexpr bool kWhole = decltype(whole_c)::value;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             if (!kWhole && hh * 32 + c >= lim) continue;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       };
-      if (kWholeAdds && lim == kBqB) add(std::true_type{});
+      if (kWholeAdds && q0 + kBqB <= p.N) add(std::true_type{});
       else add(std::false_type{});
     }
     __syncwarp();
