@@ -349,6 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P^T, dS^T(it) overwrite dQ^T(it-2) (TMEM) and dS^T(it-2) (shared memory).
       if (it >= 2 && !(ok = warp_wait_b(&bar_dqe[b], ((it - 2) >> 1) & 1, wc, kSiteBComp))) break;
       tc_fence_after();
+      auto write = [&](const uint32_t (&ppk)[16], const uint32_t (&dpk)[16]) {
+        tmem_st16(trow + C::col_pdq(b) + 16 * g, ppk);
+        tmem_st16(trow + C::col_pdq(b) + 32 + 16 * g, dpk);
+        // dS row into shared memory, 128-byte swizzle: chunk ch holds queries 8ch..8ch+7.
+        uint8_t* ds_row = sDs + b * C::kDsBytes + row * 128;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          const int ch = g * 4 + c4;
+          *reinterpret_cast<uint4*>(ds_row + ((ch ^ (row & 7)) * 16)) =
+              make_uint4(dpk[4 * c4], dpk[4 * c4 + 1], dpk[4 * c4 + 2], dpk[4 * c4 + 3]);
+        }
+      };
       // P and dS of the 32 queries, written out.  Three ways, each whole (scores in registers at the
       // meeting of two ways would cost the common one a move each): every key seen by every query;
       // masked; and masked in the general form (any argument of the cap, queries on both sides).
@@ -395,18 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             dpk[c / 2] = pack_bf16x2(ds.x, ds.y);
           }
         }
-        tmem_st16(trow + C::col_pdq(b) + 16 * g, ppk);
-        tmem_st16(trow + C::col_pdq(b) + 32 + 16 * g, dpk);
-        // dS row into shared memory, 128-byte swizzle: chunk ch holds queries 8ch..8ch+7.
-        uint8_t* ds_row = sDs + b * C::kDsBytes + row * 128;
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          const int ch = g * 4 + c4;
-          *reinterpret_cast<uint4*>(ds_row + ((ch ^ (row & 7)) * 16)) =
-              make_uint4(dpk[4 * c4], dpk[4 * c4 + 1], dpk[4 * c4 + 2], dpk[4 * c4 + 3]);
-        }
+        write(ppk, dpk);
       };
-      if (general) step(std::true_type{}, std::true_type{});
+      if (need_mask && !__any_sync(0xffffffffu, bits_between(by.x - q0, by.y - q0))) {
+        const uint32_t zero[16] = {};  // no key of the warp is seen by the 32 queries
+        write(zero, zero);
+      } else if (general) step(std::true_type{}, std::true_type{});
       else if (need_mask) step(std::true_type{}, std::false_type{});
       else step(std::false_type{}, std::false_type{});
       tmem_st_wait();
