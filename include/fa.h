@@ -514,7 +514,7 @@ FA_API int fa_fwd_scored(const void* q, const int64_t* q_strides, const void* k,
                          int B, int H, int Hkv, int N, int d, const void* plan, size_t plan_bytes, int causal,
                          float scale, float softcap, const float* slopes, fa_stream_t stream);
 
-/* Bytes of workspace fa_bwd_scored needs (0 for invalid or unsupported sizes). */
+/* Bytes of workspace fa_bwd_scored needs on the current device (0 for invalid or unsupported sizes). */
 FA_API size_t fa_bwd_scored_workspace_size(int B, int H, int Hkv, int N, int d);
 
 /*

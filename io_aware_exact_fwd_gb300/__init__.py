@@ -689,7 +689,7 @@ def fa_fwd_scored(q, k, v, o=None, lse=None, causal: bool = False, scale: float 
 
 
 def fa_bwd_scored_workspace_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
-    """Bytes of device workspace fa_bwd_scored needs (0 if unsupported)."""
+    """Bytes of device workspace fa_bwd_scored needs on the current device (0 if unsupported)."""
     return int(load_library().fa_bwd_scored_workspace_size(B, H, Hkv, N, d))
 
 

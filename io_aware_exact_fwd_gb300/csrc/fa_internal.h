@@ -255,6 +255,8 @@ struct ScoreArgs {
   int Hkv;
 };
 cudaError_t launch_fwd_scored(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream);
+// Bytes of its workspace: the plain backward's, then the partial sums of divided key blocks.
+size_t bwd_scored_workspace(int B, int H, int Hkv, int N, int d);
 cudaError_t launch_bwd_scored(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream);
 
 // ------------------------------------------------------- paged cache (fa_paged.cu)
@@ -312,6 +314,7 @@ cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+int sm_count();  // of the current device; 152 where there is none
 cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int elem_bytes, int cols,
                          int rows, int heads, int batch, const int64_t strides[3], int box_cols, int box_rows,
                          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,

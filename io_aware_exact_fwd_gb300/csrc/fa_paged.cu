@@ -654,14 +654,6 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    sms = 152;
-  return sms;
-}
-
 // Query heads per chunk (16 MT) and the CTAs of the decode.  Up to 16 heads share a key/value head
 // in most models, and two CTAs an SM with 16 rows each keep more loads in flight than one with 32
 // (64 sequences of 4000-8000 tokens, one head of d=128: 40.5 us against 46.5); larger groups read

@@ -111,7 +111,7 @@ int fa_fwd_scored(const void* q, const int64_t* q_strides, const void* k, const 
 
 size_t fa_bwd_scored_workspace_size(int B, int H, int Hkv, int N, int d) {
   if (validate_scored(B, H, Hkv, N, d, 0, 1.f, 0.f) != FA_OK) return 0;
-  return fa::bwd_workspace_layout(B, H, N, d).total;
+  return fa::bwd_scored_workspace(B, H, Hkv, N, d);
 }
 
 int fa_bwd_scored(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, const void* v,
@@ -128,7 +128,7 @@ int fa_bwd_scored(const void* q, const int64_t* q_strides, const void* k, const 
   int st = validate_plan(plan, plan_bytes, B, N, causal);
   if (st != FA_OK) return st;
   if (deterministic && static_cast<long long>(B) * Hkv > 65535) return FA_ERR_UNSUPPORTED;  // a grid's second axis
-  if (!workspace || ws_bytes < fa::bwd_workspace_layout(B, H, N, d).total) return FA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < fa::bwd_scored_workspace(B, H, Hkv, N, d)) return FA_ERR_WORKSPACE;
   fa::BwdArgs a{};
   const fa::Strides ds = fa::dense_strides(H, N, d), dkv = fa::dense_strides(Hkv, N, d);
   const struct {

@@ -17,6 +17,9 @@
 //  * Without a cap, LSE and D still enter through the extra K-step of S^T and dP^T. With
 //    one, tanh needs the bare products: S^T goes without, and the compute warps subtract
 //    LSE2 (64 fp32 values beside each query block) after the cap.
+//  * Where the key blocks are few (parts_of), the steps of each are dealt out to several CTAs,
+//    which leave fp32 sums of dK and dV in the workspace for bwd_join_kernel, added there in a
+//    fixed order.
 //  * At d = 64 dQ^T is an MMA of 64 rows, whose accumulator lies in 16 lanes of each of
 //    the four dQ warps' quarters, so all four add (with K^T padded to 128 rows two do:
 //    cap 50, B=2 H=32 N=8192 causal 2287 us, 2145 so).  The padding's box stays unused.
@@ -37,6 +40,7 @@
 // double (1235), dQ by TMA reductions from shared memory (1575).
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fa_bwd_common.cuh"
@@ -49,13 +53,14 @@ namespace {
 
 struct Params {
   MaskPlan plan;
-  int causal, N, Npad, H, Hkv, group, nkb;
+  int causal, N, Npad, H, Hkv, group, nkb, parts;
   float scale, scale_log2;
   float cap_in, cap_out;  // 4 scale / softcap (products to x = 4 u), softcap log2(e)
   CapPoly poly;           // factor 1
   const float* slopes;
   const uint8_t* aug;
   float* dq_acc;
+  float* part_sums;       // [parts][dV, dK][B Hkv][N][D] where parts > 1
   const float* dq_bmax;
   const float* kv_max;
   unsigned int* err_word;
@@ -116,8 +121,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   // Key blocks in order, heads next to one another: causal key blocks near the start see
   // the most queries and go first.
-  const int kvheads = static_cast<int>(gridDim.x) / p.nkb;  // B Hkv
-  const int kb = static_cast<int>(blockIdx.x) / kvheads, bhk = static_cast<int>(blockIdx.x) % kvheads;
+  const int unit = static_cast<int>(blockIdx.x) / p.parts, part = static_cast<int>(blockIdx.x) % p.parts;
+  const int kvheads = static_cast<int>(gridDim.x) / p.parts / p.nkb;  // B Hkv
+  const int kb = unit / kvheads, bhk = unit % kvheads;
   const int hk = bhk % p.Hkv, b_idx = bhk / p.Hkv;
   const int h0 = hk * p.group;               // first query head of the group
   const int bh0 = b_idx * p.H + h0;
@@ -148,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const Steps st = steps_of(p, kb, b_idx);
-  const int n = st.n;
+  // This part's steps: n from the first on, that one being block i_first of head head_first.
+  const int first = st.n * part / p.parts, n = st.n * (part + 1) / p.parts - first;
+  const int head_first = n > 0 ? first / st.nq : 0, i_first = st.i0 + first - head_first * st.nq;
   {
     // The extra K-step's key-side tiles (BwdCfg), one 16-byte half-row per thread.
     const int tile = threadIdx.x >> 8, krow = (threadIdx.x >> 1) & 127, half = threadIdx.x & 1;
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ TMA producer
       if (lane == 0) {
-        int issued = 0, g = 0, i = st.i0;
+        int issued = 0, g = head_first, i = i_first;
         for (int it = 0; it < n; ++it) {
           const int slot = it % kStages;
           if (!mbar_wait(&bar_empty[slot], ((it / kStages) & 1) ^ 1, wc, kSiteBLoad)) break;
@@ -312,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No key of the warp is seen by a query before it: |i - j| = i - j wherever it counts.
     const bool one_sided = !kBiased || __all_sync(0xffffffffu, by.x >= key || by.x >= by.y);
     bool ok = true;
-    int head = 0, i = st.i0, slot = 0;
+    int head = head_first, i = i_first, slot = 0;
     uint32_t ring_ph = 0;
-    float slope2 = kBiased && n > 0 ? __ldg(p.slopes + h0) * kLog2e : 0.f;
+    float slope2 = kBiased && n > 0 ? __ldg(p.slopes + h0 + head) * kLog2e : 0.f;
     for (int it = 0; it < n; ++it) {
       const int b = it & 1;
       if (!(ok = warp_wait_b_suspend(bar_sdp, it & 1, wc, kSiteBComp))) break;
@@ -433,7 +441,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------- dK, dV epilogue (warpgroup 0: dV, 1: dK)
     // (A block that no query sees only waits for K and V to land where its zeros go.)
     if (ok) ok = warp_wait_b(n > 0 ? bar_dkv : bar_kv, 0, wc, kSiteBEpi);
-    if (ok) {
+    if (ok && p.parts > 1) {
+      tc_fence_after();
+      float* dst = p.part_sums + (((static_cast<size_t>(part) * 2 + g) * kvheads + bhk) * p.N + key) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 8) {
+        uint32_t x[8] = {};
+        if (n > 0) tmem_ld8_wait(trow + (g == 0 ? C::kColDV : C::kColDK) + c, x);
+        if (key < p.N) {
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(dst + c + 4) = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+      }
+    } else if (ok) {
       tc_fence_after();
       if (n > 0) {
         if (g == 0) stage_row_bf16<D>(trow + C::kColDV, sV, row, 1.f);
@@ -462,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp - kWarpDq;
     const int dcol = D == 128 ? 32 * wq + lane : 16 * wq + (lane & 15), q_lane = D == 128 ? 0 : 32 * (lane >> 4);
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int head = 0, i = st.i0;
+    int head = head_first, i = i_first;
     for (int it = 0; it < n; ++it) {
       const int b = it & 1;
       const int q0 = i * kBqB, bh = bh0 + head;
@@ -521,6 +541,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// dV and dK of divided key blocks: the parts' sums, added in order, rounded once.  One thread per 8 columns.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_join_kernel(const float* __restrict__ part_sums, int parts, long long rows,
+                                                       int N, int Hkv, __nv_bfloat16* __restrict__ dv, Strides sdv,
+                                                       __nv_bfloat16* __restrict__ dk, Strides sdk, float scale) {
+  grid_release();
+  grid_wait();  // the parts are written
+  const long long x = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8, size = rows * D;
+  if (x >= 2 * size) return;
+  float acc[8] = {};
+  for (int s = 0; s < parts; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(part_sums + s * 2 * size + x);
+    const float4 a = src[0], b = src[1];
+    acc[0] += a.x;
+    acc[1] += a.y;
+    acc[2] += a.z;
+    acc[3] += a.w;
+    acc[4] += b.x;
+    acc[5] += b.y;
+    acc[6] += b.z;
+    acc[7] += b.w;
+  }
+  const bool is_k = x >= size;
+  const long long r = (is_k ? x - size : x) / D;
+  const float mul = is_k ? scale : 1.f;
+  uint4 out;
+  out.x = pack_bf16x2(acc[0] * mul, acc[1] * mul);
+  out.y = pack_bf16x2(acc[2] * mul, acc[3] * mul);
+  out.z = pack_bf16x2(acc[4] * mul, acc[5] * mul);
+  out.w = pack_bf16x2(acc[6] * mul, acc[7] * mul);
+  __nv_bfloat16* dst = is_k ? dk : dv;
+  *reinterpret_cast<uint4*>(dst + row_offset(is_k ? sdk : sdv, r / N, Hkv, static_cast<int>(r % N)) + x % D) = out;
+}
+
+// How many CTAs share a key block's steps: up to two a SM in all, each with 8 steps or more if every
+// query sees the block.  Undivided, a block's steps run one after another however many SMs are
+// idle (causal, d = 128: B=2 H=16/2 N=1030 155 us, 58 divided; B=1 H=8/2 N=3737 of three documents
+// 220 | 82; H=2 N=6063 109 | 67).  More parts than that cost more in sums than they gain (three a
+// SM: 72 | 92 | 80), and so do shorter ones (4 steps, H=8 N=1024: 37 us for 29).
+int parts_of(int B, int H, int Hkv, int N) {
+  const long long blocks = static_cast<long long>((N + kBkB - 1) / kBkB) * B * Hkv;
+  const long long steps = static_cast<long long>((N + kBqB - 1) / kBqB) * (H / Hkv);
+  return static_cast<int>(std::max(1ll, std::min({16ll, 2 * sm_count() / blocks, steps / 8})));
+}
+
 template <int D, int MODE, bool DET>
 cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   using C = BwdCfg<D>;
@@ -544,6 +609,8 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   p.Hkv = sc.Hkv;
   p.group = a.group;
   p.nkb = (a.N + kBkB - 1) / kBkB;
+  p.parts = parts_of(a.B, a.H, sc.Hkv, a.N);
+  p.part_sums = reinterpret_cast<float*>(ws + w.total);
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE >= 2) {
@@ -564,8 +631,13 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   cudaFuncAttributes fattr;
   if ((e = cudaFuncGetAttributes(&fattr, kern))) return e;
   if (static_cast<uint32_t>(fattr.numRegs) < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_dependent(kern, static_cast<unsigned>(p.nkb * a.B * sc.Hkv), kThreads, C::kSmemBytes, stream, tq, tk, tv,
-                          tdo, tdk, tdv, p);
+  e = launch_dependent(kern, static_cast<unsigned>(p.nkb * a.B * sc.Hkv * p.parts), kThreads, C::kSmemBytes, stream, tq,
+                       tk, tv, tdo, tdk, tdv, p);
+  if (e || p.parts == 1) return e;
+  const long long rows = static_cast<long long>(a.B) * sc.Hkv * a.N;
+  return launch_dependent(bwd_join_kernel<D>, static_cast<unsigned>((rows * D / 4 + 255) / 256), 256, 0, stream,
+                          const_cast<const float*>(p.part_sums), p.parts, rows, a.N, sc.Hkv,
+                          static_cast<__nv_bfloat16*>(a.dv), a.sdv, static_cast<__nv_bfloat16*>(a.dk), a.sdk, a.scale);
 }
 
 template <int D, int MODE>
@@ -580,6 +652,12 @@ cudaError_t launch_d(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream)
 }
 
 }  // namespace
+
+size_t bwd_scored_workspace(int B, int H, int Hkv, int N, int d) {
+  const int parts = parts_of(B, H, Hkv, N);
+  return bwd_workspace_layout(B, H, N, d).total +
+         (parts > 1 ? static_cast<size_t>(parts) * 2 * B * Hkv * N * d * sizeof(float) : 0);
+}
 
 cudaError_t launch_bwd_scored(const BwdArgs& args, const ScoreArgs& sc, cudaStream_t stream) {
   BwdArgs a = args;

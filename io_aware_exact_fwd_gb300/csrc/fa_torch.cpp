@@ -239,6 +239,7 @@ PyObject* bwd_scored(PyObject* const* a) {
   Tensor own;
   Bytes ws = bytes(a[9], "workspace", gpu);
   if (a[9] == Py_None) {
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(gpu));
     ws.n = fa_bwd_scored_workspace_size(b, h, hkv, n, dim);
     own = scratch(ws.n, q, s, gpu);
     ws.p = own.data_ptr();

@@ -74,6 +74,8 @@ CASES = [
     (1, 2, 2, 400, 64, True, 200.0, True, [[0, 130, 390]], [[20, 100]]),       # a cap far above the scores
     (1, 2, 1, 300, 128, False, 80.0, True, None, None),
     (3, 2, 2, 65, 64, True, 0.0, False, [[64, 65, 65], [0, 1, 2], [0, 64, 65]], None),
+    (1, 16, 1, 1030, 128, True, 0.0, True, None, None),                        # a key block's steps on 16 blocks
+    (1, 24, 2, 515, 64, True, 20.0, False, [[3, 100, 101, 400]], [[10, 1, 200]]),
 ]
 
 
@@ -168,9 +170,10 @@ def test_same_bits_on_every_run():
             assert torch.equal(a, b)
 
 
-def test_outputs_of_another_layout_and_neighbours_untouched():
+@pytest.mark.parametrize("N", [150, 530])  # the longer with each key block's steps divided
+def test_outputs_of_another_layout_and_neighbours_untouched(N):
     # o, dq, dk, dv as views of larger buffers: what lies between their rows stays.
-    B, H, Hkv, N, d = 1, 2, 1, 150, 64
+    B, H, Hkv, d = 1, 2, 1, 64
     q, k, v, do = _inputs(B, H, Hkv, N, d, 10, layout="bnhd")
     kw = dict(causal=True, softcap=15.0)
     o, lse = fa.fa_fwd_scored(q, k, v, **kw)
