@@ -2,7 +2,7 @@
 // (documents, prefixes), shared key/value heads.  bf16 in and out, fp32 logsumexp.
 //
 // The pipeline is the plain forward's (fa_fwd.cu): each unit 256 query rows of one head
-// as two 128-row tiles; K_j, V_j stream through a TMA ring; one thread
+// as two 128-row tiles (one where that keeps all SMs no busier); K_j, V_j stream through a TMA ring; one thread
 // issues S_t = Q_t K_j^T and O_t += P_t V_j on tcgen05 with S, P and O in TMEM; two
 // softmax warpgroups hold one query row per thread.  What differs:
 //
@@ -36,7 +36,6 @@ namespace fa {
 namespace {
 
 constexpr int kTiles = 2;                       // query tiles per unit
-constexpr int kUnitRows = kTiles * kBlockQ;
 // Warp roles.  With one part, each of the 8 softmax warps holds 32 rows of a tile, 128
 // keys a thread; with two, each of 16 holds 64 keys of 32 rows, and two threads share a
 // row.  Then K/V TMA, MMA, Q TMA and the scheduler, one warp each.  Capped scores take long chains of
@@ -114,7 +113,7 @@ struct Cfg {
 
 struct Params {
   MaskPlan plan;
-  int causal, N, H, group, BH, nunits;
+  int causal, N, H, group, BH, nunits, unit_rows;
   float scale, scale_log2;  // scale_log2 = scale log2(e)
   float cap_in;       // 4 scale / softcap: products to x = 4 u
   float cap_out;      // softcap log2(e)
@@ -127,7 +126,7 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-// A unit as the scheduler publishes it: query rows u * 256 .. of head bh (u < 0: no more
+// A unit as the scheduler publishes it: query rows u * unit_rows .. of head bh (u < 0: no more
 // units).  Tile t attends key blocks [begin[t], end[t]) (empty: both 0), and every row of
 // it sees the keys [all_lo[t], all_hi[t]).  The stream covers blocks [first, last) from
 // last - 1 down.
@@ -151,9 +150,9 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
   const int b = x.bh / p.H;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const int r0 = x.u * kUnitRows + t * kBlockQ;
+    const int r0 = x.u * p.unit_rows + t * kBlockQ;
     x.begin[t] = x.end[t] = x.all_lo[t] = x.all_hi[t] = 0;
-    if (r0 < p.N) {
+    if (t * kBlockQ < p.unit_rows && r0 < p.N) {
       const int2 head = keys_of(p.plan, p.causal, b, r0, p.N);
       const int2 tail = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N);
       if (tail.y > head.x) {
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
               tma_load_4d(sQ + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, &bar_q[t], c * kBoxCols,
-                          x.u * kUnitRows + t * kBlockQ, h, b);
+                          x.u * p.unit_rows + t * kBlockQ, h, b);
           }
           ++nload[t];
         }
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       nu.all_hi = s_unit->all_hi[t];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_unit_read);
-      const int qrow = nu.u * kUnitRows + t * kBlockQ + row;
+      const int qrow = nu.u * p.unit_rows + t * kBlockQ + row;
       nu.see = make_int2(0, 0);
       nu.slope2 = 0.f;
       if (nu.u >= 0) {
@@ -527,8 +526,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       have_next = false;
       if (nu.u < 0) break;
       const int bh = nu.bh, b = bh / p.H, h = bh % p.H;
-      const int row0 = nu.u * kUnitRows + t * kBlockQ;
-      if (row0 >= p.N) continue;
+      const int row0 = nu.u * p.unit_rows + t * kBlockQ;
+      if (t * kBlockQ >= p.unit_rows || row0 >= p.N) continue;
       const int qrow = row0 + row;
       const int2 see = nu.see;
       const float slope2 = nu.slope2;
@@ -871,7 +870,13 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.H = a.H;
   p.group = a.H / sc.Hkv;
   p.BH = a.B * a.H;
-  p.nunits = (a.N + kUnitRows - 1) / kUnitRows;
+  // Units of one tile where they all run at once: a tile by itself takes less time than two that share an SM
+  // (causal, d = 128: B=1 H=2 N=6063 91 -> 72 us, H=16 N=1030 21.4 -> 18.1; H=4 N=129 d=64 capped 9.3 -> 7.9).
+  // Where they do not, two tiles overlap each other's waits (H=6 N=4096 64.6 us, full, in units of two tiles;
+  // 98.8 in units of one).
+  const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * p.BH;
+  p.unit_rows = tiles <= sm_count() ? kBlockQ : 2 * kBlockQ;
+  p.nunits = (a.N + p.unit_rows - 1) / p.unit_rows;
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE >= 2) {
