@@ -80,7 +80,8 @@ __device__ __forceinline__ Steps steps_of(const Params& p, int kb, int b) {
 }
 
 // MODE 0: scores as they are; 1: with a distance bias; 2: capped; 3: capped and biased.
-template <int D, int MODE, bool DET>
+// DIVIDED: parts > 1.
+template <int D, int MODE, bool DET, bool DIVIDED>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -121,8 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   // Key blocks in order, heads next to one another: causal key blocks near the start see
   // the most queries and go first.
-  const int unit = static_cast<int>(blockIdx.x) / p.parts, part = static_cast<int>(blockIdx.x) % p.parts;
-  const int kvheads = static_cast<int>(gridDim.x) / p.parts / p.nkb;  // B Hkv
+  const int parts = DIVIDED ? p.parts : 1;
+  const int unit = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
+  const int kvheads = static_cast<int>(gridDim.x) / parts / p.nkb;  // B Hkv
   const int kb = unit / kvheads, bhk = unit % kvheads;
   const int hk = bhk % p.Hkv, b_idx = bhk / p.Hkv;
   const int h0 = hk * p.group;               // first query head of the group
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Steps st = steps_of(p, kb, b_idx);
   // This part's steps: n from the first on, that one being block i_first of head head_first.
-  const int first = st.n * part / p.parts, n = st.n * (part + 1) / p.parts - first;
-  const int head_first = n > 0 ? first / st.nq : 0, i_first = st.i0 + first - head_first * st.nq;
+  const int first = st.n * part / parts, n = st.n * (part + 1) / parts - first;
+  const int head_first = DIVIDED && n > 0 ? first / st.nq : 0, i_first = st.i0 + first - head_first * st.nq;
   {
     // The extra K-step's key-side tiles (BwdCfg), one 16-byte half-row per thread.
     const int tile = threadIdx.x >> 8, krow = (threadIdx.x >> 1) & 127, half = threadIdx.x & 1;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------- dK, dV epilogue (warpgroup 0: dV, 1: dK)
     // (A block that no query sees only waits for K and V to land where its zeros go.)
     if (ok) ok = warp_wait_b(n > 0 ? bar_dkv : bar_kv, 0, wc, kSiteBEpi);
-    if (ok && p.parts > 1) {
+    if (DIVIDED && ok) {
       tc_fence_after();
       float* dst = p.part_sums + (((static_cast<size_t>(part) * 2 + g) * kvheads + bhk) * p.N + key) * D;
 #pragma unroll 1
@@ -586,8 +588,8 @@ int parts_of(int B, int H, int Hkv, int N) {
   return static_cast<int>(std::max(1ll, std::min({16ll, 2 * sm_count() / blocks, steps / 8})));
 }
 
-template <int D, int MODE, bool DET>
-cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+template <int D, int MODE, bool DET, bool DIVIDED>
+cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, int parts, cudaStream_t stream) {
   using C = BwdCfg<D>;
   const BwdWorkspace w = bwd_workspace_layout(a.B, a.H, a.N, a.d);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -609,7 +611,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   p.Hkv = sc.Hkv;
   p.group = a.group;
   p.nkb = (a.N + kBkB - 1) / kBkB;
-  p.parts = parts_of(a.B, a.H, sc.Hkv, a.N);
+  p.parts = parts;
   p.part_sums = reinterpret_cast<float*>(ws + w.total);
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
@@ -625,7 +627,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   p.kv_max = reinterpret_cast<const float*>(ws + w.off_kvmax);
   p.err_word = a.err_word;
   p.wait_ns = a.dbg.wait_limit_ns;
-  auto kern = bwd_scored_kernel<D, MODE, DET>;
+  auto kern = bwd_scored_kernel<D, MODE, DET, DIVIDED>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
   // The register split assumes the block launches with kLaunchRegs per thread.
   cudaFuncAttributes fattr;
@@ -633,7 +635,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
   if (static_cast<uint32_t>(fattr.numRegs) < kLaunchRegs) return cudaErrorInvalidConfiguration;
   e = launch_dependent(kern, static_cast<unsigned>(p.nkb * a.B * sc.Hkv * p.parts), kThreads, C::kSmemBytes, stream, tq,
                        tk, tv, tdo, tdk, tdv, p);
-  if (e || p.parts == 1) return e;
+  if (e || !DIVIDED) return e;
   const long long rows = static_cast<long long>(a.B) * sc.Hkv * a.N;
   return launch_dependent(bwd_join_kernel<D>, static_cast<unsigned>((rows * D / 4 + 255) / 256), 256, 0, stream,
                           const_cast<const float*>(p.part_sums), p.parts, rows, a.N, sc.Hkv,
@@ -642,7 +644,12 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
 
 template <int D, int MODE>
 cudaError_t launch_mode(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  return a.deterministic ? launch_main<D, MODE, true>(a, sc, stream) : launch_main<D, MODE, false>(a, sc, stream);
+  const int parts = parts_of(a.B, a.H, sc.Hkv, a.N);
+  if (parts > 1)
+    return a.deterministic ? launch_main<D, MODE, true, true>(a, sc, parts, stream)
+                           : launch_main<D, MODE, false, true>(a, sc, parts, stream);
+  return a.deterministic ? launch_main<D, MODE, true, false>(a, sc, parts, stream)
+                         : launch_main<D, MODE, false, false>(a, sc, parts, stream);
 }
 
 template <int D>

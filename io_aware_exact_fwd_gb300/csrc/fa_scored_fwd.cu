@@ -2,7 +2,7 @@
 // (documents, prefixes), shared key/value heads.  bf16 in and out, fp32 logsumexp.
 //
 // The pipeline is the plain forward's (fa_fwd.cu): each unit 256 query rows of one head
-// as two 128-row tiles (one where that keeps all SMs no busier); K_j, V_j stream through a TMA ring; one thread
+// as two 128-row tiles (or one, unit_tiles); K_j, V_j stream through a TMA ring; one thread
 // issues S_t = Q_t K_j^T and O_t += P_t V_j on tcgen05 with S, P and O in TMEM; two
 // softmax warpgroups hold one query row per thread.  What differs:
 //
@@ -113,7 +113,7 @@ struct Cfg {
 
 struct Params {
   MaskPlan plan;
-  int causal, N, H, group, BH, nunits, unit_rows;
+  int causal, N, H, group, BH, nunits;
   float scale, scale_log2;  // scale_log2 = scale log2(e)
   float cap_in;       // 4 scale / softcap: products to x = 4 u
   float cap_out;      // softcap log2(e)
@@ -126,7 +126,7 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-// A unit as the scheduler publishes it: query rows u * unit_rows .. of head bh (u < 0: no more
+// A unit as the scheduler publishes it: query rows u * kUnitRows .. of head bh (u < 0: no more
 // units).  Tile t attends key blocks [begin[t], end[t]) (empty: both 0), and every row of
 // it sees the keys [all_lo[t], all_hi[t]).  The stream covers blocks [first, last) from
 // last - 1 down.
@@ -143,6 +143,7 @@ struct Unit {
   __device__ __forceinline__ int to(int t) const { return last() - begin[t]; }
 };
 // Block w of the grid: the last rows (the heaviest, when causal) first, heads next to one another.
+template <int ROWS>
 __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
   Unit x;
   x.u = p.nunits - 1 - w / p.BH;
@@ -150,9 +151,9 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
   const int b = x.bh / p.H;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const int r0 = x.u * p.unit_rows + t * kBlockQ;
+    const int r0 = x.u * ROWS + t * kBlockQ;
     x.begin[t] = x.end[t] = x.all_lo[t] = x.all_hi[t] = 0;
-    if (t * kBlockQ < p.unit_rows && r0 < p.N) {
+    if (t * kBlockQ < ROWS && r0 < p.N) {
       const int2 head = keys_of(p.plan, p.causal, b, r0, p.N);
       const int2 tail = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N);
       if (tail.y > head.x) {
@@ -194,12 +195,13 @@ __device__ __forceinline__ bool pair_or(int id, bool x) {
 template <int MODE>
 constexpr int kPartsOf = MODE == 2 || MODE == 3 ? 2 : 1;
 
-template <int D, int MODE>
+// UNIT: tiles of a unit.
+template <int D, int MODE, int UNIT>
 __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using C = Cfg<D, MODE>;
-  constexpr int kParts = kPartsOf<MODE>;
+  constexpr int kParts = kPartsOf<MODE>, kUnitRows = UNIT * kBlockQ;
   constexpr bool kBounded = MODE == 2 || MODE == 3;  // the fixed reference (kBoundedCap)
   using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         for (int k = 0;; ++k) {
           Unit x{};
           x.u = -1;
-          if (w >= 0) x = unit_of(p, w);
+          if (w >= 0) x = unit_of<kUnitRows>(p, w);
           if (k > 0 && !mbar_wait_suspend(bar_unit_read, (k - 1) & 1, wc, kSiteSched, 20000u)) break;
           *s_unit = x;
           mbar_arrive(bar_unit);
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
               tma_load_4d(sQ + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, &bar_q[t], c * kBoxCols,
-                          x.u * p.unit_rows + t * kBlockQ, h, b);
+                          x.u * kUnitRows + t * kBlockQ, h, b);
           }
           ++nload[t];
         }
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       nu.all_hi = s_unit->all_hi[t];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_unit_read);
-      const int qrow = nu.u * p.unit_rows + t * kBlockQ + row;
+      const int qrow = nu.u * kUnitRows + t * kBlockQ + row;
       nu.see = make_int2(0, 0);
       nu.slope2 = 0.f;
       if (nu.u >= 0) {
@@ -526,8 +528,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       have_next = false;
       if (nu.u < 0) break;
       const int bh = nu.bh, b = bh / p.H, h = bh % p.H;
-      const int row0 = nu.u * p.unit_rows + t * kBlockQ;
-      if (t * kBlockQ >= p.unit_rows || row0 >= p.N) continue;
+      const int row0 = nu.u * kUnitRows + t * kBlockQ;
+      if (t * kBlockQ >= kUnitRows || row0 >= p.N) continue;
       const int qrow = row0 + row;
       const int2 see = nu.see;
       const float slope2 = nu.slope2;
@@ -853,7 +855,16 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
   }
 }
 
-template <int D, int MODE>
+// One tile where all units of one run at once: a tile by itself takes less time than two that share an SM
+// (causal, d = 128: B=1 H=2 N=6063 91 -> 72 us, H=16 N=1030 21.4 -> 18.1; H=4 N=129 d=64 capped 9.3 -> 7.9).
+// Where they do not, two tiles overlap each other's waits (H=6 N=4096 64.6 us, full, in units of two tiles;
+// 98.8 in units of one).
+int unit_tiles(const FwdArgs& a) {
+  const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * a.B * a.H;
+  return tiles <= sm_count() ? 1 : 2;
+}
+
+template <int D, int MODE, int UNIT>
 cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   using C = Cfg<D, MODE>;
   using R = Roles<kPartsOf<MODE>>;
@@ -870,13 +881,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.H = a.H;
   p.group = a.H / sc.Hkv;
   p.BH = a.B * a.H;
-  // Units of one tile where they all run at once: a tile by itself takes less time than two that share an SM
-  // (causal, d = 128: B=1 H=2 N=6063 91 -> 72 us, H=16 N=1030 21.4 -> 18.1; H=4 N=129 d=64 capped 9.3 -> 7.9).
-  // Where they do not, two tiles overlap each other's waits (H=6 N=4096 64.6 us, full, in units of two tiles;
-  // 98.8 in units of one).
-  const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * p.BH;
-  p.unit_rows = tiles <= sm_count() ? kBlockQ : 2 * kBlockQ;
-  p.nunits = (a.N + p.unit_rows - 1) / p.unit_rows;
+  p.nunits = (a.N + UNIT * kBlockQ - 1) / (UNIT * kBlockQ);
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
   if (MODE >= 2) {
@@ -890,7 +895,7 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   p.lse = a.lse;
   p.err_word = a.err_word;
   p.wait_ns = a.dbg.wait_limit_ns;
-  auto kern = fwd_scored_kernel<D, MODE>;
+  auto kern = fwd_scored_kernel<D, MODE, UNIT>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
   // setmaxnreg.inc can only draw on the registers the block was launched with.
   cudaFuncAttributes fattr;
@@ -900,13 +905,18 @@ cudaError_t launch(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, int UNIT>
+cudaError_t launch_unit(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
+  if (sc.softcap > 0.f)
+    return sc.softcap * kLog2e > kBoundedCap ? launch<D, 4, UNIT>(a, sc, stream)
+           : sc.slopes                       ? launch<D, 3, UNIT>(a, sc, stream)
+                                             : launch<D, 2, UNIT>(a, sc, stream);
+  return sc.slopes ? launch<D, 1, UNIT>(a, sc, stream) : launch<D, 0, UNIT>(a, sc, stream);
+}
+
 template <int D>
 cudaError_t launch_d(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  if (sc.softcap > 0.f)
-    return sc.softcap * kLog2e > kBoundedCap ? launch<D, 4>(a, sc, stream)
-           : sc.slopes                       ? launch<D, 3>(a, sc, stream)
-                                             : launch<D, 2>(a, sc, stream);
-  return sc.slopes ? launch<D, 1>(a, sc, stream) : launch<D, 0>(a, sc, stream);
+  return unit_tiles(a) == 1 ? launch_unit<D, 1>(a, sc, stream) : launch_unit<D, 2>(a, sc, stream);
 }
 
 }  // namespace
