@@ -101,7 +101,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     # The binding finds libfa.so beside it; PyTorch's libraries are loaded before it (by importing torch).
     tmp = TORCH_LIB + ".tmp"
     _run(["g++", "-shared", "-o", tmp, torch_obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch",
-          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", LIBDIR, "-l:libfa.so", "-Wl,-rpath,$ORIGIN"], "link of the binding")
+          "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", LIBDIR, "-l:libfa.so", "-Wl,-rpath,$ORIGIN"], "link of the binding")
     os.replace(tmp, TORCH_LIB)
     return LIB
 

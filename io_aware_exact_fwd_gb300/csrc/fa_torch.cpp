@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -96,8 +97,13 @@ Bytes bytes(PyObject* x, const char* name, int gpu) {
   return {t.data_ptr(), t.nbytes()};
 }
 
+// A new tensor on the GPU of `like`, from the current stream's memory.  (at::empty comes to the same
+// function through the dispatcher, a microsecond later.)
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+}
 Tensor given_or_new(PyObject* x, const char* name, at::IntArrayRef shape, const Tensor& like, at::ScalarType type) {
-  return x != Py_None ? tensor(x, name) : at::empty(shape, like.options().dtype(type));
+  return x != Py_None ? tensor(x, name) : fresh(shape, type, like);
 }
 
 float number(PyObject* x) {
@@ -131,7 +137,7 @@ int whole(int64_t n, const char* name) {
 Tensor scratch(size_t n, const Tensor& like, fa_stream_t stream, int gpu) {
   c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream),
                                                                     static_cast<c10::DeviceIndex>(gpu)));
-  return at::empty({static_cast<int64_t>(n)}, like.options().dtype(at::kByte));
+  return fresh({static_cast<int64_t>(n)}, at::kByte, like);
 }
 
 // fn() with the GPU current, and without the interpreter's lock (nothing in fn may throw).
