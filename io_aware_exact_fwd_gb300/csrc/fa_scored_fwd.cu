@@ -2,7 +2,7 @@
 // (documents, prefixes), shared key/value heads.  bf16 in and out, fp32 logsumexp.
 //
 // The pipeline is the plain forward's (fa_fwd.cu): each unit 256 query rows of one head
-// as two 128-row tiles (or one, unit_tiles); K_j, V_j stream through a TMA ring; one thread
+// as two 128-row tiles (or one in two halves, unit_tiles); K_j, V_j stream through a TMA ring; one thread
 // issues S_t = Q_t K_j^T and O_t += P_t V_j on tcgen05 with S, P and O in TMEM; two
 // softmax warpgroups hold one query row per thread.  What differs:
 //
@@ -126,10 +126,10 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-// A unit as the scheduler publishes it: query rows u * kUnitRows .. of head bh (u < 0: no more
-// units).  Tile t attends key blocks [begin[t], end[t]) (empty: both 0), and every row of
-// it sees the keys [all_lo[t], all_hi[t]).  The stream covers blocks [first, last) from
-// last - 1 down.
+// A unit as the scheduler publishes it: rows u * 256 .. of head bh as two tiles, or rows u * 128 ..
+// in two halves (u < 0: no more units).  Tile t attends key blocks [begin[t], end[t]) (empty: both 0),
+// and every row of it sees the keys [all_lo[t], all_hi[t]).  The stream covers blocks [first, last)
+// from last - 1 down; the halves of a halved unit have the same range and take its blocks in turn.
 struct Unit {
   int u, bh;
   int begin[kTiles], end[kTiles], all_lo[kTiles], all_hi[kTiles];
@@ -143,7 +143,7 @@ struct Unit {
   __device__ __forceinline__ int to(int t) const { return last() - begin[t]; }
 };
 // Block w of the grid: the last rows (the heaviest, when causal) first, heads next to one another.
-template <int ROWS>
+template <int UNIT>
 __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
   Unit x;
   x.u = p.nunits - 1 - w / p.BH;
@@ -151,9 +151,9 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
   const int b = x.bh / p.H;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const int r0 = x.u * ROWS + t * kBlockQ;
+    const int r0 = UNIT == 1 ? x.u * kBlockQ : x.u * 2 * kBlockQ + t * kBlockQ;
     x.begin[t] = x.end[t] = x.all_lo[t] = x.all_hi[t] = 0;
-    if (t * kBlockQ < ROWS && r0 < p.N) {
+    if (r0 < p.N) {
       const int2 head = keys_of(p.plan, p.causal, b, r0, p.N);
       const int2 tail = keys_of(p.plan, p.causal, b, min(r0 + kBlockQ, p.N) - 1, p.N);
       if (tail.y > head.x) {
@@ -164,6 +164,7 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int w) {
       x.all_hi[t] = head.y;
     }
   }
+  if (UNIT == 1 && x.end[1] - x.begin[1] < 2) x.begin[1] = x.end[1] = 0;
   return x;
 }
 
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
     fwd_scored_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
   using C = Cfg<D, MODE>;
-  constexpr int kParts = kPartsOf<MODE>, kUnitRows = UNIT * kBlockQ;
+  constexpr int kParts = kPartsOf<MODE>;
   constexpr bool kBounded = MODE == 2 || MODE == 3;  // the fixed reference (kBoundedCap)
   using R = Roles<kParts>;
   extern __shared__ uint8_t smem_raw[];
@@ -284,11 +285,15 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         for (int k = 0;; ++k) {
           Unit x{};
           x.u = -1;
-          if (w >= 0) x = unit_of<kUnitRows>(p, w);
+          if (w >= 0) x = unit_of<UNIT>(p, w);
           if (k > 0 && !mbar_wait_suspend(bar_unit_read, (k - 1) & 1, wc, kSiteSched, 20000u)) break;
           *s_unit = x;
           mbar_arrive(bar_unit);
           if (w < 0) break;
+          if (UNIT == 1) {  // all blocks run at once: there is nothing to take over
+            w = -1;
+            continue;
+          }
           if (k > 0 && !mbar_wait_suspend(bar_unit_read, k & 1, wc, kSiteSched, 20000u)) break;
           mbar_arrive_expect_tx(bar_answer, 16);
           try_cancel(smem + C::kAnswerOff, bar_answer);
@@ -309,17 +314,21 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         Unit x;
         for (int k = 0; ok && next_unit(k, x, ok); ++k) {
           const int b = x.bh / p.H, hk = (x.bh % p.H) / p.group;
-          const int first = x.first();
-          for (int j = x.last() - 1; ok && j >= first; --j) {
+          const int first = x.first(), last = x.last();
+          // K_j, then V_j; in a halved unit K of two blocks, then V of one and K of the next but one in turn.
+          for (int j = UNIT == 1 ? last + 1 : last - 1; ok && j >= first; --j) {
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {  // K_j, then V_j
+            for (int i = 0; i < 2; ++i) {
+              const bool kv = UNIT == 1 ? i == 0 : i == 1;
+              const int block = UNIT == 1 && !kv ? j - 2 : j;
+              if (UNIT == 1 && (block < first || block >= last)) continue;
               const int slot = issued % C::kSlots;
               if (!(ok = mbar_wait_suspend(&bar_empty[slot], ((issued / C::kSlots) & 1) ^ 1, wc, kSiteLoadEmpty, 20000u))) break;
               mbar_arrive_expect_tx(&bar_full[slot], C::kTileBytes);
               uint8_t* dst = sRing + slot * C::kTileBytes;
 #pragma unroll
               for (int c = 0; c < C::kBoxes; ++c)
-                tma_load_4d(dst + c * C::kBoxBytes, kv ? &tm_v : &tm_k, &bar_full[slot], c * kBoxCols, j * kBlockK,
+                tma_load_4d(dst + c * C::kBoxBytes, kv ? &tm_v : &tm_k, &bar_full[slot], c * kBoxCols, block * kBlockK,
                             hk, b);
               ++issued;
             }
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         const int b = x.bh / p.H, h = x.bh % p.H;
 #pragma unroll
         for (int tt = 0; tt < kTiles; ++tt) {
-          const int t = kTiles - 1 - tt;  // the later tile's run of the stream starts first
+          const int t = UNIT == 1 ? tt : kTiles - 1 - tt;  // the later tile's run of the stream starts first
           if (!ok || !x.has(t)) continue;
           if (nload[t] > 0 && !(ok = warp_wait_suspend(&bar_qe[t], (nload[t] - 1) & 1, wc, kSiteLoadQ))) continue;
           if constexpr (MODE == 1) {  // the head's slope for the bias's K-step
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
               tma_load_4d(sQ + t * C::kTileBytes + c * C::kBoxBytes, &tm_q, &bar_q[t], c * kBoxCols,
-                          x.u * kUnitRows + t * kBlockQ, h, b);
+                          UNIT == 1 ? x.u * kBlockQ : x.u * 2 * kBlockQ + t * kBlockQ, h, b);
           }
           ++nload[t];
         }
@@ -414,6 +423,31 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           if (x.u < 0) break;
           have_next = false;
           const int n = x.last() - x.first();
+          if constexpr (UNIT == 1) {
+            // Block j from the end belongs to slot j & 1; every ring item has one user.
+            for (int j = -2; ok && j < n; ++j) {
+              const int t = j & 1;
+              if (j >= 0) {  // O_t += P_t V_j
+                const int slot = item % C::kSlots;
+                if (!(ok = mbar_wait(&bar_full[slot], (item / C::kSlots) & 1, wc, kSiteMmaV))) break;
+                if (!(ok = mbar_wait(&bar_p[t], (j >> 1) & 1, wc, kSiteMmaP))) break;
+                ++item;
+                tc_fence_after();
+                pv(t, slot, j >= 2);
+                mma_commit(&bar_empty[slot]);
+                if (j + 2 >= n) mma_commit(&bar_o[t]);
+              }
+              if (j + 2 < n) {  // S_t = Q K_{j + 2}^T
+                const int slot = item % C::kSlots;
+                if (!(ok = mbar_wait(&bar_full[slot], (item / C::kSlots) & 1, wc, kSiteMmaK))) break;
+                if (j < 0 && !(ok = mbar_wait(&bar_q[t], 0, wc, kSiteMmaQ))) break;
+                ++item;
+                tc_fence_after();
+                qk(t, slot);
+                mma_commit(&bar_empty[slot]);
+              }
+            }
+          } else
           // Stream position s: K_s is ring item 2 s, V_s item 2 s + 1 of the unit.  S_t of position
           // s is issued right after the P_t V of position s - 1 (position 0: before the loop).
           for (int s = -1; ok && s < n; ++s) {
@@ -504,6 +538,11 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       float slope2;
     } nu;
     bool have_next = false;
+    struct {  // a halved unit's result in this slot
+      bool done;
+      float m, l;
+      int nkt, bh, qrow;
+    } mine{};
     auto read_unit = [&]() {
       nu.u = s_unit->u;
       nu.bh = s_unit->bh;
@@ -513,7 +552,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       nu.all_hi = s_unit->all_hi[t];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_unit_read);
-      const int qrow = nu.u * kUnitRows + t * kBlockQ + row;
+      const int qrow = (UNIT == 1 ? nu.u * kBlockQ : nu.u * 2 * kBlockQ + t * kBlockQ) + row;
       nu.see = make_int2(0, 0);
       nu.slope2 = 0.f;
       if (nu.u >= 0) {
@@ -528,13 +567,14 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       have_next = false;
       if (nu.u < 0) break;
       const int bh = nu.bh, b = bh / p.H, h = bh % p.H;
-      const int row0 = nu.u * kUnitRows + t * kBlockQ;
-      if (t * kBlockQ >= kUnitRows || row0 >= p.N) continue;
+      const int row0 = UNIT == 1 ? nu.u * kBlockQ : nu.u * 2 * kBlockQ + t * kBlockQ;
+      if (row0 >= p.N) continue;
       const int qrow = row0 + row;
       const int2 see = nu.see;
       const float slope2 = nu.slope2;
       // Keys that every row of the tile sees: [all_lo, all_hi).
-      const int all_lo = nu.all_lo, all_hi = nu.all_hi, blk1 = nu.blk1, nkt = nu.blk1 - nu.blk0;
+      const int all_lo = nu.all_lo, all_hi = nu.all_hi, blk1 = nu.blk1;
+      const int nkt = UNIT == 1 ? (nu.blk1 - nu.blk0 - t + 1) / 2 : nu.blk1 - nu.blk0;
       // Reference maximum, log2 units (0 until the row has seen a key).  kBounded: the largest bias
       // among the row's keys: 0, at the row's own position, or for a negative slope at its farthest.
       float m_used = 0.f;
@@ -548,7 +588,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       for (int j = 0; j < nkt; ++j, ++scnt) {
         ok = warp_wait_suspend(&bar_s[t], scnt & 1, wc, kSiteSoftS) && ok;
         tc_fence_after();
-        const int kbase = (blk1 - 1 - j) * kBlockK;
+        const int kbase = (blk1 - 1 - (UNIT == 1 ? 2 * j + t : j)) * kBlockK;
         const bool need_mask = kbase < all_lo || kbase + kBlockK > all_hi;
         const bool left = one_sided || kbase + kBlockK - 1 <= row0, right = kbase >= row0 + kBlockQ - 1;
         float2 part = make_float2(0.f, 0.f);
@@ -816,6 +856,10 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         tc_fence_after();
       }
       if (!ok) continue;
+      if constexpr (UNIT == 1) {
+        mine = {true, m_used, l, nkt, bh, qrow};
+        continue;
+      }
       // O straight to memory, 16 bytes a store: staging it for a TMA store would need 32 KB that the
       // two tiles share, so one tile's epilogue would wait for the other's, and it costs ring slots.
       const bool any_key = l > 0.f;
@@ -844,6 +888,69 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       if (half == 0 && qrow < p.N)
         p.lse[static_cast<size_t>(bh) * p.N + qrow] = any_key ? (m_used + log2f(l)) * kLn2 : -INFINITY;
     }
+    if constexpr (UNIT == 1) {
+      // The two slots' softmaxes of the same rows, joined: slot 1 leaves m and l (where its Q was) and O (column
+      // by column in the ring, which both slots' products have finished with), slot 0 writes the rows. Every
+      // softmax thread comes to the barrier, whatever it met before.
+      float2* ml = reinterpret_cast<float2*>(sQ + C::kTileBytes);
+      float* other = reinterpret_cast<float*>(sRing);
+      constexpr int kChunks = D / 32 / kParts;  // of 32 columns of this thread
+      if (t == 1) {
+        if (mine.nkt > 0) mine.done = mine.done && warp_wait(&bar_o[0], 0, wc, kSiteSoftO);
+        if (mine.done && mine.nkt > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
+            uint32_t o[32];
+            tmem_ld32(trow + col_o + c * 32, o);
+            tmem_ld_wait32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) other[(c * 32 + i) * kBlockQ + row] = __uint_as_float(o[i]);
+          }
+          tc_fence_before();
+        }
+        if (half == 0) ml[row] = mine.done ? make_float2(mine.m, mine.l) : make_float2(0.f, 0.f);
+      }
+      asm volatile("bar.sync 15, %0;" ::"n"(32 * R::kSoftWarps) : "memory");
+      if (t == 0 && mine.done) {
+        tc_fence_after();
+        const float2 b1 = ml[row];
+        const bool any0 = mine.l > 0.f, any1 = b1.y > 0.f;
+        const float m = any0 && any1 ? fmaxf(mine.m, b1.x) : any0 ? mine.m : b1.x;
+        const float a0 = any0 ? ex2_approx(mine.m - m) : 0.f, a1 = any1 ? ex2_approx(b1.x - m) : 0.f;
+        const float l = a0 * mine.l + a1 * b1.y;
+        const bool any_key = any0 || any1;
+        const float f0 = any0 ? a0 / l : 0.f, f1 = any1 ? a1 / l : 0.f;
+        uint4* orow = reinterpret_cast<uint4*>(p.o + mine.bh / p.H * p.so.s[2] + mine.bh % p.H * p.so.s[1] +
+                                               static_cast<int64_t>(mine.qrow) * p.so.s[0]);
+#pragma unroll 1
+        for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
+          uint32_t o[32];
+          if (mine.nkt > 0) {
+            tmem_ld32(trow + col_o + c * 32, o);
+            tmem_ld_wait32(o);
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {  // (a slot without keys counts as 0 whatever it holds)
+            float2 y = any0 ? __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), pair(f0))
+                            : make_float2(0.f, 0.f);
+            if (any1)
+              y = __ffma2_rn(make_float2(other[(c * 32 + 2 * i) * kBlockQ + row], other[(c * 32 + 2 * i + 1) * kBlockQ + row]),
+                             pair(f1), y);
+            pk[i] = pack_bf16x2(y.x, y.y);
+          }
+          if (mine.qrow < p.N) {
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+              orow[c * 4 + q4] = make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
+          }
+        }
+        tc_fence_before();
+        if (half == 0 && mine.qrow < p.N)
+          p.lse[static_cast<size_t>(mine.bh) * p.N + mine.qrow] = any_key ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
     __syncwarp();
   }
 
@@ -855,10 +962,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
   }
 }
 
-// One tile where all units of one run at once: a tile by itself takes less time than two that share an SM
-// (causal, d = 128: B=1 H=2 N=6063 91 -> 72 us, H=16 N=1030 21.4 -> 18.1; H=4 N=129 d=64 capped 9.3 -> 7.9).
-// Where they do not, two tiles overlap each other's waits (H=6 N=4096 64.6 us, full, in units of two tiles;
-// 98.8 in units of one).
+// Halved units of one tile where all of them run at once.
 int unit_tiles(const FwdArgs& a) {
   const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * a.B * a.H;
   return tiles <= sm_count() ? 1 : 2;
