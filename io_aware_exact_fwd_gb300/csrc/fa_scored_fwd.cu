@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
           *s_unit = x;
           mbar_arrive(bar_unit);
           if (w < 0) break;
-          if (UNIT == 1) {  // all blocks run at once: there is nothing to take over
+          if (UNIT == 1) {  // (its results leave the ring and TMEM in use: one unit a block)
             w = -1;
             continue;
           }
@@ -962,10 +962,14 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
   }
 }
 
-// Halved units of one tile where all of them run at once.
-int unit_tiles(const FwdArgs& a) {
+// Halved units of one tile (1) or units of two (2).  A halved unit takes its blocks in 0.6 of the time of one
+// of two tiles, which has twice the rows: better where its longest unit sets the time.  That is so
+// while all run at once (full, d = 128, H=2 N=6063: 93 us in units of two tiles, 55 halved), and where the mask
+// makes units differ also in twice as many (causal, H=16 N=2048 35.8 | 27.8; H=6 N=4096 64.3 | 39.0; three documents,
+// H=8 N=3737 59.0 | 35.3).  Beyond, the throughput counts (causal, B=8 H=16 N=300 17.2 | 23.8; H=32 N=4096 124 | 154).
+int unit_tiles(const FwdArgs& a, const ScoreArgs& sc) {
   const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * a.B * a.H;
-  return tiles <= sm_count() ? 1 : 2;
+  return tiles <= (sc.causal || sc.plan.q ? 2 : 1) * sm_count() ? 1 : 2;
 }
 
 template <int D, int MODE, int UNIT>
@@ -1020,7 +1024,7 @@ cudaError_t launch_unit(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
 
 template <int D>
 cudaError_t launch_d(const FwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  return unit_tiles(a) == 1 ? launch_unit<D, 1>(a, sc, stream) : launch_unit<D, 2>(a, sc, stream);
+  return unit_tiles(a, sc) == 1 ? launch_unit<D, 1>(a, sc, stream) : launch_unit<D, 2>(a, sc, stream);
 }
 
 }  // namespace
