@@ -107,6 +107,41 @@ def test_forward_and_gradients(case, layout):
     report(f"scored {case} {layout} (shares of the bounds)", **r)
 
 
+# More tiles and key blocks than the SMs run at once: units of two tiles, taken over by running blocks, and undivided
+# key blocks (the cases above are mostly of halved units and divided blocks).
+MANY = [
+    (2, 32, 32, 700, 64, True, 0.0, False, None, None),
+    (2, 32, 8, 700, 128, True, 0.0, True, [[0, 130, 400, 690], [20, 300, 301, 650]], [[100, 3, 0], [0, 1, 200]]),
+    (2, 32, 32, 700, 128, True, 20.0, False, [[0, 130, 400, 690], [20, 300, 301, 650]], None),
+    (2, 32, 32, 700, 64, True, 20.0, True, None, None),
+    (2, 32, 8, 700, 128, True, 60.0, True, None, None),
+    (2, 32, 16, 700, 64, True, 0.0, True, [[0, 700], [300, 690]], None),
+    (2, 32, 16, 700, 64, True, 30.0, False, [[0, 690], [30, 400]], [[200], [5]]),
+    (5, 16, 16, 300, 128, False, 0.0, True, None, None),
+    (5, 16, 16, 300, 64, False, 60.0, False, None, None),
+    (20, 16, 4, 130, 128, True, 20.0, True, [[5 * (b % 3), 20 + b, 60 + 3 * b, 130 - b] for b in range(20)], None),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_many_tiles(case):
+    B, H, Hkv, N, d, causal, cap, bias, cu, pre = case
+    q, k, v, do = _inputs(B, H, Hkv, N, d, 31 + N, 3.0 if cap else 1.0)
+    plan = _docs(cu, pre, causal, B, N)
+    kw = _kw(case, plan)
+    args = (d ** -0.5, causal, cap, None if not bias else _slopes(H).cpu().numpy(), cu, pre)
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    grads = fa.fa_bwd_scored(q, k, v, o, do, lse, **kw)
+    fa.fa_sync_check()
+    x = [host_f64(t) for t in (q, k, v, do)]
+    o_ref, lse_ref, ob, lb = scored_forward(*x[:3], *args)
+    r = {"o": _check(o, o_ref, ob, "O"), "lse": _check(lse, lse_ref, lb, "LSE")}
+    refs, bounds = scored_backward(*x, *args)
+    for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
+        r[name] = _check(a, ref, bd, name)
+    report(f"scored {case[:8]} (shares of the bounds)", **r)
+
+
 @pytest.mark.parametrize("cap", [0.0, 10.0, 55.0, 60.0, 1000.0])
 def test_large_scores_and_slopes(cap):
     # Scores far past the cap on both sides (or without one), and slopes that leave only the nearest
@@ -128,9 +163,10 @@ def test_large_scores_and_slopes(cap):
             _check(a, ref, bd, name)
 
 
-def test_scores_that_fall_and_rise_along_the_keys():
+@pytest.mark.parametrize("H", [1, 62])
+def test_scores_that_fall_and_rise_along_the_keys(H):
     # Row maxima far apart between key blocks, both ways, without a cap: -400 to 400.
-    B, H, N, d = 1, 1, 640, 64
+    B, N, d = 1, 640, 64
     q, k, v, do = _inputs(B, H, H, N, d, 6)
     ramp = torch.linspace(-1, 1, N, device="cuda")[None, None, :, None]
     for sign in (1.0, -1.0):
@@ -156,10 +192,11 @@ def test_without_options_it_agrees_with_fa_fwd():
         assert float((o.float() - o1.float()).abs().max()) <= 2 * 2.0 ** -7 * float(v.float().abs().max())
 
 
-def test_same_bits_on_every_run():
-    q, k, v, do = _inputs(1, 4, 2, 700, 64, 9, 3.0)
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (64, 32)])
+def test_same_bits_on_every_run(H, Hkv):
+    q, k, v, do = _inputs(1, H, Hkv, 700, 64, 9, 3.0)
     plan = _docs([[0, 300, 690]], [[20, 50]], True, 1, 700)
-    kw = dict(softcap=20.0, slopes=_slopes(4), plan=plan)
+    kw = dict(softcap=20.0, slopes=_slopes(H), plan=plan)
     runs = []
     for _ in range(3):
         o, lse = fa.fa_fwd_scored(q, k, v, **kw)
