@@ -965,11 +965,12 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
 // Halved units of one tile (1) or units of two (2).  A halved unit takes its blocks in 0.6 of the time of one
 // of two tiles, which has twice the rows: better where its longest unit sets the time.  That is so
 // while all run at once (full, d = 128, H=2 N=6063: 93 us in units of two tiles, 55 halved), and where the mask
-// makes units differ also in twice as many (causal, H=16 N=2048 35.8 | 27.8; H=6 N=4096 64.3 | 39.0; three documents,
-// H=8 N=3737 59.0 | 35.3).  Beyond, the throughput counts (causal, B=8 H=16 N=300 17.2 | 23.8; H=32 N=4096 124 | 154).
+// makes units of long rows differ also in twice as many (causal, H=16 N=2048 35.8 | 27.8; H=6 N=4096 64.3 | 39.0;
+// three documents, H=8 N=3737 59.0 | 35.3).  With shorter rows or more units the throughput counts (causal, B=2 H=16
+// N=964 d=64 19.6 | 20.5; B=6 H=32 N=7 12.3 | 15.0; B=8 H=16 N=300 17.2 | 23.8; H=32 N=4096 124 | 154).
 int unit_tiles(const FwdArgs& a, const ScoreArgs& sc) {
   const long long tiles = static_cast<long long>((a.N + kBlockQ - 1) / kBlockQ) * a.B * a.H;
-  return tiles <= (sc.causal || sc.plan.q ? 2 : 1) * sm_count() ? 1 : 2;
+  return tiles <= ((sc.causal || sc.plan.q) && a.N > 8 * kBlockK ? 2 : 1) * sm_count() ? 1 : 2;
 }
 
 template <int D, int MODE, int UNIT>
