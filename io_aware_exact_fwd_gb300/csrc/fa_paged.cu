@@ -17,52 +17,71 @@ __device__ __forceinline__ int tokens_of(const PagedCache& c, int b) {
   return min(max(c.seq_lens[b], 0), c.max_pages * c.page_size);
 }
 
-// Append: one warp a new token, 16 bytes a lane, up to four pieces of K and of V a lane in
-// flight while the token's sequence, position and page are looked up, once a warp.  Bound
-// by HBM: the new rows are read once and written once.  Measured with 8 heads x 128: 35k
-// tokens in 45.6 us, 6.3 TB/s; 64 tokens in 4.1 us, a launch and three dependent loads.
-// (One 16-byte piece a thread, each with its own look-up: 49.1 us.)
-__global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a) {
-  const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  if (t >= a.T) return;
-  const uint16_t* ks = static_cast<const uint16_t*>(a.k) + t * a.sk.s[1];
-  const uint16_t* vs = static_cast<const uint16_t*>(a.v) + t * a.sv.s[1];
-  const int shift = a.c.d == 64 ? 3 : 4, pieces = a.c.Hkv << shift;  // a head's row is 8 or 16 pieces
+// Append: a warp takes as many consecutive new tokens as make up to 128 pieces of 16 bytes of K (one token from 128
+// on), up to four pieces of K and of V a lane in flight while its first lanes look the tokens' places up, a token
+// each.  Bound by HBM: the new rows are read once and written once.  Measured with 8 heads x 128: 35k tokens in 45.6
+// us, 6.3 TB/s; 64 tokens in 4.1 us, a launch and three dependent loads; 29k tokens of one head x 128 in 5.2 us, 5.8
+// TB/s.  (One 16-byte piece a thread, each with its own look-up: 49.1 us for the first; one token a warp: 11.6 for the
+// last.)
+__global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, int per_warp) {
+  const long long first = ((static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5) * per_warp;
+  if (first >= a.T) return;
+  const int t0 = static_cast<int>(first), lane = threadIdx.x & 31, tokens = min(per_warp, a.T - t0);
+  const int shift = a.c.d == 64 ? 3 : 4, row = a.c.Hkv << shift;  // pieces of a head's row: 8 or 16; of a token's
+  const int pieces = tokens * row;
+  const uint16_t* ks = static_cast<const uint16_t*>(a.k) + t0 * a.sk.s[1];
+  const uint16_t* vs = static_cast<const uint16_t*>(a.v) + t0 * a.sv.s[1];
+  // Piece x: token t, head h, column col.
+  auto piece = [&](int x, int& t, int& h, int& col) {
+    t = per_warp == 1 ? 0 : x / row;
+    x -= t * row;
+    h = x >> shift;
+    col = (x & ((1 << shift) - 1)) * 8;
+  };
   uint4 kv[4], vv[4];
   auto load = [&](int p0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int x = p0 + 32 * i, h = x >> shift, col = (x & ((1 << shift) - 1)) * 8;
+      const int x = p0 + 32 * i;
+      int t, h, col;
+      piece(x, t, h, col);
       if (x < pieces) {
-        kv[i] = *reinterpret_cast<const uint4*>(ks + h * a.sk.s[0] + col);
-        vv[i] = *reinterpret_cast<const uint4*>(vs + h * a.sv.s[0] + col);
+        kv[i] = *reinterpret_cast<const uint4*>(ks + t * a.sk.s[1] + h * a.sk.s[0] + col);
+        vv[i] = *reinterpret_cast<const uint4*>(vs + t * a.sv.s[1] + h * a.sv.s[0] + col);
       }
     }
   };
-  load(lane);  // in flight while the place is looked up
-  int lo = 0, hi = a.c.B + 1;  // the number of offsets <= t
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(a.cu_new + mid) <= t) lo = mid + 1;
-    else hi = mid;
+  load(lane);  // in flight while the places are looked up
+  int page = -1, off = 0;
+  if (lane < tokens) {
+    const int t = t0 + lane;
+    int lo = 0, hi = a.c.B + 1;  // the number of offsets <= t
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(a.cu_new + mid) <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo != 0 && lo != a.c.B + 1) {  // (else a row of no sequence)
+      const int b = lo - 1;
+      const long long pos = static_cast<long long>(a.c.seq_lens[b]) - (static_cast<long long>(a.cu_new[lo]) - t);
+      if (pos >= 0 && pos < static_cast<long long>(a.c.max_pages) * a.c.page_size) {
+        off = static_cast<int>(pos) % a.c.page_size;
+        page = a.c.page_table[b * a.c.table_stride + static_cast<int>(pos) / a.c.page_size];
+        if (page >= a.c.n_pages) page = -1;
+      }
+    }
   }
-  if (lo == 0 || lo == a.c.B + 1) return;  // a row of no sequence
-  const int b = lo - 1;
-  const long long pos = static_cast<long long>(a.c.seq_lens[b]) - (static_cast<long long>(a.cu_new[lo]) - t);
-  if (pos < 0 || pos >= static_cast<long long>(a.c.max_pages) * a.c.page_size) return;
-  const int at = static_cast<int>(pos) / a.c.page_size, off = static_cast<int>(pos) % a.c.page_size;
-  const int page = a.c.page_table[b * a.c.table_stride + at];
-  if (page < 0 || page >= a.c.n_pages) return;
-  uint16_t* kd = static_cast<uint16_t*>(a.c.k) + page * a.c.sk.s[2] + off * a.c.sk.s[0];
-  uint16_t* vd = static_cast<uint16_t*>(a.c.v) + page * a.c.sv.s[2] + off * a.c.sv.s[0];
-  for (int p0 = lane; p0 < pieces; p0 += 128) {
+  for (int p0 = lane; p0 - lane < pieces; p0 += 128) {
     if (p0 != lane) load(p0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int x = p0 + 32 * i, h = x >> shift, col = (x & ((1 << shift) - 1)) * 8;
-      if (x < pieces) {
-        *reinterpret_cast<uint4*>(kd + h * a.c.sk.s[1] + col) = kv[i];
-        *reinterpret_cast<uint4*>(vd + h * a.c.sv.s[1] + col) = vv[i];
+      const int x = p0 + 32 * i;
+      int t, h, col;
+      piece(x, t, h, col);
+      const int pg = __shfl_sync(0xffffffffu, page, t), r = __shfl_sync(0xffffffffu, off, t);
+      if (x < pieces && pg >= 0) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + pg * a.c.sk.s[2] + r * a.c.sk.s[0] + h * a.c.sk.s[1] + col) = kv[i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + pg * a.c.sv.s[2] + r * a.c.sv.s[0] + h * a.c.sv.s[1] + col) = vv[i];
       }
     }
   }
@@ -719,7 +738,9 @@ cudaError_t launch_decode_mt(const PagedDecodeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  paged_append_kernel<<<static_cast<unsigned>((static_cast<long long>(a.T) + 3) / 4), 128, 0, stream>>>(a);
+  const int per_warp = std::max(1, 128 / (a.c.Hkv * (a.c.d / 8)));
+  const long long warps = (static_cast<long long>(a.T) + per_warp - 1) / per_warp;
+  paged_append_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(a, per_warp);
   return cudaGetLastError();
 }
 
