@@ -17,12 +17,13 @@ __device__ __forceinline__ int tokens_of(const PagedCache& c, int b) {
   return min(max(c.seq_lens[b], 0), c.max_pages * c.page_size);
 }
 
-// Append: a warp takes as many consecutive new tokens as make up to 128 pieces of 16 bytes of K (one token from 128
-// on), up to four pieces of K and of V a lane in flight while its first lanes look the tokens' places up, a token
+// Append: a warp takes as many consecutive new tokens as make up to 128 pieces of 16 bytes of K (one if there are
+// few), up to four pieces of K and of V a lane in flight while its first lanes look the tokens' places up, a token
 // each.  Bound by HBM: the new rows are read once and written once.  Measured with 8 heads x 128: 35k tokens in 45.6
 // us, 6.3 TB/s; 64 tokens in 4.1 us, a launch and three dependent loads; 29k tokens of one head x 128 in 5.2 us, 5.8
 // TB/s.  (One 16-byte piece a thread, each with its own look-up: 49.1 us for the first; one token a warp: 11.6 for the
 // last.)
+template <bool ONE>  // per_warp is 1
 __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, int per_warp) {
   const long long first = ((static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5) * per_warp;
   if (first >= a.T) return;
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, in
   const uint16_t* vs = static_cast<const uint16_t*>(a.v) + t0 * a.sv.s[1];
   // Piece x: token t, head h, column col.
   auto piece = [&](int x, int& t, int& h, int& col) {
-    t = per_warp == 1 ? 0 : x / row;
+    t = ONE ? 0 : x / row;
     x -= t * row;
     h = x >> shift;
     col = (x & ((1 << shift) - 1)) * 8;
@@ -53,8 +54,8 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, in
   };
   load(lane);  // in flight while the places are looked up
   int page = -1, off = 0;
-  if (lane < tokens) {
-    const int t = t0 + lane;
+  if (ONE || lane < tokens) {
+    const int t = ONE ? t0 : t0 + lane;
     int lo = 0, hi = a.c.B + 1;  // the number of offsets <= t
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -71,17 +72,25 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, in
       }
     }
   }
-  for (int p0 = lane; p0 - lane < pieces; p0 += 128) {
+  if (ONE && page < 0) return;
+  long long k_at = page * a.c.sk.s[2] + off * a.c.sk.s[0], v_at = page * a.c.sv.s[2] + off * a.c.sv.s[0];
+  for (int p0 = lane; ONE ? p0 < pieces : p0 - lane < pieces; p0 += 128) {
     if (p0 != lane) load(p0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int x = p0 + 32 * i;
       int t, h, col;
       piece(x, t, h, col);
-      const int pg = __shfl_sync(0xffffffffu, page, t), r = __shfl_sync(0xffffffffu, off, t);
-      if (x < pieces && pg >= 0) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + pg * a.c.sk.s[2] + r * a.c.sk.s[0] + h * a.c.sk.s[1] + col) = kv[i];
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + pg * a.c.sv.s[2] + r * a.c.sv.s[0] + h * a.c.sv.s[1] + col) = vv[i];
+      bool here = x < pieces;
+      if (!ONE) {
+        const int pg = __shfl_sync(0xffffffffu, page, t), r = __shfl_sync(0xffffffffu, off, t);
+        here = here && pg >= 0;
+        k_at = pg * a.c.sk.s[2] + r * a.c.sk.s[0];
+        v_at = pg * a.c.sv.s[2] + r * a.c.sv.s[0];
+      }
+      if (here) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + k_at + h * a.c.sk.s[1] + col) = kv[i];
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + v_at + h * a.c.sv.s[1] + col) = vv[i];
       }
     }
   }
@@ -738,9 +747,12 @@ cudaError_t launch_decode_mt(const PagedDecodeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int per_warp = std::max(1, 128 / (a.c.Hkv * (a.c.d / 8)));
+  // More than one token a warp only past 16 warps an SM (64 tokens of one head: 2.7 us, 3.4 with eight a warp).
+  const int per_warp = std::max(1, std::min(128 / (a.c.Hkv * (a.c.d / 8)), a.T / (16 * sm_count())));
   const long long warps = (static_cast<long long>(a.T) + per_warp - 1) / per_warp;
-  paged_append_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(a, per_warp);
+  const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
+  if (per_warp == 1) paged_append_kernel<true><<<grid, 128, 0, stream>>>(a, per_warp);
+  else paged_append_kernel<false><<<grid, 128, 0, stream>>>(a, per_warp);
   return cudaGetLastError();
 }
 

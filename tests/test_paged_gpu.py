@@ -322,6 +322,22 @@ def test_append_of_many_heads():
     assert np.array_equal(host_f64(kc), want[0]) and np.array_equal(host_f64(vc), want[1])
 
 
+@pytest.mark.parametrize("Hkv,d", [(1, 64), (3, 64), (1, 128)])
+def test_append_of_many_short_rows(Hkv, d):
+    # More tokens than 16 warps an SM take one each: several tokens a warp, their rows' pieces not a
+    # multiple of its lanes, sequences and pages ending inside a warp's tokens, and rows of no sequence.
+    page, new = 48, [9001, 0, 1, 12345, 77, 3]
+    lens = [n + 5 * b for b, n in enumerate(new)]
+    kc, vc, table, n = _cache(lens, Hkv, d, page, torch.float16, 29)
+    T = sum(new) + 7
+    x = torch.randn(T, 2, Hkv, d, generator=torch.Generator().manual_seed(30)).half().cuda()
+    cu = np.concatenate([[0], np.cumsum(new)])
+    want = [paged_append(host_f64(x[:, i]), host_f64(c), table.tolist(), lens, cu) for i, c in enumerate((kc, vc))]
+    fa.fa_paged_append(x[:, 0], x[:, 1], kc, vc, table, n, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    fa.fa_sync_check()
+    assert np.array_equal(host_f64(kc), want[0]) and np.array_equal(host_f64(vc), want[1])
+
+
 def test_two_graphs_share_a_workspace():
     # Captured for two batches of other sizes over one workspace and replayed in turn on one stream.
     kc, vc, table, n = _cache([700, 90, 333], 2, 64, 16, torch.bfloat16, 25)
