@@ -160,6 +160,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   // This part's steps: n from the first on, that one being block i_first of head head_first.
   const int first = st.n * part / parts, n = st.n * (part + 1) / parts - first;
   const int head_first = DIVIDED && n > 0 ? first / st.nq : 0, i_first = st.i0 + first - head_first * st.nq;
+  auto load_q_do = [&](int slot, int g, int i) {
+    uint8_t* dst = sRing + slot * C::kStageBytes;
+    mbar_arrive_expect_tx(&bar_full[slot], C::kStageTx);
+    for (int c = 0; c < C::kBoxes; ++c) {
+      tma_load_4d(dst + C::kStageQ + c * C::kQBox, &tm_q, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
+      tma_load_4d(dst + C::kStageDO + c * C::kQBox, &tm_do, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
+    }
+  };
+  // Q and dO of the first steps do not wait for the preprocess either; their LSE and D follow in the producer.
+  if (threadIdx.x == kWarpLoad * 32)
+    for (int it = 0, g = head_first, i = i_first; it < min(n, kStages); ++it) {
+      load_q_do(it, g, i);
+      if (++i == st.i0 + st.nq) {
+        i = st.i0;
+        ++g;
+      }
+    }
   {
     // The extra K-step's key-side tiles (BwdCfg), one 16-byte half-row per thread.
     const int tile = threadIdx.x >> 8, krow = (threadIdx.x >> 1) & 127, half = threadIdx.x & 1;
@@ -196,11 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = it % kStages;
           if (!mbar_wait(&bar_empty[slot], ((it / kStages) & 1) ^ 1, wc, kSiteBLoad)) break;
           uint8_t* dst = sRing + slot * C::kStageBytes;
-          mbar_arrive_expect_tx(&bar_full[slot], C::kStageTx);
-          for (int c = 0; c < C::kBoxes; ++c) {
-            tma_load_4d(dst + C::kStageQ + c * C::kQBox, &tm_q, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
-            tma_load_4d(dst + C::kStageDO + c * C::kQBox, &tm_do, &bar_full[slot], c * 64, i * kBqB, h0 + g, b_idx);
-          }
+          if (it >= kStages) load_q_do(slot, g, i);
           bulk_load(dst + C::kStageAug, p.aug + ((bh0 + g) * head_blocks + i) * (2 * C::kAugTile), 2 * C::kAugTile,
                     &bar_full[slot]);
           ++issued;
