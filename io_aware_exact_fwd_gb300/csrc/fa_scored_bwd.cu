@@ -54,7 +54,7 @@ namespace {
 
 struct Params {
   MaskPlan plan;
-  int causal, N, Npad, H, Hkv, group, nkb, parts;
+  int causal, N, Npad, H, Hkv, group, nkb, parts, run;
   float scale, scale_log2;
   float cap_in, cap_out;  // 4 scale / softcap (products to x = 4 u), softcap log2(e)
   CapPoly poly;           // factor 1
@@ -121,12 +121,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // Key blocks in order, heads next to one another: causal key blocks near the start see
-  // the most queries and go first.
+  // Heads in runs of p.run: within one, key blocks in order and heads next to one another; causal key
+  // blocks near the start see the most queries and go first.
   const int parts = DIVIDED ? p.parts : 1;
   const int unit = static_cast<int>(blockIdx.x) / parts, part = static_cast<int>(blockIdx.x) % parts;
   const int kvheads = static_cast<int>(gridDim.x) / parts / p.nkb;  // B Hkv
-  const int kb = unit / kvheads, bhk = unit % kvheads;
+  const int run0 = unit / (p.run * p.nkb) * p.run, run = min(p.run, kvheads - run0), in_run = unit - run0 * p.nkb;
+  const int kb = in_run / run, bhk = run0 + in_run % run;
   const int hk = bhk % p.Hkv, b_idx = bhk / p.Hkv;
   const int h0 = hk * p.group;               // first query head of the group
   const int bh0 = b_idx * p.H + h0;
@@ -602,6 +603,18 @@ int parts_of(int B, int H, int Hkv, int N) {
   return static_cast<int>(std::max(1ll, std::min({16ll, 2 * sm_count() / blocks, steps / 8})));
 }
 
+// Key/value heads worked on together: as many as have dQ accumulators of 48 MB, which then stay in the L2 (129 MB, with
+// what else passes through it) between the adds of a head's key blocks (d = 128: B=16 H=16 N=1024 causal 373 us over
+// all heads at once, 297 in runs; B=2 H=16 N=8192 1185 | 1107-1132, full 2231 | 2133-2156; d = 64, H=32 N=8192 biased
+// 1771 | 1688).  The last run's heavy blocks start late, so only with 10 blocks an SM or more (6.7: B=2
+// H=32/8 N=8192 of eight documents 653 us, 745 in runs).
+int run_of(int B, int H, int Hkv, int N, int d) {
+  const long long heads = static_cast<long long>(B) * Hkv, blocks = (N + kBkB - 1) / kBkB * heads;
+  if (blocks < 10ll * sm_count()) return static_cast<int>(heads);
+  const long long bytes = static_cast<long long>(H / Hkv) * N * d * static_cast<long long>(sizeof(float));
+  return static_cast<int>(std::max(1ll, std::min(heads, 48000000ll / bytes)));
+}
+
 template <int D, int MODE, bool DET, bool DIVIDED>
 cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, int parts, cudaStream_t stream) {
   using C = BwdCfg<D>;
@@ -626,6 +639,7 @@ cudaError_t launch_main(const BwdArgs& a, const ScoreArgs& sc, int parts, cudaSt
   p.group = a.group;
   p.nkb = (a.N + kBkB - 1) / kBkB;
   p.parts = parts;
+  p.run = run_of(a.B, a.H, sc.Hkv, a.N, D);
   p.part_sums = reinterpret_cast<float*>(ws + w.total);
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
