@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       }
       // O straight to memory, 16 bytes a store: staging it for a TMA store would need 32 KB that the
       // two tiles share, so one tile's epilogue would wait for the other's, and it costs ring slots.
-      const bool any_key = l > 0.f;
+      const bool any_key = l != 0.f;  // a row without keys has exactly 0; a NaN sum is a NaN result
       const float inv_l = any_key ? 1.f / l : 0.f;
       uint4* orow = reinterpret_cast<uint4*>(p.o + b * p.so.s[2] + h * p.so.s[1] + static_cast<int64_t>(qrow) * p.so.s[0]);
 #pragma unroll 1
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
       if (t == 0 && mine.done) {
         tc_fence_after();
         const float2 b1 = ml[row];
-        const bool any0 = mine.l > 0.f, any1 = b1.y > 0.f;
+        const bool any0 = mine.l != 0.f, any1 = b1.y != 0.f;  // (a NaN counts)
         const float m = any0 && any1 ? fmaxf(mine.m, b1.x) : any0 ? mine.m : b1.x;
         const float a0 = any0 ? ex2_approx(mine.m - m) : 0.f, a1 = any1 ? ex2_approx(b1.x - m) : 0.f;
         const float l = a0 * mine.l + a1 * b1.y;

@@ -408,3 +408,44 @@ def test_many_heads_in_runs_agree_with_their_rows_alone():
                 if det or name != "dq":  # (dq's fp32 sums have no fixed order)
                     assert torch.equal(whole[b:b + 5], alone), (name, b)
     fa.fa_sync_check()
+
+
+def _spoil(x, at, value):
+    y = x.clone()
+    y[at] = value
+    return y
+
+
+# 300 rows of two heads are halved units, 400 rows of 80 heads units of two tiles.
+@pytest.mark.parametrize("B,H,N", [(1, 2, 300), (2, 40, 400)])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (0.0, True), (20.0, False), (20.0, True), (60.0, False), (60.0, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_and_infinities_come_through(B, H, N, cap, bias, d):
+    # One entry of a key, or of a query, is NaN or infinite.  What the definition makes of it (NaN, or a
+    # finite result where the cap or a weight of 0 absorbs an infinity) has to come out in the rows that
+    # see it, and in no other.
+    from oracle.scored import _score_error
+
+    q, k, v, _ = _inputs(B, H, H, N, d, 51)
+    slopes = _slopes(H) if bias else None
+    s0 = [float(slopes[0])] if bias else None
+    clean = [host_f64(t[:1, :1]) for t in (q, k, v)]
+    # The bound of scored_forward, with sum P |v| replaced by the largest |v| (P of the spoilt rows is another).
+    err = _score_error(clean[0][0, 0], clean[1][0, 0], d ** -0.5, cap, s0[0] if bias else 0.0, d)
+    for name, at in (("key", 77), ("query", 200)):
+        for value in (float("nan"), float("inf"), float("-inf")):
+            spoilt = [_spoil(t, (0, 0, at, 5), value) if name == n else t for n, t in (("query", q), ("key", k))]
+            for causal in (True, False):
+                o, lse = fa.fa_fwd_scored(*spoilt, v, causal=causal, softcap=cap, slopes=slopes)
+                fa.fa_sync_check()
+                with np.errstate(invalid="ignore"):
+                    o_ref, lse_ref, _, _ = scored_forward(*(host_f64(t[:1, :1]) for t in (*spoilt, v)), d ** -0.5, causal, cap, s0)
+                ob = (2.0 ** -8 + 3 * err) * 1.01 * np.abs(clean[2]).max() + 2.0 ** -8 * np.abs(o_ref)
+                lb = 2 * err + 4 * 2.0 ** -24 * np.abs(lse_ref)
+                what = f"{name} {value} causal={causal}"
+                for got, ref, bound, n in ((o[:1, :1], o_ref, ob, "O"), (lse[:1, :1], lse_ref, lb, "LSE")):
+                    got = host_f64(got)
+                    assert np.array_equal(np.isnan(got), np.isnan(ref)), f"{n} {what}: NaN in other rows than the definition's"
+                    fin = ~np.isnan(ref)
+                    assert (np.abs(got - ref)[fin] <= bound[fin]).all(), f"{n} {what}"
+                assert torch.isfinite(o[-1, -1]).all() and torch.isfinite(lse[-1, -1]).all(), what
