@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
   for (int m = kTpr / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m, kTpr);
   if (t == 0) {
     uint32_t a[3], dd[3];
-    const float neg_lse2 = lse_row > -INFINITY ? -lse_row * kLog2e : -1e30f;
+    const float neg_lse2 = lse_row == -INFINITY ? -1e30f : -lse_row * kLog2e;  // (a NaN row stays NaN)
     split3_bf16(neg_lse2, a);
     split3_bf16(nrow < N ? -acc : 0.f, dd);
     const int rr = nrow % kBqB;
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
     // multiples of kRpb, which divides 64): reduce to one atomic per block.
 #pragma unroll
     for (int m = kTpr / 2; m >= 1; m >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, m, kTpr);
-    float mx = lse_row > -INFINITY ? sqrtf(nrm) : 0.f;  // 0 for padded rows and rows without keys
+    float mx = lse_row == -INFINITY ? 0.f : sqrtf(nrm);  // 0 for padded rows and rows without keys
 #pragma unroll
     for (int m = kTpr; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
     __shared__ float red[8];

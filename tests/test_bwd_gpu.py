@@ -183,3 +183,17 @@ def test_staged_backward_equals_fa_bwd(causal, d):
     fa.fa_sync_check()
     assert torch.equal(dk, ref[1]) and torch.equal(dv, ref[2])
     assert _rel_err(dq, ref[0].double().cpu().numpy()) <= 1e-2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("causal", [False, True])
+def test_nan_in_a_key_reaches_the_gradients_of_the_others(causal, deterministic, d):
+    # A row that sees the key has a NaN LSE, so dK and dV of every key that the row sees are NaN.
+    q, k, v, do = _inputs(1, 1, 300, d, 61)
+    k[0, 0, 77, 5] = float("nan")
+    o, lse = fa.fa_fwd(q, k, v, causal=causal)
+    _, dk, dv = fa.fa_bwd(q, k, v, o, do, lse, causal=causal, deterministic=deterministic)
+    fa.fa_sync_check()
+    assert bool(torch.isnan(lse[0, 0, 77:]).all())
+    assert bool(torch.isnan(dk).all()) and bool(torch.isnan(dv).all())

@@ -449,3 +449,29 @@ def test_nan_and_infinities_come_through(B, H, N, cap, bias, d):
                     fin = ~np.isnan(ref)
                     assert (np.abs(got - ref)[fin] <= bound[fin]).all(), f"{n} {what}"
                 assert torch.isfinite(o[-1, -1]).all() and torch.isfinite(lse[-1, -1]).all(), what
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (0.0, True), (20.0, False), (20.0, True)])
+@pytest.mark.parametrize("H", [1, 64])  # key blocks whose steps are divided, and whole ones
+def test_nan_in_a_key_reaches_the_gradients_of_its_document(H, cap, bias):
+    # Two documents: every row of the first sees the key, so dK and dV of all its keys are NaN; those of
+    # the second keep their values.
+    B, N, d, cut = 1, 700, 64, 333
+    q, k, v, do = _inputs(B, H, H, N, d, 62)
+    plan = _docs([[0, cut, N]], None, False, B, N)
+    kw = dict(softcap=cap, slopes=_slopes(H) if bias else None, plan=plan)
+    clean = fa.fa_bwd_scored(q, k, v, *_out(q, k, v, do, kw), **kw)
+    k[0, 0, 77, 5] = float("nan")
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    for det in (False, True):
+        _, dk, dv = fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=det, **kw)
+        fa.fa_sync_check()
+        assert bool(torch.isnan(lse[0, 0, :cut]).all()) and bool(torch.isfinite(lse[0, 0, cut:]).all())
+        for got, want in ((dk, clean[1]), (dv, clean[2])):
+            assert bool(torch.isnan(got[0, 0, :cut]).all())
+            assert torch.equal(got[0, 0, cut:], want[0, 0, cut:]) and torch.equal(got[0, 1:], want[0, 1:])
+
+
+def _out(q, k, v, do, kw):
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    return o, do, lse
