@@ -130,7 +130,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 enum : uint32_t { kSiteDecLoad = 0x131, kSiteDecFull = 0x331 };
 
-template <int D, int MT>
+template <int D, int MT, bool FP16>
 struct DecCfg {
   static constexpr int kRows = 16 * MT;                   // query heads per chunk
   static constexpr int kTile = 8192 / D;                  // tokens per tile: K and V of one are 32 KB
@@ -145,6 +145,11 @@ struct DecCfg {
   static constexpr int kBarOff = kMlOff + kConsumers * kRows * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
+  // A row's reference stands this far below its maximum, in log2 units.  P is rounded to the cache's
+  // type; fp16 holds 2^-14 .. 2^15 with all its bits, so with P up to 2^15 weights keep them down to 2^-29 of the
+  // largest and none above 2^-40 is lost (a million tokens of 2^-25 together are 3 % of the one they
+  // follow).  bf16 has fp32's range.  The factor is in l too and cancels.
+  static constexpr float kHeadroom = FP16 ? 15.f : 0.f;
   static_assert(kConsumers * 16 * D * 4 <= kStage, "the warps' O of 16 heads fit a stage");
 };
 
@@ -226,7 +231,7 @@ template <int D, int MT, bool FP16>
 __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ DecParams p) {
-  using C = DecCfg<D, MT>;
+  using C = DecCfg<D, MT, FP16>;
   constexpr int kTile = C::kTile, NB = C::kBlocks;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
           for (int e = 0; e < 2; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            const float mn = fmaxf(m[mt][e], mx[e]);  // finite: the warp has at least one token
+            const float mn = fmaxf(m[mt][e], mx[e] - C::kHeadroom);  // finite: the warp has at least one token
             alpha[e] = ex2_approx(m[mt][e] - mn);
             up |= mn > m[mt][e];
             m[mt][e] = mn;
@@ -695,7 +700,7 @@ size_t part_bytes(int group, int d) {
 
 template <int D, int MT, bool FP16>
 cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
-  using C = DecCfg<D, MT>;
+  using C = DecCfg<D, MT, FP16>;
   DecParams p{};
   p.c = a.c;
   p.q = static_cast<const uint16_t*>(a.q);

@@ -378,3 +378,28 @@ def test_a_stream_given_by_the_caller():
     fa.fa_sync_check()
     for o, lse in got:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("below", [20.0, 25.5, 28.0])
+def test_many_small_weights_behind_a_dominant_token(dtype, below):
+    # The first token weighs 2^below times as much as each of the others and adds nothing to the output,
+    # which is theirs alone.  320 sequences over the same pages: more heads than blocks, so that a block's
+    # warp meets the first token and a quarter of the rest with one reference.
+    B, H, n, d, page = 320, 2, 2055, 64, 16
+    pages = -(-n // page)
+    g = torch.Generator().manual_seed(31)
+    kc = torch.zeros(pages, 1, page, d, dtype=dtype)
+    kc[..., 0] = -below * float(np.log(2.0))
+    vc = (1.0 + torch.rand(pages, 1, page, d, generator=g)).to(dtype)
+    kc[0, 0, 0], vc[0, 0, 0] = 0.0, 0.0
+    q = torch.zeros(B, H, d, dtype=dtype)
+    q[..., 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32).expand(B, pages).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32)
+    o, lse = fa.fa_paged_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), scale=1.0)
+    fa.fa_sync_check()
+    ref = paged_decode(host_f64(q[:1]), host_f64(kc), host_f64(vc), table[:1].tolist(), [n], 1.0, half=HALF[dtype])
+    for b in range(B):
+        _check(o[b], ref[0][0], ref[2][0], "O")
+        _check(lse[b], ref[1][0], ref[3][0], "LSE")
