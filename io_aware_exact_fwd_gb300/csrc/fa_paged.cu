@@ -127,6 +127,9 @@ constexpr int kConsumers = 4;     // consumer warps
 constexpr int kDecThreads = 32 * (kConsumers + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994530942f;
+// The reference of a row before its first token, and where every score so far is -inf (a key with an infinite entry):
+// finite, so that such tokens weigh 0 and a part that holds no others joins with weight 0.
+constexpr float kNoScore = -3.0e38f;
 
 enum : uint32_t { kSiteDecLoad = 0x131, kSiteDecFull = 0x331 };
 
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
     float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -INFINITY;
+      m[mt][0] = m[mt][1] = kNoScore;
       l[mt][0] = l[mt][1] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) o[mt][c][0] = o[mt][c][1] = o[mt][c][2] = o[mt][c][3] = 0.f;
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
           for (int e = 0; e < 2; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            const float mn = fmaxf(m[mt][e], mx[e] - C::kHeadroom);  // finite: the warp has at least one token
+            const float mn = fmaxf(m[mt][e], mx[e] - C::kHeadroom);
             alpha[e] = ex2_approx(m[mt][e] - mn);
             up |= mn > m[mt][e];
             m[mt][e] = mn;
@@ -575,13 +578,13 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
       consumers_sync();
       const int r = threadIdx.x >> 3, gl = 16 * mt + r;  // 8 threads a row
       if (gl < rows) {
-        float M = -INFINITY, L = 0.f, wgt[kConsumers];
+        float M = kNoScore, L = 0.f, wgt[kConsumers];
 #pragma unroll
         for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, s_ml[x * C::kRows + gl].x);
 #pragma unroll
         for (int x = 0; x < kConsumers; ++x) {
           const float2 ml = s_ml[x * C::kRows + gl];
-          wgt[x] = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);  // a warp without tokens
+          wgt[x] = ex2_approx(ml.x - M);
           L += ml.y * wgt[x];
         }
         const float inv = whole ? 1.f / L : 1.f;
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   }
   const int c0 = static_cast<int>(w0 / share), c1 = static_cast<int>((w0 + tiles - 1) / share);
   if (c0 == c1) return;  // one CTA had the whole head and wrote it
-  float m = -INFINITY, l = 0.f, acc[E] = {};
+  float m = kNoScore, l = 0.f, acc[E] = {};
 #pragma unroll 4
   for (int c = c0 + warp; c <= c1; c += 4) {
     // A CTA's first segment has slot 0; only the first part can be another segment of its CTA.
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
     float v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = part[row * D + lane + 32 * e];
-    const float mn = fmaxf(m, ml.x), wa = ex2_approx(m - mn), wb = ex2_approx(ml.x - mn);  // ml.x is finite
+    const float mn = fmaxf(m, ml.x), wa = ex2_approx(m - mn), wb = ex2_approx(ml.x - mn);
     l = l * wa + ml.y * wb;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = acc[e] * wa + v[e] * wb;
@@ -671,13 +674,13 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = acc[e];
   __syncthreads();
   if (threadIdx.x < D / 2) {
-    float M = -INFINITY, L = 0.f;
+    float M = kNoScore, L = 0.f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) M = fmaxf(M, s_ml[x].x);
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float wgt = s_ml[x].x == -INFINITY ? 0.f : ex2_approx(s_ml[x].x - M);
+      const float wgt = ex2_approx(s_ml[x].x - M);
       L += s_ml[x].y * wgt;
       sum.x = fmaf(s_o[x][2 * threadIdx.x], wgt, sum.x);
       sum.y = fmaf(s_o[x][2 * threadIdx.x + 1], wgt, sum.y);

@@ -403,3 +403,35 @@ def test_many_small_weights_behind_a_dominant_token(dtype, below):
     for b in range(B):
         _check(o[b], ref[0][0], ref[2][0], "O")
         _check(lse[b], ref[1][0], ref[3][0], "LSE")
+
+
+@pytest.mark.parametrize("n", [17, 33, 65, 129, 700])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_tokens_of_weight_zero_alone_in_a_warps_share(n, dtype):
+    # The last token's score is -inf (a key with an infinite entry): its weight is 0, also where it is the only
+    # token of a warp or of a block.
+    H, d, page = 3, 128, 16
+    kc, vc, table, lens = _cache([n], 1, d, page, dtype, 36)
+    q = torch.randn(1, H, d, generator=torch.Generator().manual_seed(37)).to(dtype).cuda()
+    q[:, :, 5] = q[:, :, 5].abs() + 0.5
+    kc[table[0, (n - 1) // page].item(), 0, (n - 1) % page, 5] = float("-inf")
+    o, lse = fa.fa_paged_decode(q, kc, vc, table, lens)
+    fa.fa_sync_check()
+    # Its place counts for nothing without a bias: the same without the token.
+    ref = paged_decode(host_f64(q), host_f64(torch.nan_to_num(kc, neginf=0.0)), host_f64(vc), table.tolist(), [n - 1], d ** -0.5,
+                       half=HALF[dtype])
+    _check(o, ref[0], ref[2], "O")
+    _check(lse, ref[1], ref[3], "LSE")
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("at", [0, 64, 699])
+def test_nan_in_a_visible_key_comes_through(at, cap):
+    # ... to the heads that read it, also from a warp, a block or a part that holds no other token.
+    kc, vc, table, lens = _cache([700], 2, 128, 16, torch.bfloat16, 38)
+    q = torch.randn(1, 6, 128, generator=torch.Generator().manual_seed(39)).to(torch.bfloat16).cuda()
+    kc[table[0, at // 16].item(), 0, at % 16, 5] = float("nan")
+    o, lse = fa.fa_paged_decode(q, kc, vc, table, lens, softcap=cap)
+    fa.fa_sync_check()
+    assert bool(torch.isnan(o[:, :3]).all()) and bool(torch.isnan(lse[:, :3]).all())
+    assert bool(torch.isfinite(o[:, 3:]).all()) and bool(torch.isfinite(lse[:, 3:]).all())
