@@ -166,6 +166,7 @@ struct DecParams {
   long long* offsets;        // [B + 1] tiles before each sequence, then the share
   int H, group, chunks, piece;
   float scale_log2, cap_in, cap_out;
+  CapPoly poly;              // factor cap_out
   const float* slopes;
   unsigned int* err_word;
   unsigned long long wait_ns;
@@ -462,13 +463,38 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float mx[2] = {-INFINITY, -INFINITY};
+          if (p.cap_out > 0.f) {
+            // As in the forward: relative to the score while |x| < 2, so that a cap far above the scores costs
+            // them no bits; the other form only where an argument of the warp needs it.
+            uint32_t bits = 0;
+#pragma unroll
+            for (int nt = 0; nt < 2 * NB; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[mt][nt][e] *= p.cap_in;
+                bits |= __float_as_uint(s[mt][nt][e]);
+              }
+            const bool any_far = __any_sync(0xffffffffu, bits & kReachesTwo);
+#pragma unroll
+            for (int nt = 0; nt < 2 * NB; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float2 x = make_float2(s[mt][nt][e], s[mt][nt][e + 1]);
+                float2 y = __fmul2_rn(x, tanh_over_x(x, p.poly));
+                if (any_far) {
+                  const float2 far = tanh_any(x, p.cap_out, pair(0.f));
+                  y = make_float2(fabsf(x.x) < 2.f ? y.x : far.x, fabsf(x.y) < 2.f ? y.y : far.y);
+                }
+                s[mt][nt][e] = y.x;
+                s[mt][nt][e + 1] = y.y;
+              }
+          }
 #pragma unroll
           for (int nt = 0; nt < 2 * NB; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + 8 * nt + gc + (e & 1);
-              float x = s[mt][nt][e];
-              x = p.cap_out > 0.f ? tanh_any(pair(x * p.cap_in), p.cap_out, pair(0.f)).x : x * p.scale_log2;
+              float x = p.cap_out > 0.f ? s[mt][nt][e] : s[mt][nt][e] * p.scale_log2;
               x = fmaf(-slope2[mt][e >> 1], static_cast<float>(at.n - 1 - key), x);
               x = key < at.n ? x : -INFINITY;
               s[mt][nt][e] = x;
@@ -720,8 +746,9 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   p.piece = std::min(C::kTile, a.c.page_size & -a.c.page_size);
   p.scale_log2 = a.scale * kLog2e;
   if (a.softcap > 0.f) {
-    p.cap_in = 4.f * a.scale / a.softcap;  // tanh_any takes four times the cap's argument
+    p.cap_in = 4.f * a.scale / a.softcap;  // products to x = 4 u (fa_score.cuh)
     p.cap_out = a.softcap * kLog2e;
+    p.poly = cap_poly(p.cap_out);
   }
   p.slopes = a.slopes;
   p.err_word = a.err_word;

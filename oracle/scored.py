@@ -73,8 +73,8 @@ def _score_error(q, k, scale, cap, slope, d):
     """How far a score may be off in fp32: the dot product's d + 1 roundings, the cap's and the
     bias's, and the base-2 exponent's product (8 more half steps of each magnitude)."""
     size = scale * np.max(np.abs(q) @ np.abs(k).T, initial=0.0)
-    # The cap itself is evaluated to 4 half steps of the cap (absolute).
-    return HALF32 * ((d + 8) * size + 8 * cap + 8 * slope * q.shape[0]) + 2e-6
+    # The cap itself is evaluated to 8 half steps (absolute) of the cap, or of the largest score if that is smaller.
+    return HALF32 * ((d + 8) * size + 8 * min(cap, size) + 8 * slope * q.shape[0]) + 2e-6
 
 
 def scored_forward(q, k, v, scale, causal, cap=0.0, slopes=None, cu=None, prefix=None):
@@ -173,7 +173,7 @@ def paged_decode(q, k_cache, v_cache, table, lens, scale, cap=0.0, slopes=None, 
             P, lse[b, h] = e / e.sum(), top + np.log(e.sum())
             o[b, h] = P @ v[h // G]
             size = scale * np.max(np.abs(q[b, h]) @ np.abs(k[h // G]).T)
-            err = HALF32 * ((d + 8) * size + 8 * cap + 8 * abs(slope) * n) + 2e-6
+            err = HALF32 * ((d + 8) * size + 8 * min(cap, size) + 8 * abs(slope) * n) + 2e-6
             ob[b, h] = (half + 3 * err) * (P @ np.abs(v[h // G])) * 1.01 + half * np.abs(o[b, h]) + 2.0 ** -24
             lb[b, h] = 2 * err + 4 * HALF32 * abs(lse[b, h])
     return o, lse, ob, lb

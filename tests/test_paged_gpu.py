@@ -435,3 +435,40 @@ def test_nan_in_a_visible_key_comes_through(at, cap):
     fa.fa_sync_check()
     assert bool(torch.isnan(o[:, :3]).all()) and bool(torch.isnan(lse[:, :3]).all())
     assert bool(torch.isfinite(o[:, 3:]).all()) and bool(torch.isfinite(lse[:, 3:]).all())
+
+
+@pytest.mark.parametrize("cap", [200.0, 1e4, 1e6, 1e20])
+@pytest.mark.parametrize("H,Hkv,d,dtype,bias", [(4, 2, 64, torch.bfloat16, False), (24, 1, 128, torch.float16, True)])
+def test_decode_with_caps_far_above_the_scores(H, Hkv, d, dtype, bias, cap):
+    # (a cap that hardly bends: its error is relative to the score, not to the cap)
+    _decode(([1, 70, 900], H, Hkv, d, 16, dtype, cap, bias), "nhd", None)
+
+
+@pytest.mark.parametrize("cap", [10.0, 100.0, 300.0])
+def test_decode_with_small_and_large_arguments_of_the_cap(cap):
+    # Scores from far below the cap to far past it, side by side.
+    lens, H, d, page = [300, 40], 8, 64, 16
+    kc, vc, table, n = _cache(lens, 2, d, page, torch.bfloat16, 33)
+    f = torch.logspace(-2, 2.5, H)[None, :, None]
+    q = (torch.randn(2, H, d, generator=torch.Generator().manual_seed(34)) * f).to(torch.bfloat16).cuda()
+    o, lse = fa.fa_paged_decode(q, kc, vc, table, n, softcap=cap)
+    fa.fa_sync_check()
+    ref = paged_decode(host_f64(q), host_f64(kc), host_f64(vc), table.tolist(), lens, d ** -0.5, cap)
+    _check(o, ref[0], ref[2], "O")
+    _check(lse, ref[1], ref[3], "LSE")
+
+
+def test_decode_agrees_with_the_forward_at_a_large_cap():
+    H, Hkv, N, d, cap = 4, 2, 200, 64, 1e5
+    g = torch.Generator().manual_seed(35)
+    q, k, v = (torch.randn(1, h, N, d, generator=g).to(torch.bfloat16).cuda() for h in (H, Hkv, Hkv))
+    _, want = fa.fa_fwd_scored(q, k, v, causal=True, softcap=cap)
+    kc, vc = (torch.zeros(13, Hkv, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table, n = torch.arange(13, dtype=torch.int32, device="cuda")[None], ints([N])
+    fa.fa_paged_append(k[0].transpose(0, 1), v[0].transpose(0, 1), kc, vc, table, n, ints([0, N]))
+    _, lse = fa.fa_paged_decode(q[:, :, -1], kc, vc, table, n, softcap=cap)
+    fa.fa_sync_check()
+    # The bound of either LSE, twice: products of at most 10 (sums of |q k| / 8) to 80 half steps and 2e-6, in
+    # the LSE twice, and 4 half steps of the LSE.
+    assert float((lse - want[:, :, -1]).abs().max()) <= 2 * (2 * (80 * 10 * 2.0 ** -24 + 2e-6) + 4 * 10 * 2.0 ** -24)
