@@ -61,8 +61,12 @@ __device__ __forceinline__ uint32_t or_bits(uint32_t acc, float2 x) {
   return acc | __float_as_uint(x.x) | __float_as_uint(x.y);
 }
 constexpr uint32_t kReachesTwo = 0x40000000u;
+// The bound on softcap log2(e) up to which builds of the kernels may count on small caps.
+constexpr float kBoundedCap = 80.0f;
 // factor * tanh(x / 4) + add, any x: 1 - 2 / (1 + e^2u), which keeps its absolute error
-// (about 2^-22 factor) at both ends (e^2u -> 0 or infinity gives -1 or 1).
+// (about 2^-22 factor) at both ends (e^2u -> 0 or infinity gives -1 or 1).  Fit for arguments that come
+// near the cap, and for any under a cap of kBoundedCap or less (an error of 2e-5 in the exponent); above it
+// small arguments need the other form.
 __device__ __forceinline__ float2 tanh_any(float2 x, float factor, float2 add) {
   const float2 a = __fmul2_rn(x, pair(0.7213475204444817f));
   const float2 e = __fadd2_rn(make_float2(ex2_approx(a.x), ex2_approx(a.y)), pair(1.f));

@@ -80,7 +80,9 @@ __device__ __forceinline__ Steps steps_of(const Params& p, int kb, int b) {
   return {i0, nq, nq * p.group};
 }
 
-// MODE 0: scores as they are; 1: with a distance bias; 2: capped; 3: capped and biased.
+// MODE 0: scores as they are; 1: with a distance bias; 2: capped; 3: capped within kBoundedCap and
+// biased; 4: capped beyond it and biased (its own build: the fourth way through a step would cost MODE 3 14 % at B=2
+// H=16/4 N=4096 d=128, cap 20, causal: 505 us, 576 with it).
 // DIVIDED: parts > 1 (its own build: the undivided one would be 1 % slower with it).
 template <int D, int MODE, bool DET, bool DIVIDED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // time, and in bursts hold up the compute warps' stores (d = 128: 1272 us with the test, 1337 without; d = 64: 2145 |
   // 2325).
   constexpr bool kWholeAdds = DET;
-  constexpr bool kCapped = MODE >= 2, kBiased = MODE == 1 || MODE == 3;
+  constexpr bool kCapped = MODE >= 2, kBiased = MODE != 0 && MODE != 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::kKOff;
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = i * kBqB, q0 = qb + 32 * g;
       const bool need_mask = qb < all_lo || qb + kBqB > all_hi;
       bool general = kBiased && !one_sided && qb < kb * kBkB + kBkB - 1;
+      bool small = false;  // MODE 4: general, but no argument of the cap reaches 1/2
       const float4* lse4 = nullptr;
       if constexpr (kCapped) {
         uint32_t bits = 0;
@@ -365,7 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[c] = __float_as_uint(x.x);
           s[c + 1] = __float_as_uint(x.y);
         }
-        general = general || __any_sync(0xffffffffu, bits & kReachesTwo);
+        if constexpr (MODE == 4) {
+          small = !__any_sync(0xffffffffu, bits & kReachesTwo);
+          general = general || !small;
+        } else {
+          general = general || __any_sync(0xffffffffu, bits & kReachesTwo);
+        }
         // LSE2 of the step's queries: the slot landed before S^T was made of it (the wait makes its
         // bytes visible here), and is refilled only after this step's dV and dK.
         if (!(ok = warp_wait_b(&bar_full[slot], ring_ph, wc, kSiteBComp))) break;
@@ -388,9 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // P and dS of the 32 queries, written out.  Three ways, each whole (scores in registers at the
       // meeting of two ways would cost the common one a move each): every key seen by every query;
-      // masked; and masked in the general form (any argument of the cap, queries on both sides).
-      auto step = [&](auto masked_c, auto general_c) {
+      // masked; and masked in the general form (any argument of the cap, queries on both sides).  Beyond
+      // kBoundedCap a fourth: queries on both sides, but tanh in the form for small arguments.
+      auto step = [&](auto masked_c, auto general_c, auto small_c) {
         constexpr bool kMasked = decltype(masked_c)::value, kGeneral = decltype(general_c)::value;
+        constexpr bool kAny = kGeneral && !decltype(small_c)::value;
         const uint32_t vis = kMasked ? bits_between(by.x - q0, by.y - q0) : 0xffffffffu;
         // The bias with i >= j: -slope2 more for every query; four steps are added up, then the sum
         // starts afresh.
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             float2 dpp = make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
             if constexpr (kCapped) {
-              const float2 t = kGeneral ? tanh_any(x, 1.f, pair(0.f)) : __fmul2_rn(x, tanh_over_x(x, p.poly));
+              const float2 t = kAny ? tanh_any(x, 1.f, pair(0.f)) : __fmul2_rn(x, tanh_over_x(x, p.poly));
               x = __ffma2_rn(t, pair(p.cap_out), e ? make_float2(-l4.z, -l4.w) : make_float2(-l4.x, -l4.y));
               dpp = __fmul2_rn(dpp, __ffma2_rn(t, make_float2(-t.x, -t.y), pair(1.f)));
             }
@@ -437,9 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (need_mask && !__any_sync(0xffffffffu, bits_between(by.x - q0, by.y - q0))) {
         const uint32_t zero[16] = {};  // no key of the warp is seen by the 32 queries
         write(zero, zero);
-      } else if (general) step(std::true_type{}, std::true_type{});
-      else if (need_mask) step(std::true_type{}, std::false_type{});
-      else step(std::false_type{}, std::false_type{});
+      } else if (MODE == 4 && general && small) step(std::true_type{}, std::true_type{}, std::true_type{});
+      else if (general) step(std::true_type{}, std::true_type{}, std::false_type{});
+      else if (need_mask) step(std::true_type{}, std::false_type{}, std::false_type{});
+      else step(std::false_type{}, std::false_type{}, std::false_type{});
       tmem_st_wait();
       fence_proxy_async_smem();
       tc_fence_before();
@@ -682,7 +693,10 @@ cudaError_t launch_mode(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stre
 
 template <int D>
 cudaError_t launch_d(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream) {
-  if (sc.softcap > 0.f) return sc.slopes ? launch_mode<D, 3>(a, sc, stream) : launch_mode<D, 2>(a, sc, stream);
+  if (sc.softcap > 0.f)
+    return !sc.slopes                           ? launch_mode<D, 2>(a, sc, stream)
+           : sc.softcap * kLog2e <= kBoundedCap ? launch_mode<D, 3>(a, sc, stream)
+                                                : launch_mode<D, 4>(a, sc, stream);
   return sc.slopes ? launch_mode<D, 1>(a, sc, stream) : launch_mode<D, 0>(a, sc, stream);
 }
 

@@ -63,10 +63,9 @@ constexpr uint32_t kTmemCols = 512;
 // weights, sums and O stay far from the ends of the exponent's range.
 constexpr float kSpeculationSumBound = 1.152921504606847e18f;
 // With a cap, scores lie in [-softcap, softcap] log2(e) (plus a bias whose maximum over
-// the row's keys is known): up to this bound on softcap log2(e) that maximum alone is the
+// the row's keys is known): up to kBoundedCap on softcap log2(e) that maximum alone is the
 // reference, with P in 2^-80 .. 2^80 and no maximum taken at all (a cap of 55 at B=2 H=16/4
 // N=8192 causal: 535 us; one of 56, with the running reference: 767).
-constexpr float kBoundedCap = 80.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -679,7 +678,7 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
         // it is rare, the kernel's speed depends on its code fitting the instruction caches, and a
         // second form of 128 scores in registers would cost the common one a move for each.
         const bool biased = MODE == 1 || (MODE == 4 && p.slopes != nullptr);
-        bool pre = biased && !left;
+        bool pre = biased && !left, far = false;  // far: an argument of the cap reaches 1/2
         if constexpr (MODE == 4) {
           uint32_t bits = 0;
 #pragma unroll 1
@@ -690,7 +689,8 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             for (int i = 0; i < 8; i += 2)
               bits = or_bits(bits, __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), pair(p.cap_in)));
           }
-          pre = pre || __any_sync(0xffffffffu, bits & kReachesTwo);
+          far = __any_sync(0xffffffffu, bits & kReachesTwo);
+          pre = pre || far;
         }
         if (pre) {
 #pragma unroll 1
@@ -698,12 +698,18 @@ __global__ void __launch_bounds__(Roles<kPartsOf<MODE>>::kThreads, 1)
             uint32_t x[8];
             tmem_ld8_wait(trow + col_s + c, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float s = __uint_as_float(x[i]);
-              // MODE 1: the K-step's slope times the key's place is taken out again.
-              const float a = MODE == 4 ? tanh_any(pair(s * p.cap_in), p.cap_out, pair(0.f)).x
-                                        : fmaf(-slope2, static_cast<float>(c + i), s * p.scale_log2);
-              x[i] = __float_as_uint(fmaf(-slope2, fabsf(static_cast<float>(kbase + c + i - qrow)), a));
+            for (int i = 0; i < 8; i += 2) {
+              float2 a = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+              if constexpr (MODE == 4) {
+                a = __fmul2_rn(a, pair(p.cap_in));
+                a = far ? tanh_any(a, p.cap_out, pair(0.f)) : __fmul2_rn(a, tanh_over_x(a, p.poly));
+              } else {  // the K-step's slope times the key's place is taken out again
+                a = __ffma2_rn(pair(-slope2), make_float2(static_cast<float>(c + i), static_cast<float>(c + i + 1)),
+                               __fmul2_rn(a, pair(p.scale_log2)));
+              }
+              const float off = static_cast<float>(kbase + c + i - qrow);
+              x[i] = __float_as_uint(fmaf(-slope2, fabsf(off), a.x));
+              x[i + 1] = __float_as_uint(fmaf(-slope2, fabsf(off + 1.f), a.y));
             }
             tmem_st8(trow + col_s + c, x);
           }

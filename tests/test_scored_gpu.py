@@ -475,3 +475,24 @@ def test_nan_in_a_key_reaches_the_gradients_of_its_document(H, cap, bias):
 def _out(q, k, v, do, kw):
     o, lse = fa.fa_fwd_scored(q, k, v, **kw)
     return o, do, lse
+
+
+@pytest.mark.parametrize("cap", [30.0, 200.0, 1e4, 1e6, 1e20])
+@pytest.mark.parametrize("H,N", [(2, 300), (62, 400)])
+def test_biased_scores_on_both_sides_far_below_the_cap(H, N, cap):
+    # Keys on both sides of a row take the general form of the bias; the cap's error stays relative to the
+    # score there, whatever the cap.
+    B, d = 1, 64
+    q, k, v, do = _inputs(B, H, H, N, d, 63)
+    slopes = _slopes(H)
+    o, lse = fa.fa_fwd_scored(q, k, v, softcap=cap, slopes=slopes)
+    grads = fa.fa_bwd_scored(q, k, v, o, do, lse, softcap=cap, slopes=slopes)
+    fa.fa_sync_check()
+    x = [host_f64(t) for t in (q, k, v, do)]
+    args = (d ** -0.5, False, cap, slopes.cpu().numpy())
+    o_ref, lse_ref, ob, lb = scored_forward(*x[:3], *args)
+    _check(o, o_ref, ob, "O")
+    _check(lse, lse_ref, lb, "LSE")
+    refs, bounds = scored_backward(*x, *args)
+    for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
+        _check(a, ref, bd, name)
