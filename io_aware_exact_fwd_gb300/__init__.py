@@ -7,7 +7,8 @@ tensors, passes their device pointers and the current CUDA stream, and raises
 kernels; there is no fallback.  If libfa.so is missing, importing the binding
 still works but every call raises, so a missing build is never silent.
 
-PyTorch is used only as device-memory and stream plumbing.  Most calls marshal with
+PyTorch is used only as device-memory and stream plumbing.  With ``stream`` a call runs on that stream,
+and what it allocates comes from that stream's memory, as under ``torch.cuda.stream(stream)``.  Most calls marshal with
 ctypes; those of scored attention and of the paged cache, made once a layer and token,
 with a small compiled module (csrc/fa_torch.cpp).
 """
@@ -171,6 +172,18 @@ def _stream_handle(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _empty(stream, shape, dtype, device):
+    """A new tensor from the memory of the stream that the call runs on.
+
+    So what other streams still do with memory that was freed there cannot meet it, and
+    a workspace that the call lets go is only used again behind the call.
+    """
+    import torch
+
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _ptr(t):
@@ -668,7 +681,7 @@ def fa_mask_plan(B: int, N: int, cu_docs=None, prefix=None, causal: bool = True,
     if plan is None:
         ref = cu_docs if cu_docs is not None else prefix
         dev = ref.device if ref is not None else torch.device("cuda" if device is None else device)
-        plan = torch.empty(max(fa_mask_plan_size(B, N), 1), dtype=torch.uint8, device=dev)
+        plan = _empty(stream, max(fa_mask_plan_size(B, N), 1), torch.uint8, dev)
     _done(load_binding().mask_plan(B, N, cu_docs, prefix, causal, plan, None if stream is None else stream.cuda_stream),
           "fa_mask_plan")
     return plan

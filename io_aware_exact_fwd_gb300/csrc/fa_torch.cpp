@@ -118,26 +118,33 @@ int truth(PyObject* x) {
   return t;
 }
 
-// The caller's stream (its handle), or the GPU's current one.
-fa_stream_t stream_of(PyObject* x, int gpu) {
-  if (x == Py_None) return reinterpret_cast<fa_stream_t>(c10::cuda::getCurrentCUDAStream(gpu).stream());
-  void* p = PyLong_AsVoidPtr(x);
-  if (!p && PyErr_Occurred()) throw python_error();
-  return static_cast<fa_stream_t>(p);
-}
+// The caller's stream (its handle), or the GPU's current one.  A given stream is the current one while the
+// call allocates: an output, or a workspace let go when the call returns, comes from the memory of the
+// stream that uses it, so that what other streams still do with freed memory cannot meet it, and what
+// that stream gets the memory for next runs after the call.
+class CallStream {
+ public:
+  CallStream(PyObject* x, int gpu) {
+    if (x == Py_None) {
+      handle_ = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(gpu)).stream();
+      return;
+    }
+    void* p = PyLong_AsVoidPtr(x);
+    if (!p && PyErr_Occurred()) throw python_error();
+    handle_ = static_cast<cudaStream_t>(p);
+    guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, static_cast<c10::DeviceIndex>(gpu)));
+  }
+  operator fa_stream_t() const { return reinterpret_cast<fa_stream_t>(handle_); }
+
+ private:
+  cudaStream_t handle_ = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 // The sizes the library takes as int.
 int whole(int64_t n, const char* name) {
   if (n > INT32_MAX || n < INT32_MIN) unfit(PyExc_ValueError, c10::str(name, " is too large: ", n));
   return static_cast<int>(n);
-}
-
-// A workspace the caller did not give.  It is let go when the call returns, so it comes from
-// the memory of the stream that uses it: what that stream gets it for next runs after the call.
-Tensor scratch(size_t n, const Tensor& like, fa_stream_t stream, int gpu) {
-  c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream),
-                                                                    static_cast<c10::DeviceIndex>(gpu)));
-  return fresh({static_cast<int64_t>(n)}, at::kByte, like);
 }
 
 // fn() with the GPU current, and without the interpreter's lock (nothing in fn may throw).
@@ -185,7 +192,7 @@ PyObject* mask_plan(PyObject* const* a) {
   const int32_t* prefix = flat<const int32_t>(a[3], "prefix", at::kInt, {B, docs}, gpu);
   const Bytes p = bytes(a[5], "plan", gpu);
   const int t = whole(docs, "cu_docs"), b = whole(B, "B"), n = whole(N, "N"), causal = truth(a[4]);
-  const fa_stream_t s = stream_of(a[6], gpu);
+  const CallStream s(a[6], gpu);
   const int st = call(gpu, [&] { return fa_mask_plan(cu, prefix, t, p.p, p.n, b, n, causal, s); });
   if (st) return PyLong_FromLong(st);
   Py_RETURN_NONE;
@@ -202,6 +209,7 @@ PyObject* fwd_scored(PyObject* const* a) {
   const int64_t B = q.size(0), H = q.size(1), N = q.size(2), d = q.size(3), Hkv = k.size(1);
   const Layout lq = layout(q, "q", type, {B, H, N, d}, gpu), lk = layout(k, "k", type, {B, Hkv, N, d}, gpu),
                lv = layout(v, "v", type, {B, Hkv, N, d}, gpu);
+  const CallStream s(a[10], gpu);
   const Tensor o = given_or_new(a[3], "o", {B, H, N, d}, q, type);
   const Tensor lse = given_or_new(a[4], "lse", {B, H, N}, q, at::kFloat);
   const Layout lo = layout(o, "o", type, {B, H, N, d}, gpu);
@@ -212,7 +220,6 @@ PyObject* fwd_scored(PyObject* const* a) {
   const float scale = scale_of(a[6], d), cap = number(a[7]);
   const int causal = truth(a[5]), b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N"),
             dim = whole(d, "d");
-  const fa_stream_t s = stream_of(a[10], gpu);
   const int st = call(gpu, [&] {
     return fa_fwd_scored(lq.p, lq.strides(), lk.p, lk.strides(), lv.p, lv.strides(), lo.p, lo.strides(),
                          static_cast<float*>(lse.data_ptr()), b, h, hkv, n, dim, plan.p, plan.n, causal,
@@ -236,18 +243,18 @@ PyObject* bwd_scored(PyObject* const* a) {
                lo = layout(o, "o", type, qs, gpu), lg = layout(go, "do", type, qs, gpu);
   if (a[5] == Py_None) unfit(PyExc_TypeError, "lse must be a torch.Tensor");
   const float* lse = flat<const float>(a[5], "lse", at::kFloat, {B, H, N}, gpu);
+  const CallStream s(a[15], gpu);
   const Tensor dq = given_or_new(a[6], "dq", qs, q, type), dk = given_or_new(a[7], "dk", ks, q, type),
                dv = given_or_new(a[8], "dv", ks, q, type);
   const Layout ldq = layout(dq, "dq", type, qs, gpu), ldk = layout(dk, "dk", type, ks, gpu),
                ldv = layout(dv, "dv", type, ks, gpu);
   const int b = whole(B, "B"), h = whole(H, "H"), hkv = whole(Hkv, "Hkv"), n = whole(N, "N"), dim = whole(d, "d");
-  const fa_stream_t s = stream_of(a[15], gpu);
   Tensor own;
   Bytes ws = bytes(a[9], "workspace", gpu);
   if (a[9] == Py_None) {
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(gpu));
     ws.n = fa_bwd_scored_workspace_size(b, h, hkv, n, dim);
-    own = scratch(ws.n, q, s, gpu);
+    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, q);
     ws.p = own.data_ptr();
   }
   const float* slopes = flat<const float>(a[13], "slopes", at::kFloat, {H}, gpu);
@@ -308,7 +315,7 @@ PyObject* paged_append(PyObject* const* a) {
   if (a[6] == Py_None) unfit(PyExc_TypeError, "cu_new must be a torch.Tensor");
   const int32_t* cu = flat<const int32_t>(a[6], "cu_new", at::kInt, {c.B + 1}, c.gpu);
   const int b = whole(c.B, "B"), t = whole(T, "T");
-  const fa_stream_t s = stream_of(a[7], c.gpu);
+  const CallStream s(a[7], c.gpu);
   const int st = call(c.gpu, [&] {
     return fa_paged_append(lk.p, lk.strides(), lv.p, lv.strides(), c.k.p, c.k.strides(), c.v.p, c.v.strides(), c.table,
                            c.table_stride, c.lens, cu, b, t, c.hkv, c.d, c.page, c.pages, c.width, c.code, s);
@@ -324,19 +331,19 @@ PyObject* paged_decode(PyObject* const* a) {
   if (q.dim() != 3) unfit(PyExc_ValueError, "q must be [B, H, d]");
   const int64_t H = q.size(1);
   const Layout lq = layout(q, "q", c.type, {c.B, H, c.d}, c.gpu);
+  const CallStream s(a[11], c.gpu);
   const Tensor o = given_or_new(a[5], "o", {c.B, H, c.d}, q, c.type);
   const Tensor lse = given_or_new(a[6], "lse", {c.B, H}, q, at::kFloat);
   const Layout lo = layout(o, "o", c.type, {c.B, H, c.d}, c.gpu);
   check(lse, "lse", at::kFloat, {c.B, H}, c.gpu);
   if (!lse.is_contiguous()) unfit(PyExc_ValueError, "lse must be contiguous");
   const int b = whole(c.B, "B"), h = whole(H, "H");
-  const fa_stream_t s = stream_of(a[11], c.gpu);
   Tensor own;
   Bytes ws = bytes(a[7], "workspace", c.gpu);
   if (a[7] == Py_None) {
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.gpu));
     ws.n = fa_paged_decode_workspace_size(b, h, c.hkv, c.d);
-    own = scratch(ws.n, q, s, c.gpu);
+    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, q);
     ws.p = own.data_ptr();
   }
   const float* slopes = flat<const float>(a[10], "slopes", at::kFloat, {H}, c.gpu);
