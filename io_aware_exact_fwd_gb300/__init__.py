@@ -182,7 +182,9 @@ def _empty(stream, shape, dtype, device):
     """
     import torch
 
-    with torch.cuda.stream(stream):  # (None: the current one)
+    if stream is None:  # the current one
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -242,9 +244,9 @@ def fa_fwd(q, k, v, o=None, lse=None, causal: bool = False, scale: float | None 
     for name, t in (("q", q), ("k", k), ("v", v)):
         _check_strided(name, t, (B, H, N, d), torch.bfloat16)
     if o is None:
-        o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+        o = _empty(stream, (B, H, N, d), torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, H, N), torch.float32, q.device)
     _check_strided("o", o, (B, H, N, d), torch.bfloat16)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [B, H, N]")
@@ -284,7 +286,7 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None, causa
         _check_strided(name, t, (B, H, N, d), torch.bfloat16)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [B, H, N]")
-    dense = lambda: torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+    dense = lambda: _empty(stream, (B, H, N, d), torch.bfloat16, q.device)
     dq = dense() if dq is None else dq
     dk = dense() if dk is None else dk
     dv = dense() if dv is None else dv
@@ -292,7 +294,7 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, workspace=None, causa
         _check_strided(name, t, (B, H, N, d), torch.bfloat16)
     need = int(lib.fa_bwd_workspace_size(B, H, N, d))
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(need, 1), torch.uint8, q.device)
     if scale is None:
         scale = d ** -0.5
     with torch.cuda.device(q.device):
@@ -373,7 +375,7 @@ def _fp8_prepare_call(q, k, v, signs, seed, workspace, stream, name):
     if signs is not None and (signs.dtype != torch.int8 or tuple(signs.shape) != (d,) or not signs.is_cuda):
         raise ValueError("signs must be an int8 CUDA tensor of shape [d]")
     if workspace is None:
-        workspace = torch.empty(max(fa_fp8_workspace_size(B, H, N, d), 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(fa_fp8_workspace_size(B, H, N, d), 1), torch.uint8, q.device)
     in_dtype = 1 if dt == torch.bfloat16 else 0
     seed64 = ctypes.c_uint64(seed & (2 ** 64 - 1))
     with torch.cuda.device(q.device):
@@ -425,9 +427,9 @@ def fa_fwd_fp8(workspace, shape, o=None, lse=None, causal: bool = False, scale: 
     B, H, N, d = shape
     dev = workspace.device
     if o is None:
-        o = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+        o = _empty(stream, (B, H, N, d), torch.bfloat16, dev)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+        lse = _empty(stream, (B, H, N), torch.float32, dev)
     _check_bhnd("o", o, (B, H, N, d), torch.bfloat16)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor [B, H, N]")
@@ -446,7 +448,7 @@ def fa_fp8_dequantize(workspace, shape, stream=None):
 
     lib = load_library()
     B, H, N, d = shape
-    out = [torch.empty((B, H, N, d), dtype=torch.bfloat16, device=workspace.device) for _ in range(3)]
+    out = [_empty(stream, (B, H, N, d), torch.bfloat16, workspace.device) for _ in range(3)]
     with torch.cuda.device(workspace.device):
         st = lib.fa_fp8_dequantize(_ptr(workspace), _ws_bytes(workspace), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
                                    B, H, N, d, _stream_handle(stream))
@@ -481,14 +483,14 @@ def fa_bwd_fp8(fp8_workspace, signs, o, do, lse, dq=None, dk=None, dv=None, work
             raise ValueError("lse must be a contiguous float32 tensor [B, H, N]")
     if signs.dtype != torch.int8 or tuple(signs.shape) != (d,) or not signs.is_cuda:
         raise ValueError("signs must be an int8 CUDA tensor of shape [d]")
-    dense = lambda: torch.empty((B, H, N, d), dtype=torch.bfloat16, device=do.device)
+    dense = lambda: _empty(stream, (B, H, N, d), torch.bfloat16, do.device)
     dq = dense() if dq is None else dq
     dk = dense() if dk is None else dk
     dv = dense() if dv is None else dv
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _check_bhnd(name, t, (B, H, N, d), torch.bfloat16)
     if workspace is None:
-        workspace = torch.empty(max(fa_bwd_fp8_workspace_size(B, H, N, d), 1), dtype=torch.uint8, device=do.device)
+        workspace = _empty(stream, max(fa_bwd_fp8_workspace_size(B, H, N, d), 1), torch.uint8, do.device)
     if scale is None:
         scale = d ** -0.5
     with torch.cuda.device(do.device):
@@ -563,9 +565,9 @@ def fa_fwd_splitkv_partial(q, k, v, n_split: int, o_part=None, lse_part=None, ca
     lib = load_library()
     B, H, Nq, Nk, d = _check_kv(q, k, v)
     if o_part is None:
-        o_part = torch.empty((n_split, B, H, Nq, d), dtype=torch.float32, device=q.device)
+        o_part = _empty(stream, (n_split, B, H, Nq, d), torch.float32, q.device)
     if lse_part is None:
-        lse_part = torch.empty((n_split, B, H, Nq), dtype=torch.float32, device=q.device)
+        lse_part = _empty(stream, (n_split, B, H, Nq), torch.float32, q.device)
     _check_bhnd("o_part", o_part.view(n_split * B, H, Nq, d), (n_split * B, H, Nq, d), torch.float32)
     _check_bhnd("lse_part", lse_part.view(n_split * B, H, Nq, 1), (n_split * B, H, Nq, 1), torch.float32)
     sc = float(scale) if scale is not None else d ** -0.5
@@ -585,9 +587,9 @@ def fa_merge_partials(o_part, lse_part, o=None, lse=None, stream=None):
     _check_bhnd("o_part", o_part.view(n_split * B, H, Nq, d), (n_split * B, H, Nq, d), torch.float32)
     _check_bhnd("lse_part", lse_part.view(n_split * B, H, Nq, 1), (n_split * B, H, Nq, 1), torch.float32)
     if o is None:
-        o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=o_part.device)
+        o = _empty(stream, (B, H, Nq, d), torch.bfloat16, o_part.device)
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=o_part.device)
+        lse = _empty(stream, (B, H, Nq), torch.float32, o_part.device)
     _check_bhnd("o", o, (B, H, Nq, d), torch.bfloat16)
     _check_bhnd("lse", lse.view(B, H, Nq, 1), (B, H, Nq, 1), torch.float32)
     with torch.cuda.device(o_part.device):
@@ -614,14 +616,13 @@ def fa_fwd_splitkv(q, k, v, o=None, lse=None, workspace=None, n_split: int = 0, 
     _check_strided("v", v, (B, H, Nk, d), torch.bfloat16)
     n = n_split if n_split > 0 else max(1, fa_splitkv_default_splits(B, H, Nq, Nk, d))
     if o is None:
-        o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+        o = _empty(stream, (B, H, Nq, d), torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, H, Nq), torch.float32, q.device)
     _check_strided("o", o, (B, H, Nq, d), torch.bfloat16)
     _check_bhnd("lse", lse.view(B, H, Nq, 1), (B, H, Nq, 1), torch.float32)
     if workspace is None:
-        workspace = torch.empty(max(fa_splitkv_workspace_size(B, H, Nq, d, n), 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(stream, max(fa_splitkv_workspace_size(B, H, Nq, d, n), 1), torch.uint8, q.device)
     sc = float(scale) if scale is not None else d ** -0.5
     with torch.cuda.device(q.device):
         if all(t.is_contiguous() for t in (q, k, v, o)):
@@ -773,11 +774,11 @@ def fa_w4a16_gemm(x, wq, scales, zeros, y=None, workspace=None, n_split: int = 0
         if t.dtype != dt or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor of shape {shape}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _empty(stream, (M, N), torch.float16, x.device)
     n = n_split if n_split > 0 else max(1, int(lib.fa_w4a16_default_splits(M, N, K)))
     need = int(lib.fa_w4a16_workspace_size(M, N, K, n))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(stream, need, torch.uint8, x.device)
     with torch.cuda.device(x.device):
         st = lib.fa_w4a16_gemm(_ptr(x), _ptr(wq), _ptr(scales), _ptr(zeros), _ptr(y), _ptr(workspace),
                                0 if workspace is None else _ws_bytes(workspace), M, N, K, n, _stream_handle(stream))

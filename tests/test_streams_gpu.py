@@ -59,3 +59,54 @@ def test_paged_decode():
     n = torch.tensor([400, 1, 77], dtype=torch.int32, device="cuda")
     q = _randn(B, H, d, seed=3)
     _check(lambda stream: fa.fa_paged_decode(q, kc, vc, table, n, stream=stream), fa.fa_paged_decode_workspace_size(B, H, Hkv, d))
+
+
+def _qkvdo(B, H, N, d, dtype=torch.bfloat16):
+    return [_randn(B, H, N, d, seed=10 + i, dtype=dtype) for i in range(4)]
+
+
+def test_forward_and_backward():
+    B, H, N, d = 1, 4, 600, 64
+    q, k, v, do = _qkvdo(B, H, N, d)
+    o, lse = fa.fa_fwd(q, k, v, causal=True)
+    _check(lambda stream: fa.fa_fwd(q, k, v, causal=True, stream=stream))
+    _check(lambda stream: fa.fa_bwd(q, k, v, o, do, lse, causal=True, deterministic=True, stream=stream),
+           fa.fa_bwd_workspace_size(B, H, N, d))
+
+
+def test_fp8():
+    B, H, N, d = 1, 3, 500, 64
+    q, k, v, do = _qkvdo(B, H, N, d)
+    shape = (B, H, N, d)
+    signs = fa.fa_fp8_rotation_signs(7, d).cuda()
+
+    def forward(stream):
+        ws = fa.fa_fp8_prepare(q, k, v, signs, stream=stream)
+        return fa.fa_fwd_fp8(ws, shape, causal=True, stream=stream)
+    o, lse = forward(None)
+    ws = fa.fa_fp8_prepare_seeded(q, k, v, 7)
+    _check(forward, fa.fa_fp8_workspace_size(*shape))
+    _check(lambda stream: fa.fa_fwd_fp8(fa.fa_fp8_prepare_seeded(q, k, v, 7, stream=stream), shape, causal=True, stream=stream),
+           fa.fa_fp8_workspace_size(*shape))
+    _check(lambda stream: fa.fa_fp8_dequantize(ws, shape, stream=stream))
+    _check(lambda stream: fa.fa_bwd_fp8(ws, signs, o, do, lse, causal=True, deterministic=True, stream=stream),
+           fa.fa_bwd_fp8_workspace_size(*shape))
+
+
+def test_split_kv():
+    B, H, Nq, Nk, d = 2, 4, 3, 1500, 128
+    q, k, v = (_randn(B, H, n, d, seed=20 + i) for i, n in enumerate((Nq, Nk, Nk)))
+    parts = fa.fa_fwd_splitkv_partial(q, k, v, 4)
+    _check(lambda stream: fa.fa_fwd_splitkv_partial(q, k, v, 4, stream=stream))
+    _check(lambda stream: fa.fa_merge_partials(*parts, stream=stream))
+    _check(lambda stream: fa.fa_fwd_splitkv(q, k, v, n_split=4, stream=stream), fa.fa_splitkv_workspace_size(B, H, Nq, d, 4))
+
+
+def test_w4a16():
+    M, N, K = 3, 512, 1024
+    g = torch.Generator().manual_seed(30)
+    x = torch.randn(M, K, generator=g).half().cuda()
+    wq = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=g).to(torch.int32).cuda()
+    scales = (torch.rand(K // 128, N, generator=g) * 0.01 + 0.005).half().cuda()
+    zeros = torch.randint(0, 16, (K // 128, N), generator=g).to(torch.uint8).cuda()
+    _check(lambda stream: [fa.fa_w4a16_gemm(x, wq, scales, zeros, n_split=2, stream=stream)], fa.fa_w4a16_workspace_size(M, N, K, 2))
