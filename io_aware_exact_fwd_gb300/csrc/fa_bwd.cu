@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* dst = dq_acc + (static_cast<size_t>(bh) * N + q0) * D + dcol;
       const int lim = min(kBqB, N - q0);
       if constexpr (DET) {
-        const float mul = pow2f(det_shift(dq_bmax[static_cast<size_t>(bh) * (Npad / kBqB) + i0 + it],
-                                          kv_max[2 * bh], kv_max[2 * bh + 1]));
+        const float mul = pow2f(det_shift(det_bound(dq_bmax[static_cast<size_t>(bh) * (Npad / kBqB) + i0 + it],
+                                                    kv_max[2 * bh], kv_max[2 * bh + 1])));
         constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: x + kMagic rounds x to an integer in the low bits
         int* dsti = reinterpret_cast<int*>(dst);
 #pragma unroll
@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const __nv_bfloat16
     // multiples of kRpb, which divides 64): reduce to one atomic per block.
 #pragma unroll
     for (int m = kTpr / 2; m >= 1; m >>= 1) nrm += __shfl_xor_sync(0xffffffffu, nrm, m, kTpr);
-    float mx = lse_row == -INFINITY ? 0.f : sqrtf(nrm);  // 0 for padded rows and rows without keys
+    // 0 for padded rows and rows without keys; infinite if dQ of the row is not finite.
+    float mx = lse_row == -INFINITY ? 0.f : fabsf(lse_row) + fabsf(acc) + nrm < INFINITY ? sqrtf(nrm) : INFINITY;
 #pragma unroll
     for (int m = kTpr; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
     __shared__ float red[8];
@@ -556,12 +557,12 @@ __global__ void __launch_bounds__(256) bwd_kv_bound_kernel(const __nv_bfloat16* 
     for (int e = 0; e < 4; ++e) {
       const float2 a = __bfloat1622float2(kp[e]);
       const float2 b = __bfloat1622float2(vp[e]);
-      km = fmaxf(km, fmaxf(fabsf(a.x), fabsf(a.y)));
+      km = fmaxf(km, a.x + a.y == a.x + a.y ? fmaxf(fabsf(a.x), fabsf(a.y)) : INFINITY);  // (NaN counts as one)
       vn = fmaf(b.x, b.x, fmaf(b.y, b.y, vn));
     }
 #pragma unroll
     for (int m = kTpr / 2; m >= 1; m >>= 1) vn += __shfl_xor_sync(0xffffffffu, vn, m, kTpr);
-    vm = fmaxf(vm, sqrtf(vn));
+    vm = fmaxf(vm, vn == vn ? sqrtf(vn) : INFINITY);
   }
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) {
@@ -602,8 +603,8 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
   const int qrow = static_cast<int>(row - bh * N);
   if (DET) {
     const long long kvh = bh / group;  // = b Hkv + h / group: the key/value head that query head bh reads
-    const float inv =
-        pow2f(-det_shift(dq_bmax[bh * (Npad / kBqB) + qrow / kBqB], kv_max[2 * kvh], kv_max[2 * kvh + 1]));
+    const float bound = det_bound(dq_bmax[bh * (Npad / kBqB) + qrow / kBqB], kv_max[2 * kvh], kv_max[2 * kvh + 1]);
+    const float inv = bound < INFINITY ? pow2f(-det_shift(bound)) : NAN;
     auto cv = [&](float x) { return static_cast<float>(__float_as_int(x)) * inv; };
     a = make_float4(cv(a.x), cv(a.y), cv(a.z), cv(a.w));
     b = make_float4(cv(b.x), cv(b.y), cv(b.z), cv(b.w));

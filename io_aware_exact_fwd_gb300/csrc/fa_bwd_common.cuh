@@ -111,10 +111,17 @@ __device__ __forceinline__ bool warp_wait_b_suspend(uint64_t* bar, uint32_t pari
 // once (x 2^S, nearest) and added as int32: integer addition does not depend on
 // order, so dQ is the same bits on every run.  2^22 keeps the float-to-int step
 // a single add of 1.5 * 2^23 (the rounding is the fp32 add's).
-__device__ __forceinline__ int det_shift(float dq_block_max, float vmax, float kmax) {
-  const float bound = 2.25f * dq_block_max * vmax * kmax;
+//
+// NaN and infinities have no place in such sums (a NaN contribution would add an ordinary integer), so they are
+// met in the maxima: a row that sees a key with an LSE, D or |dO| that is not finite gives its block an infinite
+// maximum, a k or v that is not finite gives its head one, and the conversion writes NaN wherever the bound is
+// not finite.  (Telling them apart contribution by contribution costs the plain kernel 4 %.)
+__device__ __forceinline__ float det_bound(float dq_block_max, float vmax, float kmax) {
+  return dq_block_max > 0.f ? 2.25f * dq_block_max * vmax * kmax : 0.f;  // (0 times an infinity counts as 0 there)
+}
+__device__ __forceinline__ int det_shift(float bound) {
   if (!(bound > 0.f)) return 100;           // all-zero block (or no data): nothing to scale
-  if (!(bound < 3.0e38f)) return -100;      // non-finite inputs: the result is undefined anyway
+  if (!(bound < 3.0e38f)) return -100;
   int e;
   frexpf(bound, &e);                        // bound < 2^e
   return max(-100, min(100, 22 - e));

@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = p.N - q0 - q_lane;
       float mul = 1.f;
       if constexpr (DET)
-        mul = pow2f(det_shift(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1]));
+        mul = pow2f(det_shift(
+            det_bound(p.dq_bmax[bh * head_blocks + q0 / kBqB], p.kv_max[2 * bhk], p.kv_max[2 * bhk + 1])));
       auto add = [&](auto whole_c) {
         constexpr bool kWhole = decltype(whole_c)::value;
 #pragma unroll

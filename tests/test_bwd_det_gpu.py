@@ -124,3 +124,32 @@ def test_deterministic_config_n8192_whole_heads(causal):
     report(f"bwd deterministic B=2 H=16 N=8192 d=128 causal={int(causal)}", heads=len(errs), dq=worst[0],
            dk=worst[1], dv=worst[2])
     assert max(worst) <= BWD_REL, worst
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what,value", [("k", float("nan")), ("k", float("inf")), ("q", float("nan")), ("v", float("nan")),
+                                        ("v", float("-inf")), ("do", float("nan")), ("do", float("inf"))])
+def test_nan_and_infinities_come_through_deterministic_dq(what, value, d):
+    # Wherever fa_bwd's dQ is not finite, the fixed-point sums say NaN too; what a query or its dO holds stays
+    # inside its block of 64 rows, and inside its head.
+    N = 6400  # 50 key blocks
+    t = dict(zip(("q", "k", "v", "do"), _inputs(1, 2, N, d, 62)))
+    at = 3000
+    t[what][0, 0, at, 5] = value
+    q, k, v, do = t["q"], t["k"], t["v"], t["do"]
+    for causal in (False, True):
+        o, lse = fa.fa_fwd(q, k, v, causal=causal)
+        want, dk, dv = fa.fa_bwd(q, k, v, o, do, lse, causal=causal)
+        got, dk1, dv1 = fa.fa_bwd(q, k, v, o, do, lse, causal=causal, deterministic=True)
+        fa.fa_sync_check()
+        bad = ~torch.isfinite(want)
+        assert bool(bad.any())
+        assert bool(torch.isnan(got[bad]).all())
+        assert torch.equal(torch.isnan(dk), torch.isnan(dk1)) and torch.equal(torch.isnan(dv), torch.isnan(dv1))
+        if what in ("q", "do"):
+            ok = torch.ones(N, dtype=torch.bool)
+            ok[at // 64 * 64:at // 64 * 64 + 64] = False
+            assert bool(torch.isfinite(want[0, 0, ok]).all())
+            err = (got[0, 0, ok].float() - want[0, 0, ok].float()).abs().max()
+            assert float(err) <= BWD_REL * float(want[0, 0, ok].abs().max())
+        assert bool(torch.isfinite(got[0, 1]).all())

@@ -496,3 +496,22 @@ def test_biased_scores_on_both_sides_far_below_the_cap(H, N, cap):
     refs, bounds = scored_backward(*x, *args)
     for name, a, ref, bd in zip(("dq", "dk", "dv"), grads, refs, bounds):
         _check(a, ref, bd, name)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("H,Hkv", [(2, 1), (64, 32)])  # key blocks whose steps are divided, and whole ones
+@pytest.mark.parametrize("what,value", [("k", float("nan")), ("k", float("inf")), ("v", float("nan")), ("do", float("inf"))])
+def test_nan_and_infinities_come_through_deterministic_dq(what, value, H, Hkv, cap):
+    B, N, d = 1, 700, 64
+    t = dict(zip(("q", "k", "v", "do"), _inputs(B, H, Hkv, N, d, 64)))
+    t[what][0, 0, 300, 5] = value
+    q, k, v, do = t["q"], t["k"], t["v"], t["do"]
+    kw = dict(causal=True, softcap=cap, slopes=_slopes(H))
+    o, lse = fa.fa_fwd_scored(q, k, v, **kw)
+    want = fa.fa_bwd_scored(q, k, v, o, do, lse, **kw)[0]
+    got = fa.fa_bwd_scored(q, k, v, o, do, lse, deterministic=True, **kw)[0]
+    fa.fa_sync_check()
+    bad = ~torch.isfinite(want)
+    assert bool(bad.any()) and bool(torch.isnan(got[bad]).all())
+    other = slice(H // Hkv, None)  # heads that read another key/value head
+    assert bool(torch.isfinite(got[:, other]).all())
