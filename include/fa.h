@@ -505,7 +505,7 @@ FA_API int fa_mask_plan(const int32_t* cu_docs, const int32_t* prefix, int n_doc
  * with the stride rules of fa_fwd_strided (NULL = dense).
  *   plan    : from fa_mask_plan for the same B, N (plan_bytes its size), or NULL.  One
  *             made for other rows gives an unspecified mask, but no access outside the tensors
- *   softcap : 0, or > 0 with 2 softcap and 4 scale / softcap finite in fp32
+ *   softcap : 0, or > 0 with 2 softcap finite and 4 scale / softcap a normal number in fp32
  *   slopes  : const float [H] on the device (finite), or NULL
  * Numerics as fa_fwd: scores, their cap and bias, the running maximum and sum and
  * the accumulators in fp32, P rounded to bf16 for P V.  The same bits on every run.

@@ -13,10 +13,11 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 constexpr long long kIntMax = 0x7fffffffLL;
 
-// The kernels multiply products by 4 scale / softcap and tanh by softcap log2(e): both have to be finite.
+// The kernels multiply products by 4 scale / softcap and tanh by softcap log2(e): both have to be finite, and
+// the first a normal number (a subnormal one has lost bits).
 bool bad_score(float scale, float softcap) {
   return !(scale > 0.f) || !isfinite(scale) || !(softcap >= 0.f) || !isfinite(2.f * softcap) ||
-         (softcap > 0.f && !isfinite(4.f * scale / softcap));
+         (softcap > 0.f && !isnormal(4.f * scale / softcap));
 }
 
 // FA_OK, a status, or -1 for "valid, but nothing to do".

@@ -140,3 +140,14 @@ def test_binding_refuses_before_the_library(lib):
         fa.fa_mask_plan(1, 8, torch.zeros(1, 3, dtype=torch.int32))
     with pytest.raises(TypeError):
         fa.fa_paged_decode(torch.zeros(1, 2, 64), x, x, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("scale,cap", [(0.125, 1e38), (1e-8, 1e31), (1e-30, 1e10), (1e-38, 4.0)])
+def test_caps_so_large_that_the_scores_lose_their_bits(lib, scale, cap):
+    # 4 scale / softcap would be subnormal or 0 in fp32.
+    t = (vp(FAKE), None)
+    mask = (2, 4, 2, 100, 64, vp(0), 0, 0, scale, cap, vp(0))
+    assert lib.fa_fwd_scored(*t, *t, *t, *t, vp(FAKE), *mask, vp(0)) == INV
+    assert lib.fa_bwd_scored(*t, *t, *t, *t, *t, vp(FAKE), *t, *t, *t, vp(FAKE), 1 << 40, *mask, 0, vp(0)) == INV
+    assert lib.fa_paged_decode(*t, *t, *t, vp(FAKE), 4, vp(FAKE), *t, vp(FAKE), vp(FAKE), 1 << 40, 2, 4, 2, 64, 16, 9, 4, 1, scale,
+                               cap, vp(0), vp(0)) == INV
