@@ -515,3 +515,28 @@ def test_nan_and_infinities_come_through_deterministic_dq(what, value, H, Hkv, c
     assert bool(bad.any()) and bool(torch.isnan(got[bad]).all())
     other = slice(H // Hkv, None)  # heads that read another key/value head
     assert bool(torch.isfinite(got[:, other]).all())
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("H,Hkv", [(2, 1), (64, 64)])  # key blocks whose steps are divided, and whole ones
+def test_masks_that_break_the_contract_give_finite_values_inside_the_outputs(H, Hkv, deterministic):
+    # Offsets that decrease or leave the row, a plan of longer rows, arbitrary bytes: any mask, but outputs that
+    # are finite (an LSE may be -inf) and nothing written beside them.
+    B, N, d = 2, 400, 64
+    q, k, v, do = _inputs(B, H, Hkv, N, d, 65)
+    plans = [_docs([cu, cu], [[7, -3, 2 ** 31 - 1]] * B, True, B, N)
+             for cu in ([-50, 300, 100, 9999], [390, 10, 380, 20], [500, 600, 700, 800], [-9, -8, -7, -6])]
+    plans.append(fa.fa_mask_plan(1, B * N, device="cuda"))
+    plans.append(torch.randint(0, 256, (16 * B * N,), dtype=torch.uint8, generator=torch.Generator().manual_seed(4)).cuda())
+    for plan in plans:
+        bufs = [torch.full((B, h + 2, N, d), 3.0, dtype=torch.bfloat16, device="cuda") for h in (H, H, Hkv, Hkv)]
+        lbuf = torch.full((B * H * N + 512,), 3.0, device="cuda")
+        views = [x[:, 1:-1] for x in bufs]
+        o, lse = fa.fa_fwd_scored(q, k, v, o=views[0], lse=lbuf[256:-256].view(B, H, N), plan=plan)
+        fa.fa_bwd_scored(q, k, v, o, do, lse, *views[1:], plan=plan, deterministic=deterministic)
+        fa.fa_sync_check()
+        for x, view in zip(bufs, views):
+            assert bool(torch.isfinite(view).all())
+            assert bool((x[:, 0] == 3).all()) and bool((x[:, -1] == 3).all())
+        assert bool((torch.isfinite(lse) | torch.isneginf(lse)).all())
+        assert bool((lbuf[:256] == 3).all()) and bool((lbuf[-256:] == 3).all())
