@@ -618,8 +618,11 @@ int parts_of(int B, int H, int Hkv, int N) {
 // Key/value heads worked on together: as many as have dQ accumulators of 48 MB, which then stay in the L2 (129 MB, with
 // what else passes through it) between the adds of a head's key blocks (d = 128: B=16 H=16 N=1024 causal 373 us over
 // all heads at once, 297 in runs; B=2 H=16 N=8192 1185 | 1107-1132, full 2231 | 2133-2156; d = 64, H=32 N=8192 biased
-// 1771 | 1688).  The last run's heavy blocks start late, so only with 10 blocks an SM or more (6.7: B=2
-// H=32/8 N=8192 of eight documents 653 us, 745 in runs).
+// 1771 | 1688).  Where a group's alone are more (long rows of large groups), one key/value head at a time: its key
+// blocks walk the query heads in the same order, so the adds of a time still fall on few of them (d = 128, B=1 H=64/8
+// N=32768: full 81.6 ms over all heads, 66.0 one at a time, causal 34.7 | 33.4; N=16384 17.2 | 17.3, 8.5 | 8.5; budgeted
+// by one query head instead 67.2 and 33.4).  The last run's heavy blocks start late, so only with 10 blocks an SM or
+// more (6.7: B=2 H=32/8 N=8192 of eight documents 653 us, 745 in runs).
 int run_of(int B, int H, int Hkv, int N, int d) {
   const long long heads = static_cast<long long>(B) * Hkv, blocks = (N + kBkB - 1) / kBkB * heads;
   if (blocks < 10ll * sm_count()) return static_cast<int>(heads);
