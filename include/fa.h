@@ -155,7 +155,9 @@ FA_API int fa_bwd_strided(const void* q, const int64_t* q_strides, const void* k
  * 64-row query block from a bound on |dQ| that holds for any inputs:
  *     |dQacc_ic| <= 2 |dO_i| max_j |v_j| max_jc |k_jc|   (x 1.125 margin)
  * so that every partial sum stays below 2^22 in magnitude; the rounding of each
- * contribution is at most 2^-S / 2, far below the bf16 output's rounding.  dK and
+ * contribution is at most 2^-S / 2, about 2^-23 of the bound: less than the bf16 output's
+ * rounding for elements near their block's largest, and an absolute error for those far
+ * below it (rows whose softmax leaves them almost no gradient).  dK and
  * dV are those of fa_bwd (already reproducible).  Costs one extra pass over K and
  * V for the bound.  Arguments, workspace and errors: exactly as fa_bwd.
  * Precondition: `lse` is the forward's LSE for the same q, k, scale and causal
@@ -477,6 +479,11 @@ FA_API int fa_fwd_splitkv_strided(const void* q, const int64_t* q_strides, const
  * is 0, their LSE -inf, and their dQ, dK, dV are 0.  What q, k, v and dout hold in
  * padding does not matter as long as it is finite (a weight of exactly 0 times an
  * infinity or NaN would not be 0).
+ *
+ * NaN and infinities in what a row sees come out as the formulas have them: a NaN
+ * score makes the row's O and LSE NaN, the cap takes an infinite score to +-softcap, a
+ * score of -inf weighs 0.  Where the mask hides a pair, a NaN or infinity of its v (in
+ * the gradients also of its k, q or dout) may still reach results of the same block of 128 keys.
  */
 
 /* Bytes of a mask plan for B rows of N positions (16 B N; 0 for invalid sizes). */
@@ -509,6 +516,10 @@ FA_API int fa_mask_plan(const int32_t* cu_docs, const int32_t* prefix, int n_doc
  *   slopes  : const float [H] on the device (finite), or NULL
  * Numerics as fa_fwd: scores, their cap and bias, the running maximum and sum and
  * the accumulators in fp32, P rounded to bf16 for P V.  The same bits on every run.
+ * The bias comes with an error of up to 2^-15 |slope| + 2^-23 |slope| |i - j|.  O is summed
+ * before it is divided, with weights up to 2^60 (no cap, or one above 80 / log2(e) = 55.4)
+ * or of 2^-80 .. 2^80 (caps up to that): |v| has to stay below 2^68 / N and 2^48 / N, and
+ * with such a cap parts of v below 2^-46 may be lost in rows that score near -softcap.
  * Errors as fa_fwd_strided; FA_ERR_INVALID_ARG also for H not a multiple of Hkv, a
  * bad softcap, or causal = 1 with a plan; FA_ERR_WORKSPACE for a short plan.
  */
@@ -588,7 +599,9 @@ FA_API size_t fa_paged_decode_workspace_size(int B, int H, int Hkv, int d);
  * evenly over the SMs on the device (the lengths are never read by the host) and the
  * parts of a sequence joined by their LSE; the same bits on every run.
  * The workspace (256-byte aligned) is scratch; calls that overlap need their own.
- * softcap and slopes as fa_fwd_scored.  Errors as fa_fwd_splitkv.
+ * softcap and slopes as fa_fwd_scored.  fp16 weights keep all their bits down to 2^-29 of
+ * a sequence's largest and are lost below 2^-40.  NaN and infinities as fa_fwd_scored,
+ * but none reaches a sequence or key/value head that does not hold it.  Errors as fa_fwd_splitkv.
  */
 FA_API int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache,
                            const int64_t* k_cache_strides, const void* v_cache, const int64_t* v_cache_strides,

@@ -60,12 +60,13 @@ constexpr uint32_t kTmemCols = 512;
 // A block is exponentiated against the running reference without its own maximum; its
 // row sum then proves that no P passed 2^60 (else the block is redone).  P is bf16 and
 // everything it enters is fp32, so a reference that is off costs no precision while
-// weights, sums and O stay far from the ends of the exponent's range.
+// weights, sums and O stay inside the exponent's range (|v| below 2^68 / N).
 constexpr float kSpeculationSumBound = 1.152921504606847e18f;
 // With a cap, scores lie in [-softcap, softcap] log2(e) (plus a bias whose maximum over
 // the row's keys is known): up to kBoundedCap on softcap log2(e) that maximum alone is the
-// reference, with P in 2^-80 .. 2^80 and no maximum taken at all (a cap of 55 at B=2 H=16/4
-// N=8192 causal: 535 us; one of 56, with the running reference: 767).
+// reference, with P in 2^-80 .. 2^80 (so |v| below 2^48 / N, and what is below 2^-46 of it may be lost where
+// scores lie near -softcap) and no maximum taken at all (a cap of 55 at B=2 H=16/4
+// N=8192 causal: 535 us; one of 56, with the running reference: 781).
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
 
