@@ -167,7 +167,7 @@ FA_API int fa_bwd_strided(const void* q, const int64_t* q_strides, const void* k
  * being reported (fa_bwd would return finite but equally meaningless values).
  * NaN and infinities: integer sums cannot carry them, so dq is NaN wherever the bound
  * is not finite: for the 64-row block of a query row whose LSE, D or |dout| is not
- * finite, and for every row of a head whose k or v holds such a value.
+ * finite, and for every block with a dout other than 0 of a head whose k or v holds such a value.
  */
 FA_API int fa_bwd_deterministic(const void* q, const void* k, const void* v, const void* o, const void* dout,
                                 const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,

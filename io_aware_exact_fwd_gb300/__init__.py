@@ -7,10 +7,11 @@ tensors, passes their device pointers and the current CUDA stream, and raises
 kernels; there is no fallback.  If libfa.so is missing, importing the binding
 still works but every call raises, so a missing build is never silent.
 
-PyTorch is used only as device-memory and stream plumbing.  With ``stream`` a call runs on that stream,
-and what it allocates comes from that stream's memory, as under ``torch.cuda.stream(stream)``.  Most calls marshal with
-ctypes; those of scored attention and of the paged cache, made once a layer and token,
-with a small compiled module (csrc/fa_torch.cpp).
+PyTorch is used only as device-memory and stream plumbing.  With ``stream`` a call
+runs on that stream, and what it allocates comes from that stream's memory, as under
+``torch.cuda.stream(stream)``.  Most calls marshal with ctypes; those of scored
+attention and of the paged cache, made once a layer and token, with a small compiled
+module (csrc/fa_torch.cpp).
 """
 
 from __future__ import annotations

@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(256) bwd_dq_convert_kernel(const float* __rest
   if (DET) {
     const long long kvh = bh / group;  // = b Hkv + h / group: the key/value head that query head bh reads
     const float bound = det_bound(dq_bmax[bh * (Npad / kBqB) + qrow / kBqB], kv_max[2 * kvh], kv_max[2 * kvh + 1]);
-    const float inv = bound < INFINITY ? pow2f(-det_shift(bound)) : NAN;
+    const float inv = bound == 0.f ? 0.f : bound < INFINITY ? pow2f(-det_shift(bound)) : NAN;
     auto cv = [&](float x) { return static_cast<float>(__float_as_int(x)) * inv; };
     a = make_float4(cv(a.x), cv(a.y), cv(a.z), cv(a.w));
     b = make_float4(cv(b.x), cv(b.y), cv(b.z), cv(b.w));

@@ -153,3 +153,15 @@ def test_nan_and_infinities_come_through_deterministic_dq(what, value, d):
             err = (got[0, 0, ok].float() - want[0, 0, ok].float()).abs().max()
             assert float(err) <= BWD_REL * float(want[0, 0, ok].abs().max())
         assert bool(torch.isfinite(got[0, 1]).all())
+
+
+def test_deterministic_dq_of_a_block_without_a_gradient_is_zero():
+    # dO is 0 in rows 64 .. 127 and a key is infinite (its scores are +-inf): those rows get 0 or, where their
+    # LSE is not finite, NaN, and nothing in between.
+    q, k, v, do = _inputs(1, 1, 256, 64, 63)
+    do[0, 0, 64:128] = 0.0
+    k[0, 0, 200, 5] = float("inf")
+    o, lse = fa.fa_fwd(q, k, v)
+    got = fa.fa_bwd(q, k, v, o, do, lse, deterministic=True)[0][0, 0, 64:128]
+    fa.fa_sync_check()
+    assert bool((torch.isnan(got) | (got == 0)).all())
