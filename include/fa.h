@@ -611,6 +611,113 @@ FA_API int fa_paged_decode(const void* q, const int64_t* q_strides, const void* 
                            float softcap, const float* slopes, fa_stream_t stream);
 
 /*
+ * The cache in 8 bits: as above, but k_cache and v_cache hold e4m3 codes (OCP, "fn"; strides multiples
+ * of 16 elements) and each block of 16 tokens of a page and head has a scale: k_scales,
+ * v_scales are float [n_pages, Hkv, page_size / 16], dense, and a value is decode(code) * scale.
+ * dtype is that of the 16-bit tensors of the call.  Half the bytes of the 16-bit cache a token (and
+ * 4 / (16 d) for the scales), at a rounding of at most 2^-4 a value.
+ */
+
+/*
+ * fa_paged_append_fp8 -- fa_paged_append into such a cache.  A block's scale is the power of two 2^e:
+ *   e = the smallest integer >= -126 such that every new value of the block is at most 448 * 2^e,
+ *   or the block's e before, if it held tokens of the sequence and that is larger;
+ *   code = e4m3(x * 2^-e), round to nearest even, saturating.
+ * Where the scale grows the older tokens' codes are re-coded, code * 2^(e before - e): exact unless a
+ * code falls below the type's normal range.  What a block held before its first token (page reuse) does not
+ * matter, nor is it changed behind the last new one.  Infinities do not count for e and saturate; a NaN
+ * does not count either and stays a NaN.  A scale in a half-filled block that is no power of two (not
+ * this call's) is rounded up to one.  Otherwise as fa_paged_append; one call must not write a block twice.
+ */
+FA_API int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                               void* k_cache, const int64_t* k_cache_strides, void* v_cache,
+                               const int64_t* v_cache_strides, float* k_scales, float* v_scales,
+                               const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                               const int32_t* cu_new, int B, int T, int Hkv, int d, int page_size, int n_pages,
+                               int max_pages, int dtype, fa_stream_t stream);
+
+/*
+ * fa_paged_decode_fp8 -- fa_paged_decode over such a cache; the workspace is fa_paged_decode's.
+ * Any positive finite scales.  The products take q as fp16 times a power of two of its row: entries
+ * keep all their bits down to 2^-29 of the row's largest and are off by at most 2^-40 of that below.
+ * Weights times V scales keep theirs down to 2^-29 of the largest such product of the sequence and are
+ * lost below 2^-40.  Sums, maxima and scores are fp32.  The same bits on every run.
+ */
+FA_API int fa_paged_decode_fp8(const void* q, const int64_t* q_strides, const void* k_cache,
+                               const int64_t* k_cache_strides, const void* v_cache, const int64_t* v_cache_strides,
+                               const float* k_scales, const float* v_scales, const int32_t* page_table,
+                               int64_t table_stride, const int32_t* seq_lens, void* o, const int64_t* o_strides,
+                               float* lse, void* workspace, size_t ws_bytes, int B, int H, int Hkv, int d,
+                               int page_size, int n_pages, int max_pages, int dtype, float scale, float softcap,
+                               const float* slopes, fa_stream_t stream);
+
+/* Bytes of workspace fa_paged_resize needs (0 for invalid or unsupported sizes). */
+FA_API size_t fa_paged_resize_workspace_size(int B);
+
+/*
+ * fa_paged_resize -- a paged cache's bookkeeping, all on the device: sequence b becomes delta[b] tokens longer, or
+ * shorter (a sequence that ends: -seq_lens[b]; tokens taken back).  Pages come from and go to a list of free ones.
+ *   page_table  : int32, row b at page_table + b*table_stride, max_pages entries; the entries of the pages that a
+ *                 sequence gets are written, all others stay (those of pages given back too)
+ *   seq_lens    : const int32 [B]       delta : const int32 [B]
+ *   free_pages  : int32 [capacity], the first free_count[0] (clamped to [0, capacity]) are free
+ *   seq_lens_out, free_count_out : the new lengths and count; each may be its input itself
+ *   cu_new      : int32 [B + 1], the sums of max(delta, 0): the rows of each sequence's new tokens
+ *   status      : int32 [2]: pages that were missing, and sequences whose length would be negative or past the table
+ *                 (one more if pages given back do not fit the list, or the new tokens pass 2^31 - 1).  If either is
+ *                 not 0 the call has changed nothing: lengths and count as they were, cu_new 0
+ *   slots       : int64 [T] or NULL: new token t's place in the cache, page * page_size + its place in the page
+ *   positions   : int32 [T] or NULL: its position in the sequence.  Both -1 from cu_new[B] on
+ * The order is fixed: pages given back go behind the free ones, by sequence and place in it; then the pages taken come
+ * from the end of the list, by sequence and place.  A page that several sequences share must not be given
+ * back.  delta and the outputs must not overlap each other.  page_size as above, B up to 65535.
+ */
+FA_API int fa_paged_resize(int32_t* page_table, int64_t table_stride, const int32_t* seq_lens, const int32_t* delta,
+                           int32_t* free_pages, int capacity, const int32_t* free_count, int32_t* seq_lens_out,
+                           int32_t* free_count_out, int32_t* cu_new, int32_t* status, int64_t* slots,
+                           int32_t* positions, int T, void* workspace, size_t ws_bytes, int B, int page_size,
+                           int max_pages, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope -- queries and keys as attention takes them: every head's row normalised, weighted and rotated
+ * by its token's position.
+ *   q, q_out : [B, H, N, d]   k, k_out : [B, Hkv, N, d]   (strides as fa_fwd_strided; NULL = dense)
+ *   dtype    : 1 = bf16, 2 = fp16, of these four.  An output may be its input itself, with the same strides
+ *   norm = 1 : y = x / sqrt(mean(x^2) + eps) * w, over the d values of a row, with w = q_weight or k_weight, [d] of
+ *              weight_dtype (0 = fp32, 1 = bf16, 2 = fp16), NULL: no weights.  eps finite, > 0
+ *   norm = 0 : y = x; no weights
+ *   rot, inv_freq : the first rot values of a row (a multiple of 16, at most d) are rotated in pairs: pair i, of
+ *              values i and i + rot / 2, or with interleaved = 1 of 2i and 2i + 1, by the angle position * inv_freq[i],
+ *              (a, b) -> (a cos - b sin, a sin + b cos).  inv_freq: const float [rot / 2], finite, |inv_freq| < 2^64;
+ *              NULL with rot = 0: no rotation
+ *   positions : const int32 [B, N], any value; NULL: 0 .. N - 1
+ * Sums and products in fp32, angles exact to 2^-32 of a turn (then fp32) at any position, one rounding at the end.  The
+ * squares' sum has to stay below fp32's range.  Packed tokens are B = 1.  H or Hkv may be 0.
+ */
+FA_API int fa_qk_norm_rope(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                           const void* q_weight, const void* k_weight, const float* inv_freq, const int32_t* positions,
+                           void* q_out, const int64_t* q_out_strides, void* k_out, const int64_t* k_out_strides, int B,
+                           int H, int Hkv, int N, int d, int rot, int norm, float eps, int weight_dtype,
+                           int interleaved, int dtype, fa_stream_t stream);
+
+/* Bytes of workspace fa_qk_norm_rope_bwd needs for weights' gradients on the current device (0 for another d). */
+FA_API size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * fa_qk_norm_rope_bwd -- its gradient: from q, k as given to the forward and the gradients dq_out, dk_out of its
+ * outputs, dq and dk (dtype, any strides; dq may be dq_out itself) and, fp32 [d] each or NULL, those of the weights,
+ * summed over all rows in a fixed order (the same bits on every run; 0 for no rows).  Without a norm q and k are not
+ * read and may be NULL.  The workspace (4-byte aligned scratch) is needed if dq_weight or dk_weight is given.
+ */
+FA_API int fa_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                               const void* dq_out, const int64_t* dq_out_strides, const void* dk_out,
+                               const int64_t* dk_out_strides, const void* q_weight, const void* k_weight,
+                               const float* inv_freq, const int32_t* positions, void* dq, const int64_t* dq_strides,
+                               void* dk, const int64_t* dk_strides, float* dq_weight, float* dk_weight,
+                               void* workspace, size_t ws_bytes, int B, int H, int Hkv, int N, int d, int rot, int norm,
+                               float eps, int weight_dtype, int interleaved, int dtype, fa_stream_t stream);
+
+/*
  * W4A16: 4-bit weights times 16-bit activations, dequantised on the fly
  * ("FlashAttention-Skalierung, Multi-GPU-Training und Gewichtsquantisierung",
  * section 3, "Wie spezielle CUDA-Kernels während der Ausführung dequantisieren

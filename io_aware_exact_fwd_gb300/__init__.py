@@ -10,8 +10,8 @@ still works but every call raises, so a missing build is never silent.
 PyTorch is used only as device-memory and stream plumbing.  With ``stream`` a call
 runs on that stream, and what it allocates comes from that stream's memory, as under
 ``torch.cuda.stream(stream)``.  Most calls marshal with ctypes; those of scored
-attention and of the paged cache, made once a layer and token, with a small compiled
-module (csrc/fa_torch.cpp).
+attention, of the paged caches and of the norm and rotation of queries and keys, made
+once a layer and token, with a small compiled module (csrc/fa_torch.cpp).
 """
 
 from __future__ import annotations
@@ -25,6 +25,8 @@ __all__ = [
     "fa_fp8_workspace_offsets", "fa_fp8_prepare", "fa_fp8_prepare_seeded", "fa_fp8_rotation_signs", "fa_fwd_fp8",
     "fa_mask_plan_size", "fa_mask_plan", "fa_fwd_scored", "fa_bwd_scored_workspace_size", "fa_bwd_scored",
     "fa_paged_append", "fa_paged_decode_workspace_size", "fa_paged_decode",
+    "fa_paged_append_fp8", "fa_paged_decode_fp8", "fa_paged_resize_workspace_size", "fa_paged_resize",
+    "fa_qk_norm_rope", "fa_qk_norm_rope_bwd_workspace_size", "fa_qk_norm_rope_bwd",
     "fa_sync_check",
     "fa_strerror",
     "fa_version", "fa_last_error_site", "fa_debug_set_wait_limit_ns", "fa_debug_set_fault",
@@ -144,6 +146,20 @@ def load_library():
     lib.fa_paged_decode_workspace_size.argtypes = [i] * 4
     lib.fa_paged_decode.restype = i
     lib.fa_paged_decode.argtypes = [vp] * 7 + [i64] + [vp] * 5 + [sz] + [i] * 8 + [f, f, vp, vp]
+    lib.fa_paged_append_fp8.restype = i
+    lib.fa_paged_append_fp8.argtypes = [vp] * 11 + [i64, vp, vp] + [i] * 8 + [vp]
+    lib.fa_paged_decode_fp8.restype = i
+    lib.fa_paged_decode_fp8.argtypes = [vp] * 9 + [i64] + [vp] * 5 + [sz] + [i] * 8 + [f, f, vp, vp]
+    lib.fa_paged_resize_workspace_size.restype = sz
+    lib.fa_paged_resize_workspace_size.argtypes = [i]
+    lib.fa_paged_resize.restype = i
+    lib.fa_paged_resize.argtypes = [vp, i64, vp, vp, vp, i] + [vp] * 7 + [i, vp, sz, i, i, i, vp]
+    lib.fa_qk_norm_rope.restype = i
+    lib.fa_qk_norm_rope.argtypes = [vp] * 12 + [i] * 7 + [f, i, i, i, vp]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 19 + [sz] + [i] * 7 + [f, i, i, i, vp]
     lib.fa_w4a16_workspace_size.restype = ctypes.c_size_t
     lib.fa_w4a16_workspace_size.argtypes = [i, i, i, i]
     lib.fa_w4a16_default_splits.restype = i
@@ -748,6 +764,84 @@ def fa_paged_decode(q, k_cache, v_cache, page_table, seq_lens, o=None, lse=None,
     """
     return _done(load_binding().paged_decode(q, k_cache, v_cache, page_table, seq_lens, o, lse, workspace, scale, softcap, slopes,
                                       None if stream is None else stream.cuda_stream), "fa_paged_decode")
+
+
+def fa_paged_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, cu_new, stream=None):
+    """fa_paged_append into a cache of 8-bit codes with a scale for each block of 16 tokens and head (in place).
+
+    k, v: [T, Hkv, d], bf16 or fp16; k_cache, v_cache: torch.float8_e4m3fn, indexed
+    [n_pages, Hkv, page_size, d], any layout with contiguous d and strides of 16 elements;
+    k_scales, v_scales: fp32 [n_pages, Hkv, page_size // 16].  A block's scale is the least power
+    of two that takes all its tokens to 448 or below; where a later token makes it grow,
+    the codes of those before it are re-coded.  Fresh blocks need no initial values.
+    """
+    _done(load_binding().paged_append_fp8(k, v, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, cu_new,
+                                          None if stream is None else stream.cuda_stream), "fa_paged_append_fp8")
+
+
+def fa_paged_decode_fp8(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, o=None, lse=None, workspace=None,
+                        scale: float | None = None, softcap: float = 0.0, slopes=None, stream=None):
+    """fa_paged_decode over a cache of fa_paged_append_fp8: returns (o [B, H, d], lse fp32 [B, H]).
+
+    q, o: bf16 or fp16.  The workspace is fa_paged_decode's (fa_paged_decode_workspace_size).
+    """
+    return _done(load_binding().paged_decode_fp8(q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, o, lse, workspace,
+                                                 scale, softcap, slopes, None if stream is None else stream.cuda_stream),
+                 "fa_paged_decode_fp8")
+
+
+def fa_paged_resize_workspace_size(B: int) -> int:
+    """Bytes of device workspace fa_paged_resize needs (0 if unsupported)."""
+    return int(load_library().fa_paged_resize_workspace_size(B))
+
+
+def fa_paged_resize(page_table, seq_lens, delta, free_pages, free_count, page_size: int, slots=None, positions=None,
+                    seq_lens_out=None, free_count_out=None, cu_new=None, status=None, workspace=None, stream=None):
+    """Sequences of a paged cache made longer or shorter: returns (seq_lens_out, cu_new, free_count_out, status).
+
+    delta: int32 [B], tokens that each sequence gains, or (negative) loses; page_table:
+    int32 [B, max_pages], in place; free_pages: int32, its first free_count[0] (int32 [1])
+    entries are the free pages, in place.  seq_lens_out and free_count_out may be seq_lens
+    and free_count themselves.  cu_new is what the appends take; slots (int64 [T]) and
+    positions (int32 [T]) get each new token's place in the cache and in its sequence, -1
+    behind the last.  status (int32 [2]): pages that were missing, and sequences that do not
+    fit; if either is not 0, nothing has changed and cu_new is 0.  Nothing is read by the host.
+    """
+    return _done(load_binding().paged_resize(page_table, seq_lens, delta, free_pages, free_count, page_size, slots, positions,
+                                             seq_lens_out, free_count_out, cu_new, status, workspace,
+                                             None if stream is None else stream.cuda_stream), "fa_paged_resize")
+
+
+def fa_qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, q_out=None, k_out=None,
+                    eps: float = 1e-6, norm: bool = True, interleaved: bool = False, stream=None):
+    """Norm of every query and key head and rotation by position, in one pass: returns (q_out, k_out).
+
+    q: bf16 or fp16 [B, H, N, d]; k: [B, Hkv, N, d]; any layout with contiguous d (packed tokens
+    [T, H, d] are x.transpose(0, 1)[None]).  y = x / sqrt(mean(x^2) + eps) * weight (norm=False: y = x);
+    weights: fp32 or q's type [d], or None.  inv_freq (fp32 [rot / 2], None: no rotation): the first rot values of
+    a head are rotated in pairs (i, i + rot / 2), or (2i, 2i + 1) if interleaved, by positions * inv_freq[i];
+    positions: int32 [B, N], None: 0 .. N - 1.  New outputs have heads and tokens in the inputs'
+    order; q_out and k_out may be q and k.
+    """
+    return _done(load_binding().qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, norm, interleaved,
+                                             None if stream is None else stream.cuda_stream), "fa_qk_norm_rope")
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    """Bytes of device workspace fa_qk_norm_rope_bwd needs on the current device (0 if unsupported)."""
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(d))
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_freq=None, positions=None, dq=None, dk=None,
+                        workspace=None, eps: float = 1e-6, norm: bool = True, interleaved: bool = False, stream=None):
+    """Gradients of fa_qk_norm_rope for the same arguments: returns (dq, dk, dq_weight, dk_weight).
+
+    dq_out, dk_out: gradients of its outputs; the weights' gradients are fp32 [d], None without
+    the weight.  The same bits on every run.
+    """
+    return _done(load_binding().qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, dq, dk, workspace,
+                                                 eps, norm, interleaved, None if stream is None else stream.cuda_stream),
+                 "fa_qk_norm_rope_bwd")
 
 
 def fa_w4a16_workspace_size(M: int, N: int, K: int, n_split: int) -> int:

@@ -269,6 +269,8 @@ struct PagedCache {
   int64_t table_stride;
   const int32_t* seq_lens;
   int B, Hkv, d, page_size, n_pages, max_pages;
+  float* k_scales;           // of a cache of e4m3 codes: [n_pages, Hkv, page_size / 16]
+  float* v_scales;
 };
 struct PagedAppendArgs {
   PagedCache c;
@@ -277,6 +279,7 @@ struct PagedAppendArgs {
   Strides sk, sv;            // (head, token)
   const int32_t* cu_new;
   int T;
+  int fp16;                  // of k and v, where the cache holds codes
 };
 struct PagedDecodeArgs {
   PagedCache c;
@@ -295,6 +298,55 @@ struct PagedDecodeArgs {
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream);
 size_t paged_decode_workspace(int B, int H, int Hkv, int d);
+// The same on a cache of e4m3 codes (fa_paged_fp8.cu).
+cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_decode_fp8(const PagedDecodeArgs& a, cudaStream_t stream);
+
+// The sequences' lengths, pages and new tokens (fa_paged_resize.cu).
+struct PagedResizeArgs {
+  int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* delta;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* lens_out;         // may be seq_lens
+  int32_t* count_out;        // may be free_count
+  int32_t* cu_new;
+  int32_t* status;
+  int64_t* slots;            // [T] or NULL
+  int32_t* positions;        // [T] or NULL
+  void* workspace;
+  int B, page_size, max_pages, capacity;
+  int T;
+};
+size_t paged_resize_workspace(int B);
+cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream);
+
+// ------------------------------------------- queries and keys of a layer (fa_qk_norm.cu)
+
+struct QkArgs {
+  const void* q;
+  const void* k;
+  const void* dq_in;         // gradients of the outputs, in the backward
+  const void* dk_in;
+  void* q_out;
+  void* k_out;
+  Strides sq, sk, sdq_in, sdk_in, sq_out, sk_out;
+  const void* q_weight;      // [d] or NULL
+  const void* k_weight;
+  int weight_type;           // 0: fp32, 1: bf16, 2: fp16
+  float* dq_weight;          // [d] or NULL (backward)
+  float* dk_weight;
+  const float* inv_freq;     // [rot / 2] or NULL
+  const int32_t* positions;  // [B, N] or NULL: 0 .. N - 1
+  void* workspace;
+  int B, H, Hkv, N, d, rot, norm, pairs, fp16;
+  float eps;
+};
+cudaError_t launch_qk_norm_rope(const QkArgs& a, cudaStream_t stream);
+size_t qk_norm_rope_bwd_workspace(int d);
+cudaError_t launch_qk_norm_rope_bwd(const QkArgs& a, cudaStream_t stream);
 
 // kern<<<grid, block, smem, stream>>>(args...) that may start before the stream's previous
 // kernel has ended; the kernel waits for it (grid_wait, fa_device.cuh).

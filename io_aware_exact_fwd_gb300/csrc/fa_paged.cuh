@@ -1,0 +1,273 @@
+// Device pieces that the paged cache's kernels share: how the tiles of all sequences are
+// dealt out to the CTAs of a decode, and the join of a head's parts.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "fa_device.cuh"
+#include "fa_internal.h"
+#include "fa_score.cuh"
+
+namespace fa {
+namespace {
+
+__device__ __forceinline__ int tokens_of(const PagedCache& c, int b) {
+  return min(max(c.seq_lens[b], 0), c.max_pages * c.page_size);
+}
+
+constexpr int kConsumers = 4;     // consumer warps
+constexpr int kDecThreads = 32 * (kConsumers + 1);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// The reference of a row before its first token, and where every score so far is -inf (a key with an infinite entry):
+// finite, so that such tokens weigh 0 and a part that holds no others joins with weight 0.
+constexpr float kNoScore = -3.0e38f;
+
+struct DecParams {
+  PagedCache c;
+  const uint16_t* q;
+  uint16_t* o;
+  Strides sq, so;
+  float* lse;
+  float* part;               // [2 CTAs][rows][D + 2]: O, then m and l
+  long long* offsets;        // [B + 1] tiles before each sequence, then the share
+  int H, group, chunks, piece;
+  float scale_log2, cap_in, cap_out;
+  CapPoly poly;              // factor cap_out
+  const float* slopes;
+  unsigned int* err_word;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool FP16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (FP16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (FP16) {
+    const __half2 x = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); }
+__device__ __forceinline__ int tiles_of(const PagedCache& c, int b, int tile) {
+  return (tokens_of(c, b) + tile - 1) / tile;
+}
+
+// A place in the line of tiles: tile t of head unit u (key/value head and chunk) of
+// sequence b, with n tokens in T tiles.
+template <int TILE>
+struct Place {
+  int b, u, t, n, T;
+  __device__ __forceinline__ void sequence(const PagedCache& c) {
+    n = tokens_of(c, b);
+    T = (n + TILE - 1) / TILE;
+  }
+  // To the next head unit (the next sequence with tokens after the last one).
+  __device__ __forceinline__ void next_unit(const PagedCache& c, int units) {
+    t = 0;
+    if (++u < units) return;
+    u = 0;
+    do {
+      ++b;
+      if (b >= c.B) return;
+      sequence(c);
+    } while (T == 0);
+  }
+};
+
+// The CTA's share [w0, w1) of the line of tiles, and the place of its first one; false if
+// it has none.  Every thread of the block calls it, once; s_sums (kDecThreads / 32 words
+// of 8 bytes) and s_start (16 bytes, 8-byte aligned) are scratch until then.
+template <int TILE>
+__device__ __forceinline__ bool share_of_tiles(const DecParams& p, int units, long long* s_sums, int* s_start,
+                                               Place<TILE>& at, long long& w0, long long& w1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Tiles before each sequence: a thread sums a run of sequences, the block scans the sums.
+  const int per = (p.c.B + kDecThreads - 1) / kDecThreads;
+  const int b_lo = min(static_cast<int>(threadIdx.x) * per, p.c.B), b_hi = min(b_lo + per, p.c.B);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(tiles_of(p.c, b, TILE)) * units;
+  long long before = mine;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, w);
+    if (lane >= w) before += x;
+  }
+  if (lane == 31) s_sums[warp] = before;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w <= kConsumers; ++w) {
+    if (w < warp) before += s_sums[w];
+    total += s_sums[w];
+  }
+  before -= mine;
+  const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  const long long share = (total + G - 1) / G;  // down to one tile: a block's tile costs more than its join
+  w0 = cta * share;
+  w1 = min(w0 + share, total);
+  const long long after = before + mine;
+  if (cta == 0) {  // for the join
+    for (int b = b_lo; b < b_hi; ++b) {
+      p.offsets[b] = before;
+      before += static_cast<long long>(tiles_of(p.c, b, TILE)) * units;
+    }
+    if (threadIdx.x == 0) {
+      p.offsets[p.c.B] = total;
+      p.offsets[p.c.B + 1] = share;
+    }
+    before = after - mine;
+  }
+  if (w0 < total && before <= w0 && w0 < after) {  // this thread's run holds the CTA's first tile
+    int b = b_lo;
+    for (;; ++b) {
+      const long long x = static_cast<long long>(tiles_of(p.c, b, TILE)) * units;
+      if (w0 < before + x) break;
+      before += x;
+    }
+    s_start[0] = b;
+    *reinterpret_cast<long long*>(s_start + 2) = w0 - before;
+  }
+  __syncthreads();
+  grid_release();
+  if (w0 >= total) return false;
+  at.b = s_start[0];
+  at.sequence(p.c);
+  {
+    const long long into = *reinterpret_cast<const long long*>(s_start + 2);
+    at.u = static_cast<int>(into / at.T);
+    at.t = static_cast<int>(into % at.T);
+  }
+  return true;
+}
+
+// Joins the parts of heads whose tiles lie in several CTAs' shares, and writes the
+// result of empty sequences.  One block per (sequence, query head): warp x takes parts
+// x, x + 4, ...
+template <int D, bool FP16>
+__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_part) {
+  __shared__ float2 s_ml[4];
+  __shared__ __align__(16) float s_o[4][D];
+  grid_wait();  // the parts are written
+  const int b = blockIdx.x / p.H, head = blockIdx.x % p.H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int E = D / 32;
+  const int hk = head / p.group, in_group = head % p.group;
+  const int u = hk * p.chunks + in_group / rows_per_part, row = in_group % rows_per_part;
+  const long long first = p.offsets[b], tiles = (p.offsets[b + 1] - first) / (p.c.Hkv * p.chunks);
+  const long long share = p.offsets[p.c.B + 1];
+  const long long w0 = first + u * tiles;
+  uint16_t* dst = p.o + b * p.so.s[1] + head * p.so.s[0];
+  float* lse = p.lse + static_cast<size_t>(b) * p.H + head;
+  if (tiles == 0) {
+    if (threadIdx.x < D / 8) *reinterpret_cast<uint4*>(dst + 8 * threadIdx.x) = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) *lse = -INFINITY;
+    return;
+  }
+  const int c0 = static_cast<int>(w0 / share), c1 = static_cast<int>((w0 + tiles - 1) / share);
+  if (c0 == c1) return;  // one CTA had the whole head and wrote it
+  float m = kNoScore, l = 0.f, acc[E] = {};
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    // A CTA's first segment has slot 0; only the first part can be another segment of its CTA.
+    const int slot = 2 * c + (c * share >= w0 ? 0 : 1);
+    const float* part = p.part + static_cast<size_t>(slot) * rows_per_part * (D + 2);
+    const float2 ml = *reinterpret_cast<const float2*>(part + rows_per_part * D + 2 * row);
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = part[row * D + lane + 32 * e];
+    const float mn = fmaxf(m, ml.x), wa = ex2_approx(m - mn), wb = ex2_approx(ml.x - mn);
+    l = l * wa + ml.y * wb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * wa + v[e] * wb;
+    m = mn;
+  }
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float M = kNoScore, L = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) M = fmaxf(M, s_ml[x].x);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float wgt = ex2_approx(s_ml[x].x - M);
+      L += s_ml[x].y * wgt;
+      sum.x = fmaf(s_o[x][2 * threadIdx.x], wgt, sum.x);
+      sum.y = fmaf(s_o[x][2 * threadIdx.x + 1], wgt, sum.y);
+    }
+    reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack2<FP16>(sum.x / L, sum.y / L);
+    if (threadIdx.x == 0) *lse = (M + log2f(L)) * kLn2;
+  }
+}
+
+// Query heads per chunk (16 MT) and the CTAs of the decode.  Up to 16 heads share a key/value head
+// in most models, and two CTAs an SM with 16 rows each keep more loads in flight than one with 32
+// (64 sequences of 4000-8000 tokens, one head of d=128: 40.5 us against 46.5); larger groups read
+// the cache once a chunk, so chunks of 32 pay (32 heads: 49.2 us against 54.0).
+inline int paged_decode_mt(int group) { return group <= 16 ? 1 : 2; }
+inline int paged_decode_ctas(int group) { return sm_count() * (paged_decode_mt(group) == 1 ? 2 : 1); }
+
+inline size_t part_bytes(int group, int d) {
+  return (static_cast<size_t>(2) * paged_decode_ctas(group) * 16 * paged_decode_mt(group) * (d + 2) * sizeof(float) + 255) /
+         256 * 256;
+}
+
+inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile) {
+  DecParams p{};
+  p.c = a.c;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.o = static_cast<uint16_t*>(a.o);
+  p.sq = a.sq;
+  p.so = a.so;
+  p.lse = a.lse;
+  p.H = a.H;
+  p.group = a.H / a.c.Hkv;
+  p.chunks = (p.group + rows - 1) / rows;
+  p.part = static_cast<float*>(a.workspace);
+  p.offsets = reinterpret_cast<long long*>(static_cast<uint8_t*>(a.workspace) + part_bytes(p.group, a.c.d));
+  // The tokens of one page inside a tile: the largest power of two that divides both.
+  p.piece = std::min(tile, a.c.page_size & -a.c.page_size);
+  p.scale_log2 = a.scale * kLog2e;
+  if (a.softcap > 0.f) {
+    p.cap_in = 4.f * a.scale / a.softcap;  // products to x = 4 u (fa_score.cuh)
+    p.cap_out = a.softcap * kLog2e;
+    p.poly = cap_poly(p.cap_out);
+  }
+  p.slopes = a.slopes;
+  p.err_word = a.err_word;
+  p.wait_ns = a.dbg.wait_limit_ns;
+  return p;
+}
+
+}  // namespace
+}  // namespace fa

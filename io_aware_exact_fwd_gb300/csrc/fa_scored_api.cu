@@ -1,4 +1,4 @@
-// C entry points of scored attention and of the paged cache: argument validation and
+// C entry points of scored attention and of the paged caches: argument validation and
 // dispatch to the kernels.  Their contract: include/fa.h.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -287,6 +287,139 @@ int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache
   a.err_word = c.err_word;
   a.dbg = c.dbg;
   return status_of(fa::launch_paged_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The strides and scales of a cache of codes: rows start on 16 bytes, as TMA needs them.
+int codes_of(fa::PagedCache* c, float* k_scales, float* v_scales) {
+  for (int i = 0; i < 3; ++i)
+    if (c->sk.s[i] % 16 != 0 || c->sv.s[i] % 16 != 0) return FA_ERR_MISALIGNED;
+  if (!k_scales || !v_scales) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return FA_ERR_MISALIGNED;
+  c->k_scales = k_scales;
+  c->v_scales = v_scales;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides, void* k_cache,
+                        const int64_t* k_cache_strides, void* v_cache, const int64_t* v_cache_strides, float* k_scales,
+                        float* v_scales, const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                        const int32_t* cu_new, int B, int T, int Hkv, int d, int page_size, int n_pages, int max_pages,
+                        int dtype, fa_stream_t stream) {
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  const int vs = validate_paged(B, Hkv, d, page_size, n_pages, max_pages, table_stride, dtype);
+  if (vs < 0) return FA_OK;
+  if (vs != FA_OK) return vs;
+  if (T == 0) return FA_OK;
+  if (static_cast<long long>(T) * Hkv > kIntMax) return FA_ERR_UNSUPPORTED;
+  if (!k || !v || !cu_new) return FA_ERR_INVALID_ARG;
+  fa::PagedAppendArgs a{};
+  int st = paged_cache(&a.c, k_cache, k_cache_strides, v_cache, v_cache_strides, page_table, table_stride, seq_lens,
+                       B, Hkv, d, page_size, n_pages, max_pages);
+  const fa::Strides dense{{d, static_cast<int64_t>(Hkv) * d, 0}};
+  if (st == FA_OK) st = codes_of(&a.c, k_scales, v_scales);
+  if (st == FA_OK) st = fa::strides_or(&a.sk, k_strides, 2, dense, d);
+  if (st == FA_OK) st = fa::strides_or(&a.sv, v_strides, 2, dense, d);
+  if (st != FA_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4)) return FA_ERR_MISALIGNED;
+  fa::CallContext c;
+  if ((st = fa::call_context(&c)) != FA_OK) return st;
+  a.k = k;
+  a.v = v;
+  a.cu_new = cu_new;
+  a.T = T;
+  a.fp16 = dtype == kFp16;
+  return status_of(fa::launch_paged_append_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int fa_paged_decode_fp8(const void* q, const int64_t* q_strides, const void* k_cache, const int64_t* k_cache_strides,
+                        const void* v_cache, const int64_t* v_cache_strides, const float* k_scales,
+                        const float* v_scales, const int32_t* page_table, int64_t table_stride,
+                        const int32_t* seq_lens, void* o, const int64_t* o_strides, float* lse, void* workspace,
+                        size_t ws_bytes, int B, int H, int Hkv, int d, int page_size, int n_pages, int max_pages,
+                        int dtype, float scale, float softcap, const float* slopes, fa_stream_t stream) {
+  if (H < 0 || bad_score(scale, softcap)) return FA_ERR_INVALID_ARG;
+  const int vs = validate_paged(B, Hkv, d, page_size, n_pages, max_pages, table_stride, dtype);
+  if (vs < 0 || (vs == FA_OK && H == 0)) return FA_OK;
+  if (vs != FA_OK) return vs;
+  if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * H > kIntMax) return FA_ERR_UNSUPPORTED;
+  if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, H, Hkv, d)) return FA_ERR_WORKSPACE;
+  fa::PagedDecodeArgs a{};
+  int st = paged_cache(&a.c, k_cache, k_cache_strides, v_cache, v_cache_strides, page_table, table_stride, seq_lens,
+                       B, Hkv, d, page_size, n_pages, max_pages);
+  const fa::Strides dense{{d, static_cast<int64_t>(H) * d, 0}};
+  if (st == FA_OK) st = codes_of(&a.c, const_cast<float*>(k_scales), const_cast<float*>(v_scales));
+  if (st == FA_OK) st = fa::strides_or(&a.sq, q_strides, 2, dense, d);
+  if (st == FA_OK) st = fa::strides_or(&a.so, o_strides, 2, dense, d);
+  if (st != FA_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(slopes, 4))
+    return FA_ERR_MISALIGNED;
+  fa::CallContext c;
+  if ((st = fa::call_context(&c)) != FA_OK) return st;
+  a.q = q;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.H = H;
+  a.fp16 = dtype == kFp16;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.slopes = slopes;
+  a.err_word = c.err_word;
+  a.dbg = c.dbg;
+  return status_of(fa::launch_paged_decode_fp8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_paged_resize_workspace_size(int B) { return B < 0 || B > 65535 ? 0 : fa::paged_resize_workspace(B); }
+
+int fa_paged_resize(int32_t* page_table, int64_t table_stride, const int32_t* seq_lens, const int32_t* delta,
+                    int32_t* free_pages, int capacity, const int32_t* free_count, int32_t* seq_lens_out,
+                    int32_t* free_count_out, int32_t* cu_new, int32_t* status, int64_t* slots, int32_t* positions, int T,
+                    void* workspace, size_t ws_bytes, int B, int page_size, int max_pages, fa_stream_t stream) {
+  if (B < 0 || T < 0 || capacity < 0 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 1024 || page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || static_cast<long long>(max_pages) * page_size > kIntMax / 2) return FA_ERR_UNSUPPORTED;
+  if (!free_count || !free_count_out || !cu_new || !status || (capacity > 0 && !free_pages)) return FA_ERR_INVALID_ARG;
+  if (B > 0 && (!page_table || !seq_lens || !delta || !seq_lens_out || max_pages == 0 || table_stride < max_pages))
+    return FA_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < fa::paged_resize_workspace(B)) return FA_ERR_WORKSPACE;
+  const void* words[] = {page_table, seq_lens, delta,  free_pages, free_count, seq_lens_out,
+                         free_count_out, cu_new, status, positions, workspace};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  if (!aligned(slots, 8)) return FA_ERR_MISALIGNED;
+  fa::CallContext c;
+  const int st = fa::call_context(&c);
+  if (st != FA_OK) return st;
+  fa::PagedResizeArgs a{};
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.seq_lens = seq_lens;
+  a.delta = delta;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.lens_out = seq_lens_out;
+  a.count_out = free_count_out;
+  a.cu_new = cu_new;
+  a.status = status;
+  a.slots = slots;
+  a.positions = positions;
+  a.workspace = workspace;
+  a.B = B;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.capacity = capacity;
+  a.T = slots || positions ? T : 0;
+  return status_of(fa::launch_paged_resize(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

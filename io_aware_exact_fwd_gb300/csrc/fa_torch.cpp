@@ -1,5 +1,5 @@
-// Binding of scored attention and of the paged cache to PyTorch tensors, for calls made
-// once a layer and token: checks, output allocation and the C call in one step.  In
+// Binding of scored attention, of the paged caches and of the norm and rotation of queries
+// and keys to PyTorch tensors, for calls made once a layer and token: checks, output allocation and the C call in one step.  In
 // Python with ctypes the same work takes 20 us a call on the GB300's host (a decode step
 // 27 us where its kernels take 12), here about 1.
 //
@@ -163,7 +163,7 @@ PyObject* tuple_of(std::initializer_list<Tensor> ts) {
   if (!out) throw python_error();
   Py_ssize_t i = 0;
   for (const Tensor& t : ts) {
-    PyObject* x = THPVariable_Wrap(t);
+    PyObject* x = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
     if (!x) {
       Py_DECREF(out);
       throw python_error();
@@ -269,7 +269,7 @@ PyObject* bwd_scored(PyObject* const* a) {
   return st ? PyLong_FromLong(st) : tuple_of({dq, dk, dv});
 }
 
-// What the two calls on a paged cache share.
+// What the calls on a paged cache share.
 struct Cache {
   at::ScalarType type;
   int code, gpu;
@@ -278,12 +278,12 @@ struct Cache {
   int64_t table_stride, B;
   int hkv, d, page, pages, width;
 };
-Cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
+Cache cache_of(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo, bool codes = false) {
   const Tensor &k = tensor(ko, "k_cache"), &v = tensor(vo, "v_cache"), &t = tensor(to, "page_table");
   Cache c;
   c.type = k.scalar_type();
-  if (c.type != at::kBFloat16 && c.type != at::kHalf)
-    unfit(PyExc_TypeError, c10::str("k_cache must be BFloat16 or Half, got ", c.type));
+  if (codes ? c.type != at::kFloat8_e4m3fn : c.type != at::kBFloat16 && c.type != at::kHalf)
+    unfit(PyExc_TypeError, c10::str("k_cache must be ", codes ? "Float8_e4m3fn" : "BFloat16 or Half", ", got ", c.type));
   c.code = c.type == at::kBFloat16 ? 1 : 2;
   c.gpu = gpu_of(k, "k_cache");
   sizes4(k, "k_cache");
@@ -356,6 +356,243 @@ PyObject* paged_decode(PyObject* const* a) {
   return st ? PyLong_FromLong(st) : tuple_of({o, lse});
 }
 
+// What the two calls on a cache of codes share with the 16-bit one's, and its scales.
+struct Cache8 {
+  Cache c;
+  at::ScalarType type;  // of the 16-bit tensors
+  float *k_scales, *v_scales;
+};
+Cache8 cache8_of(const Tensor& x, const char* name, PyObject* ko, PyObject* vo, PyObject* ks, PyObject* vs, PyObject* to,
+                 PyObject* lo) {
+  Cache8 r;
+  r.type = x.scalar_type();
+  if (r.type != at::kBFloat16 && r.type != at::kHalf)
+    unfit(PyExc_TypeError, c10::str(name, " must be BFloat16 or Half, got ", r.type));
+  r.c = cache_of(ko, vo, to, lo, true);
+  r.c.code = r.type == at::kBFloat16 ? 1 : 2;
+  const std::array<int64_t, 3> shape{r.c.pages, r.c.hkv, r.c.page / 16};
+  if (ks == Py_None || vs == Py_None) unfit(PyExc_TypeError, "k_scales and v_scales must be torch.Tensors");
+  r.k_scales = flat<float>(ks, "k_scales", at::kFloat, shape, r.c.gpu);
+  r.v_scales = flat<float>(vs, "v_scales", at::kFloat, shape, r.c.gpu);
+  return r;
+}
+
+// k, v, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, cu_new, stream
+PyObject* paged_append_fp8(PyObject* const* a) {
+  const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  const Cache8 x = cache8_of(k, "k", a[2], a[3], a[4], a[5], a[6], a[7]);
+  const Cache& c = x.c;
+  if (k.dim() != 3) unfit(PyExc_ValueError, "k must be [T, Hkv, d]");
+  const int64_t T = k.size(0);
+  const Layout lk = layout(k, "k", x.type, {T, c.hkv, c.d}, c.gpu), lv = layout(v, "v", x.type, {T, c.hkv, c.d}, c.gpu);
+  if (a[8] == Py_None) unfit(PyExc_TypeError, "cu_new must be a torch.Tensor");
+  const int32_t* cu = flat<const int32_t>(a[8], "cu_new", at::kInt, {c.B + 1}, c.gpu);
+  const int b = whole(c.B, "B"), t = whole(T, "T");
+  const CallStream s(a[9], c.gpu);
+  const int st = call(c.gpu, [&] {
+    return fa_paged_append_fp8(lk.p, lk.strides(), lv.p, lv.strides(), c.k.p, c.k.strides(), c.v.p, c.v.strides(),
+                               x.k_scales, x.v_scales, c.table, c.table_stride, c.lens, cu, b, t, c.hkv, c.d, c.page,
+                               c.pages, c.width, c.code, s);
+  });
+  if (st) return PyLong_FromLong(st);
+  Py_RETURN_NONE;
+}
+
+// q, k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, o, lse, workspace, scale, softcap, slopes, stream
+PyObject* paged_decode_fp8(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  const Cache8 x = cache8_of(q, "q", a[1], a[2], a[3], a[4], a[5], a[6]);
+  const Cache& c = x.c;
+  if (q.dim() != 3) unfit(PyExc_ValueError, "q must be [B, H, d]");
+  const int64_t H = q.size(1);
+  const Layout lq = layout(q, "q", x.type, {c.B, H, c.d}, c.gpu);
+  const CallStream s(a[13], c.gpu);
+  const Tensor o = given_or_new(a[7], "o", {c.B, H, c.d}, q, x.type);
+  const Tensor lse = given_or_new(a[8], "lse", {c.B, H}, q, at::kFloat);
+  const Layout lo = layout(o, "o", x.type, {c.B, H, c.d}, c.gpu);
+  check(lse, "lse", at::kFloat, {c.B, H}, c.gpu);
+  if (!lse.is_contiguous()) unfit(PyExc_ValueError, "lse must be contiguous");
+  const int b = whole(c.B, "B"), h = whole(H, "H");
+  Tensor own;
+  Bytes ws = bytes(a[9], "workspace", c.gpu);
+  if (a[9] == Py_None) {
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.gpu));
+    ws.n = fa_paged_decode_workspace_size(b, h, c.hkv, c.d);
+    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, q);
+    ws.p = own.data_ptr();
+  }
+  const float* slopes = flat<const float>(a[12], "slopes", at::kFloat, {H}, c.gpu);
+  const float scale = scale_of(a[10], c.d), cap = number(a[11]);
+  const int st = call(c.gpu, [&] {
+    return fa_paged_decode_fp8(lq.p, lq.strides(), c.k.p, c.k.strides(), c.v.p, c.v.strides(), x.k_scales, x.v_scales,
+                               c.table, c.table_stride, c.lens, lo.p, lo.strides(), static_cast<float*>(lse.data_ptr()),
+                               ws.p, ws.n, b, h, c.hkv, c.d, c.page, c.pages, c.width, c.code, scale, cap, slopes, s);
+  });
+  return st ? PyLong_FromLong(st) : tuple_of({o, lse});
+}
+
+// page_table, seq_lens, delta, free_pages, free_count, page_size, slots, positions, seq_lens_out, free_count_out, cu_new,
+// status, workspace, stream
+PyObject* paged_resize(PyObject* const* a) {
+  const Tensor& t = tensor(a[0], "page_table");
+  const int gpu = gpu_of(t, "page_table");
+  if (t.dim() != 2) unfit(PyExc_ValueError, "page_table must be [B, max_pages]");
+  const int64_t B = t.size(0), width = t.size(1);
+  check(t, "page_table", at::kInt, t.sizes(), gpu);
+  if (width > 1 && t.stride(1) != 1) unfit(PyExc_ValueError, "page_table must have contiguous rows");
+  const int64_t stride = B > 1 ? t.stride(0) : std::max<int64_t>(width, t.stride(0));
+  const char* needed[] = {"seq_lens", "delta", "free_pages", "free_count"};
+  for (int i = 0; i < 4; ++i) tensor(a[1 + i], needed[i]);
+  const int32_t* lens = flat<const int32_t>(a[1], "seq_lens", at::kInt, {B}, gpu);
+  const int32_t* delta = flat<const int32_t>(a[2], "delta", at::kInt, {B}, gpu);
+  const Tensor& list = tensor(a[3], "free_pages");
+  int32_t* pages = flat<int32_t>(a[3], "free_pages", at::kInt, {list.numel()}, gpu);
+  const int32_t* count = flat<const int32_t>(a[4], "free_count", at::kInt, {1}, gpu);
+  const int64_t page = PyLong_AsLongLong(a[5]);
+  if (PyErr_Occurred()) throw python_error();
+  int64_t T = 0;
+  if (a[6] != Py_None) T = tensor(a[6], "slots").numel();
+  else if (a[7] != Py_None) T = tensor(a[7], "positions").numel();
+  int64_t* slots = flat<int64_t>(a[6], "slots", at::kLong, {T}, gpu);
+  int32_t* positions = flat<int32_t>(a[7], "positions", at::kInt, {T}, gpu);
+  const CallStream s(a[13], gpu);
+  auto out = [&](PyObject* x, const char* name, int64_t n) {
+    const Tensor r = given_or_new(x, name, {n}, t, at::kInt);
+    check(r, name, at::kInt, {n}, gpu);
+    if (!r.is_contiguous()) unfit(PyExc_ValueError, c10::str(name, " must be contiguous"));
+    return r;
+  };
+  const Tensor lens_out = out(a[8], "seq_lens_out", B), count_out = out(a[9], "free_count_out", 1),
+               cu = out(a[10], "cu_new", B + 1), status = out(a[11], "status", 2);
+  const int b = whole(B, "B"), w = whole(width, "max_pages"), n = whole(T, "T"), cap = whole(list.numel(), "free_pages"),
+            ps = whole(page, "page_size");
+  Tensor own;
+  Bytes ws = bytes(a[12], "workspace", gpu);
+  if (a[12] == Py_None) {
+    ws.n = fa_paged_resize_workspace_size(b);
+    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, t);
+    ws.p = own.data_ptr();
+  }
+  const int st = call(gpu, [&] {
+    auto ints = [](const Tensor& x) { return static_cast<int32_t*>(x.data_ptr()); };
+    return fa_paged_resize(static_cast<int32_t*>(t.data_ptr()), stride, lens, delta, pages, cap, count, ints(lens_out),
+                           ints(count_out), ints(cu), ints(status), slots, positions, n, ws.p, ws.n, b, ps, w, s);
+  });
+  return st ? PyLong_FromLong(st) : tuple_of({lens_out, cu, count_out, status});
+}
+
+// A new tensor of x's shape and type; heads beside each other in a token where x has them so.
+Tensor fresh_like(const Tensor& x) {
+  const int64_t B = x.size(0), H = x.size(1), N = x.size(2), d = x.size(3);
+  if (H > 1 && N > 1 ? x.stride(1) < x.stride(2) : N > 1 && x.stride(2) > d)
+    return fresh({B, N, H, d}, x.scalar_type(), x).transpose(1, 2);
+  return fresh({B, H, N, d}, x.scalar_type(), x);
+}
+
+// What the norm and rotation and its gradient share: q, k (tensors that give the sizes), the weights, frequencies and positions.
+struct Qk {
+  at::ScalarType type;
+  int code, gpu, weight_code, b, h, hkv, n, d, rot, norm, pairs;
+  int64_t B, H, Hkv, N, D;
+  const void *qw, *kw;
+  const float* freq;
+  const int32_t* pos;
+  float eps;
+};
+Qk qk_of(const Tensor& q, const char* qname, const Tensor& k, const char* kname, PyObject* qw, PyObject* kw, PyObject* freq,
+         PyObject* pos, PyObject* eps, PyObject* norm, PyObject* pairs) {
+  Qk x;
+  sizes4(q, qname);
+  sizes4(k, kname);
+  x.type = q.scalar_type();
+  if (x.type != at::kBFloat16 && x.type != at::kHalf)
+    unfit(PyExc_TypeError, c10::str(qname, " must be BFloat16 or Half, got ", x.type));
+  x.code = x.type == at::kBFloat16 ? 1 : 2;
+  x.gpu = gpu_of(q, qname);
+  x.B = q.size(0);
+  x.H = q.size(1);
+  x.N = q.size(2);
+  x.D = q.size(3);
+  x.Hkv = k.size(1);
+  x.weight_code = 0;
+  auto weight = [&](PyObject* w, const char* name) -> const void* {
+    if (w == Py_None) return nullptr;
+    const Tensor& t = tensor(w, name);
+    const at::ScalarType type = t.scalar_type();
+    if (type != at::kFloat && type != x.type)
+      unfit(PyExc_ValueError, c10::str(name, " must be Float or ", x.type, ", got ", type));
+    x.weight_code = type == at::kFloat ? 0 : x.code;
+    return flat<void>(w, name, type, {x.D}, x.gpu);
+  };
+  x.qw = weight(qw, "q_weight");
+  const int first = x.weight_code;
+  x.kw = weight(kw, "k_weight");
+  if (x.qw && x.kw && first != x.weight_code) unfit(PyExc_ValueError, "q_weight and k_weight must have the same dtype");
+  if (x.qw && !x.kw) x.weight_code = first;
+  const int64_t half = freq == Py_None ? 0 : tensor(freq, "inv_freq").numel();
+  x.freq = half ? flat<const float>(freq, "inv_freq", at::kFloat, {half}, x.gpu) : nullptr;
+  x.pos = flat<const int32_t>(pos, "positions", at::kInt, {x.B, x.N}, x.gpu);
+  x.eps = number(eps);
+  x.norm = truth(norm);
+  x.pairs = truth(pairs);
+  x.b = whole(x.B, "B");
+  x.h = whole(x.H, "H");
+  x.hkv = whole(x.Hkv, "Hkv");
+  x.n = whole(x.N, "N");
+  x.d = whole(x.D, "d");
+  x.rot = whole(2 * half, "inv_freq");
+  return x;
+}
+
+// q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out, eps, norm, interleaved, stream
+PyObject* qk_norm_rope(PyObject* const* a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+  const Qk x = qk_of(q, "q", k, "k", a[2], a[3], a[4], a[5], a[8], a[9], a[10]);
+  const std::array<int64_t, 4> qs{x.B, x.H, x.N, x.D}, ks{x.B, x.Hkv, x.N, x.D};
+  const Layout lq = layout(q, "q", x.type, qs, x.gpu), lk = layout(k, "k", x.type, ks, x.gpu);
+  const CallStream s(a[11], x.gpu);
+  const Tensor qo = a[6] != Py_None ? tensor(a[6], "q_out") : fresh_like(q),
+               ko = a[7] != Py_None ? tensor(a[7], "k_out") : fresh_like(k);
+  const Layout lqo = layout(qo, "q_out", x.type, qs, x.gpu), lko = layout(ko, "k_out", x.type, ks, x.gpu);
+  const int st = call(x.gpu, [&] {
+    return fa_qk_norm_rope(lq.p, lq.strides(), lk.p, lk.strides(), x.qw, x.kw, x.freq, x.pos, lqo.p, lqo.strides(), lko.p,
+                           lko.strides(), x.b, x.h, x.hkv, x.n, x.d, x.rot, x.norm, x.eps, x.weight_code, x.pairs, x.code, s);
+  });
+  return st ? PyLong_FromLong(st) : tuple_of({qo, ko});
+}
+
+// q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, dq, dk, workspace, eps, norm, interleaved, stream
+PyObject* qk_norm_rope_bwd(PyObject* const* a) {
+  const Tensor &gq = tensor(a[2], "dq_out"), &gk = tensor(a[3], "dk_out");
+  const Qk x = qk_of(gq, "dq_out", gk, "dk_out", a[4], a[5], a[6], a[7], a[11], a[12], a[13]);
+  const std::array<int64_t, 4> qs{x.B, x.H, x.N, x.D}, ks{x.B, x.Hkv, x.N, x.D};
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+  const Layout lq = layout(q, "q", x.type, qs, x.gpu), lk = layout(k, "k", x.type, ks, x.gpu),
+               lgq = layout(gq, "dq_out", x.type, qs, x.gpu), lgk = layout(gk, "dk_out", x.type, ks, x.gpu);
+  const CallStream s(a[14], x.gpu);
+  const Tensor dq = a[8] != Py_None ? tensor(a[8], "dq") : fresh_like(gq),
+               dk = a[9] != Py_None ? tensor(a[9], "dk") : fresh_like(gk);
+  const Layout ldq = layout(dq, "dq", x.type, qs, x.gpu), ldk = layout(dk, "dk", x.type, ks, x.gpu);
+  Tensor dqw, dkw, own;
+  if (x.qw) dqw = fresh({x.D}, at::kFloat, gq);
+  if (x.kw) dkw = fresh({x.D}, at::kFloat, gq);
+  Bytes ws = bytes(a[10], "workspace", x.gpu);
+  if (a[10] == Py_None && (x.qw || x.kw)) {
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.gpu));
+    ws.n = fa_qk_norm_rope_bwd_workspace_size(x.d);
+    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, gq);
+    ws.p = own.data_ptr();
+  }
+  const int st = call(x.gpu, [&] {
+    return fa_qk_norm_rope_bwd(lq.p, lq.strides(), lk.p, lk.strides(), lgq.p, lgq.strides(), lgk.p, lgk.strides(), x.qw,
+                               x.kw, x.freq, x.pos, ldq.p, ldq.strides(), ldk.p, ldk.strides(),
+                               x.qw ? static_cast<float*>(dqw.data_ptr()) : nullptr,
+                               x.kw ? static_cast<float*>(dkw.data_ptr()) : nullptr, ws.p, ws.n, x.b, x.h, x.hkv, x.n, x.d,
+                               x.rot, x.norm, x.eps, x.weight_code, x.pairs, x.code, s);
+  });
+  return st ? PyLong_FromLong(st) : tuple_of({dq, dk, dqw, dkw});
+}
+
 // No C++ exception leaves a function: its own become the Python exceptions they name,
 // PyTorch's (an allocation that fails) those of PyTorch.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -381,7 +618,11 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<mask_plan, 7>("mask_plan"),       method<fwd_scored, 11>("fwd_scored"),
                            method<bwd_scored, 17>("bwd_scored"),    method<paged_append, 8>("paged_append"),
-                           method<paged_decode, 12>("paged_decode"), {nullptr, nullptr, 0, nullptr}};
+                           method<paged_decode, 12>("paged_decode"),
+                           method<paged_append_fp8, 10>("paged_append_fp8"),
+                           method<paged_decode_fp8, 14>("paged_decode_fp8"), method<paged_resize, 14>("paged_resize"),
+                           method<qk_norm_rope, 12>("qk_norm_rope"), method<qk_norm_rope_bwd, 15>("qk_norm_rope_bwd"),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

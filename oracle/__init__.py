@@ -36,6 +36,10 @@ check it against the pages by eye:
   gradient, and its decode over a paged cache.  The pages name none of these; the
   definition is the dense one, pair by pair.
 
+* ``serving``    -- norm and rotation of queries and keys with its gradient, and the paged
+  cache in 8-bit codes (appending, decode, the bookkeeping of its pages), each from its
+  plain definition.  The pages name none of these either.
+
 Only ``tests/``, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 ``--impl reference`` legs of ``bench.py`` may import this package.  The product
 path (``io_aware_exact_fwd_gb300``) never imports it, and this package imports
@@ -81,6 +85,14 @@ from .fp8_backward import (
     fp8_backward_from_operands,
     fp8_backward,
 )
+from .serving import (
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    paged_append_fp8,
+    paged_values,
+    paged_decode_fp8,
+    paged_resize,
+)
 from .scored import visible, scored_forward, scored_backward, paged_gather, paged_decode, paged_append
 
 __all__ = [
@@ -122,4 +134,10 @@ __all__ = [
     "paged_gather",
     "paged_decode",
     "paged_append",
+    "qk_norm_rope",
+    "qk_norm_rope_backward",
+    "paged_append_fp8",
+    "paged_values",
+    "paged_decode_fp8",
+    "paged_resize",
 ]
