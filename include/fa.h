@@ -639,9 +639,9 @@ FA_API int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const vo
 /*
  * fa_paged_decode_fp8 -- fa_paged_decode over such a cache; the workspace is fa_paged_decode's.
  * Any positive finite scales.  The products take q as fp16 times a power of two of its row: entries
- * keep all their bits down to 2^-29 of the row's largest and are off by at most 2^-40 of that below.
- * Weights times V scales keep theirs down to 2^-29 of the largest such product of the sequence and are
- * lost below 2^-40.  Sums, maxima and scores are fp32.  The same bits on every run.
+ * keep all their bits down to 2^-28 of the row's largest and are off by at most 2^-39 of that below.
+ * Weights times V scales, rounded to fp16, keep theirs down to 2^-21 of the largest such product of the
+ * sequence and are lost below 2^-32.  Sums, maxima and scores are fp32.  The same bits on every run.
  */
 FA_API int fa_paged_decode_fp8(const void* q, const int64_t* q_strides, const void* k_cache,
                                const int64_t* k_cache_strides, const void* v_cache, const int64_t* v_cache_strides,

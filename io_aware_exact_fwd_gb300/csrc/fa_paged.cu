@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   Place<kTile> at;
   long long w0, w1;
   const int cta = static_cast<int>(blockIdx.x);
-  if (!share_of_tiles(p, units, s_sums, s_start, at, w0, w1)) return;
+  if (!share_of_tiles<kConsumers + 1>(p, units, s_sums, s_start, at, w0, w1)) return;
   const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
 
   if (warp == kConsumers) {
@@ -549,8 +549,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-size_t paged_decode_workspace(int B, int H, int Hkv, int d) {
-  return part_bytes(H / Hkv, d) + (static_cast<size_t>(B) + 2) * sizeof(long long);
+size_t paged_decode_workspace(int B, int d) {
+  return part_bytes(d) + (static_cast<size_t>(B) + 2) * sizeof(long long);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream) {

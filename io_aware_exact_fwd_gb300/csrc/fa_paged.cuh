@@ -103,14 +103,14 @@ struct Place {
 };
 
 // The CTA's share [w0, w1) of the line of tiles, and the place of its first one; false if
-// it has none.  Every thread of the block calls it, once; s_sums (kDecThreads / 32 words
+// it has none.  Every thread of the block, of WARPS warps, calls it, once; s_sums (WARPS words
 // of 8 bytes) and s_start (16 bytes, 8-byte aligned) are scratch until then.
-template <int TILE>
+template <int WARPS, int TILE>
 __device__ __forceinline__ bool share_of_tiles(const DecParams& p, int units, long long* s_sums, int* s_start,
                                                Place<TILE>& at, long long& w0, long long& w1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tiles before each sequence: a thread sums a run of sequences, the block scans the sums.
-  const int per = (p.c.B + kDecThreads - 1) / kDecThreads;
+  const int per = (p.c.B + 32 * WARPS - 1) / (32 * WARPS);
   const int b_lo = min(static_cast<int>(threadIdx.x) * per, p.c.B), b_hi = min(b_lo + per, p.c.B);
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) mine += static_cast<long long>(tiles_of(p.c, b, TILE)) * units;
@@ -124,7 +124,7 @@ __device__ __forceinline__ bool share_of_tiles(const DecParams& p, int units, lo
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w <= kConsumers; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_sums[w];
     total += s_sums[w];
   }
@@ -230,16 +230,16 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   }
 }
 
-// Query heads per chunk (16 MT) and the CTAs of the decode.  Up to 16 heads share a key/value head
+// Query heads per chunk (16 MT) and the CTAs of the 16-bit decode.  Up to 16 heads share a key/value head
 // in most models, and two CTAs an SM with 16 rows each keep more loads in flight than one with 32
 // (64 sequences of 4000-8000 tokens, one head of d=128: 40.5 us against 46.5); larger groups read
 // the cache once a chunk, so chunks of 32 pay (32 heads: 49.2 us against 54.0).
 inline int paged_decode_mt(int group) { return group <= 16 ? 1 : 2; }
 inline int paged_decode_ctas(int group) { return sm_count() * (paged_decode_mt(group) == 1 ? 2 : 1); }
 
-inline size_t part_bytes(int group, int d) {
-  return (static_cast<size_t>(2) * paged_decode_ctas(group) * 16 * paged_decode_mt(group) * (d + 2) * sizeof(float) + 255) /
-         256 * 256;
+// The parts of both decodes: two a CTA, of at most 32 (16-bit) or 48 rows an SM.
+inline size_t part_bytes(int d) {
+  return (static_cast<size_t>(2) * 48 * sm_count() * (d + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
 inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile) {
@@ -254,7 +254,7 @@ inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile) {
   p.group = a.H / a.c.Hkv;
   p.chunks = (p.group + rows - 1) / rows;
   p.part = static_cast<float*>(a.workspace);
-  p.offsets = reinterpret_cast<long long*>(static_cast<uint8_t*>(a.workspace) + part_bytes(p.group, a.c.d));
+  p.offsets = reinterpret_cast<long long*>(static_cast<uint8_t*>(a.workspace) + part_bytes(a.c.d));
   // The tokens of one page inside a tile: the largest power of two that divides both.
   p.piece = std::min(tile, a.c.page_size & -a.c.page_size);
   p.scale_log2 = a.scale * kLog2e;

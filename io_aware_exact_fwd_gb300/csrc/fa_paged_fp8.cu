@@ -162,43 +162,74 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const __grid_constant__
 // Decode: as the 16-bit cache's (fa_paged.cu has the division of the work, the ring and the join), with half the
 // bytes to read a token and so half the time for the arithmetic on it.
 //
-// Products are m16n8k16 instructions in fp16 with the codes widened to fp16 (exact, one instruction for two): q, whatever
-// its type, comes in as fp16 times a power of two of its head, with its largest entry in [2^14, 2^15), so that entries
-// down to 2^-29 of the largest keep all their bits.  K's scale multiplies the finished scores of its block.  V's cannot
-// follow its products, which sum over blocks: it goes into the weights.  A row therefore has two running references: m
+// Products are m16n8k16 instructions in fp16 with the codes widened to fp16 (exact, one instruction for two).  The 16 rows
+// are K's tokens and V's columns, the 8 columns the heads, S^T = K Q^T and O^T += V^T P^T: with heads as rows, as in the
+// 16-bit decode, half of a product and of the softmax is for rows of zeros where up to 8 heads share a key/value head, and the tensor
+// instructions (11 cycles each and scheduler) would take half the time that HBM leaves.  (The 8-bit m16n8k32 form is no way
+// round the widening: it takes 29 cycles here, conversions and two fp16 products.)
+//
+// q, whatever its type, comes in as fp16 times a power of two of its head, with its largest entry in [2^14, 2^15), so that
+// entries down to 2^-28 of the largest keep all their bits.  K's scale multiplies the finished scores of its block.  V's
+// cannot follow its products, which sum over blocks: it goes into the weights.  A head therefore has two running references: m
 // for its scores, under which l sums the weights, and mv for scores + log2 of the block's V scale, under which the
-// weights are rounded to fp16 for P V.  mv stands 15 below its maximum, so weights times scales keep all their bits down to
-// 2^-29 of the largest and none above 2^-40 is lost.  O goes back to the reference m where a segment ends.
+// weights are rounded to fp16 for P V.  Both are only raised when they have to be: a tile's weights are made under the old
+// ones and kept if those for P V sum up to 2^15 at most and those for l to 2^60; else the maxima are found (shuffles over 8 lanes) and
+// mv set 7 below its own.  So weights times scales keep all their bits down to 2^-21 of the largest, and none above 2^-32 is
+// lost.  O goes back to the reference m where a segment ends.
 //
 // Fragments.  An 8 x 8 matrix of 16-bit units that ldmatrix loads is one of 8 tokens x 16 codes.  For K a thread gets four
 // neighbouring codes of a token, columns 4t .. 4t + 3 of 16: the products take them as their columns {2t, 2t + 1} and
 // {2t + 8, 2t + 9}, and Q's fragments are put in the same order.  For V, transposed, it gets two codes of two tokens: a
-// byte shuffle makes pairs of tokens, for the even columns of 16 and for the odd ones, whose products are kept apart
-// until O is written.
+// byte shuffle makes pairs of tokens, of the even column 2g (row g of the product) and the odd one (row g + 8).  The weights
+// come out with a token's heads side by side and go in with a head's tokens side by side: movmatrix transposes them.
+//
+// Warps.  A warp's tile of work is 32 tokens for 8 or 16 query heads.  Up to 16 heads share a key/value head in most models:
+// CTAs of four such warps and a producer, two or three an SM.  More heads go to two or three groups of four warps of one
+// CTA, which work on the same stages: the cache is read once.
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
-template <int D, int MT>
+template <int D, int W, int NH>  // W groups of four consumer warps, each for 8 NH heads
 struct Dec8Cfg {
-  static constexpr int kRows = 16 * MT;                      // query heads per chunk
+  static constexpr int kWarps = 4 * W + 1;
+  static constexpr int kHeads = 8 * NH;                      // of a group
+  static constexpr int kRows = kHeads * W;                   // query heads per chunk
   static constexpr int kTile = 128;                          // tokens per tile
   static constexpr int kBlocksOfTile = kTile / 16;
-  static constexpr int kBlocks = kBlocksOfTile / kConsumers; // of a warp
   static constexpr int kHalf = kTile * D;                    // K or V of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = (MT == 1 ? 98304 : 196608) / kStage;  // two CTAs per SM, or one
+  static constexpr int kPerSm = W > 1 ? 1 : NH * D <= 128 ? 3 : 2;
+  static constexpr int kStages = (kPerSm == 3 ? 65536 : 98304) / kStage;
+  static constexpr int kORow = D + (NH == 1 ? 8 : 0);        // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
+  static constexpr int kO = 4 * kHeads * kORow * 4;          // a group's O: in the segment's last stage, or with several groups its own
   static constexpr int kQStride = D * 2 + 32;                // bytes; 8-byte loads of 4 rows meet every bank once
-  static constexpr int kScaleOff = kStages * kStage;         // K's and V's scales of each stage
+  static constexpr int kOOff = kStages * kStage;
+  static constexpr int kScaleOff = kOOff + (W == 1 ? 0 : W * kO);  // K's and V's scales of each stage
   static constexpr int kQOff = kScaleOff + kStages * 2 * kBlocksOfTile * 4;
   static constexpr int kQsOff = kQOff + kRows * kQStride;    // q's powers of two
-  static constexpr int kMlOff = kQsOff + kRows * 4;          // (m, l) of each warp's rows
-  static constexpr int kBarOff = kMlOff + kConsumers * kRows * 8;
+  static constexpr int kMlOff = kQsOff + kRows * 4;          // (m, l) of each warp's heads
+  static constexpr int kBarOff = kMlOff + 4 * kRows * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
-  static constexpr float kHeadroom = 15.f;
   static constexpr int kScaleLanes = 2 * kBlocksOfTile;
-  static_assert(kConsumers * 16 * D * 4 <= kStage, "the warps' O of 16 heads fit a stage");
+  static_assert(kO <= kStage, "the warps' O fits a stage");
   static_assert(kQOff % 16 == 0 && kQsOff % 16 == 0 && kMlOff % 8 == 0 && kBarOff % 8 == 0 && kScaleLanes <= 32, "layout");
 };
+
+// mma16816 in fp16 of registers alone: the compiler may move it.
+__device__ __forceinline__ void mma_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit numbers, two neighbours of row lane / 4 a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
+__device__ __forceinline__ float2 max_pair(float2 x, float2 y) { return make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y)); }
+__device__ __forceinline__ float2 minus(float2 x, float2 y) { return __fadd2_rn(x, make_float2(-y.x, -y.y)); }
 
 // Where the 16-byte piece `chunk` of a row of D codes stands in a tile that TMA swizzled in spans of min(D, 128) bytes.
 template <int D>
@@ -207,12 +238,12 @@ __device__ __forceinline__ uint32_t piece_of(int row, int chunk) {
   else return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D, int MT, bool FP16>
-__global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
+template <int D, int W, int NH, bool FP16>
+__global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, NH>::kPerSm)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ DecParams p) {
-  using C = Dec8Cfg<D, MT>;
-  constexpr int kTile = C::kTile, NB = C::kBlocks;
+  using C = Dec8Cfg<D, W, NH>;
+  constexpr int kTile = C::kTile, kHeads = C::kHeads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -226,7 +257,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar_full[s], 1 + C::kScaleLanes);
-      mbar_init(&bar_empty[s], kConsumers);
+      mbar_init(&bar_empty[s], 4 * W);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -236,10 +267,10 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   Place<kTile> at;
   long long w0, w1;
   const int cta = static_cast<int>(blockIdx.x);
-  if (!share_of_tiles(p, units, s_sums, s_start, at, w0, w1)) return;
+  if (!share_of_tiles<C::kWarps>(p, units, s_sums, s_start, at, w0, w1)) return;
   const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
 
-  if (warp == kConsumers) {
+  if (warp == 4 * W) {
     // ------------------------------------------------------------- producer warp
     // Lane x: block x mod 8 of the tile, of K (x < 8) or V.  It fetches the block's scale, and if a piece (the tokens
     // of one page in the tile) starts with its block, the piece's codes.  Past the sequence's end, and for a page index
@@ -291,54 +322,54 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   }
 
   // ---------------------------------------------------------------- consumer warps
+  const int wg = W == 1 ? 0 : warp >> 2, quarter = W == 1 ? warp : warp & 3, tid = W == 1 ? threadIdx.x : threadIdx.x & 127;
+  auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
   const uint32_t ring = smem_u32(smem);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlOff);  // [warp][row]
-  float* s_qs = reinterpret_cast<float*>(smem + C::kQsOff);
-  const int gr = lane >> 2, gc = 2 * (lane & 3);  // fragment row and first column of this thread
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlOff) + wg * 4 * kHeads;  // [warp][head]
+  float* s_qs = reinterpret_cast<float*>(smem + C::kQsOff) + wg * kHeads;
+  uint8_t* s_q = smem + C::kQOff + wg * kHeads * C::kQStride;
+  // In fragments of scores this thread has tokens gr and gr + 8 of 16 and heads gc and gc + 1 of 8.
+  const int gr = lane >> 2, gc = 2 * (lane & 3);
   int slot = 0;
   uint32_t phase = 0;
   bool first_segment = true;
   // A segment's Q rows (those past the group's heads: zeros) and slopes, fetched into registers while
   // the segment before it ends.
-  constexpr int kQPer = C::kRows * (D / 8) / (32 * kConsumers);  // 16-byte pieces a thread
+  constexpr int kPieces = kHeads * (D / 8);             // of 16 bytes
+  constexpr int kQPer = (kPieces + 127) / 128;          // a thread
   uint4 q_next[kQPer];
-  float slope_next[MT][2];
+  float2 slope_next[NH];
+  auto rows_of = [&](const Place<kTile>& x) { return min(p.group - (x.u % p.chunks) * C::kRows - kHeads * wg, kHeads); };
+  auto head_of = [&](const Place<kTile>& x) { return (x.u / p.chunks) * p.group + (x.u % p.chunks) * C::kRows + kHeads * wg; };
   auto fetch_q = [&](const Place<kTile>& x) {
-    const int chunk = x.u % p.chunks, head0 = (x.u / p.chunks) * p.group + chunk * C::kRows;
-    const int rows = min(p.group - chunk * C::kRows, C::kRows);
+    const int head0 = head_of(x), rows = rows_of(x);
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int y = threadIdx.x + i * 32 * kConsumers, r = y / (D / 8), c = y % (D / 8);
+      const int y = tid + i * 128, r = y / (D / 8), c = y % (D / 8);
       q_next[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows)
         q_next[i] = *reinterpret_cast<const uint4*>(p.q + x.b * p.sq.s[1] + (head0 + r) * p.sq.s[0] + c * 8);
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * mt + gr + 8 * e;
-        slope_next[mt][e] = p.slopes && r < rows ? p.slopes[head0 + r] * kLog2e : 0.f;
-      }
+    for (int h = 0; h < NH; ++h) {
+      const int r = 8 * h + gc;
+      slope_next[h].x = p.slopes && r < rows ? p.slopes[head0 + r] * -kLog2e : 0.f;
+      slope_next[h].y = p.slopes && r + 1 < rows ? p.slopes[head0 + r + 1] * -kLog2e : 0.f;
+    }
   };
   fetch_q(at);
   for (long long w = w0; w < w1;) {
     // ---- a segment: tiles [at.t, at.t + count) of one head unit
-    const int hk = at.u / p.chunks, chunk = at.u % p.chunks;
-    const int head0 = hk * p.group + chunk * C::kRows;
-    const int rows = min(p.group - chunk * C::kRows, C::kRows);
+    const int head0 = head_of(at), rows = rows_of(at);
     const int count = static_cast<int>(min(static_cast<long long>(at.T - at.t), w1 - w));
     const bool whole = count == at.T;
-    float slope2[MT][2];
+    float2 slope2[NH];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      slope2[mt][0] = slope_next[mt][0];
-      slope2[mt][1] = slope_next[mt][1];
-    }
+    for (int h = 0; h < NH; ++h) slope2[h] = slope_next[h];
     // Q to fp16 in [2^14, 2^15) of its row's largest entry.
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int y = threadIdx.x + i * 32 * kConsumers, r = y / (D / 8), c = y % (D / 8);
+      const int y = tid + i * 128, r = y / (D / 8), c = y % (D / 8);
       const uint32_t in[4] = {q_next[i].x, q_next[i].y, q_next[i].z, q_next[i].w};
       float2 f[4];
       float top = 0.f;
@@ -356,34 +387,30 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
       out.y = pack2<true>(f[1].x * by, f[1].y * by);
       out.z = pack2<true>(f[2].x * by, f[2].y * by);
       out.w = pack2<true>(f[3].x * by, f[3].y * by);
-      *reinterpret_cast<uint4*>(smem + C::kQOff + r * C::kQStride + c * 16) = out;
-      if (c == 0) s_qs[r] = power_of_two(e);
+      if (y < kPieces) {
+        *reinterpret_cast<uint4*>(s_q + r * C::kQStride + c * 16) = out;
+        if (c == 0) s_qs[r] = power_of_two(e);
+      }
     }
-    consumers_sync();
-    // A fragments of Q in the order of K's codes: four neighbouring columns a thread.
-    auto load_q = [&](uint32_t (&f)[4], int mt, int kk) {
-      const uint8_t* at_q = smem + C::kQOff + (16 * mt + gr) * C::kQStride + kk * 32 + 4 * gc;
-      const uint2 x = *reinterpret_cast<const uint2*>(at_q), y = *reinterpret_cast<const uint2*>(at_q + 8 * C::kQStride);
-      f[0] = x.x;
-      f[1] = y.x;
-      f[2] = x.y;
-      f[3] = y.y;
+    group_sync();
+    // B fragments of Q^T in the order of K's codes: four neighbouring columns of head gr.
+    auto load_q = [&](int h, int kk) {
+      return *reinterpret_cast<const uint2*>(s_q + (8 * h + gr) * C::kQStride + kk * 32 + 4 * gc);
     };
-    uint32_t qf[MT == 1 ? D / 16 : 1][4];
-    if constexpr (MT == 1) {
+    uint2 qf[NH == 1 ? D / 16 : 1];
+    if constexpr (NH == 1) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) load_q(qf[kk], 0, kk);
+      for (int kk = 0; kk < D / 16; ++kk) qf[kk] = load_q(0, kk);
     }
-    float o[MT][D / 8][4], m[MT][2], mv[MT][2], l[MT][2], to_log2[MT][2];
+    float o[D / 16][NH][4];  // columns 2 gr and 2 gr + 1 of 16 for heads gc, gc + 1: {even, head gc}, {even, gc + 1}, {odd, gc}, ...
+    float2 m[NH], mv[NH], l[NH], to_log2[NH];  // of heads gc and gc + 1; l over this thread's tokens
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = mv[mt][0] = mv[mt][1] = kNoScore;
-      l[mt][0] = l[mt][1] = 0.f;
+    for (int h = 0; h < NH; ++h) {
+      m[h] = mv[h] = pair(kNoScore);
+      l[h] = pair(0.f);
+      to_log2[h] = __fmul2_rn(pair(p.cap_out > 0.f ? p.cap_in : p.scale_log2), make_float2(s_qs[8 * h + gc], s_qs[8 * h + gc + 1]));
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        to_log2[mt][e] = (p.cap_out > 0.f ? p.cap_in : p.scale_log2) * s_qs[16 * mt + gr + 8 * e];
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) o[mt][c][0] = o[mt][c][1] = o[mt][c][2] = o[mt][c][3] = 0.f;
+      for (int c = 0; c < D / 16; ++c) o[c][h][0] = o[c][h][1] = o[c][h][2] = o[c][h][3] = 0.f;
     }
 
     for (int i = 0; i < count; ++i) {
@@ -391,151 +418,156 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
       // warps, which it meets at barriers.
       const bool landed = __all_sync(0xffffffffu, mbar_wait(&bar_full[slot], phase, wc, kSite8Full));
       const uint32_t kb = ring + slot * C::kStage, vb = kb + C::kHalf;
-      const int key0 = (at.t + i) * kTile + 16 * NB * warp;  // this warp's first token
+      const int key0 = (at.t + i) * kTile + 32 * quarter;  // this warp's first token
       if (landed && key0 < at.n) {
-        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes + NB * warp;
-        const int frow = 16 * NB * warp + (lane & 15), fchunk = lane >> 4;  // what this lane addresses for ldmatrix
-        float s[MT][2 * NB][4] = {};
+        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes + 2 * quarter;
+        const int frow = 32 * quarter + (lane & 15), fchunk = lane >> 4;  // what this lane addresses for ldmatrix
+        // S^T = K Q^T of two blocks of 16 tokens.
+        float s[2][NH][4] = {};
 #pragma unroll
         for (int c2 = 0; c2 < D / 32; ++c2) {
-          uint32_t b4[NB][4];
+          uint32_t b4[2][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) ldsm4(b4[nb], kb + piece_of<D>(frow + 16 * nb, 2 * c2 + fchunk));
+          for (int nb = 0; nb < 2; ++nb) ldsm4(b4[nb], kb + piece_of<D>(frow + 16 * nb, 2 * c2 + fchunk));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int kk = 2 * c2 + half;
-            uint32_t kf[NB][4];
+            uint2 b[NH];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              kf[nb][0] = codes_to_half2(b4[nb][2 * half]);
-              kf[nb][1] = codes_to_half2(b4[nb][2 * half] >> 16);
-              kf[nb][2] = codes_to_half2(b4[nb][2 * half + 1]);
-              kf[nb][3] = codes_to_half2(b4[nb][2 * half + 1] >> 16);
-            }
+            for (int h = 0; h < NH; ++h) b[h] = NH == 1 ? qf[NH == 1 ? kk : 0] : load_q(h, kk);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint32_t a4[4];
-              if constexpr (MT > 1) load_q(a4, mt, kk);
+            for (int nb = 0; nb < 2; ++nb) {
+              const uint32_t x = b4[nb][2 * half], y = b4[nb][2 * half + 1];
+              const uint32_t a4[4] = {codes_to_half2(x), codes_to_half2(y), codes_to_half2(x >> 16), codes_to_half2(y >> 16)};
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                  if constexpr (MT == 1) mma16816<true>(s[mt][2 * nb + nt], qf[kk], kf[nb][2 * nt], kf[nb][2 * nt + 1]);
-                  else mma16816<true>(s[mt][2 * nb + nt], a4, kf[nb][2 * nt], kf[nb][2 * nt + 1]);
-                }
+              for (int h = 0; h < NH; ++h) mma_half(s[nb][h], a4, b[h].x, b[h].y);
             }
           }
         }
         // Scales; a block past the end has whatever its page holds there.
-        float ks[NB], lgv[NB];
+        const bool ragged = key0 + 32 > at.n;
+        float ks[2], lgv[2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int nb = 0; nb < 2; ++nb) {
           const bool inside = key0 + 16 * nb < at.n;
           ks[nb] = inside ? sc[nb] : 0.f;
           lgv[nb] = inside ? __log2f(sc[C::kBlocksOfTile + nb]) : 0.f;
         }
-        // Scores in log2 units, and the running softmax of the warp's rows.
-        uint32_t pf[MT][NB][4];
+        // Scores in log2 units: x[block][h][token gr or gr + 8], of heads gc and gc + 1.
+        float2 x[2][NH][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float2 f = __fmul2_rn(to_log2[h], pair(ks[nb]));
+            x[nb][h][0] = __fmul2_rn(make_float2(s[nb][h][0], s[nb][h][1]), f);
+            x[nb][h][1] = __fmul2_rn(make_float2(s[nb][h][2], s[nb][h][3]), f);
+          }
+        if (p.cap_out > 0.f) {
+          // As in the 16-bit decode: relative to the score while |x| < 2.
           uint32_t bits = 0;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const float f[2] = {to_log2[mt][0] * ks[nb], to_log2[mt][1] * ks[nb]};
+          for (int y = 0; y < 4 * NH; ++y) bits = or_bits(bits, x[y & 1][y >> 2][(y >> 1) & 1]);
+          const bool any_far = __any_sync(0xffffffffu, bits & kReachesTwo);
 #pragma unroll
-            for (int nt = 2 * nb; nt < 2 * nb + 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s[mt][nt][e] *= f[e >> 1];
-                bits |= __float_as_uint(s[mt][nt][e]);
-              }
-          }
-          if (p.cap_out > 0.f) {
-            // As in the 16-bit decode: relative to the score while |x| < 2.
-            const bool any_far = __any_sync(0xffffffffu, bits & kReachesTwo);
-#pragma unroll
-            for (int nt = 0; nt < 2 * NB; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                const float2 x = make_float2(s[mt][nt][e], s[mt][nt][e + 1]);
-                float2 y = __fmul2_rn(x, tanh_over_x(x, p.poly));
-                if (any_far) {
-                  const float2 far = tanh_any(x, p.cap_out, pair(0.f));
-                  y = make_float2(fabsf(x.x) < 2.f ? y.x : far.x, fabsf(x.y) < 2.f ? y.y : far.y);
-                }
-                s[mt][nt][e] = y.x;
-                s[mt][nt][e + 1] = y.y;
-              }
-          }
-          float mx[2] = {-INFINITY, -INFINITY}, mxv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int nt = 2 * nb; nt < 2 * nb + 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = key0 + 8 * nt + gc + (e & 1);
-                float x = fmaf(-slope2[mt][e >> 1], static_cast<float>(at.n - 1 - key), s[mt][nt][e]);
-                x = key < at.n ? x : -INFINITY;
-                s[mt][nt][e] = x;
-                top[e >> 1] = fmaxf(top[e >> 1], x);
-              }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mx[e] = fmaxf(mx[e], top[e]);
-              mxv[e] = fmaxf(mxv[e], top[e] + lgv[nb]);
+          for (int y = 0; y < 4 * NH; ++y) {
+            float2& u = x[y & 1][y >> 2][(y >> 1) & 1];
+            float2 z = __fmul2_rn(u, tanh_over_x(u, p.poly));
+            if (any_far) {
+              const float2 far = tanh_any(u, p.cap_out, pair(0.f));
+              z = make_float2(fabsf(u.x) < 2.f ? z.x : far.x, fabsf(u.y) < 2.f ? z.y : far.y);
             }
-          }
-          float alpha[2], alpha_v[2];
-          bool up = false;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mxv[e] = fmaxf(mxv[e], __shfl_xor_sync(0xffffffffu, mxv[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-            mxv[e] = fmaxf(mxv[e], __shfl_xor_sync(0xffffffffu, mxv[e], 2));
-            const float mn = fmaxf(m[mt][e], mx[e]), mvn = fmaxf(mv[mt][e], mxv[e] - C::kHeadroom);
-            alpha[e] = ex2_approx(m[mt][e] - mn);
-            alpha_v[e] = ex2_approx(mv[mt][e] - mvn);
-            up |= mn > m[mt][e] || mvn > mv[mt][e];
-            m[mt][e] = mn;
-            mv[mt][e] = mvn;
-          }
-          if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) l[mt][e] *= alpha[e];
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              o[mt][c][0] *= alpha_v[0];
-              o[mt][c][1] *= alpha_v[0];
-              o[mt][c][2] *= alpha_v[1];
-              o[mt][c][3] *= alpha_v[1];
-            }
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const float to_v[2] = {lgv[nb] - mv[mt][0], lgv[nb] - mv[mt][1]};
-            float pr[2][4];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x = s[mt][2 * nb + nt][e];
-                l[mt][e >> 1] += ex2_approx(x - m[mt][e >> 1]);  // this thread's columns; summed over the quad at the end
-                pr[nt][e] = ex2_approx(x + to_v[e >> 1]);
-              }
-            pf[mt][nb][0] = pack2<true>(pr[0][0], pr[0][1]);
-            pf[mt][nb][1] = pack2<true>(pr[0][2], pr[0][3]);
-            pf[mt][nb][2] = pack2<true>(pr[1][0], pr[1][1]);
-            pf[mt][nb][3] = pack2<true>(pr[1][2], pr[1][3]);
+            u = z;
           }
         }
-        // O += P V: B fragments of 16 tokens x the even or the odd columns of 16.
-        const bool ragged = key0 + 16 * NB > at.n;
+        if (p.slopes) {
+          const float back = static_cast<float>(at.n - 1 - key0 - gr);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          // Tokens past the end: their weight is 0, but what the page holds there may be anything.
+          for (int y = 0; y < 4 * NH; ++y) {
+            float2& u = x[y & 1][y >> 2][(y >> 1) & 1];
+            u = __ffma2_rn(slope2[y >> 2], pair(back - (16 * (y & 1) + 8 * ((y >> 1) & 1))), u);
+          }
+        }
+        if (ragged) {
+#pragma unroll
+          for (int y = 0; y < 4 * NH; ++y)
+            if (key0 + gr + 16 * (y & 1) + 8 * ((y >> 1) & 1) >= at.n) x[y & 1][y >> 2][(y >> 1) & 1] = pair(-INFINITY);
+        }
+        // Weights under the references so far: for l, and times 2^(lgv + m - mv) for P V.  That factor stays below 2^100, so that a
+        // weight that is 0 in fp32 would be under 2^-26 in P V.
+        uint32_t pf[2][NH][2];
+        float2 sum[NH];
+        bool fits = true;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float2 sum_v = pair(0.f);
+          sum[h] = pair(0.f);
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            const float2 to_v = __fadd2_rn(minus(m[h], mv[h]), pair(lgv[nb])), by = ex2_pair(to_v);
+            fits = fits && to_v.x <= 100.f && to_v.y <= 100.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 y = ex2_pair(minus(x[nb][h][e], m[h])), v = __fmul2_rn(y, by);
+              sum[h] = __fadd2_rn(sum[h], y);
+              sum_v = __fadd2_rn(sum_v, v);
+              pf[nb][h][e] = pack2<true>(v.x, v.y);
+            }
+          }
+          fits = fits && fmaxf(sum_v.x, sum_v.y) <= 32768.f && fmaxf(sum[h].x, sum[h].y) <= 0x1p60f;
+        }
+        if (!__all_sync(0xffffffffu, fits)) {
+          // New references, O and l brought to them, and the weights again, each kind from the scores.
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            float2 mx = pair(-INFINITY), mxv = pair(-INFINITY);
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              const float2 top = max_pair(x[nb][h][0], x[nb][h][1]);
+              mx = max_pair(mx, top);
+              mxv = max_pair(mxv, __fadd2_rn(top, pair(lgv[nb])));
+            }
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) {
+              mx = max_pair(mx, make_float2(__shfl_xor_sync(0xffffffffu, mx.x, y), __shfl_xor_sync(0xffffffffu, mx.y, y)));
+              mxv = max_pair(mxv, make_float2(__shfl_xor_sync(0xffffffffu, mxv.x, y), __shfl_xor_sync(0xffffffffu, mxv.y, y)));
+            }
+            mx = max_pair(mx, m[h]);
+            mxv = max_pair(__fadd2_rn(mxv, pair(-7.f)), mv[h]);
+            const float2 alpha = ex2_pair(minus(m[h], mx)), alpha_v = ex2_pair(minus(mv[h], mxv));
+            m[h] = mx;
+            mv[h] = mxv;
+            l[h] = __fmul2_rn(l[h], alpha);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][h][0] *= alpha_v.x;
+              o[c][h][1] *= alpha_v.y;
+              o[c][h][2] *= alpha_v.x;
+              o[c][h][3] *= alpha_v.y;
+            }
+            sum[h] = pair(0.f);
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                sum[h] = __fadd2_rn(sum[h], ex2_pair(minus(x[nb][h][e], mx)));
+                const float2 v = ex2_pair(__fadd2_rn(x[nb][h][e], minus(pair(lgv[nb]), mxv)));
+                pf[nb][h][e] = pack2<true>(v.x, v.y);
+              }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          l[h] = __fadd2_rn(l[h], sum[h]);
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            pf[nb][h][0] = transposed(pf[nb][h][0]);
+            pf[nb][h][1] = transposed(pf[nb][h][1]);
+          }
+        }
+        // O^T += V^T P^T.  Tokens past the end: their weight is 0, but what the page holds there may be anything.
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
           const int left = at.n - (key0 + 16 * nb + gc);
           const uint32_t keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
           const uint32_t keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
@@ -550,22 +582,16 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
               b4[3] &= keep1;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b4[j] = __byte_perm(b4[j], 0, 0x3120);  // columns 2g of both tokens, then 2g + 1
-#pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const uint32_t x = b4[2 * half], y = b4[2 * half + 1];
-              const uint32_t even[2] = {codes_to_half2(x), codes_to_half2(y)};
-              const uint32_t odd[2] = {codes_to_half2(x >> 16), codes_to_half2(y >> 16)};
+              const uint32_t u = __byte_perm(b4[2 * half], 0, 0x3120), v = __byte_perm(b4[2 * half + 1], 0, 0x3120);
+              const uint32_t a4[4] = {codes_to_half2(u), codes_to_half2(u >> 16), codes_to_half2(v), codes_to_half2(v >> 16)};
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<true>(o[mt][4 * c2 + 2 * half], pf[mt][nb], even[0], even[1]);
-                mma16816<true>(o[mt][4 * c2 + 2 * half + 1], pf[mt][nb], odd[0], odd[1]);
-              }
+              for (int h = 0; h < NH; ++h) mma_half(o[2 * c2 + half][h], a4, pf[nb][h][0], pf[nb][h][1]);
             }
           }
         }
       }
-      if (i + 1 < count) {  // the segment's last stage is kept for the warps' meeting below
+      if (W > 1 || i + 1 < count) {  // (one group keeps the segment's last stage for the warps' meeting below)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[slot]);
         if (++slot == C::kStages) {
@@ -580,74 +606,78 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
       next.next_unit(p.c, units);
       fetch_q(next);
     }
-    // ---- the four warps' parts, joined through the segment's last stage
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-        l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
-        if ((lane & 3) == 0) s_ml[warp * C::kRows + 16 * mt + gr + 8 * e] = make_float2(m[mt][e], l[mt][e]);
-      }
-    float* s_o = reinterpret_cast<float*>(smem + slot * C::kStage);  // [warp][16][D]
+    // ---- the four warps' parts, joined
+    float* s_o = reinterpret_cast<float*>(smem + (W == 1 ? slot * C::kStage : C::kOOff + wg * C::kO));  // [warp][head][kORow]
     float* part = p.part + static_cast<size_t>(2 * cta + (first_segment ? 0 : 1)) * C::kRows * (D + 2);
+    group_sync();  // every warp of the group is done with the stage
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      consumers_sync();  // every warp is done with the stage (or with the previous 16 rows)
-      const float back[2] = {ex2_approx(mv[mt][0] - m[mt][0]), ex2_approx(mv[mt][1] - m[mt][1])};
+    for (int h = 0; h < NH; ++h) {
+      float2 all = l[h];
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1)
+        all = __fadd2_rn(all, make_float2(__shfl_xor_sync(0xffffffffu, all.x, y), __shfl_xor_sync(0xffffffffu, all.y, y)));
+      const int head = quarter * kHeads + 8 * h + gc;
+      if (gr == 0) {
+        s_ml[head] = make_float2(m[h].x, all.x);
+        s_ml[head + 1] = make_float2(m[h].y, all.y);
+      }
+      const float2 back = ex2_pair(minus(mv[h], m[h]));
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        float* dst = s_o + (warp * 16 + gr) * D + 16 * c + 2 * gc;
-        const float(&x)[4] = o[mt][2 * c], (&y)[4] = o[mt][2 * c + 1];
-        *reinterpret_cast<float4*>(dst) = make_float4(x[0] * back[0], y[0] * back[0], x[1] * back[0], y[1] * back[0]);
-        *reinterpret_cast<float4*>(dst + 8 * D) = make_float4(x[2] * back[1], y[2] * back[1], x[3] * back[1], y[3] * back[1]);
-      }
-      consumers_sync();
-      const int r = threadIdx.x >> 3, gl = 16 * mt + r;  // 8 threads a row
-      if (gl < rows) {
-        float M = kNoScore, L = 0.f, wgt[kConsumers];
-#pragma unroll
-        for (int x = 0; x < kConsumers; ++x) M = fmaxf(M, s_ml[x * C::kRows + gl].x);
-#pragma unroll
-        for (int x = 0; x < kConsumers; ++x) {
-          const float2 ml = s_ml[x * C::kRows + gl];
-          wgt[x] = ex2_approx(ml.x - M);
-          L += ml.y * wgt[x];
-        }
-        const float inv = whole ? 1.f / L : 1.f;
-        const int head = head0 + gl;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const int col = 4 * ((threadIdx.x & 7) + 8 * c);
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int x = 0; x < kConsumers; ++x) {
-            const float4 v = *reinterpret_cast<const float4*>(s_o + (x * 16 + r) * D + col);
-            acc.x = fmaf(wgt[x], v.x, acc.x);
-            acc.y = fmaf(wgt[x], v.y, acc.y);
-            acc.z = fmaf(wgt[x], v.z, acc.z);
-            acc.w = fmaf(wgt[x], v.w, acc.w);
-          }
-          if (whole)
-            *reinterpret_cast<uint2*>(p.o + at.b * p.so.s[1] + head * p.so.s[0] + col) =
-                make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
-          else
-            *reinterpret_cast<float4*>(part + gl * D + col) = acc;
-        }
-        if ((threadIdx.x & 7) == 0) {
-          if (whole)
-            p.lse[static_cast<size_t>(at.b) * p.H + head] = (M + log2f(L)) * kLn2;
-          else
-            *reinterpret_cast<float2*>(part + C::kRows * D + 2 * gl) = make_float2(M, L);
-        }
+        float* dst = s_o + head * C::kORow + 16 * c + 2 * gr;
+        const float(&x)[4] = o[c][h];
+        *reinterpret_cast<float2*>(dst) = make_float2(x[0] * back.x, x[2] * back.x);
+        *reinterpret_cast<float2*>(dst + C::kORow) = make_float2(x[1] * back.y, x[3] * back.y);
       }
     }
-    fence_proxy_async_smem();  // the stage goes back to the TMA producer
-    consumers_sync();          // (also: s_ml and Q are free)
-    if (lane == 0) mbar_arrive(&bar_empty[slot]);
-    if (++slot == C::kStages) {
-      slot = 0;
-      phase ^= 1u;
+    group_sync();
+    constexpr int kThreadsOfRow = 128 / kHeads;
+    const int r = tid / kThreadsOfRow, in_row = tid % kThreadsOfRow;
+    if (r < rows) {
+      float M = kNoScore, L = 0.f, wgt[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) M = fmaxf(M, s_ml[x * kHeads + r].x);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float2 ml = s_ml[x * kHeads + r];
+        wgt[x] = ex2_approx(ml.x - M);
+        L += ml.y * wgt[x];
+      }
+      const float inv = whole ? 1.f / L : 1.f;
+      const int head = head0 + r;
+#pragma unroll
+      for (int c = 0; c < D / (4 * kThreadsOfRow); ++c) {
+        const int col = 4 * (in_row + kThreadsOfRow * c);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (x * kHeads + r) * C::kORow + col);
+          acc.x = fmaf(wgt[x], v.x, acc.x);
+          acc.y = fmaf(wgt[x], v.y, acc.y);
+          acc.z = fmaf(wgt[x], v.z, acc.z);
+          acc.w = fmaf(wgt[x], v.w, acc.w);
+        }
+        if (whole)
+          *reinterpret_cast<uint2*>(p.o + at.b * p.so.s[1] + head * p.so.s[0] + col) =
+              make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
+        else
+          *reinterpret_cast<float4*>(part + (kHeads * wg + r) * D + col) = acc;
+      }
+      if (in_row == 0) {
+        if (whole)
+          p.lse[static_cast<size_t>(at.b) * p.H + head] = (M + log2f(L)) * kLn2;
+        else
+          *reinterpret_cast<float2*>(part + C::kRows * D + 2 * (kHeads * wg + r)) = make_float2(M, L);
+      }
+    }
+    if constexpr (W == 1) fence_proxy_async_smem();  // the stage goes back to the TMA producer
+    group_sync();                                    // (also: s_ml and Q are free)
+    if constexpr (W == 1) {
+      if (lane == 0) mbar_arrive(&bar_empty[slot]);
+      if (++slot == C::kStages) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     w += count;
     first_segment = false;
@@ -655,9 +685,9 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
   }
 }
 
-template <int D, int MT, bool FP16>
+template <int D, int W, int NH, bool FP16>
 cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
-  using C = Dec8Cfg<D, MT>;
+  using C = Dec8Cfg<D, W, NH>;
   const DecParams p = decode_params(a, C::kRows, C::kTile);
   CUtensorMap tk, tv;
   cudaError_t e;
@@ -671,17 +701,21 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   };
   if ((e = map(&tk, a.c.k, a.c.sk))) return e;
   if ((e = map(&tv, a.c.v, a.c.sv))) return e;
-  auto kern = decode_fp8_kernel<D, MT, FP16>;
+  auto kern = decode_fp8_kernel<D, W, NH, FP16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
-  kern<<<static_cast<unsigned>(paged_decode_ctas(p.group)), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
+  static_assert(C::kPerSm * C::kRows <= 48, "the workspace's parts");
+  kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), 32 * C::kWarps, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
   return launch_dependent(decode_join_kernel<D, FP16>, static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H), 128, 0,
                           stream, p, C::kRows);
 }
 
 template <int D, bool FP16>
-cudaError_t launch_decode8_mt(const PagedDecodeArgs& a, cudaStream_t stream) {
-  return paged_decode_mt(a.H / a.c.Hkv) == 1 ? launch_decode8<D, 1, FP16>(a, stream) : launch_decode8<D, 2, FP16>(a, stream);
+cudaError_t launch_decode8_groups(const PagedDecodeArgs& a, cudaStream_t stream) {
+  const int group = a.H / a.c.Hkv;
+  if (group <= 8) return launch_decode8<D, 1, 1, FP16>(a, stream);
+  if (group <= 16) return launch_decode8<D, 1, 2, FP16>(a, stream);
+  return group <= 32 ? launch_decode8<D, 2, 2, FP16>(a, stream) : launch_decode8<D, 3, 2, FP16>(a, stream);
 }
 
 }  // namespace
@@ -698,8 +732,8 @@ cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t strea
 }
 
 cudaError_t launch_paged_decode_fp8(const PagedDecodeArgs& a, cudaStream_t stream) {
-  if (a.c.d == 64) return a.fp16 ? launch_decode8_mt<64, true>(a, stream) : launch_decode8_mt<64, false>(a, stream);
-  return a.fp16 ? launch_decode8_mt<128, true>(a, stream) : launch_decode8_mt<128, false>(a, stream);
+  if (a.c.d == 64) return a.fp16 ? launch_decode8_groups<64, true>(a, stream) : launch_decode8_groups<64, false>(a, stream);
+  return a.fp16 ? launch_decode8_groups<128, true>(a, stream) : launch_decode8_groups<128, false>(a, stream);
 }
 
 }  // namespace fa

@@ -30,6 +30,21 @@ namespace {
 
 constexpr int kQkThreads = 256;
 
+// x / n for 0 <= x < 2^31 by a product: with s the least number such that n <= 2^s, ceil(2^(31 + s) / n) has 32 bits.
+struct Div {
+  uint32_t by, shift;
+  Div() = default;
+  explicit Div(int n) {
+    int s = 0;
+    while ((1ll << s) < n) ++s;
+    shift = static_cast<uint32_t>(31 + s);
+    by = static_cast<uint32_t>(((1ull << shift) + n - 1) / n);
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * by >> shift);
+  }
+};
+
 // inv_freq / 2 pi modulo 1, as a 64-bit fraction, of a finite |inv_freq| < 2^64.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
   // 1 / 2 pi = 0x0.28be60db9391054a7f09d5f47d4d3770...
@@ -93,7 +108,7 @@ __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
   return __half2float(__ushort_as_half(u));
 }
 
-// A row's layout in its lanes, and one block's tokens.
+// A row's layout in its lanes.
 template <int D>
 struct Rows {
   static constexpr int kLanes = D / 16;                  // of a row
@@ -133,211 +148,306 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], cons
   }
 }
 
+constexpr int kMostTokens = 8;  // of a tile
+
 template <int D>
-struct QkShared {
-  float c[8][D / 2], s[8][D / 2];        // of the block's tokens
-  float w[2][D];                         // q's and k's weights
-  long long in[8][2], out[8][2], g[8][2];  // where the tokens' rows start in q and k
+struct Angles {
+  float c[kMostTokens][D / 2], s[kMostTokens][D / 2];
 };
-
-// The places and angles of tokens first .. first + tokens of the line of all.
-template <int D, bool BACK>
-__device__ __forceinline__ void make_tokens(QkShared<D>& sh, const QkArgs& a, long long first, int tokens) {
+// Of tokens first .. first + tokens of the line of all.
+template <int D>
+__device__ __forceinline__ void make_angles(Angles<D>& x, const QkArgs& a, const Div& per_row, int first, int tokens) {
   const int half = a.rot / 2;
-  if (threadIdx.x < tokens) {
-    const long long at = first + threadIdx.x;
-    const int b = static_cast<int>(at / a.N), n = static_cast<int>(at % a.N);
-    auto place = [&](const Strides& s) { return b * s.s[2] + n * s.s[0]; };
-    sh.in[threadIdx.x][0] = place(a.sq);
-    sh.in[threadIdx.x][1] = place(a.sk);
-    sh.out[threadIdx.x][0] = place(a.sq_out);
-    sh.out[threadIdx.x][1] = place(a.sk_out);
-    if constexpr (BACK) {
-      sh.g[threadIdx.x][0] = place(a.sdq_in);
-      sh.g[threadIdx.x][1] = place(a.sdk_in);
-    }
-  }
-  for (int x = threadIdx.x; x < tokens * half; x += kQkThreads) {
-    const int t = x / half, i = x % half;
-    const long long at = first + t;
-    const int pos = a.positions ? __ldg(a.positions + at) : static_cast<int>(at % a.N);
+  for (int y = threadIdx.x; y < tokens * half; y += kQkThreads) {
+    const int t = y / half, i = y % half, at = first + t;
+    const int pos = a.positions ? __ldg(a.positions + at) : at - per_row(at) * a.N;
     const float2 cs = turn(turns_of(__ldg(a.inv_freq + i)), pos);
-    sh.c[t][i] = cs.x;
-    sh.s[t][i] = cs.y;
+    x.c[t][i] = cs.x;
+    x.s[t][i] = cs.y;
   }
 }
-
 template <int D>
-__device__ __forceinline__ void make_weights(QkShared<D>& sh, const QkArgs& a) {
-  for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
-    const void* w = x < D ? a.q_weight : a.k_weight;
-    sh.w[x / D][x % D] = w ? weight_at(w, a.weight_type, x % D) : 1.f;
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void angles_of(const QkShared<D>& sh, const Rows<D>& me, int t, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void angles_of(const Angles<D>& x, const Rows<D>& me, int t, float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; j += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(&sh.c[t][8 * me.lane + j]);
-    const float4 y = *reinterpret_cast<const float4*>(&sh.s[t][8 * me.lane + j]);
-    c[j] = me.turned ? x.x : 1.f;
-    c[j + 1] = me.turned ? x.y : 1.f;
-    c[j + 2] = me.turned ? x.z : 1.f;
-    c[j + 3] = me.turned ? x.w : 1.f;
-    s[j] = me.turned ? y.x : 0.f;
-    s[j + 1] = me.turned ? y.y : 0.f;
-    s[j + 2] = me.turned ? y.z : 0.f;
-    s[j + 3] = me.turned ? y.w : 0.f;
-  }
-}
-template <int D>
-__device__ __forceinline__ void weights_of(const QkShared<D>& sh, const Rows<D>& me, int side, float (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w[j] = sh.w[side][me.c0 + j];
-    w[8 + j] = sh.w[side][me.c1 + j];
+    const float4 y = *reinterpret_cast<const float4*>(&x.c[t][8 * me.lane + j]);
+    const float4 z = *reinterpret_cast<const float4*>(&x.s[t][8 * me.lane + j]);
+    c[j] = me.turned ? y.x : 1.f;
+    c[j + 1] = me.turned ? y.y : 1.f;
+    c[j + 2] = me.turned ? y.z : 1.f;
+    c[j + 3] = me.turned ? y.w : 1.f;
+    s[j] = me.turned ? z.x : 0.f;
+    s[j + 1] = me.turned ? z.y : 0.f;
+    s[j + 2] = me.turned ? z.z : 0.f;
+    s[j + 3] = me.turned ? z.w : 0.f;
   }
 }
 
-// How the grid divides the rows: blocks of `tokens` tokens and `heads` heads (of q's and k's in one line).
+template <int D>
+__device__ __forceinline__ void make_weights(float (&w)[2][D], const QkArgs& a) {
+  for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
+    const void* from = x < D ? a.q_weight : a.k_weight;
+    w[x / D][x % D] = from ? weight_at(from, a.weight_type, x % D) : 1.f;
+  }
+}
+template <int D>
+__device__ __forceinline__ void weights_of(const float (&in)[2][D], const Rows<D>& me, int side, float (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(&in[side][me.c0 + j]);
+    const float4 y = *reinterpret_cast<const float4*>(&in[side][me.c1 + j]);
+    w[j] = x.x;
+    w[j + 1] = x.y;
+    w[j + 2] = x.z;
+    w[j + 3] = x.w;
+    w[8 + j] = y.x;
+    w[9 + j] = y.y;
+    w[10 + j] = y.z;
+    w[11 + j] = y.w;
+  }
+}
+
+// How the grid divides the rows: tiles of `tokens` tokens and (forward) `heads` heads of q's and k's in one line.
 struct QkGrid {
   int tokens, heads, slices;
   bool heads_first;  // rows that follow each other are heads of a token
+  Div per_row;       // by N
 };
 
+// The rows of a tile and some heads, kGroups at a time: this thread's place among them, with no division after the first.
+struct Walk {
+  int minor, major, minors, majors, step_minor, step_major;
+  __device__ __forceinline__ void start(int group, int groups, int tokens, int heads, bool heads_first) {
+    minors = heads_first ? heads : tokens;
+    majors = heads_first ? tokens : heads;
+    minor = group % minors;
+    major = group / minors;
+    step_minor = groups % minors;
+    step_major = groups / minors;
+  }
+  __device__ __forceinline__ void step() {
+    minor += step_minor;
+    major += step_major;
+    if (minor >= minors) {
+      minor -= minors;
+      ++major;
+    }
+  }
+  __device__ __forceinline__ bool real() const { return major < majors; }
+};
+
+__device__ __forceinline__ long long row_at(const Strides& s, int b, int n, int h) {
+  return b * s.s[2] + n * s.s[0] + h * s.s[1];
+}
+
+// Two pieces of a row.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw load_row(const void* base, long long at, int c0, int c1) {
+  const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+  return Raw{__ldcs(reinterpret_cast<const uint4*>(p + c0)), __ldcs(reinterpret_cast<const uint4*>(p + c1))};
+}
+
+// The forward.  A block's rows stream through its threads, the next ones' loads in flight while this one is worked on; the
+// first are requested before the angles are made.
 template <int D, bool FP16, bool PAIRS>
-__global__ void __launch_bounds__(kQkThreads) qk_forward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
-  __shared__ __align__(16) QkShared<D> sh;
+__global__ void __launch_bounds__(kQkThreads, 4) qk_forward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
+  __shared__ __align__(16) Angles<D> angles;
+  __shared__ __align__(16) float weights[2][D];
   using R = Rows<D>;
   const R me(a);
-  const long long all = static_cast<long long>(a.B) * a.N, first = static_cast<long long>(blockIdx.x / g.slices) * g.tokens;
-  const int tokens = static_cast<int>(min(static_cast<long long>(g.tokens), all - first));
-  const int h0 = (blockIdx.x % g.slices) * g.heads, heads = min(g.heads, a.H + a.Hkv - h0);
-  make_tokens<D, false>(sh, a, first, tokens);
-  make_weights<D>(sh, a);
+  const int tile = blockIdx.x / g.slices, first = tile * g.tokens, tokens = min(g.tokens, a.B * a.N - first);
+  const int h0 = (blockIdx.x - tile * g.slices) * g.heads, heads = min(g.heads, a.H + a.Hkv - h0);
+  Walk at;
+  at.start(me.group, R::kGroups, tokens, heads, g.heads_first);
+  // A row: its token in the tile, whether it is k's, its head there; and its pieces.
+  struct Row {
+    int t, side, head, b, n;
+    bool real;
+  };
+  auto here = [&]() {
+    Row r;
+    r.real = at.real();
+    const int minor = r.real ? at.minor : 0, major = r.real ? at.major : 0;
+    r.t = g.heads_first ? major : minor;
+    const int h = h0 + (g.heads_first ? minor : major);
+    r.side = h >= a.H;
+    r.head = r.side ? h - a.H : h;
+    r.b = g.per_row(first + r.t);
+    r.n = first + r.t - r.b * a.N;
+    return r;
+  };
+  auto load = [&](const Row& r) {
+    return load_row(r.side ? a.k : a.q, row_at(r.side ? a.sk : a.sq, r.b, r.n, r.head), me.c0, me.c1);
+  };
+  Row row = here();
+  Raw raw = load(row);
+  make_angles<D>(angles, a, g.per_row, first, tokens);
+  make_weights<D>(weights, a);
   __syncthreads();
-  const int rows = tokens * heads;
-  for (int r0 = 0; r0 < rows; r0 += R::kGroups) {  // (a whole warp goes through: the sums are shuffles)
-    const int r = r0 + me.group;
-    const bool real = r < rows;
-    const int t = !real ? 0 : g.heads_first ? r / heads : r % tokens, h = h0 + (!real ? 0 : g.heads_first ? r % heads : r / tokens);
-    const int side = h >= a.H;
-    const long long head = side ? h - a.H : h;
-    const uint16_t* in = static_cast<const uint16_t*>(side ? a.k : a.q) + sh.in[t][side] + head * (side ? a.sk : a.sq).s[1];
+  for (int r0 = 0, rows = tokens * heads; r0 < rows; r0 += R::kGroups) {  // (a whole warp goes through: the sums are shuffles)
+    at.step();
+    const Row next = here();
+    Raw ahead = raw;
+    if (r0 + R::kGroups < rows) ahead = load(next);
     float x[16];
-    unpack8<FP16>(*reinterpret_cast<const uint4*>(in + me.c0), x);
-    unpack8<FP16>(*reinterpret_cast<const uint4*>(in + me.c1), x + 8);
+    unpack8<FP16>(raw.a, x);
+    unpack8<FP16>(raw.b, x + 8);
     if (a.norm) {
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
       const float r_norm = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
       float w[16];
-      weights_of<D>(sh, me, side, w);
+      weights_of<D>(weights, me, row.side, w);
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] *= r_norm * w[j];
     }
     float c[8], s[8];
-    angles_of<D>(sh, me, t, c, s);
+    angles_of<D>(angles, me, row.t, c, s);
     rotate<PAIRS>(x, c, s, 1.f);
-    uint16_t* out = static_cast<uint16_t*>(side ? a.k_out : a.q_out) + sh.out[t][side] + head * (side ? a.sk_out : a.sq_out).s[1];
-    if (real) {
+    if (row.real) {
+      uint16_t* out = static_cast<uint16_t*>(row.side ? a.k_out : a.q_out) +
+                      row_at(row.side ? a.sk_out : a.sq_out, row.b, row.n, row.head);
       *reinterpret_cast<uint4*>(out + me.c0) = pack8<FP16>(x);
       *reinterpret_cast<uint4*>(out + me.c1) = pack8<FP16>(x + 8);
     }
+    row = next;
+    raw = ahead;
   }
 }
 
-// The gradient.  Blocks stay on the GPU and take tiles of tokens in turn, so that the weights' gradients add up in registers; each block's sums go
-// to the workspace and a second kernel adds them in order: the same bits on every run.
+// The gradient.  Blocks stay on the GPU and take tiles of tokens in turn, so that the weights' gradients add up in a thread; each block's
+// sums go to the workspace and a second kernel adds them in order: the same bits on every run.  Rows stream as in the forward, over the
+// ends of sides (q, then k) and tiles too.  A thread's sums of the side that it is not at lie in shared memory: 16 registers less.
 template <int D, bool FP16, bool PAIRS>
-__global__ void __launch_bounds__(kQkThreads) qk_backward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
-  __shared__ __align__(16) QkShared<D> sh;
-  __shared__ float s_dw[kQkThreads / 32][D];
+__global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
+  __shared__ __align__(16) Angles<D> angles[2];
+  __shared__ __align__(16) float weights[2][D];
+  __shared__ float4 sums[2][4][kQkThreads];
   using R = Rows<D>;
   const R me(a);
-  const long long all = static_cast<long long>(a.B) * a.N, tiles = (all + g.tokens - 1) / g.tokens;
-  make_weights<D>(sh, a);
-  float dw[2][16] = {};
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const long long first = tile * g.tokens;
-    const int tokens = static_cast<int>(min(static_cast<long long>(g.tokens), all - first));
-    __syncthreads();
-    make_tokens<D, true>(sh, a, first, tokens);
-    __syncthreads();
+  const int all = a.B * a.N, tiles = (all + g.tokens - 1) / g.tokens;
+  // The place of the rows that are being loaded: a tile, a side, a pass of the walk through its rows.
+  struct Place {
+    int tile, side, left;  // passes left
+    Walk at;
+    int t, head, b, n;
+    bool real;
+  } ahead;
+  auto enter = [&]() {  // to the first pass of (tile, side), or of the next that has rows
+    for (; ahead.tile < tiles; ahead.tile += gridDim.x, ahead.side = 0)
+      for (; ahead.side < 2; ++ahead.side) {
+        const int tokens = min(g.tokens, all - ahead.tile * g.tokens), heads = ahead.side ? a.Hkv : a.H;
+        ahead.left = (tokens * heads + R::kGroups - 1) / R::kGroups;
+        if (ahead.left == 0) continue;
+        ahead.at.start(me.group, R::kGroups, tokens, heads, g.heads_first);
+        return;
+      }
+  };
+  Raw raw_x, raw_g;
+  auto load = [&]() {
+    if (ahead.tile >= tiles) return;
+    ahead.real = ahead.at.real();
+    ahead.t = !ahead.real ? 0 : g.heads_first ? ahead.at.major : ahead.at.minor;
+    ahead.head = !ahead.real ? 0 : g.heads_first ? ahead.at.minor : ahead.at.major;
+    const int at = ahead.tile * g.tokens + ahead.t;
+    ahead.b = g.per_row(at);
+    ahead.n = at - ahead.b * a.N;
+    const bool k = ahead.side;
+    raw_x = raw_g = Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (ahead.real) {  // (a row that is none: zeros, which add nothing to the sums)
+      raw_g = load_row(k ? a.dk_in : a.dq_in, row_at(k ? a.sdk_in : a.sdq_in, ahead.b, ahead.n, ahead.head), me.c0, me.c1);
+      if (a.norm) raw_x = load_row(k ? a.k : a.q, row_at(k ? a.sk : a.sq, ahead.b, ahead.n, ahead.head), me.c0, me.c1);
+    }
+  };
+  ahead.tile = blockIdx.x;
+  ahead.side = 0;
+  enter();
+  load();
+  make_weights<D>(weights, a);
 #pragma unroll
+  for (int i = 0; i < 8; ++i) sums[i / 4][i % 4][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int buffer = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buffer ^= 1) {
+    make_angles<D>(angles[buffer], a, g.per_row, tile * g.tokens, min(g.tokens, all - tile * g.tokens));
+    __syncthreads();  // (and the buffer of the tile before the last is free)
     for (int side = 0; side < 2; ++side) {
-      const int heads = side ? a.Hkv : a.H, rows = tokens * heads;
-      const uint16_t *xs = static_cast<const uint16_t*>(side ? a.k : a.q),
-                     *gs = static_cast<const uint16_t*>(side ? a.dk_in : a.dq_in);
-      uint16_t* os = static_cast<uint16_t*>(side ? a.k_out : a.q_out);
-      const long long hx = (side ? a.sk : a.sq).s[1], hg = (side ? a.sdk_in : a.sdq_in).s[1], ho = (side ? a.sk_out : a.sq_out).s[1];
-      float w[16];
-      weights_of<D>(sh, me, side, w);
-      for (int r0 = 0; r0 < rows; r0 += R::kGroups) {
-        const int r = r0 + me.group;
-        const bool real = r < rows;
-        const int t = !real ? 0 : g.heads_first ? r / heads : r % tokens, h = !real ? 0 : g.heads_first ? r % heads : r / tokens;
-        const uint16_t* grow = gs + sh.g[t][side] + h * hg;
-        float y[16], c[8], s[8];
-        unpack8<FP16>(*reinterpret_cast<const uint4*>(grow + me.c0), y);
-        unpack8<FP16>(*reinterpret_cast<const uint4*>(grow + me.c1), y + 8);
-        angles_of<D>(sh, me, t, c, s);
+      if (ahead.tile != tile || ahead.side != side) continue;  // no rows on this side
+      uint16_t* outs = static_cast<uint16_t*>(side ? a.k_out : a.q_out);
+      const Strides& so = side ? a.sk_out : a.sq_out;
+      float dw[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(dw + 4 * i) = sums[side][i][threadIdx.x];
+      for (bool last = false; !last;) {
+        float x[16], y[16], c[8], s[8];
+        unpack8<FP16>(raw_g.a, y);
+        unpack8<FP16>(raw_g.b, y + 8);
+        unpack8<FP16>(raw_x.a, x);
+        unpack8<FP16>(raw_x.b, x + 8);
+        const bool real = ahead.real;
+        const int t = ahead.t;
+        uint16_t* out = outs + row_at(so, ahead.b, ahead.n, ahead.head);
+        last = --ahead.left == 0;
+        if (last) {
+          ++ahead.side;
+          enter();
+        } else {
+          ahead.at.step();
+        }
+        load();
+        angles_of<D>(angles[buffer], me, t, c, s);
+        rotate<PAIRS>(y, c, s, -1.f);
         if (a.norm) {
-          const uint16_t* in = xs + sh.in[t][side] + h * hx;
-          float x[16];
-          unpack8<FP16>(*reinterpret_cast<const uint4*>(in + me.c0), x);
-          unpack8<FP16>(*reinterpret_cast<const uint4*>(in + me.c1), x + 8);
-          rotate<PAIRS>(y, c, s, -1.f);
           float ss = 0.f;
 #pragma unroll
           for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
           const float r_norm = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-          float dot = 0.f;
+          float w[16], dot = 0.f;
+          weights_of<D>(weights, me, side, w);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             x[j] *= r_norm;
-            if (real) dw[side][j] = fmaf(y[j], x[j], dw[side][j]);
+            dw[j] = fmaf(y[j], x[j], dw[j]);
             y[j] *= w[j];
             dot = fmaf(y[j], x[j], dot);
           }
           dot = row_sum<D>(dot) * (1.f / D);
 #pragma unroll
           for (int j = 0; j < 16; ++j) y[j] = r_norm * fmaf(-dot, x[j], y[j]);
-        } else {
-          rotate<PAIRS>(y, c, s, -1.f);
         }
-        uint16_t* out = os + sh.out[t][side] + h * ho;
         if (real) {
           *reinterpret_cast<uint4*>(out + me.c0) = pack8<FP16>(y);
           *reinterpret_cast<uint4*>(out + me.c1) = pack8<FP16>(y + 8);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[side][i][threadIdx.x] = *reinterpret_cast<float4*>(dw + 4 * i);
     }
   }
   grid_release();
   if (!a.dq_weight && !a.dk_weight) return;
-  // This block's sums: over a warp's rows by shuffles, over the warps in shared memory.
+  // This block's sums: column i of a side over all groups of lanes.
+  __syncthreads();
   float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(blockIdx.x) * 2 * D;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float x = dw[side][j];
-#pragma unroll
-      for (int m = R::kLanes; m < 32; m <<= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-      if (lane < R::kLanes) s_dw[warp][(j < 8 ? me.c0 : me.c1 - 8) + j] = x;
+  for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
+    const int side = x / D, i = x % D;
+    // The lane and place whose pieces hold the column.
+    int lane, j;
+    if (a.pairs || i >= a.rot) {
+      lane = i / 16;
+      j = i % 16;
+    } else {
+      const int half = i >= a.rot / 2, k = i - half * (a.rot / 2);
+      lane = k / 8;
+      j = k % 8 + 8 * half;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < D; i += kQkThreads) {
-      float x = 0.f;
-#pragma unroll
-      for (int k = 0; k < kQkThreads / 32; ++k) x += s_dw[k][i];
-      part[side * D + i] = x;
-    }
+    const float* from = reinterpret_cast<const float*>(&sums[side][j / 4][0]) + j % 4;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < R::kGroups; ++k) sum += from[4 * (k * R::kLanes + lane)];
+    part[x] = sum;
   }
 }
 
@@ -362,7 +472,7 @@ __global__ void __launch_bounds__(1024) qk_weights_kernel(const __grid_constant_
   }
 }
 
-constexpr int kBackBlocksPerSm = 3;
+constexpr int kBackBlocksPerSm = 2;
 
 bool heads_first(const QkArgs& a) { return a.sq.s[1] < a.sq.s[0]; }
 
@@ -371,7 +481,7 @@ cudaError_t launch_forward(const QkArgs& a, cudaStream_t stream) {
   constexpr int kGroups = Rows<D>::kGroups;
   const long long all = static_cast<long long>(a.B) * a.N;
   const int sms = sm_count(), heads = a.H + a.Hkv;
-  QkGrid g{8, heads, 1, heads_first(a)};
+  QkGrid g{kMostTokens, heads, 1, heads_first(a), Div(a.N)};
   while (g.tokens > 1 && (all + g.tokens - 1) / g.tokens < 4LL * sms) g.tokens /= 2;
   if (g.tokens == 1) {
     // Too few tokens for the SMs: their heads in slices of one row a group at least.
@@ -389,7 +499,7 @@ template <int D, bool FP16, bool PAIRS>
 cudaError_t launch_backward(const QkArgs& a, cudaStream_t stream) {
   const long long all = static_cast<long long>(a.B) * a.N;
   const int most = sm_count() * kBackBlocksPerSm;
-  QkGrid g{8, 0, 1, heads_first(a)};
+  QkGrid g{kMostTokens, 0, 1, heads_first(a), Div(a.N)};
   while (g.tokens > 1 && (all + g.tokens - 1) / g.tokens < most) g.tokens /= 2;
   const int blocks = static_cast<int>(std::max(1LL, std::min<long long>(most, (all + g.tokens - 1) / g.tokens)));
   qk_backward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, 0, stream>>>(a, g);

@@ -248,7 +248,7 @@ int fa_paged_append(const void* k, const int64_t* k_strides, const void* v, cons
 size_t fa_paged_decode_workspace_size(int B, int H, int Hkv, int d) {
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
   if (B > 65535 || static_cast<long long>(B) * H > kIntMax) return 0;
-  return fa::paged_decode_workspace(B, H, Hkv, d);
+  return fa::paged_decode_workspace(B, d);
 }
 
 int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache, const int64_t* k_cache_strides,
@@ -263,7 +263,7 @@ int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache
   if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H > kIntMax) return FA_ERR_UNSUPPORTED;
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, H, Hkv, d)) return FA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, d)) return FA_ERR_WORKSPACE;
   fa::PagedDecodeArgs a{};
   int st = paged_cache(&a.c, k_cache, k_cache_strides, v_cache, v_cache_strides, page_table, table_stride, seq_lens,
                        B, Hkv, d, page_size, n_pages, max_pages);
@@ -352,7 +352,7 @@ int fa_paged_decode_fp8(const void* q, const int64_t* q_strides, const void* k_c
   if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H > kIntMax) return FA_ERR_UNSUPPORTED;
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, H, Hkv, d)) return FA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, d)) return FA_ERR_WORKSPACE;
   fa::PagedDecodeArgs a{};
   int st = paged_cache(&a.c, k_cache, k_cache_strides, v_cache, v_cache_strides, page_table, table_stride, seq_lens,
                        B, Hkv, d, page_size, n_pages, max_pages);

@@ -186,11 +186,15 @@ def paged_decode_fp8(q, k_codes, v_codes, k_scales, v_scales, table, lens, scale
             P, lse[b, h] = e / e.sum(), top + np.log(e.sum())
             o[b, h] = P @ vv
             size = scale * np.max(np.abs(q[b, h]) @ np.abs(kk).T)
-            lost = scale * 2.0 ** -40 * np.abs(q[b, h]).max() * np.abs(kk).sum(axis=1).max()  # q's smallest entries
+            # What fp16's range loses of q's small entries, and of the weights times V's scales, beside the largest.
+            small = np.abs(q[b, h]) * (np.abs(q[b, h]) < 2.0 ** -28 * np.abs(q[b, h]).max())
+            lost = scale * np.max(np.abs(kk) @ np.minimum(small, 2.0 ** -39 * np.abs(q[b, h]).max()))
             err = HALF32 * ((d + 12) * size + 8 * min(cap, size) + 8 * abs(slope) * n) + lost + 2e-6
-            # P times V's scale rounded to fp16, and what falls below 2^-40 of the largest.
+            w = P * sv[h // G]
+            w = np.where(w < 2.0 ** -21 * w.max(), np.minimum(w, 2.0 ** -32 * w.max()), 0.0)
+            # P times V's scale rounded to fp16, and what it loses.
             ob[b, h] = (2.0 ** -11 + 3 * err) * (P @ np.abs(vv)) * 1.01 + half * np.abs(o[b, h]) + 2.0 ** -24
-            ob[b, h] += n * 448.0 * 2.0 ** -40 * np.max(P * sv[h // G])
+            ob[b, h] += w @ np.where(sv[h // G][:, None] > 0, np.abs(vv) / np.maximum(sv[h // G], 1e-300)[:, None], 0.0)
             lb[b, h] = 2 * err + 4 * HALF32 * abs(lse[b, h])
     return o, lse, ob, lb
 
