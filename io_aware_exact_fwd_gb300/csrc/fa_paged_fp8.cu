@@ -183,31 +183,29 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const __grid_constant__
 // byte shuffle makes pairs of tokens, of the even column 2g (row g of the product) and the odd one (row g + 8).  The weights
 // come out with a token's heads side by side and go in with a head's tokens side by side: movmatrix transposes them.
 //
-// Warps.  A warp's tile of work is 32 tokens for 8 or 16 query heads.  Up to 16 heads share a key/value head in most models:
-// CTAs of four such warps and a producer, two or three an SM.  More heads go to two or three groups of four warps of one
-// CTA, which work on the same stages: the cache is read once.
+// A warp's part of a tile is 32 tokens for 8 or 16 query heads.  More heads a key/value head are chunks of 16, head units of their
+// own, whose tiles come from L2 for all but the first.  (Two or three groups of four warps that work on the same stages, so
+// that the cache is read once, ran at 3.6 TB/s of codes with 32 heads and 1.9 with 40: no more than chunks reach
+// with nothing in L2, for their arithmetic is the same and one CTA an SM hides less of it.)
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
-template <int D, int W, int NH>  // W groups of four consumer warps, each for 8 NH heads
+template <int D, int NH>
 struct Dec8Cfg {
-  static constexpr int kWarps = 4 * W + 1;
-  static constexpr int kHeads = 8 * NH;                      // of a group
-  static constexpr int kRows = kHeads * W;                   // query heads per chunk
+  static constexpr int kHeads = 8 * NH;                      // query heads per chunk
   static constexpr int kTile = 128;                          // tokens per tile
   static constexpr int kBlocksOfTile = kTile / 16;
   static constexpr int kHalf = kTile * D;                    // K or V of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kPerSm = W > 1 ? 1 : NH * D <= 128 ? 3 : 2;
+  static constexpr int kPerSm = NH * D <= 128 ? 3 : 2;
   static constexpr int kStages = (kPerSm == 3 ? 65536 : 98304) / kStage;
   static constexpr int kORow = D + (NH == 1 ? 8 : 0);        // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
-  static constexpr int kO = 4 * kHeads * kORow * 4;          // a group's O: in the segment's last stage, or with several groups its own
+  static constexpr int kO = 4 * kHeads * kORow * 4;          // the warps' O, in a segment's last stage
   static constexpr int kQStride = D * 2 + 32;                // bytes; 8-byte loads of 4 rows meet every bank once
-  static constexpr int kOOff = kStages * kStage;
-  static constexpr int kScaleOff = kOOff + (W == 1 ? 0 : W * kO);  // K's and V's scales of each stage
+  static constexpr int kScaleOff = kStages * kStage;         // K's and V's scales of each stage
   static constexpr int kQOff = kScaleOff + kStages * 2 * kBlocksOfTile * 4;
-  static constexpr int kQsOff = kQOff + kRows * kQStride;    // q's powers of two
-  static constexpr int kMlOff = kQsOff + kRows * 4;          // (m, l) of each warp's heads
-  static constexpr int kBarOff = kMlOff + 4 * kRows * 8;
+  static constexpr int kQsOff = kQOff + kHeads * kQStride;    // q's powers of two
+  static constexpr int kMlOff = kQsOff + kHeads * 4;          // (m, l) of each warp's heads
+  static constexpr int kBarOff = kMlOff + 4 * kHeads * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
   static constexpr int kScaleLanes = 2 * kBlocksOfTile;
@@ -238,11 +236,11 @@ __device__ __forceinline__ uint32_t piece_of(int row, int chunk) {
   else return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D, int W, int NH, bool FP16>
-__global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, NH>::kPerSm)
+template <int D, int NH, bool FP16>
+__global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ DecParams p) {
-  using C = Dec8Cfg<D, W, NH>;
+  using C = Dec8Cfg<D, NH>;
   constexpr int kTile = C::kTile, kHeads = C::kHeads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -257,7 +255,7 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar_full[s], 1 + C::kScaleLanes);
-      mbar_init(&bar_empty[s], 4 * W);
+      mbar_init(&bar_empty[s], kConsumers);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -267,10 +265,10 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
   Place<kTile> at;
   long long w0, w1;
   const int cta = static_cast<int>(blockIdx.x);
-  if (!share_of_tiles<C::kWarps>(p, units, s_sums, s_start, at, w0, w1)) return;
+  if (!share_of_tiles<kConsumers + 1>(p, units, s_sums, s_start, at, w0, w1)) return;
   const WaitCtl wc{abort_flag, p.err_word, p.wait_ns};
 
-  if (warp == 4 * W) {
+  if (warp == kConsumers) {
     // ------------------------------------------------------------- producer warp
     // Lane x: block x mod 8 of the tile, of K (x < 8) or V.  It fetches the block's scale, and if a piece (the tokens
     // of one page in the tile) starts with its block, the piece's codes.  Past the sequence's end, and for a page index
@@ -322,12 +320,10 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
   }
 
   // ---------------------------------------------------------------- consumer warps
-  const int wg = W == 1 ? 0 : warp >> 2, quarter = W == 1 ? warp : warp & 3, tid = W == 1 ? threadIdx.x : threadIdx.x & 127;
-  auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
   const uint32_t ring = smem_u32(smem);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlOff) + wg * 4 * kHeads;  // [warp][head]
-  float* s_qs = reinterpret_cast<float*>(smem + C::kQsOff) + wg * kHeads;
-  uint8_t* s_q = smem + C::kQOff + wg * kHeads * C::kQStride;
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlOff);  // [warp][head]
+  float* s_qs = reinterpret_cast<float*>(smem + C::kQsOff);
+  uint8_t* s_q = smem + C::kQOff;
   // In fragments of scores this thread has tokens gr and gr + 8 of 16 and heads gc and gc + 1 of 8.
   const int gr = lane >> 2, gc = 2 * (lane & 3);
   int slot = 0;
@@ -339,13 +335,13 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
   constexpr int kQPer = (kPieces + 127) / 128;          // a thread
   uint4 q_next[kQPer];
   float2 slope_next[NH];
-  auto rows_of = [&](const Place<kTile>& x) { return min(p.group - (x.u % p.chunks) * C::kRows - kHeads * wg, kHeads); };
-  auto head_of = [&](const Place<kTile>& x) { return (x.u / p.chunks) * p.group + (x.u % p.chunks) * C::kRows + kHeads * wg; };
+  auto rows_of = [&](const Place<kTile>& x) { return min(p.group - (x.u % p.chunks) * kHeads, kHeads); };
+  auto head_of = [&](const Place<kTile>& x) { return (x.u / p.chunks) * p.group + (x.u % p.chunks) * kHeads; };
   auto fetch_q = [&](const Place<kTile>& x) {
     const int head0 = head_of(x), rows = rows_of(x);
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int y = tid + i * 128, r = y / (D / 8), c = y % (D / 8);
+      const int y = threadIdx.x + i * 128, r = y / (D / 8), c = y % (D / 8);
       q_next[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows)
         q_next[i] = *reinterpret_cast<const uint4*>(p.q + x.b * p.sq.s[1] + (head0 + r) * p.sq.s[0] + c * 8);
@@ -369,7 +365,7 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
     // Q to fp16 in [2^14, 2^15) of its row's largest entry.
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
-      const int y = tid + i * 128, r = y / (D / 8), c = y % (D / 8);
+      const int y = threadIdx.x + i * 128, r = y / (D / 8), c = y % (D / 8);
       const uint32_t in[4] = {q_next[i].x, q_next[i].y, q_next[i].z, q_next[i].w};
       float2 f[4];
       float top = 0.f;
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
         if (c == 0) s_qs[r] = power_of_two(e);
       }
     }
-    group_sync();
+    consumers_sync();
     // B fragments of Q^T in the order of K's codes: four neighbouring columns of head gr.
     auto load_q = [&](int h, int kk) {
       return *reinterpret_cast<const uint2*>(s_q + (8 * h + gr) * C::kQStride + kk * 32 + 4 * gc);
@@ -418,10 +414,10 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
       // warps, which it meets at barriers.
       const bool landed = __all_sync(0xffffffffu, mbar_wait(&bar_full[slot], phase, wc, kSite8Full));
       const uint32_t kb = ring + slot * C::kStage, vb = kb + C::kHalf;
-      const int key0 = (at.t + i) * kTile + 32 * quarter;  // this warp's first token
+      const int key0 = (at.t + i) * kTile + 32 * warp;  // this warp's first token
       if (landed && key0 < at.n) {
-        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes + 2 * quarter;
-        const int frow = 32 * quarter + (lane & 15), fchunk = lane >> 4;  // what this lane addresses for ldmatrix
+        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes + 2 * warp;
+        const int frow = 32 * warp + (lane & 15), fchunk = lane >> 4;  // what this lane addresses for ldmatrix
         // S^T = K Q^T of two blocks of 16 tokens.
         float s[2][NH][4] = {};
 #pragma unroll
@@ -591,7 +587,7 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
           }
         }
       }
-      if (W > 1 || i + 1 < count) {  // (one group keeps the segment's last stage for the warps' meeting below)
+      if (i + 1 < count) {  // the segment's last stage is kept for the warps' meeting below
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[slot]);
         if (++slot == C::kStages) {
@@ -607,16 +603,16 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
       fetch_q(next);
     }
     // ---- the four warps' parts, joined
-    float* s_o = reinterpret_cast<float*>(smem + (W == 1 ? slot * C::kStage : C::kOOff + wg * C::kO));  // [warp][head][kORow]
-    float* part = p.part + static_cast<size_t>(2 * cta + (first_segment ? 0 : 1)) * C::kRows * (D + 2);
-    group_sync();  // every warp of the group is done with the stage
+    float* s_o = reinterpret_cast<float*>(smem + slot * C::kStage);  // [warp][head][kORow]
+    float* part = p.part + static_cast<size_t>(2 * cta + (first_segment ? 0 : 1)) * kHeads * (D + 2);
+    consumers_sync();  // every warp is done with the stage
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       float2 all = l[h];
 #pragma unroll
       for (int y = 4; y < 32; y <<= 1)
         all = __fadd2_rn(all, make_float2(__shfl_xor_sync(0xffffffffu, all.x, y), __shfl_xor_sync(0xffffffffu, all.y, y)));
-      const int head = quarter * kHeads + 8 * h + gc;
+      const int head = warp * kHeads + 8 * h + gc;
       if (gr == 0) {
         s_ml[head] = make_float2(m[h].x, all.x);
         s_ml[head + 1] = make_float2(m[h].y, all.y);
@@ -630,9 +626,9 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
         *reinterpret_cast<float2*>(dst + C::kORow) = make_float2(x[1] * back.y, x[3] * back.y);
       }
     }
-    group_sync();
+    consumers_sync();
     constexpr int kThreadsOfRow = 128 / kHeads;
-    const int r = tid / kThreadsOfRow, in_row = tid % kThreadsOfRow;
+    const int r = threadIdx.x / kThreadsOfRow, in_row = threadIdx.x % kThreadsOfRow;
     if (r < rows) {
       float M = kNoScore, L = 0.f, wgt[4];
 #pragma unroll
@@ -661,23 +657,21 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
           *reinterpret_cast<uint2*>(p.o + at.b * p.so.s[1] + head * p.so.s[0] + col) =
               make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
         else
-          *reinterpret_cast<float4*>(part + (kHeads * wg + r) * D + col) = acc;
+          *reinterpret_cast<float4*>(part + r * D + col) = acc;
       }
       if (in_row == 0) {
         if (whole)
           p.lse[static_cast<size_t>(at.b) * p.H + head] = (M + log2f(L)) * kLn2;
         else
-          *reinterpret_cast<float2*>(part + C::kRows * D + 2 * (kHeads * wg + r)) = make_float2(M, L);
+          *reinterpret_cast<float2*>(part + kHeads * D + 2 * r) = make_float2(M, L);
       }
     }
-    if constexpr (W == 1) fence_proxy_async_smem();  // the stage goes back to the TMA producer
-    group_sync();                                    // (also: s_ml and Q are free)
-    if constexpr (W == 1) {
-      if (lane == 0) mbar_arrive(&bar_empty[slot]);
-      if (++slot == C::kStages) {
-        slot = 0;
-        phase ^= 1u;
-      }
+    fence_proxy_async_smem();  // the stage goes back to the TMA producer
+    consumers_sync();          // (also: s_ml and Q are free)
+    if (lane == 0) mbar_arrive(&bar_empty[slot]);
+    if (++slot == C::kStages) {
+      slot = 0;
+      phase ^= 1u;
     }
     w += count;
     first_segment = false;
@@ -685,10 +679,10 @@ __global__ void __launch_bounds__(32 * Dec8Cfg<D, W, NH>::kWarps, Dec8Cfg<D, W, 
   }
 }
 
-template <int D, int W, int NH, bool FP16>
+template <int D, int NH, bool FP16>
 cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
-  using C = Dec8Cfg<D, W, NH>;
-  const DecParams p = decode_params(a, C::kRows, C::kTile);
+  using C = Dec8Cfg<D, NH>;
+  const DecParams p = decode_params(a, C::kHeads, C::kTile);
   CUtensorMap tk, tv;
   cudaError_t e;
   constexpr auto kSwizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -701,21 +695,18 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   };
   if ((e = map(&tk, a.c.k, a.c.sk))) return e;
   if ((e = map(&tv, a.c.v, a.c.sv))) return e;
-  auto kern = decode_fp8_kernel<D, W, NH, FP16>;
+  auto kern = decode_fp8_kernel<D, NH, FP16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
-  static_assert(C::kPerSm * C::kRows <= 48, "the workspace's parts");
-  kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), 32 * C::kWarps, C::kSmemBytes, stream>>>(tk, tv, p);
+  static_assert(C::kPerSm * C::kHeads <= 48, "the workspace's parts");
+  kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
   return launch_dependent(decode_join_kernel<D, FP16>, static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H), 128, 0,
-                          stream, p, C::kRows);
+                          stream, p, C::kHeads);
 }
 
 template <int D, bool FP16>
 cudaError_t launch_decode8_groups(const PagedDecodeArgs& a, cudaStream_t stream) {
-  const int group = a.H / a.c.Hkv;
-  if (group <= 8) return launch_decode8<D, 1, 1, FP16>(a, stream);
-  if (group <= 16) return launch_decode8<D, 1, 2, FP16>(a, stream);
-  return group <= 32 ? launch_decode8<D, 2, 2, FP16>(a, stream) : launch_decode8<D, 3, 2, FP16>(a, stream);
+  return a.H / a.c.Hkv <= 8 ? launch_decode8<D, 1, FP16>(a, stream) : launch_decode8<D, 2, FP16>(a, stream);
 }
 
 }  // namespace
