@@ -36,6 +36,7 @@ struct DecParams {
   float* part;               // [2 CTAs][rows][D + 2]: O, then m and l
   long long* offsets;        // [B + 1] tiles before each sequence, then the share
   int H, group, chunks, piece;
+  int two;                   // 1: a head unit is two key/value heads (8-bit cache, rows of up to 8 query heads for each)
   float scale_log2, cap_in, cap_out;
   CapPoly poly;              // factor cap_out
   const float* slopes;
@@ -79,6 +80,8 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 __device__ __forceinline__ int tiles_of(const PagedCache& c, int b, int tile) {
   return (tokens_of(c, b) + tile - 1) / tile;
 }
+
+__device__ __forceinline__ int units_of(const DecParams& p) { return p.two ? p.c.Hkv / 2 : p.c.Hkv * p.chunks; }
 
 // A place in the line of tiles: tile t of head unit u (key/value head and chunk) of
 // sequence b, with n tokens in T tiles.
@@ -180,8 +183,9 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = D / 32;
   const int hk = head / p.group, in_group = head % p.group;
-  const int u = hk * p.chunks + in_group / rows_per_part, row = in_group % rows_per_part;
-  const long long first = p.offsets[b], tiles = (p.offsets[b + 1] - first) / (p.c.Hkv * p.chunks);
+  const int u = p.two ? hk / 2 : hk * p.chunks + in_group / rows_per_part;
+  const int row = p.two ? 8 * (hk & 1) + in_group : in_group % rows_per_part;
+  const long long first = p.offsets[b], tiles = (p.offsets[b + 1] - first) / units_of(p);
   const long long share = p.offsets[p.c.B + 1];
   const long long w0 = first + u * tiles;
   uint16_t* dst = p.o + b * p.so.s[1] + head * p.so.s[0];

@@ -189,26 +189,28 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const __grid_constant__
 // with nothing in L2, for their arithmetic is the same and one CTA an SM hides less of it.)
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
-template <int D, int NH>
+template <int D, int NH, bool TWO>
 struct Dec8Cfg {
-  static constexpr int kHeads = 8 * NH;                      // query heads per chunk
+  static constexpr int kHeads = 8 * NH;                      // query heads per chunk (TWO: 8 of each key/value head)
+  static constexpr int kRow = TWO ? 2 * D : D;               // bytes of a tile's row
   static constexpr int kTile = 128;                          // tokens per tile
   static constexpr int kBlocksOfTile = kTile / 16;
-  static constexpr int kHalf = kTile * D;                    // K or V of a tile
+  static constexpr int kHalf = kTile * kRow;                 // K or V of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kPerSm = NH * D <= 128 ? 3 : 2;
+  static constexpr int kPerSm = NH * D <= 128 && !TWO ? 3 : 2;
   static constexpr int kStages = (kPerSm == 3 ? 65536 : 98304) / kStage;
-  static constexpr int kORow = D + (NH == 1 ? 8 : 0);        // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
+  static constexpr int kORow = D + (NH == 1 || TWO ? 8 : 0); // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
   static constexpr int kO = 4 * kHeads * kORow * 4;          // the warps' O, in a segment's last stage
   static constexpr int kQStride = D * 2 + 32;                // bytes; 8-byte loads of 4 rows meet every bank once
   static constexpr int kScaleOff = kStages * kStage;         // K's and V's scales of each stage
-  static constexpr int kQOff = kScaleOff + kStages * 2 * kBlocksOfTile * 4;
+  static constexpr int kQOff = kScaleOff + kStages * (TWO ? 4 : 2) * kBlocksOfTile * 4;
   static constexpr int kQsOff = kQOff + kHeads * kQStride;    // q's powers of two
   static constexpr int kMlOff = kQsOff + kHeads * 4;          // (m, l) of each warp's heads
   static constexpr int kBarOff = kMlOff + 4 * kHeads * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
-  static constexpr int kScaleLanes = 2 * kBlocksOfTile;
+  static constexpr int kScaleLanes = (TWO ? 4 : 2) * kBlocksOfTile;
+  static_assert(!TWO || (D == 64 && NH == 2), "rows of two heads");
   static_assert(kO <= kStage, "the warps' O fits a stage");
   static_assert(kQOff % 16 == 0 && kQsOff % 16 == 0 && kMlOff % 8 == 0 && kBarOff % 8 == 0 && kScaleLanes <= 32, "layout");
 };
@@ -229,18 +231,18 @@ __device__ __forceinline__ float2 ex2_pair(float2 x) { return make_float2(ex2_ap
 __device__ __forceinline__ float2 max_pair(float2 x, float2 y) { return make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y)); }
 __device__ __forceinline__ float2 minus(float2 x, float2 y) { return __fadd2_rn(x, make_float2(-y.x, -y.y)); }
 
-// Where the 16-byte piece `chunk` of a row of D codes stands in a tile that TMA swizzled in spans of min(D, 128) bytes.
-template <int D>
+// Where the 16-byte piece `chunk` of a row stands in a tile whose rows of 64 or 128 bytes TMA swizzled in spans of their length.
+template <int ROW>
 __device__ __forceinline__ uint32_t piece_of(int row, int chunk) {
-  if constexpr (D == 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
+  if constexpr (ROW == 128) return row * 128 + ((chunk ^ (row & 7)) << 4);
   else return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D, int NH, bool FP16>
-__global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
+template <int D, int NH, bool TWO, bool FP16>
+__global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ DecParams p) {
-  using C = Dec8Cfg<D, NH>;
+  using C = Dec8Cfg<D, NH, TWO>;
   constexpr int kTile = C::kTile, kHeads = C::kHeads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
   long long* s_sums = reinterpret_cast<long long*>(smem + C::kMlOff);
   int* s_start = reinterpret_cast<int*>(smem + C::kMiscOff + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = p.c.Hkv * p.chunks;
+  const int units = units_of(p);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -270,11 +272,11 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer warp
-    // Lane x: block x mod 8 of the tile, of K (x < 8) or V.  It fetches the block's scale, and if a piece (the tokens
-    // of one page in the tile) starts with its block, the piece's codes.  Past the sequence's end, and for a page index
+    // Lane x: block x mod 8 of the tile, of K (x / 8 even) or V, of the unit's second head from 16 on.  It fetches the block's scale,
+    // and lanes below 16, if a piece (the tokens of one page in the tile) starts with their block, the piece's codes.  Past the sequence's end, and for a page index
     // outside the cache, the page coordinate n_pages, out of bounds, fills the piece with zeros; such a
     // block's scale is 0.
-    const bool mine = lane < C::kScaleLanes, is_v = lane >= C::kBlocksOfTile;
+    const bool mine = lane < C::kScaleLanes, is_v = (lane / C::kBlocksOfTile) & 1;
     const int block = lane % C::kBlocksOfTile, per_page = p.c.page_size >> 4;
     const float* scales = is_v ? p.c.v_scales : p.c.k_scales;
     auto page_at = [&](const Place<kTile>& x, int& row) -> int {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
       if (mine && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + tok / p.c.page_size];
       return page < 0 || page >= p.c.n_pages ? p.c.n_pages : page;
     };
-    const bool starts = mine && block * 16 % p.piece == 0;
+    const bool starts = lane < 2 * C::kBlocksOfTile && block * 16 % p.piece == 0;
     int issued = 0, row;
     int page = page_at(at, row);
     bool ok = true;
@@ -294,10 +296,10 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
         break;
       if (lane == 0) mbar_arrive_expect_tx(&bar_full[slot], C::kStage);
       __syncwarp();
-      const int hk = at.u / p.chunks;
+      const int unit = TWO ? at.u : at.u / p.chunks, hk = TWO ? 2 * unit + lane / 16 : unit;
       if (starts)
-        tma_load_4d(smem + slot * C::kStage + (is_v ? C::kHalf : 0) + block * 16 * D, is_v ? &tm_v : &tm_k, &bar_full[slot],
-                    0, row, hk, page);
+        tma_load_4d(smem + slot * C::kStage + (is_v ? C::kHalf : 0) + block * 16 * C::kRow, is_v ? &tm_v : &tm_k, &bar_full[slot],
+                    0, row, unit, page);
       if (mine) {
         const bool real = page < p.c.n_pages;
         const float* src = scales + (real ? (static_cast<long long>(page) * p.c.Hkv + hk) * per_page + (row >> 4) : 0);
@@ -335,28 +337,33 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
   constexpr int kQPer = (kPieces + 127) / 128;          // a thread
   uint4 q_next[kQPer];
   float2 slope_next[NH];
-  auto rows_of = [&](const Place<kTile>& x) { return min(p.group - (x.u % p.chunks) * kHeads, kHeads); };
-  auto head_of = [&](const Place<kTile>& x) { return (x.u / p.chunks) * p.group + (x.u % p.chunks) * kHeads; };
+  // The query head of row r of a unit, or -1.  (TWO: eight rows for each of the two key/value heads, p.group of them real.)
+  auto head_of = [&](const Place<kTile>& x, int r) {
+    if constexpr (TWO) return (r & 7) < p.group ? (2 * x.u + (r >> 3)) * p.group + (r & 7) : -1;
+    const int in_group = (x.u % p.chunks) * kHeads + r;
+    return in_group < p.group ? (x.u / p.chunks) * p.group + in_group : -1;
+  };
   auto fetch_q = [&](const Place<kTile>& x) {
-    const int head0 = head_of(x), rows = rows_of(x);
 #pragma unroll
     for (int i = 0; i < kQPer; ++i) {
       const int y = threadIdx.x + i * 128, r = y / (D / 8), c = y % (D / 8);
+      const int head = y < kPieces ? head_of(x, r) : -1;
       q_next[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows)
-        q_next[i] = *reinterpret_cast<const uint4*>(p.q + x.b * p.sq.s[1] + (head0 + r) * p.sq.s[0] + c * 8);
+      if (head >= 0) q_next[i] = *reinterpret_cast<const uint4*>(p.q + x.b * p.sq.s[1] + head * p.sq.s[0] + c * 8);
     }
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      const int r = 8 * h + gc;
-      slope_next[h].x = p.slopes && r < rows ? p.slopes[head0 + r] * -kLog2e : 0.f;
-      slope_next[h].y = p.slopes && r + 1 < rows ? p.slopes[head0 + r + 1] * -kLog2e : 0.f;
+      slope_next[h] = pair(0.f);
+      if (p.slopes) {
+        const int one = head_of(x, 8 * h + gc), two = head_of(x, 8 * h + gc + 1);
+        if (one >= 0) slope_next[h].x = p.slopes[one] * -kLog2e;
+        if (two >= 0) slope_next[h].y = p.slopes[two] * -kLog2e;
+      }
     }
   };
   fetch_q(at);
   for (long long w = w0; w < w1;) {
     // ---- a segment: tiles [at.t, at.t + count) of one head unit
-    const int head0 = head_of(at), rows = rows_of(at);
     const int count = static_cast<int>(min(static_cast<long long>(at.T - at.t), w1 - w));
     const bool whole = count == at.T;
     float2 slope2[NH];
@@ -393,10 +400,13 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
     auto load_q = [&](int h, int kk) {
       return *reinterpret_cast<const uint2*>(s_q + (8 * h + gr) * C::kQStride + kk * 32 + 4 * gc);
     };
-    uint2 qf[NH == 1 ? D / 16 : 1];
-    if constexpr (NH == 1) {
+    constexpr bool kHoldQ = NH * D <= 128;  // in registers
+    uint2 qf[kHoldQ ? NH : 1][kHoldQ ? D / 16 : 1];
+    if constexpr (kHoldQ) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) qf[kk] = load_q(0, kk);
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) qf[h][kk] = load_q(h, kk);
     }
     float o[D / 16][NH][4];  // columns 2 gr and 2 gr + 1 of 16 for heads gc, gc + 1: {even, head gc}, {even, gc + 1}, {odd, gc}, ...
     float2 m[NH], mv[NH], l[NH], to_log2[NH];  // of heads gc and gc + 1; l over this thread's tokens
@@ -421,41 +431,46 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
         // S^T = K Q^T of two blocks of 16 tokens.
         float s[2][NH][4] = {};
 #pragma unroll
-        for (int c2 = 0; c2 < D / 32; ++c2) {
+        for (int c2 = 0; c2 < C::kRow / 32; ++c2) {
           uint32_t b4[2][4];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) ldsm4(b4[nb], kb + piece_of<D>(frow + 16 * nb, 2 * c2 + fchunk));
+          for (int nb = 0; nb < 2; ++nb) ldsm4(b4[nb], kb + piece_of<C::kRow>(frow + 16 * nb, 2 * c2 + fchunk));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int kk = 2 * c2 + half;
+            // The columns of 16 codes, of all of q's heads or (TWO) of the row's first or second key/value head.
+            const int kk = (2 * c2 + half) % (D / 16), only = TWO ? c2 / (D / 32) : -1;
             uint2 b[NH];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) b[h] = NH == 1 ? qf[NH == 1 ? kk : 0] : load_q(h, kk);
+            for (int h = 0; h < NH; ++h) b[h] = kHoldQ ? qf[kHoldQ ? h : 0][kHoldQ ? kk : 0] : load_q(h, kk);
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
               const uint32_t x = b4[nb][2 * half], y = b4[nb][2 * half + 1];
               const uint32_t a4[4] = {codes_to_half2(x), codes_to_half2(y), codes_to_half2(x >> 16), codes_to_half2(y >> 16)};
 #pragma unroll
-              for (int h = 0; h < NH; ++h) mma_half(s[nb][h], a4, b[h].x, b[h].y);
+              for (int h = 0; h < NH; ++h)
+                if (!TWO || h == only) mma_half(s[nb][h], a4, b[h].x, b[h].y);
             }
           }
         }
         // Scales; a block past the end has whatever its page holds there.
         const bool ragged = key0 + 32 > at.n;
-        float ks[2], lgv[2];
+        constexpr int kKv = TWO ? 2 : 1;
+        float ks[2][kKv], lgv[2][kKv];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          const bool inside = key0 + 16 * nb < at.n;
-          ks[nb] = inside ? sc[nb] : 0.f;
-          lgv[nb] = inside ? __log2f(sc[C::kBlocksOfTile + nb]) : 0.f;
-        }
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int h = 0; h < kKv; ++h) {
+            const bool inside = key0 + 16 * nb < at.n;
+            ks[nb][h] = inside ? sc[2 * h * C::kBlocksOfTile + nb] : 0.f;
+            lgv[nb][h] = inside ? __log2f(sc[(2 * h + 1) * C::kBlocksOfTile + nb]) : 0.f;
+          }
         // Scores in log2 units: x[block][h][token gr or gr + 8], of heads gc and gc + 1.
         float2 x[2][NH][2];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
-            const float2 f = __fmul2_rn(to_log2[h], pair(ks[nb]));
+            const float2 f = __fmul2_rn(to_log2[h], pair(ks[nb][TWO ? h : 0]));
             x[nb][h][0] = __fmul2_rn(make_float2(s[nb][h][0], s[nb][h][1]), f);
             x[nb][h][1] = __fmul2_rn(make_float2(s[nb][h][2], s[nb][h][3]), f);
           }
@@ -500,7 +515,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
           sum[h] = pair(0.f);
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb) {
-            const float2 to_v = __fadd2_rn(minus(m[h], mv[h]), pair(lgv[nb])), by = ex2_pair(to_v);
+            const float2 to_v = __fadd2_rn(minus(m[h], mv[h]), pair(lgv[nb][TWO ? h : 0])), by = ex2_pair(to_v);
             fits = fits && to_v.x <= 100.f && to_v.y <= 100.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -521,7 +536,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
             for (int nb = 0; nb < 2; ++nb) {
               const float2 top = max_pair(x[nb][h][0], x[nb][h][1]);
               mx = max_pair(mx, top);
-              mxv = max_pair(mxv, __fadd2_rn(top, pair(lgv[nb])));
+              mxv = max_pair(mxv, __fadd2_rn(top, pair(lgv[nb][TWO ? h : 0])));
             }
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) {
@@ -547,7 +562,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 sum[h] = __fadd2_rn(sum[h], ex2_pair(minus(x[nb][h][e], mx)));
-                const float2 v = ex2_pair(__fadd2_rn(x[nb][h][e], minus(pair(lgv[nb]), mxv)));
+                const float2 v = ex2_pair(__fadd2_rn(x[nb][h][e], minus(pair(lgv[nb][TWO ? h : 0]), mxv)));
                 pf[nb][h][e] = pack2<true>(v.x, v.y);
               }
           }
@@ -568,9 +583,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
           const uint32_t keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
           const uint32_t keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int c2 = 0; c2 < D / 32; ++c2) {
+          for (int c2 = 0; c2 < C::kRow / 32; ++c2) {
             uint32_t b4[4];
-            ldsm4_t(b4, vb + piece_of<D>(frow + 16 * nb, 2 * c2 + fchunk));
+            ldsm4_t(b4, vb + piece_of<C::kRow>(frow + 16 * nb, 2 * c2 + fchunk));
             if (ragged) {
               b4[0] &= keep0;
               b4[1] &= keep1;
@@ -582,7 +597,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
               const uint32_t u = __byte_perm(b4[2 * half], 0, 0x3120), v = __byte_perm(b4[2 * half + 1], 0, 0x3120);
               const uint32_t a4[4] = {codes_to_half2(u), codes_to_half2(u >> 16), codes_to_half2(v), codes_to_half2(v >> 16)};
 #pragma unroll
-              for (int h = 0; h < NH; ++h) mma_half(o[2 * c2 + half][h], a4, pf[nb][h][0], pf[nb][h][1]);
+              for (int h = 0; h < NH; ++h)
+                if (!TWO || h == c2 / (D / 32)) mma_half(o[(2 * c2 + half) % (D / 16)][h], a4, pf[nb][h][0], pf[nb][h][1]);
             }
           }
         }
@@ -629,7 +645,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
     consumers_sync();
     constexpr int kThreadsOfRow = 128 / kHeads;
     const int r = threadIdx.x / kThreadsOfRow, in_row = threadIdx.x % kThreadsOfRow;
-    if (r < rows) {
+    const int head = head_of(at, r);
+    if (head >= 0) {
       float M = kNoScore, L = 0.f, wgt[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) M = fmaxf(M, s_ml[x * kHeads + r].x);
@@ -640,7 +657,6 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
         L += ml.y * wgt[x];
       }
       const float inv = whole ? 1.f / L : 1.f;
-      const int head = head0 + r;
 #pragma unroll
       for (int c = 0; c < D / (4 * kThreadsOfRow); ++c) {
         const int col = 4 * (in_row + kThreadsOfRow * c);
@@ -679,23 +695,25 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH>::kPerSm)
   }
 }
 
-template <int D, int NH, bool FP16>
+template <int D, int NH, bool TWO, bool FP16>
 cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
-  using C = Dec8Cfg<D, NH>;
-  const DecParams p = decode_params(a, C::kHeads, C::kTile);
+  using C = Dec8Cfg<D, NH, TWO>;
+  DecParams p = decode_params(a, C::kHeads, C::kTile);
+  p.two = TWO;
   CUtensorMap tk, tv;
   cudaError_t e;
-  constexpr auto kSwizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  constexpr auto kSwizzle = C::kRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   // L2 fetches no more than a row where the rows of a head lie apart (fa_paged.cu).
   auto map = [&](CUtensorMap* t, const void* x, const Strides& s) {
-    const auto fetch = s.s[0] == D ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                   : D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
-    return make_tmap_4d(t, x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, a.c.page_size, a.c.Hkv, a.c.n_pages, s.s, D, p.piece,
-                        kSwizzle, fetch);
+    const auto fetch = s.s[0] == C::kRow ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : C::kRow == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+    const int64_t strides[3] = {s.s[0], TWO ? 2 * s.s[1] : s.s[1], s.s[2]};
+    return make_tmap_4d(t, x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C::kRow, a.c.page_size, TWO ? a.c.Hkv / 2 : a.c.Hkv, a.c.n_pages,
+                        strides, C::kRow, p.piece, kSwizzle, fetch);
   };
   if ((e = map(&tk, a.c.k, a.c.sk))) return e;
   if ((e = map(&tv, a.c.v, a.c.sv))) return e;
-  auto kern = decode_fp8_kernel<D, NH, FP16>;
+  auto kern = decode_fp8_kernel<D, NH, TWO, FP16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
   static_assert(C::kPerSm * C::kHeads <= 48, "the workspace's parts");
   kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
@@ -705,8 +723,15 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
 }
 
 template <int D, bool FP16>
-cudaError_t launch_decode8_groups(const PagedDecodeArgs& a, cudaStream_t stream) {
-  return a.H / a.c.Hkv <= 8 ? launch_decode8<D, 1, FP16>(a, stream) : launch_decode8<D, 2, FP16>(a, stream);
+cudaError_t launch_decode8_heads(const PagedDecodeArgs& a, cudaStream_t stream) {
+  if (a.H / a.c.Hkv > 8) return launch_decode8<D, 2, false, FP16>(a, stream);
+  if constexpr (D == 64) {
+    // Rows of 64 bytes that lie apart, each beside the next head's: two heads a unit, whose rows of 128 bytes HBM reads faster.
+    const Strides &k = a.c.sk, &v = a.c.sv;
+    if (a.c.Hkv % 2 == 0 && k.s[1] == D && v.s[1] == D && k.s[0] >= 2 * D && v.s[0] >= 2 * D)
+      return launch_decode8<D, 2, true, FP16>(a, stream);
+  }
+  return launch_decode8<D, 1, false, FP16>(a, stream);
 }
 
 }  // namespace
@@ -723,8 +748,8 @@ cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t strea
 }
 
 cudaError_t launch_paged_decode_fp8(const PagedDecodeArgs& a, cudaStream_t stream) {
-  if (a.c.d == 64) return a.fp16 ? launch_decode8_groups<64, true>(a, stream) : launch_decode8_groups<64, false>(a, stream);
-  return a.fp16 ? launch_decode8_groups<128, true>(a, stream) : launch_decode8_groups<128, false>(a, stream);
+  if (a.c.d == 64) return a.fp16 ? launch_decode8_heads<64, true>(a, stream) : launch_decode8_heads<64, false>(a, stream);
+  return a.fp16 ? launch_decode8_heads<128, true>(a, stream) : launch_decode8_heads<128, false>(a, stream);
 }
 
 }  // namespace fa

@@ -126,6 +126,17 @@ def test_decode(case, layout):
     report(f"decode fp8 {case} {layout} (shares of the bounds)", o=o, lse=lse)
 
 
+@pytest.mark.parametrize("case", [([300, 0, 77, 129, 1], 10, 10, 64, 32, torch.bfloat16, 30.0, True),
+                                  ([1000, 2001], 20, 4, 64, 16, torch.float16, 0.0, True),
+                                  ([640, 5], 48, 6, 64, 128, torch.bfloat16, 0.0, False),
+                                  ([640, 5], 9, 3, 64, 48, torch.bfloat16, 0.0, True),
+                                  ([200, 131], 36, 4, 64, 48, torch.float16, 20.0, False)], ids=str)
+@pytest.mark.parametrize("garbage", [False, True])
+def test_rows_of_two_heads(case, garbage):
+    # Heads of 64 beside each other: two of them a unit where there are an even number and up to eight query heads each.
+    _decode(case, "nhd", garbage)
+
+
 @pytest.mark.parametrize("case", [CASES[2], CASES[3], CASES[4], CASES[5], CASES[7]], ids=str)
 def test_what_lies_behind_the_last_token_does_not_matter(case):
     _decode(case, "nhd", True)
