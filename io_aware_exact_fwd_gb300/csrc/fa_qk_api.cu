@@ -121,6 +121,7 @@ int fa_qk_norm_rope_bwd(const void* q, const int64_t* q_strides, const void* k, 
   }
   fa::CallContext c;
   if ((st = fa::call_context(&c)) != FA_OK) return st;
+  if (vs < 0) B = 0;  // no rows: the weights' gradients are 0
   a.q = q;
   a.k = k;
   a.dq_in = dq_out;

@@ -7,8 +7,14 @@
 // and back, with g the outputs' gradient turned by the opposite angles and h = w g:
 //   dx = r (h - x r mean(h x r)),  dw = sum over rows of g x r.
 //
-// Bound by HBM: 4 bytes a value forward, 6 backward, against 10 to 20 operations.  The angles are what could cost more: a sine and a cosine
-// for each pair and token, so a block makes them once for its tokens, in shared memory, for all their heads.
+// Bound by HBM: 4 bytes a value forward, 6 backward, against 10 to 20 operations.
+//
+// Work.  A warp takes a token (or, where there are few heads, some) with all its heads, q's and then k's: the angles' sines and
+// cosines, the costliest part, are made once for them and stay in registers, as do the weights.  Rows stream through the warp: each lane
+// copies its pieces of the next kDepth rows into places of its own in shared memory (cp.async: HBM's latency at full rate takes
+// more bytes on the way than registers could wait for), over the ends of sides and tokens.  (A block that shares its
+// tokens' angles in shared memory and reads them for every row: 62 us for 16384 tokens of 40 heads x 128, the
+// reads' bank conflicts being most of it.)
 //
 // Angles.  position * inv_freq in fp32 would lose all but a few bits of the angle at far positions.  An angle counts only
 // modulo one turn, so the frequency is held in turns a token as a 64-bit fraction, made from inv_freq (a 24-bit integer times
@@ -74,60 +80,39 @@ __device__ __forceinline__ float2 turn(uint64_t turns, int position) {
   return cs;
 }
 
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// Eight 16-bit values as four pairs.
 template <bool FP16>
-__device__ __forceinline__ void unpack8(const uint4& u, float* x) {
+__device__ __forceinline__ void unpack8(const uint4& u, float2* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float2 f;
-    if constexpr (FP16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-    else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
+    if constexpr (FP16) x[j] = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    else x[j] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
   }
 }
 template <bool FP16>
-__device__ __forceinline__ uint4 pack8(const float* x) {
+__device__ __forceinline__ uint4 pack8(const float2* x) {
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (FP16) {
-      const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+      const __half2 h = __floats2half2_rn(x[j].x, x[j].y);
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      w[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+      w[j] = pack_bf16x2(x[j].x, x[j].y);
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int type, int i) {
-  if (type == 0) return static_cast<const float*>(w)[i];
-  const uint16_t u = static_cast<const uint16_t*>(w)[i];
+  if (type == 0) return __ldg(static_cast<const float*>(w) + i);
+  const uint16_t u = __ldg(static_cast<const uint16_t*>(w) + i);
   if (type == 1) return __uint_as_float(static_cast<uint32_t>(u) << 16);
   return __half2float(__ushort_as_half(u));
 }
-
-// A row's layout in its lanes.
-template <int D>
-struct Rows {
-  static constexpr int kLanes = D / 16;                  // of a row
-  static constexpr int kGroups = kQkThreads / kLanes;    // rows at once
-  int lane, group, c0, c1;                               // this thread's place in its row, its row, the columns of its two pieces
-  bool turned;
-  __device__ __forceinline__ explicit Rows(const QkArgs& a) {
-    lane = threadIdx.x % kLanes;
-    group = threadIdx.x / kLanes;
-    turned = lane < a.rot / 16;
-    if (a.pairs || !turned) {
-      c0 = 16 * lane;  // (past the rotated columns the pieces of both kinds follow each other)
-      c1 = c0 + 8;
-    } else {
-      c0 = 8 * lane;
-      c1 = c0 + a.rot / 2;
-    }
-  }
-};
 
 template <int D>
 __device__ __forceinline__ float row_sum(float x) {
@@ -135,302 +120,357 @@ __device__ __forceinline__ float row_sum(float x) {
   for (int w = 1; w < D / 16; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
   return x;
 }
+__device__ __forceinline__ float dot16(const float2 (&x)[8], const float2 (&y)[8]) {
+  float2 s = __fmul2_rn(x[0], y[0]), t = __fmul2_rn(x[1], y[1]);
+#pragma unroll
+  for (int j = 2; j < 8; j += 2) {
+    s = __ffma2_rn(x[j], y[j], s);
+    t = __ffma2_rn(x[j + 1], y[j + 1], t);
+  }
+  s = __fadd2_rn(s, t);
+  return s.x + s.y;
+}
 
-// x[16] of a lane: the pairs (x[j], x[8 + j]), or with PAIRS (x[2j], x[2j + 1]), turned by (c[j], s[j]).
+// How the rows are divided: a warp takes at once `heads` heads (a power of two) of 32 / (D / 16) / heads tokens; the warps of one
+// token's slices take its heads in turns.
+struct QkGrid {
+  int heads, slices;
+  Div per_row;    // by N
+  int step;       // heads * slices
+  int rows[2];    // of q's and k's heads that a slice takes, at most: heads / step, rounded up
+};
+// The rows of a side that this block takes: where there are few tokens, blocks are for q (blockIdx.y = 0) or for k.
+__device__ __forceinline__ int rows_of(const QkGrid& g, int side) {
+  return gridDim.y == 1 || static_cast<int>(blockIdx.y) == side ? g.rows[side] : 0;
+}
+
+// Cosines, sines and their negatives of this lane's eight pairs (1 and 0 where its columns are not rotated), in pairs.
+struct Angles {
+  float2 c[4], s[4], ns[4];
+};
+// x[8] of a lane turned by them: the pairs are its first piece's values with its second's, or with PAIRS the two of
+// each x[j].
 template <bool PAIRS>
-__device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], const float (&s)[8], float sign) {
+__device__ __forceinline__ void rotate(float2 (&x)[8], const Angles& g) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (PAIRS) {
+      float2 &u = x[2 * j], &v = x[2 * j + 1];
+      u = make_float2(u.x * g.c[j].x - u.y * g.s[j].x, u.x * g.s[j].x + u.y * g.c[j].x);
+      v = make_float2(v.x * g.c[j].y - v.y * g.s[j].y, v.x * g.s[j].y + v.y * g.c[j].y);
+    } else {
+      const float2 u = x[j], v = x[4 + j];
+      x[j] = __ffma2_rn(v, g.ns[j], __fmul2_rn(u, g.c[j]));
+      x[4 + j] = __ffma2_rn(u, g.s[j], __fmul2_rn(v, g.c[j]));
+    }
+  }
+}
+
+// 16 bytes of a row (bytes = 16) or of zeros (0) to this lane's own place in shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint16_t* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups of this lane's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+constexpr int kDepth = 4;  // rows on the way
+constexpr int kForwardBlocksPerSm = 2, kBackBlocksPerSm = 2;
+
+// This thread's part: its place in its row's lanes and the columns of its two pieces; its row's head and token among the warp's.
+template <int D>
+struct Lane {
+  static constexpr int kLanes = D / 16, kGroups = 32 / kLanes;  // lanes of a row, rows of a warp
+  int lane, c0, c1, head, token;
+  __device__ __forceinline__ Lane(const QkArgs& a, const QkGrid& g) {
+    const int x = threadIdx.x & 31, group = x / kLanes;
+    lane = x % kLanes;
+    if (a.pairs || lane >= a.rot / 16) {
+      c0 = 16 * lane;  // (past the rotated columns the pieces of both kinds follow each other)
+      c1 = c0 + 8;
+    } else {
+      c0 = 8 * lane;
+      c1 = c0 + a.rot / 2;
+    }
+    head = group & (g.heads - 1);
+    token = group / g.heads;
+  }
+};
+
+// The rows that a warp takes, in order: token by token (of a step between them), side by side (q, k), heads in steps.
+// Fetching runs kDepth - 1 rows ahead of the work.
+template <int D, bool BACK>
+struct Fetch {
+  static constexpr int kParts = BACK ? 4 : 2;  // pieces a lane: of x, and of the gradient
+  static constexpr uint32_t kSlot = kParts * kQkThreads * 16;
+  const QkArgs& a;
+  const QkGrid& g;
+  const Lane<D>& me;
+  uint32_t begin, to;      // shared memory: this lane's place of slot 0, and of the slot to fill
+  int all, token_step, head;
+  int token, side;         // of the rows to fetch next
+  int left, real;          // of this side: rows that the warp takes, and rows that this lane has
+  const uint16_t *x, *dy;  // the next one's first piece
+  __device__ __forceinline__ Fetch(const QkArgs& a_, const QkGrid& g_, const Lane<D>& me_, const void* ring, int first, int step,
+                                   int slice)
+      : a(a_), g(g_), me(me_), begin(smem_u32(ring) + threadIdx.x * 16), to(begin), all(a_.B * a_.N), token_step(step),
+        head(slice * g_.heads + me_.head), token(first + me_.token), side(-1) {
+    next_side();
+#pragma unroll 1
+    for (int i = 0; i < kDepth - 1; ++i) row();
+  }
+  __device__ __forceinline__ void next_side() {
+    do {
+      if (++side == 2) {
+        side = 0;
+        token += token_step;
+      }
+      left = rows_of(g, side);
+    } while (left == 0);  // (a block without rows does not come here)
+    // Heads head, head + step, ... of this side: as many rows as the warp takes, or one less.
+    real = token < all ? left - (head + (left - 1) * g.step < (side ? a.Hkv : a.H) ? 0 : 1) : 0;
+    const int at = min(token, all - 1), b = g.per_row(at), n = at - b * a.N;
+    auto start = [&](const void* base, const Strides& s) {
+      return static_cast<const uint16_t*>(base) + (b * s.s[2] + n * s.s[0] + head * s.s[1] + me.c0);
+    };
+    if (!BACK || a.norm) x = side ? start(a.k, a.sk) : start(a.q, a.sq);
+    if constexpr (BACK) dy = side ? start(a.dk_in, a.sdk_in) : start(a.dq_in, a.sdq_in);
+  }
+  // Asks for a row (for zeros where this lane has none) and goes to the next.
+  __device__ __forceinline__ void row() {
+    const uint32_t bytes = real > 0 ? 16 : 0;
+    if (!BACK || a.norm) {
+      copy16(to, x, bytes);
+      copy16(to + 16 * kQkThreads, x + (me.c1 - me.c0), bytes);
+      x += (side ? a.sk : a.sq).s[1] * g.step;
+    }
+    if constexpr (BACK) {
+      copy16(to + 32 * kQkThreads, dy, bytes);
+      copy16(to + 48 * kQkThreads, dy + (me.c1 - me.c0), bytes);
+      dy += (side ? a.sdk_in : a.sdq_in).s[1] * g.step;
+    }
+    copies_end();
+    to = to == begin + (kDepth - 1) * kSlot ? begin : to + kSlot;
+    --real;
+    if (--left == 0) next_side();
+  }
+};
+
+// The angles of a warp's tokens: each lane makes those of one or two pairs, all read theirs.
+template <int D>
+struct Turns {
+  static constexpr int kPairs = D / 2, kOwn = kPairs / 32;
+  uint64_t turns[kOwn];
+  __device__ __forceinline__ explicit Turns(const QkArgs& a) {
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      turns[k] = i < a.rot / 2 ? turns_of(__ldg(a.inv_freq + i)) : 0;  // (0: cos = 1, sin = 0)
+    }
+  }
+  template <bool BACK>
+  __device__ __forceinline__ Angles of(const QkArgs& a, const QkGrid& g, const Lane<D>& me, float2* mine, int first) const {
+    constexpr int kMost = Lane<D>::kGroups;
+    const int all = a.B * a.N, tokens = kMost / g.heads, lane = threadIdx.x & 31;
+    int pos[kMost];
+#pragma unroll
+    for (int t = 0; t < kMost; ++t) {
+      const int at = min(first + t, all - 1);
+      if (t < tokens) pos[t] = a.positions ? __ldg(a.positions + at) : at - g.per_row(at) * a.N;
+    }
+    __syncwarp();  // every lane has read the angles before
+#pragma unroll
+    for (int t = 0; t < kMost; ++t)
+      if (t < tokens) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) mine[t * kPairs + lane + 32 * k] = turn(turns[k], pos[t]);
+      }
+    __syncwarp();
+    const float4* from = reinterpret_cast<const float4*>(mine + me.token * kPairs + 8 * me.lane);
+    Angles r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 y = from[j];
+      r.c[j] = make_float2(y.x, y.z);
+      r.s[j] = BACK ? make_float2(-y.y, -y.w) : make_float2(y.y, y.w);
+      r.ns[j] = make_float2(-r.s[j].x, -r.s[j].y);
+    }
+    return r;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_weights(const QkArgs& a, const Lane<D>& me, int side, float2 (&w)[8]) {
+  const void* from = side ? a.k_weight : a.q_weight;
+  if (!from) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = twice(1.f);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float &a = x[PAIRS ? 2 * j : j], &b = x[PAIRS ? 2 * j + 1 : 8 + j];
-    const float sj = sign * s[j], y = a * c[j] - b * sj;
-    b = a * sj + b * c[j];
-    a = y;
+    const int c = j < 4 ? me.c0 + 2 * j : me.c1 + 2 * (j - 4);
+    w[j] = make_float2(weight_at(from, a.weight_type, c), weight_at(from, a.weight_type, c + 1));
   }
 }
 
-constexpr int kMostTokens = 8;  // of a tile
-
+// This lane's first piece of its slice's first head in token first + me.token (the last there is, if none) of an output.
 template <int D>
-struct Angles {
-  float c[kMostTokens][D / 2], s[kMostTokens][D / 2];
-};
-// Of tokens first .. first + tokens of the line of all.
-template <int D>
-__device__ __forceinline__ void make_angles(Angles<D>& x, const QkArgs& a, const Div& per_row, int first, int tokens) {
-  const int half = a.rot / 2;
-  for (int y = threadIdx.x; y < tokens * half; y += kQkThreads) {
-    const int t = y / half, i = y % half, at = first + t;
-    const int pos = a.positions ? __ldg(a.positions + at) : at - per_row(at) * a.N;
-    const float2 cs = turn(turns_of(__ldg(a.inv_freq + i)), pos);
-    x.c[t][i] = cs.x;
-    x.s[t][i] = cs.y;
-  }
-}
-template <int D>
-__device__ __forceinline__ void angles_of(const Angles<D>& x, const Rows<D>& me, int t, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    const float4 y = *reinterpret_cast<const float4*>(&x.c[t][8 * me.lane + j]);
-    const float4 z = *reinterpret_cast<const float4*>(&x.s[t][8 * me.lane + j]);
-    c[j] = me.turned ? y.x : 1.f;
-    c[j + 1] = me.turned ? y.y : 1.f;
-    c[j + 2] = me.turned ? y.z : 1.f;
-    c[j + 3] = me.turned ? y.w : 1.f;
-    s[j] = me.turned ? z.x : 0.f;
-    s[j + 1] = me.turned ? z.y : 0.f;
-    s[j + 2] = me.turned ? z.z : 0.f;
-    s[j + 3] = me.turned ? z.w : 0.f;
-  }
+__device__ __forceinline__ uint16_t* out_row(const QkArgs& a, const QkGrid& g, const Lane<D>& me, int first, int side, int slice) {
+  const int at = min(first + me.token, a.B * a.N - 1), b = g.per_row(at), n = at - b * a.N;
+  const Strides& s = side ? a.sk_out : a.sq_out;
+  return static_cast<uint16_t*>(side ? a.k_out : a.q_out) +
+         (b * s.s[2] + n * s.s[0] + (slice * g.heads + me.head) * s.s[1] + me.c0);
 }
 
-template <int D>
-__device__ __forceinline__ void make_weights(float (&w)[2][D], const QkArgs& a) {
-  for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
-    const void* from = x < D ? a.q_weight : a.k_weight;
-    w[x / D][x % D] = from ? weight_at(from, a.weight_type, x % D) : 1.f;
+// Where a warp begins and what it takes.
+struct Share {
+  int slice, begin, step;
+  bool any;
+  __device__ __forceinline__ Share(const QkGrid& g, int tokens, int all) {
+    const int unit = blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5), units = gridDim.x * (kQkThreads / 32);
+    const int lines = units / g.slices;  // warps that take the same slice
+    begin = unit / g.slices;
+    slice = unit - begin * g.slices;
+    any = begin < lines;
+    begin *= tokens;
+    step = lines * tokens;
+    any = any && begin < all && (rows_of(g, 0) > 0 || rows_of(g, 1) > 0);
   }
-}
-template <int D>
-__device__ __forceinline__ void weights_of(const float (&in)[2][D], const Rows<D>& me, int side, float (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(&in[side][me.c0 + j]);
-    const float4 y = *reinterpret_cast<const float4*>(&in[side][me.c1 + j]);
-    w[j] = x.x;
-    w[j + 1] = x.y;
-    w[j + 2] = x.z;
-    w[j + 3] = x.w;
-    w[8 + j] = y.x;
-    w[9 + j] = y.y;
-    w[10 + j] = y.z;
-    w[11 + j] = y.w;
-  }
-}
-
-// How the grid divides the rows: tiles of `tokens` tokens and (forward) `heads` heads of q's and k's in one line.
-struct QkGrid {
-  int tokens, heads, slices;
-  bool heads_first;  // rows that follow each other are heads of a token
-  Div per_row;       // by N
 };
 
-// The rows of a tile and some heads, kGroups at a time: this thread's place among them, with no division after the first.
-struct Walk {
-  int minor, major, minors, majors, step_minor, step_major;
-  __device__ __forceinline__ void start(int group, int groups, int tokens, int heads, bool heads_first) {
-    minors = heads_first ? heads : tokens;
-    majors = heads_first ? tokens : heads;
-    minor = group % minors;
-    major = group / minors;
-    step_minor = groups % minors;
-    step_major = groups / minors;
-  }
-  __device__ __forceinline__ void step() {
-    minor += step_minor;
-    major += step_major;
-    if (minor >= minors) {
-      minor -= minors;
-      ++major;
-    }
-  }
-  __device__ __forceinline__ bool real() const { return major < majors; }
-};
-
-__device__ __forceinline__ long long row_at(const Strides& s, int b, int n, int h) {
-  return b * s.s[2] + n * s.s[0] + h * s.s[1];
-}
-
-// Two pieces of a row.
-struct Raw {
-  uint4 a, b;
-};
-__device__ __forceinline__ Raw load_row(const void* base, long long at, int c0, int c1) {
-  const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-  return Raw{__ldcs(reinterpret_cast<const uint4*>(p + c0)), __ldcs(reinterpret_cast<const uint4*>(p + c1))};
-}
-
-// The forward.  A block's rows stream through its threads, the next ones' loads in flight while this one is worked on; the
-// first are requested before the angles are made.
 template <int D, bool FP16, bool PAIRS>
-__global__ void __launch_bounds__(kQkThreads, 4) qk_forward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
-  __shared__ __align__(16) Angles<D> angles;
-  __shared__ __align__(16) float weights[2][D];
-  using R = Rows<D>;
-  const R me(a);
-  const int tile = blockIdx.x / g.slices, first = tile * g.tokens, tokens = min(g.tokens, a.B * a.N - first);
-  const int h0 = (blockIdx.x - tile * g.slices) * g.heads, heads = min(g.heads, a.H + a.Hkv - h0);
-  Walk at;
-  at.start(me.group, R::kGroups, tokens, heads, g.heads_first);
-  // A row: its token in the tile, whether it is k's, its head there; and its pieces.
-  struct Row {
-    int t, side, head, b, n;
-    bool real;
-  };
-  auto here = [&]() {
-    Row r;
-    r.real = at.real();
-    const int minor = r.real ? at.minor : 0, major = r.real ? at.major : 0;
-    r.t = g.heads_first ? major : minor;
-    const int h = h0 + (g.heads_first ? minor : major);
-    r.side = h >= a.H;
-    r.head = r.side ? h - a.H : h;
-    r.b = g.per_row(first + r.t);
-    r.n = first + r.t - r.b * a.N;
-    return r;
-  };
-  auto load = [&](const Row& r) {
-    return load_row(r.side ? a.k : a.q, row_at(r.side ? a.sk : a.sq, r.b, r.n, r.head), me.c0, me.c1);
-  };
-  Row row = here();
-  Raw raw = load(row);
-  make_angles<D>(angles, a, g.per_row, first, tokens);
-  make_weights<D>(weights, a);
-  __syncthreads();
-  for (int r0 = 0, rows = tokens * heads; r0 < rows; r0 += R::kGroups) {  // (a whole warp goes through: the sums are shuffles)
-    at.step();
-    const Row next = here();
-    Raw ahead = raw;
-    if (r0 + R::kGroups < rows) ahead = load(next);
-    float x[16];
-    unpack8<FP16>(raw.a, x);
-    unpack8<FP16>(raw.b, x + 8);
-    if (a.norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
-      const float r_norm = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-      float w[16];
-      weights_of<D>(weights, me, row.side, w);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] *= r_norm * w[j];
-    }
-    float c[8], s[8];
-    angles_of<D>(angles, me, row.t, c, s);
-    rotate<PAIRS>(x, c, s, 1.f);
-    if (row.real) {
-      uint16_t* out = static_cast<uint16_t*>(row.side ? a.k_out : a.q_out) +
-                      row_at(row.side ? a.sk_out : a.sq_out, row.b, row.n, row.head);
-      *reinterpret_cast<uint4*>(out + me.c0) = pack8<FP16>(x);
-      *reinterpret_cast<uint4*>(out + me.c1) = pack8<FP16>(x + 8);
-    }
-    row = next;
-    raw = ahead;
-  }
-}
-
-// The gradient.  Blocks stay on the GPU and take tiles of tokens in turn, so that the weights' gradients add up in a thread; each block's
-// sums go to the workspace and a second kernel adds them in order: the same bits on every run.  Rows stream as in the forward, over the
-// ends of sides (q, then k) and tiles too.  A thread's sums of the side that it is not at lie in shared memory: 16 registers less.
-template <int D, bool FP16, bool PAIRS>
-__global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid_constant__ QkArgs a, const QkGrid g) {
-  __shared__ __align__(16) Angles<D> angles[2];
-  __shared__ __align__(16) float weights[2][D];
-  __shared__ float4 sums[2][4][kQkThreads];
-  using R = Rows<D>;
-  const R me(a);
-  const int all = a.B * a.N, tiles = (all + g.tokens - 1) / g.tokens;
-  // The place of the rows that are being loaded: a tile, a side, a pass of the walk through its rows.
-  struct Place {
-    int tile, side, left;  // passes left
-    Walk at;
-    int t, head, b, n;
-    bool real;
-  } ahead;
-  auto enter = [&]() {  // to the first pass of (tile, side), or of the next that has rows
-    for (; ahead.tile < tiles; ahead.tile += gridDim.x, ahead.side = 0)
-      for (; ahead.side < 2; ++ahead.side) {
-        const int tokens = min(g.tokens, all - ahead.tile * g.tokens), heads = ahead.side ? a.Hkv : a.H;
-        ahead.left = (tokens * heads + R::kGroups - 1) / R::kGroups;
-        if (ahead.left == 0) continue;
-        ahead.at.start(me.group, R::kGroups, tokens, heads, g.heads_first);
-        return;
-      }
-  };
-  Raw raw_x, raw_g;
-  auto load = [&]() {
-    if (ahead.tile >= tiles) return;
-    ahead.real = ahead.at.real();
-    ahead.t = !ahead.real ? 0 : g.heads_first ? ahead.at.major : ahead.at.minor;
-    ahead.head = !ahead.real ? 0 : g.heads_first ? ahead.at.minor : ahead.at.major;
-    const int at = ahead.tile * g.tokens + ahead.t;
-    ahead.b = g.per_row(at);
-    ahead.n = at - ahead.b * a.N;
-    const bool k = ahead.side;
-    raw_x = raw_g = Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (ahead.real) {  // (a row that is none: zeros, which add nothing to the sums)
-      raw_g = load_row(k ? a.dk_in : a.dq_in, row_at(k ? a.sdk_in : a.sdq_in, ahead.b, ahead.n, ahead.head), me.c0, me.c1);
-      if (a.norm) raw_x = load_row(k ? a.k : a.q, row_at(k ? a.sk : a.sq, ahead.b, ahead.n, ahead.head), me.c0, me.c1);
-    }
-  };
-  ahead.tile = blockIdx.x;
-  ahead.side = 0;
-  enter();
-  load();
-  make_weights<D>(weights, a);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sums[i / 4][i % 4][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  int buffer = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buffer ^= 1) {
-    make_angles<D>(angles[buffer], a, g.per_row, tile * g.tokens, min(g.tokens, all - tile * g.tokens));
-    __syncthreads();  // (and the buffer of the tile before the last is free)
+__global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
+    qk_forward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
+  __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
+  extern __shared__ uint4 ring[];
+  const Lane<D> me(a, g);
+  const int all = a.B * a.N;
+  const Share mine(g, Lane<D>::kGroups / g.heads, all);
+  if (!mine.any) return;
+  Fetch<D, false> fetch(a, g, me, ring, mine.begin, mine.step, mine.slice);
+  const Turns<D> turns(a);
+  uint32_t slot = threadIdx.x;
+  float2 w[8];
+  const int one_side = rows_of(g, 1) == 0 ? 0 : rows_of(g, 0) == 0 ? 1 : -1;
+  if (a.norm && one_side >= 0) load_weights<D>(a, me, one_side, w);
+  for (int first = mine.begin; first < all; first += mine.step) {
+    const Angles turn_by = turns.template of<false>(a, g, me, angles[threadIdx.x >> 5], first);
+#pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-      if (ahead.tile != tile || ahead.side != side) continue;  // no rows on this side
-      uint16_t* outs = static_cast<uint16_t*>(side ? a.k_out : a.q_out);
-      const Strides& so = side ? a.sk_out : a.sq_out;
-      float dw[16];
+      const int heads = side ? a.Hkv : a.H, rows = rows_of(g, side);
+      if (rows == 0) continue;
+      uint16_t* out = out_row<D>(a, g, me, first, side, mine.slice);
+      const long long out_step = (side ? a.sk_out : a.sq_out).s[1] * g.step;
+      int h = first + me.token < all ? mine.slice * g.heads + me.head : heads;  // (no token: no head)
+      if (a.norm && one_side < 0) load_weights<D>(a, me, side, w);
+      for (int left = rows; left > 0; --left, h += g.step, out += out_step) {
+        copies_wait<kDepth - 2>();
+        const uint4* from = ring + slot;
+        slot = slot == (kDepth - 1) * 2 * kQkThreads + threadIdx.x ? threadIdx.x : slot + 2 * kQkThreads;
+        float2 x[8];
+        unpack8<FP16>(from[0], x);
+        unpack8<FP16>(from[kQkThreads], x + 4);
+        fetch.row();   // into the place of the row before this one
+        if (a.norm) {  // (the root comes last: the rotation does not wait for it)
+          const float2 r = twice(rsqrtf(row_sum<D>(dot16(x, x)) * (1.f / D) + a.eps));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(dw + 4 * i) = sums[side][i][threadIdx.x];
-      for (bool last = false; !last;) {
-        float x[16], y[16], c[8], s[8];
-        unpack8<FP16>(raw_g.a, y);
-        unpack8<FP16>(raw_g.b, y + 8);
-        unpack8<FP16>(raw_x.a, x);
-        unpack8<FP16>(raw_x.b, x + 8);
-        const bool real = ahead.real;
-        const int t = ahead.t;
-        uint16_t* out = outs + row_at(so, ahead.b, ahead.n, ahead.head);
-        last = --ahead.left == 0;
-        if (last) {
-          ++ahead.side;
-          enter();
+          for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], w[j]);
+          rotate<PAIRS>(x, turn_by);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], r);
         } else {
-          ahead.at.step();
+          rotate<PAIRS>(x, turn_by);
         }
-        load();
-        angles_of<D>(angles[buffer], me, t, c, s);
-        rotate<PAIRS>(y, c, s, -1.f);
-        if (a.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
-          const float r_norm = rsqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-          float w[16], dot = 0.f;
-          weights_of<D>(weights, me, side, w);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            x[j] *= r_norm;
-            dw[j] = fmaf(y[j], x[j], dw[j]);
-            y[j] *= w[j];
-            dot = fmaf(y[j], x[j], dot);
-          }
-          dot = row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = r_norm * fmaf(-dot, x[j], y[j]);
-        }
-        if (real) {
-          *reinterpret_cast<uint4*>(out + me.c0) = pack8<FP16>(y);
-          *reinterpret_cast<uint4*>(out + me.c1) = pack8<FP16>(y + 8);
+        if (h < heads) {
+          *reinterpret_cast<uint4*>(out) = pack8<FP16>(x);
+          *reinterpret_cast<uint4*>(out + (me.c1 - me.c0)) = pack8<FP16>(x + 4);
         }
       }
+    }
+  }
+}
+
+// The gradient.  Blocks stay on the GPU and their warps take tokens in turn, so that the weights' gradients add up in a thread; each
+// block's sums go to the workspace and a second kernel adds them in order: the same bits on every run.  A thread's sums of the side that
+// it is not at lie in shared memory: 16 registers less.
+template <int D, bool FP16, bool PAIRS>
+__global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
+  __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
+  extern __shared__ float4 sums[];  // [2][4][kQkThreads], then the ring
+  uint4* ring = reinterpret_cast<uint4*>(sums + 8 * kQkThreads);
+  const Lane<D> me(a, g);
+  const int all = a.B * a.N;
+  const Share mine(g, Lane<D>::kGroups / g.heads, all);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sums[side][i][threadIdx.x] = *reinterpret_cast<float4*>(dw + 4 * i);
+  for (int i = 0; i < 8; ++i) sums[i * kQkThreads + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine.any) {
+    Fetch<D, true> fetch(a, g, me, ring, mine.begin, mine.step, mine.slice);
+    const Turns<D> turns(a);
+    uint32_t slot = threadIdx.x;
+    float2 w[8];
+    const int one_side = rows_of(g, 1) == 0 ? 0 : rows_of(g, 0) == 0 ? 1 : -1;
+    if (a.norm && one_side >= 0) load_weights<D>(a, me, one_side, w);
+    for (int first = mine.begin; first < all; first += mine.step) {
+      const Angles turn_by = turns.template of<true>(a, g, me, angles[threadIdx.x >> 5], first);
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        const int heads = side ? a.Hkv : a.H, rows = rows_of(g, side);
+        if (rows == 0) continue;
+        uint16_t* out = out_row<D>(a, g, me, first, side, mine.slice);
+        const long long out_step = (side ? a.sk_out : a.sq_out).s[1] * g.step;
+        int h = first + me.token < all ? mine.slice * g.heads + me.head : heads;  // (no token: no head)
+        float2 dw[8];
+        if (a.norm && one_side < 0) load_weights<D>(a, me, side, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 s = sums[(4 * side + i) * kQkThreads + threadIdx.x];
+          dw[2 * i] = make_float2(s.x, s.y);
+          dw[2 * i + 1] = make_float2(s.z, s.w);
+        }
+        for (int left = rows; left > 0; --left, h += g.step, out += out_step) {
+          copies_wait<kDepth - 2>();
+          const uint4* from = ring + slot;
+          slot = slot == (kDepth - 1) * 4 * kQkThreads + threadIdx.x ? threadIdx.x : slot + 4 * kQkThreads;
+          float2 x[8], y[8];
+          unpack8<FP16>(from[2 * kQkThreads], y);
+          unpack8<FP16>(from[3 * kQkThreads], y + 4);
+          if (a.norm) {
+            unpack8<FP16>(from[0], x);
+            unpack8<FP16>(from[kQkThreads], x + 4);
+          }
+          fetch.row();  // into the place of the row before this one
+          rotate<PAIRS>(y, turn_by);
+          if (a.norm) {
+            const float2 r = twice(rsqrtf(row_sum<D>(dot16(x, x)) * (1.f / D) + a.eps));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              x[j] = __fmul2_rn(x[j], r);
+              dw[j] = __ffma2_rn(y[j], x[j], dw[j]);
+              y[j] = __fmul2_rn(y[j], w[j]);
+            }
+            const float2 dot = twice(row_sum<D>(dot16(x, y)) * (-1.f / D));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(__ffma2_rn(dot, x[j], y[j]), r);
+          }
+          if (h < heads) {
+            *reinterpret_cast<uint4*>(out) = pack8<FP16>(y);
+            *reinterpret_cast<uint4*>(out + (me.c1 - me.c0)) = pack8<FP16>(y + 4);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sums[(4 * side + i) * kQkThreads + threadIdx.x] = make_float4(dw[2 * i].x, dw[2 * i].y, dw[2 * i + 1].x, dw[2 * i + 1].y);
+      }
     }
   }
   grid_release();
   if (!a.dq_weight && !a.dk_weight) return;
-  // This block's sums: column i of a side over all groups of lanes.
+  // This block's sums: column i of a side over all rows' lanes.
   __syncthreads();
-  float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(blockIdx.x) * 2 * D;
+  float* part = static_cast<float*>(a.workspace) + static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) * 2 * D;
   for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
     const int side = x / D, i = x % D;
     // The lane and place whose pieces hold the column.
@@ -443,10 +483,10 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid
       lane = k / 8;
       j = k % 8 + 8 * half;
     }
-    const float* from = reinterpret_cast<const float*>(&sums[side][j / 4][0]) + j % 4;
+    const float* from = reinterpret_cast<const float*>(sums + (4 * side + j / 4) * kQkThreads) + j % 4;
     float sum = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < R::kGroups; ++k) sum += from[4 * (k * R::kLanes + lane)];
+    for (int k = lane; k < kQkThreads; k += Lane<D>::kLanes) sum += from[4 * k];
     part[x] = sum;
   }
 }
@@ -472,40 +512,55 @@ __global__ void __launch_bounds__(1024) qk_weights_kernel(const __grid_constant_
   }
 }
 
-constexpr int kBackBlocksPerSm = 2;
+constexpr size_t kFetched = kDepth * 2 * kQkThreads * sizeof(uint4);  // the forward's; the backward's is twice that
+constexpr size_t kSums = 8 * kQkThreads * sizeof(float4);
 
-bool heads_first(const QkArgs& a) { return a.sq.s[1] < a.sq.s[0]; }
+// As many heads at once as keep at most an eighth more rows than there are (few heads: more tokens instead), as long as there
+// are tokens for `most` warps; and slices of the heads where there are fewer.
+template <int D>
+QkGrid grid_of(const QkArgs& a, long long most, dim3* blocks) {
+  constexpr int kGroups = Lane<D>::kGroups, kWarps = kQkThreads / 32;
+  const long long all = static_cast<long long>(a.B) * a.N;
+  int heads = kGroups;
+  auto steps = [](int n, int step) { return (n + step - 1) / step; };
+  auto rows = [&](int n) { return (steps(a.H, n) + steps(a.Hkv, n)) * n; };
+  auto units = [&](int n) { return std::max(1LL, (all + kGroups / n - 1) / (kGroups / n)); };
+  while (heads > 1 && 8 * rows(heads) > 9 * (a.H + a.Hkv) && units(heads / 2) >= most) heads /= 2;
+  QkGrid g{};
+  g.heads = heads;
+  g.slices = static_cast<int>(std::max(1LL, std::min<long long>(std::max(steps(a.H, heads), steps(a.Hkv, heads)), most / units(heads))));
+  g.per_row = Div(std::max(a.N, 1));
+  g.step = heads * g.slices;
+  g.rows[0] = steps(a.H, g.step);
+  g.rows[1] = steps(a.Hkv, g.step);
+  // The same number of tokens to every warp.
+  const long long lines = units(heads) * g.slices, rounds = (lines + most - 1) / most;
+  *blocks = dim3(static_cast<unsigned>(((lines + rounds - 1) / rounds + kWarps - 1) / kWarps), 2 * lines <= most ? 2 : 1);
+  return g;
+}
 
 template <int D, bool FP16, bool PAIRS>
 cudaError_t launch_forward(const QkArgs& a, cudaStream_t stream) {
-  constexpr int kGroups = Rows<D>::kGroups;
-  const long long all = static_cast<long long>(a.B) * a.N;
-  const int sms = sm_count(), heads = a.H + a.Hkv;
-  QkGrid g{kMostTokens, heads, 1, heads_first(a), Div(a.N)};
-  while (g.tokens > 1 && (all + g.tokens - 1) / g.tokens < 4LL * sms) g.tokens /= 2;
-  if (g.tokens == 1) {
-    // Too few tokens for the SMs: their heads in slices of one row a group at least.
-    const long long want = std::max(1LL, 4LL * sms / all);
-    g.slices = static_cast<int>(std::min<long long>(want, (heads + kGroups - 1) / kGroups));
-    g.heads = (heads + g.slices - 1) / g.slices;
-    g.slices = (heads + g.heads - 1) / g.heads;
-  }
-  const long long blocks = (all + g.tokens - 1) / g.tokens * g.slices;
-  qk_forward_kernel<D, FP16, PAIRS><<<static_cast<unsigned>(blocks), kQkThreads, 0, stream>>>(a, g);
+  dim3 blocks;
+  const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kForwardBlocksPerSm * (kQkThreads / 32), &blocks);
+  auto kern = qk_forward_kernel<D, FP16, PAIRS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFetched));
+  if (e) return e;
+  kern<<<blocks, kQkThreads, kFetched, stream>>>(a, g);
   return cudaGetLastError();
 }
 
 template <int D, bool FP16, bool PAIRS>
 cudaError_t launch_backward(const QkArgs& a, cudaStream_t stream) {
-  const long long all = static_cast<long long>(a.B) * a.N;
-  const int most = sm_count() * kBackBlocksPerSm;
-  QkGrid g{kMostTokens, 0, 1, heads_first(a), Div(a.N)};
-  while (g.tokens > 1 && (all + g.tokens - 1) / g.tokens < most) g.tokens /= 2;
-  const int blocks = static_cast<int>(std::max(1LL, std::min<long long>(most, (all + g.tokens - 1) / g.tokens)));
-  qk_backward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, 0, stream>>>(a, g);
-  cudaError_t e = cudaGetLastError();
+  dim3 blocks;
+  const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kBackBlocksPerSm * (kQkThreads / 32), &blocks);
+  auto kern = qk_backward_kernel<D, FP16, PAIRS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSums + 2 * kFetched));
+  if (e) return e;
+  kern<<<blocks, kQkThreads, kSums + 2 * kFetched, stream>>>(a, g);
+  e = cudaGetLastError();
   if (e || (!a.dq_weight && !a.dk_weight)) return e;
-  return launch_dependent(qk_weights_kernel<D>, 2, 1024, 0, stream, a, blocks);
+  return launch_dependent(qk_weights_kernel<D>, 2, 1024, 0, stream, a, static_cast<int>(blocks.x * blocks.y));
 }
 
 template <int D, bool FP16>
