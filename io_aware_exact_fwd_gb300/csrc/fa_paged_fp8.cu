@@ -24,8 +24,8 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t two) {
 // block's new rows (16 bytes a lane and row part) into registers, finds their largest value, and if the block held
 // tokens whose scale is smaller, re-codes those.  A unit is a run of consecutive new tokens and one head of K or
 // V; the lanes look the tokens' places up, one each, and a token that is the first new one of its block stands for
-// the block.  With few tokens the runs are of one token, so that blocks do not wait for each other; with many of 16, so
-// that the look-ups are not done for every token that stands for none.  Bound by HBM: 2 bytes read and 1 written a
+// the block.  With few tokens, or many sequences with few each, the runs are of one token, so that blocks do not wait for
+// each other; else of up to 32, so that the look-ups are not done for every token that stands for none.  Bound by HBM: 2 bytes read and 1 written a
 // value.
 template <bool FP16>
 __device__ __forceinline__ float2 widen(uint32_t two) {
@@ -41,7 +41,7 @@ __device__ __forceinline__ int exponent_for(float top) {
 }
 
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) append_fp8_kernel(const __grid_constant__ PagedAppendArgs a, int run) {
+__global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const __grid_constant__ PagedAppendArgs a, int run) {
   constexpr int kLanes = D / 8;             // lanes of a row, 16 bytes of new values each
   constexpr int kRows = 32 / kLanes;        // rows at once
   constexpr int kPasses = 16 / kRows;
@@ -56,13 +56,16 @@ __global__ void __launch_bounds__(128) append_fp8_kernel(const __grid_constant__
   // Lane x < run: the place of token first + x, if it stands for its block.
   int page = -1, off = 0, count = 0;
   const int t = static_cast<int>(first) + lane;
+  int lo = 0, hi = a.c.B + 1;  // the number of offsets <= first, by the whole warp: 32 probes at once
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step - 1;
+    const int k = __popc(__ballot_sync(0xffffffffu, probe < hi && __ldg(a.cu_new + probe) <= first));
+    hi = min(hi, lo + (k + 1) * step - 1);
+    lo += k * step;
+  }
   if (lane < run && t < a.T) {
-    int lo = 0, hi = a.c.B + 1;  // the number of offsets <= t
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (__ldg(a.cu_new + mid) <= t) lo = mid + 1;
-      else hi = mid;
-    }
+    // From there to the number of offsets <= t, a few further on.
+    while (lo <= a.c.B && __ldg(a.cu_new + lo) <= t) ++lo;
     if (lo != 0 && lo != a.c.B + 1) {  // (else a row of no sequence)
       const int b = lo - 1, end = __ldg(a.cu_new + lo);
       const long long pos = static_cast<long long>(a.c.seq_lens[b]) - (static_cast<long long>(end) - t);
@@ -738,7 +741,8 @@ cudaError_t launch_decode8_heads(const PagedDecodeArgs& a, cudaStream_t stream) 
 
 cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t stream) {
   const long long sides = 2LL * a.c.Hkv;
-  const int run = a.T * sides > 64LL * sm_count() ? 16 : 1;
+  // About two blocks a warp (each sequence's tokens are a block for every 16, and one more), one where there are few.
+  const int run = a.T * sides <= 64LL * sm_count() ? 1 : std::max(1, static_cast<int>(32LL * a.T / (a.T + 16LL * a.c.B)));
   const long long warps = (a.T + run - 1LL) / run * sides;
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
   auto kern = a.c.d == 64 ? (a.fp16 ? append_fp8_kernel<64, true> : append_fp8_kernel<64, false>)

@@ -7,10 +7,11 @@
 // The rest needs no order: page k of all that are taken, page r of all that come back and new token t each find
 // their sequence by bisection in those sums.  Pages that come back are written behind the free ones, and the pages taken are
 // the last of that longer list, so a page may come back and be taken in one call: its taker reads it from the table of
-// the sequence that gave it.
+// the sequence that gave it.  A token's page, if it is a taken one, is found in the same way and not in the table, so
+// nothing waits for the table's new entries.
 //
-// Bound by latency: a launch, two dependent loads of the lengths, the scan.  The second part runs in the same block where
-// there is little of it and as a dependent launch over the GPU where there is more.
+// Bound by latency: a launch, two dependent loads of the lengths, the scan.  The second part runs in the same block, with the
+// sums in shared memory, where there is little of it, and as a dependent launch over the GPU where there is more.
 #include "fa_device.cuh"
 #include "fa_internal.h"
 
@@ -68,43 +69,71 @@ __device__ __forceinline__ int owner_of(const int32_t* sums, int B, int x) {
   }
   return lo;
 }
-
-// The second part: threads `at`, at + step, ... of the work.
-__device__ __forceinline__ void spread(const PagedResizeArgs& a, long long at, long long step) {
-  const Sums s = sums_of(a.workspace, a.B);
-  const int grow = s.grow[a.B], drop = s.drop[a.B], count = *s.count;
-  // (after a refusal grow, drop and the new tokens are 0)
-  auto given_back = [&](int r) {
-    const int b = owner_of(s.drop, a.B, r);
-    return a.page_table[b * a.table_stride + pages_of(a.lens_out[b], a.page_size) + (r - s.drop[b])];
-  };
-  for (long long r = at; r < drop; r += step) a.free_pages[count + r] = given_back(static_cast<int>(r));
-  for (long long k = at; k < grow; k += step) {
-    const int b = owner_of(s.grow, a.B, static_cast<int>(k)), place = count + drop - 1 - static_cast<int>(k);
-    const int has = pages_of(a.lens_out[b], a.page_size), mine = s.grow[b + 1] - s.grow[b];
-    a.page_table[b * a.table_stride + has - mine + (k - s.grow[b])] =
-        place >= count ? given_back(place - count) : a.free_pages[place];
+// The same by a whole warp, for an x of the warp's: 32 probes at once.
+__device__ __forceinline__ int owner_of_warp(const int32_t* sums, int B, int x, int lane) {
+  int lo = 0, hi = B;  // sums[lo] <= x < sums[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, probe < hi && sums[probe] <= x));
+    hi = min(hi, lo + (k + 1) * step);
+    lo += k * step;
   }
+  return lo;
 }
-__device__ __forceinline__ void tokens(const PagedResizeArgs& a, long long at, long long step) {
-  const int total = a.cu_new[a.B];
-  for (long long t = at; t < a.T; t += step) {
+
+// What the second part goes by: the sums, the new lengths, and the list's length on entry.
+struct Plan {
+  const int32_t *grow, *drop, *cu, *lens;
+  int count;
+};
+
+// Page r of those given back, and page k of those taken.
+__device__ __forceinline__ int given_back(const PagedResizeArgs& a, const Plan& p, int r) {
+  const int b = owner_of(p.drop, a.B, r);
+  return a.page_table[b * a.table_stride + pages_of(p.lens[b], a.page_size) + (r - p.drop[b])];
+}
+__device__ __forceinline__ int taken(const PagedResizeArgs& a, const Plan& p, int k) {
+  const int place = p.count + p.drop[a.B] - 1 - k;
+  return place >= p.count ? given_back(a, p, place - p.count) : a.free_pages[place];
+}
+
+// The second part: thread `at` of `all`, of whole warps.  (After a refusal there are no pages and no new tokens.)
+__device__ __forceinline__ void spread(const PagedResizeArgs& a, const Plan& p, int at, int all) {
+  const int grow = p.grow[a.B], drop = p.drop[a.B], total = p.cu[a.B], lane = at & 31;
+  for (long long r = at; r < drop; r += all) a.free_pages[p.count + r] = given_back(a, p, static_cast<int>(r));
+  for (long long k = at; k < grow; k += all) {
+    const int b = owner_of(p.grow, a.B, static_cast<int>(k));
+    const int had = pages_of(p.lens[b], a.page_size) - (p.grow[b + 1] - p.grow[b]);
+    a.page_table[b * a.table_stride + had + (k - p.grow[b])] = taken(a, p, static_cast<int>(k));
+  }
+  // 32 rows a warp: the first one's sequence by all lanes, the others' from there on.
+  for (long long t0 = at - lane; t0 < a.T; t0 += all) {
     long long pos = -1, slot = -1;
-    if (t < total) {
-      const int b = owner_of(a.cu_new, a.B, static_cast<int>(t));
-      pos = a.lens_out[b] - (a.cu_new[b + 1] - t);
-      if (a.slots)
-        slot = static_cast<long long>(a.page_table[b * a.table_stride + static_cast<int>(pos) / a.page_size]) * a.page_size +
-               static_cast<int>(pos) % a.page_size;
+    const long long t = t0 + lane;
+    if (t0 < total) {
+      int b = owner_of_warp(p.cu, a.B, static_cast<int>(t0), lane);
+      if (t < total && t < a.T) {
+        while (p.cu[b + 1] <= t) ++b;
+        pos = p.lens[b] - (p.cu[b + 1] - t);
+        if (a.slots) {
+          const int place = static_cast<int>(pos) / a.page_size, more = p.grow[b + 1] - p.grow[b];
+          const int had = pages_of(p.lens[b], a.page_size) - more;
+          const int page = place < had ? a.page_table[b * a.table_stride + place] : taken(a, p, p.grow[b] + place - had);
+          slot = static_cast<long long>(page) * a.page_size + (static_cast<int>(pos) - place * a.page_size);
+        }
+      }
     }
-    if (a.slots) a.slots[t] = slot;
-    if (a.positions) a.positions[t] = static_cast<int>(pos);
+    if (t < a.T) {
+      if (a.slots) a.slots[t] = slot;
+      if (a.positions) a.positions[t] = static_cast<int>(pos);
+    }
   }
 }
 
 __global__ void __launch_bounds__(kScanThreads) resize_scan_kernel(const __grid_constant__ PagedResizeArgs a, int alone) {
   __shared__ long long s_part[3][32];
   __shared__ int s_unfit;
+  __shared__ int32_t s_sums[3][kScanThreads + 1], s_lens[kScanThreads];  // for the second part, if it is this block's
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s_unfit = 0;
   __syncthreads();
@@ -141,42 +170,51 @@ __global__ void __launch_bounds__(kScanThreads) resize_scan_kernel(const __grid_
   const Sums s = sums_of(a.workspace, a.B);
   for (int b = lo; b < hi; ++b) {
     const Change c = change_of(a, b);
-    const int new_tokens = max(a.delta[b], 0);
-    s.grow[b] = done ? static_cast<int>(before[0]) : 0;
-    s.drop[b] = done ? static_cast<int>(before[1]) : 0;
-    a.cu_new[b] = done ? static_cast<int>(before[2]) : 0;
-    const int length = a.seq_lens[b];
-    a.lens_out[b] = done ? static_cast<int>(c.after) : length;  // (may be seq_lens: this thread alone reads entry b)
+    const int new_tokens = max(a.delta[b], 0), length = a.seq_lens[b];
+    const int now[4] = {done ? static_cast<int>(before[0]) : 0, done ? static_cast<int>(before[1]) : 0,
+                        done ? static_cast<int>(before[2]) : 0, done ? static_cast<int>(c.after) : length};
+    a.cu_new[b] = now[2];
+    a.lens_out[b] = now[3];  // (may be seq_lens: this thread alone reads entry b)
+    if (alone) {
+      s_sums[0][b] = now[0];
+      s_sums[1][b] = now[1];
+      s_sums[2][b] = now[2];
+      s_lens[b] = now[3];
+    } else {
+      s.grow[b] = now[0];
+      s.drop[b] = now[1];
+    }
     before[0] += max(c.has - c.had, 0);
     before[1] += max(c.had - c.has, 0);
     before[2] += new_tokens;
   }
   if (threadIdx.x == 0) {
-    s.grow[a.B] = done ? static_cast<int>(total[0]) : 0;
-    s.drop[a.B] = done ? static_cast<int>(total[1]) : 0;
-    a.cu_new[a.B] = done ? static_cast<int>(total[2]) : 0;
-    *s.count = count;
+    const int now[3] = {done ? static_cast<int>(total[0]) : 0, done ? static_cast<int>(total[1]) : 0,
+                        done ? static_cast<int>(total[2]) : 0};
+    a.cu_new[a.B] = now[2];
+    if (alone) {
+      s_sums[0][a.B] = now[0];
+      s_sums[1][a.B] = now[1];
+      s_sums[2][a.B] = now[2];
+    } else {
+      s.grow[a.B] = now[0];
+      s.drop[a.B] = now[1];
+      *s.count = count;
+    }
     *a.count_out = done ? static_cast<int>(longer - total[0]) : *a.free_count;
     a.status[0] = static_cast<int>(min(missing, 0x7fffffffLL));
     a.status[1] = bad;
   }
   if (!alone) return;
   __syncthreads();
-  spread(a, threadIdx.x, kScanThreads);
-  if (a.T == 0) return;
-  __syncthreads();
-  tokens(a, threadIdx.x, kScanThreads);
+  spread(a, Plan{s_sums[0], s_sums[1], s_sums[2], s_lens, count}, threadIdx.x, kScanThreads);
 }
 
-__global__ void __launch_bounds__(256) resize_pages_kernel(const __grid_constant__ PagedResizeArgs a) {
+__global__ void __launch_bounds__(256) resize_spread_kernel(const __grid_constant__ PagedResizeArgs a) {
   grid_wait();
-  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  spread(a, at, static_cast<long long>(gridDim.x) * 256);
-}
-__global__ void __launch_bounds__(256) resize_tokens_kernel(const __grid_constant__ PagedResizeArgs a) {
-  grid_wait();
-  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  tokens(a, at, static_cast<long long>(gridDim.x) * 256);
+  const Sums s = sums_of(a.workspace, a.B);
+  spread(a, Plan{s.grow, s.drop, a.cu_new, a.lens_out, *s.count}, static_cast<int>(blockIdx.x * 256 + threadIdx.x),
+         static_cast<int>(gridDim.x * 256));
 }
 
 }  // namespace
@@ -186,12 +224,9 @@ size_t paged_resize_workspace(int B) { return (2 * (static_cast<size_t>(B) + 1) 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
   const int alone = a.T <= 4 * kScanThreads && a.B <= kScanThreads;
   resize_scan_kernel<<<1, kScanThreads, 0, stream>>>(a, alone);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e || alone) return e;
-  const unsigned blocks = static_cast<unsigned>(sm_count()) * 8;
-  if ((e = launch_dependent(resize_pages_kernel, blocks, 256, 0, stream, a))) return e;
-  if (a.T == 0) return cudaSuccess;
-  return launch_dependent(resize_tokens_kernel, blocks, 256, 0, stream, a);
+  return launch_dependent(resize_spread_kernel, static_cast<unsigned>(sm_count()) * 8, 256, 0, stream, a);
 }
 
 }  // namespace fa

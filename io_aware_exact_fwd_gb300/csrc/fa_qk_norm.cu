@@ -543,10 +543,8 @@ template <int D, bool FP16, bool PAIRS>
 cudaError_t launch_forward(const QkArgs& a, cudaStream_t stream) {
   dim3 blocks;
   const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kForwardBlocksPerSm * (kQkThreads / 32), &blocks);
-  auto kern = qk_forward_kernel<D, FP16, PAIRS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFetched));
-  if (e) return e;
-  kern<<<blocks, kQkThreads, kFetched, stream>>>(a, g);
+  static_assert(kFetched + sizeof(float2) * kQkThreads / 32 * Lane<D>::kGroups * D / 2 <= 49152, "needs no attribute");
+  qk_forward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, kFetched, stream>>>(a, g);
   return cudaGetLastError();
 }
 

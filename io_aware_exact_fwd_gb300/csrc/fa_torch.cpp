@@ -485,7 +485,7 @@ PyObject* paged_resize(PyObject* const* a) {
 Tensor fresh_like(const Tensor& x) {
   const int64_t B = x.size(0), H = x.size(1), N = x.size(2), d = x.size(3);
   if (H > 1 && N > 1 ? x.stride(1) < x.stride(2) : N > 1 && x.stride(2) > d)
-    return fresh({B, N, H, d}, x.scalar_type(), x).transpose(1, 2);
+    return at::detail::empty_strided_cuda({B, H, N, d}, {N * H * d, d, H * d, 1}, x.scalar_type(), x.device());
   return fresh({B, H, N, d}, x.scalar_type(), x);
 }
 
