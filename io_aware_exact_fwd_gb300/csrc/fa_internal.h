@@ -259,6 +259,21 @@ cudaError_t launch_fwd_scored(const FwdArgs& a, const ScoreArgs& sc, cudaStream_
 size_t bwd_scored_workspace(int B, int H, int Hkv, int N, int d);
 cudaError_t launch_bwd_scored(const BwdArgs& a, const ScoreArgs& sc, cudaStream_t stream);
 
+// x / n for 0 <= x < 2^31 by a product: with s the least number such that n <= 2^s, ceil(2^(31 + s) / n) has 32 bits.
+struct Div {
+  uint32_t by, shift;
+  Div() = default;
+  explicit Div(int n) {
+    int s = 0;
+    while ((1ll << s) < n) ++s;
+    shift = static_cast<uint32_t>(31 + s);
+    by = static_cast<uint32_t>(((1ull << shift) + n - 1) / n);
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * by >> shift);
+  }
+};
+
 // ------------------------------------------------------- paged cache (fa_paged.cu)
 
 struct PagedCache {
@@ -269,6 +284,7 @@ struct PagedCache {
   int64_t table_stride;
   const int32_t* seq_lens;
   int B, Hkv, d, page_size, n_pages, max_pages;
+  Div per_page;              // by page_size
   float* k_scales;           // of a cache of e4m3 codes: [n_pages, Hkv, page_size / 16]
   float* v_scales;
 };
@@ -319,6 +335,7 @@ struct PagedResizeArgs {
   void* workspace;
   int B, page_size, max_pages, capacity;
   int T;
+  Div per_page;              // by page_size
 };
 size_t paged_resize_workspace(int B);
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream);

@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
     const int pieces = kTile / p.piece;
     auto page_at = [&](const Place<kTile>& x, int& row) -> int {
       const int tok = x.t * kTile + lane * p.piece;
-      row = tok % p.c.page_size;
+      const int place = p.c.per_page(tok);
+      row = tok - place * p.c.page_size;
       int page = p.c.n_pages;
-      if (lane < pieces && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + tok / p.c.page_size];
+      if (lane < pieces && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + place];
       return page < 0 || page >= p.c.n_pages ? p.c.n_pages : page;
     };
     int issued = 0, row;

@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
   const int lane = threadIdx.x & 31;
   const long long unit = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) >> 5;
   const int sides = 2 * a.c.Hkv;
-  const long long first = unit / sides * run;
+  const long long line = quotient(unit, sides), first = line * run;
   if (first >= a.T) return;
-  const int side = static_cast<int>(unit % sides), head = side >> 1;
+  const int side = static_cast<int>(unit - line * sides), head = side >> 1;
   const bool is_v = side & 1;
   // Lane x < run: the place of token first + x, if it stands for its block.
   int page = -1, off = 0, count = 0;
@@ -71,8 +71,9 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
       const long long pos = static_cast<long long>(a.c.seq_lens[b]) - (static_cast<long long>(end) - t);
       const bool stands = (pos & 15) == 0 || t == __ldg(a.cu_new + b);
       if (stands && pos >= 0 && pos < static_cast<long long>(a.c.max_pages) * a.c.page_size) {
-        off = static_cast<int>(pos) % a.c.page_size;
-        page = a.c.page_table[b * a.c.table_stride + static_cast<int>(pos) / a.c.page_size];
+        const int place = a.c.per_page(static_cast<int>(pos));
+        off = static_cast<int>(pos) - place * a.c.page_size;
+        page = a.c.page_table[b * a.c.table_stride + place];
         if (page >= a.c.n_pages) page = -1;
         count = min(16 - (off & 15), min(end, a.T) - t);
       }
@@ -284,9 +285,10 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     const float* scales = is_v ? p.c.v_scales : p.c.k_scales;
     auto page_at = [&](const Place<kTile>& x, int& row) -> int {
       const int tok = x.t * kTile + block * 16;
-      row = tok % p.c.page_size;
+      const int place = p.c.per_page(tok);
+      row = tok - place * p.c.page_size;
       int page = p.c.n_pages;
-      if (mine && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + tok / p.c.page_size];
+      if (mine && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + place];
       return page < 0 || page >= p.c.n_pages ? p.c.n_pages : page;
     };
     const bool starts = lane < 2 * C::kBlocksOfTile && block * 16 % p.piece == 0;

@@ -36,21 +36,6 @@ namespace {
 
 constexpr int kQkThreads = 256;
 
-// x / n for 0 <= x < 2^31 by a product: with s the least number such that n <= 2^s, ceil(2^(31 + s) / n) has 32 bits.
-struct Div {
-  uint32_t by, shift;
-  Div() = default;
-  explicit Div(int n) {
-    int s = 0;
-    while ((1ll << s) < n) ++s;
-    shift = static_cast<uint32_t>(31 + s);
-    by = static_cast<uint32_t>(((1ull << shift) + n - 1) / n);
-  }
-  __device__ __forceinline__ int operator()(int x) const {
-    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * by >> shift);
-  }
-};
-
 // inv_freq / 2 pi modulo 1, as a 64-bit fraction, of a finite |inv_freq| < 2^64.
 __device__ __forceinline__ uint64_t turns_of(float inv_freq) {
   // 1 / 2 pi = 0x0.28be60db9391054a7f09d5f47d4d3770...

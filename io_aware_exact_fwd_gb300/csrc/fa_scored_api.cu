@@ -207,6 +207,7 @@ int paged_cache(fa::PagedCache* c, const void* k, const int64_t* sk, const void*
   c->Hkv = Hkv;
   c->d = d;
   c->page_size = page_size;
+  c->per_page = fa::Div(page_size);
   c->n_pages = n_pages;
   c->max_pages = max_pages;
   return FA_OK;
@@ -416,6 +417,7 @@ int fa_paged_resize(int32_t* page_table, int64_t table_stride, const int32_t* se
   a.workspace = workspace;
   a.B = B;
   a.page_size = page_size;
+  a.per_page = fa::Div(page_size);
   a.max_pages = max_pages;
   a.capacity = capacity;
   a.T = slots || positions ? T : 0;
