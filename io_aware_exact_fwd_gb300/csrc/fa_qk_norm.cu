@@ -11,10 +11,11 @@
 //
 // Work.  A warp takes a token (or, where there are few heads, some) with all its heads, q's and then k's: the angles' sines and
 // cosines, the costliest part, are made once for them and stay in registers, as do the weights.  Rows stream through the warp: each lane
-// copies its pieces of the next kDepth rows into places of its own in shared memory (cp.async: HBM's latency at full rate takes
-// more bytes on the way than registers could wait for), over the ends of sides and tokens.  (A block that shares its
-// tokens' angles in shared memory and reads them for every row: 62 us for 16384 tokens of 40 heads x 128, the
-// reads' bank conflicts being most of it.)
+// copies its pieces of the next rows into places of its own in shared memory (cp.async: HBM's latency at full rate takes
+// more bytes on the way than registers could wait for), over the ends of sides and tokens.  Measured: 16384 tokens of 40 heads
+// x 128 in 55.0 us, 6.1 TB/s; the gradient, 32 heads, in 67.0, 6.0 TB/s; 16 tokens of 10 heads x 64 in 3.9.  (A block that
+// shares its tokens' angles in shared memory and reads them for every row: 62 and 82 us, the reads' bank conflicts being
+// most of it; rows kept in registers alone: 76 and 89.)
 //
 // Angles.  position * inv_freq in fp32 would lose all but a few bits of the angle at far positions.  An angle counts only
 // modulo one turn, so the frequency is held in turns a token as a 64-bit fraction, made from inv_freq (a 24-bit integer times
@@ -123,6 +124,7 @@ struct QkGrid {
   Div per_row;    // by N
   int step;       // heads * slices
   int rows[2];    // of q's and k's heads that a slice takes, at most: heads / step, rounded up
+  long long x_step[2], dy_step[2], out_step[2];  // elements from a warp's row to its next
 };
 // The rows of a side that this block takes: where there are few tokens, blocks are for q (blockIdx.y = 0) or for k.
 __device__ __forceinline__ int rows_of(const QkGrid& g, int side) {
@@ -161,7 +163,9 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int kDepth = 4;  // rows on the way
+// Rows of a warp in the ring, the one that is worked on among them.  16384 tokens of 40 heads x 128 forward, of 32
+// backward: 55.0 and 67.0 us; two rows 65.7 and 74.5, four 59.8 and 67.9 (HBM serves fewer streams at once better).
+constexpr int kDepth = 3;
 constexpr int kForwardBlocksPerSm = 2, kBackBlocksPerSm = 2;
 
 // This thread's part: its place in its row's lanes and the columns of its two pieces; its row's head and token among the warp's.
@@ -229,12 +233,12 @@ struct Fetch {
     if (!BACK || a.norm) {
       copy16(to, x, bytes);
       copy16(to + 16 * kQkThreads, x + (me.c1 - me.c0), bytes);
-      x += (side ? a.sk : a.sq).s[1] * g.step;
+      x += side ? g.x_step[1] : g.x_step[0];
     }
     if constexpr (BACK) {
       copy16(to + 32 * kQkThreads, dy, bytes);
       copy16(to + 48 * kQkThreads, dy + (me.c1 - me.c0), bytes);
-      dy += (side ? a.sdk_in : a.sdq_in).s[1] * g.step;
+      dy += side ? g.dy_step[1] : g.dy_step[0];
     }
     copies_end();
     to = to == begin + (kDepth - 1) * kSlot ? begin : to + kSlot;
@@ -286,18 +290,21 @@ struct Turns {
   }
 };
 
+// The weights (1 without) in shared memory, and this lane's.
 template <int D>
-__device__ __forceinline__ void load_weights(const QkArgs& a, const Lane<D>& me, int side, float2 (&w)[8]) {
-  const void* from = side ? a.k_weight : a.q_weight;
-  if (!from) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = twice(1.f);
-    return;
+__device__ __forceinline__ void make_weights(float (&w)[2][D], const QkArgs& a) {
+  for (int x = threadIdx.x; x < 2 * D; x += kQkThreads) {
+    const void* from = x < D ? a.q_weight : a.k_weight;
+    w[x / D][x % D] = from ? weight_at(from, a.weight_type, x % D) : 1.f;
   }
+}
+template <int D>
+__device__ __forceinline__ void load_weights(const float (&in)[2][D], const Lane<D>& me, int side, float2 (&w)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = j < 4 ? me.c0 + 2 * j : me.c1 + 2 * (j - 4);
-    w[j] = make_float2(weight_at(from, a.weight_type, c), weight_at(from, a.weight_type, c + 1));
+  for (int j = 0; j < 8; j += 2) {
+    const float4 x = *reinterpret_cast<const float4*>(&in[side][j < 4 ? me.c0 + 2 * j : me.c1 + 2 * (j - 4)]);
+    w[j] = make_float2(x.x, x.y);
+    w[j + 1] = make_float2(x.z, x.w);
   }
 }
 
@@ -330,7 +337,12 @@ template <int D, bool FP16, bool PAIRS>
 __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
     qk_forward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
   __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
+  __shared__ __align__(16) float weights[2][D];
   extern __shared__ uint4 ring[];
+  if (a.norm) {
+    make_weights<D>(weights, a);
+    __syncthreads();
+  }
   const Lane<D> me(a, g);
   const int all = a.B * a.N;
   const Share mine(g, Lane<D>::kGroups / g.heads, all);
@@ -338,9 +350,6 @@ __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
   Fetch<D, false> fetch(a, g, me, ring, mine.begin, mine.step, mine.slice);
   const Turns<D> turns(a);
   uint32_t slot = threadIdx.x;
-  float2 w[8];
-  const int one_side = rows_of(g, 1) == 0 ? 0 : rows_of(g, 0) == 0 ? 1 : -1;
-  if (a.norm && one_side >= 0) load_weights<D>(a, me, one_side, w);
   for (int first = mine.begin; first < all; first += mine.step) {
     const Angles turn_by = turns.template of<false>(a, g, me, angles[threadIdx.x >> 5], first);
 #pragma unroll 1
@@ -348,9 +357,10 @@ __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
       const int heads = side ? a.Hkv : a.H, rows = rows_of(g, side);
       if (rows == 0) continue;
       uint16_t* out = out_row<D>(a, g, me, first, side, mine.slice);
-      const long long out_step = (side ? a.sk_out : a.sq_out).s[1] * g.step;
+      const long long out_step = side ? g.out_step[1] : g.out_step[0];
       int h = first + me.token < all ? mine.slice * g.heads + me.head : heads;  // (no token: no head)
-      if (a.norm && one_side < 0) load_weights<D>(a, me, side, w);
+      float2 w[8];
+      if (a.norm) load_weights<D>(weights, me, side, w);
       for (int left = rows; left > 0; --left, h += g.step, out += out_step) {
         copies_wait<kDepth - 2>();
         const uint4* from = ring + slot;
@@ -384,6 +394,7 @@ __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
 template <int D, bool FP16, bool PAIRS>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
   __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
+  __shared__ __align__(16) float weights[2][D];
   extern __shared__ float4 sums[];  // [2][4][kQkThreads], then the ring
   uint4* ring = reinterpret_cast<uint4*>(sums + 8 * kQkThreads);
   const Lane<D> me(a, g);
@@ -391,13 +402,14 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid
   const Share mine(g, Lane<D>::kGroups / g.heads, all);
 #pragma unroll
   for (int i = 0; i < 8; ++i) sums[i * kQkThreads + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.norm) {
+    make_weights<D>(weights, a);
+    __syncthreads();
+  }
   if (mine.any) {
     Fetch<D, true> fetch(a, g, me, ring, mine.begin, mine.step, mine.slice);
     const Turns<D> turns(a);
     uint32_t slot = threadIdx.x;
-    float2 w[8];
-    const int one_side = rows_of(g, 1) == 0 ? 0 : rows_of(g, 0) == 0 ? 1 : -1;
-    if (a.norm && one_side >= 0) load_weights<D>(a, me, one_side, w);
     for (int first = mine.begin; first < all; first += mine.step) {
       const Angles turn_by = turns.template of<true>(a, g, me, angles[threadIdx.x >> 5], first);
 #pragma unroll 1
@@ -405,10 +417,10 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid
         const int heads = side ? a.Hkv : a.H, rows = rows_of(g, side);
         if (rows == 0) continue;
         uint16_t* out = out_row<D>(a, g, me, first, side, mine.slice);
-        const long long out_step = (side ? a.sk_out : a.sq_out).s[1] * g.step;
+        const long long out_step = side ? g.out_step[1] : g.out_step[0];
         int h = first + me.token < all ? mine.slice * g.heads + me.head : heads;  // (no token: no head)
-        float2 dw[8];
-        if (a.norm && one_side < 0) load_weights<D>(a, me, side, w);
+        float2 w[8], dw[8];
+        if (a.norm) load_weights<D>(weights, me, side, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 s = sums[(4 * side + i) * kQkThreads + threadIdx.x];
@@ -518,6 +530,12 @@ QkGrid grid_of(const QkArgs& a, long long most, dim3* blocks) {
   g.step = heads * g.slices;
   g.rows[0] = steps(a.H, g.step);
   g.rows[1] = steps(a.Hkv, g.step);
+  const Strides* each[3][2] = {{&a.sq, &a.sk}, {&a.sdq_in, &a.sdk_in}, {&a.sq_out, &a.sk_out}};
+  for (int side = 0; side < 2; ++side) {
+    g.x_step[side] = each[0][side]->s[1] * g.step;
+    g.dy_step[side] = each[1][side]->s[1] * g.step;
+    g.out_step[side] = each[2][side]->s[1] * g.step;
+  }
   // The same number of tokens to every warp.
   const long long lines = units(heads) * g.slices, rounds = (lines + most - 1) / most;
   *blocks = dim3(static_cast<unsigned>(((lines + rounds - 1) / rounds + kWarps - 1) / kWarps), 2 * lines <= most ? 2 : 1);
@@ -528,8 +546,7 @@ template <int D, bool FP16, bool PAIRS>
 cudaError_t launch_forward(const QkArgs& a, cudaStream_t stream) {
   dim3 blocks;
   const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kForwardBlocksPerSm * (kQkThreads / 32), &blocks);
-  static_assert(kFetched + sizeof(float2) * kQkThreads / 32 * Lane<D>::kGroups * D / 2 <= 49152, "needs no attribute");
-  qk_forward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, kFetched, stream>>>(a, g);
+  qk_forward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, kFetched, stream>>>(a, g);  // (48 KB with what is static: no attribute)
   return cudaGetLastError();
 }
 
