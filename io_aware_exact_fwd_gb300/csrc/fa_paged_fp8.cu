@@ -55,7 +55,6 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
   const bool is_v = side & 1;
   // Lane x < run: the place of token first + x, if it stands for its block.
   int page = -1, off = 0, count = 0;
-  const int t = static_cast<int>(first) + lane;
   int lo = 0, hi = a.c.B + 1;  // the number of offsets <= first, by the whole warp: 32 probes at once
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32, probe = lo + (lane + 1) * step - 1;
@@ -63,7 +62,8 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
     hi = min(hi, lo + (k + 1) * step - 1);
     lo += k * step;
   }
-  if (lane < run && t < a.T) {
+  if (lane < run && first + lane < a.T) {
+    const int t = static_cast<int>(first) + lane;
     // From there to the number of offsets <= t, a few further on.
     while (lo <= a.c.B && __ldg(a.cu_new + lo) <= t) ++lo;
     if (lo != 0 && lo != a.c.B + 1) {  // (else a row of no sequence)

@@ -206,6 +206,24 @@ def test_a_value_that_weighs_little_beside_a_large_scale():
     assert abs(o.double().cpu() - want).max() <= 2.0 ** -10 and abs(lse.item() - np.log(16 * (1 + w))) < 1e-5
 
 
+def test_a_weight_below_fp32_times_a_scale_far_above_the_others():
+    # Weights of e^-88, below fp32's normal range, for values 2^120 times those of weight 1: their share is still 2^-7.
+    d = 64
+    kc = torch.zeros(2, 1, 16, d, dtype=torch.uint8, device="cuda")
+    vc = torch.full_like(kc, 0x38)
+    kc[0] = 0xB8
+    ks = torch.ones(2, 1, 1, device="cuda")
+    for order in ([0, 1], [1, 0]):
+        vs = torch.tensor([2.0 ** 60, 2.0 ** -60], device="cuda").view(2, 1, 1)
+        q = torch.full((1, 1, d), 11.0, dtype=torch.bfloat16, device="cuda")
+        o, lse = fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, _ints([order]), _ints([32]), scale=0.125)
+        fa.fa_sync_check()
+        w = np.exp(-88.0)
+        want = (w * 2.0 ** 60 + 2.0 ** -60) / (1 + w)
+        assert abs(want * 2.0 ** 60 - 1.008) < 1e-3
+        assert (o.double().cpu() / want - 1).abs().max() <= 2.0 ** -8 and abs(lse.item() - np.log(16)) < 1e-5
+
+
 def test_nan_stays_in_its_sequence_and_head():
     lens = [40, 40]
     kc, vc, ks, vs, table, n = _cache(lens, 2, 64, 16, 11)
