@@ -26,7 +26,8 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t two) {
 // V; the lanes look the tokens' places up, one each, and a token that is the first new one of its block stands for
 // the block.  With few tokens, or many sequences with few each, the runs are of one token, so that blocks do not wait for
 // each other; else of up to 32, so that the look-ups are not done for every token that stands for none.  Bound by HBM: 2 bytes read and 1 written a
-// value.
+// value.  Measured: 16 prompts, 35k tokens of 8 heads x 128, in 37 us, 5.8 TB/s (runs of 16 tokens 39.7; the next block's rows
+// fetched into registers while one is coded 43.8: fewer warps an SM); 64 tokens in 3.4; 2000 sequences a token each in 26.
 template <bool FP16>
 __device__ __forceinline__ float2 widen(uint32_t two) {
   if constexpr (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&two));
@@ -191,6 +192,11 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
 // own, whose tiles come from L2 for all but the first.  (Two or three groups of four warps that work on the same stages, so
 // that the cache is read once, ran at 3.6 TB/s of codes with 32 heads and 1.9 with 40: no more than chunks reach
 // with nothing in L2, for their arithmetic is the same and one CTA an SM hides less of it.)
+//
+// Measured: 64 sequences of 1 .. 16384 tokens (0.96 GB), H=32 over 8 heads, d=128, capped: 148-151 us, 6.4-6.5 TB/s (heads
+// as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 56 us, 4.8 TB/s (one head a unit 91; 51
+// where each head's tokens lie together); 24 of 2000 .. 8000 tokens, 40 heads over one: 25.7 (chunks of 8 heads 26.5, and 147
+// for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.9, two launches and three waits on memory.  Times in a graph.
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
 template <int D, int NH, bool TWO>
