@@ -188,39 +188,42 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
 // byte shuffle makes pairs of tokens, of the even column 2g (row g of the product) and the odd one (row g + 8).  The weights
 // come out with a token's heads side by side and go in with a head's tokens side by side: movmatrix transposes them.
 //
-// A warp's part of a tile is 32 tokens for 8 or 16 query heads.  More heads a key/value head are chunks of 16, head units of their
+// A warp's part of a tile is 32 tokens for 8 or 16 query heads; where two key/value heads are a unit, half of the warps
+// have the one and half the other.  More heads a key/value head are chunks of 16, head units of their
 // own, whose tiles come from L2 for all but the first.  (Two or three groups of four warps that work on the same stages, so
 // that the cache is read once, ran at 3.6 TB/s of codes with 32 heads and 1.9 with 40: no more than chunks reach
 // with nothing in L2, for their arithmetic is the same and one CTA an SM hides less of it.)
 //
 // Measured: 64 sequences of 1 .. 16384 tokens (0.96 GB), H=32 over 8 heads, d=128, capped: 148-151 us, 6.4-6.5 TB/s (heads
-// as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 56 us, 4.8 TB/s (one head a unit 91; 51
-// where each head's tokens lie together); 24 of 2000 .. 8000 tokens, 40 heads over one: 25.7 (chunks of 8 heads 26.5, and 147
+// as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 52-57 us, 4.8-5.2 TB/s; 24 of 2000 .. 8000 tokens, 40 heads over one: 25.7 (chunks of 8 heads 26.5, and 147
 // for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.9, two launches and three waits on memory.  Times in a graph.
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
 template <int D, int NH, bool TWO>
 struct Dec8Cfg {
-  static constexpr int kHeads = 8 * NH;                      // query heads per chunk (TWO: 8 of each key/value head)
-  static constexpr int kRow = TWO ? 2 * D : D;               // bytes of a tile's row
-  static constexpr int kTile = 128;                          // tokens per tile
+  static constexpr int kWarpHeads = 8 * NH;                  // query heads of a warp
+  static constexpr int kHeads = TWO ? 16 : kWarpHeads;       // of a unit: a chunk, or (TWO) eight of each of two key/value heads
+  static constexpr int kRow = TWO && D == 64 ? 128 : D;      // bytes of a tile's row: a token's codes of one head, or of both
+  static constexpr int kTile = TWO && D == 128 ? 64 : 128;   // tokens per tile
+  static constexpr int kPart = kTile / (TWO ? 2 : 4);        // of a warp
   static constexpr int kBlocksOfTile = kTile / 16;
-  static constexpr int kHalf = kTile * kRow;                 // K or V of a tile
+  static constexpr int kHalf = kTile * D * (TWO ? 2 : 1);    // K or V of a tile
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kPerSm = NH * D <= 128 && !TWO ? 3 : 2;
+  static constexpr int kPerSm = NH * D <= 128 ? 3 : 2;
   static constexpr int kStages = (kPerSm == 3 ? 65536 : 98304) / kStage;
-  static constexpr int kORow = D + (NH == 1 || TWO ? 8 : 0); // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
-  static constexpr int kO = 4 * kHeads * kORow * 4;          // the warps' O, in a segment's last stage
+  static constexpr int kORow = D + (NH == 1 ? 8 : 0);        // of a head's O; 8 more: fewer bank conflicts, where a stage has the room
+  static constexpr int kO = 4 * kWarpHeads * kORow * 4;      // the warps' O, in a segment's last stage
   static constexpr int kQStride = D * 2 + 32;                // bytes; 8-byte loads of 4 rows meet every bank once
-  static constexpr int kScaleOff = kStages * kStage;         // K's and V's scales of each stage
-  static constexpr int kQOff = kScaleOff + kStages * (TWO ? 4 : 2) * kBlocksOfTile * 4;
-  static constexpr int kQsOff = kQOff + kHeads * kQStride;    // q's powers of two
-  static constexpr int kMlOff = kQsOff + kHeads * 4;          // (m, l) of each warp's heads
-  static constexpr int kBarOff = kMlOff + 4 * kHeads * 8;
+  static constexpr int kSets = TWO ? 4 : 2;                  // of scales: K's and V's, of one head and the other
+  static constexpr int kScaleLanes = kSets * kBlocksOfTile;
+  static constexpr int kScaleOff = kStages * kStage;         // the scales of each stage
+  static constexpr int kQOff = kScaleOff + kStages * kScaleLanes * 4;
+  static constexpr int kQsOff = kQOff + kHeads * kQStride;   // q's powers of two
+  static constexpr int kMlOff = kQsOff + kHeads * 4;         // (m, l) of each warp's heads
+  static constexpr int kBarOff = kMlOff + 4 * kWarpHeads * 8;
   static constexpr int kMiscOff = kBarOff + 2 * kStages * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
-  static constexpr int kScaleLanes = (TWO ? 4 : 2) * kBlocksOfTile;
-  static_assert(!TWO || (D == 64 && NH == 2), "rows of two heads");
+  static_assert(!TWO || NH == 1, "a warp has heads of one key/value head");
   static_assert(kO <= kStage, "the warps' O fits a stage");
   static_assert(kQOff % 16 == 0 && kQsOff % 16 == 0 && kMlOff % 8 == 0 && kBarOff % 8 == 0 && kScaleLanes <= 32, "layout");
 };
@@ -282,12 +285,12 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------- producer warp
-    // Lane x: block x mod 8 of the tile, of K (x / 8 even) or V, of the unit's second head from 16 on.  It fetches the block's scale,
-    // and lanes below 16, if a piece (the tokens of one page in the tile) starts with their block, the piece's codes.  Past the sequence's end, and for a page index
-    // outside the cache, the page coordinate n_pages, out of bounds, fills the piece with zeros; such a
-    // block's scale is 0.
+    // Lane x: a block of the tile, of K or V, of the unit's one head or of the other.  It fetches the block's scale, and
+    // if a piece (the tokens of one page in the tile) starts with its block, the piece's codes, unless they come with the other
+    // head's in one row.  Past the sequence's end, and for a page index outside the cache, the page coordinate n_pages, out of
+    // bounds, fills the piece with zeros; such a block's scale is 0.
     const bool mine = lane < C::kScaleLanes, is_v = (lane / C::kBlocksOfTile) & 1;
-    const int block = lane % C::kBlocksOfTile, per_page = p.c.page_size >> 4;
+    const int block = lane % C::kBlocksOfTile, per_page = p.c.page_size >> 4, second = lane / (2 * C::kBlocksOfTile);
     const float* scales = is_v ? p.c.v_scales : p.c.k_scales;
     auto page_at = [&](const Place<kTile>& x, int& row) -> int {
       const int tok = x.t * kTile + block * 16;
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
       if (mine && tok < x.n) page = p.c.page_table[x.b * p.c.table_stride + place];
       return page < 0 || page >= p.c.n_pages ? p.c.n_pages : page;
     };
-    const bool starts = lane < 2 * C::kBlocksOfTile && block * 16 % p.piece == 0;
+    const bool starts = mine && block * 16 % p.piece == 0 && (C::kRow == D || second == 0);
     int issued = 0, row;
     int page = page_at(at, row);
     bool ok = true;
@@ -307,10 +310,10 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
         break;
       if (lane == 0) mbar_arrive_expect_tx(&bar_full[slot], C::kStage);
       __syncwarp();
-      const int unit = TWO ? at.u : at.u / p.chunks, hk = TWO ? 2 * unit + lane / 16 : unit;
+      const int hk = TWO ? 2 * at.u + second : at.u / p.chunks;
       if (starts)
-        tma_load_4d(smem + slot * C::kStage + (is_v ? C::kHalf : 0) + block * 16 * C::kRow, is_v ? &tm_v : &tm_k, &bar_full[slot],
-                    0, row, unit, page);
+        tma_load_4d(smem + slot * C::kStage + (is_v ? C::kHalf : 0) + (second * kTile + block * 16) * C::kRow, is_v ? &tm_v : &tm_k,
+                    &bar_full[slot], 0, row, C::kRow == D ? hk : at.u, page);
       if (mine) {
         const bool real = page < p.c.n_pages;
         const float* src = scales + (real ? (static_cast<long long>(page) * p.c.Hkv + hk) * per_page + (row >> 4) : 0);
@@ -334,6 +337,9 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
 
   // ---------------------------------------------------------------- consumer warps
   const uint32_t ring = smem_u32(smem);
+  // TWO: warps 0 and 1 have the unit's first key/value head, 2 and 3 the second.
+  constexpr int kWarpHeads = C::kWarpHeads;
+  const int kv = TWO ? warp >> 1 : 0, row0 = 8 * kv, part0 = C::kPart * (TWO ? warp & 1 : warp);  // first row and token in the tile
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kMlOff);  // [warp][head]
   float* s_qs = reinterpret_cast<float*>(smem + C::kQsOff);
   uint8_t* s_q = smem + C::kQOff;
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     for (int h = 0; h < NH; ++h) {
       slope_next[h] = pair(0.f);
       if (p.slopes) {
-        const int one = head_of(x, 8 * h + gc), two = head_of(x, 8 * h + gc + 1);
+        const int one = head_of(x, row0 + 8 * h + gc), two = head_of(x, row0 + 8 * h + gc + 1);
         if (one >= 0) slope_next[h].x = p.slopes[one] * -kLog2e;
         if (two >= 0) slope_next[h].y = p.slopes[two] * -kLog2e;
       }
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     consumers_sync();
     // B fragments of Q^T in the order of K's codes: four neighbouring columns of head gr.
     auto load_q = [&](int h, int kk) {
-      return *reinterpret_cast<const uint2*>(s_q + (8 * h + gr) * C::kQStride + kk * 32 + 4 * gc);
+      return *reinterpret_cast<const uint2*>(s_q + (row0 + 8 * h + gr) * C::kQStride + kk * 32 + 4 * gc);
     };
     constexpr bool kHoldQ = NH * D <= 128;  // in registers
     uint2 qf[kHoldQ ? NH : 1][kHoldQ ? D / 16 : 1];
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     for (int h = 0; h < NH; ++h) {
       m[h] = mv[h] = pair(kNoScore);
       l[h] = pair(0.f);
-      to_log2[h] = __fmul2_rn(pair(p.cap_out > 0.f ? p.cap_in : p.scale_log2), make_float2(s_qs[8 * h + gc], s_qs[8 * h + gc + 1]));
+      to_log2[h] = __fmul2_rn(pair(p.cap_out > 0.f ? p.cap_in : p.scale_log2), make_float2(s_qs[row0 + 8 * h + gc], s_qs[row0 + 8 * h + gc + 1]));
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[c][h][0] = o[c][h][1] = o[c][h][2] = o[c][h][3] = 0.f;
     }
@@ -434,22 +440,26 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
       // A wait that gave up (the block is aborting) skips the tile but stays in step with the other
       // warps, which it meets at barriers.
       const bool landed = __all_sync(0xffffffffu, mbar_wait(&bar_full[slot], phase, wc, kSite8Full));
-      const uint32_t kb = ring + slot * C::kStage, vb = kb + C::kHalf;
-      const int key0 = (at.t + i) * kTile + 32 * warp;  // this warp's first token
-      if (landed && key0 < at.n) {
-        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes + 2 * warp;
-        const int frow = 32 * warp + (lane & 15), fchunk = lane >> 4;  // what this lane addresses for ldmatrix
+      // The warp's head: a tile of its own, or the row's second half.
+      const uint32_t kb = ring + slot * C::kStage + (TWO && C::kRow == D ? kv * kTile * C::kRow : 0), vb = kb + C::kHalf;
+#pragma unroll 1
+      for (int sub = 0; sub < C::kPart; sub += 32) {
+        const int key0 = (at.t + i) * kTile + part0 + sub;  // 32 tokens from here
+        if (!landed || key0 >= at.n) break;
+        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + slot * C::kScaleLanes +
+                          2 * kv * C::kBlocksOfTile + (part0 + sub) / 16;
+        // What this lane addresses for ldmatrix.
+        const int frow = part0 + sub + (lane & 15), fchunk = (lane >> 4) + (C::kRow == D ? 0 : 4 * kv);
         // S^T = K Q^T of two blocks of 16 tokens.
         float s[2][NH][4] = {};
 #pragma unroll
-        for (int c2 = 0; c2 < C::kRow / 32; ++c2) {
+        for (int c2 = 0; c2 < D / 32; ++c2) {
           uint32_t b4[2][4];
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb) ldsm4(b4[nb], kb + piece_of<C::kRow>(frow + 16 * nb, 2 * c2 + fchunk));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            // The columns of 16 codes, of all of q's heads or (TWO) of the row's first or second key/value head.
-            const int kk = (2 * c2 + half) % (D / 16), only = TWO ? c2 / (D / 32) : -1;
+            const int kk = 2 * c2 + half;
             uint2 b[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h) b[h] = kHoldQ ? qf[kHoldQ ? h : 0][kHoldQ ? kk : 0] : load_q(h, kk);
@@ -458,30 +468,26 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
               const uint32_t x = b4[nb][2 * half], y = b4[nb][2 * half + 1];
               const uint32_t a4[4] = {codes_to_half2(x), codes_to_half2(y), codes_to_half2(x >> 16), codes_to_half2(y >> 16)};
 #pragma unroll
-              for (int h = 0; h < NH; ++h)
-                if (!TWO || h == only) mma_half(s[nb][h], a4, b[h].x, b[h].y);
+              for (int h = 0; h < NH; ++h) mma_half(s[nb][h], a4, b[h].x, b[h].y);
             }
           }
         }
         // Scales; a block past the end has whatever its page holds there.
         const bool ragged = key0 + 32 > at.n;
-        constexpr int kKv = TWO ? 2 : 1;
-        float ks[2][kKv], lgv[2][kKv];
+        float ks[2], lgv[2];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int h = 0; h < kKv; ++h) {
-            const bool inside = key0 + 16 * nb < at.n;
-            ks[nb][h] = inside ? sc[2 * h * C::kBlocksOfTile + nb] : 0.f;
-            lgv[nb][h] = inside ? __log2f(sc[(2 * h + 1) * C::kBlocksOfTile + nb]) : 0.f;
-          }
+        for (int nb = 0; nb < 2; ++nb) {
+          const bool inside = key0 + 16 * nb < at.n;
+          ks[nb] = inside ? sc[nb] : 0.f;
+          lgv[nb] = inside ? __log2f(sc[C::kBlocksOfTile + nb]) : 0.f;
+        }
         // Scores in log2 units: x[block][h][token gr or gr + 8], of heads gc and gc + 1.
         float2 x[2][NH][2];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
-            const float2 f = __fmul2_rn(to_log2[h], pair(ks[nb][TWO ? h : 0]));
+            const float2 f = __fmul2_rn(to_log2[h], pair(ks[nb]));
             x[nb][h][0] = __fmul2_rn(make_float2(s[nb][h][0], s[nb][h][1]), f);
             x[nb][h][1] = __fmul2_rn(make_float2(s[nb][h][2], s[nb][h][3]), f);
           }
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
           sum[h] = pair(0.f);
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb) {
-            const float2 to_v = __fadd2_rn(minus(m[h], mv[h]), pair(lgv[nb][TWO ? h : 0])), by = ex2_pair(to_v);
+            const float2 to_v = __fadd2_rn(minus(m[h], mv[h]), pair(lgv[nb])), by = ex2_pair(to_v);
             fits = fits && to_v.x <= 100.f && to_v.y <= 100.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
             for (int nb = 0; nb < 2; ++nb) {
               const float2 top = max_pair(x[nb][h][0], x[nb][h][1]);
               mx = max_pair(mx, top);
-              mxv = max_pair(mxv, __fadd2_rn(top, pair(lgv[nb][TWO ? h : 0])));
+              mxv = max_pair(mxv, __fadd2_rn(top, pair(lgv[nb])));
             }
 #pragma unroll
             for (int y = 4; y < 32; y <<= 1) {
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 sum[h] = __fadd2_rn(sum[h], ex2_pair(minus(x[nb][h][e], mx)));
-                const float2 v = ex2_pair(__fadd2_rn(x[nb][h][e], minus(pair(lgv[nb][TWO ? h : 0]), mxv)));
+                const float2 v = ex2_pair(__fadd2_rn(x[nb][h][e], minus(pair(lgv[nb]), mxv)));
                 pf[nb][h][e] = pack2<true>(v.x, v.y);
               }
           }
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
           const uint32_t keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
           const uint32_t keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int c2 = 0; c2 < C::kRow / 32; ++c2) {
+          for (int c2 = 0; c2 < D / 32; ++c2) {
             uint32_t b4[4];
             ldsm4_t(b4, vb + piece_of<C::kRow>(frow + 16 * nb, 2 * c2 + fchunk));
             if (ragged) {
@@ -608,8 +614,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
               const uint32_t u = __byte_perm(b4[2 * half], 0, 0x3120), v = __byte_perm(b4[2 * half + 1], 0, 0x3120);
               const uint32_t a4[4] = {codes_to_half2(u), codes_to_half2(u >> 16), codes_to_half2(v), codes_to_half2(v >> 16)};
 #pragma unroll
-              for (int h = 0; h < NH; ++h)
-                if (!TWO || h == c2 / (D / 32)) mma_half(o[(2 * c2 + half) % (D / 16)][h], a4, pf[nb][h][0], pf[nb][h][1]);
+              for (int h = 0; h < NH; ++h) mma_half(o[2 * c2 + half][h], a4, pf[nb][h][0], pf[nb][h][1]);
             }
           }
         }
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
 #pragma unroll
       for (int y = 4; y < 32; y <<= 1)
         all = __fadd2_rn(all, make_float2(__shfl_xor_sync(0xffffffffu, all.x, y), __shfl_xor_sync(0xffffffffu, all.y, y)));
-      const int head = warp * kHeads + 8 * h + gc;
+      const int head = warp * kWarpHeads + 8 * h + gc;
       if (gr == 0) {
         s_ml[head] = make_float2(m[h].x, all.x);
         s_ml[head + 1] = make_float2(m[h].y, all.y);
@@ -658,12 +663,15 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     const int r = threadIdx.x / kThreadsOfRow, in_row = threadIdx.x % kThreadsOfRow;
     const int head = head_of(at, r);
     if (head >= 0) {
-      float M = kNoScore, L = 0.f, wgt[4];
+      // The row's parts: all four warps', or (TWO) those of its key/value head's two.
+      constexpr int kParts = TWO ? 2 : 4;
+      const int from = TWO ? (r >> 3) * 2 * kWarpHeads + (r & 7) : r;
+      float M = kNoScore, L = 0.f, wgt[kParts];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) M = fmaxf(M, s_ml[x * kHeads + r].x);
+      for (int x = 0; x < kParts; ++x) M = fmaxf(M, s_ml[x * kWarpHeads + from].x);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float2 ml = s_ml[x * kHeads + r];
+      for (int x = 0; x < kParts; ++x) {
+        const float2 ml = s_ml[x * kWarpHeads + from];
         wgt[x] = ex2_approx(ml.x - M);
         L += ml.y * wgt[x];
       }
@@ -673,8 +681,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
         const int col = 4 * (in_row + kThreadsOfRow * c);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 v = *reinterpret_cast<const float4*>(s_o + (x * kHeads + r) * C::kORow + col);
+        for (int x = 0; x < kParts; ++x) {
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (x * kWarpHeads + from) * C::kORow + col);
           acc.x = fmaf(wgt[x], v.x, acc.x);
           acc.y = fmaf(wgt[x], v.y, acc.y);
           acc.z = fmaf(wgt[x], v.z, acc.z);
@@ -716,11 +724,13 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   constexpr auto kSwizzle = C::kRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   // L2 fetches no more than a row where the rows of a head lie apart (fa_paged.cu).
   auto map = [&](CUtensorMap* t, const void* x, const Strides& s) {
+    constexpr bool kBoth = C::kRow != D;
     const auto fetch = s.s[0] == C::kRow ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                         : C::kRow == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
-    const int64_t strides[3] = {s.s[0], TWO ? 2 * s.s[1] : s.s[1], s.s[2]};
-    return make_tmap_4d(t, x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C::kRow, a.c.page_size, TWO ? a.c.Hkv / 2 : a.c.Hkv, a.c.n_pages,
-                        strides, C::kRow, p.piece, kSwizzle, fetch);
+                       : C::kRow == 128  ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                         : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+    const int64_t strides[3] = {s.s[0], kBoth ? 2 * s.s[1] : s.s[1], s.s[2]};
+    return make_tmap_4d(t, x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, C::kRow, a.c.page_size, kBoth ? a.c.Hkv / 2 : a.c.Hkv,
+                        a.c.n_pages, strides, C::kRow, p.piece, kSwizzle, fetch);
   };
   if ((e = map(&tk, a.c.k, a.c.sk))) return e;
   if ((e = map(&tv, a.c.v, a.c.sv))) return e;
@@ -736,12 +746,11 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
 template <int D, bool FP16>
 cudaError_t launch_decode8_heads(const PagedDecodeArgs& a, cudaStream_t stream) {
   if (a.H / a.c.Hkv > 8) return launch_decode8<D, 2, false, FP16>(a, stream);
-  if constexpr (D == 64) {
-    // Rows of 64 bytes that lie apart, each beside the next head's: two heads a unit, whose rows of 128 bytes HBM reads faster.
-    const Strides &k = a.c.sk, &v = a.c.sv;
-    if (a.c.Hkv % 2 == 0 && k.s[1] == D && v.s[1] == D && k.s[0] >= 2 * D && v.s[0] >= 2 * D)
-      return launch_decode8<D, 2, true, FP16>(a, stream);
-  }
+  // Rows that lie apart, each beside the next head's: two heads a unit, so that HBM is asked for both at once (64 sequences
+  // of 1 .. 16384 tokens, 8 heads x 128: 152 us, 161 one by one; 131072 tokens of 16 heads x 64: 52, 91 one by one).
+  const Strides &k = a.c.sk, &v = a.c.sv;
+  if (a.c.Hkv % 2 == 0 && k.s[1] == D && v.s[1] == D && k.s[0] >= 2 * D && v.s[0] >= 2 * D)
+    return launch_decode8<D, 1, true, FP16>(a, stream);
   return launch_decode8<D, 1, false, FP16>(a, stream);
 }
 

@@ -129,11 +129,14 @@ def test_decode(case, layout):
 @pytest.mark.parametrize("case", [([300, 0, 77, 129, 1], 10, 10, 64, 32, torch.bfloat16, 30.0, True),
                                   ([1000, 2001], 20, 4, 64, 16, torch.float16, 0.0, True),
                                   ([640, 5], 48, 6, 64, 128, torch.bfloat16, 0.0, False),
+                                  ([901, 130, 0, 64, 65], 8, 2, 128, 16, torch.bfloat16, 20.0, False),
+                                  ([3000, 63], 20, 4, 128, 1024, torch.float16, 0.0, True),
+                                  ([333, 32, 33, 31], 32, 4, 128, 48, torch.bfloat16, 0.0, True),
                                   ([640, 5], 9, 3, 64, 48, torch.bfloat16, 0.0, True),
                                   ([200, 131], 36, 4, 64, 48, torch.float16, 20.0, False)], ids=str)
 @pytest.mark.parametrize("garbage", [False, True])
 def test_rows_of_two_heads(case, garbage):
-    # Heads of 64 beside each other: two of them a unit where there are an even number and up to eight query heads each.
+    # Heads beside each other: two of them a unit where there are an even number and up to eight query heads each.
     _decode(case, "nhd", garbage)
 
 
