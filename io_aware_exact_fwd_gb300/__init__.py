@@ -806,6 +806,7 @@ def fa_paged_resize(page_table, seq_lens, delta, free_pages, free_count, page_si
     positions (int32 [T]) get each new token's place in the cache and in its sequence, -1
     behind the last.  status (int32 [2]): pages that were missing, and sequences that do not
     fit; if either is not 0, nothing has changed and cu_new is 0.  Nothing is read by the host.
+    New outputs are parts of one allocation.
     """
     return _done(load_binding().paged_resize(page_table, seq_lens, delta, free_pages, free_count, page_size, slots, positions,
                                              seq_lens_out, free_count_out, cu_new, status, workspace,

@@ -431,6 +431,15 @@ PyObject* paged_decode_fp8(PyObject* const* a) {
   return st ? PyLong_FromLong(st) : tuple_of({o, lse});
 }
 
+// n elements of a dense tensor from one on, as a tensor of its own on the same memory.  (A slice through the dispatcher takes
+// longer than an allocation.)
+Tensor part_of(const Tensor& all, int64_t from, int64_t n) {
+  Tensor r = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(all.storage()), all.key_set(), all.dtype());
+  r.unsafeGetTensorImpl()->set_storage_offset(all.storage_offset() + from);
+  r.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return r;
+}
+
 // page_table, seq_lens, delta, free_pages, free_count, page_size, slots, positions, seq_lens_out, free_count_out, cu_new,
 // status, workspace, stream
 PyObject* paged_resize(PyObject* const* a) {
@@ -456,22 +465,31 @@ PyObject* paged_resize(PyObject* const* a) {
   int64_t* slots = flat<int64_t>(a[6], "slots", at::kLong, {T}, gpu);
   int32_t* positions = flat<int32_t>(a[7], "positions", at::kInt, {T}, gpu);
   const CallStream s(a[13], gpu);
-  auto out = [&](PyObject* x, const char* name, int64_t n) {
-    const Tensor r = given_or_new(x, name, {n}, t, at::kInt);
-    check(r, name, at::kInt, {n}, gpu);
-    if (!r.is_contiguous()) unfit(PyExc_ValueError, c10::str(name, " must be contiguous"));
+  // The outputs that are not given and the workspace are parts of one allocation (five take longer than the kernel).
+  const int64_t words[5] = {B, 1, B + 1, 2, a[12] == Py_None ? static_cast<int64_t>(fa_paged_resize_workspace_size(whole(B, "B"))) / 4 : 0};
+  int64_t total = words[4];
+  for (int i = 0; i < 4; ++i) total += a[8 + i] == Py_None ? words[i] : 0;
+  const Tensor all = fresh({total}, at::kInt, t);
+  int64_t at_word = 0;
+  auto out = [&](int i, const char* name) {
+    Tensor r;
+    if (a[8 + i] == Py_None) {
+      r = part_of(all, at_word, words[i]);
+      at_word += words[i];
+    } else {
+      r = tensor(a[8 + i], name);
+      check(r, name, at::kInt, {words[i]}, gpu);
+      if (!r.is_contiguous()) unfit(PyExc_ValueError, c10::str(name, " must be contiguous"));
+    }
     return r;
   };
-  const Tensor lens_out = out(a[8], "seq_lens_out", B), count_out = out(a[9], "free_count_out", 1),
-               cu = out(a[10], "cu_new", B + 1), status = out(a[11], "status", 2);
+  const Tensor lens_out = out(0, "seq_lens_out"), count_out = out(1, "free_count_out"), cu = out(2, "cu_new"), status = out(3, "status");
   const int b = whole(B, "B"), w = whole(width, "max_pages"), n = whole(T, "T"), cap = whole(list.numel(), "free_pages"),
             ps = whole(page, "page_size");
-  Tensor own;
   Bytes ws = bytes(a[12], "workspace", gpu);
   if (a[12] == Py_None) {
-    ws.n = fa_paged_resize_workspace_size(b);
-    own = fresh({static_cast<int64_t>(ws.n)}, at::kByte, t);
-    ws.p = own.data_ptr();
+    ws.n = static_cast<size_t>(words[4]) * 4;
+    ws.p = static_cast<int32_t*>(all.data_ptr()) + at_word;
   }
   const int st = call(gpu, [&] {
     auto ints = [](const Tensor& x) { return static_cast<int32_t*>(x.data_ptr()); };
@@ -574,8 +592,11 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
                dk = a[9] != Py_None ? tensor(a[9], "dk") : fresh_like(gk);
   const Layout ldq = layout(dq, "dq", x.type, qs, x.gpu), ldk = layout(dk, "dk", x.type, ks, x.gpu);
   Tensor dqw, dkw, own;
-  if (x.qw) dqw = fresh({x.D}, at::kFloat, gq);
-  if (x.kw) dkw = fresh({x.D}, at::kFloat, gq);
+  if (x.qw || x.kw) {
+    const Tensor both = fresh({2 * x.D}, at::kFloat, gq);
+    if (x.qw) dqw = part_of(both, 0, x.D);
+    if (x.kw) dkw = part_of(both, x.D, x.D);
+  }
   Bytes ws = bytes(a[10], "workspace", x.gpu);
   if (a[10] == Py_None && (x.qw || x.kw)) {
     c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.gpu));
