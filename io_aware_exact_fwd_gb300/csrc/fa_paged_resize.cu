@@ -5,22 +5,23 @@
 // One block scans the sequences: how many pages each takes (grow) or gives back (drop) and how many tokens are new, and the
 // sums of these before each sequence.  All or nothing: if pages are missing or a length does not fit, nothing changes.
 // The rest needs no order: page k of all that are taken, page r of all that come back and new token t each find
-// their sequence by bisection in those sums.  Pages that come back are written behind the free ones, and the pages taken are
-// the last of that longer list, so a page may come back and be taken in one call: its taker reads it from the table of
+// their sequence in those sums, a warp for 32 neighbours together.  Pages that come back are written behind the free ones, and the
+// pages taken are the last of that longer list, so a page may come back and be taken in one call: its taker reads it from the table of
 // the sequence that gave it.  A token's page, if it is a taken one, is found in the same way and not in the table, so
 // nothing waits for the table's new entries.
 //
 // Bound by latency: a launch, two dependent loads of the lengths, the scan; then, for many tokens, by the instructions of
 // their look-ups.  The second part runs in the same block, with the sums in shared memory, where there is little of it, and as a
-// dependent launch over the GPU where there is more.  Measured: 64 sequences a token longer each 4.9 us in a graph; 1000
-// sequences, 600 of them longer by 750k tokens together, the others shorter, 13 us (9.7 MB written).
+// dependent launch over the GPU where there is more.  Measured, in a graph: 64 sequences a token longer each 4.0 us, 1000 of them
+// 6.6 (each row stepping through the sums by itself: 4.7 and 14.8); 1000 sequences, 600 of them longer by 750k tokens
+// together, the others shorter, 14 (9.7 MB written).
 #include "fa_device.cuh"
 #include "fa_internal.h"
 
 namespace fa {
 namespace {
 
-constexpr int kScanThreads = 1024;
+constexpr int kScanThreads = 1024, kSpreadPerSm = 5;
 
 // The workspace, int32: pages taken before each sequence [B + 1], pages given back before each [B + 1], then the list's
 // length on entry.
@@ -83,6 +84,32 @@ __device__ __forceinline__ int owner_of_warp(const int32_t* sums, int B, int x, 
   return lo;
 }
 
+// The same for rows of 32 rising numbers x, one a lane, of which none is before place `from`: 32 sums behind it at once, in
+// registers for as long as they do, and bisection among the lanes.
+struct Owners {
+  const int32_t* sums;
+  int B, lane, from, next;
+  __device__ __forceinline__ Owners(const int32_t* sums_, int B_, int lane_, int from_) : sums(sums_), B(B_), lane(lane_), from(from_) {
+    load();
+  }
+  __device__ __forceinline__ void load() { next = from + 1 + lane < B ? sums[from + 1 + lane] : 0x7fffffff; }
+  __device__ __forceinline__ int of(int x) {
+    int mine = from;
+    while (true) {
+      if (__shfl_sync(0xffffffffu, next, 0) > __shfl_sync(0xffffffffu, x, 31)) return mine;
+      int k = 0;  // how many of them are at most x
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1)
+        if (__shfl_sync(0xffffffffu, next, k + w - 1) <= x) k += w;
+      k += __shfl_sync(0xffffffffu, next, k) <= x ? 1 : 0;
+      if (mine == from) mine += k;
+      if (!__any_sync(0xffffffffu, mine == from + 32)) return mine;
+      from += 32;
+      load();
+    }
+  }
+};
+
 // What the second part goes by: the sums, the new lengths, and the list's length on entry.
 struct Plan {
   const int32_t *grow, *drop, *cu, *lens;
@@ -99,36 +126,75 @@ __device__ __forceinline__ const int32_t* taken(const PagedResizeArgs& a, const 
   return place >= p.count ? given_back(a, p, place - p.count) : a.free_pages + place;
 }
 
-// The second part: thread `at` of `all`, of whole warps.  (After a refusal there are no pages and no new tokens.)
+// The second part: thread `at` of `all`, of whole warps.  (After a refusal there are no pages and no new tokens.)  A warp takes
+// UNROLL x 32 pages or rows after each other: the first one's sequence by all lanes, the others' from there on; their loads
+// together.
+template <int UNROLL>
 __device__ __forceinline__ void pages(const PagedResizeArgs& a, const Plan& p, int at, int all) {
-  const int grow = p.grow[a.B], drop = p.drop[a.B];
-  for (long long r = at; r < drop; r += all) a.free_pages[p.count + r] = *given_back(a, p, static_cast<int>(r));
-  for (long long k = at; k < grow; k += all) {
-    const int b = owner_of(p.grow, a.B, static_cast<int>(k));
-    const int had = pages_of(a, p.lens[b]) - (p.grow[b + 1] - p.grow[b]);
-    a.page_table[b * a.table_stride + had + (k - p.grow[b])] = *taken(a, p, static_cast<int>(k));
+  const int grow = p.grow[a.B], drop = p.drop[a.B], lane = at & 31;
+  const long long start = static_cast<long long>(at - lane) * UNROLL, step = static_cast<long long>(all) * UNROLL;
+  for (long long r0 = start; r0 < drop; r0 += step) {
+    Owners owners(p.drop, a.B, lane, owner_of_warp(p.drop, a.B, static_cast<int>(r0), lane));
+    const int32_t* from[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      from[i] = nullptr;
+      if (r0 + 32 * i >= drop) continue;
+      const long long r = r0 + 32 * i + lane;
+      const int own = owners.of(static_cast<int>(min(r, drop - 1LL)));
+      if (r < drop) from[i] = a.page_table + (own * a.table_stride + pages_of(a, p.lens[own]) + (r - p.drop[own]));
+    }
+    int page[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) page[i] = from[i] ? *from[i] : 0;
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i)
+      if (from[i]) a.free_pages[p.count + r0 + 32 * i + lane] = page[i];
+  }
+  for (long long k0 = start; k0 < grow; k0 += step) {
+    Owners owners(p.grow, a.B, lane, owner_of_warp(p.grow, a.B, static_cast<int>(k0), lane));
+    const int32_t* from[UNROLL];
+    int32_t* to[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      from[i] = nullptr;
+      if (k0 + 32 * i >= grow) continue;
+      const long long k = k0 + 32 * i + lane;
+      const int own = owners.of(static_cast<int>(min(k, grow - 1LL)));
+      if (k < grow) {
+        const int had = pages_of(a, p.lens[own]) - (p.grow[own + 1] - p.grow[own]);
+        to[i] = a.page_table + (own * a.table_stride + had + (k - p.grow[own]));
+        from[i] = taken(a, p, static_cast<int>(k));
+      }
+    }
+    int page[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) page[i] = from[i] ? *from[i] : 0;
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i)
+      if (from[i]) *to[i] = page[i];
   }
 }
-// UNROLL x 32 rows a warp: the first one's sequence by all lanes, the others' from there on; the pages' loads together.
 template <int UNROLL>
 __device__ __forceinline__ void tokens(const PagedResizeArgs& a, const Plan& p, int at, int all) {
   const int total = p.cu[a.B], lane = at & 31;
   for (long long t0 = static_cast<long long>(at - lane) * UNROLL; t0 < a.T; t0 += static_cast<long long>(all) * UNROLL) {
-    int b = t0 < total ? owner_of_warp(p.cu, a.B, static_cast<int>(t0), lane) : 0;
+    Owners owners(p.cu, a.B, lane, t0 < total ? owner_of_warp(p.cu, a.B, static_cast<int>(t0), lane) : 0);
     const int32_t* from[UNROLL];
     int pos[UNROLL], row[UNROLL];
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
-      const long long t = t0 + 32 * i + lane;
       pos[i] = -1;
       from[i] = nullptr;
+      if (t0 + 32 * i >= total) continue;
+      const long long t = t0 + 32 * i + lane;
+      const int own = owners.of(static_cast<int>(min(t, total - 1LL)));
       if (t >= total || t >= a.T) continue;
-      while (p.cu[b + 1] <= t) ++b;
-      pos[i] = p.lens[b] - (p.cu[b + 1] - static_cast<int>(t));
+      pos[i] = p.lens[own] - (p.cu[own + 1] - static_cast<int>(t));
       if (!a.slots) continue;
-      const int place = a.per_page(pos[i]), had = pages_of(a, p.lens[b]) - (p.grow[b + 1] - p.grow[b]);
+      const int place = a.per_page(pos[i]), had = pages_of(a, p.lens[own]) - (p.grow[own + 1] - p.grow[own]);
       row[i] = pos[i] - place * a.page_size;
-      from[i] = place < had ? a.page_table + (b * a.table_stride + place) : taken(a, p, p.grow[b] + place - had);
+      from[i] = place < had ? a.page_table + (own * a.table_stride + place) : taken(a, p, p.grow[own] + place - had);
     }
     int page[UNROLL];
 #pragma unroll
@@ -223,18 +289,20 @@ __global__ void __launch_bounds__(kScanThreads) resize_scan_kernel(const __grid_
   // Half of the block for the pages, half for the tokens: each waits for loads that depend on each other.
   const Plan p{s_sums[0], s_sums[1], s_sums[2], s_lens, count};
   constexpr int kHalf = kScanThreads / 2;
-  if (threadIdx.x < kHalf) pages(a, p, threadIdx.x, kHalf);
+  if (threadIdx.x < kHalf) pages<8>(a, p, threadIdx.x, kHalf);
   else tokens<1>(a, p, threadIdx.x - kHalf, kHalf);
 }
 
+// The rows go to all warps, in groups of 32, UNROLL at a time.
 // (With the sums copied to each block's shared memory first: 12.7 us for 1000 sequences and 750k new tokens, 13.1 so.)
-__global__ void __launch_bounds__(256) resize_spread_kernel(const __grid_constant__ PagedResizeArgs a) {
+template <int UNROLL>
+__global__ void __launch_bounds__(256, kSpreadPerSm) resize_spread_kernel(const __grid_constant__ PagedResizeArgs a) {
   grid_wait();
   const Sums s = sums_of(a.workspace, a.B);
   const Plan p{s.grow, s.drop, a.cu_new, a.lens_out, *s.count};
   const int at = static_cast<int>(blockIdx.x * 256 + threadIdx.x), all = static_cast<int>(gridDim.x * 256);
-  tokens<4>(a, p, at, all);
-  pages(a, p, all - 32 - (at & ~31) + (at & 31), all);  // (from the other end: the last blocks have fewer tokens)
+  tokens<UNROLL>(a, p, at, all);
+  pages<1>(a, p, all - 32 - (at & ~31) + (at & 31), all);  // (from the other end: the last blocks have fewer tokens)
 }
 
 }  // namespace
@@ -242,13 +310,17 @@ __global__ void __launch_bounds__(256) resize_spread_kernel(const __grid_constan
 size_t paged_resize_workspace(int B) { return (2 * (static_cast<size_t>(B) + 1) + 1) * sizeof(int32_t); }
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
-  // One block where that is quicker: 64 sequences a token longer each 4.9 us, and 43 (the GPU 17) at its worst, 1000
-  // sequences of which 400 end with 100 pages each.
+  // One block where that is quicker most of the time: 64 sequences a token longer each 4.0 us, 4.7 with the second launch.  Long
+  // sequences that end take longer so, 0.5 us for 1000 pages, but each page comes back once for 16 or more such steps.
   const int alone = a.T <= 2 * kScanThreads && a.B <= kScanThreads / 4;
   resize_scan_kernel<<<1, kScanThreads, 0, stream>>>(a, alone);
   const cudaError_t e = cudaGetLastError();
   if (e || alone) return e;
-  return launch_dependent(resize_spread_kernel, static_cast<unsigned>(sm_count()) * 6, 256, 0, stream, a);
+  // More than 32 rows a warp: four groups at a time (1000 sequences, 750k rows: 14 us, 17.8 one by one); else one group, for
+  // there may be many sequences with few rows each (1000 of one: 6.6 us, 9.7 in fours).
+  const unsigned blocks = static_cast<unsigned>(sm_count()) * kSpreadPerSm;
+  const auto kern = static_cast<unsigned>(a.T) > blocks * 256 ? resize_spread_kernel<4> : resize_spread_kernel<1>;
+  return launch_dependent(kern, blocks, 256, 0, stream, a);
 }
 
 }  // namespace fa

@@ -463,6 +463,15 @@ def test_resize_of_many(B, seed):
     _resize(lens, delta, 16, 50, 0, new, False, seed)
 
 
+@pytest.mark.parametrize("rows", [700, 3000, 400000])  # one block; over the GPU, some rows a warp and many
+@pytest.mark.parametrize("B,every,by", [(256, 1, 1), (250, 40, 33), (1000, 1, 1), (1000, 333, 200), (400, 399, 1), (300, 2, -1)])
+def test_resize_with_idle_sequences(B, every, by, rows):
+    # Rows, and pages, of neighbours far apart, or of many sequences.
+    lens = [(7 * i) % 90 for i in range(B)]
+    delta = [0 if i % every else by if by > 0 else -lens[i] for i in range(B)]
+    _resize(lens, delta, 16, 32, 15 * B, rows, False, B)
+
+
 def test_captured_resize():
     # In place, replayed: every sequence one token longer each time, from the device's own numbers.
     B, page, width = 5, 16, 6
