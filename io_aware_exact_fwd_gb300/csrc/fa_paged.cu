@@ -529,8 +529,7 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
   kern<<<static_cast<unsigned>(paged_decode_ctas(p.group)), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
-  return launch_dependent(decode_join_kernel<D, FP16>, static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H), 128, 0,
-                          stream, p, C::kRows);
+  return launch_join<D, FP16>(p, C::kRows, stream);
 }
 
 template <int D, bool FP16>

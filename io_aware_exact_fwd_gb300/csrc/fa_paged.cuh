@@ -177,42 +177,51 @@ __device__ __forceinline__ bool share_of_tiles(const DecParams& p, int units, lo
   return true;
 }
 
-// Joins the parts of heads whose tiles lie in several CTAs' shares, and writes the
-// result of empty sequences.  One block per (sequence, query head): warp x takes parts
-// x, x + 4, ...
+// Where the tiles of one sequence's query head are: CTAs c0 to c1 had them.
+struct HeadParts {
+  int b, head, row, c0, c1;  // row: of the unit's
+  long long w0, share;
+  bool empty;
+  __device__ __forceinline__ HeadParts(const DecParams& p, int rows_per_part, int x) {
+    b = x / p.H;
+    head = x - b * p.H;
+    const int hk = head / p.group, in_group = head % p.group;
+    const int u = p.two ? hk / 2 : hk * p.chunks + in_group / rows_per_part;
+    row = p.two ? 8 * (hk & 1) + in_group : in_group % rows_per_part;
+    const long long first = p.offsets[b], tiles = quotient(p.offsets[b + 1] - first, units_of(p));
+    share = p.offsets[p.c.B + 1];
+    w0 = first + u * tiles;
+    empty = tiles == 0;
+    c0 = empty ? 0 : static_cast<int>(quotient(w0, share));
+    c1 = empty ? 0 : static_cast<int>(quotient(w0 + tiles - 1, share));
+  }
+  // Not written yet by the one CTA that had all of it.
+  __device__ __forceinline__ bool open() const { return empty || c0 != c1; }
+};
+
+// A block joins one head's parts: warp x takes parts x, x + 4, ...
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_part) {
-  __shared__ float2 s_ml[4];
-  __shared__ __align__(16) float s_o[4][D];
-  grid_wait();  // the parts are written
-  const int b = blockIdx.x / p.H, head = blockIdx.x % p.H;
+__device__ __forceinline__ void join_head(const DecParams& p, const HeadParts& h, int rows_per_part, float2 (&s_ml)[4],
+                                          float (&s_o)[4][D]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = D / 32;
-  const int hk = head / p.group, in_group = head % p.group;
-  const int u = p.two ? hk / 2 : hk * p.chunks + in_group / rows_per_part;
-  const int row = p.two ? 8 * (hk & 1) + in_group : in_group % rows_per_part;
-  const long long first = p.offsets[b], tiles = quotient(p.offsets[b + 1] - first, units_of(p));
-  const long long share = p.offsets[p.c.B + 1];
-  const long long w0 = first + u * tiles;
-  uint16_t* dst = p.o + b * p.so.s[1] + head * p.so.s[0];
-  float* lse = p.lse + static_cast<size_t>(b) * p.H + head;
-  if (tiles == 0) {
+  uint16_t* dst = p.o + h.b * p.so.s[1] + h.head * p.so.s[0];
+  float* lse = p.lse + static_cast<size_t>(h.b) * p.H + h.head;
+  if (h.empty) {
     if (threadIdx.x < D / 8) *reinterpret_cast<uint4*>(dst + 8 * threadIdx.x) = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) *lse = -INFINITY;
     return;
   }
-  const int c0 = static_cast<int>(quotient(w0, share)), c1 = static_cast<int>(quotient(w0 + tiles - 1, share));
-  if (c0 == c1) return;  // one CTA had the whole head and wrote it
   float m = kNoScore, l = 0.f, acc[E] = {};
 #pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 4) {
+  for (int c = h.c0 + warp; c <= h.c1; c += 4) {
     // A CTA's first segment has slot 0; only the first part can be another segment of its CTA.
-    const int slot = 2 * c + (c * share >= w0 ? 0 : 1);
+    const int slot = 2 * c + (c * h.share >= h.w0 ? 0 : 1);
     const float* part = p.part + static_cast<size_t>(slot) * rows_per_part * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(part + rows_per_part * D + 2 * row);
+    const float2 ml = *reinterpret_cast<const float2*>(part + rows_per_part * D + 2 * h.row);
     float v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = part[row * D + lane + 32 * e];
+    for (int e = 0; e < E; ++e) v[e] = part[h.row * D + lane + 32 * e];
     const float mn = fmaxf(m, ml.x), wa = ex2_approx(m - mn), wb = ex2_approx(ml.x - mn);
     l = l * wa + ml.y * wb;
 #pragma unroll
@@ -238,6 +247,43 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
     reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack2<FP16>(sum.x / L, sum.y / L);
     if (threadIdx.x == 0) *lse = (M + log2f(L)) * kLn2;
   }
+}
+
+// Joins the parts of heads whose tiles lie in several CTAs' shares, and writes the
+// result of empty sequences.  A block per (sequence, query head); where these would be more than 16 an SM, a block has every
+// gridDim-th and each thread looks first at one, whether there is something to do: most of so many heads are whole (the 8-bit decode of
+// 109 sequences with 9 .. 18 tokens, 192 heads: 47 us with a block each, 30 so).
+template <int D, bool FP16>
+__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_part) {
+  __shared__ float2 s_ml[4];
+  __shared__ __align__(16) float s_o[4][D];
+  __shared__ uint32_t s_open[4];
+  grid_wait();  // the parts are written
+  const int all = p.c.B * p.H, step = gridDim.x;
+  if (all == step) {
+    const HeadParts h(p, rows_per_part, blockIdx.x);
+    if (h.open()) join_head<D, FP16>(p, h, rows_per_part, s_ml, s_o);
+    return;
+  }
+  for (long long first = blockIdx.x; first < all; first += 128LL * step) {
+    const long long mine = first + static_cast<long long>(threadIdx.x) * step;
+    const bool open = mine < all && HeadParts(p, rows_per_part, static_cast<int>(mine)).open();
+    const uint32_t some = __ballot_sync(0xffffffffu, open);
+    if ((threadIdx.x & 31) == 0) s_open[threadIdx.x >> 5] = some;
+    __syncthreads();
+    for (int w = 0; w < 4; ++w)
+      for (uint32_t todo = s_open[w]; todo; todo &= todo - 1) {
+        const int x = static_cast<int>(first + static_cast<long long>(32 * w + __ffs(todo) - 1) * step);
+        join_head<D, FP16>(p, HeadParts(p, rows_per_part, x), rows_per_part, s_ml, s_o);
+        __syncthreads();  // (s_ml and s_o are free)
+      }
+    __syncthreads();
+  }
+}
+template <int D, bool FP16>
+cudaError_t launch_join(const DecParams& p, int rows_per_part, cudaStream_t stream) {
+  const unsigned heads = static_cast<unsigned>(p.c.B) * static_cast<unsigned>(p.H), most = static_cast<unsigned>(sm_count()) * 16;
+  return launch_dependent(decode_join_kernel<D, FP16>, heads < most ? heads : most, 128, 0, stream, p, rows_per_part);
 }
 
 // Query heads per chunk (16 MT) and the CTAs of the 16-bit decode.  Up to 16 heads share a key/value head

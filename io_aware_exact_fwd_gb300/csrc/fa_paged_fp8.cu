@@ -739,8 +739,7 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   static_assert(C::kPerSm * C::kHeads <= 48, "the workspace's parts");
   kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
-  return launch_dependent(decode_join_kernel<D, FP16>, static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.H), 128, 0,
-                          stream, p, C::kHeads);
+  return launch_join<D, FP16>(p, C::kHeads, stream);
 }
 
 template <int D, bool FP16>

@@ -140,6 +140,13 @@ def test_rows_of_two_heads(case, garbage):
     _decode(case, "nhd", garbage)
 
 
+@pytest.mark.parametrize("case", [([0, 300, 1, 17, 900, 0, 40, 16, 129, 31] * 20, 16, 2, 64, 16, torch.bfloat16, 0.0, True),
+                                  ([5, 0, 700, 16, 130] * 10, 80, 4, 128, 64, torch.float16, 30.0, False)], ids=["3200", "4000"])
+def test_many_heads(case):
+    # More heads than blocks that join their parts: some whole, some in parts, some of empty sequences.
+    _decode(case, "nhd", False)
+
+
 @pytest.mark.parametrize("case", [CASES[2], CASES[3], CASES[4], CASES[5], CASES[7]], ids=str)
 def test_what_lies_behind_the_last_token_does_not_matter(case):
     _decode(case, "nhd", True)

@@ -472,3 +472,10 @@ def test_decode_agrees_with_the_forward_at_a_large_cap():
     # The bound of either LSE, twice: products of at most 10 (sums of |q k| / 8) to 80 half steps and 2e-6, in
     # the LSE twice, and 4 half steps of the LSE.
     assert float((lse - want[:, :, -1]).abs().max()) <= 2 * (2 * (80 * 10 * 2.0 ** -24 + 2e-6) + 4 * 10 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("case", [([0, 300, 1, 17, 900, 0, 40, 16, 129, 31] * 20, 16, 2, 64, 16, torch.bfloat16, 0.0, True),
+                                  ([5, 0, 700, 16, 130] * 10, 80, 4, 128, 64, torch.float16, 30.0, False)], ids=["3200", "4000"])
+def test_many_heads(case):
+    # More heads than blocks that join their parts: some whole, some in parts, some of empty sequences.
+    _decode(case, "nhd", None)
