@@ -101,6 +101,14 @@ def test_backward(case):
     assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("case", [_case(N=1250, H=12, Hkv=1, d=128), _case(N=2600, H=12, Hkv=3, layout="qkv", dtype=torch.float16),
+                                  _case(B=3, N=1667, H=7, Hkv=7), _case(B=2, N=1217, H=24, Hkv=5, layout="bnhd")], ids=str)
+def test_tokens_in_rounds(case):
+    # As many tokens that warps take some after each other, with all of their heads or a part.
+    test_forward(case)
+    test_backward(case)
+
+
 def test_in_place_and_into_views():
     case = _case(B=2, N=70, H=6, Hkv=2, d=128, layout="qkv", rot=64)
     q, k, gq, gk, kw, _ = _state(case)
