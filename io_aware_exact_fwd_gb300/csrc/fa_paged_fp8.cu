@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
 //
 // Measured: 64 sequences of 1 .. 16384 tokens (0.96 GB), H=32 over 8 heads, d=128, capped: 148-151 us, 6.4-6.5 TB/s (heads
 // as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 52-57 us, 4.8-5.2 TB/s; 24 of 2000 .. 8000 tokens, 40 heads over one: 25.7 (chunks of 8 heads 26.5, and 147
-// for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.9, two launches and three waits on memory.  Times in a graph.
+// for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.6, two launches and three waits on memory.  Times in a graph.
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
 template <int D, int NH, bool TWO>
