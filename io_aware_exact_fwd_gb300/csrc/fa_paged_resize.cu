@@ -12,7 +12,7 @@
 //
 // Bound by latency: a launch, two dependent loads of the lengths, the scan; then, for many tokens, by the instructions of
 // their look-ups.  The second part runs in the same block, with the sums in shared memory, where there is little of it, and as a
-// dependent launch over the GPU where there is more.  Measured, in a graph: 64 sequences a token longer each 4.0 us, 1000 of them
+// dependent launch over the GPU where there is more.  Measured, in a graph: 64 sequences a token longer each 3.9 us, 1000 of them
 // 6.6 (each row stepping through the sums by itself: 4.7 and 14.8); 1000 sequences, 600 of them longer by 750k tokens
 // together, the others shorter, 14 (9.7 MB written).
 #include "fa_device.cuh"
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kScanThreads) resize_scan_kernel(const __grid_
   // Half of the block for the pages, half for the tokens: each waits for loads that depend on each other.
   const Plan p{s_sums[0], s_sums[1], s_sums[2], s_lens, count};
   constexpr int kHalf = kScanThreads / 2;
-  if (threadIdx.x < kHalf) pages<8>(a, p, threadIdx.x, kHalf);
+  if (threadIdx.x < kHalf) pages<4>(a, p, threadIdx.x, kHalf);
   else tokens<1>(a, p, threadIdx.x - kHalf, kHalf);
 }
 
@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(256, kSpreadPerSm) resize_spread_kernel(const 
 size_t paged_resize_workspace(int B) { return (2 * (static_cast<size_t>(B) + 1) + 1) * sizeof(int32_t); }
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
-  // One block where that is quicker most of the time: 64 sequences a token longer each 4.0 us, 4.7 with the second launch.  Long
-  // sequences that end take longer so, 0.5 us for 1000 pages, but each page comes back once for 16 or more such steps.
+  // One block where that is quicker most of the time: 64 sequences a token longer each 3.9 us, 4.7 with the second launch.  Long
+  // sequences that end take longer so, 0.6 us for 1000 pages, but each page comes back once for 16 or more such steps.
   const int alone = a.T <= 2 * kScanThreads && a.B <= kScanThreads / 4;
   resize_scan_kernel<<<1, kScanThreads, 0, stream>>>(a, alone);
   const cudaError_t e = cudaGetLastError();
