@@ -131,14 +131,17 @@ __device__ __forceinline__ int rows_of(const QkGrid& g, int side) {
   return gridDim.y == 1 || static_cast<int>(blockIdx.y) == side ? g.rows[side] : 0;
 }
 
-// Cosines, sines and their negatives of this lane's eight pairs (1 and 0 where its columns are not rotated), in pairs.
+// Cosines, sines and their negatives of this lane's eight pairs, in pairs.
 struct Angles {
   float2 c[4], s[4], ns[4];
 };
 // x[8] of a lane turned by them: the pairs are its first piece's values with its second's, or with PAIRS the two of
-// each x[j].
-template <bool PAIRS>
-__device__ __forceinline__ void rotate(float2 (&x)[8], const Angles& g) {
+// each x[j].  Where not all columns are rotated (PART), a lane past those that are (turned false) leaves its values alone:
+// times 1 and 0 an infinity would make the value beside it NaN.  A build of its own: with the choice in every row's
+// way the gradient of 16384 tokens of 32 heads x 128, whole heads rotated, took 69.9 us for 66.7.
+template <bool PAIRS, bool PART>
+__device__ __forceinline__ void rotate(float2 (&x)[8], const Angles& g, bool turned) {
+  if (PART && !turned) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (PAIRS) {
@@ -173,10 +176,12 @@ template <int D>
 struct Lane {
   static constexpr int kLanes = D / 16, kGroups = 32 / kLanes;  // lanes of a row, rows of a warp
   int lane, c0, c1, head, token;
+  bool turned;  // its columns are among the rotated (rot is a multiple of 16: all of them or none)
   __device__ __forceinline__ Lane(const QkArgs& a, const QkGrid& g) {
     const int x = threadIdx.x & 31, group = x / kLanes;
     lane = x % kLanes;
-    if (a.pairs || lane >= a.rot / 16) {
+    turned = lane < a.rot / 16;
+    if (a.pairs || !turned) {
       c0 = 16 * lane;  // (past the rotated columns the pieces of both kinds follow each other)
       c1 = c0 + 8;
     } else {
@@ -256,7 +261,7 @@ struct Turns {
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
       const int i = (threadIdx.x & 31) + 32 * k;
-      turns[k] = i < a.rot / 2 ? turns_of(__ldg(a.inv_freq + i)) : 0;  // (0: cos = 1, sin = 0)
+      turns[k] = i < a.rot / 2 ? turns_of(__ldg(a.inv_freq + i)) : 0;
     }
   }
   template <bool BACK>
@@ -333,7 +338,7 @@ struct Share {
   }
 };
 
-template <int D, bool FP16, bool PAIRS>
+template <int D, bool FP16, bool PAIRS, bool PART>
 __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
     qk_forward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
   __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
@@ -373,11 +378,11 @@ __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
           const float2 r = twice(rsqrtf(row_sum<D>(dot16(x, x)) * (1.f / D) + a.eps));
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], w[j]);
-          rotate<PAIRS>(x, turn_by);
+          rotate<PAIRS, PART>(x, turn_by, me.turned);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], r);
         } else {
-          rotate<PAIRS>(x, turn_by);
+          rotate<PAIRS, PART>(x, turn_by, me.turned);
         }
         if (h < heads) {
           *reinterpret_cast<uint4*>(out) = pack8<FP16>(x);
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kQkThreads, kForwardBlocksPerSm)
 // The gradient.  Blocks stay on the GPU and their warps take tokens in turn, so that the weights' gradients add up in a thread; each
 // block's sums go to the workspace and a second kernel adds them in order: the same bits on every run.  A thread's sums of the side that
 // it is not at lie in shared memory: 16 registers less.
-template <int D, bool FP16, bool PAIRS>
+template <int D, bool FP16, bool PAIRS, bool PART>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ QkGrid g) {
   __shared__ __align__(16) float2 angles[kQkThreads / 32][Lane<D>::kGroups * D / 2];
   __shared__ __align__(16) float weights[2][D];
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_backward_kernel(const __grid
             unpack8<FP16>(from[kQkThreads], x + 4);
           }
           fetch.row();  // into the place of the row before this one
-          rotate<PAIRS>(y, turn_by);
+          rotate<PAIRS, PART>(y, turn_by, me.turned);
           if (a.norm) {
             const float2 r = twice(rsqrtf(row_sum<D>(dot16(x, x)) * (1.f / D) + a.eps));
 #pragma unroll
@@ -542,19 +547,19 @@ QkGrid grid_of(const QkArgs& a, long long most, dim3* blocks) {
   return g;
 }
 
-template <int D, bool FP16, bool PAIRS>
+template <int D, bool FP16, bool PAIRS, bool PART>
 cudaError_t launch_forward(const QkArgs& a, cudaStream_t stream) {
   dim3 blocks;
   const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kForwardBlocksPerSm * (kQkThreads / 32), &blocks);
-  qk_forward_kernel<D, FP16, PAIRS><<<blocks, kQkThreads, kFetched, stream>>>(a, g);  // (48 KB with what is static: no attribute)
+  qk_forward_kernel<D, FP16, PAIRS, PART><<<blocks, kQkThreads, kFetched, stream>>>(a, g);  // (48 KB with what is static: no attribute)
   return cudaGetLastError();
 }
 
-template <int D, bool FP16, bool PAIRS>
+template <int D, bool FP16, bool PAIRS, bool PART>
 cudaError_t launch_backward(const QkArgs& a, cudaStream_t stream) {
   dim3 blocks;
   const QkGrid g = grid_of<D>(a, static_cast<long long>(sm_count()) * kBackBlocksPerSm * (kQkThreads / 32), &blocks);
-  auto kern = qk_backward_kernel<D, FP16, PAIRS>;
+  auto kern = qk_backward_kernel<D, FP16, PAIRS, PART>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSums + 2 * kFetched));
   if (e) return e;
   kern<<<blocks, kQkThreads, kSums + 2 * kFetched, stream>>>(a, g);
@@ -563,10 +568,14 @@ cudaError_t launch_backward(const QkArgs& a, cudaStream_t stream) {
   return launch_dependent(qk_weights_kernel<D>, 2, 1024, 0, stream, a, static_cast<int>(blocks.x * blocks.y));
 }
 
+template <int D, bool FP16, bool PAIRS>
+cudaError_t launch(const QkArgs& a, bool back, cudaStream_t stream) {
+  if (a.rot < D) return back ? launch_backward<D, FP16, PAIRS, true>(a, stream) : launch_forward<D, FP16, PAIRS, true>(a, stream);
+  return back ? launch_backward<D, FP16, PAIRS, false>(a, stream) : launch_forward<D, FP16, PAIRS, false>(a, stream);
+}
 template <int D, bool FP16>
 cudaError_t launch(const QkArgs& a, bool back, cudaStream_t stream) {
-  if (a.pairs) return back ? launch_backward<D, FP16, true>(a, stream) : launch_forward<D, FP16, true>(a, stream);
-  return back ? launch_backward<D, FP16, false>(a, stream) : launch_forward<D, FP16, false>(a, stream);
+  return a.pairs ? launch<D, FP16, true>(a, back, stream) : launch<D, FP16, false>(a, back, stream);
 }
 cudaError_t launch(const QkArgs& a, bool back, cudaStream_t stream) {
   if (a.d == 64) return a.fp16 ? launch<64, true>(a, back, stream) : launch<64, false>(a, back, stream);

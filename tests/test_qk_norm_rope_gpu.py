@@ -262,3 +262,51 @@ def test_refusals_in_the_binding():
         fa.fa_qk_norm_rope_bwd(q, k, q, k[:, :, :4])
     with pytest.raises(fa.FAError):
         fa.fa_qk_norm_rope_bwd(q, k, q, k, q_weight=w, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+# Columns past the rotated ones: each is its own, whatever stands in the others.
+@pytest.mark.parametrize("d,rot,pairs", [(64, 0, False), (64, 16, False), (64, 16, True), (128, 48, False), (128, 48, True)])
+def test_infinities_and_nan_in_columns_that_are_not_rotated(d, rot, pairs):
+    g = torch.Generator().manual_seed(7)
+    kw = dict(inv_freq=_freq(rot), norm=False, interleaved=pairs)
+    clean = [torch.randn(1, h, 9, d, generator=g).bfloat16() for h in (3, 2)]
+    x = [t.clone() for t in clean]
+    for t, c in zip(x, clean):
+        t[0, 0, 1, rot + 3] = float("inf")
+        t[0, 1, 2, d - 1] = float("-inf")
+        t[0, 0, 4, rot + 8] = float("nan")
+        t[0, 1, 5, rot:] = -0.0
+        t[0, 1, 6, rot:rot + 2] = torch.tensor([float("inf"), float("nan")])
+        c[..., rot:][~torch.isfinite(t[..., rot:])] = 0.0
+    x, clean = ([t.cuda() for t in y] for y in (x, clean))
+    for call in (lambda q, k: fa.fa_qk_norm_rope(q, k, **kw), lambda q, k: fa.fa_qk_norm_rope_bwd(q, k, q, k, **kw)[:2]):
+        got, want = call(*x), call(*clean)
+        fa.fa_sync_check()
+        for y, z, t in zip(got, want, x):
+            nan = t[..., rot:].isnan()
+            assert torch.equal(y[..., rot:].isnan(), nan)
+            assert torch.equal(y[..., rot:].view(torch.int16)[~nan], t[..., rot:].view(torch.int16)[~nan])
+            assert torch.equal(y[..., :rot], z[..., :rot])
+
+
+@pytest.mark.parametrize("d,rot,pairs", [(64, 0, False), (64, 32, True), (128, 32, False)])
+def test_an_infinite_gradient_reaches_its_own_weight_alone(d, rot, pairs):
+    case = _case(N=40, H=2, d=d, rot=rot, pairs=pairs)
+    q, k, gq, gk, kw, _ = _state(case)
+    gq[0, 1, 7, rot + 5], gk[0, 0, 3, d - 1] = 0.0, 0.0
+    want = fa.fa_qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    gq[0, 1, 7, rot + 5], gk[0, 0, 3, d - 1] = float("inf"), float("nan")
+    got = fa.fa_qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    fa.fa_sync_check()
+    for y, z, at in ((got[2], want[2], rot + 5), (got[3], want[3], d - 1)):
+        rest = torch.arange(d, device="cuda") != at
+        assert not y[at].isfinite() and torch.equal(y[rest], z[rest])
+
+
+def test_norm_of_a_row_with_an_infinity():
+    # Its mean square is infinite: finite values become 0, the infinity is divided by itself.
+    x = torch.ones(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    x[0, 0, 1, 40] = float("inf")
+    y, _ = fa.fa_qk_norm_rope(x, x, inv_freq=_freq(32))
+    fa.fa_sync_check()
+    assert y[0, 0, 0].isfinite().all() and y[0, 0, 1, 40].isnan() and y[0, 0, 1].isnan().sum() == 1 and y[0, 0, 1].nansum() == 0
