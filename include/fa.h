@@ -627,7 +627,8 @@ FA_API int fa_paged_decode(const void* q, const int64_t* q_strides, const void* 
  * code falls below the type's normal range.  What a block held before its first token (page reuse) does not
  * matter, nor is it changed behind the last new one.  Infinities do not count for e and saturate; a NaN
  * does not count either and stays a NaN.  A scale in a half-filled block that is no power of two (not
- * this call's) is rounded up to one.  Otherwise as fa_paged_append; one call must not write a block twice.
+ * this call's) is rounded up to one (2^127 at most: what that takes past 448 saturates).  Otherwise as fa_paged_append; one
+ * call must not write a block twice.
  */
 FA_API int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
                                void* k_cache, const int64_t* k_cache_strides, void* v_cache,

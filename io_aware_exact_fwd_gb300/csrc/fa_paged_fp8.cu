@@ -35,6 +35,8 @@ __device__ __forceinline__ float2 widen(uint32_t two) {
 }
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// 2^-e of a scale's e, -126 <= e <= 127.
+__device__ __forceinline__ float inverse_of_two(int e) { return e == 127 ? 0x1p-127f : power_of_two(-e); }
 // The smallest e >= -126 with top <= 448 * 2^e; top finite and not negative.
 __device__ __forceinline__ int exponent_for(float top) {
   const uint32_t bits = __float_as_uint(top);
@@ -124,12 +126,12 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
     }
     int e = exponent_for(widen<FP16>(top).x);
     if (held) {
-      // A scale that is no power of two (not one of this kernel's) counts as the next larger one.
-      const int e_old = min(static_cast<int>((old_bits >> 23) & 0xffu) - 127 + ((old_bits & 0x7fffffu) ? 1 : 0), 126);
+      // A scale that is no power of two (not one of this kernel's) counts as the next larger one, up to 2^127.
+      const int e_old = min(static_cast<int>((old_bits >> 23) & 0xffu) - 127 + ((old_bits & 0x7fffffu) ? 1 : 0), 127);
       const bool grows = e > e_old || (old_bits & 0x7fffffu);
       e = max(e, max(e_old, -126));
       if (grows) {
-        const float by = __uint_as_float(old_bits) * power_of_two(-e);
+        const float by = __uint_as_float(old_bits) * inverse_of_two(e);
         for (int r = row; r < held; r += kRows) {
           uint2* at = reinterpret_cast<uint2*>(cache + pg * sc.s[2] + ((of & ~15) + r) * sc.s[0]);
           uint2 c = *at;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
         }
       }
     }
-    const float inv = power_of_two(-e);
+    const float inv = inverse_of_two(e);
     uint8_t* dst = cache + pg * sc.s[2] + of * sc.s[0];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {

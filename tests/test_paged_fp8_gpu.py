@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import io_aware_exact_fwd_gb300 as fa
-from oracle import e4m3_decode, paged_append_fp8, paged_decode_fp8, paged_resize
+from oracle import e4m3_decode, e4m3_encode, paged_append_fp8, paged_decode_fp8, paged_resize
 
 from gpu_util import host_f64, report
 
@@ -594,3 +594,35 @@ def test_refusals_in_the_binding():
         fa.fa_paged_resize(table, n, delta, f, cnt, 8)
     with pytest.raises(fa.FAError):
         fa.fa_paged_resize(table, n, delta, f, cnt, 16, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def _append_behind(codes, scale, new):
+    """(codes, scales) of one block of 16 tokens of one head of 64: `codes` of its first tokens at `scale`, then `new` appended."""
+    held, T = codes.shape[0], new.shape[0]
+    cache = torch.full((1, 1, 16, 64), 0x55, dtype=torch.uint8)
+    cache[0, 0, :held] = codes
+    kc, vc = cache.cuda(), cache.cuda()
+    ks, vs = (torch.tensor([[[scale]]], dtype=torch.float32, device="cuda") for _ in range(2))
+    x = new[:, None].to(torch.bfloat16).cuda()
+    fa.fa_paged_append_fp8(x, x, _as_codes(kc), _as_codes(vc), ks, vs, _ints([[0]]), _ints([held + T]), _ints([0, T]))
+    fa.fa_sync_check()
+    assert torch.equal(kc, vc) and torch.equal(ks, vs)
+    want = paged_append_fp8(host_f64(x), cache.numpy(), np.array([[[scale]]], np.float32), [[0]], [held + T], [0, T])
+    return kc.cpu().numpy(), host_f64(ks), want
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 126, 1.3 * 2.0 ** 126, 2.0 ** 127, 1.5 * 2.0 ** 125, 2.0 ** -126, 1.25 * 2.0 ** -126, 1.5 * 2.0 ** -127])
+def test_append_behind_the_largest_and_smallest_scales(scale):
+    g = torch.Generator().manual_seed(5)
+    codes = torch.randint(0, 0x7F, (5, 64), generator=g, dtype=torch.uint8)
+    got, scales, want = _append_behind(codes, scale, min(scale, 1.0) * torch.randn(3, 64, generator=g))
+    assert np.array_equal(scales, want[1]) and np.array_equal(got, want[0])
+
+
+def test_append_behind_a_scale_that_no_power_of_two_reaches():
+    # 2^127 is the largest there is: codes grow by what the scale loses, up to the largest code.
+    codes = torch.arange(0, 0x7F, dtype=torch.uint8)[:64].repeat(2, 1)
+    codes[1] += 0x3F
+    got, scales, _ = _append_behind(codes, 1.5 * 2.0 ** 127, torch.ones(1, 64))
+    assert scales.item() == 2.0 ** 127 and np.array_equal(got[0, 0, :2], e4m3_encode(1.5 * e4m3_decode(codes.numpy())))
+    assert not e4m3_decode(got[0, 0, 2]).any()  # 1 beside 2^127
