@@ -37,6 +37,31 @@ __device__ __forceinline__ float2 widen(uint32_t two) {
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // 2^-e of a scale's e, -126 <= e <= 127.
 __device__ __forceinline__ float inverse_of_two(int e) { return e == 127 ? 0x1p-127f : power_of_two(-e); }
+// The codes of a block's older tokens (rows `row`, row + step, ... below `held`, eight codes a lane) times `by`, each rounded as
+// the exact product is: where `by` has 24 bits (a scale that is no power of two) fp32's product would already be rounded,
+// so it is cut off, with the last bit set if anything was lost.  A call: blocks that held tokens are few, and in line
+// it cost the append of 35k tokens of 8 heads x 128 a tenth of its time (40.7 us for 36.9; 36.5 with fp32's rounding).
+__device__ __noinline__ void recode(uint8_t* at, int64_t stride, int row, int step, int held, float by) {
+  for (int r = row; r < held; r += step) {
+    uint2* place = reinterpret_cast<uint2*>(at + r * stride);
+    const uint2 c = *place;
+    const uint32_t in[2] = {c.x, c.y};
+    uint32_t out[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 p = widen<true>(codes_to_half2(in[j])), q = widen<true>(codes_to_half2(in[j] >> 16));
+      const float x[4] = {p.x, p.y, q.x, q.y};
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = __fmul_rz(x[i], by);
+        if (fmaf(x[i], by, -y[i]) != 0.f) y[i] = __uint_as_float(__float_as_uint(y[i]) | 1u);
+      }
+      out[j] = e4m3x2_bits(y[0], y[1]) | (e4m3x2_bits(y[2], y[3]) << 16);
+    }
+    *place = make_uint2(out[0], out[1]);
+  }
+}
 // The smallest e >= -126 with top <= 448 * 2^e; top finite and not negative.
 __device__ __forceinline__ int exponent_for(float top) {
   const uint32_t bits = __float_as_uint(top);
@@ -125,27 +150,15 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
       top = __reduce_max_sync(0xffffffffu, top);
     }
     int e = exponent_for(widen<FP16>(top).x);
+    bool grows = false;
     if (held) {
       // A scale that is no power of two (not one of this kernel's) counts as the next larger one, up to 2^127.
       const int e_old = min(static_cast<int>((old_bits >> 23) & 0xffu) - 127 + ((old_bits & 0x7fffffu) ? 1 : 0), 127);
-      const bool grows = e > e_old || (old_bits & 0x7fffffu);
+      grows = e > e_old || (old_bits & 0x7fffffu);
       e = max(e, max(e_old, -126));
-      if (grows) {
-        const float by = __uint_as_float(old_bits) * inverse_of_two(e);
-        for (int r = row; r < held; r += kRows) {
-          uint2* at = reinterpret_cast<uint2*>(cache + pg * sc.s[2] + ((of & ~15) + r) * sc.s[0]);
-          uint2 c = *at;
-          uint32_t out[2];
-          const uint32_t in[2] = {c.x, c.y};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 p = widen<true>(codes_to_half2(in[j])), q = widen<true>(codes_to_half2(in[j] >> 16));
-            out[j] = e4m3x2_bits(p.x * by, p.y * by) | (e4m3x2_bits(q.x * by, q.y * by) << 16);
-          }
-          *at = make_uint2(out[0], out[1]);
-        }
-      }
     }
+    if (grows)
+      recode(cache + pg * sc.s[2] + (of & ~15) * sc.s[0], sc.s[0], row, kRows, held, __uint_as_float(old_bits) * inverse_of_two(e));
     const float inv = inverse_of_two(e);
     uint8_t* dst = cache + pg * sc.s[2] + of * sc.s[0];
 #pragma unroll

@@ -626,3 +626,41 @@ def test_append_behind_a_scale_that_no_power_of_two_reaches():
     got, scales, _ = _append_behind(codes, 1.5 * 2.0 ** 127, torch.ones(1, 64))
     assert scales.item() == 2.0 ** 127 and np.array_equal(got[0, 0, :2], e4m3_encode(1.5 * e4m3_decode(codes.numpy())))
     assert not e4m3_decode(got[0, 0, 2]).any()  # 1 beside 2^127
+
+
+def test_recoding_rounds_the_exact_product():
+    # Scales s in (1/2, 1) whose product with a code's value lies next to the middle between two codes, nearer than fp32
+    # tells: the scale becomes 1 and the code that of the exact product.
+    values = e4m3_decode(np.arange(0x7F, dtype=np.uint8))
+    middles = (values[1:] + values[:-1]) / 2
+    tried = 0
+    for p in (0x39, 0x3B, 0x3D, 0x45):  # 1.125, 1.375, 1.625, 3.25
+        v = values[p]
+        for m in middles[(middles > v / 2) & (middles < v)]:
+            s = float(np.float32(m / v))
+            if s * v == m or float(np.float32(s * v)) != m or e4m3_encode(s * v) == e4m3_encode(m):
+                continue
+            tried += 1
+            codes = torch.full((2, 64), p, dtype=torch.uint8)
+            codes[1] |= 0x80
+            got, scales, want = _append_behind(codes, s, torch.ones(1, 64))
+            assert scales.item() == 1.0 and np.array_equal(got, want[0]), (p, m)
+    assert tried >= 4
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("size", [1.0, 16.0])  # new tokens below the scales, and above some
+def test_append_behind_scales_that_are_no_powers_of_two(size, layout):
+    g = torch.Generator().manual_seed(12)
+    new, before, Hkv, d, page = [1, 20, 0, 5, 40], [3, 31, 7, 12, 17], 2, 64, 32
+    lens = [a + b for a, b in zip(new, before)]
+    table, n_pages = _tables(lens, page, g)
+    (kc, ks), (vc, vs) = (_codes((n_pages, Hkv, page, d), layout, g) for _ in range(2))
+    x = (size * torch.randn(sum(new), 2 * Hkv, d, generator=g)).to(torch.bfloat16).cuda()
+    k, v = x[:, :Hkv], x[:, Hkv:]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    want = [paged_append_fp8(host_f64(t), c.cpu().numpy(), s.cpu().numpy(), table, lens, cu) for t, c, s in ((k, kc, ks), (v, vc, vs))]
+    fa.fa_paged_append_fp8(k, v, _as_codes(kc), _as_codes(vc), ks, vs, _ints(table), _ints(lens), _ints(cu.tolist()))
+    fa.fa_sync_check()
+    for c, s, (wc, ws) in zip((kc, vc), (ks, vs), want):
+        assert np.array_equal(host_f64(s), ws) and np.array_equal(c.cpu().numpy(), wc)
