@@ -584,8 +584,8 @@ FA_API int fa_paged_append(const void* k, const int64_t* k_strides, const void* 
                            const int32_t* seq_lens, const int32_t* cu_new, int B, int T, int Hkv, int d, int page_size,
                            int n_pages, int max_pages, int dtype, fa_stream_t stream);
 
-/* Bytes of workspace fa_paged_decode needs on the current device (0 for invalid or
- * unsupported sizes).  It does not grow with the cache's length. */
+/* Bytes of workspace fa_paged_decode and fa_paged_decode_fp8 need on the current device (0 for
+ * invalid or unsupported sizes).  It does not grow with the cache's length. */
 FA_API size_t fa_paged_decode_workspace_size(int B, int H, int Hkv, int d);
 
 /*
@@ -638,7 +638,7 @@ FA_API int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const vo
                                int max_pages, int dtype, fa_stream_t stream);
 
 /*
- * fa_paged_decode_fp8 -- fa_paged_decode over such a cache; the workspace is fa_paged_decode's.
+ * fa_paged_decode_fp8 -- fa_paged_decode over such a cache; its workspace has fa_paged_decode_workspace_size(...) bytes.
  * Any positive finite scales.  The products take q as fp16 times a power of two of its row: entries
  * keep all their bits down to 2^-28 of the row's largest and are off by at most 2^-39 of that below.
  * Weights times V scales, rounded to fp16, keep theirs down to 2^-21 of the largest such product of the

@@ -313,10 +313,11 @@ struct PagedDecodeArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream);
-size_t paged_decode_workspace(int B, int d);  // of either cache
+size_t paged_decode_workspace(int B, int d);
 // The same on a cache of e4m3 codes (fa_paged_fp8.cu).
 cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_decode_fp8(const PagedDecodeArgs& a, cudaStream_t stream);
+size_t paged_decode_fp8_workspace(int B, int H, int Hkv, int d);
 
 // The sequences' lengths, pages and new tokens (fa_paged_resize.cu).
 struct PagedResizeArgs {

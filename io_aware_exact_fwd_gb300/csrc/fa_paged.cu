@@ -112,10 +112,12 @@ __global__ void __launch_bounds__(128) paged_append_kernel(PagedAppendArgs a, in
 // other, biased: 92-101 us, 5.3-5.8 TB/s (86 us where each head's tokens lie together); one
 // of 900 tokens, H=16 over 4: 9.3 us in a graph, two launches and two waits on memory.
 enum : uint32_t { kSiteDecLoad = 0x131, kSiteDecFull = 0x331 };
+constexpr int kRowsPerSm = 32;  // of parts: two CTAs with 16 heads each, or one with 32
 
 template <int D, int MT, bool FP16>
 struct DecCfg {
   static constexpr int kRows = 16 * MT;                   // query heads per chunk
+  static constexpr int kPerSm = MT == 1 ? 2 : 1;          // CTAs
   static constexpr int kTile = 8192 / D;                  // tokens per tile: K and V of one are 32 KB
   static constexpr int kBlocks = kTile / (16 * kConsumers);  // 16-token blocks of a warp in a tile
   static constexpr int kBoxes = D / 64;                   // 128-byte TMA boxes per row
@@ -137,7 +139,7 @@ struct DecCfg {
 };
 
 template <int D, int MT, bool FP16>
-__global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D, MT, FP16>::kPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ DecParams p) {
   using C = DecCfg<D, MT, FP16>;
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 ? 2 : 1)
 template <int D, int MT, bool FP16>
 cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   using C = DecCfg<D, MT, FP16>;
-  const DecParams p = decode_params(a, C::kRows, C::kTile);
+  const DecParams p = decode_params(a, C::kRows, C::kTile, C::kRows, C::kPerSm);
   CUtensorMap tk, tv;
   cudaError_t e;
   // L2 fetches a row of one head at a time: with heads beside each other a 256-byte fetch of a
@@ -527,14 +529,18 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
     return e;
   auto kern = decode_kernel<D, MT, FP16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
-  kern<<<static_cast<unsigned>(paged_decode_ctas(p.group)), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
+  static_assert(C::kPerSm * C::kRows == kRowsPerSm, "the workspace's parts");
+  kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
   return launch_join<D, FP16>(p, C::kRows, stream);
 }
 
 template <int D, bool FP16>
 cudaError_t launch_decode_mt(const PagedDecodeArgs& a, cudaStream_t stream) {
-  return paged_decode_mt(a.H / a.c.Hkv) == 1 ? launch_decode<D, 1, FP16>(a, stream) : launch_decode<D, 2, FP16>(a, stream);
+  // Up to 16 heads share a key/value head in most models, and two CTAs an SM with 16 rows each keep more loads in flight
+  // than one with 32 (64 sequences of 4000-8000 tokens, one head of d=128: 40.5 us against 46.5); larger groups read
+  // the cache once a chunk, so chunks of 32 pay (32 heads: 49.2 us against 54.0).
+  return a.H / a.c.Hkv <= 16 ? launch_decode<D, 1, FP16>(a, stream) : launch_decode<D, 2, FP16>(a, stream);
 }
 
 }  // namespace
@@ -549,9 +555,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-size_t paged_decode_workspace(int B, int d) {
-  return part_bytes(d) + (static_cast<size_t>(B) + 2) * sizeof(long long);
-}
+size_t paged_decode_workspace(int B, int d) { return decode_workspace(kRowsPerSm, B, d); }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t stream) {
   if (a.c.d == 64) return a.fp16 ? launch_decode_mt<64, true>(a, stream) : launch_decode_mt<64, false>(a, stream);

@@ -33,7 +33,7 @@ struct DecParams {
   uint16_t* o;
   Strides sq, so;
   float* lse;
-  float* part;               // [2 CTAs][rows][D + 2]: O, then m and l
+  float* part;               // [2 CTAs][part_rows][D + 2]: O, then m and l
   long long* offsets;        // [B + 1] tiles before each sequence, then the share
   int H, group, chunks, piece;
   int two;                   // 1: a head unit is two key/value heads (8-bit cache, rows of up to 8 query heads for each)
@@ -42,6 +42,7 @@ struct DecParams {
   const float* slopes;
   unsigned int* err_word;
   unsigned long long wait_ns;
+  int part_rows;             // even, so that parts start on 16 bytes
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -179,15 +180,15 @@ __device__ __forceinline__ bool share_of_tiles(const DecParams& p, int units, lo
 
 // Where the tiles of one sequence's query head are: CTAs c0 to c1 had them.
 struct HeadParts {
-  int b, head, row, c0, c1;  // row: of the unit's
+  int b, head, row, c0, c1;  // row: of a part's
   long long w0, share;
   bool empty;
-  __device__ __forceinline__ HeadParts(const DecParams& p, int rows_per_part, int x) {
+  __device__ __forceinline__ HeadParts(const DecParams& p, int rows_per_unit, int x) {
     b = x / p.H;
     head = x - b * p.H;
     const int hk = head / p.group, in_group = head % p.group;
-    const int u = p.two ? hk / 2 : hk * p.chunks + in_group / rows_per_part;
-    row = p.two ? 8 * (hk & 1) + in_group : in_group % rows_per_part;
+    const int u = p.two ? hk / 2 : hk * p.chunks + in_group / rows_per_unit;
+    row = p.two ? (hk & 1) * p.group + in_group : in_group % rows_per_unit;
     const long long first = p.offsets[b], tiles = quotient(p.offsets[b + 1] - first, units_of(p));
     share = p.offsets[p.c.B + 1];
     w0 = first + u * tiles;
@@ -201,8 +202,7 @@ struct HeadParts {
 
 // A block joins one head's parts: warp x takes parts x, x + 4, ...
 template <int D, bool FP16>
-__device__ __forceinline__ void join_head(const DecParams& p, const HeadParts& h, int rows_per_part, float2 (&s_ml)[4],
-                                          float (&s_o)[4][D]) {
+__device__ __forceinline__ void join_head(const DecParams& p, const HeadParts& h, float2 (&s_ml)[4], float (&s_o)[4][D]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = D / 32;
   uint16_t* dst = p.o + h.b * p.so.s[1] + h.head * p.so.s[0];
@@ -217,8 +217,8 @@ __device__ __forceinline__ void join_head(const DecParams& p, const HeadParts& h
   for (int c = h.c0 + warp; c <= h.c1; c += 4) {
     // A CTA's first segment has slot 0; only the first part can be another segment of its CTA.
     const int slot = 2 * c + (c * h.share >= h.w0 ? 0 : 1);
-    const float* part = p.part + static_cast<size_t>(slot) * rows_per_part * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(part + rows_per_part * D + 2 * h.row);
+    const float* part = p.part + static_cast<size_t>(slot) * p.part_rows * (D + 2);
+    const float2 ml = *reinterpret_cast<const float2*>(part + p.part_rows * D + 2 * h.row);
     float v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = part[h.row * D + lane + 32 * e];
@@ -254,51 +254,49 @@ __device__ __forceinline__ void join_head(const DecParams& p, const HeadParts& h
 // gridDim-th and each thread looks first at one, whether there is something to do: most of so many heads are whole (the 8-bit decode of
 // 109 sequences with 9 .. 18 tokens, 192 heads: 47 us with a block each, 30 so).
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_part) {
+__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecParams p, int rows_per_unit) {
   __shared__ float2 s_ml[4];
   __shared__ __align__(16) float s_o[4][D];
   __shared__ uint32_t s_open[4];
   grid_wait();  // the parts are written
   const int all = p.c.B * p.H, step = gridDim.x;
   if (all == step) {
-    const HeadParts h(p, rows_per_part, blockIdx.x);
-    if (h.open()) join_head<D, FP16>(p, h, rows_per_part, s_ml, s_o);
+    const HeadParts h(p, rows_per_unit, blockIdx.x);
+    if (h.open()) join_head<D, FP16>(p, h, s_ml, s_o);
     return;
   }
   for (long long first = blockIdx.x; first < all; first += 128LL * step) {
     const long long mine = first + static_cast<long long>(threadIdx.x) * step;
-    const bool open = mine < all && HeadParts(p, rows_per_part, static_cast<int>(mine)).open();
+    const bool open = mine < all && HeadParts(p, rows_per_unit, static_cast<int>(mine)).open();
     const uint32_t some = __ballot_sync(0xffffffffu, open);
     if ((threadIdx.x & 31) == 0) s_open[threadIdx.x >> 5] = some;
     __syncthreads();
     for (int w = 0; w < 4; ++w)
       for (uint32_t todo = s_open[w]; todo; todo &= todo - 1) {
         const int x = static_cast<int>(first + static_cast<long long>(32 * w + __ffs(todo) - 1) * step);
-        join_head<D, FP16>(p, HeadParts(p, rows_per_part, x), rows_per_part, s_ml, s_o);
+        join_head<D, FP16>(p, HeadParts(p, rows_per_unit, x), s_ml, s_o);
         __syncthreads();  // (s_ml and s_o are free)
       }
     __syncthreads();
   }
 }
 template <int D, bool FP16>
-cudaError_t launch_join(const DecParams& p, int rows_per_part, cudaStream_t stream) {
+cudaError_t launch_join(const DecParams& p, int rows_per_unit, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(p.c.B) * static_cast<unsigned>(p.H), most = static_cast<unsigned>(sm_count()) * 16;
-  return launch_dependent(decode_join_kernel<D, FP16>, heads < most ? heads : most, 128, 0, stream, p, rows_per_part);
+  return launch_dependent(decode_join_kernel<D, FP16>, heads < most ? heads : most, 128, 0, stream, p, rows_per_unit);
 }
 
-// Query heads per chunk (16 MT) and the CTAs of the 16-bit decode.  Up to 16 heads share a key/value head
-// in most models, and two CTAs an SM with 16 rows each keep more loads in flight than one with 32
-// (64 sequences of 4000-8000 tokens, one head of d=128: 40.5 us against 46.5); larger groups read
-// the cache once a chunk, so chunks of 32 pay (32 heads: 49.2 us against 54.0).
-inline int paged_decode_mt(int group) { return group <= 16 ? 1 : 2; }
-inline int paged_decode_ctas(int group) { return sm_count() * (paged_decode_mt(group) == 1 ? 2 : 1); }
-
-// The parts of both decodes: two a CTA, of at most 32 (16-bit) or 48 rows an SM.
-inline size_t part_bytes(int d) {
-  return (static_cast<size_t>(2) * 48 * sm_count() * (d + 2) * sizeof(float) + 255) / 256 * 256;
+// The parts of a decode: two a CTA.
+inline size_t part_bytes(int rows_per_sm, int d) {
+  return (static_cast<size_t>(2) * rows_per_sm * sm_count() * (d + 2) * sizeof(float) + 255) / 256 * 256;
+}
+// With the tiles before each sequence and the share.
+inline size_t decode_workspace(int rows_per_sm, int B, int d) {
+  return part_bytes(rows_per_sm, d) + (static_cast<size_t>(B) + 2) * sizeof(long long);
 }
 
-inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile) {
+// Of units of `rows` heads, in `per_sm` CTAs an SM.
+inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile, int part_rows, int per_sm) {
   DecParams p{};
   p.c = a.c;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -309,8 +307,9 @@ inline DecParams decode_params(const PagedDecodeArgs& a, int rows, int tile) {
   p.H = a.H;
   p.group = a.H / a.c.Hkv;
   p.chunks = (p.group + rows - 1) / rows;
+  p.part_rows = part_rows;
   p.part = static_cast<float*>(a.workspace);
-  p.offsets = reinterpret_cast<long long*>(static_cast<uint8_t*>(a.workspace) + part_bytes(a.c.d));
+  p.offsets = reinterpret_cast<long long*>(static_cast<uint8_t*>(a.workspace) + part_bytes(per_sm * part_rows, a.c.d));
   // The tokens of one page inside a tile: the largest power of two that divides both.
   p.piece = std::min(tile, a.c.page_size & -a.c.page_size);
   p.scale_log2 = a.scale * kLog2e;

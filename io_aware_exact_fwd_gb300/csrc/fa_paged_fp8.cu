@@ -651,7 +651,8 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
     }
     // ---- the four warps' parts, joined
     float* s_o = reinterpret_cast<float*>(smem + slot * C::kStage);  // [warp][head][kORow]
-    float* part = p.part + static_cast<size_t>(2 * cta + (first_segment ? 0 : 1)) * kHeads * (D + 2);
+    const int part_rows = TWO ? p.part_rows : kHeads;
+    float* part = p.part + static_cast<size_t>(2 * cta + (first_segment ? 0 : 1)) * part_rows * (D + 2);
     consumers_sync();  // every warp is done with the stage
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
@@ -681,6 +682,7 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
       // The row's parts: all four warps', or (TWO) those of its key/value head's two.
       constexpr int kParts = TWO ? 2 : 4;
       const int from = TWO ? (r >> 3) * 2 * kWarpHeads + (r & 7) : r;
+      const int part_row = TWO ? (r >> 3) * p.group + (r & 7) : r;
       float M = kNoScore, L = 0.f, wgt[kParts];
 #pragma unroll
       for (int x = 0; x < kParts; ++x) M = fmaxf(M, s_ml[x * kWarpHeads + from].x);
@@ -707,13 +709,13 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
           *reinterpret_cast<uint2*>(p.o + at.b * p.so.s[1] + head * p.so.s[0] + col) =
               make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
         else
-          *reinterpret_cast<float4*>(part + r * D + col) = acc;
+          *reinterpret_cast<float4*>(part + part_row * D + col) = acc;
       }
       if (in_row == 0) {
         if (whole)
           p.lse[static_cast<size_t>(at.b) * p.H + head] = (M + log2f(L)) * kLn2;
         else
-          *reinterpret_cast<float2*>(part + kHeads * D + 2 * r) = make_float2(M, L);
+          *reinterpret_cast<float2*>(part + part_rows * D + 2 * part_row) = make_float2(M, L);
       }
     }
     fence_proxy_async_smem();  // the stage goes back to the TMA producer
@@ -729,10 +731,16 @@ __global__ void __launch_bounds__(kDecThreads, Dec8Cfg<D, NH, TWO>::kPerSm)
   }
 }
 
+// Rows of a part: the heads of a unit (TWO: those that there are).
+template <class C, bool TWO>
+int part_rows_of(int group) {
+  return TWO ? 2 * group : C::kHeads;
+}
+
 template <int D, int NH, bool TWO, bool FP16>
 cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   using C = Dec8Cfg<D, NH, TWO>;
-  DecParams p = decode_params(a, C::kHeads, C::kTile);
+  DecParams p = decode_params(a, C::kHeads, C::kTile, part_rows_of<C, TWO>(a.H / a.c.Hkv), C::kPerSm);
   p.two = TWO;
   CUtensorMap tk, tv;
   cudaError_t e;
@@ -751,7 +759,6 @@ cudaError_t launch_decode8(const PagedDecodeArgs& a, cudaStream_t stream) {
   if ((e = map(&tv, a.c.v, a.c.sv))) return e;
   auto kern = decode_fp8_kernel<D, NH, TWO, FP16>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes))) return e;
-  static_assert(C::kPerSm * C::kHeads <= 48, "the workspace's parts");
   kern<<<static_cast<unsigned>(sm_count() * C::kPerSm), kDecThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError())) return e;
   return launch_join<D, FP16>(p, C::kHeads, stream);
@@ -780,6 +787,18 @@ cudaError_t launch_paged_append_fp8(const PagedAppendArgs& a, cudaStream_t strea
                           : (a.fp16 ? append_fp8_kernel<128, true> : append_fp8_kernel<128, false>);
   kern<<<grid, 128, 0, stream>>>(a, run);
   return cudaGetLastError();
+}
+
+// Whatever the cache's layout.  Both d have the same builds' rows, but for groups past 8.
+size_t paged_decode_fp8_workspace(int B, int H, int Hkv, int d) {
+  const int group = H / Hkv;
+  using One = Dec8Cfg<128, 1, false>;
+  using Two = Dec8Cfg<128, 1, true>;
+  static_assert(One::kPerSm == Dec8Cfg<64, 1, false>::kPerSm && Two::kPerSm == Dec8Cfg<64, 1, true>::kPerSm, "as said");
+  int rows;
+  if (group > 8) rows = d == 64 ? Dec8Cfg<64, 2, false>::kPerSm * 16 : Dec8Cfg<128, 2, false>::kPerSm * 16;
+  else rows = std::max(One::kPerSm * One::kHeads, Hkv % 2 == 0 ? Two::kPerSm * part_rows_of<Two, true>(group) : 0);
+  return decode_workspace(rows, B, d);
 }
 
 cudaError_t launch_paged_decode_fp8(const PagedDecodeArgs& a, cudaStream_t stream) {

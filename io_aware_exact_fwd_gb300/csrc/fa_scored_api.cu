@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fa.h"
 #include "fa_internal.h"
 
@@ -249,7 +251,7 @@ int fa_paged_append(const void* k, const int64_t* k_strides, const void* v, cons
 size_t fa_paged_decode_workspace_size(int B, int H, int Hkv, int d) {
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
   if (B > 65535 || static_cast<long long>(B) * H > kIntMax) return 0;
-  return fa::paged_decode_workspace(B, d);
+  return std::max(fa::paged_decode_workspace(B, d), fa::paged_decode_fp8_workspace(B, H, Hkv, d));
 }
 
 int fa_paged_decode(const void* q, const int64_t* q_strides, const void* k_cache, const int64_t* k_cache_strides,
@@ -353,7 +355,7 @@ int fa_paged_decode_fp8(const void* q, const int64_t* q_strides, const void* k_c
   if (H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * H > kIntMax) return FA_ERR_UNSUPPORTED;
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!workspace || ws_bytes < fa::paged_decode_workspace(B, d)) return FA_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < fa_paged_decode_workspace_size(B, H, Hkv, d)) return FA_ERR_WORKSPACE;
   fa::PagedDecodeArgs a{};
   int st = paged_cache(&a.c, k_cache, k_cache_strides, v_cache, v_cache_strides, page_table, table_stride, seq_lens,
                        B, Hkv, d, page_size, n_pages, max_pages);

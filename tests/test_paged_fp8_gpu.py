@@ -664,3 +664,23 @@ def test_append_behind_scales_that_are_no_powers_of_two(size, layout):
     fa.fa_sync_check()
     for c, s, (wc, ws) in zip((kc, vc), (ks, vs), want):
         assert np.array_equal(host_f64(s), ws) and np.array_equal(c.cpu().numpy(), wc)
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 64), (3, 1, 128), (14, 2, 64), (16, 2, 128), (21, 3, 64), (9, 1, 64), (16, 1, 64), (17, 1, 64),
+                                     (22, 2, 128), (40, 1, 128)])
+def test_decode_in_the_workspace_that_it_asks_for(H, Hkv, d, layout):
+    # Of every build: parts of as many rows as a unit has heads, none written past the workspace's end.
+    lens = [5000, 0, 700, 1, 9000]
+    kc, vc, ks, vs, table, n = _cache(lens, Hkv, d, 16, 43, layout)
+    q = torch.randn(5, H, d, generator=torch.Generator().manual_seed(44)).to(torch.bfloat16).cuda()
+    size = fa.fa_paged_decode_workspace_size(5, H, Hkv, d)
+    buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    o, lse = fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, table, n, workspace=buf[:size])
+    fa.fa_sync_check()
+    ref = _oracle(q, kc, vc, ks, vs, table, lens, d, 0.0, None, torch.bfloat16)
+    _check(o, ref[0], ref[2], "O")
+    _check(lse, ref[1], ref[3], "LSE")
+    assert bool((buf[size:] == 0xA5).all())
+    with pytest.raises(fa.FAError):
+        fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, table, n, workspace=buf[:size - 1])

@@ -479,3 +479,22 @@ def test_decode_agrees_with_the_forward_at_a_large_cap():
 def test_many_heads(case):
     # More heads than blocks that join their parts: some whole, some in parts, some of empty sequences.
     _decode(case, "nhd", None)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(16, 2, 64), (8, 1, 128), (64, 2, 64), (40, 1, 128)])
+def test_decode_in_the_workspace_that_it_uses(H, Hkv, d):
+    # Two parts for each of 32 rows an SM and the tiles before each sequence: what the 8-bit cache's decode needs beside
+    # that, this one neither asks for nor writes.
+    lens = [3000, 0, 700, 1]
+    kc, vc, table, n = _cache(lens, Hkv, d, 16, torch.bfloat16, 41)
+    q = torch.randn(4, H, d, generator=torch.Generator().manual_seed(42)).to(torch.bfloat16).cuda()
+    want = fa.fa_paged_decode(q, kc, vc, table, n)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    size = (2 * 32 * sms * (d + 2) * 4 + 255) // 256 * 256 + (4 + 2) * 8
+    buf = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = fa.fa_paged_decode(q, kc, vc, table, n, workspace=buf[:size])
+    fa.fa_sync_check()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and bool((buf[size:] == 0xA5).all())
+    with pytest.raises(fa.FAError):
+        fa.fa_paged_decode(q, kc, vc, table, n, workspace=buf[:size - 1])
+    assert fa.fa_paged_decode_workspace_size(4, H, Hkv, d) >= size
