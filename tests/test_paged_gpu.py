@@ -498,3 +498,21 @@ def test_decode_in_the_workspace_that_it_uses(H, Hkv, d):
     with pytest.raises(fa.FAError):
         fa.fa_paged_decode(q, kc, vc, table, n, workspace=buf[:size - 1])
     assert fa.fa_paged_decode_workspace_size(4, H, Hkv, d) >= size
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(32, 8, 128), (24, 24, 64)])
+def test_idle_places(H, Hkv, d):
+    # A batch of a fixed number of places, most of them idle: zeros and -inf there, nothing written beside them.
+    lens = [0] * 997
+    lens[5], lens[128], lens[996] = 700, 1, 333
+    kc, vc, table, n = _cache(lens, Hkv, d, 16, torch.bfloat16, 51)
+    q = torch.randn(997, H, d, generator=torch.Generator().manual_seed(52)).to(torch.bfloat16).cuda()
+    buf = torch.full((997, H + 1, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.fa_paged_decode(q, kc, vc, table, n, o=buf[:, :H])
+    live = [5, 128, 996]
+    want, want_l = fa.fa_paged_decode(q[live], kc, vc, table[live], n[live])
+    fa.fa_sync_check()
+    idle = n == 0
+    assert not o[idle].any() and torch.isneginf(lse[idle]).all() and bool((buf[:, H] == 9).all())
+    # (other shares: the parts' sums in another order; a few fp32 steps, before one of bf16)
+    assert (o[live].float() - want.float()).abs().max() <= 2.0 ** -7 * want.abs().max() and (lse[live] - want_l).abs().max() < 1e-4
