@@ -310,3 +310,25 @@ def test_norm_of_a_row_with_an_infinity():
     y, _ = fa.fa_qk_norm_rope(x, x, inv_freq=_freq(32))
     fa.fa_sync_check()
     assert y[0, 0, 0].isfinite().all() and y[0, 0, 1, 40].isnan() and y[0, 0, 1].isnan().sum() == 1 and y[0, 0, 1].nansum() == 0
+
+
+@pytest.mark.parametrize("rows", ["last", "few"])
+@pytest.mark.parametrize("case", [_case(N=1250, H=12, Hkv=1, d=128), _case(N=2600, H=12, Hkv=3, layout="qkv", dtype=torch.float16),
+                                  _case(B=3, N=1667, H=7, Hkv=7), _case(B=2, N=1217, H=24, Hkv=5, layout="bnhd")], ids=str)
+def test_weights_gradient_of_few_rows_among_many(case, rows):
+    # One row that is lost, or one that is counted twice, is a large part of what is left: the bound of all rows' sum
+    # (2^-24 of it for each) would not see it.
+    q, k, gq, gk, kw, refs = _state(case)
+    for g in (gq, gk):
+        B, H, N, _ = g.shape
+        keep = torch.zeros(B, N, H, dtype=torch.bool)  # (tokens first, as warps take them)
+        if rows == "last":
+            keep[-1, -1, -1] = True
+        else:
+            keep.view(-1)[::997] = True
+        g.masked_fill_(~keep.transpose(1, 2)[..., None].cuda(), 0.0)
+    got = fa.fa_qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    fa.fa_sync_check()
+    for dw, x, g, r in zip(got[2:], (q, k), (gq, gk), refs):
+        (_, ref), (_, bound) = qk_norm_rope_backward(host_f64(x), host_f64(g), **r)
+        _within(dw, ref, bound, "dw")
