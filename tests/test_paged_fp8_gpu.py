@@ -684,3 +684,74 @@ def test_decode_in_the_workspace_that_it_asks_for(H, Hkv, d, layout):
     assert bool((buf[size:] == 0xA5).all())
     with pytest.raises(fa.FAError):
         fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, table, n, workspace=buf[:size - 1])
+
+
+@pytest.mark.parametrize("B", [40, 700])  # one block; over the GPU
+@pytest.mark.parametrize("which", ["slots", "positions", "neither"])
+def test_resize_without_slots_or_positions(B, which):
+    lens = [(7 * i) % 90 for i in range(B)]
+    delta = [(11 * i) % 60 - min(lens[i], 20) for i in range(B)]
+    new = sum(x for x in delta if x > 0)
+    page, width, spare = 16, 12, 6 * B
+    used = sum(-(-n // page) for n in lens)
+    order = torch.randperm(used + spare, generator=torch.Generator().manual_seed(B)).tolist()
+    table, at = [], 0
+    for n in lens:
+        m = -(-n // page)
+        table.append((order[at:at + m] + [-1] * width)[:width])
+        at += m
+    free = order[used:] + [-7] * used
+    want = paged_resize(table, lens, delta, free, spare, page, new + 3)
+    t, n, d, f, c = _ints(table), _ints(lens), _ints(delta), _ints(free), _ints([spare])
+    slots, pos = torch.full((new + 3,), 5, dtype=torch.int64, device="cuda"), torch.full((new + 3,), 5, dtype=torch.int32, device="cuda")
+    kw = dict(slots=dict(slots=slots), positions=dict(positions=pos), neither={})[which]
+    out = fa.fa_paged_resize(t, n, d, f, c, page, **kw)
+    fa.fa_sync_check()
+    got = dict(zip("lens cu count status table free".split(), (*out, t, f)))
+    for name, x, y in zip(got, got.values(), want):
+        assert np.array_equal(x.cpu().numpy().ravel(), np.array([y] if name == "count" else y, dtype=np.int64).ravel()), name
+    assert slots.tolist() == (want[6] if which == "slots" else [5] * (new + 3))
+    assert pos.tolist() == (want[7] if which == "positions" else [5] * (new + 3))
+
+
+def test_two_graphs_share_a_workspace():
+    # Captured for two batches of other sizes over one workspace and replayed in turn on one stream; one's units are of two heads.
+    kc, vc, ks, vs, table, n = _cache([700, 90, 333], 2, 64, 16, 25, "nhd")
+    kd, vd = (t.contiguous() for t in (kc, vc))
+    q = torch.randn(3, 16, 64, generator=torch.Generator().manual_seed(26)).to(torch.bfloat16).cuda()
+    ws = torch.empty(fa.fa_paged_decode_workspace_size(3, 16, 2, 64), dtype=torch.uint8, device="cuda")
+    runs = [lambda o, l, w: fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, table, n, o=o, lse=l, workspace=w),
+            lambda o, l, w: fa.fa_paged_decode_fp8(q[:1], _as_codes(kd), _as_codes(vd), ks, vs, table[:1], n[:1], o=o, lse=l, workspace=w)]
+    want = [run(None, None, None) for run in runs]
+    outs = [(torch.zeros_like(o), torch.zeros_like(l)) for o, l in want]
+    graphs = []
+    for run, out in zip(runs, outs):
+        run(*out, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(*out, ws)
+        graphs.append(graph)
+    for turn in (0, 1, 1, 0):
+        for t in outs[turn]:
+            t.fill_(7)
+        graphs[turn].replay()
+        for a, b in zip(outs[turn], want[turn]):
+            assert torch.equal(a, b)
+    fa.fa_sync_check()
+
+
+@pytest.mark.parametrize("n", [5, 200, 5000])
+def test_the_largest_values_that_the_sums_take(n):
+    # 448 times the scale just below 2^122 / n: their weighted mean is itself.
+    d = 64
+    e = int(np.floor(113.1 - np.log2(n)))  # log2(448) = 8.81
+    pages = -(-n // 16)
+    kc = torch.randint(0, 0x50, (pages, 2, 16, d), generator=torch.Generator().manual_seed(3), dtype=torch.uint8).cuda()
+    vc = torch.full_like(kc, 0x7E)
+    ks, vs = torch.full((pages, 2, 1), 0.02, device="cuda"), torch.full((pages, 2, 1), 2.0 ** e, device="cuda")
+    q = torch.randn(1, 6, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    o, _ = fa.fa_paged_decode_fp8(q, _as_codes(kc), _as_codes(vc), ks, vs, torch.arange(pages, dtype=torch.int32, device="cuda")[None], _ints([n]))
+    fa.fa_sync_check()
+    # The weights' fp16 rounding (2^-11) in the sum alone, fp32's few steps, and bf16's of the result.
+    assert float((o.double() / (448 * 2.0 ** e) - 1).abs().max()) <= 2.0 ** -8 + 1.1 * 2.0 ** -11

@@ -110,3 +110,32 @@ def test_w4a16():
     scales = (torch.rand(K // 128, N, generator=g) * 0.01 + 0.005).half().cuda()
     zeros = torch.randint(0, 16, (K // 128, N), generator=g).to(torch.uint8).cuda()
     _check(lambda stream: [fa.fa_w4a16_gemm(x, wq, scales, zeros, n_split=2, stream=stream)], fa.fa_w4a16_workspace_size(M, N, K, 2))
+
+
+def test_paged_cache_in_8_bits():
+    B, H, Hkv, d, page = 3, 8, 2, 128, 16
+    kc, vc = (_randn(80, Hkv, page, d, seed=i).to(torch.float8_e4m3fn) for i in range(2))
+    ks, vs = (torch.full((80, Hkv, 1), 0.01, device="cuda") for _ in range(2))
+    table = torch.randperm(75, generator=torch.Generator().manual_seed(2)).to(torch.int32).view(B, 25).cuda()
+    n = torch.tensor([400, 1, 77], dtype=torch.int32, device="cuda")
+    q = _randn(B, H, d, seed=3)
+    _check(lambda stream: fa.fa_paged_decode_fp8(q, kc, vc, ks, vs, table, n, stream=stream), fa.fa_paged_decode_workspace_size(B, H, Hkv, d))
+
+
+@pytest.mark.parametrize("B", [5, 600])
+def test_paged_bookkeeping(B):
+    # Each sequence a token longer inside its page: the table and the list stay, so that both calls do the same.
+    table = torch.arange(2 * B, dtype=torch.int32, device="cuda").view(B, 2)
+    n, delta = (torch.full((B,), x, dtype=torch.int32, device="cuda") for x in (17, 1))
+    free, count = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    _check(lambda stream: fa.fa_paged_resize(table, n, delta, free, count, 16, stream=stream),
+           4 * (2 * B + 4) + fa.fa_paged_resize_workspace_size(B))
+
+
+def test_norm_and_rotation():
+    B, H, Hkv, N, d = 2, 6, 2, 300, 64
+    q, k, gq, gk = (_randn(B, h, N, d, seed=i) for i, h in enumerate((H, Hkv, H, Hkv)))
+    w, f = torch.ones(d, device="cuda"), torch.tensor([1e4 ** (-i / d) for i in range(0, d, 2)], dtype=torch.float32, device="cuda")
+    kw = dict(q_weight=w, k_weight=w, inv_freq=f)
+    _check(lambda stream: fa.fa_qk_norm_rope(q, k, stream=stream, **kw))
+    _check(lambda stream: fa.fa_qk_norm_rope_bwd(q, k, gq, gk, stream=stream, **kw), 2 * 4 * d, fa.fa_qk_norm_rope_bwd_workspace_size(d))
