@@ -615,7 +615,7 @@ FA_API int fa_paged_decode(const void* q, const int64_t* q_strides, const void* 
  * of 16 elements) and each block of 16 tokens of a page and head has a scale: k_scales,
  * v_scales are float [n_pages, Hkv, page_size / 16], dense, and a value is decode(code) * scale.
  * dtype is that of the 16-bit tensors of the call.  Half the bytes of the 16-bit cache a token (and
- * 4 / (16 d) for the scales), at a rounding of at most 2^-4 a value.
+ * 4 / (16 d) for the scales), at a rounding of a value x of at most max(2^-4 |x|, 2^-10 scale).
  */
 
 /*
@@ -639,8 +639,9 @@ FA_API int fa_paged_append_fp8(const void* k, const int64_t* k_strides, const vo
 
 /*
  * fa_paged_decode_fp8 -- fa_paged_decode over such a cache; its workspace has fa_paged_decode_workspace_size(...) bytes.
- * Any positive finite scales.  The products take q as fp16 times a power of two of its row: entries
- * keep all their bits down to 2^-28 of the row's largest and are off by at most 2^-39 of that below.
+ * Any positive finite scales, with 448 times V's largest below 2^122 / N for N tokens (O is summed before it is
+ * divided).  The products take q as fp16 times a power of two of its row: entries keep all their bits down to 2^-28 of
+ * the row's largest (of 2^-112 or more) and are off by at most 2^-39 of that below.
  * Weights times V scales, rounded to fp16, keep theirs down to 2^-21 of the largest such product of the
  * sequence and are lost below 2^-32.  Sums, maxima and scores are fp32.  The same bits on every run.
  */

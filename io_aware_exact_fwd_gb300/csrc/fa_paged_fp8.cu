@@ -25,9 +25,10 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t two) {
 // tokens whose scale is smaller, re-codes those.  A unit is a run of consecutive new tokens and one head of K or
 // V; the lanes look the tokens' places up, one each, and a token that is the first new one of its block stands for
 // the block.  With few tokens, or many sequences with few each, the runs are of one token, so that blocks do not wait for
-// each other; else of up to 32, so that the look-ups are not done for every token that stands for none.  Bound by HBM: 2 bytes read and 1 written a
-// value.  Measured: 16 prompts, 35k tokens of 8 heads x 128, in 37 us, 5.8 TB/s (runs of 16 tokens 39.7; the next block's rows
-// fetched into registers while one is coded 43.8: fewer warps an SM); 64 tokens in 3.4; 2000 sequences a token each in 26.
+// each other; else of up to 31, so that the look-ups are not done for every token that stands for none.  Bound by HBM: 2 bytes read and 1 written a
+// value.  Measured, in a graph: 16 prompts, 35k tokens of 8 heads x 128, in 37 us, 5.8 TB/s (runs of 16 tokens 39.7; the next block's rows
+// fetched into registers while one is coded 43.8: fewer warps an SM); 64 tokens in 3.1; 2000 sequences a token each in 26.  The time grows with the
+// idle sequences between two that a run spans: 35k tokens in the first and the last of 2 sequences 31 us, of 1000 75, of 4000 252.
 template <bool FP16>
 __device__ __forceinline__ float2 widen(uint32_t two) {
   if constexpr (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&two));
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
   }
   if (lane < run && first + lane < a.T) {
     const int t = static_cast<int>(first) + lane;
-    // From there to the number of offsets <= t, a few further on.
+    // From there to the number of offsets <= t: a few further on, and one for every idle sequence between.
     while (lo <= a.c.B && __ldg(a.cu_new + lo) <= t) ++lo;
     if (lo != 0 && lo != a.c.B + 1) {  // (else a row of no sequence)
       const int b = lo - 1, end = __ldg(a.cu_new + lo);
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
 // instructions (11 cycles each and scheduler) would take half the time that HBM leaves.  (The 8-bit m16n8k32 form is no way
 // round the widening: it takes 29 cycles here, conversions and two fp16 products.)
 //
-// q, whatever its type, comes in as fp16 times a power of two of its head, with its largest entry in [2^14, 2^15), so that
-// entries down to 2^-28 of the largest keep all their bits.  K's scale multiplies the finished scores of its block.  V's
+// q, whatever its type, comes in as fp16 times a power of two of its head, with its largest entry in [2^14, 2^15) (below that in rows
+// under 2^-112), so that entries down to 2^-28 of the largest keep all their bits.  K's scale multiplies the finished scores of its block.  V's
 // cannot follow its products, which sum over blocks: it goes into the weights.  A head therefore has two running references: m
 // for its scores, under which l sums the weights, and mv for scores + log2 of the block's V scale, under which the
 // weights are rounded to fp16 for P V.  Both are only raised when they have to be: a tile's weights are made under the old
@@ -209,9 +210,9 @@ __global__ void __launch_bounds__(128, D == 128 ? 6 : 8) append_fp8_kernel(const
 // that the cache is read once, ran at 3.6 TB/s of codes with 32 heads and 1.9 with 40: no more than chunks reach
 // with nothing in L2, for their arithmetic is the same and one CTA an SM hides less of it.)
 //
-// Measured: 64 sequences of 1 .. 16384 tokens (0.96 GB), H=32 over 8 heads, d=128, capped: 148-151 us, 6.4-6.5 TB/s (heads
-// as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 52-57 us, 4.8-5.2 TB/s; 24 of 2000 .. 8000 tokens, 40 heads over one: 25.7 (chunks of 8 heads 26.5, and 147
-// for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.6, two launches and three waits on memory.  Times in a graph.
+// Measured, in a graph: 64 sequences of 1 .. 16384 tokens (0.96 GB), H=32 over 8 heads, d=128, capped: 148-151 us, 6.4-6.5 TB/s (heads
+// as rows 197); one of 131072 tokens, 16 heads of d=64 beside each other, biased: 52-57 us, 4.8-5.2 TB/s; 24 of 2000 .. 8000 tokens, 40 heads over one: 25.3 (chunks of 8 heads 26.5, and 147
+// for 90 at 32000 tokens each); one of 900 tokens, H=16 over 4: 7.5, two launches and three waits on memory.
 enum : uint32_t { kSite8Load = 0x141, kSite8Full = 0x341 };
 
 template <int D, int NH, bool TWO>

@@ -12,7 +12,7 @@
 //
 // Bound by latency: a launch, two dependent loads of the lengths, the scan; then, for many tokens, by the instructions of
 // their look-ups.  The second part runs in the same block, with the sums in shared memory, where there is little of it, and as a
-// dependent launch over the GPU where there is more.  Measured, in a graph: 64 sequences a token longer each 3.9 us, 1000 of them
+// dependent launch over the GPU where there is more.  Measured, in a graph: 64 sequences a token longer each 3.9-4.1 us, 1000 of them
 // 6.6 (each row stepping through the sums by itself: 4.7 and 14.8); 1000 sequences, 600 of them longer by 750k tokens
 // together, the others shorter, 14 (9.7 MB written).
 #include "fa_device.cuh"
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kScanThreads) resize_scan_kernel(const __grid_
 }
 
 // The rows go to all warps, in groups of 32, UNROLL at a time.
-// (With the sums copied to each block's shared memory first: 12.7 us for 1000 sequences and 750k new tokens, 13.1 so.)
+// (The sums copied to each block's shared memory first did not pay: with rows that each stepped through them, 12.7 us for 1000 sequences and
+// 750k new tokens against 13.1.)
 template <int UNROLL>
 __global__ void __launch_bounds__(256, kSpreadPerSm) resize_spread_kernel(const __grid_constant__ PagedResizeArgs a) {
   grid_wait();
@@ -310,8 +311,10 @@ __global__ void __launch_bounds__(256, kSpreadPerSm) resize_spread_kernel(const 
 size_t paged_resize_workspace(int B) { return (2 * (static_cast<size_t>(B) + 1) + 1) * sizeof(int32_t); }
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
-  // One block where that is quicker most of the time: 64 sequences a token longer each 3.9 us, 4.7 with the second launch.  Long
-  // sequences that end take longer so, 0.6 us for 1000 pages, but each page comes back once for 16 or more such steps.
+  // One block where that is quicker most of the time: 64 sequences a token longer each 3.9 us, 4.7 with the second launch.  Many
+  // pages take longer so, 0.5 us for 1000 of them, but each is taken and comes back once for 16 or more such steps: 256 sequences of
+  // 131072 tokens in pages of 16 that all end, 2 million pages, 1.1 ms (257 of them, by two launches, 15 us); 64 prompts of 4000
+  // tokens without slots or positions 16.6 us, with slots 8.4.
   const int alone = a.T <= 2 * kScanThreads && a.B <= kScanThreads / 4;
   resize_scan_kernel<<<1, kScanThreads, 0, stream>>>(a, alone);
   const cudaError_t e = cudaGetLastError();

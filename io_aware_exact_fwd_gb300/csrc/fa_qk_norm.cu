@@ -13,7 +13,8 @@
 // cosines, the costliest part, are made once for them and stay in registers, as do the weights.  Rows stream through the warp: each lane
 // copies its pieces of the next rows into places of its own in shared memory (cp.async: HBM's latency at full rate takes
 // more bytes on the way than registers could wait for), over the ends of sides and tokens.  Measured: 16384 tokens of 40 heads
-// x 128 in 55.0 us, 6.1 TB/s; the gradient, 32 heads, in 67.0, 6.0 TB/s; 16 tokens of 10 heads x 64 in 3.9.  (A block that
+// x 128 in 55 us, 6.1 TB/s; the gradient, 32 heads, in 67, 6.0 TB/s; 16 tokens of 10 heads x 64 in 3.7.  In neighbouring pairs, which do
+// not go through the packed products of two values, 76 and 104; half of each head rotated, in halves, 67 and 87.  Times in a graph.  (A block that
 // shares its tokens' angles in shared memory and reads them for every row: 62 and 82 us, the reads' bank conflicts being
 // most of it; rows kept in registers alone: 76 and 89.)
 //
