@@ -755,3 +755,11 @@ def test_the_largest_values_that_the_sums_take(n):
     fa.fa_sync_check()
     # The weights' fp16 rounding (2^-11) in the sum alone, fp32's few steps, and bf16's of the result.
     assert float((o.double() / (448 * 2.0 ** e) - 1).abs().max()) <= 2.0 ** -8 + 1.1 * 2.0 ** -11
+
+
+@pytest.mark.parametrize("B", [300, 2500])
+def test_append_with_idle_sequences_inside_a_run(B):
+    # A warp's run of tokens ends one sequence and begins another far behind it.
+    new, before = [0] * B, [(3 * b) % 50 for b in range(B)]
+    new[0], new[B // 2], new[B // 2 + 1], new[B - 1] = 4001, 7, 1, 3999
+    _append(new, before, 2, 64, 64, torch.bfloat16, "hnd", tail=3)

@@ -332,3 +332,19 @@ def test_weights_gradient_of_few_rows_among_many(case, rows):
     for dw, x, g, r in zip(got[2:], (q, k), (gq, gk), refs):
         (_, ref), (_, bound) = qk_norm_rope_backward(host_f64(x), host_f64(g), **r)
         _within(dw, ref, bound, "dw")
+
+
+@pytest.mark.parametrize("which", ["q_weight", "k_weight"])
+def test_one_weight_alone(which):
+    case = _case(B=2, N=40, H=4, Hkv=2, weight="own")
+    q, k, gq, gk, kw, _ = _state(case)
+    both, back = fa.fa_qk_norm_rope(q, k, **kw), fa.fa_qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    other = "k_weight" if which == "q_weight" else "q_weight"
+    side = 0 if which == "q_weight" else 1
+    kw[other] = None
+    one, grads = fa.fa_qk_norm_rope(q, k, **kw), fa.fa_qk_norm_rope_bwd(q, k, gq, gk, **kw)
+    kw[other] = torch.ones_like(kw[which])
+    ones = fa.fa_qk_norm_rope(q, k, **kw)
+    fa.fa_sync_check()
+    assert torch.equal(one[side], both[side]) and torch.equal(one[1 - side], ones[1 - side])
+    assert torch.equal(grads[side], back[side]) and torch.equal(grads[2 + side], back[2 + side]) and grads[3 - side] is None
